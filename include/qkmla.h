@@ -71,8 +71,9 @@ enum {
     QKMLA_ERR_TIMEOUT = -6        /* device bounded wait expired */
 };
 
-/* Element types. */
-enum { QKMLA_F32 = 0, QKMLA_BF16 = 1 };
+/* Element types.  QKMLA_E4M3 names the 8-bit latent cache of qkmla_append_q8 and
+ * qkmla_decode_ext; no other call takes it. */
+enum { QKMLA_F32 = 0, QKMLA_BF16 = 1, QKMLA_E4M3 = 2 };
 
 /* Flags. */
 enum {
@@ -170,6 +171,37 @@ int qkmla_append_rope(const float* c_new, const float* k_rope_raw, const int32_t
                       void* ak_cache, int64_t num_slots, void* stream);
 
 /*
+ * qkmla_append_q8 -- write new tokens into the 8-bit latent cache.
+ *
+ * The cache of the pages' method (latent, alpha^k, RoPE key) with the latent in
+ * e4m3 (4 exponent, 3 mantissa bits, largest value 448) and one fp32 scale a
+ * token.  The latent is the cache's only "head", and a scale covers one token:
+ * outlier tokens (tens of times the others) would otherwise take the codes of
+ * their neighbours.  Scales are powers of two, so code x scale is exact.
+ *
+ * For each new token n with slot s = slot_mapping[n] (s < 0: skipped):
+ *   kv_scale[s]    = 2^e, the least with max_j |c_new[n][j]| <= 448 2^e (at least
+ *                    2^-126); 0 for an all-zero latent
+ *   kv[s][0:d_c]   = e4m3(c_new[n] / kv_scale[s]), round to nearest even; a value
+ *                    that is not finite is stored as NaN
+ *   ak[s][g]       = 1 / sqrt(mean_j (c^ W^K_g)_j^2 + eps)  with c^ the stored
+ *                    latent (code x scale)
+ *   kv[s][d_c:]    = bf16(RoPE key, rotated by positions[n] if positions is given,
+ *                    normalised) as qkmla_append / qkmla_append_rope store it
+ * kv_cache [num_slots][d_c + 2 d_r] bytes: d_c codes, then d_r bf16 values.
+ * kv_scale [num_slots] fp32.  ak_cache as in qkmla_append.  positions [N] int32
+ * or NULL (k_rope_new is already rotated; rope_theta is then ignored).
+ * PLAIN_MLA: the raw RoPE key is stored and ak = 1.
+ * A slot >= num_slots is a device-side bounds error (skipped, status set).
+ * N == 0 is a no-op.  Errors: INVALID for null pointers, sizes, odd d_c, d_h >
+ * 256, misaligned bases; UNSUPPORTED for d_c > 512 or d_r > 64.
+ */
+int qkmla_append_q8(const float* c_new, const float* k_rope_new, const int32_t* positions, float rope_theta,
+                    const float* w_k, const float* gamma_rope_k, const int64_t* slot_mapping, int N, int G, int d_c,
+                    int d_h, int d_r, float eps, unsigned flags, void* kv_cache, float* kv_scale, void* ak_cache,
+                    int64_t num_slots, void* stream);
+
+/*
  * qkmla_project_query -- the query projection ahead of qkmla_absorb_query,
  * with the RoPE rotation of the RoPE block fused in.
  * Source: thelatestinai.com abstract (the static key weight is absorbed into
@@ -245,6 +277,41 @@ size_t qkmla_decode_workspace_size(const qkmla_decode_args* a);
  * affected rows are then undefined.
  */
 int qkmla_decode(const qkmla_decode_args* a, void* stream);
+
+/* What qkmla_decode_ext takes besides qkmla_decode_args. */
+typedef struct qkmla_decode_ext_args {
+    const float* kv_scale;      /* [num_slots] fp32, with cache_dtype QKMLA_E4M3 only (else NULL) */
+    int window;                 /* 0: every token; w >= 1: the last w tokens of each query */
+    int sinks;                  /* with a window: the first tokens that stay visible */
+} qkmla_decode_ext_args;
+
+/*
+ * qkmla_decode_ext -- qkmla_decode over an 8-bit cache, through a sliding window
+ * with sinks, or both.
+ *
+ * 8-bit cache (cache_dtype QKMLA_E4M3): kv_cache and kv_scale as
+ * qkmla_append_q8 writes them; q_tilde is bf16.  The stored latent is
+ * c^_t = kv_scale_t x codes_t, in the logits and in the output; everything else
+ * is qkmla_decode's definition.
+ *
+ * Window w, sinks f: query i of sequence b, of causal length n = seq_lens[b] -
+ * s_q + i + 1, attends to the tokens t < n with t < f or t >= n - w.  Tokens
+ * outside are neither read nor do their page-table entries matter, except in
+ * tiles that a visible token shares; no value stored there (NaN included)
+ * reaches the result.
+ *
+ * With an 8-bit cache or a window, seq_lens[b] may be anything from 0 to
+ * max_pages * page_size: a query without a visible token (an idle batch slot)
+ * gives o = 0 and lse = -inf.  With neither, the call is qkmla_decode.
+ * The workspace size, the kernel's name and the launches come from the _ext
+ * forms of their calls.  Errors: as qkmla_decode, and INVALID for a null
+ * argument block, a negative window or sinks, sinks without a window, kv_scale
+ * without QKMLA_E4M3 or the reverse, or an odd d_c with QKMLA_E4M3.
+ */
+int qkmla_decode_ext(const qkmla_decode_args* a, const qkmla_decode_ext_args* e, void* stream);
+size_t qkmla_decode_ext_workspace_size(const qkmla_decode_args* a, const qkmla_decode_ext_args* e);
+const char* qkmla_decode_ext_kernel_name(const qkmla_decode_args* a, const qkmla_decode_ext_args* e);
+int qkmla_decode_ext_launch_count(const qkmla_decode_args* a, const qkmla_decode_ext_args* e);
 
 /*
  * qkmla_get_device_status -- synchronise `stream`, return and clear the

@@ -5,9 +5,11 @@ kernels behind the C ABI declared in include/qkmla.h.  PyTorch provides device
 memory and streams.  There is no fallback: if the shared library is missing
 or a call fails, an exception is raised.
 
-Calls: absorb_query, append, decode (or make_decode_args + decode_raw to keep
-one argument block); prepare_absorb_query / prepare_append return a Prepared
-call whose arguments are marshalled once, for loops over fixed buffers.
+Calls: absorb_query, append (append_q8 for the 8-bit cache), decode -- over any
+of the caches, whole or through a window with sinks -- (or make_decode_args +
+decode_raw to keep one argument block); prepare_absorb_query / prepare_append /
+prepare_append_q8 / prepare_decode return a prepared call whose arguments are
+marshalled once, for loops over fixed buffers.
 """
 from __future__ import annotations
 
@@ -19,7 +21,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libqkmla.so")
 
 OK, ERR_INVALID, ERR_UNSUPPORTED, ERR_CUDA, ERR_WORKSPACE, ERR_DEVICE_BOUNDS, ERR_TIMEOUT = 0, -1, -2, -3, -4, -5, -6
-F32, BF16 = 0, 1
+F32, BF16, E4M3 = 0, 1, 2
 FLAG_PLAIN_MLA = 1
 FLAG_FORCE_SIMT = 2
 FLAG_TEST_STALL = 4
@@ -29,6 +31,8 @@ SYMBOLS = [
     "qkmla_absorb_query", "qkmla_append", "qkmla_decode_workspace_size", "qkmla_decode",
     "qkmla_get_device_status", "qkmla_status_string", "qkmla_version", "qkmla_decode_kernel_name",
     "qkmla_decode_launch_count", "qkmla_up_project", "qkmla_append_rope", "qkmla_project_query",
+    "qkmla_append_q8", "qkmla_decode_ext", "qkmla_decode_ext_workspace_size", "qkmla_decode_ext_kernel_name",
+    "qkmla_decode_ext_launch_count",
 ]
 
 
@@ -71,6 +75,15 @@ class DecodeArgs(ctypes.Structure):
     ]
 
 
+class DecodeExtArgs(ctypes.Structure):
+    """Mirror of `qkmla_decode_ext_args` in include/qkmla.h (same field order)."""
+    _fields_ = [
+        ("kv_scale", ctypes.c_void_p),
+        ("window", ctypes.c_int),
+        ("sinks", ctypes.c_int),
+    ]
+
+
 _lib: Optional[ctypes.CDLL] = None
 
 
@@ -106,6 +119,17 @@ def lib() -> ctypes.CDLL:
         L.qkmla_append_rope.restype = i
         L.qkmla_project_query.argtypes = [vp, vp, vp, f, i, i, i, i, i, vp, vp, vp]
         L.qkmla_project_query.restype = i
+        L.qkmla_append_q8.argtypes = [vp, vp, vp, f, vp, vp, vp, i, i, i, i, i, f, u, vp, vp, vp, i64, vp]
+        L.qkmla_append_q8.restype = i
+        pa, px = ctypes.POINTER(DecodeArgs), ctypes.POINTER(DecodeExtArgs)
+        L.qkmla_decode_ext.argtypes = [pa, px, vp]
+        L.qkmla_decode_ext.restype = i
+        L.qkmla_decode_ext_workspace_size.argtypes = [pa, px]
+        L.qkmla_decode_ext_workspace_size.restype = sz
+        L.qkmla_decode_ext_kernel_name.argtypes = [pa, px]
+        L.qkmla_decode_ext_kernel_name.restype = ctypes.c_char_p
+        L.qkmla_decode_ext_launch_count.argtypes = [pa, px]
+        L.qkmla_decode_ext_launch_count.restype = i
         if hasattr(L, "qkmla_decode_noalloc"):
             L.qkmla_decode_noalloc.argtypes = [ctypes.POINTER(DecodeArgs), vp]
             L.qkmla_decode_noalloc.restype = i
@@ -238,6 +262,38 @@ def append_rope(c_new, k_rope_raw, positions, rope_theta: float, w_k, gamma_rope
                         ak_cache, eps, plain)(stream)
 
 
+def prepare_append_q8(c_new, k_rope_new, w_k, gamma_rope_k, slot_mapping, kv_cache, kv_scale, ak_cache, eps: float,
+                      positions=None, rope_theta: float = 0.0, plain: bool = False) -> Prepared:
+    """qkmla_append_q8 for fixed tensors (see append_q8)."""
+    N, d_c = c_new.shape
+    d_r = k_rope_new.shape[1] if k_rope_new is not None else 0
+    G, _, d_h = w_k.shape
+    _check_q8_cache(kv_cache, kv_scale, d_c, d_r)
+    flags = (FLAG_PLAIN_MLA if plain else 0) | _alpha_flag(ak_cache)
+    return Prepared("qkmla_append_q8",
+                    (_ptr(c_new), _ptr(k_rope_new), _ptr(positions), float(rope_theta), _ptr(w_k), _ptr(gamma_rope_k),
+                     _ptr(slot_mapping), N, G, d_c, d_h, d_r, float(eps), flags, _ptr(kv_cache), _ptr(kv_scale),
+                     _ptr(ak_cache), kv_cache.shape[0]))
+
+
+def append_q8(c_new, k_rope_new, w_k, gamma_rope_k, slot_mapping, kv_cache, kv_scale, ak_cache, eps: float,
+              positions=None, rope_theta: float = 0.0, plain: bool = False, stream=None):
+    """append() into the 8-bit cache: kv_cache [num_slots, d_c + 2 d_r] uint8 (e4m3 codes, then the
+    RoPE key in bf16), kv_scale [num_slots] fp32 (a power of two per token), ak_cache as in append().
+    With positions [N] (int32) and rope_theta the RoPE keys come unrotated, as in append_rope()."""
+    prepare_append_q8(c_new, k_rope_new, w_k, gamma_rope_k, slot_mapping, kv_cache, kv_scale, ak_cache, eps, positions,
+                      rope_theta, plain)(stream)
+
+
+def _check_q8_cache(kv_cache, kv_scale, d_c: int, d_r: int) -> None:
+    torch = _torch()
+    if kv_cache.dtype != torch.uint8 or kv_cache.shape[1] != d_c + 2 * d_r:
+        raise ValueError(f"qkmla: the 8-bit cache is uint8 [num_slots, d_c + 2 d_r], not {kv_cache.dtype} "
+                         f"{tuple(kv_cache.shape)}")
+    if kv_scale is None or kv_scale.dtype != torch.float32 or kv_scale.numel() != kv_cache.shape[0]:
+        raise ValueError("qkmla: the 8-bit cache needs kv_scale, float32 [num_slots]")
+
+
 def prepare_project_query(x, w_q, positions, rope_theta: float, q, q_rope) -> Prepared:
     """qkmla_project_query for fixed tensors: x [rows, d_x] bf16, w_q [H, d_h + d_r, d_x] bf16,
     positions [rows] int32 -> q [rows, H, d_h] fp32, q_rope [rows, H, d_r] fp32 (rotated)."""
@@ -267,7 +323,7 @@ def make_decode_args(q_tilde, alpha_q, q_rope, gamma_rope_q, kv_cache, ak_cache,
     a.num_slots = kv_cache.shape[0]
     a.page_size, a.max_pages = int(page_size), int(max_pages)
     a.B, a.s_q, a.H, a.G, a.d_c, a.d_r = B, s_q, H, int(G), d_c, d_r
-    a.cache_dtype = _dtype_code(kv_cache.dtype)
+    a.cache_dtype = E4M3 if kv_cache.dtype == _torch().uint8 else _dtype_code(kv_cache.dtype)
     a.softmax_scale, a.eps = float(softmax_scale), float(eps)
     a.flags = (FLAG_PLAIN_MLA if plain else 0) | (FLAG_FORCE_SIMT if force_simt else 0) | _alpha_flag(ak_cache)
     a.num_splits = int(num_splits)
@@ -296,9 +352,18 @@ def decode_raw(args: DecodeArgs, stream=None) -> None:
 
 def decode(q_tilde, alpha_q, q_rope, gamma_rope_q, kv_cache, ak_cache, seq_lens, page_table, page_size: int,
            max_pages: int, G: int, softmax_scale: float, eps: float, o, lse, plain: bool = False,
-           force_simt: bool = False, num_splits: int = 0, workspace=None, stream=None):
-    """QK-Normed MLA decode; allocates the workspace with torch when none is given."""
+           force_simt: bool = False, num_splits: int = 0, workspace=None, stream=None, kv_scale=None,
+           window: int = 0, sinks: int = 0):
+    """QK-Normed MLA decode; allocates the workspace with torch when none is given.
+
+    kv_scale: the scales of an 8-bit kv_cache (see append_q8; q_tilde is then bf16).  window > 0: each
+    query sees its last `window` tokens and the sequence's first `sinks`."""
     torch = _torch()
+    if kv_scale is not None or window or sinks:
+        prepare_decode(q_tilde, alpha_q, q_rope, gamma_rope_q, kv_cache, ak_cache, seq_lens, page_table, page_size,
+                       max_pages, G, softmax_scale, eps, o, lse, plain, force_simt, num_splits, workspace, kv_scale,
+                       window, sinks)(stream)
+        return o, lse
     a = make_decode_args(q_tilde, alpha_q, q_rope, gamma_rope_q, kv_cache, ak_cache, seq_lens, page_table,
                          page_size, max_pages, G, softmax_scale, eps, o, lse, plain, force_simt, num_splits,
                          workspace)
@@ -308,6 +373,54 @@ def decode(q_tilde, alpha_q, q_rope, gamma_rope_q, kv_cache, ak_cache, seq_lens,
         a.workspace, a.workspace_bytes = workspace.data_ptr(), need
     decode_raw(a, stream)
     return o, lse
+
+
+class PreparedDecode:
+    """One qkmla_decode / qkmla_decode_ext call with its arguments marshalled and its workspace
+    allocated once: the tensors must stay alive and in place; a call only adds the stream.  Calls that
+    may overlap on the GPU need a PreparedDecode (a workspace) each."""
+
+    def __init__(self, args: DecodeArgs, ext: Optional[DecodeExtArgs], workspace, device):
+        torch = _torch()
+        self.args, self.ext = args, ext
+        self.name = "qkmla_decode" if ext is None else "qkmla_decode_ext"
+        self.refs = (ctypes.byref(args),) if ext is None else (ctypes.byref(args), ctypes.byref(ext))
+        need = int(getattr(lib(), self.name + "_workspace_size")(*self.refs))
+        if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
+            workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        self.workspace = workspace
+        if workspace is not None:
+            args.workspace, args.workspace_bytes = _ptr(workspace), workspace.numel() * workspace.element_size()
+        self.fn = getattr(lib(), self.name)
+
+    @property
+    def kernel_name(self) -> str:
+        return getattr(lib(), self.name + "_kernel_name")(*self.refs).decode()
+
+    @property
+    def launch_count(self) -> int:
+        return int(getattr(lib(), self.name + "_launch_count")(*self.refs))
+
+    def __call__(self, stream=None) -> None:
+        _check(self.name, self.fn(*self.refs, _stream(stream)))
+
+
+def prepare_decode(q_tilde, alpha_q, q_rope, gamma_rope_q, kv_cache, ak_cache, seq_lens, page_table, page_size: int,
+                   max_pages: int, G: int, softmax_scale: float, eps: float, o, lse, plain: bool = False,
+                   force_simt: bool = False, num_splits: int = 0, workspace=None, kv_scale=None, window: int = 0,
+                   sinks: int = 0) -> PreparedDecode:
+    """decode() for fixed tensors (see decode)."""
+    torch = _torch()
+    a = make_decode_args(q_tilde, alpha_q, q_rope, gamma_rope_q, kv_cache, ak_cache, seq_lens, page_table, page_size,
+                         max_pages, G, softmax_scale, eps, o, lse, plain, force_simt, num_splits)
+    ext = None
+    if kv_scale is not None or window or sinks or a.cache_dtype == E4M3:
+        if a.cache_dtype == E4M3:
+            _check_q8_cache(kv_cache, kv_scale, a.d_c, a.d_r)
+            if q_tilde.dtype != torch.bfloat16:
+                raise ValueError(f"qkmla: with an 8-bit cache q_tilde is bfloat16, not {q_tilde.dtype}")
+        ext = DecodeExtArgs(_ptr(kv_scale), int(window), int(sinks))
+    return PreparedDecode(a, ext, workspace, q_tilde.device)
 
 
 def prepare_up_project(o, w_v, out) -> Prepared:

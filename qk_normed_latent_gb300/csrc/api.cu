@@ -3,6 +3,7 @@
 // Every call validates on the host before launching anything and returns a
 // QKMLA_* code; nothing here allocates device memory except the per-device
 // status word, a static __device__ variable.
+#include <algorithm>
 #include <mutex>
 
 #include "common.cuh"
@@ -44,15 +45,19 @@ int* device_status_ptr() {
     return g_status_ptr[dev];
 }
 
-static int validate_decode(const qkmla_decode_args* a) {
+static int validate_decode(const qkmla_decode_args* a, const DecodeExt& x) {
     if (!a) return QKMLA_ERR_INVALID;
+    if (x.window < 0 || x.sinks < 0 || (x.sinks > 0 && x.window == 0)) return QKMLA_ERR_INVALID;
+    const bool q8 = a->cache_dtype == QKMLA_E4M3;
+    if (!q8 && x.kv_scale) return QKMLA_ERR_INVALID;
     const bool plain = (a->flags & QKMLA_FLAG_PLAIN_MLA) != 0;
     if (a->B < 1 || a->s_q < 1 || a->H < 1 || a->G < 1 || a->d_c < 1 || a->d_r < 0) return QKMLA_ERR_INVALID;
     if (a->H % a->G) return QKMLA_ERR_INVALID;
     if (a->page_size < 1 || a->max_pages < 1 || a->num_slots < 1 || a->num_slots % a->page_size)
         return QKMLA_ERR_INVALID;
     if (a->num_splits < 0 || a->num_splits > 1024) return QKMLA_ERR_INVALID;
-    if (a->cache_dtype != QKMLA_F32 && a->cache_dtype != QKMLA_BF16) return QKMLA_ERR_UNSUPPORTED;
+    if (a->cache_dtype != QKMLA_F32 && a->cache_dtype != QKMLA_BF16 && !(q8 && x.kv_scale)) return QKMLA_ERR_UNSUPPORTED;
+    if (q8 && (a->d_c % 2 || !aligned(x.kv_scale, 4))) return QKMLA_ERR_INVALID;
     if (a->o_dtype != QKMLA_F32 && a->o_dtype != QKMLA_BF16) return QKMLA_ERR_UNSUPPORTED;
     if (!a->q_tilde || !a->kv_cache || !a->seq_lens || !a->o) return QKMLA_ERR_INVALID;
     if (!plain && (!a->alpha_q || !a->ak_cache)) return QKMLA_ERR_INVALID;
@@ -66,13 +71,14 @@ static int validate_decode(const qkmla_decode_args* a) {
     return QKMLA_OK;
 }
 
-int plan_decode(const qkmla_decode_args* a, DecodePlan* plan) {
-    const int v = validate_decode(a);
+int plan_decode(const qkmla_decode_args* a, const DecodeExt& x, DecodePlan* plan) {
+    const int v = validate_decode(a, x);
     if (v != QKMLA_OK) return v;
     const int sms = device_sm_count();
     if (sms <= 0) return QKMLA_ERR_CUDA;
     const bool stall = (a->flags & QKMLA_FLAG_TEST_STALL) != 0;
-    if (!(a->flags & QKMLA_FLAG_FORCE_SIMT) && tc_supported(a) && a->num_splits <= 256) {
+    if (stall && x.active()) return QKMLA_ERR_UNSUPPORTED;
+    if (!(a->flags & QKMLA_FLAG_FORCE_SIMT) && !x.active() && tc_supported(a) && a->num_splits <= 256) {
         if (stall && pair_shape(a)) return QKMLA_ERR_UNSUPPORTED;   // the hook exists in the 64-row kernel only
         plan->kernel = 1;
         plan->num_splits = a->num_splits;
@@ -85,7 +91,8 @@ int plan_decode(const qkmla_decode_args* a, DecodePlan* plan) {
     int ns = a->num_splits;
     if (ns == 0) {
         const int64_t base = (int64_t)a->B * a->s_q * a->G;
-        const int64_t max_len = (int64_t)a->max_pages * a->page_size;
+        int64_t max_len = (int64_t)a->max_pages * a->page_size;
+        if (x.window > 0) max_len = std::min(max_len, (int64_t)x.window + x.sinks);
         int64_t want = (2LL * sms + base - 1) / base;
         const int64_t cap = (max_len + 255) / 256;
         if (want > cap) want = cap;
@@ -171,33 +178,98 @@ int qkmla_append_rope(const float* c_new, const float* k_rope_raw, const int32_t
                          rope_theta, (cudaStream_t)stream);
 }
 
-size_t qkmla_decode_workspace_size(const qkmla_decode_args* a) {
+int qkmla_append_q8(const float* c_new, const float* k_rope_new, const int32_t* positions, float rope_theta,
+                    const float* w_k, const float* gamma_rope_k, const int64_t* slot_mapping, int N, int G, int d_c,
+                    int d_h, int d_r, float eps, unsigned flags, void* kv_cache, float* kv_scale, void* ak_cache,
+                    int64_t num_slots, void* stream) {
+    const bool plain = (flags & QKMLA_FLAG_PLAIN_MLA) != 0;
+    if (N < 0 || G < 1 || d_c < 1 || d_h < 1 || d_r < 0 || num_slots < 1) return QKMLA_ERR_INVALID;
+    if (d_h > 256 || d_c % 2 || !(eps >= 0.f)) return QKMLA_ERR_INVALID;
+    if (d_c > 512 || d_r > 64) return QKMLA_ERR_UNSUPPORTED;
+    if (N == 0) return QKMLA_OK;
+    if (positions && d_r > 0 && (!(rope_theta > 1.f) || d_r % 2)) return QKMLA_ERR_INVALID;
+    if (!c_new || !w_k || !slot_mapping || !kv_cache || !kv_scale || !ak_cache) return QKMLA_ERR_INVALID;
+    if (d_r > 0 && !k_rope_new) return QKMLA_ERR_INVALID;
+    if (!aligned(kv_cache, 2) || !aligned(kv_scale, 4)) return QKMLA_ERR_INVALID;
+    const bool ak_f16 = !plain && (flags & QKMLA_FLAG_ALPHA_F16) != 0;
+    return launch_append_q8(c_new, k_rope_new, w_k, gamma_rope_k, slot_mapping, N, G, d_c, d_h, d_r, eps, plain,
+                            (uint8_t*)kv_cache, kv_scale, ak_cache, ak_f16, num_slots, d_r > 0 ? positions : nullptr,
+                            rope_theta, (cudaStream_t)stream);
+}
+
+}  // extern "C"
+
+namespace {
+
+size_t workspace_size(const qkmla_decode_args* a, const DecodeExt& x) {
     DecodePlan plan;
-    if (plan_decode(a, &plan) != QKMLA_OK) return 0;
+    if (plan_decode(a, x, &plan) != QKMLA_OK) return 0;
     return plan.ws_bytes;
 }
 
-const char* qkmla_decode_kernel_name(const qkmla_decode_args* a) {
+const char* kernel_name(const qkmla_decode_args* a, const DecodeExt& x) {
     DecodePlan plan;
-    if (plan_decode(a, &plan) != QKMLA_OK) return "invalid";
+    if (plan_decode(a, x, &plan) != QKMLA_OK) return "invalid";
     return plan.kernel == 1 ? "tcgen05" : "simt";
 }
 
-int qkmla_decode_launch_count(const qkmla_decode_args* a) {
+int launch_count(const qkmla_decode_args* a, const DecodeExt& x) {
     DecodePlan plan;
-    if (plan_decode(a, &plan) != QKMLA_OK) return 0;
+    if (plan_decode(a, x, &plan) != QKMLA_OK) return 0;
     if (plan.kernel == 1) return sched_in_kernel(a) ? 2 : 3;   // [scheduler,] decode, combine
     return plan.parts > 1 ? 2 : 1;
 }
 
-int qkmla_decode(const qkmla_decode_args* a, void* stream) {
+int decode(const qkmla_decode_args* a, const DecodeExt& x, void* stream) {
     DecodePlan plan;
-    const int rc = plan_decode(a, &plan);
+    const int rc = plan_decode(a, x, &plan);
     if (rc != QKMLA_OK) return rc;
     if (plan.ws_bytes > 0 && (!a->workspace || a->workspace_bytes < plan.ws_bytes)) return QKMLA_ERR_WORKSPACE;
     if (plan.ws_bytes > 0 && !aligned(a->workspace, 16)) return QKMLA_ERR_INVALID;
     if (plan.kernel == 1) return launch_decode_tc(a, plan, (cudaStream_t)stream);
-    return launch_decode_simt(a, plan, (cudaStream_t)stream);
+    return launch_decode_simt(a, x, plan, (cudaStream_t)stream);
+}
+
+// The caller's extension as the library's; false for one the cache type cannot have.
+bool read_ext(const qkmla_decode_args* a, const qkmla_decode_ext_args* e, DecodeExt* x) {
+    *x = DecodeExt{};
+    if (!a || !e) return false;
+    x->kv_scale = e->kv_scale;
+    x->window = e->window;
+    x->sinks = e->sinks;
+    return (a->cache_dtype == QKMLA_E4M3) == (e->kv_scale != nullptr);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t qkmla_decode_workspace_size(const qkmla_decode_args* a) { return workspace_size(a, DecodeExt{}); }
+
+const char* qkmla_decode_kernel_name(const qkmla_decode_args* a) { return kernel_name(a, DecodeExt{}); }
+
+int qkmla_decode_launch_count(const qkmla_decode_args* a) { return launch_count(a, DecodeExt{}); }
+
+int qkmla_decode(const qkmla_decode_args* a, void* stream) { return decode(a, DecodeExt{}, stream); }
+
+size_t qkmla_decode_ext_workspace_size(const qkmla_decode_args* a, const qkmla_decode_ext_args* e) {
+    DecodeExt x;
+    return read_ext(a, e, &x) ? workspace_size(a, x) : 0;
+}
+
+const char* qkmla_decode_ext_kernel_name(const qkmla_decode_args* a, const qkmla_decode_ext_args* e) {
+    DecodeExt x;
+    return read_ext(a, e, &x) ? kernel_name(a, x) : "invalid";
+}
+
+int qkmla_decode_ext_launch_count(const qkmla_decode_args* a, const qkmla_decode_ext_args* e) {
+    DecodeExt x;
+    return read_ext(a, e, &x) ? launch_count(a, x) : 0;
+}
+
+int qkmla_decode_ext(const qkmla_decode_args* a, const qkmla_decode_ext_args* e, void* stream) {
+    DecodeExt x;
+    return read_ext(a, e, &x) ? decode(a, x, stream) : QKMLA_ERR_INVALID;
 }
 
 int qkmla_get_device_status(void* stream) {

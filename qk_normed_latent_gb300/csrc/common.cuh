@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <cuda_fp8.h>
 #include <stdint.h>
 
 #include "../../include/qkmla.h"
@@ -35,6 +36,47 @@ template <> struct Elem<__nv_bfloat16> {
     static __device__ __forceinline__ float load(const __nv_bfloat16* p) { return __bfloat162float(*p); }
     static __device__ __forceinline__ float cast(float x) { return __bfloat162float(__float2bfloat16_rn(x)); }
     static __device__ __forceinline__ void store(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+};
+
+// The 8-bit latent cache: a row is d_c e4m3 codes, then d_r bf16 RoPE values.
+struct E4M3 {};
+
+__device__ __forceinline__ float e4m3_to_float(uint8_t v) {
+    return __half2float(__half(__nv_cvt_fp8_to_halfraw(v, __NV_E4M3)));
+}
+
+// Power-of-two scale of a latent with largest magnitude `top`: the least 2^e with
+// top <= 448 2^e (448 = 0.875 2^9 is the largest e4m3 value), 0 for a zero latent.
+// e4m3 is a floating-point format, so a power of two loses nothing against
+// top / 448 but up to one binade of its 2^-9..448 range, and makes c / s, s x and
+// every later product with s exact.
+__device__ __forceinline__ float e4m3_scale(float top, float* inv) {
+    if (!(top > 0.f)) { *inv = 0.f; return 0.f; }
+    int k;
+    const float m = frexpf(fminf(top, 3.402823466e38f), &k);   // top = m 2^k, 0.5 <= m < 1
+    const int e = max(k - (m <= 0.875f ? 9 : 8), -126);
+    *inv = ldexpf(1.f, -e);
+    return ldexpf(1.f, e);
+}
+// Code of c with the scale 1 / inv; a value that is not finite becomes NaN.
+__device__ __forceinline__ uint8_t e4m3_code(float c, float inv) {
+    if (!isfinite(c)) return 0x7F;
+    return (uint8_t)__nv_cvt_float_to_fp8(c * inv, __NV_SATFINITE, __NV_E4M3);
+}
+
+// Tokens a query of causal length n sees through a window with sinks: all of them
+// (window 0, or nothing between the sinks and the window), else [0, sinks) and
+// [n - window, n), numbered 0 .. count - 1 without the gap.
+struct VisibleRange {
+    int count, head, gap;
+    __host__ __device__ __forceinline__ VisibleRange(int n, int window, int sinks) {
+        const int first = n - window;
+        const bool cut = window > 0 && first > sinks;
+        head = cut ? sinks : n;
+        gap = cut ? first - sinks : 0;
+        count = n - gap;
+    }
+    __host__ __device__ __forceinline__ int token(int u) const { return u < head ? u : u + gap; }
 };
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -114,13 +156,23 @@ struct DecodePlan {
     int parts;             // number of partial (o, lse) records in the workspace
     size_t ws_bytes;
 };
-int plan_decode(const qkmla_decode_args* a, DecodePlan* plan);
-int launch_decode_simt(const qkmla_decode_args* a, const DecodePlan& plan, cudaStream_t s);
+// qkmla_decode_ext's additions (all zero for qkmla_decode).
+struct DecodeExt {
+    const float* kv_scale;
+    int window, sinks;
+    bool active() const { return kv_scale != nullptr || window > 0; }
+};
+int plan_decode(const qkmla_decode_args* a, const DecodeExt& x, DecodePlan* plan);
+int launch_decode_simt(const qkmla_decode_args* a, const DecodeExt& x, const DecodePlan& plan, cudaStream_t s);
 int launch_decode_tc(const qkmla_decode_args* a, const DecodePlan& plan, cudaStream_t s);
 bool tc_supported(const qkmla_decode_args* a);
 bool pair_shape(const qkmla_decode_args* a);        // served by the two-CTA cluster kernel
 bool sched_in_kernel(const qkmla_decode_args* a);   // split plan computed by the decode kernels themselves
 size_t tc_workspace(const qkmla_decode_args* a, int sms, int* max_items_out);
+int launch_append_q8(const float* c_new, const float* r_new, const float* wk, const float* grk, const int64_t* slots,
+                     int N, int G, int d_c, int d_h, int d_r, float eps, bool plain, uint8_t* kv, float* kv_scale,
+                     void* ak, bool ak_f16, int64_t num_slots, const int32_t* positions, float rope_theta,
+                     cudaStream_t s);
 int launch_combine(const float* o_part, const float* lse_part, int rows, int nsplit, int d_c, void* o,
                    int o_dtype, float* lse, cudaStream_t s);
 int device_sm_count();

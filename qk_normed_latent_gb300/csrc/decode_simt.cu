@@ -1,4 +1,6 @@
-// CUDA-core decode kernel (any cache dtype; the only path for an fp32 cache).
+// CUDA-core decode kernel (any cache type; the only path for an fp32 cache, and
+// for shapes of the 8-bit cache and of windowed calls that the tensor-core
+// kernels are not built for).
 //
 // Source: "QK-Normed MLA: QK normalization without full key caching", Technical
 // Summary, Methodology -- decode-logit equation l = (q~ . c_t) alpha^q alpha^k_{t,g(h)}
@@ -12,6 +14,9 @@
 // are staged 32 at a time in shared memory (fp32); logits, an online softmax
 // (running max / sum in the exp2 domain) and the latent accumulation follow.
 // fp32 arithmetic throughout.
+//
+// A windowed row walks its visible tokens only: the first `sinks`, then the last
+// `window`, numbered without the gap between them.
 #include "common.cuh"
 
 namespace qkmla {
@@ -28,6 +33,7 @@ struct SimtParams {
     const float* grq;
     const void* kv;
     const void* ak;     // fp32, or fp16 when ak_f16
+    const float* kv_scale;  // [num_slots] (8-bit cache)
     const int32_t* seq_lens;
     const int32_t* page_table;
     int64_t num_pages;
@@ -36,6 +42,8 @@ struct SimtParams {
     float scale, eps;
     int plain;
     int ak_f16;
+    int window, sinks;  // window 0: every token up to the causal length
+    int allow_short;    // lengths below s_q leave rows without a token instead of being an error
     int nsplit;
     float* o_part;      // [rows*H][nsplit][d_c] when nsplit > 1
     float* lse_part;    // [rows*H][nsplit]
@@ -43,6 +51,24 @@ struct SimtParams {
     int o_dtype;
     float* lse;
     int* status;
+};
+
+// Element k of the cache row in slot s as fp32, and the query's element type.
+template <typename CT>
+struct Row {
+    using QT = CT;
+    static __device__ __forceinline__ float load(const SimtParams& p, int64_t s, int k) {
+        return Elem<CT>::load((const CT*)p.kv + s * (p.d_c + p.d_r) + k);
+    }
+};
+template <>
+struct Row<E4M3> {
+    using QT = __nv_bfloat16;
+    static __device__ __forceinline__ float load(const SimtParams& p, int64_t s, int k) {
+        const uint8_t* row = (const uint8_t*)p.kv + s * (p.d_c + 2 * p.d_r);
+        if (k < p.d_c) return e4m3_to_float(row[k]) * p.kv_scale[s];
+        return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(row + p.d_c)[k - p.d_c]);
+    }
 };
 
 template <typename CT, int HPG, int NJ>
@@ -68,16 +94,18 @@ decode_simt_kernel(SimtParams p) {
     const int b = bi / p.s_q, i = bi % p.s_q;
     const int sp = blockIdx.y;
     const int h0 = g * HPG;
-    const CT* qt = (const CT*)p.qt;
-    const CT* kv = (const CT*)p.kv;
+    using QT = typename Row<CT>::QT;
+    const QT* qt = (const QT*)p.qt;
     const float l2e = kLog2e;
 
     pdl_wait();
     pdl_trigger();
     const int seq_len = p.seq_lens[b];
-    const bool bad_len = seq_len < p.s_q || seq_len > p.max_pages * p.page_size;
+    const bool bad_len = seq_len < (p.allow_short ? 0 : p.s_q) || seq_len > p.max_pages * p.page_size;
     if (bad_len && tid == 0) report(p.status, QKMLA_ERR_DEVICE_BOUNDS);
-    const int L = bad_len ? 0 : seq_len - p.s_q + i + 1;
+    const int n_causal = bad_len ? 0 : max(0, seq_len - p.s_q + i + 1);
+    const VisibleRange vis(n_causal, p.window, p.sinks);
+    const int L = vis.count;
     int chunk = (L + p.nsplit - 1) / p.nsplit;
     chunk = (chunk + kTC - 1) / kTC * kTC;
     const int t0 = sp * chunk, t1 = min(L, t0 + chunk);
@@ -85,7 +113,7 @@ decode_simt_kernel(SimtParams p) {
     // stage the query rows: q~ in fp32, the RoPE query normalised per head
     for (int e = tid; e < HPG * p.d_c; e += kThreads) {
         const int hl = e / p.d_c, k = e % p.d_c;
-        qs[hl * row + k] = Elem<CT>::load(qt + (((int64_t)bi * p.H) + h0 + hl) * p.d_c + k);
+        qs[hl * row + k] = Elem<QT>::load(qt + (((int64_t)bi * p.H) + h0 + hl) * p.d_c + k);
     }
     for (int hl = warp; hl < HPG; hl += kThreads / 32) {
         const float* src = p.qr + (((int64_t)bi * p.H) + h0 + hl) * p.d_r;
@@ -115,14 +143,14 @@ decode_simt_kernel(SimtParams p) {
     for (int tb = t0; tb < t1; tb += kTC) {
         __syncthreads();
         if (tid < kTC) {
-            const int t = tb + tid;
-            slot[tid] = (t < t1) ? slot_of(p.page_table, b, t, p.page_size, p.max_pages, p.num_pages, p.status) : -1;
+            const int t = vis.token(tb + tid);
+            slot[tid] = (tb + tid < t1) ? slot_of(p.page_table, b, t, p.page_size, p.max_pages, p.num_pages, p.status) : -1;
         }
         __syncthreads();
         for (int e = tid; e < kTC * row; e += kThreads) {
             const int tl = e / row, k = e % row;
             const int64_t s = slot[tl];
-            kvs[tl * ldk + k] = (s >= 0) ? Elem<CT>::load(kv + s * row + k) : 0.f;
+            kvs[tl * ldk + k] = (s >= 0) ? Row<CT>::load(p, s, k) : 0.f;
         }
         if (tid < kTC) {
             const int64_t s = slot[tid];
@@ -248,7 +276,7 @@ int launch_c(const SimtParams& p, int hpg, cudaStream_t s) {
 
 }  // namespace
 
-int launch_decode_simt(const qkmla_decode_args* a, const DecodePlan& plan, cudaStream_t s) {
+int launch_decode_simt(const qkmla_decode_args* a, const DecodeExt& x, const DecodePlan& plan, cudaStream_t s) {
     SimtParams p;
     p.qt = a->q_tilde;
     p.aq = a->alpha_q;
@@ -256,6 +284,10 @@ int launch_decode_simt(const qkmla_decode_args* a, const DecodePlan& plan, cudaS
     p.grq = a->gamma_rope_q;
     p.kv = a->kv_cache;
     p.ak = a->ak_cache;
+    p.kv_scale = x.kv_scale;
+    p.window = x.window;
+    p.sinks = x.sinks;
+    p.allow_short = x.active() ? 1 : 0;
     p.seq_lens = a->seq_lens;
     p.page_table = a->page_table;
     p.num_pages = a->num_slots / a->page_size;
@@ -275,7 +307,9 @@ int launch_decode_simt(const qkmla_decode_args* a, const DecodePlan& plan, cudaS
     p.lse = a->lse;
     p.status = device_status_ptr();
     const int hpg = a->H / a->G;
-    int rc = (a->cache_dtype == QKMLA_F32) ? launch_c<float>(p, hpg, s) : launch_c<__nv_bfloat16>(p, hpg, s);
+    const int rc = a->cache_dtype == QKMLA_F32    ? launch_c<float>(p, hpg, s)
+                   : a->cache_dtype == QKMLA_BF16 ? launch_c<__nv_bfloat16>(p, hpg, s)
+                                                  : launch_c<E4M3>(p, hpg, s);
     if (rc != QKMLA_OK || plan.num_splits == 1) return rc;
     return launch_combine(p.o_part, p.lse_part, (int)rows_h, plan.num_splits, a->d_c, a->o, a->o_dtype,
                           a->lse, s);
