@@ -83,10 +83,17 @@ int plan_decode(const qkmla_decode_args* a, const DecodeExt& x, DecodePlan* plan
         plan->kernel = 1;
         plan->num_splits = a->num_splits;
         plan->parts = 0;
-        plan->ws_bytes = tc_workspace(a, sms, nullptr);
+        plan->ws_bytes = tc_workspace(a, sms);
         return QKMLA_OK;
     }
     if (stall) return QKMLA_ERR_UNSUPPORTED;
+    if (!(a->flags & QKMLA_FLAG_FORCE_SIMT) && q8_tc_supported(a, x) && a->num_splits <= 256) {
+        plan->kernel = 1;
+        plan->num_splits = a->num_splits;
+        plan->parts = 0;
+        plan->ws_bytes = q8_tc_workspace(a, sms);
+        return QKMLA_OK;
+    }
     plan->kernel = 0;
     int ns = a->num_splits;
     if (ns == 0) {
@@ -226,6 +233,7 @@ int decode(const qkmla_decode_args* a, const DecodeExt& x, void* stream) {
     if (rc != QKMLA_OK) return rc;
     if (plan.ws_bytes > 0 && (!a->workspace || a->workspace_bytes < plan.ws_bytes)) return QKMLA_ERR_WORKSPACE;
     if (plan.ws_bytes > 0 && !aligned(a->workspace, 16)) return QKMLA_ERR_INVALID;
+    if (plan.kernel == 1 && x.kv_scale) return launch_decode_q8(a, x, (cudaStream_t)stream);
     if (plan.kernel == 1) return launch_decode_tc(a, plan, (cudaStream_t)stream);
     return launch_decode_simt(a, x, plan, (cudaStream_t)stream);
 }

@@ -168,7 +168,10 @@ int launch_decode_tc(const qkmla_decode_args* a, const DecodePlan& plan, cudaStr
 bool tc_supported(const qkmla_decode_args* a);
 bool pair_shape(const qkmla_decode_args* a);        // served by the two-CTA cluster kernel
 bool sched_in_kernel(const qkmla_decode_args* a);   // split plan computed by the decode kernels themselves
-size_t tc_workspace(const qkmla_decode_args* a, int sms, int* max_items_out);
+size_t tc_workspace(const qkmla_decode_args* a, int sms);
+bool q8_tc_supported(const qkmla_decode_args* a, const DecodeExt& x);   // 8-bit cache, tensor-core kernel
+size_t q8_tc_workspace(const qkmla_decode_args* a, int sms);
+int launch_decode_q8(const qkmla_decode_args* a, const DecodeExt& x, cudaStream_t s);
 int launch_append_q8(const float* c_new, const float* r_new, const float* wk, const float* grk, const int64_t* slots,
                      int N, int G, int d_c, int d_h, int d_r, float eps, bool plain, uint8_t* kv, float* kv_scale,
                      void* ak, bool ak_f16, int64_t num_slots, const int32_t* positions, float rope_theta,

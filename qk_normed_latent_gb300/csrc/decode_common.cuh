@@ -26,6 +26,28 @@ struct WorkItem {
 // Parameters of the split-KV schedule (see decode_sched.cuh).
 struct SchedArgs {
     int max_len, n_rb, sms, min_tokens, tile, fixed_splits;
+    int min_len;           // shortest valid length: s_q, or 0 where rows without a token are allowed
+    int window, sinks;     // 0, 0: every tile of the sequence
+};
+
+// Tiles of a sequence that some query of the step sees, numbered 0 .. count - 1:
+// `head` tiles from the start, then (past `gap` unseen tiles) those from the first
+// query's window on.
+struct TileRange {
+    int count, head, gap;
+    __host__ __device__ __forceinline__ TileRange(int len, int s_q, int window, int sinks, int tile) {
+        const int all = (len + tile - 1) / tile;
+        head = (min_(sinks, len) + tile - 1) / tile;
+        const int first = max_(0, len - s_q + 1 - window) / tile;     // first window tile of the first query
+        gap = window > 0 ? max_(0, first - head) : 0;
+        if (gap == 0) head = all;
+        count = all - gap;
+    }
+    __host__ __device__ __forceinline__ int tile(int j) const { return j < head ? j : j + gap; }
+
+private:
+    static __host__ __device__ __forceinline__ int min_(int a, int b) { return a < b ? a : b; }
+    static __host__ __device__ __forceinline__ int max_(int a, int b) { return a > b ? a : b; }
 };
 
 struct TcParams {
@@ -236,6 +258,20 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn();   // the driver's tensor-map enco
 bool make_map(CUtensorMap* m, const void* base, int64_t rows, int row_elems, int box_cols, int box_rows,
               CUtensorMapSwizzle sw);
 int launch_pair(const qkmla_decode_args* a, const TcParams& tp, int max_items, cudaStream_t s);
+
+// Split-KV scratch of a call with n_rb CTAs (row blocks) per tile range, laid out in
+// `ws` (null: sizes only).
+struct SplitScratch {
+    int max_items;
+    size_t bytes;
+    WorkItem* items;
+    int *n_items, *seq_nsplit, *seq_part0, *split_list;
+    float *o_part, *lse_part;
+};
+SplitScratch split_scratch(const qkmla_decode_args* a, int n_rb, int sms, void* ws);
+// The scheduler kernel (batches the decode kernels do not plan themselves) and the merge of split rows.
+int launch_sched(const qkmla_decode_args* a, const SchedArgs& sa, const SplitScratch& w, cudaStream_t s);
+int launch_combine_var(const qkmla_decode_args* a, const SchedArgs& sa, const SplitScratch& w, cudaStream_t s);
 }  // namespace dec
 bool pair_shape(const qkmla_decode_args* a);
 namespace dec {

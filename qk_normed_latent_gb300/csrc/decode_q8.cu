@@ -1,0 +1,751 @@
+// Tensor-core decode kernel for the 8-bit latent cache (tcgen05 + TMEM + TMA).
+//
+// Definition (qkmla.h): with c^_t = s_t x_t, x_t the e4m3 codes and s_t the token's
+// power-of-two scale,
+//     l_{i,t,h} = scale (alpha^q_{i,h} alpha^k_{t,g(h)} s_t (q~_{i,h} . x_t) + q^r_{i,h} . k^r_t)
+//     o_{i,h}   = sum_t p_t s_t x_t,  p = softmax over the tokens query i sees.
+//
+// The codes go to the tensor core as they are stored (kind::f8f6f4: no conversion
+// pass, half the shared memory of bf16), and the other operand of each product is
+// split into two e4m3 parts, a = hi + lo, hi = e4m3(a), lo = e4m3(a - hi).  For the
+// bf16 query the sum is exact down to 2^-18 of the row's largest value (8 significant
+// bits in two times 4); for the weights it is off by at most 2^-8, like a bf16
+// rounding.  Both parts are rows of one operand, so one MMA forms both products and
+// the epilogue adds them: a tcgen05.mma of M = 128, K = 32 costs 55 cycles (A
+// K-major) or 64 (A MN-major) for every N <= 64, 64 / 69 at N = 128 (measured), so
+// the second part costs almost nothing.
+//
+// Orientation.  Tokens are the M of the logit product and latents the M of the
+// output product, both the full 128; query rows (heads x query tokens) are N:
+//   S   = X_tile [Q_hi | Q_lo]^T   M = 128 tokens,  N = 2 ROWS, K = d_c    (e4m3)
+//   R   = Kr_tile [Qr_hi | Qr_lo]^T M = 128 tokens, N = 2 ROWS, K = d_r    (bf16)
+//   O^T += X_tile^T [P_hi | P_lo]  M = 128 latents of a chunk, N = 2 ROWS, K = 128 tokens
+// With ROWS = 32, S and R of two tiles and O^T of 512 latents fill TMEM's 512
+// columns.  A softmax thread is a token: its scale, alpha^k and mask are its own
+// registers, the row sums stay in registers until the end, and the running maximum
+// is only looked at (one vote a tile) -- it moves when a logit exceeds it by 2^8.
+//
+// Weights in units of the output.  P carries s_t, so that the output product runs on
+// the bare codes: p_{t,h} = 32 2^(x_t - m_h) s_t 2^(m_h - v_h) with m_h the running
+// maximum of the logits x (log2) and v_h that of x + log2 s, the largest single
+// contribution -- a maximum over logits alone would push the weights of ordinary
+// tokens beside an outlier's scale below e4m3's range.  m and v are integers: every
+// rescale is a power of two, hence exact.
+//
+// Warps: 0 TMA producer (+ TMEM owner), 1 MMA issuer, 2-9 softmax and epilogue
+// (two groups of 128 threads = tokens; a group takes half the rows).  All waits are
+// bounded (2 s).
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "decode_common.cuh"
+#include "decode_sched.cuh"
+#include "tc_ptx.cuh"
+
+namespace qkmla {
+namespace {
+
+using namespace tc;
+using namespace dec;
+
+constexpr int kT = 128;              // tokens per tile
+constexpr int kThreads = 320;
+constexpr uint32_t kTmemCols = 512;
+constexpr float kPUnit = 32.f;       // P of the largest contribution: lazy maxima let it grow to 2^8 < 448
+constexpr float kLazyX = 256.f;      // 2^8: a weight this large moves the maximum of the logits
+constexpr float kLazyP = 256.f;      // a scaled weight this large moves the maximum of the contributions
+
+template <int DC, int DR, int ROWS>
+struct Q8Layout {
+    static constexpr int kN = 2 * ROWS;                       // hi and lo rows
+    static constexpr int kBlocks = DC / 128;                  // 128-column boxes = output chunks
+    static constexpr int kRopeRow = DR * 2;                   // bytes: 128 (SW128) or 64 (SW64)
+    static constexpr int kQLat = kBlocks * kN * 128;
+    static constexpr int kQRope = kN * kRopeRow;
+    static constexpr int kQ = (kQLat + kQRope + 1023) / 1024 * 1024;
+    static constexpr int kSLat = kBlocks * kT * 128;
+    static constexpr int kSRope = kT * kRopeRow;              // P (kN bytes a token) takes this place
+    static constexpr int kOffAk = kSLat + kSRope;
+    static constexpr int kOffScale = kOffAk + kT * kMaxG * 4;
+    static constexpr int kStage = (kOffScale + kT * 4 + 1023) / 1024 * 1024;
+    // per-row floats: coef, m, v, f, corr, inv, and the column maxima of 4 warps (two kinds)
+    static constexpr int kRowFloats = 6 * ROWS + 8 * ROWS;
+    static constexpr int kMiscMax = 512 + kRowFloats * 4 + 1024;
+    static constexpr int kNst = std::min(4, (232448 - kQ - kMiscMax - 8192) / kStage);
+    static constexpr int kOffStage = kQ;
+    static constexpr int kOffMisc = kQ + kNst * kStage;
+    static constexpr int kNumBars = 4 * kNst + 5;
+    static constexpr int kBytes = kOffMisc + 512 + kRowFloats * 4 + 1024;
+    static constexpr uint32_t kColO = 8 * ROWS;               // two buffers of S_hi S_lo R_hi R_lo
+    static_assert(kNst >= 2 && kN <= kRopeRow, "two stages, and P fits the RoPE slot");
+    static_assert(kColO + kBlocks * kN <= kTmemCols, "TMEM budget");
+    static_assert(kNumBars * 8 + 16 <= 512 && kBytes + 8192 <= 232448, "shared memory budget");
+};
+
+struct Q8Params {
+    const __nv_bfloat16* qt;
+    const float *aq, *qr, *grq;
+    const uint8_t* ak;           // fp32 or fp16
+    const float* kv_scale;
+    const int32_t *seq_lens, *page_table;
+    int64_t num_pages;
+    int page_size, max_pages, piece;     // piece: tokens per TMA box
+    int B, s_q, H, G, window, sinks;
+    float scale, eps;
+    int plain, ak_f16;
+    const WorkItem* items;
+    const int* n_items;
+    SchedArgs sa;
+    int sched_inline;
+    float *o_part, *lse_part;
+    void* o;
+    int o_dtype;
+    float* lse;
+    int* status;
+};
+
+// hi and lo e4m3 parts of two values, each pair packed in 16 bits.
+__device__ __forceinline__ void split_e4m3(float a, float b, uint32_t& hi, uint32_t& lo) {
+    const __nv_fp8x2_storage_t h = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+    const float2 back = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3)));
+    const __nv_fp8x2_storage_t l =
+        __nv_cvt_float2_to_fp8x2(make_float2(a - back.x, b - back.y), __NV_SATFINITE, __NV_E4M3);
+    hi = h;
+    lo = l;
+}
+
+__device__ __forceinline__ bool group_any(int grp, bool pred) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %2, 0;\n\t"
+        "bar.red.or.pred p, %1, 128, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r) : "r"(grp + 1), "r"((uint32_t)pred) : "memory");
+    return r != 0;
+}
+__device__ __forceinline__ void group_sync(int grp) { asm volatile("bar.sync %0, 128;" ::"r"(grp + 1) : "memory"); }
+
+// Maximum over the warp of a float that is not NaN (order-preserving integers).
+__device__ __forceinline__ float redux_max(float v) {
+    const int b = __float_as_int(v);
+    const int m = __reduce_max_sync(0xffffffffu, b >= 0 ? b : b ^ 0x7fffffff);
+    return __int_as_float(m >= 0 ? m : m ^ 0x7fffffff);
+}
+
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t a, uint32_t (&r)[N]) {
+    if constexpr (N == 16) tmem_ld16(a, r);
+    else tmem_ld8(a, r);
+}
+template <int N>
+__device__ __forceinline__ void tmem_st(uint32_t a, const uint32_t (&r)[N]) {
+    if constexpr (N == 16) tmem_st16(a, r);
+    else tmem_st8(a, r);
+}
+
+template <int DC, int DR, int ROWS>
+__global__ void __launch_bounds__(kThreads, 1)
+decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ CUtensorMap tm_rope,
+                 const Q8Params p) {
+    using LY = Q8Layout<DC, DR, ROWS>;
+    constexpr int NST = LY::kNst, N = LY::kN, HPT = ROWS / 2;
+    extern __shared__ __align__(1024) uint8_t smraw[];
+    uint8_t* sm = smraw + ((1024u - (smem_u32(smraw) & 1023u)) & 1023u);
+    uint8_t* sQ = sm;
+    uint64_t* bars = (uint64_t*)(sm + LY::kOffMisc);
+    uint64_t* full = bars;                   // [NST] tile landed -> MMA
+    uint64_t* empty = bars + NST;            // [NST] output MMA done -> TMA
+    uint64_t* pfull = bars + 2 * NST;        // [NST] P written -> output MMA (one arrive per softmax warp)
+    uint64_t* odone = bars + 3 * NST;        // [NST] output MMA done -> softmax (rescale, epilogue)
+    uint64_t* sfull = bars + 4 * NST;        // [2] logit MMA done -> softmax
+    uint64_t* sfree = sfull + 2;             // [2] softmax read S, R -> MMA
+    uint64_t* drain = sfree + 2;             // abort path: the MMAs in flight are done
+    uint32_t* tmem_slot = (uint32_t*)(bars + LY::kNumBars);
+    int* abort_flag = (int*)(tmem_slot + 1);
+    float* coef_s = (float*)(sm + LY::kOffMisc + 512);   // scale log2e alpha^q x the row's code scale
+    float* m_s = coef_s + ROWS;              // running maximum of the logits (integer)
+    float* v_s = m_s + ROWS;                 // running maximum of the contributions (integer)
+    float* f_s = v_s + ROWS;                 // unit of P: kPUnit 2^(m - v)
+    float* corr_s = f_s + ROWS;              // rescale factor of O^T in this tile
+    float* inv_s = corr_s + ROWS;            // epilogue: 1 / (f l)
+    float* red_s = inv_s + ROWS;             // [2 kinds][4 warps][ROWS]
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    WorkItem it;
+    int seq_len;
+    if (p.sched_inline) {
+        __shared__ SchedSmem S;
+        compute_schedule(p.seq_lens, p.B, p.s_q, p.sa, S, p.status, blockIdx.x == 0 && blockIdx.y == 0);
+        if ((int)blockIdx.y >= S.n_items) return;
+        it = schedule_item(S, p.B, (int)blockIdx.y);
+        seq_len = S.len[it.b];
+    } else {
+        pdl_wait();
+        if ((int)blockIdx.y >= *p.n_items) return;
+        it = p.items[blockIdx.y];
+        seq_len = p.seq_lens[it.b];
+    }
+    const int b = it.b;
+    const int n_rows = p.s_q * p.H;
+    const int row0 = blockIdx.x * ROWS;                      // first row (query token x head) of this CTA
+    const bool bad = seq_len < 0 || seq_len > p.max_pages * p.page_size;
+    const int len = bad ? 0 : seq_len;
+    const TileRange tiles(len, p.s_q, p.window, p.sinks, kT);
+    const int jt0 = it.tile_begin;
+    const int n_t = max(0, min(it.tile_end, tiles.count) - jt0);
+    // tokens some row of this CTA sees: [0, len_last) less [sinks, win_first)
+    const int i_first = row0 / p.H, i_last = (min(row0 + ROWS, n_rows) - 1) / p.H;
+    const int len_last = max(0, len - p.s_q + i_last + 1);
+    const int win_first = p.window > 0 ? len - p.s_q + i_first + 1 - p.window : 0;
+    // [all_lo, all_hi): tokens from the window on that every row sees; [0, all_sinks): sinks that every row sees
+    const int len_first = max(0, len - p.s_q + i_first + 1);
+    const int all_lo = p.window > 0 ? max(0, len - p.s_q + i_last + 1 - p.window) : 0;
+
+    if (tid == 0) {
+        if (bad && blockIdx.x == 0) report(p.status, QKMLA_ERR_DEVICE_BOUNDS);
+        for (int i = 0; i < LY::kNumBars; ++i) {
+            const bool eight = (i >= 2 * NST && i < 3 * NST) || i == 4 * NST + 2 || i == 4 * NST + 3;
+            mbar_init(&bars[i], eight ? 8u : 1u);
+        }
+        *abort_flag = 0;
+        fence_barrier_init();
+        prefetch_tmap(&tm_lat);
+        prefetch_tmap(&tm_rope);
+    }
+    __syncthreads();
+    pdl_wait();
+    pdl_trigger();
+
+    // ---- TMA producer: lane q issues piece q of a tile (kT / piece pieces) ----
+    const int n_pieces = kT / p.piece;
+    const uint32_t ak_row = p.plain ? 0u : (uint32_t)(p.G * (p.ak_f16 ? 2 : 4));
+    const uint32_t piece_bytes = (uint32_t)p.piece * (DC + 2 * DR + 4 + ak_row);
+    auto issue_tile = [&](int j) {                            // whole warp 0
+        const int s = j % NST;
+        uint8_t* stg = sm + LY::kOffStage + s * LY::kStage;
+        const int t0 = tiles.tile(jt0 + j) * kT + lane * p.piece;
+        // a piece without a token that some row sees is not read (its rows are zeroed by the softmax)
+        const bool want = lane < n_pieces && t0 < len_last && (t0 < p.sinks || t0 + p.piece > win_first);
+        int64_t page = 0;
+        if (want) {
+            const int pg = t0 / p.page_size;
+            page = p.page_table ? (int64_t)p.page_table[(int64_t)b * p.max_pages + pg] : (int64_t)b * p.max_pages + pg;
+            if (page < 0 || page >= p.num_pages) {
+                report(p.status, QKMLA_ERR_DEVICE_BOUNDS);
+                page = 0;
+            }
+        }
+        const int n_want = __popc(__ballot_sync(0xffffffffu, want));
+        if (lane == 0) mbar_arrive_expect_tx(&full[s], (uint32_t)n_want * piece_bytes);
+        __syncwarp();
+        if (want) {
+            const int64_t slot = page * p.page_size + t0 % p.page_size;
+            const int at = lane * p.piece;
+#pragma unroll
+            for (int blk = 0; blk < LY::kBlocks; ++blk)
+                tma_load_2d(stg + blk * (kT * 128) + at * 128, &tm_lat, blk * 128, (int)slot, &full[s]);
+            tma_load_2d(stg + LY::kSLat + at * LY::kRopeRow, &tm_rope, 0, (int)slot, &full[s]);
+            bulk_load(stg + LY::kOffScale + at * 4, p.kv_scale + slot, (uint32_t)p.piece * 4, &full[s]);
+            if (ak_row) bulk_load(stg + LY::kOffAk + at * ak_row, p.ak + slot * ak_row, (uint32_t)p.piece * ak_row, &full[s]);
+        }
+    };
+    const size_t grow0 = (size_t)b * n_rows + row0;           // first row in the query arrays
+    if (warp == 0) {
+        tmem_alloc(tmem_slot, kTmemCols);
+        tmem_relinquish();
+        for (int j = 0; j < NST && j < n_t; ++j) issue_tile(j);
+    } else if (warp >= 2) {
+        // ---- prologue: the query rows as hi / lo parts, a warp per row ----
+        for (int r = warp - 2; r < ROWS; r += 8) {
+            const bool ok = row0 + r < n_rows;
+            float q[DC / 32], top = 0.f;
+            const __nv_bfloat16* src = p.qt + (grow0 + r) * DC + lane * (DC / 32);
+#pragma unroll
+            for (int k = 0; k < DC / 32; k += 4) {            // 8-byte loads: q~ is 8-byte aligned by the rows' size
+                const uint2 w = ok ? *reinterpret_cast<const uint2*>(src + k) : make_uint2(0u, 0u);
+                const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w.x));
+                const float2 c = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w.y));
+                q[k] = a.x; q[k + 1] = a.y; q[k + 2] = c.x; q[k + 3] = c.y;
+            }
+            float rv[DR / 32];
+#pragma unroll
+            for (int k = 0; k < DR / 32; ++k) rv[k] = ok ? p.qr[(grow0 + r) * DR + lane * (DR / 32) + k] : 0.f;
+#pragma unroll
+            for (int k = 0; k < DC / 32; ++k) top = fmaxf(top, fabsf(q[k]));
+            float inv;
+            const float sq = e4m3_scale(warp_max(top), &inv);
+            uint32_t hi[DC / 128], lo[DC / 128];              // 4 codes a word
+#pragma unroll
+            for (int k = 0; k < DC / 128; ++k) {
+                uint32_t h0, l0, h1, l1;
+                split_e4m3(q[4 * k] * inv, q[4 * k + 1] * inv, h0, l0);
+                split_e4m3(q[4 * k + 2] * inv, q[4 * k + 3] * inv, h1, l1);
+                hi[k] = h0 | (h1 << 16);
+                lo[k] = l0 | (l1 << 16);
+            }
+#pragma unroll
+            for (int k = 0; k < DC / 128; ++k) {
+                const int col = lane * (DC / 32) + 4 * k, c = col & 127;
+                const uint32_t blk = (uint32_t)(col >> 7) * (N * 128);
+                const uint32_t h = (uint32_t)r, l = (uint32_t)(r + ROWS);
+                *reinterpret_cast<uint32_t*>(sQ + blk + h * 128 + (((c >> 4) ^ (h & 7)) << 4) + (c & 15)) = hi[k];
+                *reinterpret_cast<uint32_t*>(sQ + blk + l * 128 + (((c >> 4) ^ (l & 7)) << 4) + (c & 15)) = lo[k];
+            }
+            float ss = 0.f;
+#pragma unroll
+            for (int k = 0; k < DR / 32; ++k) ss = fmaf(rv[k], rv[k], ss);
+            ss = warp_sum(ss);
+            // the RoPE query carries scale log2e: R is the RoPE logit in the exp2 domain
+            const float beta = p.scale * kLog2e * (p.plain ? 1.f : 1.f / sqrtf(ss / (float)DR + p.eps));
+#pragma unroll
+            for (int k = 0; k < DR / 32; ++k) {
+                const int c = lane * (DR / 32) + k;
+                const float val = rv[k] * ((p.plain || !p.grq) ? 1.f : p.grq[c]) * beta;
+                const __nv_bfloat16 h = __float2bfloat16_rn(val);
+                const __nv_bfloat16 l = __float2bfloat16_rn(val - __bfloat162float(h));
+                const uint32_t oh = DR == 64 ? sw128_offset(r, c) : sw64_offset(r, c);
+                const uint32_t ol = DR == 64 ? sw128_offset(r + ROWS, c) : sw64_offset(r + ROWS, c);
+                *reinterpret_cast<__nv_bfloat16*>(sQ + LY::kQLat + oh) = h;
+                *reinterpret_cast<__nv_bfloat16*>(sQ + LY::kQLat + ol) = l;
+            }
+            if (lane == 0) {
+                coef_s[r] = ok ? p.scale * kLog2e * sq * (p.plain ? 1.f : p.aq[grow0 + r]) : 0.f;
+                m_s[r] = v_s[r] = -INFINITY;
+                f_s[r] = 0.f;
+            }
+        }
+        fence_proxy_async_smem();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp == 0) {
+        // ===================== TMA producer =====================
+        int issued = min(NST, n_t);
+        for (int j = NST; j < n_t; ++j) {
+            int go = 1;
+            if (lane == 0) go = wait_bounded(&empty[j % NST], ((j / NST) - 1) & 1, p.status) ? 1 : 0;
+            if (lane == 0 && *(volatile int*)abort_flag) go = 0;
+            if (!__shfl_sync(0xffffffffu, go, 0)) {
+                if (lane == 0) *(volatile int*)abort_flag = 1;
+                break;
+            }
+            issue_tile(j);
+            issued = j + 1;
+        }
+        // no exit with a copy in flight: on the ordinary path the MMA warp has waited for all of them
+        if (lane == 0 && *(volatile int*)abort_flag)
+            for (int j = max(0, issued - NST); j < issued; ++j) wait_bounded(&full[j % NST], (j / NST) & 1, p.status);
+    } else if (warp == 1) {
+        // ===================== MMA issuer: logits and outputs in readiness order =====================
+        if (lane == 0) {
+            const uint32_t id_s = idesc_e4m3(kT, N, 0, 0);
+            const uint32_t id_r = idesc_bf16(kT, N, 0, 0);
+            const uint32_t id_o = idesc_e4m3(128, N, 1, 1);
+            const uint32_t q_addr = smem_u32(sQ);
+            auto issue_s = [&](int j) {
+                tc_fence_after();
+                const uint32_t st = smem_u32(sm + LY::kOffStage + (j % NST) * LY::kStage);
+                const uint32_t d = tmem + (uint32_t)(j & 1) * (2 * N);
+#pragma unroll
+                for (int blk = 0; blk < LY::kBlocks; ++blk)
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_f8(d, smem_desc(st + blk * (kT * 128) + kk * 32, 16, 1024, kSwizzle128B),
+                               smem_desc(q_addr + blk * (N * 128) + kk * 32, 16, 1024, kSwizzle128B), id_s,
+                               (blk > 0 || kk > 0) ? 1u : 0u);
+                constexpr uint32_t sw = DR == 64 ? kSwizzle128B : kSwizzle64B, sbo = DR == 64 ? 1024 : 512;
+#pragma unroll
+                for (int kk = 0; kk < DR / 16; ++kk)
+                    mma_bf16(d + N, smem_desc(st + LY::kSLat + kk * 32, 16, sbo, sw),
+                             smem_desc(q_addr + LY::kQLat + kk * 32, 16, sbo, sw), id_r, kk > 0 ? 1u : 0u);
+                mma_commit(&sfull[j & 1]);
+            };
+            auto issue_o = [&](int j) {
+                tc_fence_after();
+                const int s = j % NST;
+                const uint32_t st = smem_u32(sm + LY::kOffStage + s * LY::kStage);
+                // A: a chunk's 128 latents x 32 tokens, MN-major (8-token groups 1024 B apart).
+                // B: P, MN-major: a token's N codes in N bytes (swizzle of the same width), 8-token groups 8 N bytes apart.
+                constexpr uint32_t swp = N == 64 ? kSwizzle64B : kSwizzle32B;
+#pragma unroll
+                for (int c = 0; c < LY::kBlocks; ++c)
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_f8(tmem + LY::kColO + c * N, smem_desc(st + c * (kT * 128) + kk * 4096, kT * 128, 1024, kSwizzle128B),
+                               smem_desc(st + LY::kSLat + kk * 32 * N, 8 * N, 8 * N, swp), id_o, (j > 0 || kk > 0) ? 1u : 0u);
+                mma_commit(&empty[s]);
+                mma_commit(&odone[s]);
+            };
+            int js = 0, jo = 0;
+            bool ok = true;
+            uint64_t t_last = globaltimer();
+            uint32_t idle = 0;
+            while (ok && jo < n_t) {
+                bool did = false;
+                if (js < n_t && mbar_test_wait(&full[js % NST], (js / NST) & 1) &&
+                    (js < 2 || mbar_test_wait(&sfree[js & 1], ((js >> 1) - 1) & 1))) {
+                    issue_s(js);
+                    ++js;
+                    did = true;
+                }
+                if (jo < js && mbar_test_wait(&pfull[jo % NST], (jo / NST) & 1)) {
+                    issue_o(jo);
+                    ++jo;
+                    did = true;
+                }
+                if (did) {
+                    idle = 0;
+                    t_last = globaltimer();
+                } else if ((++idle & 255u) == 0) {
+                    if (*(volatile int*)abort_flag || globaltimer() - t_last > kWaitNs) {
+                        report(p.status, QKMLA_ERR_TIMEOUT);
+                        ok = false;
+                    }
+                }
+            }
+            if (!ok) {                       // no exit with an MMA in flight
+                *(volatile int*)abort_flag = 1;
+                mma_commit(drain);
+                wait_bounded(drain, 0, p.status);
+            }
+        }
+    } else {
+        // ===================== softmax: thread = token, HPT rows of its group =====================
+        const int sub = warp & 3, grp = warp >= 6 ? 1 : 0;
+        const uint32_t lane_base = (uint32_t)(32 * sub) << 16;
+        const int tl = 32 * sub + lane;                      // token in the tile
+        const int u0 = grp * HPT;                            // first row of the group
+        const int hpg = p.H / p.G;                           // 1, 2, 4, 8 or 16
+        const int hshift = 31 - __clz(hpg);
+        const int h0 = (row0 + u0) % p.H;                    // its head: HPT divides H, so the rows share a query token
+        const int n_row = max(0, len - p.s_q + (row0 + u0) / p.H + 1);   // causal length of these rows
+        const int w_row = p.window > 0 ? n_row - p.window : 0;
+        float lsum[HPT];
+#pragma unroll
+        for (int u = 0; u < HPT; ++u) lsum[u] = 0.f;
+        bool ok = true;
+        for (int j = 0; j < n_t; ++j) {
+            const int s = j % NST, sb = j & 1;
+            uint8_t* stg = sm + LY::kOffStage + s * LY::kStage;
+            const int t = tiles.tile(jt0 + j) * kT + tl;
+            const bool sees = t < n_row && (t < p.sinks || t >= w_row);
+            const bool any_sees = t < len_last && (t < p.sinks || t >= win_first);   // some row of the CTA
+            const bool got_s = wait_bounded(&sfull[sb], (j >> 1) & 1, p.status);
+            tc_fence_after();
+            float x[HPT];
+            {
+                uint32_t a[HPT], c[HPT];
+                const uint32_t base = tmem + (uint32_t)sb * (2 * N) + lane_base + u0;
+                tmem_ld<HPT>(base, a);
+                tmem_ld<HPT>(base + ROWS, c);
+                uint32_t d[HPT], e[HPT];
+                tmem_ld<HPT>(base + N, d);
+                tmem_ld<HPT>(base + N + ROWS, e);
+                tmem_wait_ld();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sfree[sb]);
+                const float st = *reinterpret_cast<const float*>(stg + LY::kOffScale + tl * 4);
+                float aks = st;
+#pragma unroll
+                for (int u = 0; u < HPT; ++u) {
+                    if (!p.plain && (u == 0 || ((h0 + u) & (hpg - 1)) == 0)) {
+                        const int g = tl * p.G + ((h0 + u) >> hshift);
+                        aks = st * (p.ak_f16 ? load_alpha<true>(stg + LY::kOffAk, g) : load_alpha<false>(stg + LY::kOffAk, g));
+                    }
+                    x[u] = fmaf(aks * coef_s[u0 + u], __uint_as_float(a[u]) + __uint_as_float(c[u]),
+                                __uint_as_float(d[u]) + __uint_as_float(e[u]));
+                }
+            }
+            const float st = any_sees ? *reinterpret_cast<const float*>(stg + LY::kOffScale + tl * 4) : 0.f;
+            float e[HPT], w[HPT];
+            float top = 0.f;
+            auto weigh = [&]() {
+#pragma unroll
+                for (int u = 0; u < HPT; ++u) {
+                    const float ex = fast_exp2(x[u] - m_s[u0 + u]);
+                    e[u] = sees ? ex : 0.f;
+                    w[u] = e[u] * (st * f_s[u0 + u]);
+                    top = fmax3(top, e[u], w[u]);
+                }
+            };
+            weigh();
+            const bool need = top > kLazyX || (j == 0);
+            static_assert(kLazyX == kLazyP, "one comparison");
+            if (group_any(grp, need || !got_s)) {
+                if (group_any(grp, !got_s)) { ok = false; break; }
+                // ---- exact maxima of this tile's logits and contributions, per row ----
+                const float ls = (sees && st > 0.f) ? log2f(st) : -INFINITY;
+#pragma unroll
+                for (int u = 0; u < HPT; ++u) {
+                    const float xv = (sees && x[u] == x[u]) ? x[u] : -INFINITY;
+                    const float mx = redux_max(xv), vx = redux_max(xv + ls);
+                    if (lane == 0) {
+                        red_s[sub * ROWS + u0 + u] = mx;
+                        red_s[(4 + sub) * ROWS + u0 + u] = vx;
+                    }
+                }
+                group_sync(grp);
+                const int gt = tid - 64 - grp * 128;
+                if (gt < HPT) {
+                    const int r = u0 + gt;
+                    float mx = red_s[r], vx = red_s[4 * ROWS + r];
+#pragma unroll
+                    for (int q = 1; q < 4; ++q) {
+                        mx = fmaxf(mx, red_s[q * ROWS + r]);
+                        vx = fmaxf(vx, red_s[(4 + q) * ROWS + r]);
+                    }
+                    const float m0 = m_s[r], v0 = v_s[r], f0 = f_s[r];
+                    const float m1 = mx > m0 + 4.f ? ceilf(mx) : m0, v1 = vx > v0 + 2.f ? ceilf(vx) : v0;
+                    const float cm = m0 == -INFINITY ? 0.f : exp2f(m0 - m1);       // of the row sums
+                    const float f1 = v1 == -INFINITY ? 0.f : kPUnit * exp2f(fminf(fmaxf(m1 - v1, -110.f), 95.f));
+                    m_s[r] = m1;
+                    v_s[r] = v1;
+                    f_s[r] = f1;
+                    red_s[r] = cm;
+                    corr_s[r] = f0 > 0.f ? cm * (f1 / f0) : 0.f;                   // of O^T; nothing there yet: 0
+                }
+                group_sync(grp);
+                if (j > 0) {
+                    const bool got_o = wait_bounded(&odone[(j - 1) % NST], ((j - 1) / NST) & 1, p.status);
+                    if (group_any(grp, !got_o)) { ok = false; break; }
+                    tc_fence_after();
+                    float cr[HPT];
+                    bool moved = false;
+#pragma unroll
+                    for (int u = 0; u < HPT; ++u) {
+                        cr[u] = corr_s[u0 + u];
+                        moved = moved || cr[u] != 1.f;
+                    }
+                    if (moved) {
+#pragma unroll 1
+                        for (int c = 0; c < 2 * LY::kBlocks; ++c) {       // chunks x (hi, lo)
+                            uint32_t v[HPT];
+                            const uint32_t ta = tmem + LY::kColO + c * ROWS + u0 + lane_base;
+                            tmem_ld<HPT>(ta, v);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int u = 0; u < HPT; ++u)
+                                v[u] = cr[u] == 0.f ? 0u : __float_as_uint(__uint_as_float(v[u]) * cr[u]);
+                            tmem_st<HPT>(ta, v);
+                        }
+                        tmem_wait_st();
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < HPT; ++u) lsum[u] *= red_s[u0 + u];
+                weigh();
+                group_sync(grp);                             // red_s, corr_s are read
+            }
+            uint32_t hi[HPT / 4], lo[HPT / 4];
+#pragma unroll
+            for (int u = 0; u < HPT; u += 4) {
+                uint32_t h0, l0, h1, l1;
+                split_e4m3(w[u], w[u + 1], h0, l0);
+                split_e4m3(w[u + 2], w[u + 3], h1, l1);
+                hi[u / 4] = h0 | (h1 << 16);
+                lo[u / 4] = l0 | (l1 << 16);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) lsum[u + q] += e[u + q];
+            }
+            // P row of this token: HPT codes of hi at u0, of lo at ROWS + u0, 16-byte chunks XOR-swizzled
+            // (64-byte rows by token / 2, 32-byte rows by token / 4)
+            uint8_t* pr = stg + LY::kSLat + tl * N;
+            if constexpr (N == 64) {
+                const uint32_t xr = (tl >> 1) & 3;
+                *reinterpret_cast<uint4*>(pr + (((uint32_t)grp ^ xr) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *reinterpret_cast<uint4*>(pr + (((uint32_t)(2 + grp) ^ xr) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            } else {
+                const uint32_t xr = (tl >> 2) & 1;
+                *reinterpret_cast<uint2*>(pr + ((0u ^ xr) << 4) + u0) = make_uint2(hi[0], hi[1]);
+                *reinterpret_cast<uint2*>(pr + ((1u ^ xr) << 4) + u0) = make_uint2(lo[0], lo[1]);
+            }
+            // a token no row sees: its latents (stale or never loaded) must not reach the output MMA as NaN
+            if (!any_sees) {
+#pragma unroll
+                for (int blk = 0; blk < LY::kBlocks; ++blk)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        *reinterpret_cast<uint4*>(stg + blk * (kT * 128) + tl * 128 + (((4 * grp + c) ^ (tl & 7)) << 4)) =
+                            make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&pfull[s]);
+        }
+        if (!ok) *(volatile int*)abort_flag = 1;
+        // ---- epilogue: row sums over the tokens, then O^T / (f l) ----
+#pragma unroll
+        for (int u = 0; u < HPT; ++u) {
+            const float v = warp_sum(lsum[u]);
+            if (lane == 0) red_s[sub * ROWS + u0 + u] = v;
+        }
+        const bool got_last = (ok && n_t > 0) ? wait_bounded(&odone[(n_t - 1) % NST], ((n_t - 1) / NST) & 1, p.status) : ok;
+        if (group_any(grp, !got_last)) *(volatile int*)abort_flag = 1;
+        tc_fence_after();
+        const int gt = tid - 64 - grp * 128;
+        if (gt < HPT) {
+            const int r = u0 + gt;
+            const float l = (red_s[r] + red_s[ROWS + r]) + (red_s[2 * ROWS + r] + red_s[3 * ROWS + r]);
+            const float lse = l > 0.f ? (m_s[r] + log2f(l)) * kLn2 : (l == 0.f ? -INFINITY : l);
+            inv_s[r] = (l == 0.f || (f_s[r] == 0.f && l == l)) ? 0.f : 1.f / (f_s[r] * l);
+            if (row0 + r < n_rows) {
+                if (it.part >= 0) p.lse_part[(size_t)it.part * n_rows + row0 + r] = lse;
+                else if (p.lse) p.lse[grow0 + r] = lse;
+            }
+        }
+        group_sync(grp);
+#pragma unroll 1
+        for (int c = 0; c < LY::kBlocks; ++c) {
+            uint32_t a[HPT], d[HPT];
+            if (n_t > 0) {
+                tmem_ld<HPT>(tmem + LY::kColO + c * N + u0 + lane_base, a);
+                tmem_ld<HPT>(tmem + LY::kColO + c * N + ROWS + u0 + lane_base, d);
+                tmem_wait_ld();
+            }
+            const int col = c * 128 + tl;
+#pragma unroll
+            for (int u = 0; u < HPT; ++u) {
+                const int r = u0 + u;
+                if (row0 + r >= n_rows) continue;
+                const float inv = inv_s[r];
+                const float val = inv == 0.f ? 0.f : (__uint_as_float(a[u]) + __uint_as_float(d[u])) * inv;
+                if (it.part >= 0) p.o_part[((size_t)it.part * n_rows + row0 + r) * DC + col] = val;
+                else if (p.o_dtype == QKMLA_F32) ((float*)p.o)[(grow0 + r) * DC + col] = val;
+                else ((__nv_bfloat16*)p.o)[(grow0 + r) * DC + col] = __float2bfloat16_rn(val);
+            }
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+bool make_q8_map(CUtensorMap* m, CUtensorMapDataType type, const void* base, int64_t rows, int cols, int64_t pitch,
+                 int box_cols, int box_rows, CUtensorMapSwizzle sw) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)pitch};
+    cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
+    cuuint32_t es[2] = {1, 1};
+    return fn(m, type, 2, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Query rows per CTA: 16 when that is all there are, else 32.
+int q8_rows(const qkmla_decode_args* a) { return a->s_q * a->H <= 16 ? 16 : 32; }
+int q8_row_blocks(const qkmla_decode_args* a) {
+    const int r = q8_rows(a);
+    return (a->s_q * a->H + r - 1) / r;
+}
+
+template <int DC, int DR, int ROWS>
+int launch_q8(const Q8Params& q, const CUtensorMap& lat, const CUtensorMap& rope, dim3 grid, cudaStream_t s) {
+    auto k = decode_q8_kernel<DC, DR, ROWS>;
+    constexpr int bytes = Q8Layout<DC, DR, ROWS>::kBytes;
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return QKMLA_ERR_CUDA;
+    return launch_pdl(k, grid, dim3(kThreads), bytes, s, lat, rope, q) == cudaSuccess ? QKMLA_OK : QKMLA_ERR_CUDA;
+}
+
+}  // namespace
+
+// 8-bit cache shapes of the tensor-core kernel.  A thread's rows (8 or 16) share a query
+// token when they divide H; a tile is made of whole pages or a page of whole tiles.
+bool q8_tc_supported(const qkmla_decode_args* a, const DecodeExt& x) {
+    if (a->cache_dtype != QKMLA_E4M3) return false;
+    if (!((a->d_c == 512 && a->d_r == 64) || (a->d_c == 256 && (a->d_r == 32 || a->d_r == 64)) ||
+          (a->d_c == 128 && (a->d_r == 32 || a->d_r == 64))))
+        return false;
+    if (a->H % 16 || a->G > kMaxG || a->B > kMaxB) return false;
+    if (a->page_size % 16 || (a->page_size < kT ? kT % a->page_size : a->page_size % kT)) return false;
+    if (a->num_slots > 2147483647LL) return false;                // TMA row coordinates are 32-bit
+    if (((uintptr_t)a->kv_cache % 16) || ((uintptr_t)a->q_tilde % 16) || ((uintptr_t)a->o % 16) ||
+        ((uintptr_t)x.kv_scale % 16))
+        return false;
+    return (a->flags & QKMLA_FLAG_PLAIN_MLA) || ((uintptr_t)a->ak_cache % 16) == 0;
+}
+
+size_t q8_tc_workspace(const qkmla_decode_args* a, int sms) {
+    return split_scratch(a, q8_row_blocks(a), sms, nullptr).bytes;
+}
+
+int launch_decode_q8(const qkmla_decode_args* a, const DecodeExt& x, cudaStream_t s) {
+    const int sms = device_sm_count();
+    const int n_rb = q8_row_blocks(a);
+    const SplitScratch w = split_scratch(a, n_rb, sms, a->workspace);
+    SchedArgs sa;
+    sa.max_len = a->max_pages * a->page_size;
+    sa.n_rb = n_rb;
+    sa.sms = sms;
+    sa.min_tokens = 512;
+    sa.tile = kT;
+    sa.fixed_splits = a->num_splits;
+    sa.min_len = 0;
+    sa.window = x.window;
+    sa.sinks = x.sinks;
+    const int sched_inline = sched_in_kernel(a) ? 1 : 0;
+    if (!sched_inline && launch_sched(a, sa, w, s) != QKMLA_OK) return QKMLA_ERR_CUDA;
+
+    Q8Params q;
+    q.qt = (const __nv_bfloat16*)a->q_tilde;
+    q.aq = a->alpha_q;
+    q.qr = a->q_rope;
+    q.grq = a->gamma_rope_q;
+    q.ak = (const uint8_t*)a->ak_cache;
+    q.kv_scale = x.kv_scale;
+    q.seq_lens = a->seq_lens;
+    q.page_table = a->page_table;
+    q.num_pages = a->num_slots / a->page_size;
+    q.page_size = a->page_size;
+    q.max_pages = a->max_pages;
+    q.piece = std::min(a->page_size, kT);
+    q.B = a->B; q.s_q = a->s_q; q.H = a->H; q.G = a->G;
+    q.window = x.window;
+    q.sinks = x.sinks;
+    q.scale = a->softmax_scale;
+    q.eps = a->eps;
+    q.plain = (a->flags & QKMLA_FLAG_PLAIN_MLA) ? 1 : 0;
+    q.ak_f16 = (a->flags & QKMLA_FLAG_ALPHA_F16) ? 1 : 0;
+    q.items = w.items;
+    q.n_items = w.n_items;
+    q.sa = sa;
+    q.sched_inline = sched_inline;
+    q.o_part = w.o_part;
+    q.lse_part = w.lse_part;
+    q.o = a->o;
+    q.o_dtype = a->o_dtype;
+    q.lse = a->lse;
+    q.status = device_status_ptr();
+
+    const int64_t pitch = a->d_c + 2 * a->d_r;
+    CUtensorMap lat, rope;
+    if (!make_q8_map(&lat, CU_TENSOR_MAP_DATA_TYPE_UINT8, a->kv_cache, a->num_slots, (int)pitch, pitch, 128, q.piece,
+                     CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !make_q8_map(&rope, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (const uint8_t*)a->kv_cache + a->d_c, a->num_slots, a->d_r,
+                     pitch, a->d_r, q.piece, a->d_r == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
+        return QKMLA_ERR_CUDA;
+    const dim3 grid(n_rb, w.max_items);
+    const bool r16 = q8_rows(a) == 16;
+    int rc = QKMLA_ERR_UNSUPPORTED;
+    if (a->d_c == 512) rc = r16 ? launch_q8<512, 64, 16>(q, lat, rope, grid, s) : launch_q8<512, 64, 32>(q, lat, rope, grid, s);
+    else if (a->d_c == 256 && a->d_r == 32) rc = r16 ? launch_q8<256, 32, 16>(q, lat, rope, grid, s) : launch_q8<256, 32, 32>(q, lat, rope, grid, s);
+    else if (a->d_c == 256) rc = r16 ? launch_q8<256, 64, 16>(q, lat, rope, grid, s) : launch_q8<256, 64, 32>(q, lat, rope, grid, s);
+    else if (a->d_r == 32) rc = r16 ? launch_q8<128, 32, 16>(q, lat, rope, grid, s) : launch_q8<128, 32, 32>(q, lat, rope, grid, s);
+    else rc = r16 ? launch_q8<128, 64, 16>(q, lat, rope, grid, s) : launch_q8<128, 64, 32>(q, lat, rope, grid, s);
+    if (rc != QKMLA_OK) return rc;
+    return launch_combine_var(a, sa, w, s);
+}
+
+}  // namespace qkmla

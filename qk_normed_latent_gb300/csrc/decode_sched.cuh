@@ -2,7 +2,7 @@
 //
 // Every CTA derives the same plan from seq_lens, so no separate scheduler launch
 // (and no kernel boundary) sits between the previous kernel and the decode:
-//   * tiles per sequence tb_b = ceil(L_b / tile);
+//   * tiles per sequence tb_b = ceil(L_b / tile), less those outside a window;
 //   * tiles per work item tpi: the longest sequence when that is within 25 % of
 //     an even share of the GPU (s_total * n_rb / sms), else that share rounded
 //     up; at least min_tokens worth of tiles;
@@ -44,10 +44,10 @@ __device__ __forceinline__ void compute_schedule(const int32_t* __restrict__ seq
         const int L = __ldcg(seq_lens + b);   // through L2: the lengths may change between calls
         S.len[b] = L;
         int tl = 0;
-        if (L < s_q || L > a.max_len) {
+        if (L < a.min_len || L > a.max_len) {
             if (report_errors) report(status, QKMLA_ERR_DEVICE_BOUNDS);
         } else {
-            tl = (L + a.tile - 1) / a.tile;
+            tl = TileRange(L, s_q, a.window, a.sinks, a.tile).count;
         }
         S.tb[b] = tl;
         tot += tl;

@@ -604,8 +604,7 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
 // scheduler: seq_lens -> work items (one CTA)
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(1024)
-sched_kernel(const int32_t* __restrict__ seq_lens, int B, int s_q, int max_len, int n_rb, int sms, int min_tokens,
-             int tile, int fixed_splits, WorkItem* __restrict__ items, int* __restrict__ n_items, int* __restrict__ seq_nsplit,
+sched_kernel(const int32_t* __restrict__ seq_lens, int B, int s_q, SchedArgs a, WorkItem* __restrict__ items, int* __restrict__ n_items, int* __restrict__ seq_nsplit,
              int* __restrict__ seq_part0, int* __restrict__ split_list, int* status) {
     __shared__ int tiles_s[kMaxB];
     __shared__ int ns_by_rank[kMaxB];
@@ -619,10 +618,10 @@ sched_kernel(const int32_t* __restrict__ seq_lens, int B, int s_q, int max_len, 
     for (int b = tid; b < B; b += nt) {
         const int L = seq_lens[b];
         int tl = 0;
-        if (L < s_q || L > max_len) {
+        if (L < a.min_len || L > a.max_len) {
             report(status, QKMLA_ERR_DEVICE_BOUNDS);
         } else {
-            tl = (L + tile - 1) / tile;
+            tl = TileRange(L, s_q, a.window, a.sinks, a.tile).count;
         }
         tiles_s[b] = tl;
         tot += tl;
@@ -648,12 +647,12 @@ sched_kernel(const int32_t* __restrict__ seq_lens, int B, int s_q, int max_len, 
         int m = 0;
         for (int w = 0; w < (nt + 31) / 32; ++w) m = max(m, red[w]);
         // ideal tiles per CTA if the whole GPU shares the work evenly
-        const float ideal = (float)s_total * n_rb / (float)sms;
+        const float ideal = (float)s_total * a.n_rb / (float)a.sms;
         int tpi = (float)m <= 1.25f * ideal ? m : (int)ceilf(ideal);
-        s_tpi = max(max(tpi, min_tokens / tile), 1);
+        s_tpi = max(max(tpi, a.min_tokens / a.tile), 1);
     }
     __syncthreads();
-    const int tpi = s_tpi;
+    const int tpi = s_tpi, fixed_splits = a.fixed_splits;
     // rank sequences by descending tile count (longest first), ties by index
     for (int b = tid; b < B; b += nt) {
         const int tb = tiles_s[b];
@@ -740,6 +739,8 @@ combine_var_kernel(const float* __restrict__ o_part, const float* __restrict__ l
                 if constexpr (VEC == 4) {
                     const float4 x = __ldcg(reinterpret_cast<const float4*>(src));
                     v[u][0] = x.x; v[u][1] = x.y; v[u][2] = x.z; v[u][3] = x.w;
+                } else if constexpr (VEC == 1) {
+                    v[u][0] = __ldcg(src);
                 } else {
                     const float2 x = __ldcg(reinterpret_cast<const float2*>(src));
                     v[u][0] = x.x; v[u][1] = x.y;
@@ -789,11 +790,14 @@ combine_var_kernel(const float* __restrict__ o_part, const float* __restrict__ l
         if (o_dtype == QKMLA_F32) {
             float* dst = (float*)o + (size_t)row * kDc + VEC * tid;
             if constexpr (VEC == 4) *reinterpret_cast<float4*>(dst) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+            else if constexpr (VEC == 1) *dst = acc[0];
             else *reinterpret_cast<float2*>(dst) = make_float2(acc[0], acc[1]);
         } else {
             __nv_bfloat16* dst = (__nv_bfloat16*)o + (size_t)row * kDc + VEC * tid;
-            const __nv_bfloat162 lo = __floats2bfloat162_rn(acc[0], acc[1]);
-            if constexpr (VEC == 4) {
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(acc[0], acc[VEC > 1 ? 1 : 0]);
+            if constexpr (VEC == 1) {
+                *dst = lo.x;
+            } else if constexpr (VEC == 4) {
                 const __nv_bfloat162 hi = __floats2bfloat162_rn(acc[2], acc[3]);
                 uint2 pk;
                 pk.x = *reinterpret_cast<const uint32_t*>(&lo);
@@ -891,58 +895,80 @@ bool tc_supported(const qkmla_decode_args* a) {
     return true;
 }
 
-size_t tc_workspace(const qkmla_decode_args* a, int sms, int* max_items_out) {
-    const int rows_o = pair_shape(a) ? 64 : tc_rows(a);
-    const int n_rb = a->s_q * a->H / rows_o;
+namespace dec {
+
+SplitScratch split_scratch(const qkmla_decode_args* a, int n_rb, int sms, void* workspace) {
+    SplitScratch w;
     const int target = (sms + n_rb - 1) / n_rb;
-    int max_items = a->B + target + 1;
-    if (a->num_splits > 0) max_items = a->B * a->num_splits;
-    if (max_items_out) *max_items_out = max_items;
+    w.max_items = a->num_splits > 0 ? a->B * a->num_splits : a->B + target + 1;
+    uint8_t* ws = (uint8_t*)workspace;
     size_t off = 0;
-    off += (size_t)max_items * sizeof(WorkItem);
+    w.items = (WorkItem*)ws;
+    off += (size_t)w.max_items * sizeof(WorkItem);
+    w.n_items = (int*)(ws + off);
+    w.seq_nsplit = w.n_items + 4;
+    w.seq_part0 = w.seq_nsplit + a->B;
+    w.split_list = w.seq_part0 + a->B;
     off += 16 + 3 * (size_t)a->B * sizeof(int);
     off = (off + 255) & ~(size_t)255;
-    off += (size_t)max_items * a->s_q * a->H * a->d_c * sizeof(float);
-    off += (size_t)max_items * a->s_q * a->H * sizeof(float);
-    return off + 256;
+    w.o_part = (float*)(ws + off);
+    w.lse_part = w.o_part + (size_t)w.max_items * a->s_q * a->H * a->d_c;
+    off += (size_t)w.max_items * a->s_q * a->H * a->d_c * sizeof(float);
+    off += (size_t)w.max_items * a->s_q * a->H * sizeof(float);
+    w.bytes = off + 256;
+    return w;
+}
+
+int launch_sched(const qkmla_decode_args* a, const SchedArgs& sa, const SplitScratch& w, cudaStream_t s) {
+    return launch_pdl(sched_kernel, dim3(1), dim3(1024), 0, s, a->seq_lens, a->B, a->s_q, sa, w.items, w.n_items,
+                      w.seq_nsplit, w.seq_part0, w.split_list, device_status_ptr()) == cudaSuccess
+               ? QKMLA_OK
+               : QKMLA_ERR_CUDA;
+}
+
+int launch_combine_var(const qkmla_decode_args* a, const SchedArgs& sa, const SplitScratch& w, cudaStream_t s) {
+    // one CTA per merged row where few sequences make few, long, split rows (every
+    // CTA computes the plan, so many CTAs cost more than they give on large batches)
+    const int combine_ctas = std::min(a->B * a->s_q * a->H, (a->B <= 32 ? 8 : 2) * sa.sms);
+    auto ck = a->d_c == 512 ? combine_var_kernel<4> : a->d_c == 256 ? combine_var_kernel<2> : combine_var_kernel<1>;
+    return launch_pdl(ck, dim3(combine_ctas), dim3(128), 0, s, (const float*)w.o_part, (const float*)w.lse_part,
+                      (const int*)w.seq_nsplit, (const int*)w.seq_part0, (const int*)w.split_list,
+                      (const int*)(w.n_items + 1), a->seq_lens, a->B, a->s_q, sa, sched_in_kernel(a) ? 1 : 0,
+                      a->s_q * a->H, a->o, a->o_dtype, a->lse) == cudaSuccess
+               ? QKMLA_OK
+               : QKMLA_ERR_CUDA;
+}
+
+}  // namespace dec
+
+static int tc_row_blocks(const qkmla_decode_args* a) { return a->s_q * a->H / (pair_shape(a) ? 64 : tc_rows(a)); }
+
+size_t tc_workspace(const qkmla_decode_args* a, int sms) {
+    return split_scratch(a, tc_row_blocks(a), sms, nullptr).bytes;
 }
 
 int launch_decode_tc(const qkmla_decode_args* a, const DecodePlan& plan, cudaStream_t s) {
     const int sms = device_sm_count();
-    int max_items = 0;
-    tc_workspace(a, sms, &max_items);
     const int rows_o = pair_shape(a) ? 64 : tc_rows(a);
-    const int n_rb = a->s_q * a->H / rows_o;
-    uint8_t* ws = (uint8_t*)a->workspace;
-    WorkItem* items = (WorkItem*)ws;
-    size_t off = (size_t)max_items * sizeof(WorkItem);
-    int* n_items = (int*)(ws + off);
-    int* seq_nsplit = n_items + 4;
-    int* seq_part0 = seq_nsplit + a->B;
-    int* split_list = seq_part0 + a->B;
-    off += 16 + 3 * (size_t)a->B * sizeof(int);
-    off = (off + 255) & ~(size_t)255;
-    float* o_part = (float*)(ws + off);
-    float* lse_part = o_part + (size_t)max_items * a->s_q * a->H * a->d_c;
+    const int n_rb = tc_row_blocks(a);
+    const SplitScratch w = split_scratch(a, n_rb, sms, a->workspace);
+    const int max_items = w.max_items;
     int* status = device_status_ptr();
-    const int max_len = a->max_pages * a->page_size;
 
     const int tile = pair_shape(a) ? 64 : a->d_c == 256 ? tile_of<256>() : tile_of<512>();
     const int box = tile;
     SchedArgs sa;
-    sa.max_len = max_len;
+    sa.max_len = a->max_pages * a->page_size;
     sa.n_rb = n_rb;
     sa.sms = sms;
     sa.min_tokens = 512;
     sa.tile = tile;
     sa.fixed_splits = a->num_splits;
+    sa.min_len = a->s_q;
+    sa.window = sa.sinks = 0;
     // small batches: the decode and combine kernels plan the split themselves
     const int sched_inline = sched_in_kernel(a) ? 1 : 0;
-    if (!sched_inline &&
-        launch_pdl(sched_kernel, dim3(1), dim3(1024), 0, s, a->seq_lens, a->B, a->s_q, max_len, n_rb, sms,
-                   sa.min_tokens, tile, a->num_splits, items, n_items, seq_nsplit, seq_part0, split_list, status) !=
-            cudaSuccess)
-        return QKMLA_ERR_CUDA;
+    if (!sched_inline && launch_sched(a, sa, w, s) != QKMLA_OK) return QKMLA_ERR_CUDA;
 
     CUtensorMap lat, rope;
     const int row = a->d_c + a->d_r;
@@ -971,12 +997,12 @@ int launch_decode_tc(const qkmla_decode_args* a, const DecodePlan& plan, cudaStr
     tp.rows_o = rows_o;
     tp.scale = a->softmax_scale;
     tp.eps = a->eps;
-    tp.items = items;
-    tp.n_items = n_items;
+    tp.items = w.items;
+    tp.n_items = w.n_items;
     tp.sa = sa;
     tp.sched_inline = sched_inline;
-    tp.o_part = o_part;
-    tp.lse_part = lse_part;
+    tp.o_part = w.o_part;
+    tp.lse_part = w.lse_part;
     tp.o = a->o;
     tp.o_dtype = a->o_dtype;
     tp.lse = a->lse;
@@ -1002,16 +1028,7 @@ int launch_decode_tc(const qkmla_decode_args* a, const DecodePlan& plan, cudaStr
                    : launch_kernel<256, 32, false, 4, false>(lat, rope, qmap, tp, n_rb, max_items, s);
     }
     if (rc != QKMLA_OK) return rc;
-    // one CTA per merged row where few sequences make few, long, split rows (every
-    // CTA computes the plan, so many CTAs cost more than they give on large batches)
-    const int combine_ctas = std::min(a->B * a->s_q * a->H, (a->B <= 32 ? 8 : 2) * sms);
-    auto ck = a->d_c == 512 ? combine_var_kernel<4> : combine_var_kernel<2>;   // d_c = 128 x VEC
-    return launch_pdl(ck, dim3(combine_ctas), dim3(128), 0, s, (const float*)o_part, (const float*)lse_part,
-                      (const int*)seq_nsplit, (const int*)seq_part0, (const int*)split_list,
-                      (const int*)(n_items + 1), a->seq_lens, a->B, a->s_q, sa, sched_inline, a->s_q * a->H, a->o,
-                      a->o_dtype, a->lse) == cudaSuccess
-               ? QKMLA_OK
-               : QKMLA_ERR_CUDA;
+    return launch_combine_var(a, sa, w, s);
 }
 
 }  // namespace qkmla

@@ -107,6 +107,65 @@ def test_simt_splits(Q, splits):
     check(Q, R.Case([200, 0, 1, 90], window=60, sinks=5, s_q=2), simt=True, num_splits=splits)
 
 
+TC = [
+    dict(lens=[1]),
+    dict(lens=[0, 1, 2, 63, 64, 65, 127, 128, 129, 200, 400]),
+    dict(lens=[1000], num_splits=1),
+    dict(lens=[1000, 333], s_q=2, page=16),
+    dict(lens=[5, 64, 165], s_q=3, H=32, G=4, page=32),
+    dict(lens=[1, 2, 100], s_q=3),                                          # lengths below s_q: empty rows
+    dict(lens=[1, 2, 300], s_q=4, H=48, G=3, page=128),
+    dict(lens=[700, 77], window=1, page=64),
+    dict(lens=[700, 77, 10], window=50, sinks=4, s_q=2, page=16),
+    dict(lens=[1500, 177, 10], window=333, sinks=270, H=32, G=2, page=256),
+    dict(lens=[1500, 900], window=256, sinks=128, H=64, G=8, d_c=512, d_r=64, s_q=3, page=32),
+    dict(lens=[640, 100], H=128, G=8, d_c=512, d_r=64),
+    dict(lens=[640, 100], H=16, G=1, d_c=512, d_r=64, contiguous=True),
+    dict(lens=[300, 257], H=16, G=8, d_c=128, d_r=64, page=16),
+    dict(lens=[300, 257], H=32, G=8, d_c=128, d_r=32, page=16, s_q=2),
+    dict(lens=[300, 257], H=32, G=4, d_c=256, d_r=64, page=16, s_q=2),
+    dict(lens=[257, 20], alpha="f16"),
+    dict(lens=[257, 20], H=128, G=8, d_c=512, d_r=64, alpha="f16", window=100, sinks=3),
+    dict(lens=[257, 20], plain=True, outlier=1.0),
+    dict(lens=[2000, 900], num_splits=3),
+    dict(lens=[900, 300], spread=20.0),                                     # scales over 40 binades
+    dict(lens=[900, 300], spread=1.0, outlier=1e6),
+    dict(lens=[900, 300], zero=True),                                       # all-zero latents: scale 0
+    dict(lens=[1500], q_scale=1e-3, H=32, G=4),
+    dict(lens=[3000] * 5, d_c=512, d_r=64, H=128, G=8, s_q=2),
+    dict(lens=[(37 * k) % 300 for k in range(140)], window=100, sinks=5),   # planned by the scheduler kernel
+]
+
+
+@pytest.mark.parametrize("k", range(len(TC)))
+def test_q8_tensor_core(Q, k):
+    kw = dict(TC[k])
+    splits = kw.pop("num_splits", 0)
+    check(Q, R.Case(**kw), simt=False, num_splits=splits)
+
+
+def test_q8_tensor_core_bf16_output(Q):
+    check(Q, R.Case([600, 70], s_q=2), simt=False, o_dtype=torch.bfloat16)
+
+
+def test_q8_rising_logits(Q):
+    """Keys whose logits rise along the sequence move the running maximum in every tile."""
+    c = R.Case([1500], plain=True, outlier=1.0, seed=3)
+    g = np.random.Generator(np.random.PCG64(5))
+    direction = c.qt[0, 0, 0] / np.linalg.norm(c.qt[0, 0, 0])
+    lat = (0.1 * g.standard_normal((1500, c.d_c)) + np.linspace(-40, 40, 1500)[:, None] * direction).astype(np.float32)
+    codes, sc = R.quantise(lat)
+    t = np.arange(1500)
+    slot = c.table[0, t // c.page] * c.page + t % c.page
+    c.kv[slot, :c.d_c], c.kv_scale[slot] = codes, sc
+    kr = (c.kv[slot, c.d_c:].copy().view(np.uint16).astype(np.uint32) << 16).view(np.float32)
+    o, lse = R.attention(c.qt[0], c.aq[0], c.qr[0].astype(np.float64), R.e4m3_decode(codes) * sc[:, None], kr,
+                         np.ones((1500, c.G)), 1, 1500, 0, 0, c.scale, True)
+    c.o, c.lse = o[None], lse[None]
+    for splits in (1, 0):
+        check(Q, c, simt=False, num_splits=splits)
+
+
 APPEND = [
     dict(N=1), dict(N=16), dict(N=33), dict(N=257, G=8, d_c=512, d_h=128, d_r=64), dict(N=5, G=3, d_c=100, d_h=36, d_r=20),
     dict(N=40, rope=True), dict(N=300, G=8, d_c=512, d_h=128, d_r=64, rope=True), dict(N=20, alpha="f16"),
@@ -196,7 +255,7 @@ def test_append_q8_slot_out_of_range(Q):
 
 
 @pytest.mark.parametrize("cache", ["q8", "bf16"])
-@pytest.mark.parametrize("simt", [True])
+@pytest.mark.parametrize("simt", [True, False])
 def test_bad_page_and_length(Q, cache, simt):
     """A page id or a length out of range is reported; the other sequence keeps its result."""
     for bad_page in (True, False):
