@@ -32,13 +32,19 @@
 // tokens beside an outlier's scale below e4m3's range.  m and v are integers: every
 // rescale is a power of two, hence exact.
 //
-// Warps: 0 TMA producer (+ TMEM owner), 1 MMA issuer, 2-9 softmax and epilogue
-// (two groups of 128 threads = tokens; a group takes half the rows).  All waits are
+// The row blocks of a sequence read the same tiles: up to 4 of them form a cluster, each CTA loads
+// its share of a tile's tokens and multicasts it to all.  Without that the TMA unit bounds the
+// kernel: 128-byte rows of a box leave it at one per ~6 cycles (3600-4050 cycles for a tile of 85 KB,
+// whether or not L2 holds it), against 2100 of tensor time.
+//
+// Warps: 0 TMA producer (+ TMEM owner), 1 MMA issuer, then softmax and epilogue in
+// groups of 128 threads = tokens, 8 rows a group (16 rows a thread took 1450 cycles a tile).  All waits are
 // bounded (2 s).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "decode_common.cuh"
@@ -52,15 +58,16 @@ using namespace tc;
 using namespace dec;
 
 constexpr int kT = 128;              // tokens per tile
-constexpr int kThreads = 320;
+constexpr int HPT = 8;                // query rows of a softmax thread
 constexpr uint32_t kTmemCols = 512;
 constexpr float kPUnit = 32.f;       // P of the largest contribution: lazy maxima let it grow to 2^8 < 448
-constexpr float kLazyX = 256.f;      // 2^8: a weight this large moves the maximum of the logits
-constexpr float kLazyP = 256.f;      // a scaled weight this large moves the maximum of the contributions
+constexpr float kLazy = 256.f;       // a weight (or a scaled one) above this moves the running maxima
 
 template <int DC, int DR, int ROWS>
 struct Q8Layout {
     static constexpr int kN = 2 * ROWS;                       // hi and lo rows
+    static constexpr int kGroups = ROWS / HPT;                // softmax groups of 4 warps
+    static constexpr int kThreads = 64 + 128 * kGroups;
     static constexpr int kBlocks = DC / 128;                  // 128-column boxes = output chunks
     static constexpr int kRopeRow = DR * 2;                   // bytes: 128 (SW128) or 64 (SW64)
     static constexpr int kQLat = kBlocks * kN * 128;
@@ -77,7 +84,8 @@ struct Q8Layout {
     static constexpr int kNst = std::min(4, (232448 - kQ - kMiscMax - 8192) / kStage);
     static constexpr int kOffStage = kQ;
     static constexpr int kOffMisc = kQ + kNst * kStage;
-    static constexpr int kNumBars = 4 * kNst + 5;
+    static constexpr int kHalf = (kBlocks + 1) / 2;           // latent blocks in a stage's first part
+    static constexpr int kNumBars = 5 * kNst + 5;
     static constexpr int kBytes = kOffMisc + 512 + kRowFloats * 4 + 1024;
     static constexpr uint32_t kColO = 8 * ROWS;               // two buffers of S_hi S_lo R_hi R_lo
     static_assert(kNst >= 2 && kN <= kRopeRow, "two stages, and P fits the RoPE slot");
@@ -92,7 +100,7 @@ struct Q8Params {
     const float* kv_scale;
     const int32_t *seq_lens, *page_table;
     int64_t num_pages;
-    int page_size, max_pages, piece;     // piece: tokens per TMA box
+    int page_size, max_pages, piece;     // piece: tokens per TMA box, at most a CTA's share of a tile
     int B, s_q, H, G, window, sinks;
     float scale, eps;
     int plain, ak_f16;
@@ -100,6 +108,7 @@ struct Q8Params {
     const int* n_items;
     SchedArgs sa;
     int sched_inline;
+    int cluster;                 // CTAs (row blocks) sharing a tile: 1, 2 or 4
     float *o_part, *lse_part;
     void* o;
     int o_dtype;
@@ -107,7 +116,7 @@ struct Q8Params {
     int* status;
 };
 
-// hi and lo e4m3 parts of two values, each pair packed in 16 bits.
+// hi and lo e4m3 parts of two values, each pair packed in 16 bits: exact remainders.
 __device__ __forceinline__ void split_e4m3(float a, float b, uint32_t& hi, uint32_t& lo) {
     const __nv_fp8x2_storage_t h = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
     const float2 back = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3)));
@@ -115,6 +124,16 @@ __device__ __forceinline__ void split_e4m3(float a, float b, uint32_t& hi, uint3
         __nv_cvt_float2_to_fp8x2(make_float2(a - back.x, b - back.y), __NV_SATFINITE, __NV_E4M3);
     hi = h;
     lo = l;
+}
+// The same through fp16, for weights: fp16 holds 11 of their bits, hi and lo keep 8, and the
+// remainder is one packed subtraction.
+__device__ __forceinline__ void split_e4m3_f16(float2 v, uint32_t& hi, uint32_t& lo) {
+    const __half2 w = __floats2half2_rn(v.x, v.y);
+    const __nv_fp8x2_storage_t h =
+        __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(w), __NV_SATFINITE, __NV_E4M3);
+    const __half2 r = __hsub2(w, __half2(__nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3)));
+    hi = h;
+    lo = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(r), __NV_SATFINITE, __NV_E4M3);
 }
 
 __device__ __forceinline__ bool group_any(int grp, bool pred) {
@@ -134,32 +153,21 @@ __device__ __forceinline__ float redux_max(float v) {
     return __int_as_float(m >= 0 ? m : m ^ 0x7fffffff);
 }
 
-template <int N>
-__device__ __forceinline__ void tmem_ld(uint32_t a, uint32_t (&r)[N]) {
-    if constexpr (N == 16) tmem_ld16(a, r);
-    else tmem_ld8(a, r);
-}
-template <int N>
-__device__ __forceinline__ void tmem_st(uint32_t a, const uint32_t (&r)[N]) {
-    if constexpr (N == 16) tmem_st16(a, r);
-    else tmem_st8(a, r);
-}
-
 template <int DC, int DR, int ROWS>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(64 + 16 * ROWS, 1)
 decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ CUtensorMap tm_rope,
                  const Q8Params p) {
     using LY = Q8Layout<DC, DR, ROWS>;
-    constexpr int NST = LY::kNst, N = LY::kN, HPT = ROWS / 2;
+    constexpr int NST = LY::kNst, N = LY::kN, KB = LY::kBlocks, NW = 4 * LY::kGroups;
     extern __shared__ __align__(1024) uint8_t smraw[];
     uint8_t* sm = smraw + ((1024u - (smem_u32(smraw) & 1023u)) & 1023u);
     uint8_t* sQ = sm;
     uint64_t* bars = (uint64_t*)(sm + LY::kOffMisc);
     uint64_t* full = bars;                   // [NST] tile landed -> MMA
-    uint64_t* empty = bars + NST;            // [NST] output MMA done -> TMA
-    uint64_t* pfull = bars + 2 * NST;        // [NST] P written -> output MMA (one arrive per softmax warp)
-    uint64_t* odone = bars + 3 * NST;        // [NST] output MMA done -> softmax (rescale, epilogue)
-    uint64_t* sfull = bars + 4 * NST;        // [2] logit MMA done -> softmax
+    uint64_t* empty = full + NST;            // [NST][2] output MMA done with a part of the stage -> TMA
+    uint64_t* pfull = empty + 2 * NST;       // [NST] P written -> output MMA (one arrive per softmax warp)
+    uint64_t* odone = pfull + NST;           // [NST] output MMA done -> softmax (rescale, epilogue)
+    uint64_t* sfull = odone + NST;           // [2] logit MMA done -> softmax
     uint64_t* sfree = sfull + 2;             // [2] softmax read S, R -> MMA
     uint64_t* drain = sfree + 2;             // abort path: the MMAs in flight are done
     uint32_t* tmem_slot = (uint32_t*)(bars + LY::kNumBars);
@@ -195,19 +203,20 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
     const TileRange tiles(len, p.s_q, p.window, p.sinks, kT);
     const int jt0 = it.tile_begin;
     const int n_t = max(0, min(it.tile_end, tiles.count) - jt0);
-    // tokens some row of this CTA sees: [0, len_last) less [sinks, win_first)
-    const int i_first = row0 / p.H, i_last = (min(row0 + ROWS, n_rows) - 1) / p.H;
+    const uint32_t rank = cluster_ctarank();
+    const uint16_t everyone = (uint16_t)((1u << p.cluster) - 1u);
+    // tokens some row of the cluster sees: [0, len_last) less [sinks, win_first)
+    const int cl_row0 = row0 - (int)rank * ROWS;
+    const int i_first = cl_row0 / p.H, i_last = (min(cl_row0 + p.cluster * ROWS, n_rows) - 1) / p.H;
     const int len_last = max(0, len - p.s_q + i_last + 1);
     const int win_first = p.window > 0 ? len - p.s_q + i_first + 1 - p.window : 0;
-    // [all_lo, all_hi): tokens from the window on that every row sees; [0, all_sinks): sinks that every row sees
-    const int len_first = max(0, len - p.s_q + i_first + 1);
-    const int all_lo = p.window > 0 ? max(0, len - p.s_q + i_last + 1 - p.window) : 0;
 
     if (tid == 0) {
         if (bad && blockIdx.x == 0) report(p.status, QKMLA_ERR_DEVICE_BOUNDS);
         for (int i = 0; i < LY::kNumBars; ++i) {
-            const bool eight = (i >= 2 * NST && i < 3 * NST) || i == 4 * NST + 2 || i == 4 * NST + 3;
-            mbar_init(&bars[i], eight ? 8u : 1u);
+            const bool warps = (&bars[i] >= pfull && &bars[i] < odone) || (&bars[i] >= sfree && &bars[i] < drain);
+            const bool all = &bars[i] >= empty && &bars[i] < pfull;      // one commit per CTA of the cluster
+            mbar_init(&bars[i], warps ? (uint32_t)NW : all ? (uint32_t)p.cluster : 1u);
         }
         *abort_flag = 0;
         fence_barrier_init();
@@ -217,14 +226,18 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
     __syncthreads();
     pdl_wait();
     pdl_trigger();
+    if (p.cluster > 1) cluster_sync();         // every CTA's barriers exist before any remote access
 
-    // ---- TMA producer: lane q issues piece q of a tile (kT / piece pieces) ----
-    const int n_pieces = kT / p.piece;
+    // ---- TMA producer (warp 0): lane q holds piece q of a tile (kT / piece pieces); this CTA loads
+    //      those of its share ----
+    // A stage is freed and refilled in two parts -- the first half of the latent blocks; the rest with
+    // the RoPE key and the scalars -- so that its next load starts while the output MMAs still read it.
+    const int n_pieces = kT / p.piece, n_own = n_pieces / p.cluster, own0 = (int)rank * n_own;
     const uint32_t ak_row = p.plain ? 0u : (uint32_t)(p.G * (p.ak_f16 ? 2 : 4));
     const uint32_t piece_bytes = (uint32_t)p.piece * (DC + 2 * DR + 4 + ak_row);
-    auto issue_tile = [&](int j) {                            // whole warp 0
-        const int s = j % NST;
-        uint8_t* stg = sm + LY::kOffStage + s * LY::kStage;
+    int slots[8];                                             // slot of each piece; -1: nobody sees it
+    uint32_t n_want = 0;
+    auto locate_tile = [&](int j) {
         const int t0 = tiles.tile(jt0 + j) * kT + lane * p.piece;
         // a piece without a token that some row sees is not read (its rows are zeroed by the softmax)
         const bool want = lane < n_pieces && t0 < len_last && (t0 < p.sinks || t0 + p.piece > win_first);
@@ -237,28 +250,62 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
                 page = 0;
             }
         }
-        const int n_want = __popc(__ballot_sync(0xffffffffu, want));
-        if (lane == 0) mbar_arrive_expect_tx(&full[s], (uint32_t)n_want * piece_bytes);
-        __syncwarp();
-        if (want) {
-            const int64_t slot = page * p.page_size + t0 % p.page_size;
-            const int at = lane * p.piece;
+        const int slot = want ? (int)(page * p.page_size + t0 % p.page_size) : -1;
 #pragma unroll
-            for (int blk = 0; blk < LY::kBlocks; ++blk)
-                tma_load_2d(stg + blk * (kT * 128) + at * 128, &tm_lat, blk * 128, (int)slot, &full[s]);
-            tma_load_2d(stg + LY::kSLat + at * LY::kRopeRow, &tm_rope, 0, (int)slot, &full[s]);
-            bulk_load(stg + LY::kOffScale + at * 4, p.kv_scale + slot, (uint32_t)p.piece * 4, &full[s]);
-            if (ak_row) bulk_load(stg + LY::kOffAk + at * ak_row, p.ak + slot * ak_row, (uint32_t)p.piece * ak_row, &full[s]);
+        for (int q = 0; q < 8; ++q) slots[q] = __shfl_sync(0xffffffffu, slot, own0 + q);
+        n_want = (uint32_t)__popc(__ballot_sync(0xffffffffu, want));
+    };
+    auto issue_part = [&](int j, int part) {                  // lane 0; the slots of this CTA's pieces are in `slots`
+        const int s = j % NST;
+        uint8_t* stg = sm + LY::kOffStage + s * LY::kStage;
+        uint64_t* bar = &full[s];
+        if (part == 0) mbar_arrive_expect_tx(bar, n_want * piece_bytes);
+        const int blk0 = part ? LY::kHalf : 0, blk1 = part ? KB : LY::kHalf;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            if (q >= n_own) break;
+            const int slot = slots[q];
+            if (slot < 0) continue;
+            const int at = (own0 + q) * p.piece;
+            uint8_t* const rope = stg + LY::kSLat + at * LY::kRopeRow;
+            uint8_t* const scale = stg + LY::kOffScale + at * 4;
+            uint8_t* const ak = stg + LY::kOffAk + at * ak_row;
+            const uint8_t* ak_src = p.ak + (int64_t)slot * ak_row;
+            const uint32_t n4 = (uint32_t)p.piece * 4, na = (uint32_t)p.piece * ak_row;
+            if (p.cluster > 1) {
+                for (int blk = blk0; blk < blk1; ++blk)
+                    tma_load_2d_multicast(stg + blk * (kT * 128) + at * 128, &tm_lat, blk * 128, slot, bar, everyone);
+                if (part) {
+                    tma_load_2d_multicast(rope, &tm_rope, 0, slot, bar, everyone);
+                    bulk_load_multicast(scale, p.kv_scale + slot, n4, bar, everyone);
+                    if (ak_row) bulk_load_multicast(ak, ak_src, na, bar, everyone);
+                }
+            } else {
+                for (int blk = blk0; blk < blk1; ++blk)
+                    tma_load_2d(stg + blk * (kT * 128) + at * 128, &tm_lat, blk * 128, slot, bar);
+                if (part) {
+                    tma_load_2d(rope, &tm_rope, 0, slot, bar);
+                    bulk_load(scale, p.kv_scale + slot, n4, bar);
+                    if (ak_row) bulk_load(ak, ak_src, na, bar);
+                }
+            }
         }
     };
     const size_t grow0 = (size_t)b * n_rows + row0;           // first row in the query arrays
     if (warp == 0) {
         tmem_alloc(tmem_slot, kTmemCols);
         tmem_relinquish();
-        for (int j = 0; j < NST && j < n_t; ++j) issue_tile(j);
+        for (int j = 0; j < NST && j < n_t; ++j) {
+            locate_tile(j);
+            if (lane == 0) {
+                issue_part(j, 0);
+                issue_part(j, 1);
+            }
+            __syncwarp();
+        }
     } else if (warp >= 2) {
         // ---- prologue: the query rows as hi / lo parts, a warp per row ----
-        for (int r = warp - 2; r < ROWS; r += 8) {
+        for (int r = warp - 2; r < ROWS; r += NW) {
             const bool ok = row0 + r < n_rows;
             float q[DC / 32], top = 0.f;
             const __nv_bfloat16* src = p.qt + (grow0 + r) * DC + lane * (DC / 32);
@@ -325,21 +372,27 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
 
     if (warp == 0) {
         // ===================== TMA producer =====================
-        int issued = min(NST, n_t);
-        for (int j = NST; j < n_t; ++j) {
-            int go = 1;
-            if (lane == 0) go = wait_bounded(&empty[j % NST], ((j / NST) - 1) & 1, p.status) ? 1 : 0;
-            if (lane == 0 && *(volatile int*)abort_flag) go = 0;
-            if (!__shfl_sync(0xffffffffu, go, 0)) {
-                if (lane == 0) *(volatile int*)abort_flag = 1;
-                break;
+        bool go = true;
+        int j = NST;
+        for (; j < n_t && go; ++j) {
+            locate_tile(j);
+            int ok = 1;
+            if (lane == 0) {
+                for (int part = 0; part < 2 && ok; ++part) {
+                    ok = wait_bounded(&empty[(j % NST) * 2 + part], ((j / NST) - 1) & 1, p.status) ? 1 : 0;
+                    if (ok) issue_part(j, part);
+                }
+                if (*(volatile int*)abort_flag) ok = 0;
             }
-            issue_tile(j);
-            issued = j + 1;
+            go = __shfl_sync(0xffffffffu, ok, 0) != 0;
         }
-        // no exit with a copy in flight: on the ordinary path the MMA warp has waited for all of them
-        if (lane == 0 && *(volatile int*)abort_flag)
-            for (int j = max(0, issued - NST); j < issued; ++j) wait_bounded(&full[j % NST], (j / NST) & 1, p.status);
+        // no exit with a copy in flight: on the ordinary path the MMA warp has waited for all of them;
+        // an abandoned one is waited for here (parts never issued run into the bound)
+        if (!go && lane == 0) {
+            *(volatile int*)abort_flag = 1;
+            for (int q = max(0, j - 1 - NST); q < j; ++q)
+                wait_bounded(&full[q % NST], (q / NST) & 1, p.status, 10000000ull);
+        }
     } else if (warp == 1) {
         // ===================== MMA issuer: logits and outputs in readiness order =====================
         if (lane == 0) {
@@ -351,19 +404,23 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
                 tc_fence_after();
                 const uint32_t st = smem_u32(sm + LY::kOffStage + (j % NST) * LY::kStage);
                 const uint32_t d = tmem + (uint32_t)(j & 1) * (2 * N);
-#pragma unroll
-                for (int blk = 0; blk < LY::kBlocks; ++blk)
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        mma_f8(d, smem_desc(st + blk * (kT * 128) + kk * 32, 16, 1024, kSwizzle128B),
-                               smem_desc(q_addr + blk * (N * 128) + kk * 32, 16, 1024, kSwizzle128B), id_s,
-                               (blk > 0 || kk > 0) ? 1u : 0u);
                 constexpr uint32_t sw = DR == 64 ? kSwizzle128B : kSwizzle64B, sbo = DR == 64 ? 1024 : 512;
 #pragma unroll
                 for (int kk = 0; kk < DR / 16; ++kk)
                     mma_bf16(d + N, smem_desc(st + LY::kSLat + kk * 32, 16, sbo, sw),
                              smem_desc(q_addr + LY::kQLat + kk * 32, 16, sbo, sw), id_r, kk > 0 ? 1u : 0u);
+#pragma unroll
+                for (int blk = 0; blk < KB; ++blk)
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_f8(d, smem_desc(st + blk * (kT * 128) + kk * 32, 16, 1024, kSwizzle128B),
+                               smem_desc(q_addr + blk * (N * 128) + kk * 32, 16, 1024, kSwizzle128B), id_s,
+                               (blk > 0 || kk > 0) ? 1u : 0u);
                 mma_commit(&sfull[j & 1]);
+            };
+            auto release = [&](uint64_t* bar) {               // to every CTA that writes into the part
+                if (p.cluster > 1) mma_commit_multicast(bar, everyone);
+                else mma_commit(bar);
             };
             auto issue_o = [&](int j) {
                 tc_fence_after();
@@ -373,38 +430,37 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
                 // B: P, MN-major: a token's N codes in N bytes (swizzle of the same width), 8-token groups 8 N bytes apart.
                 constexpr uint32_t swp = N == 64 ? kSwizzle64B : kSwizzle32B;
 #pragma unroll
-                for (int c = 0; c < LY::kBlocks; ++c)
+                for (int c = 0; c < KB; ++c) {
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
                         mma_f8(tmem + LY::kColO + c * N, smem_desc(st + c * (kT * 128) + kk * 4096, kT * 128, 1024, kSwizzle128B),
                                smem_desc(st + LY::kSLat + kk * 32 * N, 8 * N, 8 * N, swp), id_o, (j > 0 || kk > 0) ? 1u : 0u);
-                mma_commit(&empty[s]);
+                    if (c == LY::kHalf - 1) release(&empty[s * 2]);
+                }
+                release(&empty[s * 2 + 1]);
                 mma_commit(&odone[s]);
             };
             int js = 0, jo = 0;
             bool ok = true;
-            uint64_t t_last = globaltimer();
+            uint64_t t_idle = 0;
             uint32_t idle = 0;
-            while (ok && jo < n_t) {
-                bool did = false;
+            while (jo < n_t) {
                 if (js < n_t && mbar_test_wait(&full[js % NST], (js / NST) & 1) &&
                     (js < 2 || mbar_test_wait(&sfree[js & 1], ((js >> 1) - 1) & 1))) {
                     issue_s(js);
                     ++js;
-                    did = true;
-                }
-                if (jo < js && mbar_test_wait(&pfull[jo % NST], (jo / NST) & 1)) {
+                    idle = 0;
+                } else if (jo < js && mbar_test_wait(&pfull[jo % NST], (jo / NST) & 1)) {
                     issue_o(jo);
                     ++jo;
-                    did = true;
-                }
-                if (did) {
                     idle = 0;
-                    t_last = globaltimer();
                 } else if ((++idle & 255u) == 0) {
-                    if (*(volatile int*)abort_flag || globaltimer() - t_last > kWaitNs) {
+                    const uint64_t now = globaltimer();
+                    if (idle == 256u) t_idle = now;
+                    if (*(volatile int*)abort_flag || now - t_idle > kWaitNs) {
                         report(p.status, QKMLA_ERR_TIMEOUT);
                         ok = false;
+                        break;
                     }
                 }
             }
@@ -416,18 +472,28 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
         }
     } else {
         // ===================== softmax: thread = token, HPT rows of its group =====================
-        const int sub = warp & 3, grp = warp >= 6 ? 1 : 0;
+        const int sub = warp & 3, grp = (warp - 2) >> 2;
         const uint32_t lane_base = (uint32_t)(32 * sub) << 16;
         const int tl = 32 * sub + lane;                      // token in the tile
         const int u0 = grp * HPT;                            // first row of the group
-        const int hpg = p.H / p.G;                           // 1, 2, 4, 8 or 16
-        const int hshift = 31 - __clz(hpg);
+        const int hshift = 31 - __clz(p.H / p.G);            // heads a group: 2, 4, 8 or 16 (H >= 16, G <= 8)
         const int h0 = (row0 + u0) % p.H;                    // its head: HPT divides H, so the rows share a query token
+        const int ak_at = tl * p.G + (h0 >> hshift);         // alpha^k of this token for the first of the rows
         const int n_row = max(0, len - p.s_q + (row0 + u0) / p.H + 1);   // causal length of these rows
         const int w_row = p.window > 0 ? n_row - p.window : 0;
-        float lsum[HPT];
+        // this group's rows in registers, two to a packed pair: -m, unit f, row sums
+        constexpr int HP2 = HPT / 2;
+        uint64_t nm2[HP2], f2v[HP2], lsum2[HP2];
+        auto reload = [&]() {
 #pragma unroll
-        for (int u = 0; u < HPT; ++u) lsum[u] = 0.f;
+            for (int u = 0; u < HP2; ++u) {
+                nm2[u] = f2(-m_s[u0 + 2 * u], -m_s[u0 + 2 * u + 1]);
+                f2v[u] = f2(f_s[u0 + 2 * u], f_s[u0 + 2 * u + 1]);
+            }
+        };
+#pragma unroll
+        for (int u = 0; u < HP2; ++u) lsum2[u] = f2(0.f, 0.f);
+        reload();
         bool ok = true;
         for (int j = 0; j < n_t; ++j) {
             const int s = j % NST, sb = j & 1;
@@ -435,55 +501,108 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
             const int t = tiles.tile(jt0 + j) * kT + tl;
             const bool sees = t < n_row && (t < p.sinks || t >= w_row);
             const bool any_sees = t < len_last && (t < p.sinks || t >= win_first);   // some row of the CTA
+            const bool masked = !__all_sync(0xffffffffu, sees);
             const bool got_s = wait_bounded(&sfull[sb], (j >> 1) & 1, p.status);
             tc_fence_after();
-            float x[HPT];
+            uint64_t x2[HP2];
+            const float st_raw = *reinterpret_cast<const float*>(stg + LY::kOffScale + tl * 4);
             {
-                uint32_t a[HPT], c[HPT];
+                uint32_t a[HPT], c[HPT], d[HPT], e[HPT];
                 const uint32_t base = tmem + (uint32_t)sb * (2 * N) + lane_base + u0;
-                tmem_ld<HPT>(base, a);
-                tmem_ld<HPT>(base + ROWS, c);
-                uint32_t d[HPT], e[HPT];
-                tmem_ld<HPT>(base + N, d);
-                tmem_ld<HPT>(base + N + ROWS, e);
+                tmem_ld8(base, a);
+                tmem_ld8(base + ROWS, c);
+                tmem_ld8(base + N, d);
+                tmem_ld8(base + N + ROWS, e);
+                // coefficient x alpha^k s_t of the rows while the loads run.  A group is 2^SH heads, known to
+                // the compiler: with a bound known only at run time the loads became a chain of
+                // branches, 2650 cycles a tile against 90 for the TMEM loads beside it
+                uint64_t ca2[HP2];
+                auto scale_rows = [&](auto sh, auto f16) {
+                    constexpr int SH = decltype(sh)::value;
+                    float ak[HPT];
+#pragma unroll
+                    for (int u = 0; u < HPT; ++u)
+                        ak[u] = (u & ((1 << SH) - 1)) == 0
+                                    ? st_raw * load_alpha<decltype(f16)::value>(stg + LY::kOffAk, ak_at + (u >> SH))
+                                    : ak[u & ~((1 << SH) - 1)];
+#pragma unroll
+                    for (int u = 0; u < HPT; u += 4) {
+                        const float4 cf = *reinterpret_cast<const float4*>(coef_s + u0 + u);
+                        ca2[u / 2] = f2_mul(f2(cf.x, cf.y), f2(ak[u], ak[u + 1]));
+                        ca2[u / 2 + 1] = f2_mul(f2(cf.z, cf.w), f2(ak[u + 2], ak[u + 3]));
+                    }
+                };
+                using std::integral_constant;
+                using yes = integral_constant<bool, true>;
+                using no = integral_constant<bool, false>;
+                if (p.plain) {
+#pragma unroll
+                    for (int u = 0; u < HPT; u += 4) {
+                        const float4 cf = *reinterpret_cast<const float4*>(coef_s + u0 + u);
+                        ca2[u / 2] = f2_mul(f2(cf.x, cf.y), f2(st_raw, st_raw));
+                        ca2[u / 2 + 1] = f2_mul(f2(cf.z, cf.w), f2(st_raw, st_raw));
+                    }
+                } else if (p.ak_f16) {
+                    if (hshift == 4) scale_rows(integral_constant<int, 4>(), yes());
+                    else if (hshift == 3) scale_rows(integral_constant<int, 3>(), yes());
+                    else if (hshift == 2) scale_rows(integral_constant<int, 2>(), yes());
+                    else scale_rows(integral_constant<int, 1>(), yes());
+                } else {
+                    if (hshift == 4) scale_rows(integral_constant<int, 4>(), no());
+                    else if (hshift == 3) scale_rows(integral_constant<int, 3>(), no());
+                    else if (hshift == 2) scale_rows(integral_constant<int, 2>(), no());
+                    else scale_rows(integral_constant<int, 1>(), no());
+                }
                 tmem_wait_ld();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sfree[sb]);
-                const float st = *reinterpret_cast<const float*>(stg + LY::kOffScale + tl * 4);
-                float aks = st;
 #pragma unroll
-                for (int u = 0; u < HPT; ++u) {
-                    if (!p.plain && (u == 0 || ((h0 + u) & (hpg - 1)) == 0)) {
-                        const int g = tl * p.G + ((h0 + u) >> hshift);
-                        aks = st * (p.ak_f16 ? load_alpha<true>(stg + LY::kOffAk, g) : load_alpha<false>(stg + LY::kOffAk, g));
-                    }
-                    x[u] = fmaf(aks * coef_s[u0 + u], __uint_as_float(a[u]) + __uint_as_float(c[u]),
-                                __uint_as_float(d[u]) + __uint_as_float(e[u]));
+                for (int u = 0; u < HP2; ++u) {
+                    const uint64_t sc = f2_add(f2(__uint_as_float(a[2 * u]), __uint_as_float(a[2 * u + 1])),
+                                               f2(__uint_as_float(c[2 * u]), __uint_as_float(c[2 * u + 1])));
+                    const uint64_t sr = f2_add(f2(__uint_as_float(d[2 * u]), __uint_as_float(d[2 * u + 1])),
+                                               f2(__uint_as_float(e[2 * u]), __uint_as_float(e[2 * u + 1])));
+                    x2[u] = f2_fma(ca2[u], sc, sr);
+                }
+                if (masked && !sees) {
+#pragma unroll
+                    for (int u = 0; u < HP2; ++u) x2[u] = f2(-INFINITY, -INFINITY);
                 }
             }
-            const float st = any_sees ? *reinterpret_cast<const float*>(stg + LY::kOffScale + tl * 4) : 0.f;
-            float e[HPT], w[HPT];
+            const float st = any_sees ? st_raw : 0.f;
+            uint64_t e2[HP2], w2[HP2];
             float top = 0.f;
+            // weights e = 2^(x - m) and, in units of the output product, w = e s_t f
             auto weigh = [&]() {
+                const uint64_t st2 = f2(st, st);
+                float t4[2] = {0.f, 0.f};
 #pragma unroll
-                for (int u = 0; u < HPT; ++u) {
-                    const float ex = fast_exp2(x[u] - m_s[u0 + u]);
-                    e[u] = sees ? ex : 0.f;
-                    w[u] = e[u] * (st * f_s[u0 + u]);
-                    top = fmax3(top, e[u], w[u]);
+                for (int u = 0; u < HP2; ++u) {
+                    const float2 d = f2_unpack(f2_add(x2[u], nm2[u]));
+                    float2 e = make_float2(fast_exp2(d.x), fast_exp2(d.y));
+                    e2[u] = f2(e.x, e.y);
+                    w2[u] = f2_mul(e2[u], f2_mul(st2, f2v[u]));
+                    const float2 w = f2_unpack(w2[u]);
+                    t4[u & 1] = fmax3(t4[u & 1], fmaxf(e.x, e.y), fmaxf(w.x, w.y));
+                }
+                top = fmaxf(t4[0], t4[1]);
+                if (masked && !sees) {                       // a row without a token yet has -inf less -inf
+#pragma unroll
+                    for (int u = 0; u < HP2; ++u) e2[u] = w2[u] = f2(0.f, 0.f);
                 }
             };
             weigh();
-            const bool need = top > kLazyX || (j == 0);
-            static_assert(kLazyX == kLazyP, "one comparison");
+            const bool need = top > kLazy || j == 0;
             if (group_any(grp, need || !got_s)) {
                 if (group_any(grp, !got_s)) { ok = false; break; }
                 // ---- exact maxima of this tile's logits and contributions, per row ----
-                const float ls = (sees && st > 0.f) ? log2f(st) : -INFINITY;
+                const float ls = st > 0.f ? log2f(st) : -INFINITY;
 #pragma unroll
                 for (int u = 0; u < HPT; ++u) {
-                    const float xv = (sees && x[u] == x[u]) ? x[u] : -INFINITY;
+                    const float2 xp = f2_unpack(x2[u / 2]);
+                    const float xu = (u & 1) ? xp.y : xp.x;
+                    const float xv = xu == xu ? xu : -INFINITY;
                     const float mx = redux_max(xv), vx = redux_max(xv + ls);
                     if (lane == 0) {
                         red_s[sub * ROWS + u0 + u] = mx;
@@ -527,51 +646,48 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
                         for (int c = 0; c < 2 * LY::kBlocks; ++c) {       // chunks x (hi, lo)
                             uint32_t v[HPT];
                             const uint32_t ta = tmem + LY::kColO + c * ROWS + u0 + lane_base;
-                            tmem_ld<HPT>(ta, v);
+                            tmem_ld8(ta, v);
                             tmem_wait_ld();
 #pragma unroll
                             for (int u = 0; u < HPT; ++u)
                                 v[u] = cr[u] == 0.f ? 0u : __float_as_uint(__uint_as_float(v[u]) * cr[u]);
-                            tmem_st<HPT>(ta, v);
+                            tmem_st8(ta, v);
                         }
                         tmem_wait_st();
                     }
                 }
 #pragma unroll
-                for (int u = 0; u < HPT; ++u) lsum[u] *= red_s[u0 + u];
+                for (int u = 0; u < HP2; ++u)
+                    lsum2[u] = f2_mul(lsum2[u], f2(red_s[u0 + 2 * u], red_s[u0 + 2 * u + 1]));
+                reload();
                 weigh();
                 group_sync(grp);                             // red_s, corr_s are read
             }
             uint32_t hi[HPT / 4], lo[HPT / 4];
 #pragma unroll
-            for (int u = 0; u < HPT; u += 4) {
+            for (int u = 0; u < HP2; u += 2) {
                 uint32_t h0, l0, h1, l1;
-                split_e4m3(w[u], w[u + 1], h0, l0);
-                split_e4m3(w[u + 2], w[u + 3], h1, l1);
-                hi[u / 4] = h0 | (h1 << 16);
-                lo[u / 4] = l0 | (l1 << 16);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) lsum[u + q] += e[u + q];
+                split_e4m3_f16(f2_unpack(w2[u]), h0, l0);
+                split_e4m3_f16(f2_unpack(w2[u + 1]), h1, l1);
+                hi[u / 2] = h0 | (h1 << 16);
+                lo[u / 2] = l0 | (l1 << 16);
+                lsum2[u] = f2_add(lsum2[u], e2[u]);
+                lsum2[u + 1] = f2_add(lsum2[u + 1], e2[u + 1]);
             }
             // P row of this token: HPT codes of hi at u0, of lo at ROWS + u0, 16-byte chunks XOR-swizzled
             // (64-byte rows by token / 2, 32-byte rows by token / 4)
-            uint8_t* pr = stg + LY::kSLat + tl * N;
-            if constexpr (N == 64) {
-                const uint32_t xr = (tl >> 1) & 3;
-                *reinterpret_cast<uint4*>(pr + (((uint32_t)grp ^ xr) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                *reinterpret_cast<uint4*>(pr + (((uint32_t)(2 + grp) ^ xr) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-            } else {
-                const uint32_t xr = (tl >> 2) & 1;
-                *reinterpret_cast<uint2*>(pr + ((0u ^ xr) << 4) + u0) = make_uint2(hi[0], hi[1]);
-                *reinterpret_cast<uint2*>(pr + ((1u ^ xr) << 4) + u0) = make_uint2(lo[0], lo[1]);
-            }
+            uint8_t* pr = stg + LY::kSLat + tl * N + (u0 & 15);
+            const uint32_t xr = N == 64 ? (tl >> 1) & 3 : (tl >> 2) & 1;
+            *reinterpret_cast<uint2*>(pr + (((uint32_t)(u0 >> 4) ^ xr) << 4)) = make_uint2(hi[0], hi[1]);
+            *reinterpret_cast<uint2*>(pr + (((uint32_t)((ROWS + u0) >> 4) ^ xr) << 4)) = make_uint2(lo[0], lo[1]);
             // a token no row sees: its latents (stale or never loaded) must not reach the output MMA as NaN
             if (!any_sees) {
+                constexpr int kShare = 8 / LY::kGroups;      // 16-byte chunks of a block's row
 #pragma unroll
-                for (int blk = 0; blk < LY::kBlocks; ++blk)
+                for (int blk = 0; blk < KB; ++blk)
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        *reinterpret_cast<uint4*>(stg + blk * (kT * 128) + tl * 128 + (((4 * grp + c) ^ (tl & 7)) << 4)) =
+                    for (int c = 0; c < kShare; ++c)
+                        *reinterpret_cast<uint4*>(stg + blk * (kT * 128) + tl * 128 + (((kShare * grp + c) ^ (tl & 7)) << 4)) =
                             make_uint4(0u, 0u, 0u, 0u);
             }
             fence_proxy_async_smem();
@@ -583,7 +699,8 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
         // ---- epilogue: row sums over the tokens, then O^T / (f l) ----
 #pragma unroll
         for (int u = 0; u < HPT; ++u) {
-            const float v = warp_sum(lsum[u]);
+            const float2 ls = f2_unpack(lsum2[u / 2]);
+            const float v = warp_sum((u & 1) ? ls.y : ls.x);
             if (lane == 0) red_s[sub * ROWS + u0 + u] = v;
         }
         const bool got_last = (ok && n_t > 0) ? wait_bounded(&odone[(n_t - 1) % NST], ((n_t - 1) / NST) & 1, p.status) : ok;
@@ -605,8 +722,8 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
         for (int c = 0; c < LY::kBlocks; ++c) {
             uint32_t a[HPT], d[HPT];
             if (n_t > 0) {
-                tmem_ld<HPT>(tmem + LY::kColO + c * N + u0 + lane_base, a);
-                tmem_ld<HPT>(tmem + LY::kColO + c * N + ROWS + u0 + lane_base, d);
+                tmem_ld8(tmem + LY::kColO + c * N + u0 + lane_base, a);
+                tmem_ld8(tmem + LY::kColO + c * N + ROWS + u0 + lane_base, d);
                 tmem_wait_ld();
             }
             const int col = c * 128 + tl;
@@ -625,6 +742,7 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
     __syncwarp();
     tc_fence_before();
     __syncthreads();
+    if (p.cluster > 1) cluster_sync();         // no CTA leaves while another may still write or signal here
     if (warp == 0) {
         __syncwarp();
         tc_fence_after();
@@ -650,19 +768,24 @@ int q8_row_blocks(const qkmla_decode_args* a) {
     const int r = q8_rows(a);
     return (a->s_q * a->H + r - 1) / r;
 }
+int q8_cluster(const qkmla_decode_args* a) {
+    const int n = q8_row_blocks(a);
+    return n % 4 == 0 ? 4 : n % 2 == 0 ? 2 : 1;
+}
 
 template <int DC, int DR, int ROWS>
 int launch_q8(const Q8Params& q, const CUtensorMap& lat, const CUtensorMap& rope, dim3 grid, cudaStream_t s) {
     auto k = decode_q8_kernel<DC, DR, ROWS>;
     constexpr int bytes = Q8Layout<DC, DR, ROWS>::kBytes;
     if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return QKMLA_ERR_CUDA;
-    return launch_pdl(k, grid, dim3(kThreads), bytes, s, lat, rope, q) == cudaSuccess ? QKMLA_OK : QKMLA_ERR_CUDA;
+    return launch_pdl_cluster(k, grid, dim3(Q8Layout<DC, DR, ROWS>::kThreads), q.cluster, bytes, s, lat, rope, q) == cudaSuccess ? QKMLA_OK
+                                                                                                    : QKMLA_ERR_CUDA;
 }
 
 }  // namespace
 
-// 8-bit cache shapes of the tensor-core kernel.  A thread's rows (8 or 16) share a query
-// token when they divide H; a tile is made of whole pages or a page of whole tiles.
+// 8-bit cache shapes of the tensor-core kernel.  A thread's 8 rows share a query
+// token when 8 divides H; a tile is made of whole pages or a page of whole tiles.
 bool q8_tc_supported(const qkmla_decode_args* a, const DecodeExt& x) {
     if (a->cache_dtype != QKMLA_E4M3) return false;
     if (!((a->d_c == 512 && a->d_r == 64) || (a->d_c == 256 && (a->d_r == 32 || a->d_r == 64)) ||
@@ -710,7 +833,8 @@ int launch_decode_q8(const qkmla_decode_args* a, const DecodeExt& x, cudaStream_
     q.num_pages = a->num_slots / a->page_size;
     q.page_size = a->page_size;
     q.max_pages = a->max_pages;
-    q.piece = std::min(a->page_size, kT);
+    q.cluster = q8_cluster(a);
+    q.piece = std::min(a->page_size, kT / q.cluster);
     q.B = a->B; q.s_q = a->s_q; q.H = a->H; q.G = a->G;
     q.window = x.window;
     q.sinks = x.sinks;
