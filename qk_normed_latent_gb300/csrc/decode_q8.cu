@@ -32,12 +32,7 @@
 // tokens beside an outlier's scale below e4m3's range.  m and v are integers: every
 // rescale is a power of two, hence exact.
 //
-// The row blocks of a sequence read the same tiles: up to 4 of them form a cluster, each CTA loads
-// its share of a tile's tokens and multicasts it to all.  Without that the TMA unit bounds the
-// kernel: 128-byte rows of a box leave it at one per ~6 cycles (3600-4050 cycles for a tile of 85 KB,
-// whether or not L2 holds it), against 2100 of tensor time.
-//
-// Warps: 0 TMA producer (+ TMEM owner), 1 MMA issuer, then softmax and epilogue in
+// Warps: 0 TMA producer (+ TMEM owner), 1 logit MMAs, 2 output MMAs, then softmax and epilogue in
 // groups of 128 threads = tokens, 8 rows a group (16 rows a thread took 1450 cycles a tile).  All waits are
 // bounded (2 s).
 #include <cuda.h>
@@ -67,7 +62,7 @@ template <int DC, int DR, int ROWS>
 struct Q8Layout {
     static constexpr int kN = 2 * ROWS;                       // hi and lo rows
     static constexpr int kGroups = ROWS / HPT;                // softmax groups of 4 warps
-    static constexpr int kThreads = 64 + 128 * kGroups;
+    static constexpr int kThreads = 96 + 128 * kGroups;
     static constexpr int kBlocks = DC / 128;                  // 128-column boxes = output chunks
     static constexpr int kRopeRow = DR * 2;                   // bytes: 128 (SW128) or 64 (SW64)
     static constexpr int kQLat = kBlocks * kN * 128;
@@ -84,8 +79,8 @@ struct Q8Layout {
     static constexpr int kNst = std::min(4, (232448 - kQ - kMiscMax - 8192) / kStage);
     static constexpr int kOffStage = kQ;
     static constexpr int kOffMisc = kQ + kNst * kStage;
-    static constexpr int kHalf = (kBlocks + 1) / 2;           // latent blocks in a stage's first part
-    static constexpr int kNumBars = 5 * kNst + 5;
+    static constexpr int kParts = kBlocks + 1;                // a stage's parts: latent blocks; RoPE key + scalars
+    static constexpr int kNumBars = 2 * kNst * kParts + 2 * kNst + 6;
     static constexpr int kBytes = kOffMisc + 512 + kRowFloats * 4 + 1024;
     static constexpr uint32_t kColO = 8 * ROWS;               // two buffers of S_hi S_lo R_hi R_lo
     static_assert(kNst >= 2 && kN <= kRopeRow, "two stages, and P fits the RoPE slot");
@@ -100,7 +95,7 @@ struct Q8Params {
     const float* kv_scale;
     const int32_t *seq_lens, *page_table;
     int64_t num_pages;
-    int page_size, max_pages, piece;     // piece: tokens per TMA box, at most a CTA's share of a tile
+    int page_size, max_pages, piece;     // piece: tokens per TMA box
     int B, s_q, H, G, window, sinks;
     float scale, eps;
     int plain, ak_f16;
@@ -108,7 +103,6 @@ struct Q8Params {
     const int* n_items;
     SchedArgs sa;
     int sched_inline;
-    int cluster;                 // CTAs (row blocks) sharing a tile: 1, 2 or 4
     float *o_part, *lse_part;
     void* o;
     int o_dtype;
@@ -154,22 +148,22 @@ __device__ __forceinline__ float redux_max(float v) {
 }
 
 template <int DC, int DR, int ROWS>
-__global__ void __launch_bounds__(64 + 16 * ROWS, 1)
+__global__ void __launch_bounds__(96 + 16 * ROWS, 1)
 decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ CUtensorMap tm_rope,
                  const Q8Params p) {
     using LY = Q8Layout<DC, DR, ROWS>;
-    constexpr int NST = LY::kNst, N = LY::kN, KB = LY::kBlocks, NW = 4 * LY::kGroups;
+    constexpr int NST = LY::kNst, N = LY::kN, KB = LY::kBlocks, KP = LY::kParts, NW = 4 * LY::kGroups;
     extern __shared__ __align__(1024) uint8_t smraw[];
     uint8_t* sm = smraw + ((1024u - (smem_u32(smraw) & 1023u)) & 1023u);
     uint8_t* sQ = sm;
     uint64_t* bars = (uint64_t*)(sm + LY::kOffMisc);
-    uint64_t* full = bars;                   // [NST] tile landed -> MMA
-    uint64_t* empty = full + NST;            // [NST][2] output MMA done with a part of the stage -> TMA
-    uint64_t* pfull = empty + 2 * NST;       // [NST] P written -> output MMA (one arrive per softmax warp)
+    uint64_t* full = bars;                   // [NST][KP] part of a tile landed -> logit MMA
+    uint64_t* empty = full + NST * KP;       // [NST][KP] output MMA done with the part -> TMA
+    uint64_t* pfull = empty + NST * KP;      // [NST] P written -> output MMA (one arrive per softmax warp)
     uint64_t* odone = pfull + NST;           // [NST] output MMA done -> softmax (rescale, epilogue)
     uint64_t* sfull = odone + NST;           // [2] logit MMA done -> softmax
     uint64_t* sfree = sfull + 2;             // [2] softmax read S, R -> MMA
-    uint64_t* drain = sfree + 2;             // abort path: the MMAs in flight are done
+    uint64_t* drain = sfree + 2;             // [2] abort path: an issuer's MMAs in flight are done
     uint32_t* tmem_slot = (uint32_t*)(bars + LY::kNumBars);
     int* abort_flag = (int*)(tmem_slot + 1);
     float* coef_s = (float*)(sm + LY::kOffMisc + 512);   // scale log2e alpha^q x the row's code scale
@@ -203,11 +197,8 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
     const TileRange tiles(len, p.s_q, p.window, p.sinks, kT);
     const int jt0 = it.tile_begin;
     const int n_t = max(0, min(it.tile_end, tiles.count) - jt0);
-    const uint32_t rank = cluster_ctarank();
-    const uint16_t everyone = (uint16_t)((1u << p.cluster) - 1u);
-    // tokens some row of the cluster sees: [0, len_last) less [sinks, win_first)
-    const int cl_row0 = row0 - (int)rank * ROWS;
-    const int i_first = cl_row0 / p.H, i_last = (min(cl_row0 + p.cluster * ROWS, n_rows) - 1) / p.H;
+    // tokens some row of this CTA sees: [0, len_last) less [sinks, win_first)
+    const int i_first = row0 / p.H, i_last = (min(row0 + ROWS, n_rows) - 1) / p.H;
     const int len_last = max(0, len - p.s_q + i_last + 1);
     const int win_first = p.window > 0 ? len - p.s_q + i_first + 1 - p.window : 0;
 
@@ -215,8 +206,7 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
         if (bad && blockIdx.x == 0) report(p.status, QKMLA_ERR_DEVICE_BOUNDS);
         for (int i = 0; i < LY::kNumBars; ++i) {
             const bool warps = (&bars[i] >= pfull && &bars[i] < odone) || (&bars[i] >= sfree && &bars[i] < drain);
-            const bool all = &bars[i] >= empty && &bars[i] < pfull;      // one commit per CTA of the cluster
-            mbar_init(&bars[i], warps ? (uint32_t)NW : all ? (uint32_t)p.cluster : 1u);
+            mbar_init(&bars[i], warps ? (uint32_t)NW : 1u);
         }
         *abort_flag = 0;
         fence_barrier_init();
@@ -226,15 +216,15 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
     __syncthreads();
     pdl_wait();
     pdl_trigger();
-    if (p.cluster > 1) cluster_sync();         // every CTA's barriers exist before any remote access
 
-    // ---- TMA producer (warp 0): lane q holds piece q of a tile (kT / piece pieces); this CTA loads
-    //      those of its share ----
-    // A stage is freed and refilled in two parts -- the first half of the latent blocks; the rest with
-    // the RoPE key and the scalars -- so that its next load starts while the output MMAs still read it.
-    const int n_pieces = kT / p.piece, n_own = n_pieces / p.cluster, own0 = (int)rank * n_own;
+    // ---- TMA producer (warp 0): lane q looks up piece q of a tile (kT / piece pieces), lane 0 loads them ----
+    // A stage is filled and freed in parts -- 128 latents of every token, the RoPE key with the scalars
+    // last: its logit MMAs start on the first part, and the load of a part two tiles on starts when the
+    // output MMA of its 128 latents is done.
+    const int n_pieces = kT / p.piece;
     const uint32_t ak_row = p.plain ? 0u : (uint32_t)(p.G * (p.ak_f16 ? 2 : 4));
-    const uint32_t piece_bytes = (uint32_t)p.piece * (DC + 2 * DR + 4 + ak_row);
+    const uint32_t lat_bytes = (uint32_t)p.piece * 128u;
+    const uint32_t aux_bytes = (uint32_t)p.piece * (2 * DR + 4 + ak_row);
     int slots[8];                                             // slot of each piece; -1: nobody sees it
     uint32_t n_want = 0;
     auto locate_tile = [&](int j) {
@@ -252,43 +242,29 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
         }
         const int slot = want ? (int)(page * p.page_size + t0 % p.page_size) : -1;
 #pragma unroll
-        for (int q = 0; q < 8; ++q) slots[q] = __shfl_sync(0xffffffffu, slot, own0 + q);
+        for (int q = 0; q < 8; ++q) slots[q] = __shfl_sync(0xffffffffu, slot, q);
         n_want = (uint32_t)__popc(__ballot_sync(0xffffffffu, want));
     };
-    auto issue_part = [&](int j, int part) {                  // lane 0; the slots of this CTA's pieces are in `slots`
+    auto issue_part = [&](int j, int part) {                  // lane 0
         const int s = j % NST;
         uint8_t* stg = sm + LY::kOffStage + s * LY::kStage;
-        uint64_t* bar = &full[s];
-        if (part == 0) mbar_arrive_expect_tx(bar, n_want * piece_bytes);
-        const int blk0 = part ? LY::kHalf : 0, blk1 = part ? KB : LY::kHalf;
+        uint64_t* bar = &full[s * KP + part];
+        mbar_arrive_expect_tx(bar, n_want * (part < KB ? lat_bytes : aux_bytes));
+        if (part < KB) {
+            uint8_t* dst = stg + part * (kT * 128);
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                if (q < n_pieces && slots[q] >= 0) tma_load_2d(dst + q * lat_bytes, &tm_lat, part * 128, slots[q], bar);
+            return;
+        }
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
-            if (q >= n_own) break;
-            const int slot = slots[q];
-            if (slot < 0) continue;
-            const int at = (own0 + q) * p.piece;
-            uint8_t* const rope = stg + LY::kSLat + at * LY::kRopeRow;
-            uint8_t* const scale = stg + LY::kOffScale + at * 4;
-            uint8_t* const ak = stg + LY::kOffAk + at * ak_row;
-            const uint8_t* ak_src = p.ak + (int64_t)slot * ak_row;
-            const uint32_t n4 = (uint32_t)p.piece * 4, na = (uint32_t)p.piece * ak_row;
-            if (p.cluster > 1) {
-                for (int blk = blk0; blk < blk1; ++blk)
-                    tma_load_2d_multicast(stg + blk * (kT * 128) + at * 128, &tm_lat, blk * 128, slot, bar, everyone);
-                if (part) {
-                    tma_load_2d_multicast(rope, &tm_rope, 0, slot, bar, everyone);
-                    bulk_load_multicast(scale, p.kv_scale + slot, n4, bar, everyone);
-                    if (ak_row) bulk_load_multicast(ak, ak_src, na, bar, everyone);
-                }
-            } else {
-                for (int blk = blk0; blk < blk1; ++blk)
-                    tma_load_2d(stg + blk * (kT * 128) + at * 128, &tm_lat, blk * 128, slot, bar);
-                if (part) {
-                    tma_load_2d(rope, &tm_rope, 0, slot, bar);
-                    bulk_load(scale, p.kv_scale + slot, n4, bar);
-                    if (ak_row) bulk_load(ak, ak_src, na, bar);
-                }
-            }
+            if (q >= n_pieces || slots[q] < 0) continue;
+            const int at = q * p.piece;
+            tma_load_2d(stg + LY::kSLat + at * LY::kRopeRow, &tm_rope, 0, slots[q], bar);
+            bulk_load(stg + LY::kOffScale + at * 4, p.kv_scale + slots[q], (uint32_t)p.piece * 4, bar);
+            if (ak_row)
+                bulk_load(stg + LY::kOffAk + at * ak_row, p.ak + (int64_t)slots[q] * ak_row, (uint32_t)p.piece * ak_row, bar);
         }
     };
     const size_t grow0 = (size_t)b * n_rows + row0;           // first row in the query arrays
@@ -297,15 +273,13 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
         tmem_relinquish();
         for (int j = 0; j < NST && j < n_t; ++j) {
             locate_tile(j);
-            if (lane == 0) {
-                issue_part(j, 0);
-                issue_part(j, 1);
-            }
+            if (lane == 0)
+                for (int part = 0; part < KP; ++part) issue_part(j, part);
             __syncwarp();
         }
-    } else if (warp >= 2) {
+    } else if (warp >= 3) {
         // ---- prologue: the query rows as hi / lo parts, a warp per row ----
-        for (int r = warp - 2; r < ROWS; r += NW) {
+        for (int r = warp - 3; r < ROWS; r += NW) {
             const bool ok = row0 + r < n_rows;
             float q[DC / 32], top = 0.f;
             const __nv_bfloat16* src = p.qt + (grow0 + r) * DC + lane * (DC / 32);
@@ -378,8 +352,8 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
             locate_tile(j);
             int ok = 1;
             if (lane == 0) {
-                for (int part = 0; part < 2 && ok; ++part) {
-                    ok = wait_bounded(&empty[(j % NST) * 2 + part], ((j / NST) - 1) & 1, p.status) ? 1 : 0;
+                for (int part = 0; part < KP && ok; ++part) {
+                    ok = wait_bounded(&empty[(j % NST) * KP + part], ((j / NST) - 1) & 1, p.status) ? 1 : 0;
                     if (ok) issue_part(j, part);
                 }
                 if (*(volatile int*)abort_flag) ok = 0;
@@ -391,41 +365,59 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
         if (!go && lane == 0) {
             *(volatile int*)abort_flag = 1;
             for (int q = max(0, j - 1 - NST); q < j; ++q)
-                wait_bounded(&full[q % NST], (q / NST) & 1, p.status, 10000000ull);
+                for (int part = 0; part < KP; ++part)
+                    wait_bounded(&full[(q % NST) * KP + part], (q / NST) & 1, p.status, 10000000ull);
         }
     } else if (warp == 1) {
-        // ===================== MMA issuer: logits and outputs in readiness order =====================
+        // ===================== logit MMAs =====================
         if (lane == 0) {
             const uint32_t id_s = idesc_e4m3(kT, N, 0, 0);
             const uint32_t id_r = idesc_bf16(kT, N, 0, 0);
-            const uint32_t id_o = idesc_e4m3(128, N, 1, 1);
             const uint32_t q_addr = smem_u32(sQ);
-            auto issue_s = [&](int j) {
-                tc_fence_after();
-                const uint32_t st = smem_u32(sm + LY::kOffStage + (j % NST) * LY::kStage);
+            constexpr uint32_t sw = DR == 64 ? kSwizzle128B : kSwizzle64B, sbo = DR == 64 ? 1024 : 512;
+            bool ok = true;
+            for (int j = 0; j < n_t && ok; ++j) {
+                const int s = j % NST;
+                const uint32_t st = smem_u32(sm + LY::kOffStage + s * LY::kStage);
                 const uint32_t d = tmem + (uint32_t)(j & 1) * (2 * N);
-                constexpr uint32_t sw = DR == 64 ? kSwizzle128B : kSwizzle64B, sbo = DR == 64 ? 1024 : 512;
+                if (j >= 2) ok = wait_bounded(&sfree[j & 1], ((j >> 1) - 1) & 1, p.status);
 #pragma unroll
-                for (int kk = 0; kk < DR / 16; ++kk)
-                    mma_bf16(d + N, smem_desc(st + LY::kSLat + kk * 32, 16, sbo, sw),
-                             smem_desc(q_addr + LY::kQLat + kk * 32, 16, sbo, sw), id_r, kk > 0 ? 1u : 0u);
-#pragma unroll
-                for (int blk = 0; blk < KB; ++blk)
+                for (int blk = 0; blk < KB; ++blk) {
+                    ok = ok && wait_bounded(&full[s * KP + blk], (j / NST) & 1, p.status);
+                    if (!ok) break;
+                    tc_fence_after();
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
                         mma_f8(d, smem_desc(st + blk * (kT * 128) + kk * 32, 16, 1024, kSwizzle128B),
                                smem_desc(q_addr + blk * (N * 128) + kk * 32, 16, 1024, kSwizzle128B), id_s,
                                (blk > 0 || kk > 0) ? 1u : 0u);
-                mma_commit(&sfull[j & 1]);
-            };
-            auto release = [&](uint64_t* bar) {               // to every CTA that writes into the part
-                if (p.cluster > 1) mma_commit_multicast(bar, everyone);
-                else mma_commit(bar);
-            };
-            auto issue_o = [&](int j) {
+                }
+                ok = ok && wait_bounded(&full[s * KP + KB], (j / NST) & 1, p.status) && !*(volatile int*)abort_flag;
+                if (!ok) break;
                 tc_fence_after();
+#pragma unroll
+                for (int kk = 0; kk < DR / 16; ++kk)
+                    mma_bf16(d + N, smem_desc(st + LY::kSLat + kk * 32, 16, sbo, sw),
+                             smem_desc(q_addr + LY::kQLat + kk * 32, 16, sbo, sw), id_r, kk > 0 ? 1u : 0u);
+                mma_commit(&sfull[j & 1]);
+            }
+            if (!ok) {                       // no exit with an MMA in flight
+                *(volatile int*)abort_flag = 1;
+                mma_commit(&drain[0]);
+                wait_bounded(&drain[0], 0, p.status);
+            }
+        }
+    } else if (warp == 2) {
+        // ===================== output MMAs (a thread of their own: neither issue waits for the other's data) ==========
+        if (lane == 0) {
+            const uint32_t id_o = idesc_e4m3(128, N, 1, 1);
+            bool ok = true;
+            for (int j = 0; j < n_t && ok; ++j) {
                 const int s = j % NST;
                 const uint32_t st = smem_u32(sm + LY::kOffStage + s * LY::kStage);
+                ok = wait_bounded(&pfull[s], (j / NST) & 1, p.status) && !*(volatile int*)abort_flag;
+                if (!ok) break;
+                tc_fence_after();
                 // A: a chunk's 128 latents x 32 tokens, MN-major (8-token groups 1024 B apart).
                 // B: P, MN-major: a token's N codes in N bytes (swizzle of the same width), 8-token groups 8 N bytes apart.
                 constexpr uint32_t swp = N == 64 ? kSwizzle64B : kSwizzle32B;
@@ -435,44 +427,20 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
                     for (int kk = 0; kk < 4; ++kk)
                         mma_f8(tmem + LY::kColO + c * N, smem_desc(st + c * (kT * 128) + kk * 4096, kT * 128, 1024, kSwizzle128B),
                                smem_desc(st + LY::kSLat + kk * 32 * N, 8 * N, 8 * N, swp), id_o, (j > 0 || kk > 0) ? 1u : 0u);
-                    if (c == LY::kHalf - 1) release(&empty[s * 2]);
+                    mma_commit(&empty[s * KP + c]);
                 }
-                release(&empty[s * 2 + 1]);
+                mma_commit(&empty[s * KP + KB]);
                 mma_commit(&odone[s]);
-            };
-            int js = 0, jo = 0;
-            bool ok = true;
-            uint64_t t_idle = 0;
-            uint32_t idle = 0;
-            while (jo < n_t) {
-                if (js < n_t && mbar_test_wait(&full[js % NST], (js / NST) & 1) &&
-                    (js < 2 || mbar_test_wait(&sfree[js & 1], ((js >> 1) - 1) & 1))) {
-                    issue_s(js);
-                    ++js;
-                    idle = 0;
-                } else if (jo < js && mbar_test_wait(&pfull[jo % NST], (jo / NST) & 1)) {
-                    issue_o(jo);
-                    ++jo;
-                    idle = 0;
-                } else if ((++idle & 255u) == 0) {
-                    const uint64_t now = globaltimer();
-                    if (idle == 256u) t_idle = now;
-                    if (*(volatile int*)abort_flag || now - t_idle > kWaitNs) {
-                        report(p.status, QKMLA_ERR_TIMEOUT);
-                        ok = false;
-                        break;
-                    }
-                }
             }
-            if (!ok) {                       // no exit with an MMA in flight
+            if (!ok) {
                 *(volatile int*)abort_flag = 1;
-                mma_commit(drain);
-                wait_bounded(drain, 0, p.status);
+                mma_commit(&drain[1]);
+                wait_bounded(&drain[1], 0, p.status);
             }
         }
     } else {
         // ===================== softmax: thread = token, HPT rows of its group =====================
-        const int sub = warp & 3, grp = (warp - 2) >> 2;
+        const int sub = warp & 3, grp = (warp - 3) >> 2;
         const uint32_t lane_base = (uint32_t)(32 * sub) << 16;
         const int tl = 32 * sub + lane;                      // token in the tile
         const int u0 = grp * HPT;                            // first row of the group
@@ -610,7 +578,7 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
                     }
                 }
                 group_sync(grp);
-                const int gt = tid - 64 - grp * 128;
+                const int gt = tid - 96 - grp * 128;
                 if (gt < HPT) {
                     const int r = u0 + gt;
                     float mx = red_s[r], vx = red_s[4 * ROWS + r];
@@ -706,7 +674,7 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
         const bool got_last = (ok && n_t > 0) ? wait_bounded(&odone[(n_t - 1) % NST], ((n_t - 1) / NST) & 1, p.status) : ok;
         if (group_any(grp, !got_last)) *(volatile int*)abort_flag = 1;
         tc_fence_after();
-        const int gt = tid - 64 - grp * 128;
+        const int gt = tid - 96 - grp * 128;
         if (gt < HPT) {
             const int r = u0 + gt;
             const float l = (red_s[r] + red_s[ROWS + r]) + (red_s[2 * ROWS + r] + red_s[3 * ROWS + r]);
@@ -742,7 +710,6 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (p.cluster > 1) cluster_sync();         // no CTA leaves while another may still write or signal here
     if (warp == 0) {
         __syncwarp();
         tc_fence_after();
@@ -768,18 +735,15 @@ int q8_row_blocks(const qkmla_decode_args* a) {
     const int r = q8_rows(a);
     return (a->s_q * a->H + r - 1) / r;
 }
-int q8_cluster(const qkmla_decode_args* a) {
-    const int n = q8_row_blocks(a);
-    return n % 4 == 0 ? 4 : n % 2 == 0 ? 2 : 1;
-}
 
 template <int DC, int DR, int ROWS>
 int launch_q8(const Q8Params& q, const CUtensorMap& lat, const CUtensorMap& rope, dim3 grid, cudaStream_t s) {
     auto k = decode_q8_kernel<DC, DR, ROWS>;
     constexpr int bytes = Q8Layout<DC, DR, ROWS>::kBytes;
     if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return QKMLA_ERR_CUDA;
-    return launch_pdl_cluster(k, grid, dim3(Q8Layout<DC, DR, ROWS>::kThreads), q.cluster, bytes, s, lat, rope, q) == cudaSuccess ? QKMLA_OK
-                                                                                                    : QKMLA_ERR_CUDA;
+    return launch_pdl(k, grid, dim3(Q8Layout<DC, DR, ROWS>::kThreads), bytes, s, lat, rope, q) == cudaSuccess
+               ? QKMLA_OK
+               : QKMLA_ERR_CUDA;
 }
 
 }  // namespace
@@ -833,8 +797,7 @@ int launch_decode_q8(const qkmla_decode_args* a, const DecodeExt& x, cudaStream_
     q.num_pages = a->num_slots / a->page_size;
     q.page_size = a->page_size;
     q.max_pages = a->max_pages;
-    q.cluster = q8_cluster(a);
-    q.piece = std::min(a->page_size, kT / q.cluster);
+    q.piece = std::min(a->page_size, kT);
     q.B = a->B; q.s_q = a->s_q; q.H = a->H; q.G = a->G;
     q.window = x.window;
     q.sinks = x.sinks;
