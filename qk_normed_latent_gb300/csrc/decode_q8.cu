@@ -68,9 +68,14 @@ struct Q8Layout {
     static constexpr int kQLat = kBlocks * kN * 128;
     static constexpr int kQRope = kN * kRopeRow;
     static constexpr int kQ = (kQLat + kQRope + 1023) / 1024 * 1024;
-    static constexpr int kSLat = kBlocks * kT * 128;
-    static constexpr int kSRope = kT * kRopeRow;              // P (kN bytes a token) takes this place
-    static constexpr int kOffAk = kSLat + kSRope;
+    // A stage holds a tile in groups of 8 tokens: kBlocks (with d_r = 64 one more, the RoPE key) blocks of
+    // 8 tokens x 128 bytes, the swizzle's atom, as one TMA box of a page piece leaves them.  P (kN
+    // bytes a token) takes the RoPE key's place.
+    static constexpr bool kRopeIn = DR == 64;
+    static constexpr int kGroup = (kBlocks + (kRopeIn ? 1 : 0)) * 1024;
+    static constexpr int kOffRope = kRopeIn ? kBlocks * 1024 : kT / 8 * kGroup;
+    static constexpr int kRopeGroup = kRopeIn ? kGroup : 8 * kRopeRow;
+    static constexpr int kOffAk = kT / 8 * kGroup + (kRopeIn ? 0 : kT * kRopeRow);
     static constexpr int kOffScale = kOffAk + kT * kMaxG * 4;
     static constexpr int kStage = (kOffScale + kT * 4 + 1023) / 1024 * 1024;
     // per-row floats: coef, m, v, f, corr, inv, and the column maxima of 4 warps (two kinds)
@@ -79,11 +84,10 @@ struct Q8Layout {
     static constexpr int kNst = std::min(4, (232448 - kQ - kMiscMax - 8192) / kStage);
     static constexpr int kOffStage = kQ;
     static constexpr int kOffMisc = kQ + kNst * kStage;
-    static constexpr int kParts = kBlocks + 1;                // a stage's parts: latent blocks; RoPE key + scalars
-    static constexpr int kNumBars = 2 * kNst * kParts + 2 * kNst + 6;
+    static constexpr int kNumBars = 5 * kNst + 6;
     static constexpr int kBytes = kOffMisc + 512 + kRowFloats * 4 + 1024;
     static constexpr uint32_t kColO = 8 * ROWS;               // two buffers of S_hi S_lo R_hi R_lo
-    static_assert(kNst >= 2 && kN <= kRopeRow, "two stages, and P fits the RoPE slot");
+    static_assert(kNst >= 2 && kN <= kRopeRow && kOffAk % 1024 == 0, "two stages, and P fits the RoPE slot");
     static_assert(kColO + kBlocks * kN <= kTmemCols, "TMEM budget");
     static_assert(kNumBars * 8 + 16 <= 512 && kBytes + 8192 <= 232448, "shared memory budget");
 };
@@ -152,14 +156,14 @@ __global__ void __launch_bounds__(96 + 16 * ROWS, 1)
 decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ CUtensorMap tm_rope,
                  const Q8Params p) {
     using LY = Q8Layout<DC, DR, ROWS>;
-    constexpr int NST = LY::kNst, N = LY::kN, KB = LY::kBlocks, KP = LY::kParts, NW = 4 * LY::kGroups;
+    constexpr int NST = LY::kNst, N = LY::kN, KB = LY::kBlocks, NW = 4 * LY::kGroups;
     extern __shared__ __align__(1024) uint8_t smraw[];
     uint8_t* sm = smraw + ((1024u - (smem_u32(smraw) & 1023u)) & 1023u);
     uint8_t* sQ = sm;
     uint64_t* bars = (uint64_t*)(sm + LY::kOffMisc);
-    uint64_t* full = bars;                   // [NST][KP] part of a tile landed -> logit MMA
-    uint64_t* empty = full + NST * KP;       // [NST][KP] output MMA done with the part -> TMA
-    uint64_t* pfull = empty + NST * KP;      // [NST] P written -> output MMA (one arrive per softmax warp)
+    uint64_t* full = bars;                   // [NST] tile landed (two halves) -> logit MMA
+    uint64_t* empty = full + NST;            // [NST][2] output MMA done with half the tokens -> TMA
+    uint64_t* pfull = empty + 2 * NST;       // [NST] P written -> output MMA (one arrive per softmax warp)
     uint64_t* odone = pfull + NST;           // [NST] output MMA done -> softmax (rescale, epilogue)
     uint64_t* sfull = odone + NST;           // [2] logit MMA done -> softmax
     uint64_t* sfree = sfull + 2;             // [2] softmax read S, R -> MMA
@@ -206,7 +210,7 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
         if (bad && blockIdx.x == 0) report(p.status, QKMLA_ERR_DEVICE_BOUNDS);
         for (int i = 0; i < LY::kNumBars; ++i) {
             const bool warps = (&bars[i] >= pfull && &bars[i] < odone) || (&bars[i] >= sfree && &bars[i] < drain);
-            mbar_init(&bars[i], warps ? (uint32_t)NW : 1u);
+            mbar_init(&bars[i], warps ? (uint32_t)NW : i < NST ? 2u : 1u);
         }
         *abort_flag = 0;
         fence_barrier_init();
@@ -217,51 +221,50 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
     pdl_wait();
     pdl_trigger();
 
-    // ---- TMA producer (warp 0): lane q looks up piece q of a tile (kT / piece pieces), lane 0 loads them ----
-    // A stage is filled and freed in parts -- 128 latents of every token, the RoPE key with the scalars
-    // last: its logit MMAs start on the first part, and the load of a part two tiles on starts when the
-    // output MMA of its 128 latents is done.
-    const int n_pieces = kT / p.piece;
+    // ---- TMA producer (warp 0): the lanes look up the slots of 32 pieces ahead, lane 0 loads them ----
+    // A stage is filled and freed in halves of 64 tokens: the output MMAs run over the tokens, so that
+    // the load of a half two tiles on starts while they still read the other.
+    const int n_pieces = kT / p.piece, half_pieces = n_pieces / 2;
     const uint32_t ak_row = p.plain ? 0u : (uint32_t)(p.G * (p.ak_f16 ? 2 : 4));
-    const uint32_t lat_bytes = (uint32_t)p.piece * 128u;
-    const uint32_t aux_bytes = (uint32_t)p.piece * (2 * DR + 4 + ak_row);
-    int slots[8];                                             // slot of each piece; -1: nobody sees it
-    uint32_t n_want = 0;
+    const uint32_t piece_bytes = (uint32_t)p.piece * (DC + 2 * DR + 4 + ak_row);
+    const int batch = 32 / n_pieces;                          // tiles whose pieces the lanes hold
+    int lane_slot = -1;                                       // of this lane's piece; -1: nobody sees it
+    int slots[8];                                             // of the current tile
     auto locate_tile = [&](int j) {
-        const int t0 = tiles.tile(jt0 + j) * kT + lane * p.piece;
-        // a piece without a token that some row sees is not read (its rows are zeroed by the softmax)
-        const bool want = lane < n_pieces && t0 < len_last && (t0 < p.sinks || t0 + p.piece > win_first);
-        int64_t page = 0;
-        if (want) {
-            const int pg = t0 / p.page_size;
-            page = p.page_table ? (int64_t)p.page_table[(int64_t)b * p.max_pages + pg] : (int64_t)b * p.max_pages + pg;
-            if (page < 0 || page >= p.num_pages) {
-                report(p.status, QKMLA_ERR_DEVICE_BOUNDS);
-                page = 0;
+        const int k = j % batch;
+        if (k == 0) {
+            const int jl = j + lane / n_pieces;
+            const int t0 = tiles.tile(jt0 + jl) * kT + (lane % n_pieces) * p.piece;
+            // a piece without a token that some row sees is not read (its rows are zeroed by the softmax)
+            lane_slot = -1;
+            if (jl < n_t && t0 < len_last && (t0 < p.sinks || t0 + p.piece > win_first)) {
+                const int pg = t0 / p.page_size;
+                int64_t page = p.page_table ? (int64_t)p.page_table[(int64_t)b * p.max_pages + pg]
+                                            : (int64_t)b * p.max_pages + pg;
+                if (page < 0 || page >= p.num_pages) {
+                    report(p.status, QKMLA_ERR_DEVICE_BOUNDS);
+                    page = 0;
+                }
+                lane_slot = (int)(page * p.page_size + t0 % p.page_size);
             }
         }
-        const int slot = want ? (int)(page * p.page_size + t0 % p.page_size) : -1;
 #pragma unroll
-        for (int q = 0; q < 8; ++q) slots[q] = __shfl_sync(0xffffffffu, slot, q);
-        n_want = (uint32_t)__popc(__ballot_sync(0xffffffffu, want));
+        for (int q = 0; q < 8; ++q) slots[q] = __shfl_sync(0xffffffffu, lane_slot, k * n_pieces + q);
     };
-    auto issue_part = [&](int j, int part) {                  // lane 0
+    auto issue_half = [&](int j, int half) {                  // lane 0
         const int s = j % NST;
         uint8_t* stg = sm + LY::kOffStage + s * LY::kStage;
-        uint64_t* bar = &full[s * KP + part];
-        mbar_arrive_expect_tx(bar, n_want * (part < KB ? lat_bytes : aux_bytes));
-        if (part < KB) {
-            uint8_t* dst = stg + part * (kT * 128);
+        uint64_t* bar = &full[s];
+        uint32_t n_want = 0;
 #pragma unroll
-            for (int q = 0; q < 8; ++q)
-                if (q < n_pieces && slots[q] >= 0) tma_load_2d(dst + q * lat_bytes, &tm_lat, part * 128, slots[q], bar);
-            return;
-        }
+        for (int q = 0; q < 8; ++q) n_want += (q / half_pieces == half && slots[q] >= 0) ? 1u : 0u;
+        mbar_arrive_expect_tx(bar, n_want * piece_bytes);
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
-            if (q >= n_pieces || slots[q] < 0) continue;
+            if (q / half_pieces != half || slots[q] < 0) continue;
             const int at = q * p.piece;
-            tma_load_2d(stg + LY::kSLat + at * LY::kRopeRow, &tm_rope, 0, slots[q], bar);
+            tma_load_4d(stg + (at >> 3) * LY::kGroup, &tm_lat, 0, 0, 0, slots[q] >> 3, bar);
+            if (!LY::kRopeIn) tma_load_2d(stg + LY::kOffRope + at * LY::kRopeRow, &tm_rope, 0, slots[q], bar);
             bulk_load(stg + LY::kOffScale + at * 4, p.kv_scale + slots[q], (uint32_t)p.piece * 4, bar);
             if (ak_row)
                 bulk_load(stg + LY::kOffAk + at * ak_row, p.ak + (int64_t)slots[q] * ak_row, (uint32_t)p.piece * ak_row, bar);
@@ -273,8 +276,10 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
         tmem_relinquish();
         for (int j = 0; j < NST && j < n_t; ++j) {
             locate_tile(j);
-            if (lane == 0)
-                for (int part = 0; part < KP; ++part) issue_part(j, part);
+            if (lane == 0) {
+                issue_half(j, 0);
+                issue_half(j, 1);
+            }
             __syncwarp();
         }
     } else if (warp >= 3) {
@@ -352,21 +357,20 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
             locate_tile(j);
             int ok = 1;
             if (lane == 0) {
-                for (int part = 0; part < KP && ok; ++part) {
-                    ok = wait_bounded(&empty[(j % NST) * KP + part], ((j / NST) - 1) & 1, p.status) ? 1 : 0;
-                    if (ok) issue_part(j, part);
+                for (int half = 0; half < 2 && ok; ++half) {
+                    ok = wait_bounded(&empty[(j % NST) * 2 + half], ((j / NST) - 1) & 1, p.status) ? 1 : 0;
+                    if (ok) issue_half(j, half);
                 }
                 if (*(volatile int*)abort_flag) ok = 0;
             }
             go = __shfl_sync(0xffffffffu, ok, 0) != 0;
         }
         // no exit with a copy in flight: on the ordinary path the MMA warp has waited for all of them;
-        // an abandoned one is waited for here (parts never issued run into the bound)
+        // an abandoned one is waited for here (a half never issued runs into the bound)
         if (!go && lane == 0) {
             *(volatile int*)abort_flag = 1;
             for (int q = max(0, j - 1 - NST); q < j; ++q)
-                for (int part = 0; part < KP; ++part)
-                    wait_bounded(&full[(q % NST) * KP + part], (q / NST) & 1, p.status, 10000000ull);
+                wait_bounded(&full[q % NST], (q / NST) & 1, p.status, 10000000ull);
         }
     } else if (warp == 1) {
         // ===================== logit MMAs =====================
@@ -381,23 +385,19 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
                 const uint32_t st = smem_u32(sm + LY::kOffStage + s * LY::kStage);
                 const uint32_t d = tmem + (uint32_t)(j & 1) * (2 * N);
                 if (j >= 2) ok = wait_bounded(&sfree[j & 1], ((j >> 1) - 1) & 1, p.status);
-#pragma unroll
-                for (int blk = 0; blk < KB; ++blk) {
-                    ok = ok && wait_bounded(&full[s * KP + blk], (j / NST) & 1, p.status);
-                    if (!ok) break;
-                    tc_fence_after();
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        mma_f8(d, smem_desc(st + blk * (kT * 128) + kk * 32, 16, 1024, kSwizzle128B),
-                               smem_desc(q_addr + blk * (N * 128) + kk * 32, 16, 1024, kSwizzle128B), id_s,
-                               (blk > 0 || kk > 0) ? 1u : 0u);
-                }
-                ok = ok && wait_bounded(&full[s * KP + KB], (j / NST) & 1, p.status) && !*(volatile int*)abort_flag;
+                ok = ok && wait_bounded(&full[s], (j / NST) & 1, p.status) && !*(volatile int*)abort_flag;
                 if (!ok) break;
                 tc_fence_after();
 #pragma unroll
+                for (int blk = 0; blk < KB; ++blk)
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_f8(d, smem_desc(st + blk * 1024 + kk * 32, 16, LY::kGroup, kSwizzle128B),
+                               smem_desc(q_addr + blk * (N * 128) + kk * 32, 16, 1024, kSwizzle128B), id_s,
+                               (blk > 0 || kk > 0) ? 1u : 0u);
+#pragma unroll
                 for (int kk = 0; kk < DR / 16; ++kk)
-                    mma_bf16(d + N, smem_desc(st + LY::kSLat + kk * 32, 16, sbo, sw),
+                    mma_bf16(d + N, smem_desc(st + LY::kOffRope + kk * 32, 16, LY::kRopeGroup, sw),
                              smem_desc(q_addr + LY::kQLat + kk * 32, 16, sbo, sw), id_r, kk > 0 ? 1u : 0u);
                 mma_commit(&sfull[j & 1]);
             }
@@ -418,18 +418,18 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
                 ok = wait_bounded(&pfull[s], (j / NST) & 1, p.status) && !*(volatile int*)abort_flag;
                 if (!ok) break;
                 tc_fence_after();
-                // A: a chunk's 128 latents x 32 tokens, MN-major (8-token groups 1024 B apart).
-                // B: P, MN-major: a token's N codes in N bytes (swizzle of the same width), 8-token groups 8 N bytes apart.
+                // A: a chunk's 128 latents x 32 tokens, MN-major (8-token groups kGroup apart).  B: P, MN-major:
+                // a token's N codes in N bytes (swizzle of the same width), 8-token groups kRopeGroup apart.
                 constexpr uint32_t swp = N == 64 ? kSwizzle64B : kSwizzle32B;
 #pragma unroll
-                for (int c = 0; c < KB; ++c) {
+                for (int kk = 0; kk < 4; ++kk) {
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        mma_f8(tmem + LY::kColO + c * N, smem_desc(st + c * (kT * 128) + kk * 4096, kT * 128, 1024, kSwizzle128B),
-                               smem_desc(st + LY::kSLat + kk * 32 * N, 8 * N, 8 * N, swp), id_o, (j > 0 || kk > 0) ? 1u : 0u);
-                    mma_commit(&empty[s * KP + c]);
+                    for (int c = 0; c < KB; ++c)
+                        mma_f8(tmem + LY::kColO + c * N, smem_desc(st + c * 1024 + kk * 4 * LY::kGroup, 1024, LY::kGroup, kSwizzle128B),
+                               smem_desc(st + LY::kOffRope + kk * 4 * LY::kRopeGroup, LY::kRopeGroup, LY::kRopeGroup, swp), id_o,
+                               (j > 0 || kk > 0) ? 1u : 0u);
+                    if (kk & 1) mma_commit(&empty[s * 2 + (kk >> 1)]);
                 }
-                mma_commit(&empty[s * KP + KB]);
                 mma_commit(&odone[s]);
             }
             if (!ok) {
@@ -644,7 +644,7 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
             }
             // P row of this token: HPT codes of hi at u0, of lo at ROWS + u0, 16-byte chunks XOR-swizzled
             // (64-byte rows by token / 2, 32-byte rows by token / 4)
-            uint8_t* pr = stg + LY::kSLat + tl * N + (u0 & 15);
+            uint8_t* pr = stg + LY::kOffRope + (tl >> 3) * LY::kRopeGroup + (tl & 7) * N + (u0 & 15);
             const uint32_t xr = N == 64 ? (tl >> 1) & 3 : (tl >> 2) & 1;
             *reinterpret_cast<uint2*>(pr + (((uint32_t)(u0 >> 4) ^ xr) << 4)) = make_uint2(hi[0], hi[1]);
             *reinterpret_cast<uint2*>(pr + (((uint32_t)((ROWS + u0) >> 4) ^ xr) << 4)) = make_uint2(lo[0], lo[1]);
@@ -655,8 +655,8 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
                 for (int blk = 0; blk < KB; ++blk)
 #pragma unroll
                     for (int c = 0; c < kShare; ++c)
-                        *reinterpret_cast<uint4*>(stg + blk * (kT * 128) + tl * 128 + (((kShare * grp + c) ^ (tl & 7)) << 4)) =
-                            make_uint4(0u, 0u, 0u, 0u);
+                        *reinterpret_cast<uint4*>(stg + (tl >> 3) * LY::kGroup + blk * 1024 + (tl & 7) * 128 +
+                                                  (((kShare * grp + c) ^ (tl & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
             }
             fence_proxy_async_smem();
             tc_fence_before();
@@ -717,16 +717,30 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
     }
 }
 
-bool make_q8_map(CUtensorMap* m, CUtensorMapDataType type, const void* base, int64_t rows, int cols, int64_t pitch,
-                 int box_cols, int box_rows, CUtensorMapSwizzle sw) {
+// Cache rows as a 4-D tensor: 128-byte blocks of a row, 8 rows, the blocks, the groups of 8 rows -- a box
+// of it lands in shared memory as the atoms the tensor core reads.
+bool make_row_map(CUtensorMap* m, const void* base, int64_t rows, int64_t pitch, int blocks, int box_rows) {
     auto fn = encode_fn();
     if (!fn) return false;
-    cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    cuuint64_t dims[4] = {128, 8, (cuuint64_t)blocks, (cuuint64_t)(rows / 8)};
+    cuuint64_t strides[3] = {(cuuint64_t)pitch, 128, (cuuint64_t)(8 * pitch)};
+    cuuint32_t box[4] = {128, 8, (cuuint32_t)blocks, (cuuint32_t)(box_rows / 8)};
+    cuuint32_t es[4] = {1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// The RoPE key of rows whose key is not a block of its own (d_r = 32: 64 bytes a row).
+bool make_rope_map(CUtensorMap* m, const void* base, int64_t rows, int64_t pitch, int d_r, int box_rows) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)d_r, (cuuint64_t)rows};
     cuuint64_t strides[1] = {(cuuint64_t)pitch};
-    cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
+    cuuint32_t box[2] = {(cuuint32_t)d_r, (cuuint32_t)box_rows};
     cuuint32_t es[2] = {1, 1};
-    return fn(m, type, 2, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Query rows per CTA: 16 when that is all there are, else 32.
@@ -797,7 +811,7 @@ int launch_decode_q8(const qkmla_decode_args* a, const DecodeExt& x, cudaStream_
     q.num_pages = a->num_slots / a->page_size;
     q.page_size = a->page_size;
     q.max_pages = a->max_pages;
-    q.piece = std::min(a->page_size, kT);
+    q.piece = std::min(a->page_size, kT / 2);
     q.B = a->B; q.s_q = a->s_q; q.H = a->H; q.G = a->G;
     q.window = x.window;
     q.sinks = x.sinks;
@@ -818,10 +832,9 @@ int launch_decode_q8(const qkmla_decode_args* a, const DecodeExt& x, cudaStream_
 
     const int64_t pitch = a->d_c + 2 * a->d_r;
     CUtensorMap lat, rope;
-    if (!make_q8_map(&lat, CU_TENSOR_MAP_DATA_TYPE_UINT8, a->kv_cache, a->num_slots, (int)pitch, pitch, 128, q.piece,
-                     CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !make_q8_map(&rope, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (const uint8_t*)a->kv_cache + a->d_c, a->num_slots, a->d_r,
-                     pitch, a->d_r, q.piece, a->d_r == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
+    if (!make_row_map(&lat, a->kv_cache, a->num_slots, pitch, a->d_c / 128 + (a->d_r == 64 ? 1 : 0), q.piece)) return QKMLA_ERR_CUDA;
+    if (a->d_r == 64) rope = lat;
+    else if (!make_rope_map(&rope, (const uint8_t*)a->kv_cache + a->d_c, a->num_slots, pitch, a->d_r, q.piece))
         return QKMLA_ERR_CUDA;
     const dim3 grid(n_rb, w.max_items);
     const bool r16 = q8_rows(a) == 16;
