@@ -52,7 +52,7 @@ namespace {
 using namespace tc;
 using namespace dec;
 
-constexpr int kT = 128;              // tokens per tile
+constexpr int kT = 64;               // tokens per tile
 constexpr int HPT = 8;                // query rows of a softmax thread
 constexpr uint32_t kTmemCols = 512;
 constexpr float kPUnit = 32.f;       // P of the largest contribution: lazy maxima let it grow to 2^8 < 448
@@ -61,35 +61,45 @@ constexpr float kLazy = 256.f;       // a weight (or a scaled one) above this mo
 template <int DC, int DR, int ROWS>
 struct Q8Layout {
     static constexpr int kN = 2 * ROWS;                       // hi and lo rows
-    static constexpr int kGroups = ROWS / HPT;                // softmax groups of 4 warps
+    static constexpr int kGroups = ROWS / 16;                 // softmax groups of 4 warps
     static constexpr int kThreads = 96 + 128 * kGroups;
-    static constexpr int kBlocks = DC / 128;                  // 128-column boxes = output chunks
+    static constexpr int kBlocks = DC / 128;                  // 128-column blocks = output chunks
     static constexpr int kRopeRow = DR * 2;                   // bytes: 128 (SW128) or 64 (SW64)
     static constexpr int kQLat = kBlocks * kN * 128;
     static constexpr int kQRope = kN * kRopeRow;
     static constexpr int kQ = (kQLat + kQRope + 1023) / 1024 * 1024;
+    // TMEM: one or two buffers of S_hi S_lo R_hi R_lo, then O^T with P_hi and P_lo as columns of one operand
+    // (two accumulators, added in the epilogue) or, where that does not fit, in two passes over one
+    static constexpr bool kStacked = 4 * ROWS + kBlocks * kN <= 512;
+    static constexpr int kON = kStacked ? kN : ROWS;          // columns of a chunk's accumulator
+    static constexpr int kNsb = 8 * ROWS + kBlocks * kON <= 512 ? 2 : 1;
+    static constexpr uint32_t kColO = kNsb * 4 * ROWS;
     // A stage holds a tile in groups of 8 tokens: kBlocks (with d_r = 64 one more, the RoPE key) blocks of
     // 8 tokens x 128 bytes, the swizzle's atom, as one TMA box of a page piece leaves them.  P (kN
-    // bytes a token) takes the RoPE key's place.
+    // bytes a token) takes the RoPE key's place where it fits.
     static constexpr bool kRopeIn = DR == 64;
+    static constexpr bool kPOwn = kN > kRopeRow;
     static constexpr int kGroup = (kBlocks + (kRopeIn ? 1 : 0)) * 1024;
     static constexpr int kOffRope = kRopeIn ? kBlocks * 1024 : kT / 8 * kGroup;
     static constexpr int kRopeGroup = kRopeIn ? kGroup : 8 * kRopeRow;
-    static constexpr int kOffAk = kT / 8 * kGroup + (kRopeIn ? 0 : kT * kRopeRow);
+    static constexpr int kOffOwn = kT / 8 * kGroup + (kRopeIn ? 0 : kT * kRopeRow);
+    static constexpr int kOffP = kPOwn ? kOffOwn : kOffRope;
+    static constexpr int kPGroup = kPOwn ? 8 * kN : kRopeGroup;
+    static constexpr int kOffAk = kOffOwn + (kPOwn ? kT * kN : 0);
     static constexpr int kOffScale = kOffAk + kT * kMaxG * 4;
     static constexpr int kStage = (kOffScale + kT * 4 + 1023) / 1024 * 1024;
     // per-row floats: coef, m, v, f, corr, inv, and the column maxima of 4 warps (two kinds)
     static constexpr int kRowFloats = 6 * ROWS + 8 * ROWS;
-    static constexpr int kMiscMax = 512 + kRowFloats * 4 + 1024;
-    static constexpr int kNst = std::min(4, (232448 - kQ - kMiscMax - 8192) / kStage);
+    static constexpr int kMisc = 512 + kRowFloats * 4 + 1024;
+    static constexpr int kStatic = (int)sizeof(SchedSmem) + 256;
+    static constexpr int kNst = std::min(6, (232448 - kQ - kMisc - kStatic) / kStage);
     static constexpr int kOffStage = kQ;
     static constexpr int kOffMisc = kQ + kNst * kStage;
-    static constexpr int kNumBars = 5 * kNst + 6;
-    static constexpr int kBytes = kOffMisc + 512 + kRowFloats * 4 + 1024;
-    static constexpr uint32_t kColO = 8 * ROWS;               // two buffers of S_hi S_lo R_hi R_lo
-    static_assert(kNst >= 2 && kN <= kRopeRow && kOffAk % 1024 == 0, "two stages, and P fits the RoPE slot");
-    static_assert(kColO + kBlocks * kN <= kTmemCols, "TMEM budget");
-    static_assert(kNumBars * 8 + 16 <= 512 && kBytes + 8192 <= 232448, "shared memory budget");
+    static constexpr int kNumBars = 4 * kNst + 2 * kNsb + 2;
+    static constexpr int kBytes = kOffMisc + kMisc;
+    static_assert(kNst >= 3 && kOffAk % 1024 == 0 && kOffOwn % 1024 == 0, "three stages, aligned atoms");
+    static_assert(kColO + kBlocks * kON <= kTmemCols, "TMEM budget");
+    static_assert(kNumBars * 8 + 16 <= 512 && kBytes + kStatic <= 232448, "shared memory budget");
 };
 
 struct Q8Params {
@@ -144,30 +154,35 @@ __device__ __forceinline__ bool group_any(int grp, bool pred) {
 }
 __device__ __forceinline__ void group_sync(int grp) { asm volatile("bar.sync %0, 128;" ::"r"(grp + 1) : "memory"); }
 
-// Maximum over the warp of a float that is not NaN (order-preserving integers).
-__device__ __forceinline__ float redux_max(float v) {
-    const int b = __float_as_int(v);
-    const int m = __reduce_max_sync(0xffffffffu, b >= 0 ? b : b ^ 0x7fffffff);
-    return __int_as_float(m >= 0 ? m : m ^ 0x7fffffff);
+// Over the 16 lanes that hold the same rows.
+__device__ __forceinline__ float half_warp_max(float v) {
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+__device__ __forceinline__ float half_warp_sum(float v) {
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
 }
 
 template <int DC, int DR, int ROWS>
-__global__ void __launch_bounds__(96 + 16 * ROWS, 1)
+__global__ void __launch_bounds__(96 + 8 * ROWS, 1)
 decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ CUtensorMap tm_rope,
                  const Q8Params p) {
     using LY = Q8Layout<DC, DR, ROWS>;
-    constexpr int NST = LY::kNst, N = LY::kN, KB = LY::kBlocks, NW = 4 * LY::kGroups;
+    constexpr int NST = LY::kNst, N = LY::kN, KB = LY::kBlocks, NW = 4 * LY::kGroups, NSB = LY::kNsb;
     extern __shared__ __align__(1024) uint8_t smraw[];
     uint8_t* sm = smraw + ((1024u - (smem_u32(smraw) & 1023u)) & 1023u);
     uint8_t* sQ = sm;
     uint64_t* bars = (uint64_t*)(sm + LY::kOffMisc);
-    uint64_t* full = bars;                   // [NST] tile landed (two halves) -> logit MMA
-    uint64_t* empty = full + NST;            // [NST][2] output MMA done with half the tokens -> TMA
-    uint64_t* pfull = empty + 2 * NST;       // [NST] P written -> output MMA (one arrive per softmax warp)
+    uint64_t* full = bars;                   // [NST] tile landed -> logit MMA
+    uint64_t* empty = full + NST;            // [NST] output MMA done -> TMA
+    uint64_t* pfull = empty + NST;           // [NST] P written -> output MMA (one arrive per softmax warp)
     uint64_t* odone = pfull + NST;           // [NST] output MMA done -> softmax (rescale, epilogue)
-    uint64_t* sfull = odone + NST;           // [2] logit MMA done -> softmax
-    uint64_t* sfree = sfull + 2;             // [2] softmax read S, R -> MMA
-    uint64_t* drain = sfree + 2;             // [2] abort path: an issuer's MMAs in flight are done
+    uint64_t* sfull = odone + NST;           // [NSB] logit MMA done -> softmax
+    uint64_t* sfree = sfull + NSB;           // [NSB] softmax read S, R -> MMA
+    uint64_t* drain = sfree + NSB;           // [2] abort path: an issuer's MMAs in flight are done
     uint32_t* tmem_slot = (uint32_t*)(bars + LY::kNumBars);
     int* abort_flag = (int*)(tmem_slot + 1);
     float* coef_s = (float*)(sm + LY::kOffMisc + 512);   // scale log2e alpha^q x the row's code scale
@@ -210,7 +225,7 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
         if (bad && blockIdx.x == 0) report(p.status, QKMLA_ERR_DEVICE_BOUNDS);
         for (int i = 0; i < LY::kNumBars; ++i) {
             const bool warps = (&bars[i] >= pfull && &bars[i] < odone) || (&bars[i] >= sfree && &bars[i] < drain);
-            mbar_init(&bars[i], warps ? (uint32_t)NW : i < NST ? 2u : 1u);
+            mbar_init(&bars[i], warps ? (uint32_t)NW : 1u);
         }
         *abort_flag = 0;
         fence_barrier_init();
@@ -222,14 +237,12 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
     pdl_trigger();
 
     // ---- TMA producer (warp 0): the lanes look up the slots of 32 pieces ahead, lane 0 loads them ----
-    // A stage is filled and freed in halves of 64 tokens: the output MMAs run over the tokens, so that
-    // the load of a half two tiles on starts while they still read the other.
-    const int n_pieces = kT / p.piece, half_pieces = n_pieces / 2;
+    const int n_pieces = kT / p.piece;
     const uint32_t ak_row = p.plain ? 0u : (uint32_t)(p.G * (p.ak_f16 ? 2 : 4));
     const uint32_t piece_bytes = (uint32_t)p.piece * (DC + 2 * DR + 4 + ak_row);
     const int batch = 32 / n_pieces;                          // tiles whose pieces the lanes hold
     int lane_slot = -1;                                       // of this lane's piece; -1: nobody sees it
-    int slots[8];                                             // of the current tile
+    int slots[4];                                             // of the current tile
     auto locate_tile = [&](int j) {
         const int k = j % batch;
         if (k == 0) {
@@ -249,19 +262,19 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
             }
         }
 #pragma unroll
-        for (int q = 0; q < 8; ++q) slots[q] = __shfl_sync(0xffffffffu, lane_slot, k * n_pieces + q);
+        for (int q = 0; q < 4; ++q) slots[q] = __shfl_sync(0xffffffffu, lane_slot, k * n_pieces + q);
     };
-    auto issue_half = [&](int j, int half) {                  // lane 0
+    auto issue_tile = [&](int j) {                            // lane 0
         const int s = j % NST;
         uint8_t* stg = sm + LY::kOffStage + s * LY::kStage;
         uint64_t* bar = &full[s];
         uint32_t n_want = 0;
 #pragma unroll
-        for (int q = 0; q < 8; ++q) n_want += (q / half_pieces == half && slots[q] >= 0) ? 1u : 0u;
+        for (int q = 0; q < 4; ++q) n_want += (q < n_pieces && slots[q] >= 0) ? 1u : 0u;
         mbar_arrive_expect_tx(bar, n_want * piece_bytes);
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-            if (q / half_pieces != half || slots[q] < 0) continue;
+        for (int q = 0; q < 4; ++q) {
+            if (q >= n_pieces || slots[q] < 0) continue;
             const int at = q * p.piece;
             tma_load_4d(stg + (at >> 3) * LY::kGroup, &tm_lat, 0, 0, 0, slots[q] >> 3, bar);
             if (!LY::kRopeIn) tma_load_2d(stg + LY::kOffRope + at * LY::kRopeRow, &tm_rope, 0, slots[q], bar);
@@ -276,10 +289,7 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
         tmem_relinquish();
         for (int j = 0; j < NST && j < n_t; ++j) {
             locate_tile(j);
-            if (lane == 0) {
-                issue_half(j, 0);
-                issue_half(j, 1);
-            }
+            if (lane == 0) issue_tile(j);
             __syncwarp();
         }
     } else if (warp >= 3) {
@@ -357,16 +367,14 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
             locate_tile(j);
             int ok = 1;
             if (lane == 0) {
-                for (int half = 0; half < 2 && ok; ++half) {
-                    ok = wait_bounded(&empty[(j % NST) * 2 + half], ((j / NST) - 1) & 1, p.status) ? 1 : 0;
-                    if (ok) issue_half(j, half);
-                }
+                ok = wait_bounded(&empty[j % NST], ((j / NST) - 1) & 1, p.status) ? 1 : 0;
                 if (*(volatile int*)abort_flag) ok = 0;
+                if (ok) issue_tile(j);
             }
             go = __shfl_sync(0xffffffffu, ok, 0) != 0;
         }
         // no exit with a copy in flight: on the ordinary path the MMA warp has waited for all of them;
-        // an abandoned one is waited for here (a half never issued runs into the bound)
+        // an abandoned one is waited for here (one never issued runs into the bound)
         if (!go && lane == 0) {
             *(volatile int*)abort_flag = 1;
             for (int q = max(0, j - 1 - NST); q < j; ++q)
@@ -383,8 +391,8 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
             for (int j = 0; j < n_t && ok; ++j) {
                 const int s = j % NST;
                 const uint32_t st = smem_u32(sm + LY::kOffStage + s * LY::kStage);
-                const uint32_t d = tmem + (uint32_t)(j & 1) * (2 * N);
-                if (j >= 2) ok = wait_bounded(&sfree[j & 1], ((j >> 1) - 1) & 1, p.status);
+                const uint32_t d = tmem + (uint32_t)(j % NSB) * (2 * N);
+                if (j >= NSB) ok = wait_bounded(&sfree[j % NSB], ((j / NSB) - 1) & 1, p.status);
                 ok = ok && wait_bounded(&full[s], (j / NST) & 1, p.status) && !*(volatile int*)abort_flag;
                 if (!ok) break;
                 tc_fence_after();
@@ -399,7 +407,7 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
                 for (int kk = 0; kk < DR / 16; ++kk)
                     mma_bf16(d + N, smem_desc(st + LY::kOffRope + kk * 32, 16, LY::kRopeGroup, sw),
                              smem_desc(q_addr + LY::kQLat + kk * 32, 16, sbo, sw), id_r, kk > 0 ? 1u : 0u);
-                mma_commit(&sfull[j & 1]);
+                mma_commit(&sfull[j % NSB]);
             }
             if (!ok) {                       // no exit with an MMA in flight
                 *(volatile int*)abort_flag = 1;
@@ -410,7 +418,7 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
     } else if (warp == 2) {
         // ===================== output MMAs (a thread of their own: neither issue waits for the other's data) ==========
         if (lane == 0) {
-            const uint32_t id_o = idesc_e4m3(128, N, 1, 1);
+            const uint32_t id_o = idesc_e4m3(128, LY::kON, 1, 1);
             bool ok = true;
             for (int j = 0; j < n_t && ok; ++j) {
                 const int s = j % NST;
@@ -419,17 +427,20 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
                 if (!ok) break;
                 tc_fence_after();
                 // A: a chunk's 128 latents x 32 tokens, MN-major (8-token groups kGroup apart).  B: P, MN-major:
-                // a token's N codes in N bytes (swizzle of the same width), 8-token groups kRopeGroup apart.
-                constexpr uint32_t swp = N == 64 ? kSwizzle64B : kSwizzle32B;
+                // a token's codes in as many bytes (swizzle of the same width), 8-token groups kPGroup apart.
+                constexpr int PN = LY::kON;
+                constexpr uint32_t swp = PN == 128 ? kSwizzle128B : PN == 64 ? kSwizzle64B : kSwizzle32B;
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk) {
+                for (int c = 0; c < KB; ++c)
 #pragma unroll
-                    for (int c = 0; c < KB; ++c)
-                        mma_f8(tmem + LY::kColO + c * N, smem_desc(st + c * 1024 + kk * 4 * LY::kGroup, 1024, LY::kGroup, kSwizzle128B),
-                               smem_desc(st + LY::kOffRope + kk * 4 * LY::kRopeGroup, LY::kRopeGroup, LY::kRopeGroup, swp), id_o,
-                               (j > 0 || kk > 0) ? 1u : 0u);
-                    if (kk & 1) mma_commit(&empty[s * 2 + (kk >> 1)]);
-                }
+                    for (int kk = 0; kk < kT / 32; ++kk)
+#pragma unroll
+                        for (int part = 0; part < (LY::kStacked ? 1 : 2); ++part)
+                            mma_f8(tmem + LY::kColO + c * PN,
+                                   smem_desc(st + c * 1024 + kk * 4 * LY::kGroup, 1024, LY::kGroup, kSwizzle128B),
+                                   smem_desc(st + LY::kOffP + kk * 4 * LY::kPGroup + part * 8 * PN, LY::kPGroup, LY::kPGroup, swp),
+                                   id_o, (j > 0 || kk > 0 || part > 0) ? 1u : 0u);
+                mma_commit(&empty[s]);
                 mma_commit(&odone[s]);
             }
             if (!ok) {
@@ -439,11 +450,14 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
             }
         }
     } else {
-        // ===================== softmax: thread = token, HPT rows of its group =====================
+        // ===================== softmax: thread = (token, 8 rows); a group of 4 warps takes 16 rows =====================
         const int sub = warp & 3, grp = (warp - 3) >> 2;
         const uint32_t lane_base = (uint32_t)(32 * sub) << 16;
-        const int tl = 32 * sub + lane;                      // token in the tile
-        const int u0 = grp * HPT;                            // first row of the group
+        // M = 64 accumulator: token t sits in TMEM lane t % 16 of sub-partition t / 16; the two-half load
+        // gives lanes 0-15 the first 8 rows of the group, lanes 16-31 the next 8 of the same tokens
+        const int tl = 16 * sub + (lane & 15);               // token in the tile
+        const int ug = grp * 16;                             // first row of the group
+        const int u0 = ug + (lane >> 4) * HPT;               // first row of this thread
         const int hshift = 31 - __clz(p.H / p.G);            // heads a group: 2, 4, 8 or 16 (H >= 16, G <= 8)
         const int h0 = (row0 + u0) % p.H;                    // its head: HPT divides H, so the rows share a query token
         const int ak_at = tl * p.G + (h0 >> hshift);         // alpha^k of this token for the first of the rows
@@ -464,23 +478,23 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
         reload();
         bool ok = true;
         for (int j = 0; j < n_t; ++j) {
-            const int s = j % NST, sb = j & 1;
+            const int s = j % NST, sb = j % NSB;
             uint8_t* stg = sm + LY::kOffStage + s * LY::kStage;
             const int t = tiles.tile(jt0 + j) * kT + tl;
             const bool sees = t < n_row && (t < p.sinks || t >= w_row);
             const bool any_sees = t < len_last && (t < p.sinks || t >= win_first);   // some row of the CTA
             const bool masked = !__all_sync(0xffffffffu, sees);
-            const bool got_s = wait_bounded(&sfull[sb], (j >> 1) & 1, p.status);
+            const bool got_s = wait_bounded(&sfull[sb], (j / NSB) & 1, p.status);
             tc_fence_after();
             uint64_t x2[HP2];
             const float st_raw = *reinterpret_cast<const float*>(stg + LY::kOffScale + tl * 4);
             {
                 uint32_t a[HPT], c[HPT], d[HPT], e[HPT];
-                const uint32_t base = tmem + (uint32_t)sb * (2 * N) + lane_base + u0;
-                tmem_ld8(base, a);
-                tmem_ld8(base + ROWS, c);
-                tmem_ld8(base + N, d);
-                tmem_ld8(base + N + ROWS, e);
+                const uint32_t base = tmem + (uint32_t)sb * (2 * N) + lane_base + ug;
+                tmem_ld8x2(base, a);
+                tmem_ld8x2(base + ROWS, c);
+                tmem_ld8x2(base + N, d);
+                tmem_ld8x2(base + N + ROWS, e);
                 // coefficient x alpha^k s_t of the rows while the loads run.  A group is 2^SH heads, known to
                 // the compiler: with a bound known only at run time the loads became a chain of
                 // branches, 2650 cycles a tile against 90 for the TMEM loads beside it
@@ -571,16 +585,16 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
                     const float2 xp = f2_unpack(x2[u / 2]);
                     const float xu = (u & 1) ? xp.y : xp.x;
                     const float xv = xu == xu ? xu : -INFINITY;
-                    const float mx = redux_max(xv), vx = redux_max(xv + ls);
-                    if (lane == 0) {
+                    const float mx = half_warp_max(xv), vx = half_warp_max(xv + ls);
+                    if ((lane & 15) == 0) {
                         red_s[sub * ROWS + u0 + u] = mx;
                         red_s[(4 + sub) * ROWS + u0 + u] = vx;
                     }
                 }
                 group_sync(grp);
                 const int gt = tid - 96 - grp * 128;
-                if (gt < HPT) {
-                    const int r = u0 + gt;
+                if (gt < 16) {
+                    const int r = ug + gt;
                     float mx = red_s[r], vx = red_s[4 * ROWS + r];
 #pragma unroll
                     for (int q = 1; q < 4; ++q) {
@@ -602,24 +616,22 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
                     const bool got_o = wait_bounded(&odone[(j - 1) % NST], ((j - 1) / NST) & 1, p.status);
                     if (group_any(grp, !got_o)) { ok = false; break; }
                     tc_fence_after();
-                    float cr[HPT];
                     bool moved = false;
 #pragma unroll
-                    for (int u = 0; u < HPT; ++u) {
-                        cr[u] = corr_s[u0 + u];
-                        moved = moved || cr[u] != 1.f;
-                    }
+                    for (int u = 0; u < 16; ++u) moved = moved || corr_s[ug + u] != 1.f;
                     if (moved) {
 #pragma unroll 1
-                        for (int c = 0; c < 2 * LY::kBlocks; ++c) {       // chunks x (hi, lo)
-                            uint32_t v[HPT];
-                            const uint32_t ta = tmem + LY::kColO + c * ROWS + u0 + lane_base;
-                            tmem_ld8(ta, v);
+                        for (int c = 0; c < KB * (LY::kStacked ? 2 : 1); ++c) {     // chunks (x hi, lo)
+                            uint32_t v[16];
+                            const uint32_t ta = tmem + LY::kColO + c * ROWS + ug + lane_base;
+                            tmem_ld16(ta, v);
                             tmem_wait_ld();
 #pragma unroll
-                            for (int u = 0; u < HPT; ++u)
-                                v[u] = cr[u] == 0.f ? 0u : __float_as_uint(__uint_as_float(v[u]) * cr[u]);
-                            tmem_st8(ta, v);
+                            for (int u = 0; u < 16; ++u) {
+                                const float cr = corr_s[ug + u];
+                                v[u] = cr == 0.f ? 0u : __float_as_uint(__uint_as_float(v[u]) * cr);
+                            }
+                            tmem_st16(ta, v);
                         }
                         tmem_wait_st();
                     }
@@ -642,21 +654,20 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
                 lsum2[u] = f2_add(lsum2[u], e2[u]);
                 lsum2[u + 1] = f2_add(lsum2[u + 1], e2[u + 1]);
             }
-            // P row of this token: HPT codes of hi at u0, of lo at ROWS + u0, 16-byte chunks XOR-swizzled
-            // (64-byte rows by token / 2, 32-byte rows by token / 4)
-            uint8_t* pr = stg + LY::kOffRope + (tl >> 3) * LY::kRopeGroup + (tl & 7) * N + (u0 & 15);
-            const uint32_t xr = N == 64 ? (tl >> 1) & 3 : (tl >> 2) & 1;
-            *reinterpret_cast<uint2*>(pr + (((uint32_t)(u0 >> 4) ^ xr) << 4)) = make_uint2(hi[0], hi[1]);
-            *reinterpret_cast<uint2*>(pr + (((uint32_t)((ROWS + u0) >> 4) ^ xr) << 4)) = make_uint2(lo[0], lo[1]);
+            // P row of this token: 8 codes of hi at u0 and of lo at ROWS + u0 (one operand) or at u0 of the next
+            // operand, 16-byte chunks XOR-swizzled (rows of 128, 64, 32 bytes: by token, token / 2, token / 4)
+            constexpr int PN = LY::kON;
+            uint8_t* pr = stg + LY::kOffP + (tl >> 3) * LY::kPGroup + (tl & 7) * PN + (u0 & 15);
+            const uint32_t xr = PN == 128 ? tl & 7 : PN == 64 ? (tl >> 1) & 3 : (tl >> 2) & 1;
+            const uint32_t chi = (uint32_t)u0 >> 4, clo = LY::kStacked ? (uint32_t)(ROWS + u0) >> 4 : chi;
+            *reinterpret_cast<uint2*>(pr + ((chi ^ xr) << 4)) = make_uint2(hi[0], hi[1]);
+            *reinterpret_cast<uint2*>(pr + (LY::kStacked ? 0 : 8 * PN) + ((clo ^ xr) << 4)) = make_uint2(lo[0], lo[1]);
             // a token no row sees: its latents (stale or never loaded) must not reach the output MMA as NaN
             if (!any_sees) {
-                constexpr int kShare = 8 / LY::kGroups;      // 16-byte chunks of a block's row
-#pragma unroll
-                for (int blk = 0; blk < KB; ++blk)
-#pragma unroll
-                    for (int c = 0; c < kShare; ++c)
-                        *reinterpret_cast<uint4*>(stg + (tl >> 3) * LY::kGroup + blk * 1024 + (tl & 7) * 128 +
-                                                  (((kShare * grp + c) ^ (tl & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+                constexpr int kShare = 2 * LY::kGroups;      // threads of a token
+                for (int c = 2 * grp + (lane >> 4); c < 8 * KB; c += kShare)
+                    *reinterpret_cast<uint4*>(stg + (tl >> 3) * LY::kGroup + (c >> 3) * 1024 + (tl & 7) * 128 +
+                                              (((c & 7) ^ (tl & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
             }
             fence_proxy_async_smem();
             tc_fence_before();
@@ -668,15 +679,15 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
 #pragma unroll
         for (int u = 0; u < HPT; ++u) {
             const float2 ls = f2_unpack(lsum2[u / 2]);
-            const float v = warp_sum((u & 1) ? ls.y : ls.x);
-            if (lane == 0) red_s[sub * ROWS + u0 + u] = v;
+            const float v = half_warp_sum((u & 1) ? ls.y : ls.x);
+            if ((lane & 15) == 0) red_s[sub * ROWS + u0 + u] = v;
         }
         const bool got_last = (ok && n_t > 0) ? wait_bounded(&odone[(n_t - 1) % NST], ((n_t - 1) / NST) & 1, p.status) : ok;
         if (group_any(grp, !got_last)) *(volatile int*)abort_flag = 1;
         tc_fence_after();
         const int gt = tid - 96 - grp * 128;
-        if (gt < HPT) {
-            const int r = u0 + gt;
+        if (gt < 16) {
+            const int r = ug + gt;
             const float l = (red_s[r] + red_s[ROWS + r]) + (red_s[2 * ROWS + r] + red_s[3 * ROWS + r]);
             const float lse = l > 0.f ? (m_s[r] + log2f(l)) * kLn2 : (l == 0.f ? -INFINITY : l);
             inv_s[r] = (l == 0.f || (f_s[r] == 0.f && l == l)) ? 0.f : 1.f / (f_s[r] * l);
@@ -687,20 +698,21 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
         }
         group_sync(grp);
 #pragma unroll 1
-        for (int c = 0; c < LY::kBlocks; ++c) {
-            uint32_t a[HPT], d[HPT];
+        for (int c = 0; c < KB; ++c) {
+            uint32_t a[16], d[16];
             if (n_t > 0) {
-                tmem_ld8(tmem + LY::kColO + c * N + u0 + lane_base, a);
-                tmem_ld8(tmem + LY::kColO + c * N + ROWS + u0 + lane_base, d);
+                tmem_ld16(tmem + LY::kColO + c * LY::kON + ug + lane_base, a);
+                if (LY::kStacked) tmem_ld16(tmem + LY::kColO + c * LY::kON + ROWS + ug + lane_base, d);
                 tmem_wait_ld();
             }
-            const int col = c * 128 + tl;
+            const int col = c * 128 + 32 * sub + lane;
 #pragma unroll
-            for (int u = 0; u < HPT; ++u) {
-                const int r = u0 + u;
+            for (int u = 0; u < 16; ++u) {
+                const int r = ug + u;
                 if (row0 + r >= n_rows) continue;
                 const float inv = inv_s[r];
-                const float val = inv == 0.f ? 0.f : (__uint_as_float(a[u]) + __uint_as_float(d[u])) * inv;
+                const float sum = LY::kStacked ? __uint_as_float(a[u]) + __uint_as_float(d[u]) : __uint_as_float(a[u]);
+                const float val = inv == 0.f ? 0.f : sum * inv;
                 if (it.part >= 0) p.o_part[((size_t)it.part * n_rows + row0 + r) * DC + col] = val;
                 else if (p.o_dtype == QKMLA_F32) ((float*)p.o)[(grow0 + r) * DC + col] = val;
                 else ((__nv_bfloat16*)p.o)[(grow0 + r) * DC + col] = __float2bfloat16_rn(val);
@@ -743,8 +755,11 @@ bool make_rope_map(CUtensorMap* m, const void* base, int64_t rows, int64_t pitch
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Query rows per CTA: 16 when that is all there are, else 32.
-int q8_rows(const qkmla_decode_args* a) { return a->s_q * a->H <= 16 ? 16 : 32; }
+// Query rows per CTA: as many as there are, to 64.
+int q8_rows(const qkmla_decode_args* a) {
+    const int n = a->s_q * a->H;
+    return n <= 16 ? 16 : n <= 32 ? 32 : 64;
+}
 int q8_row_blocks(const qkmla_decode_args* a) {
     const int r = q8_rows(a);
     return (a->s_q * a->H + r - 1) / r;
@@ -811,7 +826,7 @@ int launch_decode_q8(const qkmla_decode_args* a, const DecodeExt& x, cudaStream_
     q.num_pages = a->num_slots / a->page_size;
     q.page_size = a->page_size;
     q.max_pages = a->max_pages;
-    q.piece = std::min(a->page_size, kT / 2);
+    q.piece = std::min(a->page_size, kT);
     q.B = a->B; q.s_q = a->s_q; q.H = a->H; q.G = a->G;
     q.window = x.window;
     q.sinks = x.sinks;
@@ -837,13 +852,21 @@ int launch_decode_q8(const qkmla_decode_args* a, const DecodeExt& x, cudaStream_
     else if (!make_rope_map(&rope, (const uint8_t*)a->kv_cache + a->d_c, a->num_slots, pitch, a->d_r, q.piece))
         return QKMLA_ERR_CUDA;
     const dim3 grid(n_rb, w.max_items);
-    const bool r16 = q8_rows(a) == 16;
-    int rc = QKMLA_ERR_UNSUPPORTED;
-    if (a->d_c == 512) rc = r16 ? launch_q8<512, 64, 16>(q, lat, rope, grid, s) : launch_q8<512, 64, 32>(q, lat, rope, grid, s);
-    else if (a->d_c == 256 && a->d_r == 32) rc = r16 ? launch_q8<256, 32, 16>(q, lat, rope, grid, s) : launch_q8<256, 32, 32>(q, lat, rope, grid, s);
-    else if (a->d_c == 256) rc = r16 ? launch_q8<256, 64, 16>(q, lat, rope, grid, s) : launch_q8<256, 64, 32>(q, lat, rope, grid, s);
-    else if (a->d_r == 32) rc = r16 ? launch_q8<128, 32, 16>(q, lat, rope, grid, s) : launch_q8<128, 32, 32>(q, lat, rope, grid, s);
-    else rc = r16 ? launch_q8<128, 64, 16>(q, lat, rope, grid, s) : launch_q8<128, 64, 32>(q, lat, rope, grid, s);
+    const int rows = q8_rows(a);
+    auto by_rows = [&](auto dc, auto dr) {
+        constexpr int DC = decltype(dc)::value, DR = decltype(dr)::value;
+        return rows == 16   ? launch_q8<DC, DR, 16>(q, lat, rope, grid, s)
+               : rows == 32 ? launch_q8<DC, DR, 32>(q, lat, rope, grid, s)
+                            : launch_q8<DC, DR, 64>(q, lat, rope, grid, s);
+    };
+    using std::integral_constant;
+    using d32 = integral_constant<int, 32>;
+    using d64 = integral_constant<int, 64>;
+    const int rc = a->d_c == 512   ? by_rows(integral_constant<int, 512>(), d64())
+                   : a->d_c == 256 ? (a->d_r == 32 ? by_rows(integral_constant<int, 256>(), d32())
+                                                   : by_rows(integral_constant<int, 256>(), d64()))
+                   : a->d_r == 32  ? by_rows(integral_constant<int, 128>(), d32())
+                                   : by_rows(integral_constant<int, 128>(), d64());
     if (rc != QKMLA_OK) return rc;
     return launch_combine_var(a, sa, w, s);
 }
