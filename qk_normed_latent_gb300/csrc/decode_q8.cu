@@ -385,12 +385,17 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
         if (lane == 0) {
             const uint32_t id_s = idesc_e4m3(kT, N, 0, 0);
             const uint32_t id_r = idesc_bf16(kT, N, 0, 0);
-            const uint32_t q_addr = smem_u32(sQ);
             constexpr uint32_t sw = DR == 64 ? kSwizzle128B : kSwizzle64B, sbo = DR == 64 ? 1024 : 512;
+            // descriptors are formed once and moved by constant offsets: forming them anew for every MMA made
+            // the issue, not the tensor core, the limit (85 cycles an MMA against 65)
+            const uint64_t q_lat = smem_desc(smem_u32(sQ), 16, 1024, kSwizzle128B);
+            const uint64_t q_rope = smem_desc(smem_u32(sQ) + LY::kQLat, 16, sbo, sw);
+            const uint64_t st_lat = smem_desc(smem_u32(sm + LY::kOffStage), 16, LY::kGroup, kSwizzle128B);
+            const uint64_t st_rope = smem_desc(smem_u32(sm + LY::kOffStage) + LY::kOffRope, 16, LY::kRopeGroup, sw);
             bool ok = true;
             for (int j = 0; j < n_t && ok; ++j) {
                 const int s = j % NST;
-                const uint32_t st = smem_u32(sm + LY::kOffStage + s * LY::kStage);
+                const uint64_t lat = st_lat + (uint64_t)(s * (LY::kStage >> 4)), rope = st_rope + (uint64_t)(s * (LY::kStage >> 4));
                 const uint32_t d = tmem + (uint32_t)(j % NSB) * (2 * N);
                 if (j >= NSB) ok = wait_bounded(&sfree[j % NSB], ((j / NSB) - 1) & 1, p.status);
                 ok = ok && wait_bounded(&full[s], (j / NST) & 1, p.status) && !*(volatile int*)abort_flag;
@@ -400,13 +405,11 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
                 for (int blk = 0; blk < KB; ++blk)
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        mma_f8(d, smem_desc(st + blk * 1024 + kk * 32, 16, LY::kGroup, kSwizzle128B),
-                               smem_desc(q_addr + blk * (N * 128) + kk * 32, 16, 1024, kSwizzle128B), id_s,
-                               (blk > 0 || kk > 0) ? 1u : 0u);
+                        mma_f8(d, lat + (uint64_t)((blk * 1024 + kk * 32) >> 4), q_lat + (uint64_t)((blk * (N * 128) + kk * 32) >> 4),
+                               id_s, (blk > 0 || kk > 0) ? 1u : 0u);
 #pragma unroll
                 for (int kk = 0; kk < DR / 16; ++kk)
-                    mma_bf16(d + N, smem_desc(st + LY::kOffRope + kk * 32, 16, LY::kRopeGroup, sw),
-                             smem_desc(q_addr + LY::kQLat + kk * 32, 16, sbo, sw), id_r, kk > 0 ? 1u : 0u);
+                    mma_bf16(d + N, rope + (uint64_t)(kk * 2), q_rope + (uint64_t)(kk * 2), id_r, kk > 0 ? 1u : 0u);
                 mma_commit(&sfull[j % NSB]);
             }
             if (!ok) {                       // no exit with an MMA in flight
@@ -419,27 +422,28 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
         // ===================== output MMAs (a thread of their own: neither issue waits for the other's data) ==========
         if (lane == 0) {
             const uint32_t id_o = idesc_e4m3(128, LY::kON, 1, 1);
+            // A: a chunk's 128 latents x 32 tokens, MN-major (8-token groups kGroup apart).  B: P, MN-major:
+            // a token's codes in as many bytes (swizzle of the same width), 8-token groups kPGroup apart.
+            constexpr int PN = LY::kON;
+            constexpr uint32_t swp = PN == 128 ? kSwizzle128B : PN == 64 ? kSwizzle64B : kSwizzle32B;
+            const uint64_t st_lat = smem_desc(smem_u32(sm + LY::kOffStage), 1024, LY::kGroup, kSwizzle128B);
+            const uint64_t st_p = smem_desc(smem_u32(sm + LY::kOffStage) + LY::kOffP, LY::kPGroup, LY::kPGroup, swp);
             bool ok = true;
             for (int j = 0; j < n_t && ok; ++j) {
                 const int s = j % NST;
-                const uint32_t st = smem_u32(sm + LY::kOffStage + s * LY::kStage);
+                const uint64_t lat = st_lat + (uint64_t)(s * (LY::kStage >> 4)), pw = st_p + (uint64_t)(s * (LY::kStage >> 4));
                 ok = wait_bounded(&pfull[s], (j / NST) & 1, p.status) && !*(volatile int*)abort_flag;
                 if (!ok) break;
                 tc_fence_after();
-                // A: a chunk's 128 latents x 32 tokens, MN-major (8-token groups kGroup apart).  B: P, MN-major:
-                // a token's codes in as many bytes (swizzle of the same width), 8-token groups kPGroup apart.
-                constexpr int PN = LY::kON;
-                constexpr uint32_t swp = PN == 128 ? kSwizzle128B : PN == 64 ? kSwizzle64B : kSwizzle32B;
 #pragma unroll
                 for (int c = 0; c < KB; ++c)
 #pragma unroll
                     for (int kk = 0; kk < kT / 32; ++kk)
 #pragma unroll
                         for (int part = 0; part < (LY::kStacked ? 1 : 2); ++part)
-                            mma_f8(tmem + LY::kColO + c * PN,
-                                   smem_desc(st + c * 1024 + kk * 4 * LY::kGroup, 1024, LY::kGroup, kSwizzle128B),
-                                   smem_desc(st + LY::kOffP + kk * 4 * LY::kPGroup + part * 8 * PN, LY::kPGroup, LY::kPGroup, swp),
-                                   id_o, (j > 0 || kk > 0 || part > 0) ? 1u : 0u);
+                            mma_f8(tmem + LY::kColO + c * PN, lat + (uint64_t)((c * 1024 + kk * 4 * LY::kGroup) >> 4),
+                                   pw + (uint64_t)((kk * 4 * LY::kPGroup + part * 8 * PN) >> 4), id_o,
+                                   (j > 0 || kk > 0 || part > 0) ? 1u : 0u);
                 mma_commit(&empty[s]);
                 mma_commit(&odone[s]);
             }
@@ -487,7 +491,7 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
             const bool got_s = wait_bounded(&sfull[sb], (j / NSB) & 1, p.status);
             tc_fence_after();
             uint64_t x2[HP2];
-            const float st_raw = *reinterpret_cast<const float*>(stg + LY::kOffScale + tl * 4);
+            float st_raw;
             {
                 uint32_t a[HPT], c[HPT], d[HPT], e[HPT];
                 const uint32_t base = tmem + (uint32_t)sb * (2 * N) + lane_base + ug;
@@ -495,9 +499,13 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
                 tmem_ld8x2(base + ROWS, c);
                 tmem_ld8x2(base + N, d);
                 tmem_ld8x2(base + N + ROWS, e);
-                // coefficient x alpha^k s_t of the rows while the loads run.  A group is 2^SH heads, known to
-                // the compiler: with a bound known only at run time the loads became a chain of
-                // branches, 2650 cycles a tile against 90 for the TMEM loads beside it
+                tmem_wait_ld();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sfree[sb]);
+                // coefficient x alpha^k s_t of the rows.  A group is 2^SH heads, known to the compiler: with a
+                // bound known only at run time the loads became a chain of branches, 2650 cycles a tile
+                st_raw = *reinterpret_cast<const float*>(stg + LY::kOffScale + tl * 4);
                 uint64_t ca2[HP2];
                 auto scale_rows = [&](auto sh, auto f16) {
                     constexpr int SH = decltype(sh)::value;
@@ -535,10 +543,6 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
                     else if (hshift == 2) scale_rows(integral_constant<int, 2>(), no());
                     else scale_rows(integral_constant<int, 1>(), no());
                 }
-                tmem_wait_ld();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sfree[sb]);
 #pragma unroll
                 for (int u = 0; u < HP2; ++u) {
                     const uint64_t sc = f2_add(f2(__uint_as_float(a[2 * u]), __uint_as_float(a[2 * u + 1])),
