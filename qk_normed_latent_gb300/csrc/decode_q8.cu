@@ -144,6 +144,9 @@ __device__ __forceinline__ void split_e4m3_f16(float2 v, uint32_t& hi, uint32_t&
     lo = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(r), __NV_SATFINITE, __NV_E4M3);
 }
 
+// The softmax warps' wait: one warp of the group polls, the others sleep at a named barrier.
+__device__ __forceinline__ bool group_any(int grp, bool pred);
+__device__ __forceinline__ void group_sync(int grp);
 __device__ __forceinline__ bool group_any(int grp, bool pred) {
     uint32_t r;
     asm volatile(
@@ -294,20 +297,33 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
         }
     } else if (warp >= 3) {
         // ---- prologue: the query rows as hi / lo parts, a warp per row ----
-        for (int r = warp - 3; r < ROWS; r += NW) {
+        constexpr int kOwn = ROWS / NW;                       // rows of a warp: their loads go out together
+        uint2 raw[kOwn][DC / 128];
+        float rv4[kOwn][DR / 32], aq4[kOwn], gq[DR / 32];
+#pragma unroll
+        for (int k = 0; k < DR / 32; ++k) gq[k] = (p.plain || !p.grq) ? 1.f : p.grq[lane * (DR / 32) + k];
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i) {
+            const int r = warp - 3 + i * NW;
             const bool ok = row0 + r < n_rows;
+            const uint2* src = reinterpret_cast<const uint2*>(p.qt + (grow0 + r) * DC + lane * (DC / 32));
+#pragma unroll
+            for (int k = 0; k < DC / 128; ++k) raw[i][k] = ok ? src[k] : make_uint2(0u, 0u);
+#pragma unroll
+            for (int k = 0; k < DR / 32; ++k) rv4[i][k] = ok ? p.qr[(grow0 + r) * DR + lane * (DR / 32) + k] : 0.f;
+            aq4[i] = (ok && !p.plain) ? p.aq[grow0 + r] : ok ? 1.f : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i) {
+            const int r = warp - 3 + i * NW;
+            const float* rv = rv4[i];
             float q[DC / 32], top = 0.f;
-            const __nv_bfloat16* src = p.qt + (grow0 + r) * DC + lane * (DC / 32);
 #pragma unroll
-            for (int k = 0; k < DC / 32; k += 4) {            // 8-byte loads: q~ is 8-byte aligned by the rows' size
-                const uint2 w = ok ? *reinterpret_cast<const uint2*>(src + k) : make_uint2(0u, 0u);
-                const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w.x));
-                const float2 c = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w.y));
-                q[k] = a.x; q[k + 1] = a.y; q[k + 2] = c.x; q[k + 3] = c.y;
+            for (int k = 0; k < DC / 128; ++k) {
+                const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&raw[i][k].x));
+                const float2 c = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&raw[i][k].y));
+                q[4 * k] = a.x; q[4 * k + 1] = a.y; q[4 * k + 2] = c.x; q[4 * k + 3] = c.y;
             }
-            float rv[DR / 32];
-#pragma unroll
-            for (int k = 0; k < DR / 32; ++k) rv[k] = ok ? p.qr[(grow0 + r) * DR + lane * (DR / 32) + k] : 0.f;
 #pragma unroll
             for (int k = 0; k < DC / 32; ++k) top = fmaxf(top, fabsf(q[k]));
             float inv;
@@ -338,7 +354,7 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
 #pragma unroll
             for (int k = 0; k < DR / 32; ++k) {
                 const int c = lane * (DR / 32) + k;
-                const float val = rv[k] * ((p.plain || !p.grq) ? 1.f : p.grq[c]) * beta;
+                const float val = rv[k] * gq[k] * beta;
                 const __nv_bfloat16 h = __float2bfloat16_rn(val);
                 const __nv_bfloat16 l = __float2bfloat16_rn(val - __bfloat162float(h));
                 const uint32_t oh = DR == 64 ? sw128_offset(r, c) : sw64_offset(r, c);
@@ -347,7 +363,7 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
                 *reinterpret_cast<__nv_bfloat16*>(sQ + LY::kQLat + ol) = l;
             }
             if (lane == 0) {
-                coef_s[r] = ok ? p.scale * kLog2e * sq * (p.plain ? 1.f : p.aq[grow0 + r]) : 0.f;
+                coef_s[r] = p.scale * kLog2e * sq * aq4[i];
                 m_s[r] = v_s[r] = -INFINITY;
                 f_s[r] = 0.f;
             }
@@ -488,7 +504,9 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
             const bool sees = t < n_row && (t < p.sinks || t >= w_row);
             const bool any_sees = t < len_last && (t < p.sinks || t >= win_first);   // some row of the CTA
             const bool masked = !__all_sync(0xffffffffu, sees);
-            const bool got_s = wait_bounded(&sfull[sb], (j / NSB) & 1, p.status);
+            bool got_s = true;
+            if (((warp - 3) & 3) == 0) got_s = wait_bounded(&sfull[sb], (j / NSB) & 1, p.status);
+            group_sync(grp);
             tc_fence_after();
             uint64_t x2[HP2];
             float st_raw;
@@ -606,7 +624,9 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
                         vx = fmaxf(vx, red_s[(4 + q) * ROWS + r]);
                     }
                     const float m0 = m_s[r], v0 = v_s[r], f0 = f_s[r];
-                    const float m1 = mx > m0 + 4.f ? ceilf(mx) : m0, v1 = vx > v0 + 2.f ? ceilf(vx) : v0;
+                    // the first tiles' largest contribution will be exceeded: leave it two binades
+                    const float m1 = mx > m0 + 4.f ? ceilf(mx) : m0;
+                    const float v1 = vx > v0 + 2.f ? ceilf(vx) + (v0 == -INFINITY ? 2.f : 1.f) : v0;
                     const float cm = m0 == -INFINITY ? 0.f : exp2f(m0 - m1);       // of the row sums
                     const float f1 = v1 == -INFINITY ? 0.f : kPUnit * exp2f(fminf(fmaxf(m1 - v1, -110.f), 95.f));
                     m_s[r] = m1;
@@ -701,25 +721,43 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
             }
         }
         group_sync(grp);
+        float inv[16];
+#pragma unroll
+        for (int u = 0; u < 16; ++u) inv[u] = inv_s[ug + u];
+        const int n_out = n_rows - row0 - ug;                 // rows of the group that exist
+        const size_t at = (it.part >= 0 ? (size_t)it.part * n_rows + row0 + ug : grow0 + ug) * DC + 32 * sub + lane;
+        float* const dst_f = it.part >= 0 ? p.o_part + at : (float*)p.o + at;
+        __nv_bfloat16* const dst_h = (__nv_bfloat16*)p.o + at;
+        const bool f32 = it.part >= 0 || p.o_dtype == QKMLA_F32;
 #pragma unroll 1
         for (int c = 0; c < KB; ++c) {
-            uint32_t a[16], d[16];
+            uint32_t a[16];
+            float val[16];
             if (n_t > 0) {
                 tmem_ld16(tmem + LY::kColO + c * LY::kON + ug + lane_base, a);
-                if (LY::kStacked) tmem_ld16(tmem + LY::kColO + c * LY::kON + ROWS + ug + lane_base, d);
                 tmem_wait_ld();
-            }
-            const int col = c * 128 + 32 * sub + lane;
 #pragma unroll
-            for (int u = 0; u < 16; ++u) {
-                const int r = ug + u;
-                if (row0 + r >= n_rows) continue;
-                const float inv = inv_s[r];
-                const float sum = LY::kStacked ? __uint_as_float(a[u]) + __uint_as_float(d[u]) : __uint_as_float(a[u]);
-                const float val = inv == 0.f ? 0.f : sum * inv;
-                if (it.part >= 0) p.o_part[((size_t)it.part * n_rows + row0 + r) * DC + col] = val;
-                else if (p.o_dtype == QKMLA_F32) ((float*)p.o)[(grow0 + r) * DC + col] = val;
-                else ((__nv_bfloat16*)p.o)[(grow0 + r) * DC + col] = __float2bfloat16_rn(val);
+                for (int u = 0; u < 16; ++u) val[u] = __uint_as_float(a[u]);
+                if constexpr (LY::kStacked) {
+                    tmem_ld16(tmem + LY::kColO + c * LY::kON + ROWS + ug + lane_base, a);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int u = 0; u < 16; ++u) val[u] += __uint_as_float(a[u]);
+                }
+#pragma unroll
+                for (int u = 0; u < 16; ++u) val[u] = inv[u] == 0.f ? 0.f : val[u] * inv[u];
+            } else {
+#pragma unroll
+                for (int u = 0; u < 16; ++u) val[u] = 0.f;
+            }
+            if (f32) {
+#pragma unroll
+                for (int u = 0; u < 16; ++u)
+                    if (u < n_out) dst_f[c * 128 + u * DC] = val[u];
+            } else {
+#pragma unroll
+                for (int u = 0; u < 16; ++u)
+                    if (u < n_out) dst_h[c * 128 + u * DC] = __float2bfloat16_rn(val[u]);
             }
         }
     }
