@@ -78,7 +78,7 @@ int plan_decode(const qkmla_decode_args* a, const DecodeExt& x, DecodePlan* plan
     if (sms <= 0) return QKMLA_ERR_CUDA;
     const bool stall = (a->flags & QKMLA_FLAG_TEST_STALL) != 0;
     if (stall && x.active()) return QKMLA_ERR_UNSUPPORTED;
-    if (!(a->flags & QKMLA_FLAG_FORCE_SIMT) && !x.active() && tc_supported(a) && a->num_splits <= 256) {
+    if (!(a->flags & QKMLA_FLAG_FORCE_SIMT) && tc_supported(a) && a->num_splits <= 256) {
         if (stall && pair_shape(a)) return QKMLA_ERR_UNSUPPORTED;   // the hook exists in the 64-row kernel only
         plan->kernel = 1;
         plan->num_splits = a->num_splits;
@@ -234,7 +234,7 @@ int decode(const qkmla_decode_args* a, const DecodeExt& x, void* stream) {
     if (plan.ws_bytes > 0 && (!a->workspace || a->workspace_bytes < plan.ws_bytes)) return QKMLA_ERR_WORKSPACE;
     if (plan.ws_bytes > 0 && !aligned(a->workspace, 16)) return QKMLA_ERR_INVALID;
     if (plan.kernel == 1 && x.kv_scale) return launch_decode_q8(a, x, (cudaStream_t)stream);
-    if (plan.kernel == 1) return launch_decode_tc(a, plan, (cudaStream_t)stream);
+    if (plan.kernel == 1) return launch_decode_tc(a, x, (cudaStream_t)stream);
     return launch_decode_simt(a, x, plan, (cudaStream_t)stream);
 }
 
@@ -243,8 +243,10 @@ bool read_ext(const qkmla_decode_args* a, const qkmla_decode_ext_args* e, Decode
     *x = DecodeExt{};
     if (!a || !e) return false;
     x->kv_scale = e->kv_scale;
-    x->window = e->window;
-    x->sinks = e->sinks;
+    // a window or sinks beyond the longest sequence mean all of it; kept below, no kernel's index can wrap
+    const int64_t max_len = std::max<int64_t>(1, (int64_t)a->max_pages * a->page_size);
+    x->window = (int)std::min<int64_t>(e->window, max_len);
+    x->sinks = (int)std::min<int64_t>(e->sinks, max_len);
     return (a->cache_dtype == QKMLA_E4M3) == (e->kv_scale != nullptr);
 }
 

@@ -164,7 +164,7 @@ struct DecodeExt {
 };
 int plan_decode(const qkmla_decode_args* a, const DecodeExt& x, DecodePlan* plan);
 int launch_decode_simt(const qkmla_decode_args* a, const DecodeExt& x, const DecodePlan& plan, cudaStream_t s);
-int launch_decode_tc(const qkmla_decode_args* a, const DecodePlan& plan, cudaStream_t s);
+int launch_decode_tc(const qkmla_decode_args* a, const DecodeExt& x, cudaStream_t s);
 bool tc_supported(const qkmla_decode_args* a);
 bool pair_shape(const qkmla_decode_args* a);        // served by the two-CTA cluster kernel
 bool sched_in_kernel(const qkmla_decode_args* a);   // split plan computed by the decode kernels themselves

@@ -63,6 +63,7 @@ struct TcParams {
     int B, s_q, H, G;
     int rows_o;                // query rows per CTA (N of the output MMA)
     float scale, eps;
+    int window, sinks;         // windowed kernels (their WIN template flag)
     const WorkItem* items;     // scheduler kernel's plan (when sched_inline == 0)
     const int* n_items;
     SchedArgs sa;
@@ -257,7 +258,7 @@ __device__ __forceinline__ void cluster_sync() {
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn();   // the driver's tensor-map encoder (nullptr if absent)
 bool make_map(CUtensorMap* m, const void* base, int64_t rows, int row_elems, int box_cols, int box_rows,
               CUtensorMapSwizzle sw);
-int launch_pair(const qkmla_decode_args* a, const TcParams& tp, int max_items, cudaStream_t s);
+int launch_pair(const qkmla_decode_args* a, const TcParams& tp, int max_items, cudaStream_t s);   // windowed if tp.window > 0
 
 // Split-KV scratch of a call with n_rb CTAs (row blocks) per tile range, laid out in
 // `ws` (null: sizes only).

@@ -85,8 +85,16 @@ static_assert(kBytesP <= 232448, "shared memory budget");
 // B) at 192, O (128 rows x 256 latents) at 256
 constexpr uint32_t kCSc = 0, kCSr = 64, kCP = 128, kCOwn = 192, kCO = 256;
 
-// AKH: A^k_cache entries are fp16 (else fp32)
-template <bool PLAIN, bool AKH>
+// Bits tt of a tile whose token t0 + tt is visible to a query of causal length L.
+__device__ __forceinline__ uint64_t visible_bits(int t0, int L, int window, int sinks) {
+    auto low = [](int n) -> uint64_t { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1; };
+    return low(L - t0) & (low(sinks - t0) | ~low(L - window - t0));
+}
+
+// AKH: A^k_cache entries are fp16 (else fp32).  WIN: a sliding window with sinks -- the work items' tiles
+// are those some query of the step sees, a tile's invisible tokens are masked by its 64 visibility bits,
+// and a query may have tiles (or a whole item) without a visible token.
+template <bool PLAIN, bool AKH, bool WIN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsP, 1)
 decode_pair_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ CUtensorMap tm_rope,
                    const __grid_constant__ CUtensorMap tm_q, const TcParams p) {
@@ -133,11 +141,13 @@ decode_pair_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_cons
     const uint32_t peer = rank ^ 1u;
     const int qi = blockIdx.x >> 1;                       // query token of this pair
     const int b = it.b;
-    const bool bad = seq_len < p.s_q || seq_len > p.max_pages * p.page_size;
+    const bool bad = seq_len < (WIN ? 0 : p.s_q) || seq_len > p.max_pages * p.page_size;
     const int L = bad ? 0 : seq_len - p.s_q + qi + 1;
-    const int tiles = (L + kT - 1) / kT;
+    const TileRange tr(bad ? 0 : seq_len, p.s_q, WIN ? p.window : 0, WIN ? p.sinks : 0, kT);
+    const int tiles = WIN ? tr.count : (L + kT - 1) / kT;
     const int jt0 = it.tile_begin;
     const int n_t = max(0, min(it.tile_end, tiles) - jt0);
+    auto first_token = [&](int j) { return (WIN ? tr.tile(jt0 + j) : jt0 + j) * kT; };   // of the item's tile j
     const int hpg = p.H / p.G;
 
     if (tid == 0) {
@@ -212,7 +222,7 @@ decode_pair_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_cons
         // lane l holds the slot of tile (j & ~31) + l: 32 page-table reads in parallel
         auto slot_of_tile = [&](int j) -> int {
             if (j >= n_t) return 0;
-            const int t0 = (jt0 + j) * kT;
+            const int t0 = first_token(j);
             const int pg = t0 / p.page_size;
             int64_t page = p.page_table ? (int64_t)p.page_table[(int64_t)b * p.max_pages + pg]
                                         : (int64_t)b * p.max_pages + pg;
@@ -352,6 +362,7 @@ decode_pair_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_cons
             for (int j = 0; j < n_t; ++j) {
                 const int s = j % kNst;
                 const int valid = min(kT, L - (jt0 + j) * kT);
+                const uint64_t vis = WIN ? visible_bits(first_token(j), L, p.window, p.sinks) : 0;
                 const bool got_s = __all_sync(0xffffffffu, wait_bounded(sfull, j & 1, p.status));
                 tc_fence_after();
                 const void* ak_t = sm + kOffStage + s * kStageB + kSLat + kSRope;
@@ -380,10 +391,10 @@ decode_pair_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_cons
                         }
                     }
                 }
-                if (valid < kT) {
+                if (WIN ? vis != ~0ull : valid < kT) {
 #pragma unroll
                     for (int t = 0; t < kT; ++t)
-                        if (t >= valid) pv[t] = -INFINITY;
+                        if (WIN ? !((vis >> t) & 1) : t >= valid) pv[t] = -INFINITY;
                 }
                 // park the fp32 partials for group B once it has read the previous ones
                 bool ok_a = got_s;
@@ -449,6 +460,8 @@ decode_pair_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_cons
             for (int j = 0; j < n_t; ++j) {
                 const int s = j % kNst, pb = j & 1;
                 const int valid = min(kT, L - (jt0 + j) * kT);
+                const uint64_t vis = WIN ? visible_bits(first_token(j), L, p.window, p.sinks) : 0;
+                const bool whole = WIN ? vis == ~0ull : valid == kT;
                 // ---- this CTA's fp32 partials from group A ----
                 const bool got_own = __all_sync(0xffffffffu, wait_bounded(ownfull, j & 1, p.status));
                 tc_fence_after();
@@ -495,7 +508,7 @@ decode_pair_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_cons
                 // own max + partner max bounds the tile max: when it cannot move the running
                 // max (by > 8, log2) for any row of the warp and the tile is full, the sums go
                 // straight into the exponentials
-                const bool fast = __all_sync(0xffffffffu, valid == kT && coef * (m_own + off) <= m_run + 8.f);
+                const bool fast = __all_sync(0xffffffffu, whole && coef * (m_own + off) <= m_run + 8.f);
                 float ps4[4] = {0.f, 0.f, 0.f, 0.f};
                 if (fast) {
                     // two tokens per packed instruction: (lg + (off + x)) - m_run, then
@@ -528,10 +541,10 @@ decode_pair_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_cons
                         lg[t] += a.x;
                         lg[t + 1] += a.y;
                     }
-                    if (valid < kT) {
+                    if (!whole) {
 #pragma unroll
                         for (int t = 0; t < kT; ++t)
-                            if (t >= valid) lg[t] = -INFINITY;
+                            if (WIN ? !((vis >> t) & 1) : t >= valid) lg[t] = -INFINITY;
                     }
                     float corr = 1.f;
                     bool need = false;
@@ -568,13 +581,15 @@ decode_pair_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_cons
                         tmem_wait_st();
                     }
                     l_run *= corr;
+                    // a row without a token yet (windowed only) has weights 0, not 2^(-inf + inf)
+                    const float m_e = (WIN && m_run == -INFINITY) ? 0.f : m_run;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         uint32_t w16[16];
 #pragma unroll
                         for (int q = 0; q < 16; ++q) {
-                            const float e0 = fast_exp2(fmaf(coef, lg[32 * h + 2 * q], -m_run));
-                            const float e1 = fast_exp2(fmaf(coef, lg[32 * h + 2 * q + 1], -m_run));
+                            const float e0 = fast_exp2(fmaf(coef, lg[32 * h + 2 * q], -m_e));
+                            const float e1 = fast_exp2(fmaf(coef, lg[32 * h + 2 * q + 1], -m_e));
                             ps4[q & 3] += e0 + e1;
                             const __nv_bfloat162 b2 = __floats2bfloat162_rn(e0, e1);
                             w16[q] = *reinterpret_cast<const uint32_t*>(&b2);
@@ -584,7 +599,17 @@ decode_pair_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_cons
                     tmem_wait_st();
                     l_run += (ps4[0] + ps4[1]) + (ps4[2] + ps4[3]);
                 }
-                if (valid < kT) {   // zero this CTA's latent rows past the sequence end (this warp's share)
+                if (WIN && !whole) {   // zero this CTA's latent rows of invisible tokens (this warp's share)
+                    uint8_t* stg = sm + kOffStage + s * kStageB;
+                    for (int e = lane + 32 * sub; e < kT * 4 * 8; e += 128) {
+                        const int rr = e / 32, rem = e % 32;
+                        if (!((vis >> rr) & 1))
+                            *reinterpret_cast<uint4*>(stg + (rem >> 3) * (kT * 128) + rr * 128 + (rem & 7) * 16) =
+                                make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
+                }
+                if (!WIN && valid < kT) {   // zero this CTA's latent rows past the sequence end (this warp's share)
                     uint8_t* stg = sm + kOffStage + s * kStageB;
                     const int nrow = kT - valid;
                     for (int e = lane + 32 * sub; e < nrow * 4 * 8; e += 128) {
@@ -677,7 +702,10 @@ int launch_pair(const qkmla_decode_args* a, const TcParams& tp, int max_items, c
         return QKMLA_ERR_CUDA;
     const bool plain = (a->flags & QKMLA_FLAG_PLAIN_MLA) != 0;
     const bool akh = !plain && (a->flags & QKMLA_FLAG_ALPHA_F16) != 0;
-    auto k = plain ? decode_pair_kernel<true, false> : akh ? decode_pair_kernel<false, true> : decode_pair_kernel<false, false>;
+    const bool win = tp.window > 0;
+    auto k = plain ? (win ? decode_pair_kernel<true, false, true> : decode_pair_kernel<true, false, false>)
+             : akh ? (win ? decode_pair_kernel<false, true, true> : decode_pair_kernel<false, true, false>)
+                   : (win ? decode_pair_kernel<false, false, true> : decode_pair_kernel<false, false, false>);
     if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytesP) != cudaSuccess)
         return QKMLA_ERR_CUDA;
     dim3 grid(2 * a->s_q, max_items);

@@ -102,8 +102,9 @@ __device__ __forceinline__ uint32_t pt_offset(int r, int t, int rows_o) {
     return (uint32_t)(t >> 6) * (uint32_t)(rows_o * 128) + sw128_offset(r, t & 63);
 }
 
-// AKH: A^k_cache entries are fp16 (else fp32)
-template <int DC, int DR, bool PLAIN, int NST, int KT, bool AKH>
+// AKH: A^k_cache entries are fp16 (else fp32).  WIN: a sliding window with sinks -- the work items' tiles
+// are those some query of the step sees, and each row masks the tokens it does not.
+template <int DC, int DR, bool PLAIN, int NST, int KT, bool AKH, bool WIN>
 __global__ void __launch_bounds__(kThreads, 1)
 decode_tc_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ CUtensorMap tm_rope,
                  const __grid_constant__ CUtensorMap tm_q, const TcParams p) {
@@ -149,11 +150,12 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
     const int row0 = blockIdx.x * rows_o;          // row index within the sequence's s_q*H rows
     const int qi = row0 / p.H, h0 = row0 % p.H;    // the first row's query token and head
     const int b = it.b;
-    const bool bad = seq_len < p.s_q || seq_len > p.max_pages * p.page_size;
+    const bool bad = seq_len < (WIN ? 0 : p.s_q) || seq_len > p.max_pages * p.page_size;
     // rows_o may cover several query tokens (rows_o > H): the tiles run to the last
     // row's causal length, and each row masks past its own
     const int L = bad ? 0 : seq_len - p.s_q + (row0 + rows_o - 1) / p.H + 1;
-    const int tiles = (L + KT - 1) / KT;
+    const TileRange tr(bad ? 0 : seq_len, p.s_q, WIN ? p.window : 0, WIN ? p.sinks : 0, KT);
+    const int tiles = WIN ? tr.count : (L + KT - 1) / KT;
     const int jt0 = it.tile_begin;
     const int jt1 = min(it.tile_end, tiles);
     const int n_t = max(0, jt1 - jt0);
@@ -184,7 +186,7 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
     // ---- TMA producer state (warp 0): the slot of tile j + lane, 32 tiles at a time ----
     auto slot_of_tile = [&](int j) -> int64_t {
         if (j >= n_t) return 0;
-        const int t0 = (jt0 + j) * KT;
+        const int t0 = (WIN ? tr.tile(jt0 + j) : jt0 + j) * KT;
         const int pg = t0 / p.page_size;
         int64_t page = p.page_table ? (int64_t)p.page_table[(int64_t)b * p.max_pages + pg]
                                     : (int64_t)b * p.max_pages + pg;
@@ -379,6 +381,7 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
         const bool row_ok = r < rows_o;
         const int g = row_ok ? ((h0 + r) % p.H) / hpg : 0;
         const int L_r = bad ? 0 : seq_len - p.s_q + (row0 + (row_ok ? r : 0)) / p.H + 1;   // this row's length
+        const int L_first = seq_len - p.s_q + qi + 1;                                       // the first row's
         const float coef = row_ok ? coef_s[r] : 0.f;
         const float rs = p.scale * kLog2e;
         float m_run = -INFINITY, l_run = 0.f;
@@ -386,7 +389,7 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
         bool late_fail = false;      // a timed-out wait at the end of the previous tile
         for (int j = 0; j < n_t; ++j) {
             const int s = j % NST, sb = j % NSB;
-            const int tile = jt0 + j;
+            const int tile = WIN ? tr.tile(jt0 + j) : jt0 + j;
             // a timed-out wait is folded into the per-tile vote below, so every abort
             // decision is uniform across the four softmax warps (none is left at a
             // named barrier)
@@ -442,6 +445,12 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
 #pragma unroll
                 for (int jj = 0; jj < 16; ++jj)
                     if (32 * q + tb + jj >= valid_r) lg[q][jj] = -INFINITY;
+                if (WIN && tile * KT < L_r - p.window && (tile + 1) * KT > p.sinks) {
+                    const int hs = p.sinks - tile * KT, ws = L_r - p.window - tile * KT;
+#pragma unroll
+                    for (int jj = 0; jj < 16; ++jj)
+                        if (32 * q + tb + jj >= hs && 32 * q + tb + jj < ws) lg[q][jj] = -INFINITY;
+                }
             }
             float mt = -INFINITY;
 #pragma unroll
@@ -522,7 +531,19 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
             l_run += psum;
             // the last tile of the sequence: zero the latent rows past its end so that
             // stale slot contents (possibly NaN) cannot reach the output MMA
-            if (valid < KT) {
+            if (WIN) {
+                // tokens no row of the CTA sees: past its longest row, or between the sinks and its first row's window
+                const int hs = p.sinks - tile * KT, ws = L_first - p.window - tile * KT;
+                if (valid < KT || (ws > 0 && hs < KT)) {
+                    for (int e = tid - 64; e < KT * LY::kLatBlocks * 8; e += 128) {
+                        const int rr = e / (LY::kLatBlocks * 8), rem = e % (LY::kLatBlocks * 8);
+                        if (rr >= valid || (rr >= hs && rr < ws))
+                            *reinterpret_cast<uint4*>(stg + (rem >> 3) * (KT * 128) + rr * 128 + (rem & 7) * 16) =
+                                make_uint4(0, 0, 0, 0);
+                    }
+                }
+            }
+            if (!WIN && valid < KT) {
                 const int st = tid - 64;
                 const int nrow = KT - valid;
                 for (int e = st; e < nrow * LY::kLatBlocks * 8; e += 128) {
@@ -814,18 +835,25 @@ combine_var_kernel(const float* __restrict__ o_part, const float* __restrict__ l
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
-template <int DC, int DR, bool PLAIN, int NST, bool AKH>
-int launch_kernel(const CUtensorMap& lat, const CUtensorMap& rope, const CUtensorMap& qmap, const TcParams& tp,
+template <int DC, int DR, bool PLAIN, int NST, bool AKH, bool WIN>
+int launch_kernel_w(const CUtensorMap& lat, const CUtensorMap& rope, const CUtensorMap& qmap, const TcParams& tp,
                   int n_rb, int max_items, cudaStream_t s) {
     constexpr int KT = tile_of<DC>();
     using LY = Layout<DC, DR, NST, KT>;
-    auto k = decode_tc_kernel<DC, DR, PLAIN, NST, KT, AKH>;
+    auto k = decode_tc_kernel<DC, DR, PLAIN, NST, KT, AKH, WIN>;
     static_assert(LY::kBytes <= 232448, "shared memory budget");
     if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, LY::kBytes) != cudaSuccess)
         return QKMLA_ERR_CUDA;
     dim3 grid(n_rb, max_items);
     return launch_pdl(k, grid, dim3(kThreads), LY::kBytes, s, lat, rope, qmap, tp) == cudaSuccess ? QKMLA_OK
                                                                                          : QKMLA_ERR_CUDA;
+}
+
+template <int DC, int DR, bool PLAIN, int NST, bool AKH>
+int launch_kernel(const CUtensorMap& lat, const CUtensorMap& rope, const CUtensorMap& qmap, const TcParams& tp,
+                  int n_rb, int max_items, cudaStream_t s) {
+    return tp.window > 0 ? launch_kernel_w<DC, DR, PLAIN, NST, AKH, true>(lat, rope, qmap, tp, n_rb, max_items, s)
+                         : launch_kernel_w<DC, DR, PLAIN, NST, AKH, false>(lat, rope, qmap, tp, n_rb, max_items, s);
 }
 
 }  // namespace
@@ -947,7 +975,7 @@ size_t tc_workspace(const qkmla_decode_args* a, int sms) {
     return split_scratch(a, tc_row_blocks(a), sms, nullptr).bytes;
 }
 
-int launch_decode_tc(const qkmla_decode_args* a, const DecodePlan& plan, cudaStream_t s) {
+int launch_decode_tc(const qkmla_decode_args* a, const DecodeExt& x, cudaStream_t s) {
     const int sms = device_sm_count();
     const int rows_o = pair_shape(a) ? 64 : tc_rows(a);
     const int n_rb = tc_row_blocks(a);
@@ -964,8 +992,9 @@ int launch_decode_tc(const qkmla_decode_args* a, const DecodePlan& plan, cudaStr
     sa.min_tokens = 512;
     sa.tile = tile;
     sa.fixed_splits = a->num_splits;
-    sa.min_len = a->s_q;
-    sa.window = sa.sinks = 0;
+    sa.min_len = x.window > 0 ? 0 : a->s_q;
+    sa.window = x.window;
+    sa.sinks = x.sinks;
     // small batches: the decode and combine kernels plan the split themselves
     const int sched_inline = sched_in_kernel(a) ? 1 : 0;
     if (!sched_inline && launch_sched(a, sa, w, s) != QKMLA_OK) return QKMLA_ERR_CUDA;
@@ -995,6 +1024,8 @@ int launch_decode_tc(const qkmla_decode_args* a, const DecodePlan& plan, cudaStr
     tp.max_pages = a->max_pages;
     tp.B = a->B; tp.s_q = a->s_q; tp.H = a->H; tp.G = a->G;
     tp.rows_o = rows_o;
+    tp.window = x.window;
+    tp.sinks = x.sinks;
     tp.scale = a->softmax_scale;
     tp.eps = a->eps;
     tp.items = w.items;

@@ -102,6 +102,35 @@ def test_simt(Q, k, cache):
     check(Q, R.Case(cache=cache, **kw), simt=True)
 
 
+@pytest.mark.parametrize("cache", ["q8", "bf16"])
+@pytest.mark.parametrize("H", [16, 128])
+def test_repeats_and_streams(Q, cache, H):
+    """The same bits on every call, in order after work on the caller's stream, and from a captured graph."""
+    c = R.Case([900, 333, 0, 64], cache=cache, window=300, sinks=5, s_q=2, H=H, G=4 if H == 16 else 8,
+               d_c=256 if H == 16 else 512, d_r=32 if H == 16 else 64)
+    dev = Device(Q, c)
+    first = [x.copy() for x in dev.run(Q)]
+    side = torch.cuda.Stream()
+    qt = dev.in_[0].clone()
+    for _ in range(5):
+        dev.in_[0].zero_()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(200000)
+            dev.in_[0].copy_(qt)
+            dev.call(side)
+        side.synchronize()
+        assert (dev.o.double().cpu().numpy() == first[0]).all()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        dev.call()
+    dev.o.zero_()
+    graph.replay()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert (dev.o.double().cpu().numpy() == first[0]).all() and (dev.lse.double().cpu().numpy() == first[1]).all()
+
+
 @pytest.mark.parametrize("splits", [1, 3, 7])
 def test_simt_splits(Q, splits):
     check(Q, R.Case([200, 0, 1, 90], window=60, sinks=5, s_q=2), simt=True, num_splits=splits)
@@ -135,6 +164,44 @@ TC = [
     dict(lens=[3000] * 5, d_c=512, d_r=64, H=128, G=8, s_q=2),
     dict(lens=[(37 * k) % 300 for k in range(140)], window=100, sinks=5),   # planned by the scheduler kernel
 ]
+
+
+WINDOW = [
+    dict(lens=[1], window=5),
+    dict(lens=[0, 1, 2, 63, 64, 65, 127, 128, 129, 300, 700], window=100, sinks=4),
+    dict(lens=[1000, 333], window=1, s_q=2),
+    dict(lens=[1000, 333, 70], window=64, sinks=64, s_q=3),
+    dict(lens=[1, 2, 100, 400], window=70, sinks=3, s_q=4),                  # lengths below s_q
+    dict(lens=[1500, 900], window=513, sinks=130, num_splits=3),
+    dict(lens=[1500, 900], window=513, sinks=130, s_q=2, alpha="f16"),
+    dict(lens=[700, 100], window=200, sinks=7, plain=True, outlier=1.0),
+    dict(lens=[700, 100], window=200, sinks=7, contiguous=True),
+    dict(lens=[400, 100], window=2 ** 31 - 1, sinks=2 ** 31 - 1),
+    dict(lens=[(37 * k) % 300 for k in range(140)], window=100, sinks=5),    # planned by the scheduler kernel
+]
+SHAPES = [dict(), dict(H=32, G=2), dict(H=128, G=8, d_c=512, d_r=64), dict(H=64, G=8, d_c=512, d_r=64, page=128),
+          dict(H=16, G=1, d_c=512, d_r=64)]
+
+
+@pytest.mark.parametrize("shape", range(len(SHAPES)))
+@pytest.mark.parametrize("k", range(len(WINDOW)))
+def test_window_tensor_core(Q, k, shape):
+    kw = dict(WINDOW[k])
+    splits = kw.pop("num_splits", 0)
+    if len(kw["lens"]) > 20 and SHAPES[shape].get("d_c") == 512:
+        kw["lens"] = kw["lens"][:130]
+    check(Q, R.Case(cache="bf16", **kw, **SHAPES[shape]), simt=False, num_splits=splits)
+
+
+@pytest.mark.parametrize("H", [16, 128])
+def test_window_over_everything_is_decode(Q, H):
+    """A window that covers every token gives the bits of the call without one."""
+    c = R.Case([700, 130, 64], cache="bf16", H=H, G=4 if H == 16 else 8, d_c=256 if H == 16 else 512,
+               d_r=32 if H == 16 else 64, s_q=2)
+    a, la = Device(Q, c).run(Q)
+    c.window = 700
+    b, lb = Device(Q, c).run(Q)
+    assert (a == b).all() and (la == lb).all()
 
 
 @pytest.mark.parametrize("k", range(len(TC)))
