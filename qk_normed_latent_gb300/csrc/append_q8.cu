@@ -4,13 +4,28 @@
 // alpha^k_g = 1 / sqrt(mean_j (c^ W^K_g)_j^2 + eps) is the statistic of what is
 // stored, so decode normalises exactly the keys it sees.
 //
-// Plain-load kernel: CTA (token tile, g) holds 32 tokens and one group.  It takes
+// Tensor-core kernel (d_c 128 / 256 / 512, d_h 64 / 128).  The key statistic is a GEMM [N, d_c] x [d_c, d_h]
+// per group whose result is only squared and summed.  The codes are exact in bf16; W^K is split into two
+// bf16 parts, w = hi + lo up to 2^-17 of w, both columns of one B operand, so that one tcgen05.mma
+// (M = 128 tokens, N = 2 d_h, K = 16) forms both products; the epilogue adds the parts, squares and sums a
+// token's columns in one thread.  alpha^k is within ~1e-6 of the fp32 form, whose GEMM on the CUDA cores took
+// 50 times as long.  A CTA owns up to 128 tokens: it quantises them once (scale, codes, and the codes' values
+// as the A operand, all d_c columns in shared memory) and runs over its groups, W^K streaming through registers
+// (loads four chunks ahead) into a ring of 32-row chunks.  How many tokens and groups a CTA takes is chosen by
+// the host (plan_q8): whole prompts want 128 tokens and all groups, so that a token is quantised once; a
+// decode step has few tokens and spreads its groups over the GPU.
+//
+// Plain-load kernel (other dimensions): CTA (token tile, g) holds 32 tokens and one group.  It takes
 // each token's scale from its largest magnitude, forms the keys (fp32, one fmaf
 // chain per element over ascending k) chunk by chunk through shared memory and
 // reduces them to their sum of squares; the g = 0 CTA also stores the codes, the
 // scale and the RoPE key.
+#include <algorithm>
+
 #include "common.cuh"
+#include "decode_common.cuh"
 #include "rope.cuh"
+#include "tc_ptx.cuh"
 
 namespace qkmla {
 
@@ -137,12 +152,345 @@ append_q8_plain_kernel(const float* __restrict__ c_new, const float* __restrict_
     }
 }
 
+// ---------------------------------------------------------------------------
+// tensor-core kernel
+// ---------------------------------------------------------------------------
+using namespace tc;
+using dec::wait_bounded;
+
+constexpr int kMT = 128;          // rows of the MMA: tokens of a CTA, at most
+constexpr int kLoadWarps = 8, kEpiWarps = 4;
+constexpr int kTcThreads = 32 * (kLoadWarps + kEpiWarps + 1);
+constexpr int kChunk = 32;        // rows of W^K per ring stage
+constexpr int kAhead = 4;         // chunks of W^K in flight in registers
+
+template <int DC, int DH>
+struct AppendLayout {
+    static constexpr int kN = 2 * DH;                          // hi and lo columns
+    static constexpr int kA = DC / 64 * kMT * 128;             // bf16, K-major, 128-byte swizzle
+    static constexpr int kStage = kChunk * kN * 2;             // bf16, MN-major: kN / 64 atoms of 64 columns
+    static constexpr int kNst = std::min(8, (232448 - kA - 4096) / kStage);
+    static constexpr int kOffMisc = kA + kNst * kStage;
+    static constexpr int kBytes = kOffMisc + (2 * kNst + 5) * 8 + 16 + kMT * 4 + 1024;
+    static_assert(kNst >= 4 && kBytes <= 232448, "shared memory budget");
+};
+
+struct AppendQ8Params {
+    const float *c_new, *r_new, *wk, *grk;
+    const int64_t* slots;
+    int N, G, d_r;
+    float eps;
+    int plain;
+    uint8_t* kv;
+    float* kv_scale;
+    void* ak;
+    int ak_f16;
+    int64_t num_slots;
+    const int32_t* positions;
+    float theta;
+    int tokens, groups;           // per CTA
+    int* status;
+};
+
+template <int DC, int DH>
+__global__ void __launch_bounds__(kTcThreads, 1) append_q8_tc_kernel(const AppendQ8Params p) {
+    using LY = AppendLayout<DC, DH>;
+    constexpr int NST = LY::kNst, kV = DC / 128, kF4 = kChunk * DH / 4 / (32 * kLoadWarps);
+    extern __shared__ __align__(1024) uint8_t smraw[];
+    uint8_t* sm = smraw + ((1024u - (smem_u32(smraw) & 1023u)) & 1023u);
+    uint64_t* bfull = (uint64_t*)(sm + LY::kOffMisc);          // [NST] chunk written -> MMA (one arrive per warp)
+    uint64_t* bempty = bfull + NST;                            // [NST] MMA done -> loaders
+    uint64_t* dfull = bempty + NST;                            // [2] keys of a group done -> epilogue
+    uint64_t* dfree = dfull + 2;                               // [2] read -> MMA
+    uint64_t* drain = dfree + 2;
+    uint32_t* tmem_slot = (uint32_t*)(drain + 1);
+    int* abort_flag = (int*)(tmem_slot + 1);
+    float* scale_s = (float*)(tmem_slot + 4);
+    __shared__ RopeFreq freq[32];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int n0 = blockIdx.x * p.tokens, n_tok = min(p.tokens, p.N - n0);
+    const int g0 = blockIdx.y * p.groups, n_g = min(p.groups, p.G - g0);
+    const int n_chunks = n_g * (DC / kChunk);
+
+    if (tid == 0) {
+        for (int i = 0; i < NST; ++i) {
+            mbar_init(&bfull[i], kLoadWarps);
+            mbar_init(&bempty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&dfull[i], 1);
+            mbar_init(&dfree[i], kEpiWarps);
+        }
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (p.positions && tid < p.d_r / 2) freq[tid] = rope_freq(p.theta, tid, p.d_r);
+    if (warp == kLoadWarps + kEpiWarps) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    // W^K: the loads of the first chunks go out before anything else (no kernel of the library writes it)
+    const float4* w4 = reinterpret_cast<const float4*>(p.wk + (int64_t)g0 * DC * DH);
+    float4 wv[kAhead][kF4];
+    auto fetch = [&](int q, float4 (&v)[kF4]) {
+#pragma unroll
+        for (int i = 0; i < kF4; ++i)
+            v[i] = q < n_chunks ? __ldg(w4 + (int64_t)q * (kChunk * DH / 4) + tid + 32 * kLoadWarps * i)
+                                : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+    if (warp < kLoadWarps) {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) fetch(u, wv[u]);
+    }
+    __syncthreads();                                           // freq, barriers
+    pdl_wait();                                                // the cache writes follow the previous kernel
+    pdl_trigger();
+
+    // ---- quantise: a warp per token, two tokens' loads at a time ----
+    constexpr int kQWarps = kLoadWarps + kEpiWarps;
+    if (warp < kQWarps) {
+        for (int t0 = warp; t0 < n_tok; t0 += 2 * kQWarps) {
+            float4 v[2][kV];
+            float rv[2][2];
+            int64_t slot[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int tl = t0 + i * kQWarps;
+                const bool on = tl < n_tok;
+                const float4* src = reinterpret_cast<const float4*>(p.c_new + (int64_t)(n0 + tl) * DC);
+#pragma unroll
+                for (int k = 0; k < kV; ++k) v[i][k] = on ? __ldg(src + 32 * k + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
+                slot[i] = (on && g0 == 0) ? p.slots[n0 + tl] : -1;
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {                  // d_r <= 64: elements lane and lane + 32
+                    const int jj = lane + 32 * u;
+                    rv[i][u] = (on && g0 == 0 && jj < p.d_r) ? p.r_new[(int64_t)(n0 + tl) * p.d_r + jj] : 0.f;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int tl = t0 + i * kQWarps;
+                if (tl >= n_tok) break;                        // uniform over the warp
+                float top = 0.f;
+#pragma unroll
+                for (int k = 0; k < kV; ++k)
+                    top = fmaxf(top, fmaxf(fmaxf(fabsf(v[i][k].x), fabsf(v[i][k].y)), fmaxf(fabsf(v[i][k].z), fabsf(v[i][k].w))));
+                top = warp_max(top);
+                float inv;
+                const float s = e4m3_scale(top, &inv);
+                const bool store = slot[i] >= 0 && slot[i] < p.num_slots;
+                uint8_t* row = p.kv + slot[i] * (int64_t)(DC + 2 * p.d_r);
+#pragma unroll
+                for (int k = 0; k < kV; ++k) {
+                    float x[4] = {v[i][k].x, v[i][k].y, v[i][k].z, v[i][k].w};
+                    if (isinf(top)) {                          // an infinity is stored as NaN, not saturated
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) x[u] = isinf(x[u]) ? __int_as_float(0x7fffffff) : x[u];
+                    }
+                    const uint32_t c01 = __nv_cvt_float2_to_fp8x2(make_float2(x[0] * inv, x[1] * inv), __NV_SATFINITE, __NV_E4M3);
+                    const uint32_t c23 = __nv_cvt_float2_to_fp8x2(make_float2(x[2] * inv, x[3] * inv), __NV_SATFINITE, __NV_E4M3);
+                    const float2 f01 = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)c01, __NV_E4M3)));
+                    const float2 f23 = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)c23, __NV_E4M3)));
+                    const __nv_bfloat162 b01 = __floats2bfloat162_rn(f01.x, f01.y), b23 = __floats2bfloat162_rn(f23.x, f23.y);
+                    const int col = 128 * k + 4 * lane;
+                    uint2 w;
+                    w.x = *reinterpret_cast<const uint32_t*>(&b01);
+                    w.y = *reinterpret_cast<const uint32_t*>(&b23);
+                    *reinterpret_cast<uint2*>(sm + (col >> 6) * (kMT * 128) + sw128_offset(tl, col & 63)) = w;
+                    if (store) *reinterpret_cast<uint32_t*>(row + col) = c01 | (c23 << 16);
+                }
+                if (lane == 0) {
+                    scale_s[tl] = s;
+                    if (store) p.kv_scale[slot[i]] = s;
+                }
+                if (g0 == 0) {                                 // the RoPE key: rotated, then normalised on its own
+                    if (p.positions) {
+                        const int pos = p.positions[n0 + tl];
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            const int jj = lane + 32 * u;
+                            const float w = __shfl_xor_sync(0xffffffffu, rv[i][u], 1);
+                            if (jj < p.d_r) {
+                                float c, sn;
+                                rope_cos_sin(pos, freq[jj >> 1], &c, &sn);
+                                rv[i][u] = rope_apply(jj, rv[i][u], w, c, sn);
+                            }
+                        }
+                    }
+                    const float ss = warp_sum(fmaf(rv[i][0], rv[i][0], rv[i][1] * rv[i][1]));
+                    const float beta = p.plain ? 1.f : 1.f / sqrtf(ss / (float)p.d_r + p.eps);
+                    __nv_bfloat16* rope = reinterpret_cast<__nv_bfloat16*>(row + DC);
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const int jj = lane + 32 * u;
+                        if (store && jj < p.d_r)
+                            rope[jj] = __float2bfloat16_rn(p.plain ? rv[i][u] : rv[i][u] * (p.grk ? p.grk[jj] : 1.f) * beta);
+                    }
+                    if (lane == 0 && slot[i] >= p.num_slots) report(p.status, QKMLA_ERR_DEVICE_BOUNDS);
+                }
+            }
+        }
+        fence_proxy_async_smem();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp < kLoadWarps) {
+        // ===================== W^K chunks: fp32 registers -> hi and lo bf16 =====================
+        bool ok = true;
+        for (int q0 = 0; q0 < n_chunks && ok; q0 += kAhead) {
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const int q = q0 + u;
+                if (q >= n_chunks) break;
+                const int s = q % NST;
+                if (q >= NST) ok = wait_bounded(&bempty[s], ((q / NST) - 1) & 1, p.status);
+                ok = __all_sync(0xffffffffu, ok && !*(volatile int*)abort_flag);
+                if (!ok) break;
+                uint8_t* stg = sm + LY::kA + s * LY::kStage;
+#pragma unroll
+                for (int i = 0; i < kF4; ++i) {
+                    const int f = tid + 32 * kLoadWarps * i;
+                    const int k = f / (DH / 4), jc = 4 * (f % (DH / 4));
+                    const float4 w = wv[u][i];
+                    const __nv_bfloat162 h01 = __floats2bfloat162_rn(w.x, w.y), h23 = __floats2bfloat162_rn(w.z, w.w);
+                    const float2 r01 = __bfloat1622float2(h01), r23 = __bfloat1622float2(h23);
+                    const __nv_bfloat162 l01 = __floats2bfloat162_rn(w.x - r01.x, w.y - r01.y);
+                    const __nv_bfloat162 l23 = __floats2bfloat162_rn(w.z - r23.x, w.w - r23.y);
+                    uint2 hv, lv;
+                    hv.x = *reinterpret_cast<const uint32_t*>(&h01); hv.y = *reinterpret_cast<const uint32_t*>(&h23);
+                    lv.x = *reinterpret_cast<const uint32_t*>(&l01); lv.y = *reinterpret_cast<const uint32_t*>(&l23);
+                    // atom of 64 columns x 8 rows: 1024 bytes, the atom's 8-row groups back to back
+                    uint8_t* dst = stg + (jc >> 6) * (kChunk * 128) + (k >> 3) * 1024 + (k & 7) * 128 +
+                                   ((((jc & 63) >> 3) ^ (k & 7)) << 4) + (jc & 4) * 2;
+                    *reinterpret_cast<uint2*>(dst) = hv;
+                    *reinterpret_cast<uint2*>(dst + DH / 64 * (kChunk * 128)) = lv;
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bfull[s]);
+                fetch(q + kAhead, wv[u]);
+            }
+        }
+        if (!ok) *(volatile int*)abort_flag = 1;
+    } else if (warp == kLoadWarps + kEpiWarps) {
+        // ===================== MMA issuer =====================
+        if (lane == 0) {
+            const uint32_t id = idesc_bf16(kMT, LY::kN, 0, 1);
+            const uint64_t a0 = smem_desc(smem_u32(sm), 16, 1024, kSwizzle128B);
+            const uint64_t b0 = smem_desc(smem_u32(sm + LY::kA), kChunk * 128, 1024, kSwizzle128B);
+            bool ok = true;
+            int q = 0;
+            for (int gi = 0; gi < n_g && ok; ++gi) {
+                const uint32_t d = tmem + (uint32_t)(gi & 1) * 256u;
+                if (gi >= 2) ok = wait_bounded(&dfree[gi & 1], ((gi >> 1) - 1) & 1, p.status);
+                for (int c = 0; c < DC / kChunk && ok; ++c, ++q) {
+                    const int s = q % NST;
+                    ok = wait_bounded(&bfull[s], (q / NST) & 1, p.status) && !*(volatile int*)abort_flag;
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t a = a0 + (uint64_t)(((c >> 1) * (kMT * 128) + (c & 1) * 64) >> 4);
+                    const uint64_t bd = b0 + (uint64_t)(s * (LY::kStage >> 4));
+#pragma unroll
+                    for (int kk = 0; kk < kChunk / 16; ++kk)
+                        mma_bf16(d, a + (uint64_t)(kk * 2), bd + (uint64_t)(kk * 128), id, (c > 0 || kk > 0) ? 1u : 0u);
+                    mma_commit(&bempty[s]);
+                }
+                if (ok) mma_commit(&dfull[gi & 1]);
+            }
+            if (!ok) *(volatile int*)abort_flag = 1;
+            mma_commit(drain);                                 // no exit with an MMA in flight
+            wait_bounded(drain, 0, p.status);
+        }
+    } else {
+        // ===================== epilogue: thread = token =====================
+        const int sub = warp & 3, tl = 32 * sub + lane;
+        const uint32_t lane_base = (uint32_t)(32 * sub) << 16;
+        const bool on = tl < n_tok;
+        const int64_t slot = on ? p.slots[n0 + tl] : -1;
+        const float s = on ? scale_s[tl] : 0.f;
+        for (int gi = 0; gi < n_g; ++gi) {
+            const bool got = __all_sync(0xffffffffu, wait_bounded(&dfull[gi & 1], (gi >> 1) & 1, p.status));
+            if (!got) { *(volatile int*)abort_flag = 1; break; }
+            tc_fence_after();
+            const uint32_t d = tmem + (uint32_t)(gi & 1) * 256u + lane_base;
+            float ss[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
+            for (int c = 0; c < DH; c += 16) {
+                uint32_t h[16], l[16];
+                tmem_ld16(d + c, h);
+                tmem_ld16(d + DH + c, l);
+                tmem_wait_ld();
+#pragma unroll
+                for (int u = 0; u < 16; ++u) {
+                    const float k = __uint_as_float(h[u]) + __uint_as_float(l[u]);
+                    ss[u & 3] = fmaf(k, k, ss[u & 3]);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&dfree[gi & 1]);
+            const float mean = ((ss[0] + ss[1]) + (ss[2] + ss[3])) / (float)DH;   // of the keys of the codes
+            if (slot >= 0 && slot < p.num_slots)
+                store_alpha(p.ak, slot * p.G + g0 + gi, p.plain ? 1.f : 1.f / sqrtf(s * s * mean + p.eps), p.ak_f16 != 0);
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kLoadWarps + kEpiWarps) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// Tokens and groups per CTA: the cheapest of a few splits by a simple model -- a fixed part, a part per token
+// (quantising: a warp per token) and a part per group (its W^K streamed and multiplied), times the waves.
+void plan_q8(int N, int G, int d_c, int d_h, int sms, int* tokens, int* groups) {
+    const float per_token = 0.02f, per_group = 2.2f * (float)d_c * d_h / (512 * 128), fixed = 4.f;   // us
+    float best = 1e30f;
+    for (int t = 16; t <= kMT; t *= 2)
+        for (int g = 1; g <= G; ++g) {
+            const int64_t ctas = (int64_t)((N + t - 1) / t) * ((G + g - 1) / g);
+            const float cost = (float)((ctas + sms - 1) / sms) * (fixed + per_token * t + per_group * g);
+            if (cost < best) { best = cost; *tokens = t; *groups = g; }
+        }
+}
+
+template <int DC, int DH>
+cudaError_t launch_tc(const AppendQ8Params& p, cudaStream_t s) {
+    auto k = append_q8_tc_kernel<DC, DH>;
+    constexpr int bytes = AppendLayout<DC, DH>::kBytes;
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    const dim3 grid((p.N + p.tokens - 1) / p.tokens, (p.G + p.groups - 1) / p.groups);
+    return launch_pdl(k, grid, dim3(kTcThreads), bytes, s, p);
+}
+
 }  // namespace
 
 int launch_append_q8(const float* c_new, const float* r_new, const float* wk, const float* grk, const int64_t* slots,
                      int N, int G, int d_c, int d_h, int d_r, float eps, bool plain, uint8_t* kv, float* kv_scale,
                      void* ak, bool ak_f16, int64_t num_slots, const int32_t* positions, float rope_theta,
                      cudaStream_t s) {
+    const bool tc = (d_c == 128 || d_c == 256 || d_c == 512) && (d_h == 64 || d_h == 128) && d_r % 2 == 0 &&
+                    ((uintptr_t)c_new % 16) == 0 && ((uintptr_t)wk % 16) == 0 && ((uintptr_t)kv % 4) == 0;
+    if (tc) {
+        const int sms = device_sm_count();
+        if (sms <= 0) return QKMLA_ERR_CUDA;
+        AppendQ8Params p{c_new, r_new, wk, grk, slots, N, G, d_r, eps, (int)plain, kv, kv_scale, ak, (int)ak_f16,
+                         num_slots, positions, rope_theta, 0, 0, device_status_ptr()};
+        plan_q8(N, G, d_c, d_h, sms, &p.tokens, &p.groups);
+        const bool wide = d_h == 128;
+        const cudaError_t e = d_c == 512   ? (wide ? launch_tc<512, 128>(p, s) : launch_tc<512, 64>(p, s))
+                              : d_c == 256 ? (wide ? launch_tc<256, 128>(p, s) : launch_tc<256, 64>(p, s))
+                                           : (wide ? launch_tc<128, 128>(p, s) : launch_tc<128, 64>(p, s));
+        return e == cudaSuccess ? QKMLA_OK : QKMLA_ERR_CUDA;
+    }
     const size_t smem = (size_t)kKC * d_h * sizeof(float);
     if (cudaFuncSetAttribute(append_q8_plain_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
         cudaSuccess)
