@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) append_q8_tc_kernel(const Appen
                     *reinterpret_cast<uint2*>(dst) = hv;
                     *reinterpret_cast<uint2*>(dst + DH / 64 * (kChunk * 128)) = lv;
                 }
-                fence_proxy_async_smem();
+                // the fence to the async proxy is the MMA thread's: here it would wait for the loads in flight
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bfull[s]);
                 fetch(q + kAhead, wv[u]);
@@ -391,6 +391,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) append_q8_tc_kernel(const Appen
                     const int s = q % NST;
                     ok = wait_bounded(&bfull[s], (q / NST) & 1, p.status) && !*(volatile int*)abort_flag;
                     if (!ok) break;
+                    fence_proxy_async_smem();                  // the loaders' writes, seen through the barrier
                     tc_fence_after();
                     const uint64_t a = a0 + (uint64_t)(((c >> 1) * (kMT * 128) + (c & 1) * 64) >> 4);
                     const uint64_t bd = b0 + (uint64_t)(s * (LY::kStage >> 4));
