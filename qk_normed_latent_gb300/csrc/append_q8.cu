@@ -192,6 +192,14 @@ struct AppendQ8Params {
     int* status;
 };
 
+// A read-only load that stays where it is written: as an ordinary one the compiler may move it down to its use.
+__device__ __forceinline__ float4 load_stream(const float4* p) {
+    float4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p));
+    return v;
+}
+
 template <int DC, int DH>
 __global__ void __launch_bounds__(kTcThreads, 1) append_q8_tc_kernel(const AppendQ8Params p) {
     using LY = AppendLayout<DC, DH>;
@@ -236,8 +244,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) append_q8_tc_kernel(const Appen
     auto fetch = [&](int q, float4 (&v)[kF4]) {
 #pragma unroll
         for (int i = 0; i < kF4; ++i)
-            v[i] = q < n_chunks ? __ldg(w4 + (int64_t)q * (kChunk * DH / 4) + tid + 32 * kLoadWarps * i)
-                                : make_float4(0.f, 0.f, 0.f, 0.f);
+            if (q < n_chunks) v[i] = load_stream(w4 + (int64_t)q * (kChunk * DH / 4) + tid + 32 * kLoadWarps * i);
     };
     if (warp < kLoadWarps) {
 #pragma unroll
