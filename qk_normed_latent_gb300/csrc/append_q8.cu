@@ -159,10 +159,13 @@ using namespace tc;
 using dec::wait_bounded;
 
 constexpr int kMT = 128;          // rows of the MMA: tokens of a CTA, at most
-constexpr int kLoadWarps = 8, kEpiWarps = 4;
-constexpr int kTcThreads = 32 * (kLoadWarps + kEpiWarps + 1);
+constexpr int kLoadWarps = 8;     // of a set; two sets take the chunks of W^K in turn (a set's chunk costs it
+constexpr int kSets = 2;          // ~700 cycles of dependent instructions, the MMAs 256)
+constexpr int kEpiWarps = 4;
+constexpr int kMmaWarp = kSets * kLoadWarps + kEpiWarps;
+constexpr int kTcThreads = 32 * (kMmaWarp + 1);
 constexpr int kChunk = 32;        // rows of W^K per ring stage
-constexpr int kAhead = 4;         // chunks of W^K in flight in registers
+constexpr int kAhead = 2;         // chunks of a set in flight in registers
 
 template <int DC, int DH>
 struct AppendLayout {
@@ -234,28 +237,29 @@ __global__ void __launch_bounds__(kTcThreads, 1) append_q8_tc_kernel(const Appen
         fence_barrier_init();
     }
     if (p.positions && tid < p.d_r / 2) freq[tid] = rope_freq(p.theta, tid, p.d_r);
-    if (warp == kLoadWarps + kEpiWarps) {
+    if (warp == kMmaWarp) {
         tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
     }
     // W^K: the loads of the first chunks go out before anything else (no kernel of the library writes it)
     const float4* w4 = reinterpret_cast<const float4*>(p.wk + (int64_t)g0 * DC * DH);
+    const int set = warp / kLoadWarps, st = tid % (32 * kLoadWarps);   // loader set, thread in it
     float4 wv[kAhead][kF4];
     auto fetch = [&](int q, float4 (&v)[kF4]) {
 #pragma unroll
         for (int i = 0; i < kF4; ++i)
-            if (q < n_chunks) v[i] = load_stream(w4 + (int64_t)q * (kChunk * DH / 4) + tid + 32 * kLoadWarps * i);
+            if (q < n_chunks) v[i] = load_stream(w4 + (int64_t)q * (kChunk * DH / 4) + st + 32 * kLoadWarps * i);
     };
-    if (warp < kLoadWarps) {
+    if (warp < kSets * kLoadWarps) {
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) fetch(u, wv[u]);
+        for (int u = 0; u < kAhead; ++u) fetch(u * kSets + set, wv[u]);
     }
     __syncthreads();                                           // freq, barriers
     pdl_wait();                                                // the cache writes follow the previous kernel
     pdl_trigger();
 
     // ---- quantise: a warp per token, two tokens' loads at a time ----
-    constexpr int kQWarps = kLoadWarps + kEpiWarps;
+    constexpr int kQWarps = kMmaWarp;
     if (warp < kQWarps) {
         for (int t0 = warp; t0 < n_tok; t0 += 2 * kQWarps) {
             float4 v[2][kV];
@@ -345,22 +349,21 @@ __global__ void __launch_bounds__(kTcThreads, 1) append_q8_tc_kernel(const Appen
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
-    if (warp < kLoadWarps) {
+    if (warp < kSets * kLoadWarps) {
         // ===================== W^K chunks: fp32 registers -> hi and lo bf16 =====================
         bool ok = true;
-        for (int q0 = 0; q0 < n_chunks && ok; q0 += kAhead) {
+        for (int q0 = set; q0 < n_chunks && ok; q0 += kAhead * kSets) {
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
-                const int q = q0 + u;
+                const int q = q0 + u * kSets;
                 if (q >= n_chunks) break;
                 const int s = q % NST;
-                if (q >= NST) ok = wait_bounded(&bempty[s], ((q / NST) - 1) & 1, p.status);
-                ok = __all_sync(0xffffffffu, ok && !*(volatile int*)abort_flag);
+                if (q >= NST) ok = __all_sync(0xffffffffu, wait_bounded(&bempty[s], ((q / NST) - 1) & 1, p.status));
                 if (!ok) break;
                 uint8_t* stg = sm + LY::kA + s * LY::kStage;
 #pragma unroll
                 for (int i = 0; i < kF4; ++i) {
-                    const int f = tid + 32 * kLoadWarps * i;
+                    const int f = st + 32 * kLoadWarps * i;
                     const int k = f / (DH / 4), jc = 4 * (f % (DH / 4));
                     const float4 w = wv[u][i];
                     const __nv_bfloat162 h01 = __floats2bfloat162_rn(w.x, w.y), h23 = __floats2bfloat162_rn(w.z, w.w);
@@ -379,11 +382,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) append_q8_tc_kernel(const Appen
                 // the fence to the async proxy is the MMA thread's: here it would wait for the loads in flight
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bfull[s]);
-                fetch(q + kAhead, wv[u]);
+                fetch(q + kAhead * kSets, wv[u]);
             }
         }
         if (!ok) *(volatile int*)abort_flag = 1;
-    } else if (warp == kLoadWarps + kEpiWarps) {
+    } else if (warp == kMmaWarp) {
         // ===================== MMA issuer =====================
         if (lane == 0) {
             const uint32_t id = idesc_bf16(kMT, LY::kN, 0, 1);
@@ -449,7 +452,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) append_q8_tc_kernel(const Appen
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (warp == kLoadWarps + kEpiWarps) {
+    if (warp == kMmaWarp) {
         __syncwarp();
         tc_fence_after();
         tmem_dealloc(tmem, 512);

@@ -52,11 +52,11 @@ __device__ __forceinline__ float e4m3_to_float(uint8_t v) {
 // every later product with s exact.
 __device__ __forceinline__ float e4m3_scale(float top, float* inv) {
     if (!(top > 0.f)) { *inv = 0.f; return 0.f; }
-    int k;
-    const float m = frexpf(fminf(top, 3.402823466e38f), &k);   // top = m 2^k, 0.5 <= m < 1
-    const int e = max(k - (m <= 0.875f ? 9 : 8), -126);
-    *inv = ldexpf(1.f, -e);
-    return ldexpf(1.f, e);
+    // top = 1.f x 2^(E - 127), so 2^(E - 135) <= top / 256 and one more binade above 1.75 2^(E - 127)
+    const int b = __float_as_int(fminf(top, 3.402823466e38f));
+    const int e = max((b >> 23) - 135 + ((b & 0x7fffff) > 0x600000 ? 1 : 0), -126);
+    *inv = __int_as_float((127 - e) << 23);
+    return __int_as_float((127 + e) << 23);
 }
 // Code of c with the scale 1 / inv; a value that is not finite becomes NaN.
 __device__ __forceinline__ uint8_t e4m3_code(float c, float inv) {

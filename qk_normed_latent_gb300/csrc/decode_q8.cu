@@ -196,7 +196,7 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
     float* inv_s = corr_s + ROWS;            // epilogue: 1 / (f l)
     float* red_s = inv_s + ROWS;             // [2 kinds][4 warps][ROWS]
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;   // warp: uniform
     WorkItem it;
     int seq_len;
     if (p.sched_inline) {
@@ -398,7 +398,8 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
         }
     } else if (warp == 1) {
         // ===================== logit MMAs =====================
-        if (lane == 0) {
+        {
+            const uint32_t lead = lane == 0 ? 1u : 0u;
             const uint32_t id_s = idesc_e4m3(kT, N, 0, 0);
             const uint32_t id_r = idesc_bf16(kT, N, 0, 0);
             constexpr uint32_t sw = DR == 64 ? kSwizzle128B : kSwizzle64B, sbo = DR == 64 ? 1024 : 512;
@@ -414,29 +415,30 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
                 const uint64_t lat = st_lat + (uint64_t)(s * (LY::kStage >> 4)), rope = st_rope + (uint64_t)(s * (LY::kStage >> 4));
                 const uint32_t d = tmem + (uint32_t)(j % NSB) * (2 * N);
                 if (j >= NSB) ok = wait_bounded(&sfree[j % NSB], ((j / NSB) - 1) & 1, p.status);
-                ok = ok && wait_bounded(&full[s], (j / NST) & 1, p.status) && !*(volatile int*)abort_flag;
+                ok = __all_sync(0xffffffffu, ok && wait_bounded(&full[s], (j / NST) & 1, p.status) && !*(volatile int*)abort_flag);
                 if (!ok) break;
                 tc_fence_after();
 #pragma unroll
                 for (int blk = 0; blk < KB; ++blk)
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        mma_f8(d, lat + (uint64_t)((blk * 1024 + kk * 32) >> 4), q_lat + (uint64_t)((blk * (N * 128) + kk * 32) >> 4),
+                        mma_f8_if(lead, d, lat + (uint64_t)((blk * 1024 + kk * 32) >> 4), q_lat + (uint64_t)((blk * (N * 128) + kk * 32) >> 4),
                                id_s, (blk > 0 || kk > 0) ? 1u : 0u);
 #pragma unroll
                 for (int kk = 0; kk < DR / 16; ++kk)
-                    mma_bf16(d + N, rope + (uint64_t)(kk * 2), q_rope + (uint64_t)(kk * 2), id_r, kk > 0 ? 1u : 0u);
-                mma_commit(&sfull[j % NSB]);
+                    mma_bf16_if(lead, d + N, rope + (uint64_t)(kk * 2), q_rope + (uint64_t)(kk * 2), id_r, kk > 0 ? 1u : 0u);
+                mma_commit_if(lead, &sfull[j % NSB]);
             }
             if (!ok) {                       // no exit with an MMA in flight
                 *(volatile int*)abort_flag = 1;
-                mma_commit(&drain[0]);
+                mma_commit_if(lead, &drain[0]);
                 wait_bounded(&drain[0], 0, p.status);
             }
         }
     } else if (warp == 2) {
         // ===================== output MMAs (a thread of their own: neither issue waits for the other's data) ==========
-        if (lane == 0) {
+        {
+            const uint32_t lead = lane == 0 ? 1u : 0u;
             const uint32_t id_o = idesc_e4m3(128, LY::kON, 1, 1);
             // A: a chunk's 128 latents x 32 tokens, MN-major (8-token groups kGroup apart).  B: P, MN-major:
             // a token's codes in as many bytes (swizzle of the same width), 8-token groups kPGroup apart.
@@ -448,7 +450,7 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
             for (int j = 0; j < n_t && ok; ++j) {
                 const int s = j % NST;
                 const uint64_t lat = st_lat + (uint64_t)(s * (LY::kStage >> 4)), pw = st_p + (uint64_t)(s * (LY::kStage >> 4));
-                ok = wait_bounded(&pfull[s], (j / NST) & 1, p.status) && !*(volatile int*)abort_flag;
+                ok = __all_sync(0xffffffffu, wait_bounded(&pfull[s], (j / NST) & 1, p.status) && !*(volatile int*)abort_flag);
                 if (!ok) break;
                 tc_fence_after();
 #pragma unroll
@@ -457,15 +459,15 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
                     for (int kk = 0; kk < kT / 32; ++kk)
 #pragma unroll
                         for (int part = 0; part < (LY::kStacked ? 1 : 2); ++part)
-                            mma_f8(tmem + LY::kColO + c * PN, lat + (uint64_t)((c * 1024 + kk * 4 * LY::kGroup) >> 4),
+                            mma_f8_if(lead, tmem + LY::kColO + c * PN, lat + (uint64_t)((c * 1024 + kk * 4 * LY::kGroup) >> 4),
                                    pw + (uint64_t)((kk * 4 * LY::kPGroup + part * 8 * PN) >> 4), id_o,
                                    (j > 0 || kk > 0 || part > 0) ? 1u : 0u);
-                mma_commit(&empty[s]);
-                mma_commit(&odone[s]);
+                mma_commit_if(lead, &empty[s]);
+                mma_commit_if(lead, &odone[s]);
             }
             if (!ok) {
                 *(volatile int*)abort_flag = 1;
-                mma_commit(&drain[1]);
+                mma_commit_if(lead, &drain[1]);
                 wait_bounded(&drain[1], 0, p.status);
             }
         }
