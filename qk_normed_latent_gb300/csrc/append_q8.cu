@@ -215,10 +215,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) append_q8_tc_kernel(const Appen
     uint64_t* dfree = dfull + 2;                               // [2] read -> MMA
     uint64_t* drain = dfree + 2;
     uint32_t* tmem_slot = (uint32_t*)(drain + 1);
-    int* abort_flag = (int*)(tmem_slot + 1);
     float* scale_s = (float*)(tmem_slot + 4);
     __shared__ RopeFreq freq[32];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;   // warp: uniform
     const int n0 = blockIdx.x * p.tokens, n_tok = min(p.tokens, p.N - n0);
     const int g0 = blockIdx.y * p.groups, n_g = min(p.groups, p.G - g0);
     const int n_chunks = n_g * (DC / kChunk);
@@ -233,7 +232,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) append_q8_tc_kernel(const Appen
             mbar_init(&dfree[i], kEpiWarps);
         }
         mbar_init(drain, 1);
-        *abort_flag = 0;
         fence_barrier_init();
     }
     if (p.positions && tid < p.d_r / 2) freq[tid] = rope_freq(p.theta, tid, p.d_r);
@@ -258,87 +256,96 @@ __global__ void __launch_bounds__(kTcThreads, 1) append_q8_tc_kernel(const Appen
     pdl_wait();                                                // the cache writes follow the previous kernel
     pdl_trigger();
 
-    // ---- quantise: a warp per token, two tokens' loads at a time ----
+    // ---- quantise: a warp per token, the next token's loads in flight ----
     constexpr int kQWarps = kMmaWarp;
     if (warp < kQWarps) {
-        for (int t0 = warp; t0 < n_tok; t0 += 2 * kQWarps) {
-            float4 v[2][kV];
-            float rv[2][2];
-            int64_t slot[2];
+        const bool store_cache = g0 == 0;
+        float gr[2];                                           // d_r <= 64: elements lane and lane + 32
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int tl = t0 + i * kQWarps;
-                const bool on = tl < n_tok;
-                const float4* src = reinterpret_cast<const float4*>(p.c_new + (int64_t)(n0 + tl) * DC);
+        for (int u = 0; u < 2; ++u) {
+            const int jj = lane + 32 * u;
+            gr[u] = (jj < p.d_r && p.grk && !p.plain) ? p.grk[jj] : 1.f;
+        }
+        float4 v[kV];
+        float rv[2];
+        int64_t slot = -1;
+        int pos = 0;
+        auto load = [&](int tl) {
+            const bool on = tl < n_tok;
+            const float4* src = reinterpret_cast<const float4*>(p.c_new + (int64_t)(n0 + tl) * DC);
 #pragma unroll
-                for (int k = 0; k < kV; ++k) v[i][k] = on ? __ldg(src + 32 * k + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
-                slot[i] = (on && g0 == 0) ? p.slots[n0 + tl] : -1;
+            for (int k = 0; k < kV; ++k)
+                if (on) v[k] = load_stream(src + 32 * k + lane);
+            slot = (on && store_cache) ? p.slots[n0 + tl] : -1;
+            pos = (on && store_cache && p.positions) ? p.positions[n0 + tl] : 0;
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {                  // d_r <= 64: elements lane and lane + 32
-                    const int jj = lane + 32 * u;
-                    rv[i][u] = (on && g0 == 0 && jj < p.d_r) ? p.r_new[(int64_t)(n0 + tl) * p.d_r + jj] : 0.f;
-                }
+            for (int u = 0; u < 2; ++u) {
+                const int jj = lane + 32 * u;
+                rv[u] = (on && store_cache && jj < p.d_r) ? p.r_new[(int64_t)(n0 + tl) * p.d_r + jj] : 0.f;
             }
+        };
+        load(warp);
+        for (int tl = warp; tl < n_tok; tl += kQWarps) {
+            float4 x4[kV];
+            float r2[2] = {rv[0], rv[1]};
+            const int64_t at = slot;
+            const int turn = pos;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int tl = t0 + i * kQWarps;
-                if (tl >= n_tok) break;                        // uniform over the warp
-                float top = 0.f;
+            for (int k = 0; k < kV; ++k) x4[k] = v[k];
+            load(tl + kQWarps);
+            float top = 0.f;
 #pragma unroll
-                for (int k = 0; k < kV; ++k)
-                    top = fmaxf(top, fmaxf(fmaxf(fabsf(v[i][k].x), fabsf(v[i][k].y)), fmaxf(fabsf(v[i][k].z), fabsf(v[i][k].w))));
-                top = warp_max(top);
-                float inv;
-                const float s = e4m3_scale(top, &inv);
-                const bool store = slot[i] >= 0 && slot[i] < p.num_slots;
-                uint8_t* row = p.kv + slot[i] * (int64_t)(DC + 2 * p.d_r);
+            for (int k = 0; k < kV; ++k)
+                top = fmaxf(top, fmaxf(fmaxf(fabsf(x4[k].x), fabsf(x4[k].y)), fmaxf(fabsf(x4[k].z), fabsf(x4[k].w))));
+            top = warp_max(top);
+            float inv;
+            const float s = e4m3_scale(top, &inv);
+            const bool store = at >= 0 && at < p.num_slots;
+            uint8_t* row = p.kv + at * (int64_t)(DC + 2 * p.d_r);
 #pragma unroll
-                for (int k = 0; k < kV; ++k) {
-                    float x[4] = {v[i][k].x, v[i][k].y, v[i][k].z, v[i][k].w};
-                    if (isinf(top)) {                          // an infinity is stored as NaN, not saturated
+            for (int k = 0; k < kV; ++k) {
+                float x[4] = {x4[k].x, x4[k].y, x4[k].z, x4[k].w};
+                if (isinf(top)) {                              // an infinity is stored as NaN, not saturated
 #pragma unroll
-                        for (int u = 0; u < 4; ++u) x[u] = isinf(x[u]) ? __int_as_float(0x7fffffff) : x[u];
-                    }
-                    const uint32_t c01 = __nv_cvt_float2_to_fp8x2(make_float2(x[0] * inv, x[1] * inv), __NV_SATFINITE, __NV_E4M3);
-                    const uint32_t c23 = __nv_cvt_float2_to_fp8x2(make_float2(x[2] * inv, x[3] * inv), __NV_SATFINITE, __NV_E4M3);
-                    const float2 f01 = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)c01, __NV_E4M3)));
-                    const float2 f23 = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)c23, __NV_E4M3)));
-                    const __nv_bfloat162 b01 = __floats2bfloat162_rn(f01.x, f01.y), b23 = __floats2bfloat162_rn(f23.x, f23.y);
-                    const int col = 128 * k + 4 * lane;
-                    uint2 w;
-                    w.x = *reinterpret_cast<const uint32_t*>(&b01);
-                    w.y = *reinterpret_cast<const uint32_t*>(&b23);
-                    *reinterpret_cast<uint2*>(sm + (col >> 6) * (kMT * 128) + sw128_offset(tl, col & 63)) = w;
-                    if (store) *reinterpret_cast<uint32_t*>(row + col) = c01 | (c23 << 16);
+                    for (int u = 0; u < 4; ++u) x[u] = isinf(x[u]) ? __int_as_float(0x7fffffff) : x[u];
                 }
-                if (lane == 0) {
-                    scale_s[tl] = s;
-                    if (store) p.kv_scale[slot[i]] = s;
-                }
-                if (g0 == 0) {                                 // the RoPE key: rotated, then normalised on its own
-                    if (p.positions) {
-                        const int pos = p.positions[n0 + tl];
-#pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            const int jj = lane + 32 * u;
-                            const float w = __shfl_xor_sync(0xffffffffu, rv[i][u], 1);
-                            if (jj < p.d_r) {
-                                float c, sn;
-                                rope_cos_sin(pos, freq[jj >> 1], &c, &sn);
-                                rv[i][u] = rope_apply(jj, rv[i][u], w, c, sn);
-                            }
-                        }
-                    }
-                    const float ss = warp_sum(fmaf(rv[i][0], rv[i][0], rv[i][1] * rv[i][1]));
-                    const float beta = p.plain ? 1.f : 1.f / sqrtf(ss / (float)p.d_r + p.eps);
-                    __nv_bfloat16* rope = reinterpret_cast<__nv_bfloat16*>(row + DC);
+                const uint32_t c01 = __nv_cvt_float2_to_fp8x2(make_float2(x[0] * inv, x[1] * inv), __NV_SATFINITE, __NV_E4M3);
+                const uint32_t c23 = __nv_cvt_float2_to_fp8x2(make_float2(x[2] * inv, x[3] * inv), __NV_SATFINITE, __NV_E4M3);
+                const float2 f01 = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)c01, __NV_E4M3)));
+                const float2 f23 = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)c23, __NV_E4M3)));
+                const __nv_bfloat162 b01 = __floats2bfloat162_rn(f01.x, f01.y), b23 = __floats2bfloat162_rn(f23.x, f23.y);
+                const int col = 128 * k + 4 * lane;
+                uint2 w;
+                w.x = *reinterpret_cast<const uint32_t*>(&b01);
+                w.y = *reinterpret_cast<const uint32_t*>(&b23);
+                *reinterpret_cast<uint2*>(sm + (col >> 6) * (kMT * 128) + sw128_offset(tl, col & 63)) = w;
+                if (store) *reinterpret_cast<uint32_t*>(row + col) = c01 | (c23 << 16);
+            }
+            if (lane == 0) {
+                scale_s[tl] = s;
+                if (store) p.kv_scale[at] = s;
+                if (at >= p.num_slots) report(p.status, QKMLA_ERR_DEVICE_BOUNDS);
+            }
+            if (store_cache) {                                 // the RoPE key: rotated, then normalised on its own
+                if (p.positions) {
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
                         const int jj = lane + 32 * u;
-                        if (store && jj < p.d_r)
-                            rope[jj] = __float2bfloat16_rn(p.plain ? rv[i][u] : rv[i][u] * (p.grk ? p.grk[jj] : 1.f) * beta);
+                        const float w = __shfl_xor_sync(0xffffffffu, r2[u], 1);
+                        if (jj < p.d_r) {
+                            float c, sn;
+                            rope_cos_sin(turn, freq[jj >> 1], &c, &sn);
+                            r2[u] = rope_apply(jj, r2[u], w, c, sn);
+                        }
                     }
-                    if (lane == 0 && slot[i] >= p.num_slots) report(p.status, QKMLA_ERR_DEVICE_BOUNDS);
+                }
+                const float ss = warp_sum(fmaf(r2[0], r2[0], r2[1] * r2[1]));
+                const float beta = p.plain ? 1.f : 1.f / sqrtf(ss / (float)p.d_r + p.eps);
+                __nv_bfloat16* rope = reinterpret_cast<__nv_bfloat16*>(row + DC);
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int jj = lane + 32 * u;
+                    if (store && jj < p.d_r) rope[jj] = __float2bfloat16_rn(r2[u] * gr[u] * beta);
                 }
             }
         }
@@ -385,37 +392,39 @@ __global__ void __launch_bounds__(kTcThreads, 1) append_q8_tc_kernel(const Appen
                 fetch(q + kAhead * kSets, wv[u]);
             }
         }
-        if (!ok) *(volatile int*)abort_flag = 1;
     } else if (warp == kMmaWarp) {
-        // ===================== MMA issuer =====================
-        if (lane == 0) {
-            const uint32_t id = idesc_bf16(kMT, LY::kN, 0, 1);
-            const uint64_t a0 = smem_desc(smem_u32(sm), 16, 1024, kSwizzle128B);
-            const uint64_t b0 = smem_desc(smem_u32(sm + LY::kA), kChunk * 128, 1024, kSwizzle128B);
-            bool ok = true;
-            int q = 0;
-            for (int gi = 0; gi < n_g && ok; ++gi) {
-                const uint32_t d = tmem + (uint32_t)(gi & 1) * 256u;
-                if (gi >= 2) ok = wait_bounded(&dfree[gi & 1], ((gi >> 1) - 1) & 1, p.status);
-                for (int c = 0; c < DC / kChunk && ok; ++c, ++q) {
-                    const int s = q % NST;
-                    ok = wait_bounded(&bfull[s], (q / NST) & 1, p.status) && !*(volatile int*)abort_flag;
-                    if (!ok) break;
-                    fence_proxy_async_smem();                  // the loaders' writes, seen through the barrier
-                    tc_fence_after();
-                    const uint64_t a = a0 + (uint64_t)(((c >> 1) * (kMT * 128) + (c & 1) * 64) >> 4);
-                    const uint64_t bd = b0 + (uint64_t)(s * (LY::kStage >> 4));
+        // ===================== MMA issuer (uniform control flow, one lane's instructions) =====================
+        const uint32_t lead = lane == 0 ? 1u : 0u;
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        const int groups = __shfl_sync(0xffffffffu, n_g, 0);
+        const uint32_t id = idesc_bf16(kMT, LY::kN, 0, 1);
+        const uint64_t a0 = smem_desc(smem_u32(sm), 16, 1024, kSwizzle128B);
+        const uint64_t b0 = smem_desc(smem_u32(sm + LY::kA), kChunk * 128, 1024, kSwizzle128B);
+        bool ok = true;
+        int s = 0;
+        uint32_t phase = 0;
+        for (int gi = 0; gi < groups && ok; ++gi) {
+            const uint32_t d = tm + (uint32_t)(gi & 1) * 256u;
+            bool got = true;
+            if (gi >= 2) got = wait_bounded(&dfree[gi & 1], ((gi >> 1) - 1) & 1, p.status);
+#pragma unroll 4
+            for (int c = 0; c < DC / kChunk; ++c) {
+                got = got && wait_bounded(&bfull[s], phase, p.status);
+                if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
+                fence_proxy_async_smem();                      // the loaders' writes, seen through the barrier
+                tc_fence_after();
+                const uint64_t a = a0 + (uint64_t)(((c >> 1) * (kMT * 128) + (c & 1) * 64) >> 4);
+                const uint64_t bd = b0 + (uint64_t)(s * (LY::kStage >> 4));
 #pragma unroll
-                    for (int kk = 0; kk < kChunk / 16; ++kk)
-                        mma_bf16(d, a + (uint64_t)(kk * 2), bd + (uint64_t)(kk * 128), id, (c > 0 || kk > 0) ? 1u : 0u);
-                    mma_commit(&bempty[s]);
-                }
-                if (ok) mma_commit(&dfull[gi & 1]);
+                for (int kk = 0; kk < kChunk / 16; ++kk)
+                    mma_bf16_if(lead, d, a + (uint64_t)(kk * 2), bd + (uint64_t)(kk * 128), id, (c > 0 || kk > 0) ? 1u : 0u);
+                mma_commit_if(lead, &bempty[s]);
+                if (++s == NST) { s = 0; phase ^= 1; }
             }
-            if (!ok) *(volatile int*)abort_flag = 1;
-            mma_commit(drain);                                 // no exit with an MMA in flight
-            wait_bounded(drain, 0, p.status);
+            if (ok) mma_commit_if(lead, &dfull[gi & 1]);
         }
+        mma_commit_if(lead, drain);                            // no exit with an MMA in flight
+        wait_bounded(drain, 0, p.status);
     } else {
         // ===================== epilogue: thread = token =====================
         const int sub = warp & 3, tl = 32 * sub + lane;
@@ -425,7 +434,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) append_q8_tc_kernel(const Appen
         const float s = on ? scale_s[tl] : 0.f;
         for (int gi = 0; gi < n_g; ++gi) {
             const bool got = __all_sync(0xffffffffu, wait_bounded(&dfull[gi & 1], (gi >> 1) & 1, p.status));
-            if (!got) { *(volatile int*)abort_flag = 1; break; }
+            if (!got) break;
             tc_fence_after();
             const uint32_t d = tmem + (uint32_t)(gi & 1) * 256u + lane_base;
             float ss[4] = {0.f, 0.f, 0.f, 0.f};
