@@ -172,10 +172,10 @@ struct AppendLayout {
     static constexpr int kN = 2 * DH;                          // hi and lo columns
     static constexpr int kA = DC / 64 * kMT * 128;             // bf16, K-major, 128-byte swizzle
     static constexpr int kStage = kChunk * kN * 2;             // bf16, MN-major: kN / 64 atoms of 64 columns
-    static constexpr int kNst = std::min(8, (232448 - kA - 4096) / kStage);
+    static constexpr int kNst = 4;                              // divides the chunks of a group: slots are constants
     static constexpr int kOffMisc = kA + kNst * kStage;
     static constexpr int kBytes = kOffMisc + (2 * kNst + 5) * 8 + 16 + kMT * 4 + 1024;
-    static_assert(kNst >= 4 && kBytes <= 232448, "shared memory budget");
+    static_assert(DC / kChunk % kNst == 0 && kBytes <= 232448, "shared memory budget");
 };
 
 struct AppendQ8Params {
@@ -401,25 +401,28 @@ __global__ void __launch_bounds__(kTcThreads, 1) append_q8_tc_kernel(const Appen
         const uint64_t a0 = smem_desc(smem_u32(sm), 16, 1024, kSwizzle128B);
         const uint64_t b0 = smem_desc(smem_u32(sm + LY::kA), kChunk * 128, 1024, kSwizzle128B);
         bool ok = true;
-        int s = 0;
         uint32_t phase = 0;
         for (int gi = 0; gi < groups && ok; ++gi) {
             const uint32_t d = tm + (uint32_t)(gi & 1) * 256u;
             bool got = true;
             if (gi >= 2) got = wait_bounded(&dfree[gi & 1], ((gi >> 1) - 1) & 1, p.status);
-#pragma unroll 4
-            for (int c = 0; c < DC / kChunk; ++c) {
-                got = got && wait_bounded(&bfull[s], phase, p.status);
-                if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
-                fence_proxy_async_smem();                      // the loaders' writes, seen through the barrier
-                tc_fence_after();
-                const uint64_t a = a0 + (uint64_t)(((c >> 1) * (kMT * 128) + (c & 1) * 64) >> 4);
-                const uint64_t bd = b0 + (uint64_t)(s * (LY::kStage >> 4));
+            for (int c4 = 0; c4 < DC / kChunk; c4 += NST, phase ^= 1) {
 #pragma unroll
-                for (int kk = 0; kk < kChunk / 16; ++kk)
-                    mma_bf16_if(lead, d, a + (uint64_t)(kk * 2), bd + (uint64_t)(kk * 128), id, (c > 0 || kk > 0) ? 1u : 0u);
-                mma_commit_if(lead, &bempty[s]);
-                if (++s == NST) { s = 0; phase ^= 1; }
+                for (int s = 0; s < NST; s += 2) {             // two chunks a fence
+                    got = got && wait_bounded(&bfull[s], phase, p.status) && wait_bounded(&bfull[s + 1], phase, p.status);
+                    if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
+                    fence_proxy_async_smem();                  // the loaders' writes, seen through the barriers
+                    tc_fence_after();
+                    const uint64_t a = a0 + (uint64_t)(((c4 + s) >> 1) * (kMT * 128 >> 4));
+#pragma unroll
+                    for (int kk = 0; kk < 2 * kChunk / 16; ++kk) {
+                        mma_bf16_if(lead, d, a + (uint64_t)(kk * 2),
+                                    b0 + (uint64_t)(((s + (kk >> 1)) * LY::kStage + (kk & 1) * 2048) >> 4), id,
+                                    (c4 > 0 || s > 0 || kk > 0) ? 1u : 0u);
+                        if (kk & 1) mma_commit_if(lead, &bempty[s + (kk >> 1)]);
+                    }
+                }
+                if (!ok) break;
             }
             if (ok) mma_commit_if(lead, &dfull[gi & 1]);
         }
