@@ -394,7 +394,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) append_q8_tc_kernel(const Appen
         }
     } else if (warp == kMmaWarp) {
         // ===================== MMA issuer (uniform control flow, one lane's instructions) =====================
-        const uint32_t lead = lane == 0 ? 1u : 0u;
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
         const int groups = __shfl_sync(0xffffffffu, n_g, 0);
         const uint32_t id = idesc_bf16(kMT, LY::kN, 0, 1);
@@ -414,19 +413,24 @@ __global__ void __launch_bounds__(kTcThreads, 1) append_q8_tc_kernel(const Appen
                     fence_proxy_async_smem();                  // the loaders' writes, seen through the barriers
                     tc_fence_after();
                     const uint64_t a = a0 + (uint64_t)(((c4 + s) >> 1) * (kMT * 128 >> 4));
+                    if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < 2 * kChunk / 16; ++kk) {
-                        mma_bf16_if(lead, d, a + (uint64_t)(kk * 2),
+                        mma_bf16(d, a + (uint64_t)(kk * 2),
                                     b0 + (uint64_t)(((s + (kk >> 1)) * LY::kStage + (kk & 1) * 2048) >> 4), id,
                                     (c4 > 0 || s > 0 || kk > 0) ? 1u : 0u);
-                        if (kk & 1) mma_commit_if(lead, &bempty[s + (kk >> 1)]);
+                        if (kk & 1) mma_commit(&bempty[s + (kk >> 1)]);
                     }
+                    }
+                    __syncwarp();
                 }
                 if (!ok) break;
             }
-            if (ok) mma_commit_if(lead, &dfull[gi & 1]);
+            if (ok && elect_one()) mma_commit(&dfull[gi & 1]);
+            __syncwarp();
         }
-        mma_commit_if(lead, drain);                            // no exit with an MMA in flight
+        if (elect_one()) mma_commit(drain);
+        __syncwarp();                            // no exit with an MMA in flight
         wait_bounded(drain, 0, p.status);
     } else {
         // ===================== epilogue: thread = token =====================

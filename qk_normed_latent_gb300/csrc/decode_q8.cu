@@ -399,7 +399,6 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
     } else if (warp == 1) {
         // ===================== logit MMAs =====================
         {
-            const uint32_t lead = lane == 0 ? 1u : 0u;
             const int nt = __shfl_sync(0xffffffffu, n_t, 0);              // uniform to the compiler, like tm
             const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
             const uint32_t id_s = idesc_e4m3(kT, N, 0, 0);
@@ -421,27 +420,29 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
                 got = got && wait_bounded(&full[s], (j / NST) & 1, p.status) && !*(volatile int*)abort_flag;
                 if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
                 tc_fence_after();
+                if (elect_one()) {
 #pragma unroll
                 for (int blk = 0; blk < KB; ++blk)
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        mma_f8_if(lead, d, lat + (uint64_t)((blk * 1024 + kk * 32) >> 4), q_lat + (uint64_t)((blk * (N * 128) + kk * 32) >> 4),
+                        mma_f8(d, lat + (uint64_t)((blk * 1024 + kk * 32) >> 4), q_lat + (uint64_t)((blk * (N * 128) + kk * 32) >> 4),
                                id_s, (blk > 0 || kk > 0) ? 1u : 0u);
 #pragma unroll
                 for (int kk = 0; kk < DR / 16; ++kk)
-                    mma_bf16_if(lead, d + N, rope + (uint64_t)(kk * 2), q_rope + (uint64_t)(kk * 2), id_r, kk > 0 ? 1u : 0u);
-                mma_commit_if(lead, &sfull[j % NSB]);
+                    mma_bf16(d + N, rope + (uint64_t)(kk * 2), q_rope + (uint64_t)(kk * 2), id_r, kk > 0 ? 1u : 0u);
+                mma_commit(&sfull[j % NSB]);
+                }
+                __syncwarp();
             }
             if (!ok) {                       // no exit with an MMA in flight
                 *(volatile int*)abort_flag = 1;
-                mma_commit_if(lead, &drain[0]);
+                if (elect_one()) mma_commit(&drain[0]);
                 wait_bounded(&drain[0], 0, p.status);
             }
         }
     } else if (warp == 2) {
         // ===================== output MMAs (a thread of their own: neither issue waits for the other's data) ==========
         {
-            const uint32_t lead = lane == 0 ? 1u : 0u;
             const int nt = __shfl_sync(0xffffffffu, n_t, 0);              // uniform to the compiler, like tm
             const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
             const uint32_t id_o = idesc_e4m3(128, LY::kON, 1, 1);
@@ -458,21 +459,24 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
                 const bool got = wait_bounded(&pfull[s], (j / NST) & 1, p.status) && !*(volatile int*)abort_flag;
                 if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
                 tc_fence_after();
+                if (elect_one()) {
 #pragma unroll
                 for (int c = 0; c < KB; ++c)
 #pragma unroll
                     for (int kk = 0; kk < kT / 32; ++kk)
 #pragma unroll
                         for (int part = 0; part < (LY::kStacked ? 1 : 2); ++part)
-                            mma_f8_if(lead, tm + LY::kColO + c * PN, lat + (uint64_t)((c * 1024 + kk * 4 * LY::kGroup) >> 4),
+                            mma_f8(tm + LY::kColO + c * PN, lat + (uint64_t)((c * 1024 + kk * 4 * LY::kGroup) >> 4),
                                    pw + (uint64_t)((kk * 4 * LY::kPGroup + part * 8 * PN) >> 4), id_o,
                                    (j > 0 || kk > 0 || part > 0) ? 1u : 0u);
-                mma_commit_if(lead, &empty[s]);
-                mma_commit_if(lead, &odone[s]);
+                mma_commit(&empty[s]);
+                mma_commit(&odone[s]);
+                }
+                __syncwarp();
             }
             if (!ok) {
                 *(volatile int*)abort_flag = 1;
-                mma_commit_if(lead, &drain[1]);
+                if (elect_one()) mma_commit(&drain[1]);
                 wait_bounded(&drain[1], 0, p.status);
             }
         }
