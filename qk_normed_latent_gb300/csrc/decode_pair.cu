@@ -239,7 +239,7 @@ decode_pair_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_cons
             if ((j & 31) == 0 && j > 0) slot_batch = slot_of_tile(j + lane);
             const int slot0 = __shfl_sync(0xffffffffu, slot_batch, j & 31);
             int go = 1;
-            if (lane == 0) {
+            if (elect_one()) {
                 const int s = j % kNst;
                 if (j >= kNst && !wait_bounded(&empty[s], ((j / kNst) - 1) & 1, p.status)) {
                     *abort_flag = 1;
@@ -258,11 +258,11 @@ decode_pair_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_cons
                                   ak_bytes, &full[s]);
                 }
             }
-            if (!__shfl_sync(0xffffffffu, go, 0)) break;
+            if (!__all_sync(0xffffffffu, go)) break;
         }
     } else if (warp == 1) {
         // ===================== MMA issuer: S(j) and O(j) in readiness order =====================
-        if (lane == 0) {
+        if (elect_one()) {
             const uint32_t id_s = idesc_bf16(kR, kT, 0, 0);
             const uint32_t id_o = idesc_bf16(kR, kHalfLat, 0, 1);
             const uint32_t q_addr = smem_u32(sQ);

@@ -239,7 +239,7 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
     pdl_wait();
     pdl_trigger();
 
-    // ---- TMA producer (warp 0): the lanes look up the slots of 32 pieces ahead, lane 0 loads them ----
+    // ---- TMA producer (warp 0): the lanes look up the slots of 32 pieces ahead, one loads them ----
     const int n_pieces = kT / p.piece;
     const uint32_t ak_row = p.plain ? 0u : (uint32_t)(p.G * (p.ak_f16 ? 2 : 4));
     const uint32_t piece_bytes = (uint32_t)p.piece * (DC + 2 * DR + 4 + ak_row);
@@ -267,7 +267,7 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
 #pragma unroll
         for (int q = 0; q < 4; ++q) slots[q] = __shfl_sync(0xffffffffu, lane_slot, k * n_pieces + q);
     };
-    auto issue_tile = [&](int j) {                            // lane 0
+    auto issue_tile = [&](int j) {                            // one lane
         const int s = j % NST;
         uint8_t* stg = sm + LY::kOffStage + s * LY::kStage;
         uint64_t* bar = &full[s];
@@ -292,7 +292,7 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
         tmem_relinquish();
         for (int j = 0; j < NST && j < n_t; ++j) {
             locate_tile(j);
-            if (lane == 0) issue_tile(j);
+            if (elect_one()) issue_tile(j);
             __syncwarp();
         }
     } else if (warp >= 3) {
@@ -381,13 +381,10 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
         int j = NST;
         for (; j < n_t && go; ++j) {
             locate_tile(j);
-            int ok = 1;
-            if (lane == 0) {
-                ok = wait_bounded(&empty[j % NST], ((j / NST) - 1) & 1, p.status) ? 1 : 0;
-                if (*(volatile int*)abort_flag) ok = 0;
-                if (ok) issue_tile(j);
-            }
-            go = __shfl_sync(0xffffffffu, ok, 0) != 0;
+            go = __all_sync(0xffffffffu, wait_bounded(&empty[j % NST], ((j / NST) - 1) & 1, p.status) &&
+                                             !*(volatile int*)abort_flag);
+            if (go && elect_one()) issue_tile(j);
+            __syncwarp();
         }
         // no exit with a copy in flight: on the ordinary path the MMA warp has waited for all of them;
         // an abandoned one is waited for here (one never issued runs into the bound)

@@ -218,7 +218,7 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
         tmem_relinquish();
         // the Q~ tile and the first NST tiles go out before the prologue barrier
         slot_batch = slot_of_tile(lane);
-        if (lane == 0) {
+        if (elect_one()) {
             mbar_arrive_expect_tx(qfull, (uint32_t)(LY::kLatBlocks * rows_o * 128));
 #pragma unroll
             for (int blk = 0; blk < LY::kLatBlocks; ++blk)
@@ -226,7 +226,7 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
         }
         for (int j = 0; j < NST && j < n_issue; ++j) {
             const int64_t slot0 = __shfl_sync(0xffffffffu, slot_batch, j);
-            if (lane == 0) issue_tile(j, slot0);
+            if (elect_one()) issue_tile(j, slot0);
         }
     } else if (warp >= 2) {
         // ---- prologue (softmax warps): the normalised RoPE query, alpha^q, and
@@ -281,7 +281,7 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
             if ((j & 31) == 0) slot_batch = slot_of_tile(j + lane);
             const int64_t slot0 = __shfl_sync(0xffffffffu, slot_batch, j & 31);
             int go = 1;
-            if (lane == 0) {
+            if (elect_one()) {
                 const int s = j % NST;
                 if (!wait_bounded(&empty[s], ((j / NST) - 1) & 1, p.status, p.wait_ns)) {
                     *abort_flag = 1;
@@ -292,11 +292,11 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
                     issue_tile(j, slot0);
                 }
             }
-            if (!__shfl_sync(0xffffffffu, go, 0)) break;
+            if (!__all_sync(0xffffffffu, go)) break;
         }
     } else if (warp == 1) {
         // ===================== MMA issuer =====================
-        if (lane == 0) {
+        if (elect_one()) {
             const uint32_t id_s = idesc_bf16(kRowsMMA, KT, 0, 0);
             const uint32_t id_o = idesc_bf16(128, rows_o, 1, 0);
             const uint32_t q_addr = smem_u32(sQ);
