@@ -279,11 +279,11 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
         for (int q = 0; q < 4; ++q) {
             if (q >= n_pieces || slots[q] < 0) continue;
             const int at = q * p.piece;
-            tma_load_4d(stg + (at >> 3) * LY::kGroup, &tm_lat, 0, 0, 0, slots[q] >> 3, bar);
-            if (!LY::kRopeIn) tma_load_2d(stg + LY::kOffRope + at * LY::kRopeRow, &tm_rope, 0, slots[q], bar);
             bulk_load(stg + LY::kOffScale + at * 4, p.kv_scale + slots[q], (uint32_t)p.piece * 4, bar);
             if (ak_row)
                 bulk_load(stg + LY::kOffAk + at * ak_row, p.ak + (int64_t)slots[q] * ak_row, (uint32_t)p.piece * ak_row, bar);
+            tma_load_4d(stg + (at >> 3) * LY::kGroup, &tm_lat, 0, 0, 0, slots[q] >> 3, bar);
+            if (!LY::kRopeIn) tma_load_2d(stg + LY::kOffRope + at * LY::kRopeRow, &tm_rope, 0, slots[q], bar);
         }
     };
     const size_t grow0 = (size_t)b * n_rows + row0;           // first row in the query arrays
