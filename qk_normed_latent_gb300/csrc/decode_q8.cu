@@ -395,9 +395,7 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
         }
     } else if (warp == 1) {
         // ===================== logit MMAs =====================
-        {
-            const int nt = __shfl_sync(0xffffffffu, n_t, 0);              // uniform to the compiler, like tm
-            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        if (elect_one()) {
             const uint32_t id_s = idesc_e4m3(kT, N, 0, 0);
             const uint32_t id_r = idesc_bf16(kT, N, 0, 0);
             constexpr uint32_t sw = DR == 64 ? kSwizzle128B : kSwizzle64B, sbo = DR == 64 ? 1024 : 512;
@@ -408,16 +406,15 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
             const uint64_t st_lat = smem_desc(smem_u32(sm + LY::kOffStage), 16, LY::kGroup, kSwizzle128B);
             const uint64_t st_rope = smem_desc(smem_u32(sm + LY::kOffStage) + LY::kOffRope, 16, LY::kRopeGroup, sw);
             bool ok = true;
-            for (int j = 0; j < nt; ++j) {
+            for (int j = 0; j < n_t; ++j) {
                 const int s = j % NST;
                 const uint64_t lat = st_lat + (uint64_t)(s * (LY::kStage >> 4)), rope = st_rope + (uint64_t)(s * (LY::kStage >> 4));
-                const uint32_t d = tm + (uint32_t)(j % NSB) * (2 * N);
-                bool got = true;
-                if (j >= NSB) got = wait_bounded(&sfree[j % NSB], ((j / NSB) - 1) & 1, p.status);
-                got = got && wait_bounded(&full[s], (j / NST) & 1, p.status) && !*(volatile int*)abort_flag;
-                if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
+                const uint32_t d = tmem + (uint32_t)(j % NSB) * (2 * N);
+                // the tile first: once the softmax has read S, nothing but the MMAs is left to do
+                ok = wait_bounded(&full[s], (j / NST) & 1, p.status) && !*(volatile int*)abort_flag;
+                if (ok && j >= NSB) ok = wait_bounded(&sfree[j % NSB], ((j / NSB) - 1) & 1, p.status);
+                if (!ok) break;
                 tc_fence_after();
-                if (elect_one()) {
 #pragma unroll
                 for (int blk = 0; blk < KB; ++blk)
 #pragma unroll
@@ -428,20 +425,16 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
                 for (int kk = 0; kk < DR / 16; ++kk)
                     mma_bf16(d + N, rope + (uint64_t)(kk * 2), q_rope + (uint64_t)(kk * 2), id_r, kk > 0 ? 1u : 0u);
                 mma_commit(&sfull[j % NSB]);
-                }
-                __syncwarp();
             }
             if (!ok) {                       // no exit with an MMA in flight
                 *(volatile int*)abort_flag = 1;
-                if (elect_one()) mma_commit(&drain[0]);
+                mma_commit(&drain[0]);
                 wait_bounded(&drain[0], 0, p.status);
             }
         }
     } else if (warp == 2) {
         // ===================== output MMAs (a thread of their own: neither issue waits for the other's data) ==========
-        {
-            const int nt = __shfl_sync(0xffffffffu, n_t, 0);              // uniform to the compiler, like tm
-            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        if (elect_one()) {
             const uint32_t id_o = idesc_e4m3(128, LY::kON, 1, 1);
             // A: a chunk's 128 latents x 32 tokens, MN-major (8-token groups kGroup apart).  B: P, MN-major:
             // a token's codes in as many bytes (swizzle of the same width), 8-token groups kPGroup apart.
@@ -450,30 +443,27 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
             const uint64_t st_lat = smem_desc(smem_u32(sm + LY::kOffStage), 1024, LY::kGroup, kSwizzle128B);
             const uint64_t st_p = smem_desc(smem_u32(sm + LY::kOffStage) + LY::kOffP, LY::kPGroup, LY::kPGroup, swp);
             bool ok = true;
-            for (int j = 0; j < nt; ++j) {
+            for (int j = 0; j < n_t; ++j) {
                 const int s = j % NST;
                 const uint64_t lat = st_lat + (uint64_t)(s * (LY::kStage >> 4)), pw = st_p + (uint64_t)(s * (LY::kStage >> 4));
-                const bool got = wait_bounded(&pfull[s], (j / NST) & 1, p.status) && !*(volatile int*)abort_flag;
-                if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
+                ok = wait_bounded(&pfull[s], (j / NST) & 1, p.status) && !*(volatile int*)abort_flag;
+                if (!ok) break;
                 tc_fence_after();
-                if (elect_one()) {
 #pragma unroll
                 for (int c = 0; c < KB; ++c)
 #pragma unroll
                     for (int kk = 0; kk < kT / 32; ++kk)
 #pragma unroll
                         for (int part = 0; part < (LY::kStacked ? 1 : 2); ++part)
-                            mma_f8(tm + LY::kColO + c * PN, lat + (uint64_t)((c * 1024 + kk * 4 * LY::kGroup) >> 4),
+                            mma_f8(tmem + LY::kColO + c * PN, lat + (uint64_t)((c * 1024 + kk * 4 * LY::kGroup) >> 4),
                                    pw + (uint64_t)((kk * 4 * LY::kPGroup + part * 8 * PN) >> 4), id_o,
                                    (j > 0 || kk > 0 || part > 0) ? 1u : 0u);
                 mma_commit(&empty[s]);
                 mma_commit(&odone[s]);
-                }
-                __syncwarp();
             }
             if (!ok) {
                 *(volatile int*)abort_flag = 1;
-                if (elect_one()) mma_commit(&drain[1]);
+                mma_commit(&drain[1]);
                 wait_bounded(&drain[1], 0, p.status);
             }
         }
