@@ -286,6 +286,15 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
             if (!LY::kRopeIn) tma_load_2d(stg + LY::kOffRope + at * LY::kRopeRow, &tm_rope, 0, slots[q], bar);
         }
     };
+    auto prefetch_tile = [&]() {                              // one lane
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            if (q >= n_pieces || slots[q] < 0) continue;
+            tma_prefetch_4d(&tm_lat, 0, 0, 0, slots[q] >> 3);
+            bulk_prefetch(p.kv_scale + slots[q], (uint32_t)p.piece * 4);
+            if (ak_row) bulk_prefetch(p.ak + (int64_t)slots[q] * ak_row, (uint32_t)p.piece * ak_row);
+        }
+    };
     const size_t grow0 = (size_t)b * n_rows + row0;           // first row in the query arrays
     if (warp == 0) {
         tmem_alloc(tmem_slot, kTmemCols);
@@ -384,6 +393,12 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
             go = __all_sync(0xffffffffu, wait_bounded(&empty[j % NST], ((j / NST) - 1) & 1, p.status) &&
                                              !*(volatile int*)abort_flag);
             if (go && elect_one()) issue_tile(j);
+            // the next tile into L2 while the ring has no room for it: its load then takes the L2's latency
+            // (a stage is held for its load, and three or four tiles' loads are what the ring can hide)
+            if ((j + 1) % batch && j + 1 < n_t) {
+                locate_tile(j + 1);
+                if (elect_one()) prefetch_tile();
+            }
             __syncwarp();
         }
         // no exit with a copy in flight: on the ordinary path the MMA warp has waited for all of them;
