@@ -35,7 +35,9 @@ struct SchedSmem {
 
 // Block-wide: every thread of the CTA calls it; on return `S` holds the plan.
 // Sequences with an invalid length get no tiles (and a status report when
-// `report_errors`).
+// `report_errors`).  With SPLITS_ONLY (the combine kernel) a plan without a split
+// sequence ends as soon as that is known: n_split is 0 and nothing else is set.
+template <bool SPLITS_ONLY = false>
 __device__ __forceinline__ void compute_schedule(const int32_t* __restrict__ seq_lens, int B, int s_q,
                                                  const SchedArgs& a, SchedSmem& S, int* status, bool report_errors) {
     const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = (nt + 31) >> 5;
@@ -74,9 +76,13 @@ __device__ __forceinline__ void compute_schedule(const int32_t* __restrict__ seq
         const float ideal = (float)S.n_items * a.n_rb / (float)a.sms;
         const int tpi = (float)m <= 1.25f * ideal ? m : (int)ceilf(ideal);
         S.tpi = max(max(tpi, a.min_tokens / a.tile), 1);
+        if constexpr (SPLITS_ONLY) S.n_split = (a.fixed_splits == 0 && m <= S.tpi) ? 0 : -1;
     }
     __syncthreads();
     const int tpi = S.tpi;
+    if constexpr (SPLITS_ONLY) {
+        if (S.n_split == 0) return;        // uniform: written before the barrier
+    }
     for (int b = tid; b < B; b += nt) {
         const int tb = S.tb[b];
         int rk = 0;

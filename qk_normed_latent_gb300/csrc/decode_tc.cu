@@ -738,7 +738,7 @@ combine_var_kernel(const float* __restrict__ o_part, const float* __restrict__ l
     __shared__ float w_s[256];
     __shared__ float s_inv, s_lse;
     __shared__ SchedSmem S;
-    if (sched_inline) compute_schedule(seq_lens, B, s_q, sa, S, nullptr, false);
+    if (sched_inline) compute_schedule<true>(seq_lens, B, s_q, sa, S, nullptr, false);
     pdl_wait();
     pdl_trigger();
     const int tasks = (sched_inline ? S.n_split : *n_split) * rows_per_seq;
