@@ -11,10 +11,11 @@ import torch
 
 import workloads as W
 
-from . import (F32, BF16, append, decode_workspace_size, decode_raw, make_decode_args, prepare_absorb_query,
-               prepare_append)
+from . import (F32, BF16, append, append_q8, decode_workspace_size, decode_raw, make_decode_args,
+               prepare_absorb_query, prepare_append, prepare_append_q8, prepare_decode)
 
-_TORCH_DT = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+# element types; "e4m3" is the 8-bit latent cache (bytes: codes and the bf16 RoPE key, scales beside them)
+_TORCH_DT = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16, "e4m3": torch.uint8}
 # quiet-NaN bit patterns written into untouched cache slots
 SENTINEL_BF16 = 0x7FC1
 SENTINEL_F32 = 0x7FC00001
@@ -55,17 +56,25 @@ def sentinel_fill(t: torch.Tensor) -> None:
         t.view(torch.int16).fill_(SENTINEL_F16)
     elif t.dtype == torch.float32:
         t.view(torch.int32).fill_(SENTINEL_F32)
+    elif t.dtype == torch.uint8:
+        t.fill_(0xFF)                    # NaN as e4m3 and as bf16
     else:
         raise ValueError(t.dtype)
 
 
 class DeviceState:
     """Device tensors of one workload.  Prefill writes every token except the
-    last `n_append` of each sequence; `step()` appends those and decodes."""
+    last `n_append` of each sequence; `step()` appends those and decodes.
+
+    A workload with cache_dtype "e4m3" keeps the 8-bit latent cache (append_q8).
+    window > 0: each query sees its last `window` tokens and the first `sinks`."""
 
     def __init__(self, w: W.Workload, plain: bool = False, o_dtype=torch.float32, device: str = "cuda",
-                 prefill_chunk: int = 1 << 18, sentinel: bool = True, keep_host: bool = False):
+                 prefill_chunk: int = 1 << 18, sentinel: bool = True, keep_host: bool = False, window: int = 0,
+                 sinks: int = 0):
         self.w = w
+        self.q8 = w.cache_dtype == "e4m3"
+        self.window, self.sinks = window, sinks
         self.plain = plain
         self.dev = torch.device(device)
         self.lens = W.seq_lens(w)
@@ -80,15 +89,18 @@ class DeviceState:
         self.grq = torch.from_numpy(grq).to(d)
         self.grk = torch.from_numpy(grk).to(d)
         cdt = _TORCH_DT[w.cache_dtype]
-        self.kv = torch.empty((self.num_slots, w.d_c + w.d_r), dtype=cdt, device=d)
+        self.kv = torch.empty((self.num_slots, w.d_c + (2 if self.q8 else 1) * w.d_r), dtype=cdt, device=d)
+        self.kv_scale = torch.empty(self.num_slots, dtype=torch.float32, device=d) if self.q8 else None
         self.ak = torch.empty((self.num_slots, w.G), dtype=_TORCH_DT[w.alpha_dtype], device=d)
         if sentinel:
             sentinel_fill(self.kv)
             sentinel_fill(self.ak)
+            if self.q8:
+                sentinel_fill(self.kv_scale)
         self.seq_lens = torch.from_numpy(self.lens.astype(np.int32)).to(d)
         self.page_table = torch.from_numpy(table).to(d) if self.paged else None
         q, qr = W.queries(w)
-        self.q_tilde = torch.empty((w.B, w.s_q, w.H, w.d_c), dtype=cdt, device=d)
+        self.q_tilde = torch.empty((w.B, w.s_q, w.H, w.d_c), dtype=torch.bfloat16 if self.q8 else cdt, device=d)
         self.alpha_q = torch.empty((w.B, w.s_q, w.H), dtype=torch.float32, device=d)
         # the step's results, o and lse, in one buffer
         self.step_out, (self.o, self.lse) = packed(
@@ -106,8 +118,11 @@ class DeviceState:
             for s0 in range(0, pre, prefill_chunk):
                 s1 = min(pre, s0 + prefill_chunk)
                 slots = torch.from_numpy(W.slots_of(table, self.page_size, b, np.arange(s0, s1))).to(d)
-                append(torch.from_numpy(c[s0:s1]).to(d), torch.from_numpy(r[s0:s1]).to(d), self.wk, self.grk,
-                       slots, self.kv, self.ak, w.eps, plain=plain)
+                new = (torch.from_numpy(c[s0:s1]).to(d), torch.from_numpy(r[s0:s1]).to(d), self.wk, self.grk, slots)
+                if self.q8:
+                    append_q8(*new, self.kv, self.kv_scale, self.ak, w.eps, plain=plain)
+                else:
+                    append(*new, self.kv, self.ak, w.eps, plain=plain)
             if n_new:
                 new_c.append(c[pre:])
                 new_r.append(r[pre:])
@@ -125,6 +140,7 @@ class DeviceState:
         self.workspace = None
         self.args = None
         self._absorb = self._append = None
+        self._decode = {}
 
     # -- the three calls -------------------------------------------------------
     def absorb(self, stream=None):
@@ -138,10 +154,25 @@ class DeviceState:
     def append_step(self, stream=None):
         if self.c_new is None:
             return
-        if self._append is None:
+        if self._append is None and self.q8:
+            self._append = prepare_append_q8(self.c_new, self.r_new, self.wk, self.grk, self.slots_new, self.kv,
+                                             self.kv_scale, self.ak, self.w.eps, plain=self.plain)
+        elif self._append is None:
             self._append = prepare_append(self.c_new, self.r_new, self.wk, self.grk, self.slots_new, self.kv,
                                           self.ak, self.w.eps, plain=self.plain)
         self._append(stream)
+
+    def prepared_decode(self, num_splits: int = 0, force_simt: bool = False):
+        """The decode call over an 8-bit cache or through a window (its workspace allocated once)."""
+        key = (num_splits, force_simt)
+        if self._decode.get(key) is None:
+            w = self.w
+            self._decode[key] = prepare_decode(
+                self.q_tilde, self.alpha_q, self.q_rope, self.grq, self.kv, self.ak, self.seq_lens, self.page_table,
+                self.page_size, self.max_pages, w.G, w.scale, w.eps, self.o, self.lse, plain=self.plain,
+                force_simt=force_simt, num_splits=num_splits, kv_scale=self.kv_scale, window=self.window,
+                sinks=self.sinks)
+        return self._decode[key]
 
     def decode_args(self, num_splits: int = 0, force_simt: bool = False):
         w = self.w
@@ -156,6 +187,9 @@ class DeviceState:
         return a
 
     def decode(self, num_splits: int = 0, force_simt: bool = False, stream=None):
+        if self.q8 or self.window:
+            self.prepared_decode(num_splits, force_simt)(stream)
+            return
         self.args = self.decode_args(num_splits, force_simt)
         decode_raw(self.args, stream)
 
@@ -163,6 +197,9 @@ class DeviceState:
         """One pass of the whole path: absorb, append this step's tokens, decode."""
         self.absorb(stream)
         self.append_step(stream)
+        if self.q8 or self.window:
+            self.prepared_decode(num_splits, force_simt)(stream)
+            return
         if self.args is None or num_splits != self.args.num_splits:
             self.args = self.decode_args(num_splits, force_simt)
         decode_raw(self.args, stream)

@@ -335,3 +335,32 @@ def test_bad_page_and_length(Q, cache, simt):
         dev.call()
         assert Q.get_device_status() == Q.ERR_DEVICE_BOUNDS
         assert np.linalg.norm(dev.o[1].double().cpu().numpy() - c.o[1]) <= 5e-3 * np.linalg.norm(c.o[1])
+
+
+@pytest.mark.parametrize("cache,window,sinks", [("e4m3", 0, 0), ("e4m3", 300, 4), ("bf16", 300, 4)])
+def test_pipeline_step(Q, cache, window, sinks):
+    """The whole path -- absorb, append of the step's tokens, decode -- on the 8-bit cache and through a window,
+    against the 64-bit form over what the cache then holds; the appended latents against their quantised inputs."""
+    import workloads as W
+    from qk_normed_latent_gb300.pipeline import DeviceState
+    w = W.small(W.WORKLOADS[1].with_(cache_dtype=cache), 3, (700, 130, 64))
+    st = DeviceState(w, window=window, sinks=sinks, keep_host=True)
+    st.step()
+    assert Q.get_device_status() == 0
+    kv, ak = st.kv.cpu(), st.ak.double().cpu().numpy()
+    qt, aq = st.q_tilde.double().cpu().numpy(), st.alpha_q.double().cpu().numpy()
+    qr = R.rms_normalise(st.q_rope.cpu().numpy(), st.grq.cpu().numpy().astype(np.float64))
+    for b, n in enumerate(int(x) for x in st.lens):
+        slot = W.slots_of(st.table_np, st.page_size, b, np.arange(n))
+        if cache == "e4m3":
+            codes, scale = kv[slot, :w.d_c].numpy(), st.kv_scale.cpu().numpy()[slot].astype(np.float64)
+            want, want_scale = R.quantise(st.host_seqs[b][0])
+            assert (scale == want_scale).all() and ((codes == want) | ((codes & 127 == 0) & (want & 127 == 0))).all()
+            c_hat = R.e4m3_decode(codes) * scale[:, None]
+            kr = kv[slot, w.d_c:].contiguous().view(torch.bfloat16).double().numpy()
+        else:
+            c_hat, kr = kv[slot, :w.d_c].double().numpy(), kv[slot, w.d_c:].double().numpy()
+        o, lse = R.attention(qt[b], aq[b], qr[b], c_hat, kr, ak[slot], w.s_q, n, window, sinks, w.scale)
+        got = st.o[b].double().cpu().numpy()
+        assert np.linalg.norm(got - o) <= 5e-3 * np.linalg.norm(o)
+        assert np.abs(st.lse[b].double().cpu().numpy() - lse).max() <= 2e-2
