@@ -223,7 +223,8 @@ const char* kernel_name(const qkmla_decode_args* a, const DecodeExt& x) {
 int launch_count(const qkmla_decode_args* a, const DecodeExt& x) {
     DecodePlan plan;
     if (plan_decode(a, x, &plan) != QKMLA_OK) return 0;
-    if (plan.kernel == 1) return sched_in_kernel(a) ? 2 : 3;   // [scheduler,] decode, combine
+    if (plan.kernel == 1)                                      // [scheduler,] decode[, combine]
+        return (sched_in_kernel(a) ? 1 : 2) + (x.active() && never_splits(a, x) ? 0 : 1);
     return plan.parts > 1 ? 2 : 1;
 }
 

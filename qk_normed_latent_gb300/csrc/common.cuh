@@ -170,6 +170,8 @@ bool pair_shape(const qkmla_decode_args* a);        // served by the two-CTA clu
 bool sched_in_kernel(const qkmla_decode_args* a);   // split plan computed by the decode kernels themselves
 size_t tc_workspace(const qkmla_decode_args* a, int sms);
 bool q8_tc_supported(const qkmla_decode_args* a, const DecodeExt& x);   // 8-bit cache, tensor-core kernel
+// qkmla_decode_ext calls whose arguments alone rule out a split sequence: no combine kernel.
+bool never_splits(const qkmla_decode_args* a, const DecodeExt& x);
 size_t q8_tc_workspace(const qkmla_decode_args* a, int sms);
 int launch_decode_q8(const qkmla_decode_args* a, const DecodeExt& x, cudaStream_t s);
 int launch_append_q8(const float* c_new, const float* r_new, const float* wk, const float* grk, const int64_t* slots,

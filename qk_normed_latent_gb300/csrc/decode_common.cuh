@@ -14,6 +14,7 @@ using namespace tc;
 
 constexpr int kMaxG = 8;
 constexpr int kMaxB = 4096;
+constexpr int kMinItemTokens = 512;           // a sequence splits into items of at least this many tokens
 constexpr uint64_t kWaitNs = 2000000000ull;   // 2 s bound on any single wait
 
 struct WorkItem {

@@ -860,7 +860,7 @@ int launch_decode_q8(const qkmla_decode_args* a, const DecodeExt& x, cudaStream_
     sa.max_len = a->max_pages * a->page_size;
     sa.n_rb = n_rb;
     sa.sms = sms;
-    sa.min_tokens = 512;
+    sa.min_tokens = kMinItemTokens;
     sa.tile = kT;
     sa.fixed_splits = a->num_splits;
     sa.min_len = 0;
@@ -922,7 +922,7 @@ int launch_decode_q8(const qkmla_decode_args* a, const DecodeExt& x, cudaStream_
                                                    : by_rows(integral_constant<int, 256>(), d64()))
                    : a->d_r == 32  ? by_rows(integral_constant<int, 128>(), d32())
                                    : by_rows(integral_constant<int, 128>(), d64());
-    if (rc != QKMLA_OK) return rc;
+    if (rc != QKMLA_OK || never_splits(a, x)) return rc;
     return launch_combine_var(a, sa, w, s);
 }
 

@@ -895,6 +895,16 @@ bool pair_shape(const qkmla_decode_args* a) {
 // Batches whose split plan every decode CTA computes itself (no scheduler launch).
 bool sched_in_kernel(const qkmla_decode_args* a) { return a->B >= 1 && a->B <= dec::kMaxBSched; }
 
+// Items hold kMinItemTokens at least, so a batch whose longest possible sequence (or what a window leaves
+// of it) is no longer has one item a sequence.
+bool never_splits(const qkmla_decode_args* a, const DecodeExt& x) {
+    if (a->num_splits == 1) return true;
+    int64_t tokens = (int64_t)a->max_pages * a->page_size;
+    if (x.window > 0)                       // sinks and window, each rounded out to whole tiles (64 tokens at most)
+        tokens = std::min<int64_t>(tokens, (x.sinks + 63LL) / 64 * 64 + ((int64_t)x.window + a->s_q - 1 + 63 + 63) / 64 * 64);
+    return a->num_splits == 0 && tokens <= dec::kMinItemTokens;
+}
+
 // Query rows per CTA of the 64-row kernel.  With fewer than 64 heads it packs k
 // query tokens of a sequence (k dividing s_q), so that a CTA streams each tile
 // once for all of them, while k H stays within the 64 MMA rows and, for d_c =
@@ -989,7 +999,7 @@ int launch_decode_tc(const qkmla_decode_args* a, const DecodeExt& x, cudaStream_
     sa.max_len = a->max_pages * a->page_size;
     sa.n_rb = n_rb;
     sa.sms = sms;
-    sa.min_tokens = 512;
+    sa.min_tokens = kMinItemTokens;
     sa.tile = tile;
     sa.fixed_splits = a->num_splits;
     sa.min_len = x.window > 0 ? 0 : a->s_q;
@@ -1058,7 +1068,7 @@ int launch_decode_tc(const qkmla_decode_args* a, const DecodeExt& x, cudaStream_
              : akh ? launch_kernel<256, 32, false, 4, true>(lat, rope, qmap, tp, n_rb, max_items, s)
                    : launch_kernel<256, 32, false, 4, false>(lat, rope, qmap, tp, n_rb, max_items, s);
     }
-    if (rc != QKMLA_OK) return rc;
+    if (rc != QKMLA_OK || (x.active() && never_splits(a, x))) return rc;
     return launch_combine_var(a, sa, w, s);
 }
 

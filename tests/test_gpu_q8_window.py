@@ -211,6 +211,16 @@ def test_q8_tensor_core(Q, k):
     check(Q, R.Case(**kw), simt=False, num_splits=splits)
 
 
+@pytest.mark.parametrize("cache", ["q8", "bf16"])
+def test_launches(Q, cache):
+    """One kernel where no sequence can be split, a combine kernel where one can, a scheduler beyond 128 sequences."""
+    for kw, launches in ((dict(lens=[512, 3], window=600), 1), (dict(lens=[513, 3], window=600), 2),
+                         (dict(lens=[3000], window=300, sinks=60), 1), (dict(lens=[3000], window=2000), 2),
+                         (dict(lens=[5] * 129, window=9), 2)):
+        dev = check(Q, R.Case(cache=cache, **kw), simt=False)
+        assert dev.call.launch_count == launches, kw
+
+
 def test_q8_tensor_core_bf16_output(Q):
     check(Q, R.Case([600, 70], s_q=2), simt=False, o_dtype=torch.bfloat16)
 
