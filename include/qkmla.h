@@ -44,8 +44,9 @@
  *    anything a kernel of this library produces (q~, alpha^q, the cache, q and
  *    q_rope of qkmla_project_query, o), wait for the previous kernel of the
  *    stream.  Reads of inputs no kernel of the library writes may start
- *    earlier: seq_lens in qkmla_decode; W^K, the new tokens, their slots and
- *    positions in qkmla_append / qkmla_append_rope.  A previous kernel that
+ *    earlier: seq_lens in qkmla_decode and qkmla_decode_ext; W^K, the new tokens,
+ *    their slots and positions in qkmla_append, qkmla_append_rope and
+ *    qkmla_append_q8.  A previous kernel that
  *    itself signals early dependent launch must therefore not be writing
  *    those inputs (kernels that do not signal it, and copies, are waited for
  *    in full as usual).
@@ -295,14 +296,23 @@ typedef struct qkmla_decode_ext_args {
  * is qkmla_decode's definition.
  *
  * Window w, sinks f: query i of sequence b, of causal length n = seq_lens[b] -
- * s_q + i + 1, attends to the tokens t < n with t < f or t >= n - w.  Tokens
- * outside are neither read nor do their page-table entries matter, except in
- * tiles that a visible token shares; no value stored there (NaN included)
- * reaches the result.
+ * s_q + i + 1, attends to the tokens t < n with t < f or t >= n - w.  What is
+ * stored for tokens that no query of the step sees (NaN included) does not reach
+ * the result, and pages without such a token are not read; a tile of up to 64
+ * tokens that holds a visible one is loaded whole, so its page-table entry has
+ * to be valid.
  *
  * With an 8-bit cache or a window, seq_lens[b] may be anything from 0 to
  * max_pages * page_size: a query without a visible token (an idle batch slot)
  * gives o = 0 and lse = -inf.  With neither, the call is qkmla_decode.
+ *
+ * Accuracy: fp32 sums, with the output's weights rounded -- 8-bit cache: to two
+ * e4m3 parts (2^-8); bf16 cache: as qkmla_decode.  Tensor-core kernels serve the
+ * 8-bit cache for (d_c, d_r) of (512, 64), (256, 32 or 64) and (128, 32 or 64), H a
+ * multiple of 16, G <= 8, B <= 4096, page sizes 16, 32 or a multiple of 64 and
+ * 16-byte aligned bases, and windows over the bf16 cache where qkmla_decode has one;
+ * the CUDA-core kernel serves the rest.
+ *
  * The workspace size, the kernel's name and the launches come from the _ext
  * forms of their calls.  Errors: as qkmla_decode, and INVALID for a null
  * argument block, a negative window or sinks, sinks without a window, kv_scale

@@ -10,20 +10,24 @@
 // split into two e4m3 parts, a = hi + lo, hi = e4m3(a), lo = e4m3(a - hi).  For the
 // bf16 query the sum is exact down to 2^-18 of the row's largest value (8 significant
 // bits in two times 4); for the weights it is off by at most 2^-8, like a bf16
-// rounding.  Both parts are rows of one operand, so one MMA forms both products and
-// the epilogue adds them: a tcgen05.mma of M = 128, K = 32 costs 55 cycles (A
-// K-major) or 64 (A MN-major) for every N <= 64, 64 / 69 at N = 128 (measured), so
-// the second part costs almost nothing.
+// rounding.  The RoPE query is two bf16 parts likewise (2^-16).  A tcgen05.mma with
+// K = 32 costs 45 cycles up to N = 32, 48 at N = 64 and 65 at N = 128 (M = 64 or 128,
+// K-major or MN-major, measured), so both parts as rows of one operand cost little more
+// than one.
 //
-// Orientation.  Tokens are the M of the logit product and latents the M of the
-// output product, both the full 128; query rows (heads x query tokens) are N:
-//   S   = X_tile [Q_hi | Q_lo]^T   M = 128 tokens,  N = 2 ROWS, K = d_c    (e4m3)
-//   R   = Kr_tile [Qr_hi | Qr_lo]^T M = 128 tokens, N = 2 ROWS, K = d_r    (bf16)
-//   O^T += X_tile^T [P_hi | P_lo]  M = 128 latents of a chunk, N = 2 ROWS, K = 128 tokens
-// With ROWS = 32, S and R of two tiles and O^T of 512 latents fill TMEM's 512
-// columns.  A softmax thread is a token: its scale, alpha^k and mask are its own
-// registers, the row sums stay in registers until the end, and the running maximum
-// is only looked at (one vote a tile) -- it moves when a logit exceeds it by 2^8.
+// Orientation.  A CTA owns up to 64 query rows (heads x query tokens) and a range of
+// 64-token tiles; tokens are the M of the logit product, latents that of the output:
+//   S   = X_tile [Q_hi | Q_lo]^T    M = 64 tokens, N = 2 ROWS, K = d_c              (e4m3)
+//   R   = Kr_tile [Qr_hi | Qr_lo]^T M = 64 tokens, N = 2 ROWS, K = d_r              (bf16)
+//   O^T += X_tile^T [P_hi | P_lo]   M = 128 latents of a chunk, K = 64 tokens       (e4m3)
+// With 64 rows and 512 latents S, R and O^T fill TMEM's 512 columns (one S buffer; P_hi
+// and P_lo then go into one accumulator by two MMAs), and the query parts, 80 KB, leave
+// room for three 43 KB stages.  64 rows a CTA rather than 32 with 128-token tiles halve
+// what a row costs in shared-memory traffic and loads (4400 cycles for 32 rows x 128 tokens
+// against 2340 for 64 x 64).  A softmax thread is a token and 8 rows: the token's scale,
+// alpha^k and mask are its registers, the row sums stay in registers until the end, and the
+// running maximum is only looked at (one vote a tile) -- it moves when a weight exceeds it
+// by 2^8.
 //
 // Weights in units of the output.  P carries s_t, so that the output product runs on
 // the bare codes: p_{t,h} = 32 2^(x_t - m_h) s_t 2^(m_h - v_h) with m_h the running
@@ -32,9 +36,16 @@
 // tokens beside an outlier's scale below e4m3's range.  m and v are integers: every
 // rescale is a power of two, hence exact.
 //
-// Warps: 0 TMA producer (+ TMEM owner), 1 logit MMAs, 2 output MMAs, then softmax and epilogue in
-// groups of 128 threads = tokens, 8 rows a group (16 rows a thread took 1450 cycles a tile).  All waits are
-// bounded (2 s).
+// What bounds it (512 / 64, 64 rows): a tile takes 2340 cycles, of which the tensor core
+// needs 2076 (20 x 65 + 16 x 48); the rest is the one S buffer's hand-over (MMA done ->
+// read -> next MMA).  64 sequences x 4096 tokens x 128 heads: 111 us (1.77 TB/s, 0.66 PFLOP/s
+// counted once; the two parts make it 1.3), of which ~33 us are the start and end of the
+// items; 4 x 262144 tokens: 301 us (0.97 PFLOP/s).  The bf16 pair kernel takes 119 and 372 us.
+// With 16 rows (d_c = 256) the calls are latency-bound: 16 sequences of 1k-8k tokens 17 us.
+//
+// Warps: 0 TMA producer (+ TMEM owner), 1 logit MMAs, 2 output MMAs (each issue loop in
+// one elected lane: a branch on the lane number costs ~88 cycles an MMA), then softmax and
+// epilogue in groups of 4 warps, 16 rows a group.  All waits are bounded (2 s).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -53,7 +64,7 @@ using namespace tc;
 using namespace dec;
 
 constexpr int kT = 64;               // tokens per tile
-constexpr int HPT = 8;                // query rows of a softmax thread
+constexpr int kHpt = 8;              // query rows of a softmax thread
 constexpr uint32_t kTmemCols = 512;
 constexpr float kPUnit = 32.f;       // P of the largest contribution: lazy maxima let it grow to 2^8 < 448
 constexpr float kLazy = 256.f;       // a weight (or a scaled one) above this moves the running maxima
@@ -144,9 +155,7 @@ __device__ __forceinline__ void split_e4m3_f16(float2 v, uint32_t& hi, uint32_t&
     lo = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(r), __NV_SATFINITE, __NV_E4M3);
 }
 
-// The softmax warps' wait: one warp of the group polls, the others sleep at a named barrier.
-__device__ __forceinline__ bool group_any(int grp, bool pred);
-__device__ __forceinline__ void group_sync(int grp);
+// Vote and barrier of a softmax group (named barriers 1 ..).
 __device__ __forceinline__ bool group_any(int grp, bool pred) {
     uint32_t r;
     asm volatile(
@@ -394,7 +403,7 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
                                              !*(volatile int*)abort_flag);
             if (go && elect_one()) issue_tile(j);
             // the next tile into L2 while the ring has no room for it: its load then takes the L2's latency
-            // (a stage is held for its load, and three or four tiles' loads are what the ring can hide)
+            // (a stage is held for its load, so the load's latency counts against the ring's three tiles)
             if ((j + 1) % batch && j + 1 < n_t) {
                 locate_tile(j + 1);
                 if (elect_one()) prefetch_tile();
@@ -414,8 +423,7 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
             const uint32_t id_s = idesc_e4m3(kT, N, 0, 0);
             const uint32_t id_r = idesc_bf16(kT, N, 0, 0);
             constexpr uint32_t sw = DR == 64 ? kSwizzle128B : kSwizzle64B, sbo = DR == 64 ? 1024 : 512;
-            // descriptors are formed once and moved by constant offsets: forming them anew for every MMA made
-            // the issue, not the tensor core, the limit (85 cycles an MMA against 65)
+            // descriptors are formed once and moved by constant offsets: the issue must keep up with 65 cycles an MMA
             const uint64_t q_lat = smem_desc(smem_u32(sQ), 16, 1024, kSwizzle128B);
             const uint64_t q_rope = smem_desc(smem_u32(sQ) + LY::kQLat, 16, sbo, sw);
             const uint64_t st_lat = smem_desc(smem_u32(sm + LY::kOffStage), 16, LY::kGroup, kSwizzle128B);
@@ -490,14 +498,14 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
         // gives lanes 0-15 the first 8 rows of the group, lanes 16-31 the next 8 of the same tokens
         const int tl = 16 * sub + (lane & 15);               // token in the tile
         const int ug = grp * 16;                             // first row of the group
-        const int u0 = ug + (lane >> 4) * HPT;               // first row of this thread
+        const int u0 = ug + (lane >> 4) * kHpt;               // first row of this thread
         const int hshift = 31 - __clz(p.H / p.G);            // heads a group: 2, 4, 8 or 16 (H >= 16, G <= 8)
-        const int h0 = (row0 + u0) % p.H;                    // its head: HPT divides H, so the rows share a query token
+        const int h0 = (row0 + u0) % p.H;                    // its head: kHpt divides H, so the rows share a query token
         const int ak_at = tl * p.G + (h0 >> hshift);         // alpha^k of this token for the first of the rows
         const int n_row = max(0, len - p.s_q + (row0 + u0) / p.H + 1);   // causal length of these rows
         const int w_row = p.window > 0 ? n_row - p.window : 0;
         // this group's rows in registers, two to a packed pair: -m, unit f, row sums
-        constexpr int HP2 = HPT / 2;
+        constexpr int HP2 = kHpt / 2;
         uint64_t nm2[HP2], f2v[HP2], lsum2[HP2];
         auto reload = [&]() {
 #pragma unroll
@@ -517,14 +525,14 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
             const bool sees = t < n_row && (t < p.sinks || t >= w_row);
             const bool any_sees = t < len_last && (t < p.sinks || t >= win_first);   // some row of the CTA
             const bool masked = !__all_sync(0xffffffffu, sees);
-            bool got_s = true;
+            bool got_s = true;                               // one warp polls, the others sleep at the barrier
             if (((warp - 3) & 3) == 0) got_s = wait_bounded(&sfull[sb], (j / NSB) & 1, p.status);
             group_sync(grp);
             tc_fence_after();
             uint64_t x2[HP2];
             float st_raw;
             {
-                uint32_t a[HPT], c[HPT], d[HPT], e[HPT];
+                uint32_t a[kHpt], c[kHpt], d[kHpt], e[kHpt];
                 const uint32_t base = tmem + (uint32_t)sb * (2 * N) + lane_base + ug;
                 tmem_ld8x2(base, a);
                 tmem_ld8x2(base + ROWS, c);
@@ -540,14 +548,14 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
                 uint64_t ca2[HP2];
                 auto scale_rows = [&](auto sh, auto f16) {
                     constexpr int SH = decltype(sh)::value;
-                    float ak[HPT];
+                    float ak[kHpt];
 #pragma unroll
-                    for (int u = 0; u < HPT; ++u)
+                    for (int u = 0; u < kHpt; ++u)
                         ak[u] = (u & ((1 << SH) - 1)) == 0
                                     ? st_raw * load_alpha<decltype(f16)::value>(stg + LY::kOffAk, ak_at + (u >> SH))
                                     : ak[u & ~((1 << SH) - 1)];
 #pragma unroll
-                    for (int u = 0; u < HPT; u += 4) {
+                    for (int u = 0; u < kHpt; u += 4) {
                         const float4 cf = *reinterpret_cast<const float4*>(coef_s + u0 + u);
                         ca2[u / 2] = f2_mul(f2(cf.x, cf.y), f2(ak[u], ak[u + 1]));
                         ca2[u / 2 + 1] = f2_mul(f2(cf.z, cf.w), f2(ak[u + 2], ak[u + 3]));
@@ -558,7 +566,7 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
                 using no = integral_constant<bool, false>;
                 if (p.plain) {
 #pragma unroll
-                    for (int u = 0; u < HPT; u += 4) {
+                    for (int u = 0; u < kHpt; u += 4) {
                         const float4 cf = *reinterpret_cast<const float4*>(coef_s + u0 + u);
                         ca2[u / 2] = f2_mul(f2(cf.x, cf.y), f2(st_raw, st_raw));
                         ca2[u / 2 + 1] = f2_mul(f2(cf.z, cf.w), f2(st_raw, st_raw));
@@ -616,7 +624,7 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
                 // ---- exact maxima of this tile's logits and contributions, per row ----
                 const float ls = st > 0.f ? log2f(st) : -INFINITY;
 #pragma unroll
-                for (int u = 0; u < HPT; ++u) {
+                for (int u = 0; u < kHpt; ++u) {
                     const float2 xp = f2_unpack(x2[u / 2]);
                     const float xu = (u & 1) ? xp.y : xp.x;
                     const float xv = xu == xu ? xu : -INFINITY;
@@ -680,7 +688,7 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
                 weigh();
                 group_sync(grp);                             // red_s, corr_s are read
             }
-            uint32_t hi[HPT / 4], lo[HPT / 4];
+            uint32_t hi[kHpt / 4], lo[kHpt / 4];
 #pragma unroll
             for (int u = 0; u < HP2; u += 2) {
                 uint32_t h0, l0, h1, l1;
@@ -714,7 +722,7 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
         if (!ok) *(volatile int*)abort_flag = 1;
         // ---- epilogue: row sums over the tokens, then O^T / (f l) ----
 #pragma unroll
-        for (int u = 0; u < HPT; ++u) {
+        for (int u = 0; u < kHpt; ++u) {
             const float2 ls = f2_unpack(lsum2[u / 2]);
             const float v = half_warp_sum((u & 1) ? ls.y : ls.x);
             if ((lane & 15) == 0) red_s[sub * ROWS + u0 + u] = v;
