@@ -9,11 +9,11 @@
 // bf16 parts, w = hi + lo up to 2^-17 of w, both columns of one B operand, so that one tcgen05.mma
 // (M = 128 tokens, N = 2 d_h, K = 16) forms both products; the epilogue adds the parts, squares and sums a
 // token's columns in one thread.  alpha^k is within ~1e-6 of the fp32 form, whose GEMM on the CUDA cores took
-// 50 times as long.  A CTA owns up to 128 tokens: it quantises them once (scale, codes, and the codes' values
+// 30 times as long.  A CTA owns up to 128 tokens: it quantises them once (scale, codes, and the codes' values
 // as the A operand, all d_c columns in shared memory) and runs over its groups, W^K streaming through registers
-// (loads four chunks ahead) into a ring of 32-row chunks.  How many tokens and groups a CTA takes is chosen by
-// the host (plan_q8): whole prompts want 128 tokens and all groups, so that a token is quantised once; a
-// decode step has few tokens and spreads its groups over the GPU.
+// (a chunk of each loader set in flight) into a ring of 32-row chunks.  How many tokens and groups a CTA takes
+// is chosen by the host (plan_q8): whole prompts want 128 tokens and all groups, so that a token is quantised
+// once; a decode step has few tokens and spreads its groups over the GPU.
 //
 // Plain-load kernel (other dimensions): CTA (token tile, g) holds 32 tokens and one group.  It takes
 // each token's scale from its largest magnitude, forms the keys (fp32, one fmaf
@@ -159,13 +159,13 @@ using namespace tc;
 using dec::wait_bounded;
 
 constexpr int kMT = 128;          // rows of the MMA: tokens of a CTA, at most
-constexpr int kLoadWarps = 8;     // of a set; two sets take the chunks of W^K in turn (a set's chunk costs it
-constexpr int kSets = 2;          // ~700 cycles of dependent instructions, the MMAs 256)
+constexpr int kLoadWarps = 8;     // of a set; the sets take the chunks of W^K in turn (a set's chunk costs it
+constexpr int kSets = 3;          // ~1000 cycles of dependent instructions, the MMAs 256)
 constexpr int kEpiWarps = 4;
 constexpr int kMmaWarp = kSets * kLoadWarps + kEpiWarps;
 constexpr int kTcThreads = 32 * (kMmaWarp + 1);
 constexpr int kChunk = 32;        // rows of W^K per ring stage
-constexpr int kAhead = 2;         // chunks of a set in flight in registers
+constexpr int kAhead = 1;         // chunks of a set in flight in registers
 
 template <int DC, int DH>
 struct AppendLayout {
