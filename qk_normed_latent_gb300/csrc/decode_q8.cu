@@ -7,10 +7,11 @@
 //
 // The codes go to the tensor core as they are stored (kind::f8f6f4: no conversion
 // pass, half the shared memory of bf16), and the other operand of each product is
-// split into two e4m3 parts, a = hi + lo, hi = e4m3(a), lo = e4m3(a - hi).  For the
-// bf16 query the sum is exact down to 2^-18 of the row's largest value (8 significant
-// bits in two times 4); for the weights it is off by at most 2^-8, like a bf16
-// rounding.  The RoPE query is two bf16 parts likewise (2^-16).  A tcgen05.mma with
+// split into two 8-bit parts, a = hi + lo, hi = e4m3(a), lo = a - hi rounded.  For the
+// bf16 query (lo in e4m3) the sum is exact down to 2^-18 of the row's largest value (8
+// significant bits in two times 4); for the weights (lo in e5m2, or in e4m3 with an
+// accumulator and a unit of its own) it is off by at most 2^-8, like a bf16 rounding,
+// plus 2^-15 of the row's largest.  The RoPE query is two bf16 parts (2^-16).  A tcgen05.mma with
 // K = 32 costs 45 cycles up to N = 32, 48 at N = 64 and 65 at N = 128 (M = 64 or 128,
 // K-major or MN-major, measured), so both parts as rows of one operand cost little more
 // than one.
@@ -26,22 +27,25 @@
 // what a row costs in shared-memory traffic and loads (4400 cycles for 32 rows x 128 tokens
 // against 2340 for 64 x 64).  A softmax thread is a token and 8 rows: the token's scale,
 // alpha^k and mask are its registers, the row sums stay in registers until the end, and the
-// running maximum is only looked at (one vote a tile) -- it moves when a weight exceeds it
-// by 2^8.
+// running maximum is only looked at (one vote a tile) -- it moves when a weight outgrows e4m3.
 //
 // Weights in units of the output.  P carries s_t, so that the output product runs on
-// the bare codes: p_{t,h} = 32 2^(x_t - m_h) s_t 2^(m_h - v_h) with m_h the running
+// the bare codes: p_{t,h} = 16 2^(x_t - m_h) s_t 2^(m_h - v_h) with m_h the running
 // maximum of the logits x (log2) and v_h that of x + log2 s, the largest single
 // contribution -- a maximum over logits alone would push the weights of ordinary
 // tokens beside an outlier's scale below e4m3's range.  m and v are integers: every
-// rescale is a power of two, hence exact.
+// rescale is a power of two, hence exact.  A move costs a tile's time (2350 cycles: O^T is
+// rescaled, so the previous output product has to end first), and the slowest CTA of a call
+// had 20 when the first tile's largest contribution was put at 8 of at most 256 (64 x 4096
+// tokens 111 us against 95, 4 x 262144 301 against 279).  With the remainders in e5m2, down
+// to 2^-16, it sits at 2 .. 4 of at most 448 and a move is rare.
 //
 // What bounds it (512 / 64, 64 rows): a tile takes 2340 cycles, of which the tensor core
 // needs 2076 (20 x 65 + 16 x 48); the rest is the one S buffer's hand-over (MMA done ->
-// read -> next MMA).  64 sequences x 4096 tokens x 128 heads: 111 us (1.77 TB/s, 0.66 PFLOP/s
-// counted once; the two parts make it 1.3), of which ~33 us are the start and end of the
-// items; 4 x 262144 tokens: 301 us (0.97 PFLOP/s).  The bf16 pair kernel takes 119 and 372 us.
-// With 16 rows (d_c = 256) the calls are latency-bound: 16 sequences of 1k-8k tokens 17 us.
+// read -> next MMA).  64 sequences x 4096 tokens x 128 heads: 95 us (2.07 TB/s, 0.77 PFLOP/s
+// counted once; the two parts make it 1.5), of which ~15 us are the start and end of the
+// items; 4 x 262144 tokens: 279 us (1.05 PFLOP/s).  The bf16 pair kernel takes 119 and 372 us.
+// With 16 rows (d_c = 256) the calls are latency-bound: 16 sequences of 1k-8k tokens 16 us.
 //
 // Warps: 0 TMA producer (+ TMEM owner), 1 logit MMAs, 2 output MMAs (each issue loop in
 // one elected lane: a branch on the lane number costs ~88 cycles an MMA), then softmax and
@@ -66,8 +70,10 @@ using namespace dec;
 constexpr int kT = 64;               // tokens per tile
 constexpr int kHpt = 8;              // query rows of a softmax thread
 constexpr uint32_t kTmemCols = 512;
-constexpr float kPUnit = 32.f;       // P of the largest contribution: lazy maxima let it grow to 2^8 < 448
-constexpr float kLazy = 256.f;       // a weight (or a scaled one) above this moves the running maxima
+constexpr float kPUnit = 16.f;       // P of a contribution of 2^v
+constexpr float kTopP = 448.f;       // a P above this (e4m3's largest value) moves the running maxima,
+constexpr float kTopE = 1.09951163e12f;   // and so does 2^(x - m) above 2^40, fp32's margin for the row sums
+constexpr float kLoUnit = 16.f;      // of the remainder's column where it has an accumulator of its own
 
 template <int DC, int DR, int ROWS>
 struct Q8Layout {
@@ -144,15 +150,25 @@ __device__ __forceinline__ void split_e4m3(float a, float b, uint32_t& hi, uint3
     hi = h;
     lo = l;
 }
-// The same through fp16, for weights: fp16 holds 11 of their bits, hi and lo keep 8, and the
-// remainder is one packed subtraction.
-__device__ __forceinline__ void split_e4m3_f16(float2 v, uint32_t& hi, uint32_t& lo) {
+// Weights, through fp16 (11 of their bits).  The remainder of hi, at most half a step, is exact; it is stored in
+// e5m2, whose half step is at most 2^-8 of the weight and which reaches to 2^-16, or (STACKED, one operand type
+// for both) kLoUnit times in e4m3: 2^-9 and 2^-13.  One packed subtraction.
+template <bool STACKED>
+__device__ __forceinline__ void split_weight(float2 v, uint32_t& hi, uint32_t& lo) {
     const __half2 w = __floats2half2_rn(v.x, v.y);
     const __nv_fp8x2_storage_t h =
         __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(w), __NV_SATFINITE, __NV_E4M3);
-    const __half2 r = __hsub2(w, __half2(__nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3)));
+    __half2 r = __hsub2(w, __half2(__nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3)));
+    if constexpr (STACKED) r = __hmul2(r, __float2half2_rn(kLoUnit));
     hi = h;
-    lo = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(r), __NV_SATFINITE, __NV_E4M3);
+    lo = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(r), __NV_SATFINITE, STACKED ? __NV_E4M3 : __NV_E5M2);
+}
+
+template <int W>
+__device__ __forceinline__ void store_codes(uint8_t* at, const uint32_t (&w)[W]) {
+    if constexpr (W == 4) *reinterpret_cast<uint4*>(at) = make_uint4(w[0], w[1], w[2], w[3]);
+    else if constexpr (W == 2) *reinterpret_cast<uint2*>(at) = make_uint2(w[0], w[1]);
+    else *reinterpret_cast<uint32_t*>(at) = w[0];
 }
 
 // Vote and barrier of a softmax group (named barriers 1 ..).
@@ -355,14 +371,10 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
                 hi[k] = h0 | (h1 << 16);
                 lo[k] = l0 | (l1 << 16);
             }
-#pragma unroll
-            for (int k = 0; k < DC / 128; ++k) {
-                const int col = lane * (DC / 32) + 4 * k, c = col & 127;
-                const uint32_t blk = (uint32_t)(col >> 7) * (N * 128);
-                const uint32_t h = (uint32_t)r, l = (uint32_t)(r + ROWS);
-                *reinterpret_cast<uint32_t*>(sQ + blk + h * 128 + (((c >> 4) ^ (h & 7)) << 4) + (c & 15)) = hi[k];
-                *reinterpret_cast<uint32_t*>(sQ + blk + l * 128 + (((c >> 4) ^ (l & 7)) << 4) + (c & 15)) = lo[k];
-            }
+            const int col = lane * (DC / 32), c = col & 127;  // a lane's codes lie within a 16-byte chunk
+            const uint32_t h = (uint32_t)r, l = (uint32_t)(r + ROWS), blk = (uint32_t)(col >> 7) * (N * 128);
+            store_codes<DC / 128>(sQ + blk + h * 128 + (((c >> 4) ^ (h & 7)) << 4) + (c & 15), hi);
+            store_codes<DC / 128>(sQ + blk + l * 128 + (((c >> 4) ^ (l & 7)) << 4) + (c & 15), lo);
             float ss = 0.f;
 #pragma unroll
             for (int k = 0; k < DR / 32; ++k) ss = fmaf(rv[k], rv[k], ss);
@@ -371,14 +383,14 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
             const float beta = p.scale * kLog2e * (p.plain ? 1.f : 1.f / sqrtf(ss / (float)DR + p.eps));
 #pragma unroll
             for (int k = 0; k < DR / 32; ++k) {
-                const int c = lane * (DR / 32) + k;
+                const int cr = lane * (DR / 32) + k;
                 const float val = rv[k] * gq[k] * beta;
-                const __nv_bfloat16 h = __float2bfloat16_rn(val);
-                const __nv_bfloat16 l = __float2bfloat16_rn(val - __bfloat162float(h));
-                const uint32_t oh = DR == 64 ? sw128_offset(r, c) : sw64_offset(r, c);
-                const uint32_t ol = DR == 64 ? sw128_offset(r + ROWS, c) : sw64_offset(r + ROWS, c);
-                *reinterpret_cast<__nv_bfloat16*>(sQ + LY::kQLat + oh) = h;
-                *reinterpret_cast<__nv_bfloat16*>(sQ + LY::kQLat + ol) = l;
+                const __nv_bfloat16 vh = __float2bfloat16_rn(val);
+                const __nv_bfloat16 vl = __float2bfloat16_rn(val - __bfloat162float(vh));
+                const uint32_t oh = DR == 64 ? sw128_offset(r, cr) : sw64_offset(r, cr);
+                const uint32_t ol = DR == 64 ? sw128_offset(r + ROWS, cr) : sw64_offset(r + ROWS, cr);
+                *reinterpret_cast<__nv_bfloat16*>(sQ + LY::kQLat + oh) = vh;
+                *reinterpret_cast<__nv_bfloat16*>(sQ + LY::kQLat + ol) = vl;
             }
             if (lane == 0) {
                 coef_s[r] = p.scale * kLog2e * sq * aq4[i];
@@ -458,7 +470,7 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
     } else if (warp == 2) {
         // ===================== output MMAs (a thread of their own: neither issue waits for the other's data) ==========
         if (elect_one()) {
-            const uint32_t id_o = idesc_e4m3(128, LY::kON, 1, 1);
+            const uint32_t id_o[2] = {idesc_e4m3(128, LY::kON, 1, 1), idesc_e4m3(128, LY::kON, 1, 1, 1)};   // hi, lo
             // A: a chunk's 128 latents x 32 tokens, MN-major (8-token groups kGroup apart).  B: P, MN-major:
             // a token's codes in as many bytes (swizzle of the same width), 8-token groups kPGroup apart.
             constexpr int PN = LY::kON;
@@ -479,7 +491,7 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
 #pragma unroll
                         for (int part = 0; part < (LY::kStacked ? 1 : 2); ++part)
                             mma_f8(tmem + LY::kColO + c * PN, lat + (uint64_t)((c * 1024 + kk * 4 * LY::kGroup) >> 4),
-                                   pw + (uint64_t)((kk * 4 * LY::kPGroup + part * 8 * PN) >> 4), id_o,
+                                   pw + (uint64_t)((kk * 4 * LY::kPGroup + part * 8 * PN) >> 4), id_o[part],
                                    (j > 0 || kk > 0 || part > 0) ? 1u : 0u);
                 mma_commit(&empty[s]);
                 mma_commit(&odone[s]);
@@ -597,11 +609,11 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
             }
             const float st = any_sees ? st_raw : 0.f;
             uint64_t e2[HP2], w2[HP2];
-            float top = 0.f;
+            float top_e, top_w;
             // weights e = 2^(x - m) and, in units of the output product, w = e s_t f
             auto weigh = [&]() {
                 const uint64_t st2 = f2(st, st);
-                float t4[2] = {0.f, 0.f};
+                top_e = top_w = 0.f;
 #pragma unroll
                 for (int u = 0; u < HP2; ++u) {
                     const float2 d = f2_unpack(f2_add(x2[u], nm2[u]));
@@ -609,16 +621,16 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
                     e2[u] = f2(e.x, e.y);
                     w2[u] = f2_mul(e2[u], f2_mul(st2, f2v[u]));
                     const float2 w = f2_unpack(w2[u]);
-                    t4[u & 1] = fmax3(t4[u & 1], fmaxf(e.x, e.y), fmaxf(w.x, w.y));
+                    top_e = fmax3(top_e, e.x, e.y);
+                    top_w = fmax3(top_w, w.x, w.y);
                 }
-                top = fmaxf(t4[0], t4[1]);
                 if (masked && !sees) {                       // a row without a token yet has -inf less -inf
 #pragma unroll
                     for (int u = 0; u < HP2; ++u) e2[u] = w2[u] = f2(0.f, 0.f);
                 }
             };
             weigh();
-            const bool need = top > kLazy || j == 0;
+            const bool need = top_w > kTopP || top_e > kTopE || j == 0;
             if (group_any(grp, need || !got_s)) {
                 if (group_any(grp, !got_s)) { ok = false; break; }
                 // ---- exact maxima of this tile's logits and contributions, per row ----
@@ -692,8 +704,8 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
 #pragma unroll
             for (int u = 0; u < HP2; u += 2) {
                 uint32_t h0, l0, h1, l1;
-                split_e4m3_f16(f2_unpack(w2[u]), h0, l0);
-                split_e4m3_f16(f2_unpack(w2[u + 1]), h1, l1);
+                split_weight<LY::kStacked>(f2_unpack(w2[u]), h0, l0);
+                split_weight<LY::kStacked>(f2_unpack(w2[u + 1]), h1, l1);
                 hi[u / 2] = h0 | (h1 << 16);
                 lo[u / 2] = l0 | (l1 << 16);
                 lsum2[u] = f2_add(lsum2[u], e2[u]);
@@ -763,7 +775,7 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
                     tmem_ld16(tmem + LY::kColO + c * LY::kON + ROWS + ug + lane_base, a);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int u = 0; u < 16; ++u) val[u] += __uint_as_float(a[u]);
+                    for (int u = 0; u < 16; ++u) val[u] = fmaf(__uint_as_float(a[u]), 1.f / kLoUnit, val[u]);
                 }
 #pragma unroll
                 for (int u = 0; u < 16; ++u) val[u] = inv[u] == 0.f ? 0.f : val[u] * inv[u];

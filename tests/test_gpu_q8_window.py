@@ -3,11 +3,13 @@ plain 64-bit forms.
 
 Tolerances.  CUDA-core kernel: fp32 throughout, the fp32 rule of this method (rel-L2 and element-wise
 1e-5).  Tensor-core kernels: the weights of the output product are rounded -- 8-bit cache: to the sum of
-two e4m3 values, off by at most 2^-4 x 2^-4 = 2^-8 of the weight; bf16 cache: to bf16, 2^-8 -- so |o - ref|
+two 8-bit values, off by at most 2^-4 x 2^-4 = 2^-8 of the weight; bf16 cache: to bf16, 2^-8 -- so |o - ref|
 <= 2^-8 sum_t p_t |c_t|, and rel-L2 stays within the method's rule for a bf16 cache, 5e-3, max-abs 2e-2 of
 the output's scale.  lse (fp32) of the 8-bit cache has no rounded weight in it: RoPE queries as two bf16
 parts leave 2^-16 of a logit part of at most d_r max|gamma| scale < 8, far below 1e-3.
 """
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -241,6 +243,39 @@ def test_q8_rising_logits(Q):
     c.o, c.lse = o[None], lse[None]
     for splits in (1, 0):
         check(Q, c, simt=False, num_splits=splits)
+
+
+@pytest.mark.parametrize("binades", [8, 11, 14])
+@pytest.mark.parametrize("shape", [dict(), dict(H=32, G=2), dict(H=64, G=8, d_c=512, d_r=64)])
+def test_q8_heavy_token_over_flat_background(Q, shape, binades):
+    """One token outweighs each of 20000 others by 2^binades, and together they outweigh it or nearly: what
+    the 8-bit weights keep of small ones.  A contribution p_t s_t is off by 2^-8 of itself (2^-11 more from
+    its rounding to fp16, 2^-12 for the logit) and by 2^-15 of the row's largest."""
+    T = 20000
+    c = R.Case([T], plain=True, outlier=1.0, seed=9, **shape)
+    g = np.random.Generator(np.random.PCG64(binades))
+    base = c.qt[0, 0, 0]
+    c.qt[:] = R.bf16(base * (1 + 0.01 * g.standard_normal(c.qt.shape)))
+    lat = (0.3 * g.standard_normal((T, c.d_c))).astype(np.float32)
+    lat[0] += base * (binades * math.log(2) / (c.scale * np.linalg.norm(base) ** 2))
+    codes, sc = R.quantise(lat)
+    t = np.arange(T)
+    slot = c.table[0, t // c.page] * c.page + t % c.page
+    c.kv[slot, :c.d_c], c.kv_scale[slot] = codes, sc
+    kr = (c.kv[slot, c.d_c:].copy().view(np.uint16).astype(np.uint32) << 16).view(np.float32) * np.float32(0.1)
+    c.kv[slot, c.d_c:] = R.bf16_bits(kr).view(np.uint8)
+    kr = R.bf16(kr)
+    x = R.e4m3_decode(codes)
+    o, lse = R.attention(c.qt[0], c.aq[0], c.qr[0].astype(np.float64), x * sc[:, None], kr, np.ones((T, c.G)), 1, T, 0, 0,
+                         c.scale, True)
+    logit = c.scale * (c.qt[0, 0].astype(np.float64) @ (x * sc[:, None]).T + c.qr[0, 0].astype(np.float64) @ kr.T)
+    a = np.exp(logit - lse[0][:, None]) * sc                                  # contributions, [H, T]
+    off = (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -12) * a + 2.0 ** -15 * a.max(axis=1, keepdims=True)
+    got, got_lse = Device(Q, c).run(Q)
+    assert (np.abs(got[0, 0] - o[0]) <= off @ np.abs(x) + 1e-6).all()
+    assert np.abs(got_lse[0] - lse).max() <= 1e-3
+    print("share of the heavy token", np.exp(logit[0, 0] - lse[0, 0]), "of the bound used",
+          (np.abs(got[0, 0] - o[0]) / (off @ np.abs(x))).max(), "rel-L2", np.linalg.norm(got[0] - o) / np.linalg.norm(o))
 
 
 APPEND = [
