@@ -11,7 +11,7 @@
 //   * items are numbered by sequence, longest first (ties by index), so the
 //     work that bounds the tail starts first; an item's index is also the index
 //     of its partial output when its sequence is split.
-// Ranking costs B^2 / threads comparisons, so this path serves batches of up to
+// Ranking costs B^2 / 32 / warps votes, so this path serves batches of up to
 // kMaxBSched sequences; larger batches use the scheduler kernel.
 #pragma once
 
@@ -29,8 +29,7 @@ struct SchedSmem {
     int base[kMaxBSched];      // first item of sequence b
     int by_rank[kMaxBSched];   // sequence at rank k
     int split[kMaxBSched];     // the split sequences (ns > 1), in rank order
-    int red[32];
-    int n_items, n_split, tpi;
+    int n_items, n_split;
 };
 
 // Block-wide: every thread of the CTA calls it; on return `S` holds the plan.
@@ -40,8 +39,8 @@ struct SchedSmem {
 template <bool SPLITS_ONLY = false>
 __device__ __forceinline__ void compute_schedule(const int32_t* __restrict__ seq_lens, int B, int s_q,
                                                  const SchedArgs& a, SchedSmem& S, int* status, bool report_errors) {
-    const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = (nt + 31) >> 5;
-    int tot = 0, mx = 0;
+    constexpr int K = kMaxBSched / 32;
+    const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = nt >> 5;
     for (int b = tid; b < B; b += nt) {
         const int L = __ldcg(seq_lens + b);   // through L2: the lengths may change between calls
         S.len[b] = L;
@@ -52,55 +51,48 @@ __device__ __forceinline__ void compute_schedule(const int32_t* __restrict__ seq
             tl = TileRange(L, s_q, a.window, a.sinks, a.tile).count;
         }
         S.tb[b] = tl;
-        tot += tl;
-        mx = max(mx, tl);
     }
+    __syncthreads();
+    // every warp holds all tile counts, sequence 32 i + lane in tb[i], and forms the totals and its share of the
+    // ranks with votes: no further barrier until the ranks are written
+    int tb[K], tot = 0, m = 0;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        tot += __shfl_xor_sync(0xffffffffu, tot, o);
-        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    for (int i = 0; i < K; ++i) {
+        tb[i] = 32 * i + lane < B ? S.tb[32 * i + lane] : -1;
+        tot += max(tb[i], 0);
+        m = max(m, tb[i]);
     }
-    if (lane == 0) S.red[warp] = tot;
-    __syncthreads();
-    if (tid == 0) {
-        int t = 0;
-        for (int w = 0; w < nw; ++w) t += S.red[w];
-        S.n_items = t;                       // s_total for now
-    }
-    __syncthreads();
-    if (lane == 0) S.red[warp] = mx;
-    __syncthreads();
-    if (tid == 0) {
-        int m = 0;
-        for (int w = 0; w < nw; ++w) m = max(m, S.red[w]);
-        const float ideal = (float)S.n_items * a.n_rb / (float)a.sms;
-        const int tpi = (float)m <= 1.25f * ideal ? m : (int)ceilf(ideal);
-        S.tpi = max(max(tpi, a.min_tokens / a.tile), 1);
-        if constexpr (SPLITS_ONLY) S.n_split = (a.fixed_splits == 0 && m <= S.tpi) ? 0 : -1;
-    }
-    __syncthreads();
-    const int tpi = S.tpi;
+    tot = __reduce_add_sync(0xffffffffu, tot);
+    m = __reduce_max_sync(0xffffffffu, m);
+    const float ideal = (float)tot * a.n_rb / (float)a.sms;
+    const int tpi = max(max((float)m <= 1.25f * ideal ? m : (int)ceilf(ideal), a.min_tokens / a.tile), 1);
     if constexpr (SPLITS_ONLY) {
-        if (S.n_split == 0) return;        // uniform: written before the barrier
-    }
-    for (int b = tid; b < B; b += nt) {
-        const int tb = S.tb[b];
-        int rk = 0;
-        for (int o = 0; o < B; ++o) {
-            const int to = S.tb[o];
-            rk += (to > tb) || (to == tb && o < b);
+        if (a.fixed_splits == 0 && m <= tpi) {      // uniform
+            if (tid == 0) S.n_split = 0;
+            __syncthreads();
+            return;
         }
-        S.by_rank[rk] = b;
-        S.ns[b] = a.fixed_splits > 0 ? max(1, min(a.fixed_splits, tb)) : max(1, (tb + tpi - 1) / tpi);
+    }
+    for (int b = warp; b < B; b += nw) {
+        const int mine = S.tb[b];
+        int rk = 0;
+#pragma unroll
+        for (int i = 0; i < K; ++i)
+            if (32 * i < B)
+                rk += __popc(__ballot_sync(0xffffffffu, tb[i] > mine || (tb[i] == mine && 32 * i + lane < b)));
+        if (lane == 0) {
+            S.by_rank[rk] = b;
+            S.ns[b] = a.fixed_splits > 0 ? max(1, min(a.fixed_splits, mine)) : max(1, (mine + tpi - 1) / tpi);
+        }
     }
     __syncthreads();
     // exclusive prefix of the item counts in rank order (one warp, B <= 128: four ranks a lane)
     if (warp == 0) {
-        int v[kMaxBSched / 32], sp[kMaxBSched / 32];
+        int v[K], sp[K];
         int run = 0, nsp = 0;
 #pragma unroll
-        for (int i = 0; i < kMaxBSched / 32; ++i) {
-            const int k = lane * (kMaxBSched / 32) + i;
+        for (int i = 0; i < K; ++i) {
+            const int k = lane * K + i;
             v[i] = k < B ? S.ns[S.by_rank[k]] : 0;
             sp[i] = (k < B && v[i] > 1) ? 1 : 0;
             run += v[i];
@@ -115,8 +107,8 @@ __device__ __forceinline__ void compute_schedule(const int32_t* __restrict__ seq
         }
         int acc = incl - run, acc_sp = incl_sp - nsp;
 #pragma unroll
-        for (int i = 0; i < kMaxBSched / 32; ++i) {
-            const int k = lane * (kMaxBSched / 32) + i;
+        for (int i = 0; i < K; ++i) {
+            const int k = lane * K + i;
             if (k < B) {
                 const int b = S.by_rank[k];
                 S.base[b] = acc;
