@@ -42,10 +42,10 @@
 //
 // What bounds it (512 / 64, 64 rows): a tile takes 2340 cycles, of which the tensor core
 // needs 2076 (20 x 65 + 16 x 48); the rest is the one S buffer's hand-over (MMA done ->
-// read -> next MMA).  64 sequences x 4096 tokens x 128 heads: 95 us (2.07 TB/s, 0.77 PFLOP/s
+// read -> next MMA).  64 sequences x 4096 tokens x 128 heads: 94 us (2.09 TB/s, 0.78 PFLOP/s
 // counted once; the two parts make it 1.5), of which ~15 us are the start and end of the
 // items; 4 x 262144 tokens: 279 us (1.05 PFLOP/s).  The bf16 pair kernel takes 119 and 372 us.
-// With 16 rows (d_c = 256) the calls are latency-bound: 16 sequences of 1k-8k tokens 16 us.
+// With 16 rows (d_c = 256) the calls are latency-bound: 16 sequences of 1k-8k tokens 15 us.
 //
 // Warps: 0 TMA producer (+ TMEM owner), 1 logit MMAs, 2 output MMAs (each issue loop in
 // one elected lane: a branch on the lane number costs ~88 cycles an MMA), then softmax and
@@ -141,27 +141,21 @@ struct Q8Params {
     int* status;
 };
 
-// hi and lo e4m3 parts of two values, each pair packed in 16 bits: exact remainders.
-__device__ __forceinline__ void split_e4m3(float a, float b, uint32_t& hi, uint32_t& lo) {
-    const __nv_fp8x2_storage_t h = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-    const float2 back = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3)));
-    const __nv_fp8x2_storage_t l =
-        __nv_cvt_float2_to_fp8x2(make_float2(a - back.x, b - back.y), __NV_SATFINITE, __NV_E4M3);
-    hi = h;
-    lo = l;
-}
-// Weights, through fp16 (11 of their bits).  The remainder of hi, at most half a step, is exact; it is stored in
-// e5m2, whose half step is at most 2^-8 of the weight and which reaches to 2^-16, or (STACKED, one operand type
-// for both) kLoUnit times in e4m3: 2^-9 and 2^-13.  One packed subtraction.
-template <bool STACKED>
-__device__ __forceinline__ void split_weight(float2 v, uint32_t& hi, uint32_t& lo) {
+// Two values as two 8-bit parts each, hi = e4m3(a) and lo = unit (a - hi), a pair packed in 16 bits.  Through fp16,
+// which holds what matters of both operands (a scaled bf16 query exactly down to 2^-17, 11 bits of a weight) and
+// has packed conversions; the remainder, at most half a step, is exact.  For the weights lo is stored in e5m2,
+// whose half step is at most 2^-8 of the weight and which reaches to 2^-16, or, where one operand holds both
+// parts and has one type, with kLoUnit in e4m3: 2^-9 and 2^-13.
+enum class Lo { e4m3, e5m2, e4m3_unit };
+template <Lo L>
+__device__ __forceinline__ void split8(float2 v, uint32_t& hi, uint32_t& lo) {
     const __half2 w = __floats2half2_rn(v.x, v.y);
     const __nv_fp8x2_storage_t h =
         __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(w), __NV_SATFINITE, __NV_E4M3);
     __half2 r = __hsub2(w, __half2(__nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3)));
-    if constexpr (STACKED) r = __hmul2(r, __float2half2_rn(kLoUnit));
+    if constexpr (L == Lo::e4m3_unit) r = __hmul2(r, __float2half2_rn(kLoUnit));
     hi = h;
-    lo = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(r), __NV_SATFINITE, STACKED ? __NV_E4M3 : __NV_E5M2);
+    lo = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(r), __NV_SATFINITE, L == Lo::e5m2 ? __NV_E5M2 : __NV_E4M3);
 }
 
 template <int W>
@@ -182,16 +176,26 @@ __device__ __forceinline__ bool group_any(int grp, bool pred) {
 }
 __device__ __forceinline__ void group_sync(int grp) { asm volatile("bar.sync %0, 128;" ::"r"(grp + 1) : "memory"); }
 
-// Over the 16 lanes that hold the same rows.
-__device__ __forceinline__ float half_warp_max(float v) {
+// Eight rows' values reduced over the 16 lanes of a half warp that hold them: each exchange halves the rows a lane
+// still holds (4 + 2 + 1 shuffles and one for the last pair of lanes, not 32).  Lane l of the half gets row
+// `half_row(l)`, pairs of lanes the same one.
+__device__ __forceinline__ int half_row(int l) { return ((l >> 3) & 1) * 4 + ((l >> 2) & 1) * 2 + ((l >> 1) & 1); }
+template <typename F>
+__device__ __forceinline__ float half_warp_reduce(const float (&v)[8], int lane, F op) {
+    float a[4], b[2];
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-    return v;
-}
-__device__ __forceinline__ float half_warp_sum(float v) {
+    for (int u = 0; u < 4; ++u) {
+        const float send = (lane & 8) ? v[u] : v[u + 4], keep = (lane & 8) ? v[u + 4] : v[u];
+        a[u] = op(keep, __shfl_xor_sync(0xffffffffu, send, 8));
+    }
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
+    for (int u = 0; u < 2; ++u) {
+        const float send = (lane & 4) ? a[u] : a[u + 2], keep = (lane & 4) ? a[u + 2] : a[u];
+        b[u] = op(keep, __shfl_xor_sync(0xffffffffu, send, 4));
+    }
+    const float send = (lane & 2) ? b[0] : b[1], keep = (lane & 2) ? b[1] : b[0];
+    const float c = op(keep, __shfl_xor_sync(0xffffffffu, send, 2));
+    return op(c, __shfl_xor_sync(0xffffffffu, c, 1));
 }
 
 template <int DC, int DR, int ROWS>
@@ -324,9 +328,9 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
     if (warp == 0) {
         tmem_alloc(tmem_slot, kTmemCols);
         tmem_relinquish();
-        for (int j = 0; j < NST && j < n_t; ++j) {
-            locate_tile(j);
-            if (elect_one()) issue_tile(j);
+        if (n_t > 0) {                                        // the others behind the queries' loads
+            locate_tile(0);
+            if (elect_one()) issue_tile(0);
             __syncwarp();
         }
     } else if (warp >= 3) {
@@ -351,23 +355,22 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
         for (int i = 0; i < kOwn; ++i) {
             const int r = warp - 3 + i * NW;
             const float* rv = rv4[i];
-            float q[DC / 32], top = 0.f;
+            __nv_bfloat162 top2 = __floats2bfloat162_rn(0.f, 0.f);
 #pragma unroll
             for (int k = 0; k < DC / 128; ++k) {
-                const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&raw[i][k].x));
-                const float2 c = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&raw[i][k].y));
-                q[4 * k] = a.x; q[4 * k + 1] = a.y; q[4 * k + 2] = c.x; q[4 * k + 3] = c.y;
+                top2 = __hmax2(top2, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&raw[i][k].x)));
+                top2 = __hmax2(top2, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&raw[i][k].y)));
             }
-#pragma unroll
-            for (int k = 0; k < DC / 32; ++k) top = fmaxf(top, fabsf(q[k]));
             float inv;
-            const float sq = e4m3_scale(warp_max(top), &inv);
+            const float sq = e4m3_scale(warp_max(fmaxf(__low2float(top2), __high2float(top2))), &inv);
             uint32_t hi[DC / 128], lo[DC / 128];              // 4 codes a word
 #pragma unroll
             for (int k = 0; k < DC / 128; ++k) {
+                const float2 a0 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&raw[i][k].x));
+                const float2 a1 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&raw[i][k].y));
                 uint32_t h0, l0, h1, l1;
-                split_e4m3(q[4 * k] * inv, q[4 * k + 1] * inv, h0, l0);
-                split_e4m3(q[4 * k + 2] * inv, q[4 * k + 3] * inv, h1, l1);
+                split8<Lo::e4m3>(make_float2(a0.x * inv, a0.y * inv), h0, l0);
+                split8<Lo::e4m3>(make_float2(a1.x * inv, a1.y * inv), h1, l1);
                 hi[k] = h0 | (h1 << 16);
                 lo[k] = l0 | (l1 << 16);
             }
@@ -380,7 +383,7 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
             for (int k = 0; k < DR / 32; ++k) ss = fmaf(rv[k], rv[k], ss);
             ss = warp_sum(ss);
             // the RoPE query carries scale log2e: R is the RoPE logit in the exp2 domain
-            const float beta = p.scale * kLog2e * (p.plain ? 1.f : 1.f / sqrtf(ss / (float)DR + p.eps));
+            const float beta = p.scale * kLog2e * (p.plain ? 1.f : rsqrtf(ss * (1.f / DR) + p.eps));
 #pragma unroll
             for (int k = 0; k < DR / 32; ++k) {
                 const int cr = lane * (DR / 32) + k;
@@ -408,15 +411,16 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
     if (warp == 0) {
         // ===================== TMA producer =====================
         bool go = true;
-        int j = NST;
+        int j = 1;
         for (; j < n_t && go; ++j) {
             locate_tile(j);
-            go = __all_sync(0xffffffffu, wait_bounded(&empty[j % NST], ((j / NST) - 1) & 1, p.status) &&
-                                             !*(volatile int*)abort_flag);
+            if (j >= NST)
+                go = __all_sync(0xffffffffu, wait_bounded(&empty[j % NST], ((j / NST) - 1) & 1, p.status) &&
+                                                 !*(volatile int*)abort_flag);
             if (go && elect_one()) issue_tile(j);
             // the next tile into L2 while the ring has no room for it: its load then takes the L2's latency
             // (a stage is held for its load, so the load's latency counts against the ring's three tiles)
-            if ((j + 1) % batch && j + 1 < n_t) {
+            if (j >= NST && (j + 1) % batch && j + 1 < n_t) {
                 locate_tile(j + 1);
                 if (elect_one()) prefetch_tile();
             }
@@ -635,16 +639,19 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
                 if (group_any(grp, !got_s)) { ok = false; break; }
                 // ---- exact maxima of this tile's logits and contributions, per row ----
                 const float ls = st > 0.f ? log2f(st) : -INFINITY;
+                float xs[kHpt], vs[kHpt];
 #pragma unroll
                 for (int u = 0; u < kHpt; ++u) {
                     const float2 xp = f2_unpack(x2[u / 2]);
                     const float xu = (u & 1) ? xp.y : xp.x;
-                    const float xv = xu == xu ? xu : -INFINITY;
-                    const float mx = half_warp_max(xv), vx = half_warp_max(xv + ls);
-                    if ((lane & 15) == 0) {
-                        red_s[sub * ROWS + u0 + u] = mx;
-                        red_s[(4 + sub) * ROWS + u0 + u] = vx;
-                    }
+                    xs[u] = xu == xu ? xu : -INFINITY;
+                    vs[u] = xs[u] + ls;
+                }
+                const auto larger = [](float a, float b) { return fmaxf(a, b); };
+                const float mx = half_warp_reduce(xs, lane, larger), vx = half_warp_reduce(vs, lane, larger);
+                if ((lane & 1) == 0) {
+                    red_s[sub * ROWS + u0 + half_row(lane)] = mx;
+                    red_s[(4 + sub) * ROWS + u0 + half_row(lane)] = vx;
                 }
                 group_sync(grp);
                 const int gt = tid - 96 - grp * 128;
@@ -700,12 +707,13 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
                 weigh();
                 group_sync(grp);                             // red_s, corr_s are read
             }
+            constexpr Lo kLo = LY::kStacked ? Lo::e4m3_unit : Lo::e5m2;
             uint32_t hi[kHpt / 4], lo[kHpt / 4];
 #pragma unroll
             for (int u = 0; u < HP2; u += 2) {
                 uint32_t h0, l0, h1, l1;
-                split_weight<LY::kStacked>(f2_unpack(w2[u]), h0, l0);
-                split_weight<LY::kStacked>(f2_unpack(w2[u + 1]), h1, l1);
+                split8<kLo>(f2_unpack(w2[u]), h0, l0);
+                split8<kLo>(f2_unpack(w2[u + 1]), h1, l1);
                 hi[u / 2] = h0 | (h1 << 16);
                 lo[u / 2] = l0 | (l1 << 16);
                 lsum2[u] = f2_add(lsum2[u], e2[u]);
@@ -733,12 +741,15 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
         }
         if (!ok) *(volatile int*)abort_flag = 1;
         // ---- epilogue: row sums over the tokens, then O^T / (f l) ----
+        float ls[kHpt];
 #pragma unroll
-        for (int u = 0; u < kHpt; ++u) {
-            const float2 ls = f2_unpack(lsum2[u / 2]);
-            const float v = half_warp_sum((u & 1) ? ls.y : ls.x);
-            if ((lane & 15) == 0) red_s[sub * ROWS + u0 + u] = v;
+        for (int u = 0; u < HP2; ++u) {
+            const float2 l2 = f2_unpack(lsum2[u]);
+            ls[2 * u] = l2.x;
+            ls[2 * u + 1] = l2.y;
         }
+        const float sum = half_warp_reduce(ls, lane, [](float a, float b) { return a + b; });
+        if ((lane & 1) == 0) red_s[sub * ROWS + u0 + half_row(lane)] = sum;
         const bool got_last = (ok && n_t > 0) ? wait_bounded(&odone[(n_t - 1) % NST], ((n_t - 1) / NST) & 1, p.status) : ok;
         if (group_any(grp, !got_last)) *(volatile int*)abort_flag = 1;
         tc_fence_after();
