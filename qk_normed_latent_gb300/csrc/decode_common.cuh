@@ -26,7 +26,7 @@ struct WorkItem {
 
 // Parameters of the split-KV schedule (see decode_sched.cuh).
 struct SchedArgs {
-    int max_len, n_rb, sms, min_tokens, tile, fixed_splits;
+    int max_len, n_rb, sms, min_tokens, tile, fixed_splits;   // tile: a power of two
     int min_len;           // shortest valid length: s_q, or 0 where rows without a token are allowed
     int window, sinks;     // 0, 0: every tile of the sequence
 };
@@ -37,9 +37,11 @@ struct SchedArgs {
 struct TileRange {
     int count, head, gap;
     __host__ __device__ __forceinline__ TileRange(int len, int s_q, int window, int sinks, int tile) {
-        const int all = (len + tile - 1) / tile;
-        head = (min_(sinks, len) + tile - 1) / tile;
-        const int first = max_(0, len - s_q + 1 - window) / tile;     // first window tile of the first query
+        int sh = 0;                                       // tiles are powers of two
+        while ((1 << sh) < tile) ++sh;
+        const int all = (len + tile - 1) >> sh;
+        head = (min_(sinks, len) + tile - 1) >> sh;
+        const int first = max_(0, len - s_q + 1 - window) >> sh;      // first window tile of the first query
         gap = window > 0 ? max_(0, first - head) : 0;
         if (gap == 0) head = all;
         count = all - gap;

@@ -42,10 +42,10 @@
 //
 // What bounds it (512 / 64, 64 rows): a tile takes 2340 cycles, of which the tensor core
 // needs 2076 (20 x 65 + 16 x 48); the rest is the one S buffer's hand-over (MMA done ->
-// read -> next MMA).  64 sequences x 4096 tokens x 128 heads: 94 us (2.09 TB/s, 0.78 PFLOP/s
-// counted once; the two parts make it 1.5), of which ~15 us are the start and end of the
-// items; 4 x 262144 tokens: 279 us (1.05 PFLOP/s).  The bf16 pair kernel takes 119 and 372 us.
-// With 16 rows (d_c = 256) the calls are latency-bound: 16 sequences of 1k-8k tokens 15 us.
+// read -> next MMA).  64 sequences x 4096 tokens x 128 heads: 88 us (2.22 TB/s, 0.83 PFLOP/s
+// counted once; the two parts make it 1.6), of which ~13 us are the start and end of the
+// items; 4 x 262144 tokens: 269 us (1.09 PFLOP/s).  The bf16 pair kernel takes 119 and 372 us.
+// With 16 rows (d_c = 256) the calls are latency-bound: 16 sequences of 1k-8k tokens 14 us.
 //
 // Warps: 0 TMA producer (+ TMEM owner), 1 logit MMAs, 2 output MMAs (each issue loop in
 // one elected lane: a branch on the lane number costs ~88 cycles an MMA), then softmax and
@@ -226,19 +226,30 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
     float* red_s = inv_s + ROWS;             // [2 kinds][4 warps][ROWS]
 
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;   // warp: uniform
+    if (tid == 32) {                                          // beside the plan's loads; its barriers publish it
+        for (int i = 0; i < LY::kNumBars; ++i) {
+            const bool warps = (&bars[i] >= pfull && &bars[i] < odone) || (&bars[i] >= sfree && &bars[i] < drain);
+            mbar_init(&bars[i], warps ? (uint32_t)NW : 1u);
+        }
+        *abort_flag = 0;
+        fence_barrier_init();
+        prefetch_tmap(&tm_lat);
+        prefetch_tmap(&tm_rope);
+    }
     WorkItem it;
     int seq_len;
     if (p.sched_inline) {
         __shared__ SchedSmem S;
-        compute_schedule(p.seq_lens, p.B, p.s_q, p.sa, S, p.status, blockIdx.x == 0 && blockIdx.y == 0);
+        compute_schedule(p.seq_lens, p.B, p.s_q, p.sa, (int)blockIdx.y, S, p.status, blockIdx.x == 0 && blockIdx.y == 0);
         if ((int)blockIdx.y >= S.n_items) return;
-        it = schedule_item(S, p.B, (int)blockIdx.y);
-        seq_len = S.len[it.b];
+        it = S.item;
+        seq_len = S.item_len;
     } else {
         pdl_wait();
         if ((int)blockIdx.y >= *p.n_items) return;
         it = p.items[blockIdx.y];
         seq_len = p.seq_lens[it.b];
+        __syncthreads();
     }
     const int b = it.b;
     const int n_rows = p.s_q * p.H;
@@ -253,18 +264,7 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
     const int len_last = max(0, len - p.s_q + i_last + 1);
     const int win_first = p.window > 0 ? len - p.s_q + i_first + 1 - p.window : 0;
 
-    if (tid == 0) {
-        if (bad && blockIdx.x == 0) report(p.status, QKMLA_ERR_DEVICE_BOUNDS);
-        for (int i = 0; i < LY::kNumBars; ++i) {
-            const bool warps = (&bars[i] >= pfull && &bars[i] < odone) || (&bars[i] >= sfree && &bars[i] < drain);
-            mbar_init(&bars[i], warps ? (uint32_t)NW : 1u);
-        }
-        *abort_flag = 0;
-        fence_barrier_init();
-        prefetch_tmap(&tm_lat);
-        prefetch_tmap(&tm_rope);
-    }
-    __syncthreads();
+    if (tid == 0 && bad && blockIdx.x == 0) report(p.status, QKMLA_ERR_DEVICE_BOUNDS);
     pdl_wait();
     pdl_trigger();
 

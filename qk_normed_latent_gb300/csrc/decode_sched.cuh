@@ -30,15 +30,19 @@ struct SchedSmem {
     int by_rank[kMaxBSched];   // sequence at rank k
     int split[kMaxBSched];     // the split sequences (ns > 1), in rank order
     int n_items, n_split;
+    WorkItem item;             // the caller's item and its sequence's length
+    int item_len;
 };
 
-// Block-wide: every thread of the CTA calls it; on return `S` holds the plan.
+// Block-wide: every thread of the CTA calls it; on return `S` holds the plan, with item number `item` where it
+// exists (item < S.n_items).
 // Sequences with an invalid length get no tiles (and a status report when
 // `report_errors`).  With SPLITS_ONLY (the combine kernel) a plan without a split
 // sequence ends as soon as that is known: n_split is 0 and nothing else is set.
 template <bool SPLITS_ONLY = false>
 __device__ __forceinline__ void compute_schedule(const int32_t* __restrict__ seq_lens, int B, int s_q,
-                                                 const SchedArgs& a, SchedSmem& S, int* status, bool report_errors) {
+                                                 const SchedArgs& a, int item, SchedSmem& S, int* status,
+                                                 bool report_errors) {
     constexpr int K = kMaxBSched / 32;
     const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = nt >> 5;
     for (int b = tid; b < B; b += nt) {
@@ -80,10 +84,7 @@ __device__ __forceinline__ void compute_schedule(const int32_t* __restrict__ seq
         for (int i = 0; i < K; ++i)
             if (32 * i < B)
                 rk += __popc(__ballot_sync(0xffffffffu, tb[i] > mine || (tb[i] == mine && 32 * i + lane < b)));
-        if (lane == 0) {
-            S.by_rank[rk] = b;
-            S.ns[b] = a.fixed_splits > 0 ? max(1, min(a.fixed_splits, mine)) : max(1, (mine + tpi - 1) / tpi);
-        }
+        if (lane == 0) S.by_rank[rk] = b;
     }
     __syncthreads();
     // exclusive prefix of the item counts in rank order (one warp, B <= 128: four ranks a lane)
@@ -93,8 +94,14 @@ __device__ __forceinline__ void compute_schedule(const int32_t* __restrict__ seq
 #pragma unroll
         for (int i = 0; i < K; ++i) {
             const int k = lane * K + i;
-            v[i] = k < B ? S.ns[S.by_rank[k]] : 0;
-            sp[i] = (k < B && v[i] > 1) ? 1 : 0;
+            v[i] = 0;
+            if (k < B) {
+                const int b = S.by_rank[k], tiles = S.tb[b];
+                v[i] = a.fixed_splits > 0 ? max(1, min(a.fixed_splits, tiles))
+                                          : max(1, (int)((uint32_t)(tiles + tpi - 1) / (uint32_t)tpi));
+                S.ns[b] = v[i];
+            }
+            sp[i] = v[i] > 1 ? 1 : 0;
             run += v[i];
             nsp += sp[i];
         }
@@ -113,6 +120,14 @@ __device__ __forceinline__ void compute_schedule(const int32_t* __restrict__ seq
                 const int b = S.by_rank[k];
                 S.base[b] = acc;
                 if (sp[i]) S.split[acc_sp] = b;
+                if (item >= acc && item < acc + v[i]) {
+                    const int per = (int)((uint32_t)(S.tb[b] + v[i] - 1) / (uint32_t)v[i]);
+                    S.item.b = b;
+                    S.item.tile_begin = (item - acc) * per;
+                    S.item.tile_end = min(S.tb[b], (item - acc + 1) * per);
+                    S.item.part = v[i] > 1 ? item : -1;
+                    S.item_len = S.len[b];
+                }
                 acc += v[i];
             }
             acc_sp += sp[i];
@@ -123,26 +138,6 @@ __device__ __forceinline__ void compute_schedule(const int32_t* __restrict__ seq
         }
     }
     __syncthreads();
-}
-
-// The work item `item` of the plan in `S` (item < S.n_items).
-__device__ __forceinline__ WorkItem schedule_item(const SchedSmem& S, int B, int item) {
-    // the rank whose items contain `item`: bases are increasing in rank order
-    int lo = 0, hi = B - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (S.base[S.by_rank[mid]] <= item) lo = mid; else hi = mid - 1;
-    }
-    const int b = S.by_rank[lo];
-    const int ns = S.ns[b], tb = S.tb[b];
-    const int k = item - S.base[b];
-    const int per = (tb + ns - 1) / ns;
-    WorkItem w;
-    w.b = b;
-    w.tile_begin = k * per;
-    w.tile_end = min(tb, (k + 1) * per);
-    w.part = ns > 1 ? item : -1;
-    return w;
 }
 
 }  // namespace dec

@@ -136,10 +136,10 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
     // is made before the dependency wait, overlapping the previous kernel's tail
     if (p.sched_inline) {
         __shared__ SchedSmem S;
-        compute_schedule(p.seq_lens, p.B, p.s_q, p.sa, S, p.status, item_idx == 0 && blockIdx.x == 0);
+        compute_schedule(p.seq_lens, p.B, p.s_q, p.sa, item_idx, S, p.status, item_idx == 0 && blockIdx.x == 0);
         if (item_idx >= S.n_items) return;
-        it = schedule_item(S, p.B, item_idx);
-        seq_len = S.len[it.b];                     // the plan's copy: no second trip to memory
+        it = S.item;
+        seq_len = S.item_len;                      // the plan's copy: no second trip to memory
     } else {
         pdl_wait();                                // the scheduler kernel's items
         if (item_idx >= *p.n_items) return;
@@ -738,7 +738,7 @@ combine_var_kernel(const float* __restrict__ o_part, const float* __restrict__ l
     __shared__ float w_s[256];
     __shared__ float s_inv, s_lse;
     __shared__ SchedSmem S;
-    if (sched_inline) compute_schedule<true>(seq_lens, B, s_q, sa, S, nullptr, false);
+    if (sched_inline) compute_schedule<true>(seq_lens, B, s_q, sa, -1, S, nullptr, false);
     pdl_wait();
     pdl_trigger();
     const int tasks = (sched_inline ? S.n_split : *n_split) * rows_per_seq;
