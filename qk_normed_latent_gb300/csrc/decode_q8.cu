@@ -41,10 +41,13 @@
 // to 2^-16, it sits at 2 .. 4 of at most 448 and a move is rare.
 //
 // What bounds it (512 / 64, 64 rows): a tile takes 2340 cycles, of which the tensor core
-// needs 2076 (20 x 65 + 16 x 48); the rest is the one S buffer's hand-over (MMA done ->
-// read -> next MMA).  64 sequences x 4096 tokens x 128 heads: 88 us (2.22 TB/s, 0.83 PFLOP/s
-// counted once; the two parts make it 1.6), of which ~13 us are the start and end of the
-// items; 4 x 262144 tokens: 269 us (1.09 PFLOP/s).  The bf16 pair kernel takes 119 and 372 us.
+// needs 2076 (20 x 65 + 16 x 48) and shared memory at 128 bytes a cycle about 2200: the 36
+// MMAs read 6 KB of operands each, 216 KB, the tile is 43 KB, P and the softmax's loads ~20 KB.
+// (With the query parts as the M = 128 operand an MMA takes 48 cycles and S fits twice, but it
+// reads the same 6 KB and the softmax, a thread to a row, loads twice as much: 2900 cycles.)
+// 64 sequences x 4096 tokens x 128 heads: 88 us (2.22 TB/s, 0.83 PFLOP/s counted once; the
+// two parts make it 1.6), of which ~13 us are the start and end of the items; 4 x 262144
+// tokens: 269 us (1.09 PFLOP/s).  The bf16 pair kernel takes 119 and 342 us.
 // With 16 rows (d_c = 256) the calls are latency-bound: 16 sequences of 1k-8k tokens 14 us.
 //
 // Warps: 0 TMA producer (+ TMEM owner), 1 logit MMAs, 2 output MMAs (each issue loop in
