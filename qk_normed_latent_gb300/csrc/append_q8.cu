@@ -221,6 +221,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) append_q8_tc_kernel(const Appen
     const int n0 = blockIdx.x * p.tokens, n_tok = min(p.tokens, p.N - n0);
     const int g0 = blockIdx.y * p.groups, n_g = min(p.groups, p.G - g0);
     const int n_chunks = n_g * (DC / kChunk);
+    // the CTAs start at different groups: together they would read the same few lines of W^K
+    const int g_first = (int)blockIdx.x % n_g;
+    auto group_at = [&](int gi) { return gi + g_first < n_g ? gi + g_first : gi + g_first - n_g; };
 
     if (tid == 0) {
         for (int i = 0; i < NST; ++i) {
@@ -246,7 +249,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) append_q8_tc_kernel(const Appen
     auto fetch = [&](int q, float4 (&v)[kF4]) {
 #pragma unroll
         for (int i = 0; i < kF4; ++i)
-            if (q < n_chunks) v[i] = load_stream(w4 + (int64_t)q * (kChunk * DH / 4) + st + 32 * kLoadWarps * i);
+            if (q < n_chunks)
+                v[i] = load_stream(w4 + (int64_t)(group_at(q / (DC / kChunk)) * (DC / kChunk) + q % (DC / kChunk)) * (kChunk * DH / 4) +
+                                   st + 32 * kLoadWarps * i);
     };
     if (warp < kSets * kLoadWarps) {
 #pragma unroll
@@ -462,7 +467,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) append_q8_tc_kernel(const Appen
             if (lane == 0) mbar_arrive(&dfree[gi & 1]);
             const float mean = ((ss[0] + ss[1]) + (ss[2] + ss[3])) / (float)DH;   // of the keys of the codes
             if (slot >= 0 && slot < p.num_slots)
-                store_alpha(p.ak, slot * p.G + g0 + gi, p.plain ? 1.f : 1.f / sqrtf(s * s * mean + p.eps), p.ak_f16 != 0);
+                store_alpha(p.ak, slot * p.G + g0 + group_at(gi), p.plain ? 1.f : 1.f / sqrtf(s * s * mean + p.eps), p.ak_f16 != 0);
         }
     }
     __syncwarp();
