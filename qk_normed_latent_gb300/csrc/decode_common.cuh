@@ -29,6 +29,7 @@ struct SchedArgs {
     int max_len, n_rb, sms, min_tokens, tile, fixed_splits;   // tile: a power of two
     int min_len;           // shortest valid length: s_q, or 0 where rows without a token are allowed
     int window, sinks;     // 0, 0: every tile of the sequence
+    int chunks;            // a plan of more than one wave may cut chunks (chunks_of; up to 128 sequences)
 };
 
 // Tiles of a sequence that some query of the step sees, numbered 0 .. count - 1:
@@ -52,6 +53,15 @@ private:
     static __host__ __device__ __forceinline__ int min_(int a, int b) { return a < b ? a : b; }
     static __host__ __device__ __forceinline__ int max_(int a, int b) { return a > b ? a : b; }
 };
+
+constexpr int kChunkTiles = 24;   // least share for a plan of chunks: an item's start and end cost about 10 tiles' time
+
+// Chunks where the call allows any split and the lengths can reach the least share.
+inline int chunks_of(const qkmla_decode_args* a, const DecodeExt& x, const SchedArgs& sa) {
+    int64_t tokens = sa.max_len;
+    if (x.window > 0 && (int64_t)x.window + x.sinks + a->s_q < tokens) tokens = (int64_t)x.window + x.sinks + a->s_q;
+    return a->num_splits == 0 && a->B * (tokens / sa.tile + 2) * sa.n_rb >= (int64_t)kChunkTiles * sa.sms ? 1 : 0;
+}
 
 struct TcParams {
     const __nv_bfloat16* qt;   // [B][s_q][H][d_c]

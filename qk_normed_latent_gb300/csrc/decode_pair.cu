@@ -127,7 +127,7 @@ decode_pair_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_cons
     // is made before the dependency wait, overlapping the previous kernel's tail
     if (p.sched_inline) {                                // both CTAs derive the same plan
         __shared__ SchedSmem S;
-        compute_schedule(p.seq_lens, p.B, p.s_q, p.sa, (int)blockIdx.y, S, p.status, blockIdx.x == 0 && blockIdx.y == 0);
+        compute_schedule<WIN>(p.seq_lens, p.B, p.s_q, p.sa, (int)blockIdx.y, S, p.status, blockIdx.x == 0 && blockIdx.y == 0);
         if ((int)blockIdx.y >= S.n_items) return;        // uniform over the cluster
         it = S.item;
         seq_len = S.item_len;                            // the plan's copy

@@ -243,7 +243,7 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
     int seq_len;
     if (p.sched_inline) {
         __shared__ SchedSmem S;
-        compute_schedule(p.seq_lens, p.B, p.s_q, p.sa, (int)blockIdx.y, S, p.status, blockIdx.x == 0 && blockIdx.y == 0);
+        compute_schedule<true>(p.seq_lens, p.B, p.s_q, p.sa, (int)blockIdx.y, S, p.status, blockIdx.x == 0 && blockIdx.y == 0);
         if ((int)blockIdx.y >= S.n_items) return;
         it = S.item;
         seq_len = S.item_len;
@@ -900,6 +900,7 @@ int launch_decode_q8(const qkmla_decode_args* a, const DecodeExt& x, cudaStream_
     sa.min_len = 0;
     sa.window = x.window;
     sa.sinks = x.sinks;
+    sa.chunks = never_splits(a, x) ? 0 : chunks_of(a, x, sa);
     const int sched_inline = sched_in_kernel(a) ? 1 : 0;
     if (!sched_inline && launch_sched(a, sa, w, s) != QKMLA_OK) return QKMLA_ERR_CUDA;
 

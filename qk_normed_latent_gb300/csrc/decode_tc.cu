@@ -136,7 +136,7 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
     // is made before the dependency wait, overlapping the previous kernel's tail
     if (p.sched_inline) {
         __shared__ SchedSmem S;
-        compute_schedule(p.seq_lens, p.B, p.s_q, p.sa, item_idx, S, p.status, item_idx == 0 && blockIdx.x == 0);
+        compute_schedule<WIN>(p.seq_lens, p.B, p.s_q, p.sa, item_idx, S, p.status, item_idx == 0 && blockIdx.x == 0);
         if (item_idx >= S.n_items) return;
         it = S.item;
         seq_len = S.item_len;                      // the plan's copy: no second trip to memory
@@ -738,7 +738,7 @@ combine_var_kernel(const float* __restrict__ o_part, const float* __restrict__ l
     __shared__ float w_s[256];
     __shared__ float s_inv, s_lse;
     __shared__ SchedSmem S;
-    if (sched_inline) compute_schedule<true>(seq_lens, B, s_q, sa, -1, S, nullptr, false);
+    if (sched_inline) compute_schedule<true, true>(seq_lens, B, s_q, sa, -1, S, nullptr, false);
     pdl_wait();
     pdl_trigger();
     const int tasks = (sched_inline ? S.n_split : *n_split) * rows_per_seq;
@@ -1005,6 +1005,7 @@ int launch_decode_tc(const qkmla_decode_args* a, const DecodeExt& x, cudaStream_
     sa.min_len = x.window > 0 ? 0 : a->s_q;
     sa.window = x.window;
     sa.sinks = x.sinks;
+    sa.chunks = x.active() && !never_splits(a, x) ? chunks_of(a, x, sa) : 0;
     // small batches: the decode and combine kernels plan the split themselves
     const int sched_inline = sched_in_kernel(a) ? 1 : 0;
     if (!sched_inline && launch_sched(a, sa, w, s) != QKMLA_OK) return QKMLA_ERR_CUDA;

@@ -278,6 +278,20 @@ def test_q8_heavy_token_over_flat_background(Q, shape, binades):
           (np.abs(got[0, 0] - o[0]) / (off @ np.abs(x))).max(), "rel-L2", np.linalg.norm(got[0] - o) / np.linalg.norm(o))
 
 
+@pytest.mark.parametrize("kw", [
+    dict(H=128, G=8, d_c=128, d_r=64, s_q=8, outlier=3.0),
+    dict(H=64, G=8, d_c=256, d_r=32, s_q=16, outlier=3.0, window=3000, sinks=70),
+    dict(H=64, G=8, d_c=256, d_r=32, s_q=16, cache="bf16", window=100000, sinks=3),
+    dict(H=128, G=8, d_c=512, d_r=64, s_q=8, cache="bf16", window=2900, sinks=130),
+])
+def test_ragged_batch_of_more_than_a_wave(Q, kw):
+    """A plan of chunks and remainders: sequences of several chunks, of exactly one or two, of a chunk and a few
+    tokens, shorter ones, empty ones.  16 row blocks put an even share near 30 tiles."""
+    share = 64 * 30
+    lens = [4 * share + 700, 3 * share, 2 * share + 65, share + 1100, share + 64, share, 900, 513, 512, 64, 1, 0, 0, 333, 2000, 250]
+    check(Q, R.Case(lens, **kw), simt=False)
+
+
 APPEND = [
     dict(N=1), dict(N=16), dict(N=33), dict(N=257, G=8, d_c=512, d_h=128, d_r=64), dict(N=5, G=3, d_c=100, d_h=36, d_r=20),
     dict(N=40, rope=True), dict(N=300, G=8, d_c=512, d_h=128, d_r=64, rope=True), dict(N=20, alpha="f16"),
