@@ -58,7 +58,7 @@ constexpr int tile_of() { return DC == 256 ? 64 : 32; }
 // ---------------------------------------------------------------------------
 // shared-memory layout
 // ---------------------------------------------------------------------------
-template <int DC, int DR, int NST, int KT>
+template <int DC, int DR, int NST, int KT, bool LO>
 struct Layout {
     static constexpr int kLatBlocks = DC / 64;                      // 64-column TMA boxes
     static constexpr int kRopeRowBytes = DR * 2;                    // 128 (SW128) or 64 (SW64)
@@ -73,7 +73,13 @@ struct Layout {
     static constexpr bool kPOwn = kPBytes > kSRope;
     static constexpr int kOffP = kPOwn ? (kSLat + kSRope + kSAk + 1023) / 1024 * 1024 : kSLat;
     static constexpr int kStage = ((kPOwn ? kOffP + kPBytes : kSLat + kSRope + kSAk) + 1023) / 1024 * 1024;
-    static constexpr int kQ = ((kQLat + kQRope) + 1023) / 1024 * 1024;
+    // LO (windowed calls, d_c = 256): what bf16 leaves of the RoPE query as a second part behind it, products into
+    // the same accumulator.  Over a window the rounded query was as large an error of the output as its bf16 weights
+    // (1.3e-3 against 1.2e-3 of its norm, 16 heads x 1004 tokens).  It takes a stage's place: 16 sequences behind a
+    // window of 1000 take 16.0 us, not 15.5; at d_c = 512, stages of 32 tokens, it would be 11 % of a long window's
+    // time.  The call without a window keeps its results.
+    static constexpr bool kLo = LO;
+    static constexpr int kQ = ((kQLat + (LO ? 2 : 1) * kQRope) + 1023) / 1024 * 1024;
     static constexpr int kOffQ = 0;
     static constexpr int kOffStage = kQ;
     static constexpr int kOffMisc = kQ + NST * kStage;
@@ -108,7 +114,7 @@ template <int DC, int DR, bool PLAIN, int NST, int KT, bool AKH, bool WIN>
 __global__ void __launch_bounds__(kThreads, 1)
 decode_tc_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ CUtensorMap tm_rope,
                  const __grid_constant__ CUtensorMap tm_q, const TcParams p) {
-    using LY = Layout<DC, DR, NST, KT>;
+    using LY = Layout<DC, DR, NST, KT, WIN && DC == 256>;
     constexpr int kChunks = LY::kChunks;
     constexpr int NSB = LY::kNSB;
     extern __shared__ __align__(1024) uint8_t smraw[];
@@ -262,9 +268,14 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
 #pragma unroll
             for (int j = 0; j < DR / 2; j += 2) {
                 const int c = half * (DR / 2) + j;
-                __nv_bfloat162 v = __floats2bfloat162_rn(vals[j] * gq[j] * beta, vals[j + 1] * gq[j + 1] * beta);
+                const float x0 = vals[j] * gq[j] * beta, x1 = vals[j + 1] * gq[j + 1] * beta;
+                __nv_bfloat162 v = __floats2bfloat162_rn(x0, x1);
                 const uint32_t off = (DR == 64) ? sw128_offset(r, c) : sw64_offset(r, c);
                 *reinterpret_cast<__nv_bfloat162*>(qrope + off) = v;
+                if constexpr (LY::kLo) {
+                    const float2 f = __bfloat1622float2(v);
+                    *reinterpret_cast<__nv_bfloat162*>(qrope + LY::kQRope + off) = __floats2bfloat162_rn(x0 - f.x, x1 - f.y);
+                }
             }
             if (half == 0) coef_s[r] = p.scale * a * kLog2e;
         }
@@ -345,17 +356,19 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
                     }
                 }
 #pragma unroll
-                for (int kk = 0; kk < DR / 16; ++kk) {
+                for (int k2 = 0; k2 < (LY::kLo ? 2 : 1) * (DR / 16); ++k2) {
+                    const int kk = k2 % (DR / 16), part = k2 / (DR / 16);
+                    const uint32_t qr = q_addr + LY::kQLat + part * LY::kQRope;
                     uint64_t a, bd;
                     if (DR == 64) {
-                        a = smem_desc(q_addr + LY::kQLat + kk * 32, 16, 1024, kSwizzle128B);
+                        a = smem_desc(qr + kk * 32, 16, 1024, kSwizzle128B);
                         bd = smem_desc(st_addr + LY::kSLat + kk * 32, 16, 1024, kSwizzle128B);
                     } else {
-                        a = smem_desc(q_addr + LY::kQLat + kk * 32, 16, 512, kSwizzle64B);
+                        a = smem_desc(qr + kk * 32, 16, 512, kSwizzle64B);
                         bd = smem_desc(st_addr + LY::kSLat + kk * 32, 16, 512, kSwizzle64B);
                     }
                     if (!PLAIN) {
-                        mma_bf16(d_r, a, bd, id_s, kk > 0 ? 1u : 0u);
+                        mma_bf16(d_r, a, bd, id_s, k2 > 0 ? 1u : 0u);
                     } else {
                         mma_bf16(d_c, a, bd, id_s, 1u);      // plain MLA: one accumulation over K = d_c + d_r
                     }
@@ -839,7 +852,7 @@ template <int DC, int DR, bool PLAIN, int NST, bool AKH, bool WIN>
 int launch_kernel_w(const CUtensorMap& lat, const CUtensorMap& rope, const CUtensorMap& qmap, const TcParams& tp,
                   int n_rb, int max_items, cudaStream_t s) {
     constexpr int KT = tile_of<DC>();
-    using LY = Layout<DC, DR, NST, KT>;
+    using LY = Layout<DC, DR, NST, KT, WIN && DC == 256>;
     auto k = decode_tc_kernel<DC, DR, PLAIN, NST, KT, AKH, WIN>;
     static_assert(LY::kBytes <= 232448, "shared memory budget");
     if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, LY::kBytes) != cudaSuccess)
@@ -852,7 +865,7 @@ int launch_kernel_w(const CUtensorMap& lat, const CUtensorMap& rope, const CUten
 template <int DC, int DR, bool PLAIN, int NST, bool AKH>
 int launch_kernel(const CUtensorMap& lat, const CUtensorMap& rope, const CUtensorMap& qmap, const TcParams& tp,
                   int n_rb, int max_items, cudaStream_t s) {
-    return tp.window > 0 ? launch_kernel_w<DC, DR, PLAIN, NST, AKH, true>(lat, rope, qmap, tp, n_rb, max_items, s)
+    return tp.window > 0 ? launch_kernel_w<DC, DR, PLAIN, DC == 256 ? NST - 1 : NST, AKH, true>(lat, rope, qmap, tp, n_rb, max_items, s)
                          : launch_kernel_w<DC, DR, PLAIN, NST, AKH, false>(lat, rope, qmap, tp, n_rb, max_items, s);
 }
 
