@@ -75,10 +75,18 @@ constexpr int kOffX = kOffStage + kNst * kStageB;      // received partials
 constexpr int kOffY = kOffX + kXB;                     // own partials (sent)
 constexpr int kOffMisc = kOffY + kXB;
 constexpr int kNumBars = 23;
-constexpr int kBytesP = kOffMisc + kNumBars * 8 + 16 + kR * 4 + 1024;
+// Windowed calls: what bf16 leaves of the RoPE query's first 16 columns in this CTA (rows of 32 bytes, 32-byte
+// swizzle), a second product into the same accumulator.  Over a window the rounded query is as large an error of
+// the output as its bf16 weights (about 1.3e-3 of its norm each); what fits beside the ring and the exchange halves
+// its square.  The plan's scratch lies in the received partials' place there.
+constexpr int kQLo = kR * 32;
+constexpr int kOffLo = (kOffMisc + kNumBars * 8 + 16 + kR * 4 + 255) / 256 * 256;
+template <bool WIN>
+constexpr int kBytesP = (WIN ? kOffLo + kQLo : kOffMisc + kNumBars * 8 + 16 + kR * 4) + 1024;
 static_assert(kStageB % 1024 == 0 && kOffStage % 1024 == 0 && kOffX % 16 == 0 && kOffY % 16 == 0, "align");
 static_assert(kXSlice % 16 == 0, "bulk copy size");
-static_assert(kBytesP <= 232448, "shared memory budget");
+static_assert(kBytesP<true> + 1024 <= 232448 && kBytesP<false> <= 232448, "shared memory budget");
+static_assert(kOffLo % 256 == 0 && (int)sizeof(SchedSmem) <= kXB, "align, scratch");
 
 // TMEM columns: S_c at 0, S_r at 64, P[2] (64 bf16 tokens = 32 columns each) at
 // 128 / 160, this CTA's scaled partial logits (fp32, parked by group A for group
@@ -126,11 +134,20 @@ decode_pair_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_cons
     // the in-kernel plan reads only seq_lens, which no kernel of the call writes: it
     // is made before the dependency wait, overlapping the previous kernel's tail
     if (p.sched_inline) {                                // both CTAs derive the same plan
-        __shared__ SchedSmem S;
-        compute_schedule<WIN>(p.seq_lens, p.B, p.s_q, p.sa, (int)blockIdx.y, S, p.status, blockIdx.x == 0 && blockIdx.y == 0);
-        if ((int)blockIdx.y >= S.n_items) return;        // uniform over the cluster
-        it = S.item;
-        seq_len = S.item_len;                            // the plan's copy
+        auto plan = [&](SchedSmem& S) {
+            compute_schedule<WIN>(p.seq_lens, p.B, p.s_q, p.sa, (int)blockIdx.y, S, p.status, blockIdx.x == 0 && blockIdx.y == 0);
+            it = S.item;
+            seq_len = S.item_len;                        // the plan's copy
+            return (int)blockIdx.y < S.n_items;
+        };
+        bool there;
+        if constexpr (WIN) {
+            there = plan(*reinterpret_cast<SchedSmem*>(sX));   // the peer writes there after the cluster barrier
+        } else {
+            __shared__ SchedSmem S;
+            there = plan(S);
+        }
+        if (!there) return;                              // uniform over the cluster
     } else {
         pdl_wait();                                      // the scheduler kernel's items
         if ((int)blockIdx.y >= *p.n_items) return;       // uniform over the cluster
@@ -199,6 +216,12 @@ decode_pair_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_cons
                 const float v1 = rank ? v[kHalfRope + j + 1] : v[j + 1];
                 const __nv_bfloat162 w2 = __floats2bfloat162_rn(v0 * gq[j] * beta, v1 * gq[j + 1] * beta);
                 *reinterpret_cast<__nv_bfloat162*>(qrope + sw64_offset(r, j)) = w2;
+                if (WIN && j < 16) {
+                    const float2 f = __bfloat1622float2(w2);
+                    *reinterpret_cast<__nv_bfloat162*>(sm + kOffLo + (r >> 3) * 256 + (r & 7) * 32 +
+                                                       (((j >> 3) ^ ((r >> 2) & 1)) << 4) + (j & 7) * 2) =
+                        __floats2bfloat162_rn(v0 * gq[j] * beta - f.x, v1 * gq[j + 1] * beta - f.y);
+                }
             }
             coef_s[r] = PLAIN ? p.scale * kLog2e : p.scale * a * kLog2e;
         }
@@ -288,6 +311,9 @@ decode_pair_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_cons
                     else
                         mma_bf16(tmem + kCSr, a, bd, id_s, kk > 0 ? 1u : 0u);
                 }
+                if (WIN)
+                    mma_bf16(tmem + (PLAIN ? kCSc : kCSr), smem_desc(smem_u32(sm + kOffLo), 16, 256, kSwizzle32B),
+                             smem_desc(st_addr + kSLat, 16, 512, kSwizzle64B), id_s, 1u);
                 mma_commit(sfull);
             };
             auto issue_o = [&](int j) {
@@ -706,11 +732,12 @@ int launch_pair(const qkmla_decode_args* a, const TcParams& tp, int max_items, c
     auto k = plain ? (win ? decode_pair_kernel<true, false, true> : decode_pair_kernel<true, false, false>)
              : akh ? (win ? decode_pair_kernel<false, true, true> : decode_pair_kernel<false, true, false>)
                    : (win ? decode_pair_kernel<false, false, true> : decode_pair_kernel<false, false, false>);
-    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytesP) != cudaSuccess)
+    const int bytes = win ? kBytesP<true> : kBytesP<false>;
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
         return QKMLA_ERR_CUDA;
     dim3 grid(2 * a->s_q, max_items);
-    return launch_pdl(k, grid, dim3(kThreadsP), kBytesP, s, lat, rope, qmap, tp) == cudaSuccess ? QKMLA_OK
-                                                                                       : QKMLA_ERR_CUDA;
+    return launch_pdl(k, grid, dim3(kThreadsP), bytes, s, lat, rope, qmap, tp) == cudaSuccess ? QKMLA_OK
+                                                                                        : QKMLA_ERR_CUDA;
 }
 
 }  // namespace dec

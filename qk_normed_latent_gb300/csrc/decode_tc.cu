@@ -73,11 +73,10 @@ struct Layout {
     static constexpr bool kPOwn = kPBytes > kSRope;
     static constexpr int kOffP = kPOwn ? (kSLat + kSRope + kSAk + 1023) / 1024 * 1024 : kSLat;
     static constexpr int kStage = ((kPOwn ? kOffP + kPBytes : kSLat + kSRope + kSAk) + 1023) / 1024 * 1024;
-    // LO (windowed calls, d_c = 256): what bf16 leaves of the RoPE query as a second part behind it, products into
-    // the same accumulator.  Over a window the rounded query was as large an error of the output as its bf16 weights
-    // (1.3e-3 against 1.2e-3 of its norm, 16 heads x 1004 tokens).  It takes a stage's place: 16 sequences behind a
-    // window of 1000 take 16.0 us, not 15.5; at d_c = 512, stages of 32 tokens, it would be 11 % of a long window's
-    // time.  The call without a window keeps its results.
+    // LO (windowed calls): what bf16 leaves of the RoPE query as a second part behind it, products into the same
+    // accumulator.  Over a window the rounded query was as large an error of the output as its bf16 weights (1.3e-3
+    // against 1.2e-3 of its norm, 16 heads x 1004 tokens).  It takes a stage's place: 16 sequences behind a window of
+    // 1000 take 16.0 us, not 15.5, 64 heads at d_c = 512 7 % more.  The call without a window keeps its results.
     static constexpr bool kLo = LO;
     static constexpr int kQ = ((kQLat + (LO ? 2 : 1) * kQRope) + 1023) / 1024 * 1024;
     static constexpr int kOffQ = 0;
@@ -114,7 +113,7 @@ template <int DC, int DR, bool PLAIN, int NST, int KT, bool AKH, bool WIN>
 __global__ void __launch_bounds__(kThreads, 1)
 decode_tc_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ CUtensorMap tm_rope,
                  const __grid_constant__ CUtensorMap tm_q, const TcParams p) {
-    using LY = Layout<DC, DR, NST, KT, WIN && DC == 256>;
+    using LY = Layout<DC, DR, NST, KT, WIN>;
     constexpr int kChunks = LY::kChunks;
     constexpr int NSB = LY::kNSB;
     extern __shared__ __align__(1024) uint8_t smraw[];
@@ -852,7 +851,7 @@ template <int DC, int DR, bool PLAIN, int NST, bool AKH, bool WIN>
 int launch_kernel_w(const CUtensorMap& lat, const CUtensorMap& rope, const CUtensorMap& qmap, const TcParams& tp,
                   int n_rb, int max_items, cudaStream_t s) {
     constexpr int KT = tile_of<DC>();
-    using LY = Layout<DC, DR, NST, KT, WIN && DC == 256>;
+    using LY = Layout<DC, DR, NST, KT, WIN>;
     auto k = decode_tc_kernel<DC, DR, PLAIN, NST, KT, AKH, WIN>;
     static_assert(LY::kBytes <= 232448, "shared memory budget");
     if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, LY::kBytes) != cudaSuccess)
@@ -865,7 +864,7 @@ int launch_kernel_w(const CUtensorMap& lat, const CUtensorMap& rope, const CUten
 template <int DC, int DR, bool PLAIN, int NST, bool AKH>
 int launch_kernel(const CUtensorMap& lat, const CUtensorMap& rope, const CUtensorMap& qmap, const TcParams& tp,
                   int n_rb, int max_items, cudaStream_t s) {
-    return tp.window > 0 ? launch_kernel_w<DC, DR, PLAIN, DC == 256 ? NST - 1 : NST, AKH, true>(lat, rope, qmap, tp, n_rb, max_items, s)
+    return tp.window > 0 ? launch_kernel_w<DC, DR, PLAIN, NST - 1, AKH, true>(lat, rope, qmap, tp, n_rb, max_items, s)
                          : launch_kernel_w<DC, DR, PLAIN, NST, AKH, false>(lat, rope, qmap, tp, n_rb, max_items, s);
 }
 

@@ -197,19 +197,15 @@ def test_window_tensor_core(Q, k, shape):
 
 @pytest.mark.parametrize("H", [16, 128])
 def test_window_over_everything_is_decode(Q, H):
-    """A window that covers every token gives the bits of the call without one where both round alike (the pair
-    kernel), and its values where the windowed call carries the RoPE query in two parts: both are within the
-    method's rule, 5e-3 of the result's norm, and a logit's change is at most 2^-8 sum_j |q^r_j k^r_j| <= 2^-8
-    d_r max|gamma| scale < 2^-8 x 32 x 1.5 x 0.11."""
+    """A window that covers every token gives the values of the call without one.  The windowed call carries (part
+    of) the RoPE query in two parts: both are within the method's rule, 5e-3 of the result's norm, and a logit's
+    change is at most 2^-8 sum_j |q^r_j k^r_j| <= 2^-8 d_r max|gamma| scale < 2^-8 x 64 x 1.5 x 0.11."""
     c = R.Case([700, 130, 64], cache="bf16", H=H, G=4 if H == 16 else 8, d_c=256 if H == 16 else 512,
                d_r=32 if H == 16 else 64, s_q=2)
     a, la = Device(Q, c).run(Q)
     c.window = 700
     b, lb = Device(Q, c).run(Q)
-    if H == 128:
-        assert (a == b).all() and (la == lb).all()
-    else:
-        assert np.linalg.norm(a - b) <= 5e-3 * np.linalg.norm(a) and np.abs(la - lb).max() <= 2.0 ** -8 * 32 * 1.5 * 0.11
+    assert np.linalg.norm(a - b) <= 5e-3 * np.linalg.norm(a) and np.abs(la - lb).max() <= 2.0 ** -8 * 64 * 1.5 * 0.11
 
 
 @pytest.mark.parametrize("k", range(len(TC)))
