@@ -671,7 +671,9 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
                     const float m1 = mx > m0 + 4.f ? ceilf(mx) : m0;
                     const float v1 = vx > v0 + 2.f ? ceilf(vx) + (v0 == -INFINITY ? 2.f : 1.f) : v0;
                     const float cm = m0 == -INFINITY ? 0.f : exp2f(m0 - m1);       // of the row sums
-                    const float f1 = v1 == -INFINITY ? 0.f : kPUnit * exp2f(fminf(fmaxf(m1 - v1, -110.f), 95.f));
+                    // nothing to add up yet (no visible token, or latents of zeros, whose scale is 0): with the largest
+                    // unit the first contribution, whatever its tile, is above kTopP and sets it
+                    const float f1 = kPUnit * exp2f(v1 == -INFINITY ? 95.f : fminf(fmaxf(m1 - v1, -110.f), 95.f));
                     m_s[r] = m1;
                     v_s[r] = v1;
                     f_s[r] = f1;
