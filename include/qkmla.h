@@ -307,8 +307,11 @@ typedef struct qkmla_decode_ext_args {
  * gives o = 0 and lse = -inf.  With neither, the call is qkmla_decode.
  *
  * Accuracy: fp32 sums, with the output's weights rounded -- 8-bit cache: p_t
- * kv_scale_t to two 8-bit parts, off by 2^-8 of itself (2^-11 more from fp16) and
- * by 2^-15 of the row's largest; bf16 cache: as qkmla_decode.  Tensor-core kernels serve the
+ * kv_scale_t to two 8-bit parts, off by 2^-8 of itself (2^-11 more from fp16); one
+ * below 2^-7 of the row's largest instead by up to 2^-14 of that largest (2^-15, 2^-16,
+ * 2^-19 in ranges of more than 2^11, 2^13, 2^14 tokens), up or down in proportion by
+ * the token's place, so that N of them are off by sqrt(N) such steps together and not
+ * by N; bf16 cache: as qkmla_decode.  Tensor-core kernels serve the
  * 8-bit cache for (d_c, d_r) of (512, 64), (256, 32 or 64) and (128, 32 or 64), H a
  * multiple of 16, G <= 8, B <= 4096, page sizes 16, 32 or a multiple of 64 and
  * 16-byte aligned bases, and windows over the bf16 cache where qkmla_decode has one;

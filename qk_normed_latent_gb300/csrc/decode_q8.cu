@@ -9,9 +9,10 @@
 // pass, half the shared memory of bf16), and the other operand of each product is
 // split into two 8-bit parts, a = hi + lo, hi = e4m3(a), lo = a - hi rounded.  For the
 // bf16 query (lo in e4m3) the sum is exact down to 2^-18 of the row's largest value (8
-// significant bits in two times 4); for the weights (lo in e5m2, or in e4m3 with an
-// accumulator and a unit of its own) it is off by at most 2^-8, like a bf16 rounding,
-// plus 2^-15 of the row's largest.  The RoPE query is two bf16 parts (2^-16).  A tcgen05.mma with
+// significant bits in two times 4); a weight (lo in e5m2, or in e4m3 with an accumulator
+// and a unit of its own) is off by at most 2^-8, like a bf16 rounding, or, where it is
+// small, by a step of lo whose sign depends on the token's place alone (see below).  The
+// RoPE query is two bf16 parts (2^-16).  A tcgen05.mma with
 // K = 32 costs 45 cycles up to N = 32, 48 at N = 64 and 65 at N = 128 (M = 64 or 128,
 // K-major or MN-major, measured), so both parts as rows of one operand cost little more
 // than one.
@@ -37,8 +38,24 @@
 // rescale is a power of two, hence exact.  A move costs a tile's time (2350 cycles: O^T is
 // rescaled, so the previous output product has to end first), and the slowest CTA of a call
 // had 20 when the first tile's largest contribution was put at 8 of at most 256 (64 x 4096
-// tokens 111 us against 95, 4 x 262144 301 against 279).  With the remainders in e5m2, down
-// to 2^-16, it sits at 2 .. 4 of at most 448 and a move is rare.
+// tokens 111 us against 95, 4 x 262144 301 against 279).  It sits at 2 .. 4 of at most 448 and a
+// move is rare.
+//
+// Small weights.  The denominator counts a weight in full, so what its 8-bit parts lose must
+// not add up over the tokens: one token may outweigh each of 2^18 others that outweigh it
+// together (rounded to nearest, 2^-18 of the largest each, they vanished and half of the
+// result with them).  Two things keep the sum right.  (1) Below 2^-6, where hi has fewer than
+// its 4 bits, lo is rounded up or down in proportion: a dither of one step goes in before it
+// is cut, a token's place in a Weyl sequence (golden ratio), even over any run of tokens and
+// the same on every call.  What N tokens are off by is then sqrt(N) steps of at most 2^-13,
+// not N of them.  (2) Long items raise their units, by one move, when some tiles have shown
+// what is large: more than 32 tiles after 4 of them, to 4 .. 8 for the largest contribution in
+// the first and the fifth tile (8 .. 16 in more than 128 tiles), more than 256 after 128
+// again, to 64 .. 128.  Few later ones exceed that.  A step is then at most 2^-14 (2^-15,
+// 2^-16, 2^-19) of the largest for 2^11 (2^13, 2^14, more) tokens: against 64 bits, one
+// token over a flat background with latents of 3 times its norm, at the worst ratio,
+// 4.9e-3 (4.4e-3, 3.1e-3, 3.6e-3) of the result's norm.  Both cost 0 .. 3 % (64 x 4096
+// tokens 89 -> 92 us, 4 x 262144 269 -> 276, windowed 99 -> 96, 512-token items nothing).
 //
 // What bounds it (512 / 64, 64 rows): a tile takes 2340 cycles, of which the tensor core
 // needs 2076 (20 x 65 + 16 x 48) and shared memory at 128 bytes a cycle about 2200: the 36
@@ -77,6 +94,9 @@ constexpr float kPUnit = 16.f;       // P of a contribution of 2^v
 constexpr float kTopP = 448.f;       // a P above this (e4m3's largest value) moves the running maxima,
 constexpr float kTopE = 1.09951163e12f;   // and so does 2^(x - m) above 2^40, fp32's margin for the row sums
 constexpr float kLoUnit = 16.f;      // of the remainder's column where it has an accumulator of its own
+constexpr int kSettle1 = 4, kSettle2 = 128;            // tiles after which items of more than
+constexpr int kSettleFrom1 = 32, kSettleFrom2 = 256;   // this many raise their units
+constexpr int kSettleMore = 128;                       // tiles from which the first time is one binade more
 
 template <int DC, int DR, int ROWS>
 struct Q8Layout {
@@ -108,8 +128,8 @@ struct Q8Layout {
     static constexpr int kOffAk = kOffOwn + (kPOwn ? kT * kN : 0);
     static constexpr int kOffScale = kOffAk + kT * kMaxG * 4;
     static constexpr int kStage = (kOffScale + kT * 4 + 1023) / 1024 * 1024;
-    // per-row floats: coef, m, v, f, corr, inv, and the column maxima of 4 warps (two kinds)
-    static constexpr int kRowFloats = 6 * ROWS + 8 * ROWS;
+    // per-row floats: coef, m, v, t, f, corr, inv, and the column maxima of 4 warps (two kinds)
+    static constexpr int kRowFloats = 7 * ROWS + 8 * ROWS;
     static constexpr int kMisc = 512 + kRowFloats * 4 + 1024;
     static constexpr int kStatic = (int)sizeof(SchedSmem) + 256;
     static constexpr int kNst = std::min(6, (232448 - kQ - kMisc - kStatic) / kStage);
@@ -144,21 +164,56 @@ struct Q8Params {
     int* status;
 };
 
-// Two values as two 8-bit parts each, hi = e4m3(a) and lo = unit (a - hi), a pair packed in 16 bits.  Through fp16,
-// which holds what matters of both operands (a scaled bf16 query exactly down to 2^-17, 11 bits of a weight) and
-// has packed conversions; the remainder, at most half a step, is exact.  For the weights lo is stored in e5m2,
-// whose half step is at most 2^-8 of the weight and which reaches to 2^-16, or, where one operand holds both
-// parts and has one type, with kLoUnit in e4m3: 2^-9 and 2^-13.
-enum class Lo { e4m3, e5m2, e4m3_unit };
-template <Lo L>
+// Two values as two e4m3 parts each, hi = e4m3(a) and lo = a - hi, a pair packed in 16 bits.  Through fp16, which
+// holds a scaled bf16 query exactly down to 2^-17 and has packed conversions; the remainder, at most half a step,
+// is exact.
 __device__ __forceinline__ void split8(float2 v, uint32_t& hi, uint32_t& lo) {
     const __half2 w = __floats2half2_rn(v.x, v.y);
     const __nv_fp8x2_storage_t h =
         __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(w), __NV_SATFINITE, __NV_E4M3);
-    __half2 r = __hsub2(w, __half2(__nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3)));
-    if constexpr (L == Lo::e4m3_unit) r = __hmul2(r, __float2half2_rn(kLoUnit));
+    const __half2 r = __hsub2(w, __half2(__nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3)));
     hi = h;
-    lo = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(r), __NV_SATFINITE, L == Lo::e5m2 ? __NV_E5M2 : __NV_E4M3);
+    lo = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(r), __NV_SATFINITE, __NV_E4M3);
+}
+
+// Four weights (fp16: 11 bits, steps of 2^-24 at the bottom) as hi in e4m3 and a remainder: with kLoUnit in e4m3
+// where one operand holds both parts and has one type (STACKED), else in e5m2, fp16's upper byte.  Rounded to
+// nearest, half a step of lo is at most 2^-8 of the weight.  Weights below 2^-6, e4m3's least normal value (hi's
+// steps are 2^-9 below it), are rounded by the token's dither: for e5m2 0 .. 255 of the byte that is cut off; in
+// e4m3 the remainder is then below its normal values too, and one step of 2^-9, (0 .. 255) - 127.5 of 256, is added.
+template <bool STACKED>
+struct Dither {
+    uint32_t bits;           // for two values
+    __device__ __forceinline__ explicit Dither(int token) {
+        const uint32_t d = ((uint32_t)token * 0x9E3779B1u) >> 24;
+        if constexpr (STACKED) {
+            const __half2 h = __float2half2_rn(((float)d - 127.5f) * 7.62939453125e-6f);      // 2^-17
+            bits = *reinterpret_cast<const uint32_t*>(&h);
+        } else {
+            bits = d * 0x00010001u;
+        }
+    }
+};
+template <bool STACKED>
+__device__ __forceinline__ void split_weights(__half2 a, __half2 b, Dither<STACKED> dither, uint32_t& hi, uint32_t& lo) {
+    auto part = [&](__half2 w, uint32_t& h) -> uint32_t {
+        const __nv_fp8x2_storage_t c =
+            __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(w), __NV_SATFINITE, __NV_E4M3);
+        const __half2 r = __hsub2(w, __half2(__nv_cvt_fp8x2_to_halfraw2(c, __NV_E4M3)));
+        const uint32_t small = __hlt2_mask(w, __float2half2_rn(0.015625f));
+        h = c;
+        if constexpr (STACKED) {
+            const uint32_t d = small & dither.bits;
+            const __half2 l = __hfma2(r, __float2half2_rn(kLoUnit), *reinterpret_cast<const __half2*>(&d));
+            return __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(l), __NV_SATFINITE, __NV_E4M3);
+        } else {
+            return *reinterpret_cast<const uint32_t*>(&r) + ((small & dither.bits) | (~small & 0x00800080u));
+        }
+    };
+    uint32_t ha, hb;
+    const uint32_t la = part(a, ha), lb = part(b, hb);
+    hi = ha | (hb << 16);
+    lo = STACKED ? la | (lb << 16) : __byte_perm(la, lb, 0x7531);
 }
 
 template <int W>
@@ -223,7 +278,8 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
     float* coef_s = (float*)(sm + LY::kOffMisc + 512);   // scale log2e alpha^q x the row's code scale
     float* m_s = coef_s + ROWS;              // running maximum of the logits (integer)
     float* v_s = m_s + ROWS;                 // running maximum of the contributions (integer)
-    float* f_s = v_s + ROWS;                 // unit of P: kPUnit 2^(m - v)
+    float* t_s = v_s + ROWS;                 // largest contribution in the tiles whose maxima were formed
+    float* f_s = t_s + ROWS;                 // unit of P: kPUnit 2^(m - v)
     float* corr_s = f_s + ROWS;              // rescale factor of O^T in this tile
     float* inv_s = corr_s + ROWS;            // epilogue: 1 / (f l)
     float* red_s = inv_s + ROWS;             // [2 kinds][4 warps][ROWS]
@@ -372,8 +428,8 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
                 const float2 a0 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&raw[i][k].x));
                 const float2 a1 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&raw[i][k].y));
                 uint32_t h0, l0, h1, l1;
-                split8<Lo::e4m3>(make_float2(a0.x * inv, a0.y * inv), h0, l0);
-                split8<Lo::e4m3>(make_float2(a1.x * inv, a1.y * inv), h1, l1);
+                split8(make_float2(a0.x * inv, a0.y * inv), h0, l0);
+                split8(make_float2(a1.x * inv, a1.y * inv), h1, l1);
                 hi[k] = h0 | (h1 << 16);
                 lo[k] = l0 | (l1 << 16);
             }
@@ -400,7 +456,7 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
             }
             if (lane == 0) {
                 coef_s[r] = p.scale * kLog2e * sq * aq4[i];
-                m_s[r] = v_s[r] = -INFINITY;
+                m_s[r] = v_s[r] = t_s[r] = -INFINITY;
                 f_s[r] = 0.f;
             }
         }
@@ -526,6 +582,7 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
         // this group's rows in registers, two to a packed pair: -m, unit f, row sums
         constexpr int HP2 = kHpt / 2;
         uint64_t nm2[HP2], f2v[HP2], lsum2[HP2];
+        const int settle1 = n_t > kSettleFrom1 ? kSettle1 : INT32_MAX, settle2 = n_t > kSettleFrom2 ? kSettle2 : INT32_MAX;
         auto reload = [&]() {
 #pragma unroll
             for (int u = 0; u < HP2; ++u) {
@@ -637,7 +694,8 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
                 }
             };
             weigh();
-            const bool need = top_w > kTopP || top_e > kTopE || j == 0;
+            const bool settle = j == settle1 || j == settle2;
+            const bool need = top_w > kTopP || top_e > kTopE || j == 0 || settle;
             if (group_any(grp, need || !got_s)) {
                 if (group_any(grp, !got_s)) { ok = false; break; }
                 // ---- exact maxima of this tile's logits and contributions, per row ----
@@ -667,9 +725,11 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
                         vx = fmaxf(vx, red_s[(4 + q) * ROWS + r]);
                     }
                     const float m0 = m_s[r], v0 = v_s[r], f0 = f_s[r];
-                    // the first tiles' largest contribution will be exceeded: leave it two binades
+                    t_s[r] = vx = fmaxf(vx, t_s[r]);
+                    // binades between the largest contribution and 16: the first tiles' will be exceeded
+                    const float room = j >= settle2 ? -3.f : j >= settle1 ? (n_t > kSettleMore ? 0.f : 1.f) : v0 == -INFINITY ? 2.f : 1.f;
                     const float m1 = mx > m0 + 4.f ? ceilf(mx) : m0;
-                    const float v1 = vx > v0 + 2.f ? ceilf(vx) + (v0 == -INFINITY ? 2.f : 1.f) : v0;
+                    const float v1 = vx > v0 + fmaxf(2.f, 1.f - room) || (settle && vx > -INFINITY) ? ceilf(vx) + room : v0;
                     const float cm = m0 == -INFINITY ? 0.f : exp2f(m0 - m1);       // of the row sums
                     // nothing to add up yet (no visible token, or latents of zeros, whose scale is 0): with the largest
                     // unit the first contribution, whatever its tile, is above kTopP and sets it
@@ -712,15 +772,12 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
                 weigh();
                 group_sync(grp);                             // red_s, corr_s are read
             }
-            constexpr Lo kLo = LY::kStacked ? Lo::e4m3_unit : Lo::e5m2;
+            const Dither<LY::kStacked> dither(t);
             uint32_t hi[kHpt / 4], lo[kHpt / 4];
 #pragma unroll
             for (int u = 0; u < HP2; u += 2) {
-                uint32_t h0, l0, h1, l1;
-                split8<kLo>(f2_unpack(w2[u]), h0, l0);
-                split8<kLo>(f2_unpack(w2[u + 1]), h1, l1);
-                hi[u / 2] = h0 | (h1 << 16);
-                lo[u / 2] = l0 | (l1 << 16);
+                const float2 wa = f2_unpack(w2[u]), wb = f2_unpack(w2[u + 1]);
+                split_weights(__floats2half2_rn(wa.x, wa.y), __floats2half2_rn(wb.x, wb.y), dither, hi[u / 2], lo[u / 2]);
                 lsum2[u] = f2_add(lsum2[u], e2[u]);
                 lsum2[u + 1] = f2_add(lsum2[u + 1], e2[u + 1]);
             }
