@@ -304,7 +304,8 @@ typedef struct qkmla_decode_ext_args {
  *
  * With an 8-bit cache or a window, seq_lens[b] may be anything from 0 to
  * max_pages * page_size: a query without a visible token (an idle batch slot)
- * gives o = 0 and lse = -inf.  With neither, the call is qkmla_decode.
+ * gives o = 0 and lse = -inf.  With neither, the call is qkmla_decode.  A NaN in
+ * what a query sees, or in its own row, is NaN in all of its o and lse.
  *
  * Accuracy: fp32 sums, with the output's weights rounded -- 8-bit cache: p_t
  * kv_scale_t to two 8-bit parts, off by 2^-8 of itself (2^-11 more from fp16); one

@@ -39,7 +39,8 @@ combine_kernel(const float* __restrict__ o_part, const float* __restrict__ lse_p
     m = s_m;
     float sum = 0.f;
     for (int s = tid; s < nsplit; s += kThreads) {
-        const float w = (m == -INFINITY) ? 0.f : expf(lp[s] - m);
+        // NaN in a part (which m passes over) is NaN in the row
+        const float w = (lp[s] == -INFINITY) ? 0.f : expf(lp[s] - m);
         wts[s] = w;
         sum += w;
     }
@@ -50,8 +51,8 @@ combine_kernel(const float* __restrict__ o_part, const float* __restrict__ lse_p
     if (tid == 0) {
         float ss = 0.f;
         for (int w = 0; w < kThreads / 32; ++w) ss += red[w];
-        s_inv = (ss > 0.f) ? 1.f / ss : 0.f;
-        s_lse = (ss > 0.f) ? m + logf(ss) : -INFINITY;
+        s_inv = (ss == 0.f) ? 0.f : 1.f / ss;
+        s_lse = (ss == 0.f) ? -INFINITY : m + logf(ss);
     }
     __syncthreads();
     const float inv = s_inv;

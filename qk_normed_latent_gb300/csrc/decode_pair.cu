@@ -657,14 +657,15 @@ decode_pair_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_cons
             if (!got_last) *(volatile int*)abort_flag = 1;
             const size_t orow = ((size_t)b * p.s_q + qi) * p.H + r;
             if (rank == 0) {
-                const float lse = (l_run > 0.f) ? (m_run + log2f(l_run)) * kLn2 : -INFINITY;
+                // 0: no visible token; NaN in what the row sees stays NaN
+                const float lse = (l_run == 0.f) ? -INFINITY : (m_run + log2f(l_run)) * kLn2;
                 if (it.part < 0) {
                     if (p.lse) p.lse[orow] = lse;
                 } else {
                     p.lse_part[(size_t)it.part * p.s_q * p.H + (size_t)qi * p.H + r] = lse;
                 }
             }
-            const float inv = (l_run > 0.f) ? 1.f / l_run : 0.f;
+            const float inv = (l_run == 0.f) ? 0.f : 1.f / l_run;
             float* dst_part = (it.part >= 0)
                                   ? p.o_part + ((size_t)it.part * p.s_q * p.H + (size_t)qi * p.H + r) * kDC + rank * kHalfLat
                                   : nullptr;

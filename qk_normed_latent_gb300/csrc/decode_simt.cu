@@ -219,8 +219,9 @@ decode_simt_kernel(SimtParams p) {
     for (int hl = 0; hl < HPG; ++hl) {
         const int64_t rh = (int64_t)bi * p.H + h0 + hl;
         const float l = lrun[hl];
-        const float inv = (l > 0.f) ? 1.f / l : 0.f;
-        const float lse = (l > 0.f) ? (mrun[hl] + log2f(l)) * kLn2 : -INFINITY;
+        // 0: no visible token; NaN in what the row sees stays NaN
+        const float inv = (l == 0.f) ? 0.f : 1.f / l;
+        const float lse = (l == 0.f) ? -INFINITY : (mrun[hl] + log2f(l)) * kLn2;
         if (p.nsplit == 1) {
 #pragma unroll
             for (int j = 0; j < NJ; ++j) {

@@ -583,7 +583,8 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
         if (!ok) *(volatile int*)abort_flag = 1;
         if (row_ok && half == 0) {
             l_s[r] = l_run;
-            const float lse = (l_run > 0.f) ? (m_run + log2f(l_run)) * kLn2 : -INFINITY;
+            // 0: no visible token; NaN in what the row sees stays NaN
+            const float lse = (l_run == 0.f) ? -INFINITY : (m_run + log2f(l_run)) * kLn2;
             const size_t orow = ((size_t)b * p.s_q + qi) * p.H + h0 + r;
             if (it.part < 0) {
                 if (p.lse) p.lse[orow] = lse;
@@ -611,7 +612,7 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
                 for (int jj = 0; jj < 16; ++jj) {
                     const int rr = c16 + jj;
                     const float l = l_s[rr];
-                    const float val = (l > 0.f) ? __uint_as_float(v[jj]) / l : 0.f;
+                    const float val = (l == 0.f) ? 0.f : __uint_as_float(v[jj]) / l;
                     if (dst_part) {
                         dst_part[(size_t)rr * DC + dc] = val;
                     } else if (p.o_dtype == QKMLA_F32) {
@@ -786,15 +787,16 @@ combine_var_kernel(const float* __restrict__ o_part, const float* __restrict__ l
             m = warp_max(m);
             float sum = 0.f;
             for (int s = tid; s < ns; s += 32) {
-                const float w =
-                    (m == -INFINITY) ? 0.f : expf(__ldcg(lse_part + (size_t)(p0 + s) * rows_per_seq + rr) - m);
+                // an empty part has weight 0, one with NaN (which m passes over) NaN
+                const float x = __ldcg(lse_part + (size_t)(p0 + s) * rows_per_seq + rr);
+                const float w = (x == -INFINITY) ? 0.f : expf(x - m);
                 w_s[s] = w;                         // ns <= 256
                 sum += w;
             }
             sum = warp_sum(sum);
             if (tid == 0) {
-                s_inv = sum > 0.f ? 1.f / sum : 0.f;
-                s_lse = sum > 0.f ? m + logf(sum) : -INFINITY;
+                s_inv = sum == 0.f ? 0.f : 1.f / sum;
+                s_lse = sum == 0.f ? -INFINITY : m + logf(sum);
             }
         }
         __syncthreads();
