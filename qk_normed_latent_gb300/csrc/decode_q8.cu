@@ -421,7 +421,9 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
                 top2 = __hmax2(top2, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&raw[i][k].y)));
             }
             float inv;
-            const float sq = e4m3_scale(warp_max(fmaxf(__low2float(top2), __high2float(top2))), &inv);
+            const float top = warp_max(fmaxf(__low2float(top2), __high2float(top2)));
+            const float sq = e4m3_scale(top, &inv);
+            if (isinf(top)) inv = __int_as_float(0x7fffffff);   // no code is infinite: the row becomes NaN, not saturated
             uint32_t hi[DC / 128], lo[DC / 128];              // 4 codes a word
 #pragma unroll
             for (int k = 0; k < DC / 128; ++k) {

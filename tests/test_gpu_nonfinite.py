@@ -96,3 +96,17 @@ def test_nan_in_every_token(Q, kernel):  # noqa: F811
         assert np.isnan(o[bad]).all() and np.isnan(lse[bad]).all()
         assert (o[2] == 0).all() and np.isneginf(lse[2]).all()      # the empty sequence is one
         assert np.linalg.norm(o[1] - c.o[1]) <= 5e-3 * np.linalg.norm(c.o[1])
+
+
+@pytest.mark.parametrize("value", [INF, -INF])
+@pytest.mark.parametrize("splits", [1, 3])
+@pytest.mark.parametrize("kernel", range(len(KERNELS)))
+def test_infinite_query(Q, kernel, splits, value):  # noqa: F811
+    """An infinite element of a query's row: its logits are infinities of both signs, the row is NaN."""
+    cache, simt, shape = KERNELS[kernel]
+    c = R.Case([1300, 200], cache=cache, window=3000, sinks=4, **shape)
+    dev = Device(Q, c, force_simt=simt, num_splits=splits)
+    dev.in_[0][0, 0, 5, 7] = value
+    bad = np.zeros(c.lse.shape, bool)
+    bad[0, 0, 5] = True
+    check_rows(Q, dev, c, bad)
