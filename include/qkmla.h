@@ -297,8 +297,8 @@ typedef struct qkmla_decode_ext_args {
  *
  * Window w, sinks f: query i of sequence b, of causal length n = seq_lens[b] -
  * s_q + i + 1, attends to the tokens t < n with t < f or t >= n - w.  What is
- * stored for tokens that no query of the step sees (NaN included) does not reach
- * the result, and pages without such a token are not read; a tile of up to 64
+ * stored for tokens that a query does not see (NaN included) does not reach its
+ * result, and pages that no query of the step sees are not read; a tile of up to 64
  * tokens that holds a visible one is loaded whole, so its page-table entry has
  * to be valid.
  *

@@ -223,6 +223,12 @@ __device__ __forceinline__ void store_codes(uint8_t* at, const uint32_t (&w)[W])
     else *reinterpret_cast<uint32_t*>(at) = w[0];
 }
 
+// Sixteen e4m3 codes, NaNs as 0.
+__device__ __forceinline__ uint4 finite_e4m3(uint4 v) {
+    auto four = [](uint32_t w) { return w & ~__vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu); };
+    return make_uint4(four(v.x), four(v.y), four(v.z), four(v.w));
+}
+
 // Vote and barrier of a softmax group (named barriers 1 ..).
 __device__ __forceinline__ bool group_any(int grp, bool pred) {
     uint32_t r;
@@ -256,7 +262,8 @@ __device__ __forceinline__ float half_warp_reduce(const float (&v)[8], int lane,
     return op(c, __shfl_xor_sync(0xffffffffu, c, 1));
 }
 
-template <int DC, int DR, int ROWS>
+// SPANS: a CTA's rows may belong to several query tokens (the others take 3 % longer with its code).
+template <int DC, int DR, int ROWS, bool SPANS>
 __global__ void __launch_bounds__(96 + 8 * ROWS, 1)
 decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ CUtensorMap tm_rope,
                  const Q8Params p) {
@@ -322,6 +329,8 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
     const int i_first = row0 / p.H, i_last = (min(row0 + ROWS, n_rows) - 1) / p.H;
     const int len_last = max(0, len - p.s_q + i_last + 1);
     const int win_first = p.window > 0 ? len - p.s_q + i_first + 1 - p.window : 0;
+    // tokens all its query tokens see: those below end_first, less [sinks, win_last)
+    const int end_first = len - p.s_q + i_first + 1, win_last = p.window > 0 ? len - p.s_q + i_last + 1 - p.window : 0;
 
     if (tid == 0 && bad && blockIdx.x == 0) report(p.status, QKMLA_ERR_DEVICE_BOUNDS);
     pdl_wait();
@@ -791,12 +800,16 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
             const uint32_t chi = (uint32_t)u0 >> 4, clo = LY::kStacked ? (uint32_t)(ROWS + u0) >> 4 : chi;
             *reinterpret_cast<uint2*>(pr + ((chi ^ xr) << 4)) = make_uint2(hi[0], hi[1]);
             *reinterpret_cast<uint2*>(pr + (LY::kStacked ? 0 : 8 * PN) + ((clo ^ xr) << 4)) = make_uint2(lo[0], lo[1]);
-            // a token no row sees: its latents (stale or never loaded) must not reach the output MMA as NaN
-            if (!any_sees) {
+            // a token no row sees: its latents (stale or never loaded) must not reach the output MMA as NaN; a token
+            // that only some of the CTA's query tokens see: its NaNs must not reach the others' rows as 0 x NaN (in
+            // the rows that see it the logit is NaN)
+            if (!any_sees || (SPANS && (t >= end_first || (t >= p.sinks && t < win_last)))) {
                 constexpr int kShare = 2 * LY::kGroups;      // threads of a token
-                for (int c = 2 * grp + (lane >> 4); c < 8 * KB; c += kShare)
-                    *reinterpret_cast<uint4*>(stg + (tl >> 3) * LY::kGroup + (c >> 3) * 1024 + (tl & 7) * 128 +
-                                              (((c & 7) ^ (tl & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+                for (int c = 2 * grp + (lane >> 4); c < 8 * KB; c += kShare) {
+                    uint4* at = reinterpret_cast<uint4*>(stg + (tl >> 3) * LY::kGroup + (c >> 3) * 1024 + (tl & 7) * 128 +
+                                                         (((c & 7) ^ (tl & 7)) << 4));
+                    *at = SPANS && any_sees ? finite_e4m3(*at) : make_uint4(0u, 0u, 0u, 0u);
+                }
             }
             fence_proxy_async_smem();
             tc_fence_before();
@@ -917,7 +930,8 @@ int q8_row_blocks(const qkmla_decode_args* a) {
 
 template <int DC, int DR, int ROWS>
 int launch_q8(const Q8Params& q, const CUtensorMap& lat, const CUtensorMap& rope, dim3 grid, cudaStream_t s) {
-    auto k = decode_q8_kernel<DC, DR, ROWS>;
+    const bool spans = q.s_q > 1 && q.H % ROWS != 0;          // 16 rows are at most one query token's
+    auto k = ROWS > 16 && spans ? decode_q8_kernel<DC, DR, ROWS, (ROWS > 16)> : decode_q8_kernel<DC, DR, ROWS, false>;
     constexpr int bytes = Q8Layout<DC, DR, ROWS>::kBytes;
     if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return QKMLA_ERR_CUDA;
     return launch_pdl(k, grid, dim3(Q8Layout<DC, DR, ROWS>::kThreads), bytes, s, lat, rope, q) == cudaSuccess

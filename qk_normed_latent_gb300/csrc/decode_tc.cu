@@ -107,9 +107,16 @@ __device__ __forceinline__ uint32_t pt_offset(int r, int t, int rows_o) {
     return (uint32_t)(t >> 6) * (uint32_t)(rows_o * 128) + sw128_offset(r, t & 63);
 }
 
-// AKH: A^k_cache entries are fp16 (else fp32).  WIN: a sliding window with sinks -- the work items' tiles
+// Eight bf16 values, those that are not finite as 0.
+__device__ __forceinline__ uint4 finite_bf16(uint4 v) {
+    auto two = [](uint32_t w) { return w & ~__vcmpeq2(w & 0x7f807f80u, 0x7f807f80u); };
+    return make_uint4(two(v.x), two(v.y), two(v.z), two(v.w));
+}
+
+// AKH: A^k_cache entries are fp16 (else fp32).  PACK: a CTA's rows span several query tokens (the others take
+// 0.6 us of 16 longer with its code).  WIN: a sliding window with sinks -- the work items' tiles
 // are those some query of the step sees, and each row masks the tokens it does not.
-template <int DC, int DR, bool PLAIN, int NST, int KT, bool AKH, bool WIN>
+template <int DC, int DR, bool PLAIN, int NST, int KT, bool AKH, bool WIN, bool PACK>
 __global__ void __launch_bounds__(kThreads, 1)
 decode_tc_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_constant__ CUtensorMap tm_rope,
                  const __grid_constant__ CUtensorMap tm_q, const TcParams p) {
@@ -543,7 +550,22 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
             l_run += psum;
             // the last tile of the sequence: zero the latent rows past its end so that
             // stale slot contents (possibly NaN) cannot reach the output MMA
-            if (WIN) {
+            if (PACK) {
+                // as below; and of tokens that only some of the CTA's query tokens see, what is not finite must not
+                // reach the others' rows as 0 x NaN (in the rows that see it the logit is not finite either)
+                const int first_end = L_first - tile * KT;
+                const int hs = WIN ? p.sinks - tile * KT : 0;
+                const int ws = WIN ? L_first - p.window - tile * KT : 0, we = WIN ? L - p.window - tile * KT : 0;
+                if (first_end < KT || (we > 0 && hs < KT)) {
+                    const int r0 = WIN ? 0 : max(0, first_end);
+                    for (int e = tid - 64; e < (KT - r0) * LY::kLatBlocks * 8; e += 128) {
+                        const int rr = r0 + e / (LY::kLatBlocks * 8), rem = e % (LY::kLatBlocks * 8);
+                        uint4* at = reinterpret_cast<uint4*>(stg + (rem >> 3) * (KT * 128) + rr * 128 + (rem & 7) * 16);
+                        if (rr >= valid || (rr >= hs && rr < ws)) *at = make_uint4(0, 0, 0, 0);
+                        else if (rr >= first_end || (rr >= hs && rr < we)) *at = finite_bf16(*at);
+                    }
+                }
+            } else if (WIN) {
                 // tokens no row of the CTA sees: past its longest row, or between the sinks and its first row's window
                 const int hs = p.sinks - tile * KT, ws = L_first - p.window - tile * KT;
                 if (valid < KT || (ws > 0 && hs < KT)) {
@@ -555,7 +577,7 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
                     }
                 }
             }
-            if (!WIN && valid < KT) {
+            if (!PACK && !WIN && valid < KT) {
                 const int st = tid - 64;
                 const int nrow = KT - valid;
                 for (int e = st; e < nrow * LY::kLatBlocks * 8; e += 128) {
@@ -849,12 +871,12 @@ combine_var_kernel(const float* __restrict__ o_part, const float* __restrict__ l
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
-template <int DC, int DR, bool PLAIN, int NST, bool AKH, bool WIN>
+template <int DC, int DR, bool PLAIN, int NST, bool AKH, bool WIN, bool PACK>
 int launch_kernel_w(const CUtensorMap& lat, const CUtensorMap& rope, const CUtensorMap& qmap, const TcParams& tp,
                   int n_rb, int max_items, cudaStream_t s) {
     constexpr int KT = tile_of<DC>();
     using LY = Layout<DC, DR, NST, KT, WIN>;
-    auto k = decode_tc_kernel<DC, DR, PLAIN, NST, KT, AKH, WIN>;
+    auto k = decode_tc_kernel<DC, DR, PLAIN, NST, KT, AKH, WIN, PACK>;
     static_assert(LY::kBytes <= 232448, "shared memory budget");
     if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, LY::kBytes) != cudaSuccess)
         return QKMLA_ERR_CUDA;
@@ -866,8 +888,11 @@ int launch_kernel_w(const CUtensorMap& lat, const CUtensorMap& rope, const CUten
 template <int DC, int DR, bool PLAIN, int NST, bool AKH>
 int launch_kernel(const CUtensorMap& lat, const CUtensorMap& rope, const CUtensorMap& qmap, const TcParams& tp,
                   int n_rb, int max_items, cudaStream_t s) {
-    return tp.window > 0 ? launch_kernel_w<DC, DR, PLAIN, NST - 1, AKH, true>(lat, rope, qmap, tp, n_rb, max_items, s)
-                         : launch_kernel_w<DC, DR, PLAIN, NST, AKH, false>(lat, rope, qmap, tp, n_rb, max_items, s);
+    if (tp.rows_o > tp.H)
+        return tp.window > 0 ? launch_kernel_w<DC, DR, PLAIN, NST - 1, AKH, true, true>(lat, rope, qmap, tp, n_rb, max_items, s)
+                             : launch_kernel_w<DC, DR, PLAIN, NST, AKH, false, true>(lat, rope, qmap, tp, n_rb, max_items, s);
+    return tp.window > 0 ? launch_kernel_w<DC, DR, PLAIN, NST - 1, AKH, true, false>(lat, rope, qmap, tp, n_rb, max_items, s)
+                         : launch_kernel_w<DC, DR, PLAIN, NST, AKH, false, false>(lat, rope, qmap, tp, n_rb, max_items, s);
 }
 
 }  // namespace

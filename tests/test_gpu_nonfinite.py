@@ -110,3 +110,19 @@ def test_infinite_query(Q, kernel, splits, value):  # noqa: F811
     bad = np.zeros(c.lse.shape, bool)
     bad[0, 0, 5] = True
     check_rows(Q, dev, c, bad)
+
+
+@pytest.mark.parametrize("kernel", range(len(KERNELS)))
+@pytest.mark.parametrize("where,window", [("newest", 2000), ("newest", 0), ("oldest", 300)])
+def test_nan_of_another_query(Q, kernel, where, window):  # noqa: F811
+    """A NaN that only one query of the step sees -- the newest token, or the oldest of the first query's window --
+    leaves the other queries' rows alone, also where a CTA holds several queries."""
+    cache, simt, shape = KERNELS[kernel]
+    for s_q, lens in ((2, [1300, 65]), (4, [1090, 64])):
+        c = R.Case(lens, cache=cache, window=window, sinks=4 if window else 0, s_q=s_q, **shape)
+        dev = Device(Q, c, force_simt=simt)
+        n = lens[0]
+        poison(dev, c, "latent", 0, n - 1 if where == "newest" else n - s_q + 1 - window, 0)
+        bad = np.zeros(c.lse.shape, bool)
+        bad[0, s_q - 1 if where == "newest" else 0] = True
+        check_rows(Q, dev, c, bad)
