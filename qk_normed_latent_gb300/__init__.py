@@ -13,6 +13,7 @@ marshalled once, for loops over fixed buffers.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -180,6 +181,20 @@ def _stream(stream) -> Optional[int]:
     if stream is None:
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _stream_object(stream):
+    """`stream` (a torch stream or a raw handle) as a torch stream, the current one for None."""
+    torch = _torch()
+    if stream is None:
+        return torch.cuda.current_stream()
+    return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream(stream))
+
+
+def _launching(stream):
+    """Context in which torch allocates for work launched on `stream`: memory that only this call uses has to be
+    that stream's own, or the allocator hands it on while the call still runs."""
+    return contextlib.nullcontext() if stream is None else _torch().cuda.stream(_stream_object(stream))
 
 
 class Prepared:
@@ -360,16 +375,19 @@ def decode(q_tilde, alpha_q, q_rope, gamma_rope_q, kv_cache, ak_cache, seq_lens,
     query sees its last `window` tokens and the sequence's first `sinks`."""
     torch = _torch()
     if kv_scale is not None or window or sinks:
-        prepare_decode(q_tilde, alpha_q, q_rope, gamma_rope_q, kv_cache, ak_cache, seq_lens, page_table, page_size,
-                       max_pages, G, softmax_scale, eps, o, lse, plain, force_simt, num_splits, workspace, kv_scale,
-                       window, sinks)(stream)
+        with _launching(stream):
+            call = prepare_decode(q_tilde, alpha_q, q_rope, gamma_rope_q, kv_cache, ak_cache, seq_lens, page_table,
+                                  page_size, max_pages, G, softmax_scale, eps, o, lse, plain, force_simt, num_splits,
+                                  workspace, kv_scale, window, sinks)
+        call(stream)
         return o, lse
     a = make_decode_args(q_tilde, alpha_q, q_rope, gamma_rope_q, kv_cache, ak_cache, seq_lens, page_table,
                          page_size, max_pages, G, softmax_scale, eps, o, lse, plain, force_simt, num_splits,
                          workspace)
     need = decode_workspace_size(a)
     if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
-        workspace = torch.empty(need, dtype=torch.uint8, device=q_tilde.device)
+        with _launching(stream):
+            workspace = torch.empty(need, dtype=torch.uint8, device=q_tilde.device)
         a.workspace, a.workspace_bytes = workspace.data_ptr(), need
     decode_raw(a, stream)
     return o, lse
@@ -378,7 +396,10 @@ def decode(q_tilde, alpha_q, q_rope, gamma_rope_q, kv_cache, ak_cache, seq_lens,
 class PreparedDecode:
     """One qkmla_decode / qkmla_decode_ext call with its arguments marshalled and its workspace
     allocated once: the tensors must stay alive and in place; a call only adds the stream.  Calls that
-    may overlap on the GPU need a PreparedDecode (a workspace) each."""
+    may overlap on the GPU need a PreparedDecode (a workspace) each.  A workspace of its own belongs to the
+    stream that is current when it is made; the first call on another one waits for that (a captured call's
+    stream has to have waited before the capture, as torch.cuda.graph does), and the memory is kept until
+    every stream's calls are done."""
 
     def __init__(self, args: DecodeArgs, ext: Optional[DecodeExtArgs], workspace, device):
         torch = _torch()
@@ -388,6 +409,10 @@ class PreparedDecode:
         need = int(getattr(lib(), self.name + "_workspace_size")(*self.refs))
         if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
             workspace = torch.empty(need, dtype=torch.uint8, device=device)
+            self._streams = {_stream(None)}
+            self._ready = None if torch.cuda.is_current_stream_capturing() else torch.cuda.current_stream().record_event()
+        else:
+            self._streams = None             # the caller's workspace, or none
         self.workspace = workspace
         if workspace is not None:
             args.workspace, args.workspace_bytes = _ptr(workspace), workspace.numel() * workspace.element_size()
@@ -401,8 +426,17 @@ class PreparedDecode:
     def launch_count(self) -> int:
         return int(getattr(lib(), self.name + "_launch_count")(*self.refs))
 
+    def _join(self, stream) -> None:
+        if self._ready is not None and not _torch().cuda.is_current_stream_capturing():
+            stream.wait_event(self._ready)
+        self.workspace.record_stream(stream)
+
     def __call__(self, stream=None) -> None:
-        _check(self.name, self.fn(*self.refs, _stream(stream)))
+        handle = _stream(stream)
+        if self._streams is not None and handle not in self._streams:
+            self._join(_stream_object(stream))
+            self._streams.add(handle)
+        _check(self.name, self.fn(*self.refs, handle))
 
 
 def prepare_decode(q_tilde, alpha_q, q_rope, gamma_rope_q, kv_cache, ak_cache, seq_lens, page_table, page_size: int,
