@@ -242,7 +242,8 @@ typedef struct qkmla_decode_args {
     float softmax_scale;        /* multiplies the whole logit, e.g. 1/sqrt(d_h+d_r) */
     float eps;                  /* RMS epsilon of the RoPE query normalisation */
     unsigned flags;             /* QKMLA_FLAG_* */
-    int num_splits;             /* 0: automatic; k >= 1: k equal token ranges per sequence */
+    int num_splits;             /* 0: automatic; k >= 1 (to 1024): k equal token ranges per sequence; with k > 256
+                                 * or B k > 65535 the CUDA-core kernel serves the call */
     void* workspace;            /* device scratch, >= qkmla_decode_workspace_size(args) bytes */
     size_t workspace_bytes;
     void* o;                    /* [B][s_q][H][d_c] output in o_dtype */

@@ -56,6 +56,7 @@ static int validate_decode(const qkmla_decode_args* a, const DecodeExt& x) {
     if (a->page_size < 1 || a->max_pages < 1 || a->num_slots < 1 || a->num_slots % a->page_size)
         return QKMLA_ERR_INVALID;
     if (a->num_splits < 0 || a->num_splits > 1024) return QKMLA_ERR_INVALID;
+    if ((int64_t)a->B * a->s_q > INT32_MAX / a->H) return QKMLA_ERR_INVALID;   // rows are counted, and launched, as int
     if (a->cache_dtype != QKMLA_F32 && a->cache_dtype != QKMLA_BF16 && !(q8 && x.kv_scale)) return QKMLA_ERR_UNSUPPORTED;
     if (q8 && (a->d_c % 2 || !aligned(x.kv_scale, 4))) return QKMLA_ERR_INVALID;
     if (a->o_dtype != QKMLA_F32 && a->o_dtype != QKMLA_BF16) return QKMLA_ERR_UNSUPPORTED;
@@ -71,6 +72,11 @@ static int validate_decode(const qkmla_decode_args* a, const DecodeExt& x) {
     return QKMLA_OK;
 }
 
+// Split counts the tensor-core kernels are launched with: an item a CTA in the grid's y, at most 65535.
+static bool tc_splits(const qkmla_decode_args* a) {
+    return a->num_splits <= 256 && (int64_t)a->B * a->num_splits <= 65535;
+}
+
 int plan_decode(const qkmla_decode_args* a, const DecodeExt& x, DecodePlan* plan) {
     const int v = validate_decode(a, x);
     if (v != QKMLA_OK) return v;
@@ -78,7 +84,7 @@ int plan_decode(const qkmla_decode_args* a, const DecodeExt& x, DecodePlan* plan
     if (sms <= 0) return QKMLA_ERR_CUDA;
     const bool stall = (a->flags & QKMLA_FLAG_TEST_STALL) != 0;
     if (stall && x.active()) return QKMLA_ERR_UNSUPPORTED;
-    if (!(a->flags & QKMLA_FLAG_FORCE_SIMT) && tc_supported(a) && a->num_splits <= 256) {
+    if (!(a->flags & QKMLA_FLAG_FORCE_SIMT) && tc_supported(a) && tc_splits(a)) {
         if (stall && pair_shape(a)) return QKMLA_ERR_UNSUPPORTED;   // the hook exists in the 64-row kernel only
         plan->kernel = 1;
         plan->num_splits = a->num_splits;
@@ -87,7 +93,7 @@ int plan_decode(const qkmla_decode_args* a, const DecodeExt& x, DecodePlan* plan
         return QKMLA_OK;
     }
     if (stall) return QKMLA_ERR_UNSUPPORTED;
-    if (!(a->flags & QKMLA_FLAG_FORCE_SIMT) && q8_tc_supported(a, x) && a->num_splits <= 256) {
+    if (!(a->flags & QKMLA_FLAG_FORCE_SIMT) && q8_tc_supported(a, x) && tc_splits(a)) {
         plan->kernel = 1;
         plan->num_splits = a->num_splits;
         plan->parts = 0;
@@ -190,7 +196,7 @@ int qkmla_append_q8(const float* c_new, const float* k_rope_new, const int32_t* 
                     int d_h, int d_r, float eps, unsigned flags, void* kv_cache, float* kv_scale, void* ak_cache,
                     int64_t num_slots, void* stream) {
     const bool plain = (flags & QKMLA_FLAG_PLAIN_MLA) != 0;
-    if (N < 0 || G < 1 || d_c < 1 || d_h < 1 || d_r < 0 || num_slots < 1) return QKMLA_ERR_INVALID;
+    if (N < 0 || G < 1 || G > 65535 || d_c < 1 || d_h < 1 || d_r < 0 || num_slots < 1) return QKMLA_ERR_INVALID;
     if (d_h > 256 || d_c % 2 || !(eps >= 0.f)) return QKMLA_ERR_INVALID;
     if (d_c > 512 || d_r > 64) return QKMLA_ERR_UNSUPPORTED;
     if (N == 0) return QKMLA_OK;

@@ -1,0 +1,12 @@
+"""Sizes beyond a launch's limits are refused on the host."""
+import ctypes
+
+from test_q8_window import Q, args  # noqa: F401
+
+
+def test_launch_limits_are_refused(Q):  # noqa: F811
+    """More rows than an int counts, and more groups than a grid takes."""
+    lib, f = Q.lib(), ctypes.c_void_p(4096)
+    a, x = args(Q, B=1 << 20, s_q=1 << 7, H=16)
+    assert lib.qkmla_decode_ext(ctypes.byref(a), ctypes.byref(x), None) == Q.ERR_INVALID
+    assert lib.qkmla_append_q8(f, f, None, 0.0, f, None, f, 4, 65536, 256, 64, 32, 1e-6, 0, f, f, f, 64, None) == Q.ERR_INVALID
