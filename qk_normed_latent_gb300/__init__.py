@@ -284,6 +284,18 @@ def prepare_append_q8(c_new, k_rope_new, w_k, gamma_rope_k, slot_mapping, kv_cac
     d_r = k_rope_new.shape[1] if k_rope_new is not None else 0
     G, _, d_h = w_k.shape
     _check_q8_cache(kv_cache, kv_scale, d_c, d_r)
+    torch = _torch()
+    f32 = torch.float32
+    _expect("c_new", c_new, f32, N, d_c)
+    _expect("w_k", w_k, f32, G, d_c, d_h)
+    _expect("slot_mapping", slot_mapping, torch.int64, N)
+    _expect("ak_cache", ak_cache, (f32, torch.float16), kv_cache.shape[0], G)
+    if k_rope_new is not None:
+        _expect("k_rope_new", k_rope_new, f32, N, d_r)
+    if gamma_rope_k is not None:
+        _expect("gamma_rope_k", gamma_rope_k, f32, d_r)
+    if positions is not None:
+        _expect("positions", positions, torch.int32, N)
     flags = (FLAG_PLAIN_MLA if plain else 0) | _alpha_flag(ak_cache)
     return Prepared("qkmla_append_q8",
                     (_ptr(c_new), _ptr(k_rope_new), _ptr(positions), float(rope_theta), _ptr(w_k), _ptr(gamma_rope_k),
@@ -298,6 +310,17 @@ def append_q8(c_new, k_rope_new, w_k, gamma_rope_k, slot_mapping, kv_cache, kv_s
     With positions [N] (int32) and rope_theta the RoPE keys come unrotated, as in append_rope()."""
     prepare_append_q8(c_new, k_rope_new, w_k, gamma_rope_k, slot_mapping, kv_cache, kv_scale, ak_cache, eps, positions,
                       rope_theta, plain)(stream)
+
+
+def _expect(name: str, t, dtypes, *shape) -> None:
+    """`t` has one of `dtypes` and `shape` (as many elements, where it may come in another form)."""
+    want = 1
+    for n in shape:
+        want *= n
+    dtypes = dtypes if isinstance(dtypes, tuple) else (dtypes,)
+    if t is None or t.dtype not in dtypes or t.numel() != want:
+        got = "missing" if t is None else f"{t.dtype} {tuple(t.shape)}"
+        raise ValueError(f"qkmla: {name} is {' or '.join(str(d) for d in dtypes)} {tuple(shape)}, not {got}")
 
 
 def _check_q8_cache(kv_cache, kv_scale, d_c: int, d_r: int) -> None:
@@ -445,14 +468,34 @@ def prepare_decode(q_tilde, alpha_q, q_rope, gamma_rope_q, kv_cache, ak_cache, s
                    sinks: int = 0) -> PreparedDecode:
     """decode() for fixed tensors (see decode)."""
     torch = _torch()
+    f32 = torch.float32
+    B, s_q, H, d_c = q_tilde.shape
+    d_r = q_rope.shape[-1] if q_rope is not None else 0
+    q8 = kv_cache.dtype == torch.uint8
+    if q8:
+        _check_q8_cache(kv_cache, kv_scale, d_c, d_r)
+        if q_tilde.dtype != torch.bfloat16:
+            raise ValueError(f"qkmla: with an 8-bit cache q_tilde is bfloat16, not {q_tilde.dtype}")
+    else:
+        _expect("kv_cache", kv_cache, (f32, torch.bfloat16), kv_cache.shape[0], d_c + d_r)
+        _expect("q_tilde", q_tilde, kv_cache.dtype, B, s_q, H, d_c)
+    if not plain:
+        _expect("alpha_q", alpha_q, f32, B, s_q, H)
+        _expect("ak_cache", ak_cache, (f32, torch.float16), kv_cache.shape[0], G)
+    if q_rope is not None:
+        _expect("q_rope", q_rope, f32, B, s_q, H, d_r)
+    if gamma_rope_q is not None:
+        _expect("gamma_rope_q", gamma_rope_q, f32, d_r)
+    _expect("seq_lens", seq_lens, torch.int32, B)
+    if page_table is not None:
+        _expect("page_table", page_table, torch.int32, B, max_pages)
+    _expect("o", o, (f32, torch.bfloat16), B, s_q, H, d_c)
+    if lse is not None:
+        _expect("lse", lse, f32, B, s_q, H)
     a = make_decode_args(q_tilde, alpha_q, q_rope, gamma_rope_q, kv_cache, ak_cache, seq_lens, page_table, page_size,
                          max_pages, G, softmax_scale, eps, o, lse, plain, force_simt, num_splits)
     ext = None
-    if kv_scale is not None or window or sinks or a.cache_dtype == E4M3:
-        if a.cache_dtype == E4M3:
-            _check_q8_cache(kv_cache, kv_scale, a.d_c, a.d_r)
-            if q_tilde.dtype != torch.bfloat16:
-                raise ValueError(f"qkmla: with an 8-bit cache q_tilde is bfloat16, not {q_tilde.dtype}")
+    if kv_scale is not None or window or sinks or q8:
         ext = DecodeExtArgs(_ptr(kv_scale), int(window), int(sinks))
     return PreparedDecode(a, ext, workspace, q_tilde.device)
 
