@@ -75,6 +75,7 @@ class DeviceState:
         self.w = w
         self.q8 = w.cache_dtype == "e4m3"
         self.window, self.sinks = window, sinks
+        self.extended = self.q8 or window != 0 or sinks != 0      # decoded by qkmla_decode_ext
         self.plain = plain
         self.dev = torch.device(device)
         self.lens = W.seq_lens(w)
@@ -187,7 +188,7 @@ class DeviceState:
         return a
 
     def decode(self, num_splits: int = 0, force_simt: bool = False, stream=None):
-        if self.q8 or self.window:
+        if self.extended:
             self.prepared_decode(num_splits, force_simt)(stream)
             return
         self.args = self.decode_args(num_splits, force_simt)
@@ -197,7 +198,7 @@ class DeviceState:
         """One pass of the whole path: absorb, append this step's tokens, decode."""
         self.absorb(stream)
         self.append_step(stream)
-        if self.q8 or self.window:
+        if self.extended:
             self.prepared_decode(num_splits, force_simt)(stream)
             return
         if self.args is None or num_splits != self.args.num_splits:
