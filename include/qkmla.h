@@ -226,11 +226,11 @@ int qkmla_project_query(const void* x, const void* w_q, const int32_t* positions
 
 /* Arguments of qkmla_decode (plain pointers and sizes). */
 typedef struct qkmla_decode_args {
-    const void* q_tilde;        /* [B][s_q][H][d_c] in cache_dtype (from absorb) */
+    const void* q_tilde;        /* [B][s_q][H][d_c] in cache_dtype (from absorb); bf16 with QKMLA_E4M3 */
     const float* alpha_q;       /* [B][s_q][H] fp32 */
     const float* q_rope;        /* [B][s_q][H][d_r] fp32, post-RoPE, not normalised */
     const float* gamma_rope_q;  /* [d_r] fp32 or NULL (ones) */
-    const void* kv_cache;       /* [num_slots][d_c+d_r] cache_dtype */
+    const void* kv_cache;       /* [num_slots][d_c+d_r] cache_dtype; with QKMLA_E4M3 rows of d_c codes and d_r bf16 */
     const void* ak_cache;       /* [num_slots][G] fp32 (fp16 with QKMLA_FLAG_ALPHA_F16) */
     const int32_t* seq_lens;    /* [B] int32 device: tokens in the cache incl. this step's s_q */
     const int32_t* page_table;  /* [B][max_pages] int32 device, or NULL (contiguous) */
@@ -238,7 +238,7 @@ typedef struct qkmla_decode_args {
     int page_size;              /* tokens per page (> 0) */
     int max_pages;              /* page-table row length; max tokens = max_pages*page_size */
     int B, s_q, H, G, d_c, d_r;
-    int cache_dtype;            /* QKMLA_F32 or QKMLA_BF16 */
+    int cache_dtype;            /* QKMLA_F32 or QKMLA_BF16; QKMLA_E4M3 in qkmla_decode_ext alone */
     float softmax_scale;        /* multiplies the whole logit, e.g. 1/sqrt(d_h+d_r) */
     float eps;                  /* RMS epsilon of the RoPE query normalisation */
     unsigned flags;             /* QKMLA_FLAG_* */
