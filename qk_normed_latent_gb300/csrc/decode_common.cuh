@@ -147,6 +147,12 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
+// The same, NaN if any input is.
+__device__ __forceinline__ float fmax3_nan(float a, float b, float c) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
 // Bounded wait: spins on try_wait, checks the wall clock every 256 polls and
 // gives up (recording QKMLA_ERR_TIMEOUT) after limit_ns.
 __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, int* status,

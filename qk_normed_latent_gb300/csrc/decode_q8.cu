@@ -697,16 +697,17 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
                     w2[u] = f2_mul(e2[u], f2_mul(st2, f2v[u]));
                     const float2 w = f2_unpack(w2[u]);
                     top_e = fmax3(top_e, e.x, e.y);
-                    top_w = fmax3(top_w, w.x, w.y);
+                    top_w = fmax3_nan(top_w, w.x, w.y);
                 }
                 if (masked && !sees) {                       // a row without a token yet has -inf less -inf
 #pragma unroll
                     for (int u = 0; u < HP2; ++u) e2[u] = w2[u] = f2(0.f, 0.f);
+                    top_w = top_e = 0.f;
                 }
             };
             weigh();
             const bool settle = j == settle1 || j == settle2;
-            const bool need = top_w > kTopP || top_e > kTopE || j == 0 || settle;
+            const bool need = !(top_w <= kTopP) || top_e > kTopE || j == 0 || settle;
             if (group_any(grp, need || !got_s)) {
                 if (group_any(grp, !got_s)) { ok = false; break; }
                 // ---- exact maxima of this tile's logits and contributions, per row ----
@@ -744,12 +745,12 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
                     const float cm = m0 == -INFINITY ? 0.f : exp2f(m0 - m1);       // of the row sums
                     // nothing to add up yet (no visible token, or latents of zeros, whose scale is 0): with the largest
                     // unit the first contribution, whatever its tile, is above kTopP and sets it
-                    const float f1 = kPUnit * exp2f(v1 == -INFINITY ? 95.f : fminf(fmaxf(m1 - v1, -110.f), 95.f));
+                    const float f1 = kPUnit * exp2f(v1 == -INFINITY ? 122.f : fminf(fmaxf(m1 - v1, -126.f), 122.f));
                     m_s[r] = m1;
                     v_s[r] = v1;
                     f_s[r] = f1;
                     red_s[r] = cm;
-                    corr_s[r] = f0 > 0.f ? cm * (f1 / f0) : 0.f;                   // of O^T; nothing there yet: 0
+                    corr_s[r] = f0 > 0.f ? cm * f1 / f0 : 0.f;                     // of O^T; nothing there yet: 0
                 }
                 group_sync(grp);
                 if (j > 0) {
@@ -781,6 +782,11 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
                     lsum2[u] = f2_mul(lsum2[u], f2(red_s[u0 + 2 * u], red_s[u0 + 2 * u + 1]));
                 reload();
                 weigh();
+#pragma unroll
+                for (int u = 0; u < HP2; ++u) {              // s_t f beyond fp32 beside e = 0: no weight, not NaN
+                    const float2 e = f2_unpack(e2[u]), w = f2_unpack(w2[u]);
+                    w2[u] = f2(e.x == 0.f ? 0.f : w.x, e.y == 0.f ? 0.f : w.y);
+                }
                 group_sync(grp);                             // red_s, corr_s are read
             }
             const Dither<LY::kStacked> dither(t);
@@ -835,7 +841,7 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
             const int r = ug + gt;
             const float l = (red_s[r] + red_s[ROWS + r]) + (red_s[2 * ROWS + r] + red_s[3 * ROWS + r]);
             const float lse = l > 0.f ? (m_s[r] + log2f(l)) * kLn2 : (l == 0.f ? -INFINITY : l);
-            inv_s[r] = (l == 0.f || (f_s[r] == 0.f && l == l)) ? 0.f : 1.f / (f_s[r] * l);
+            inv_s[r] = l == 0.f ? 0.f : 1.f / f_s[r] / l;
             if (row0 + r < n_rows) {
                 if (it.part >= 0) p.lse_part[(size_t)it.part * n_rows + row0 + r] = lse;
                 else if (p.lse) p.lse[grow0 + r] = lse;
