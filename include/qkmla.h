@@ -236,7 +236,7 @@ typedef struct qkmla_decode_args {
     const int32_t* page_table;  /* [B][max_pages] int32 device, or NULL (contiguous) */
     int64_t num_slots;          /* slots in kv_cache / ak_cache (multiple of page_size) */
     int page_size;              /* tokens per page (> 0) */
-    int max_pages;              /* page-table row length; max tokens = max_pages*page_size */
+    int max_pages;              /* page-table row length; max tokens = max_pages*page_size, below 2^31 - 4096 */
     int B, s_q, H, G, d_c, d_r;
     int cache_dtype;            /* QKMLA_F32 or QKMLA_BF16; QKMLA_E4M3 in qkmla_decode_ext alone */
     float softmax_scale;        /* multiplies the whole logit, e.g. 1/sqrt(d_h+d_r) */

@@ -55,6 +55,7 @@ static int validate_decode(const qkmla_decode_args* a, const DecodeExt& x) {
     if (a->H % a->G) return QKMLA_ERR_INVALID;
     if (a->page_size < 1 || a->max_pages < 1 || a->num_slots < 1 || a->num_slots % a->page_size)
         return QKMLA_ERR_INVALID;
+    if ((int64_t)a->max_pages * a->page_size > INT32_MAX - 4096) return QKMLA_ERR_INVALID;   // tokens are counted as int
     if (a->num_splits < 0 || a->num_splits > 1024) return QKMLA_ERR_INVALID;
     if ((int64_t)a->B * a->s_q > INT32_MAX / a->H) return QKMLA_ERR_INVALID;   // rows are counted, and launched, as int
     if (a->cache_dtype != QKMLA_F32 && a->cache_dtype != QKMLA_BF16 && !(q8 && x.kv_scale)) return QKMLA_ERR_UNSUPPORTED;
