@@ -312,6 +312,11 @@ def append_q8(c_new, k_rope_new, w_k, gamma_rope_k, slot_mapping, kv_cache, kv_s
                       rope_theta, plain)(stream)
 
 
+def _c_int(n) -> int:
+    """n as a C int takes it: a window or sinks beyond mean every token, as the largest one does."""
+    return max(-1, min(int(n), 0x7FFFFFFF))
+
+
 def _expect(name: str, t, dtypes, *shape) -> None:
     """`t` has one of `dtypes` and `shape` (as many elements, where it may come in another form)."""
     want = 1
@@ -496,7 +501,7 @@ def prepare_decode(q_tilde, alpha_q, q_rope, gamma_rope_q, kv_cache, ak_cache, s
                          max_pages, G, softmax_scale, eps, o, lse, plain, force_simt, num_splits)
     ext = None
     if kv_scale is not None or window or sinks or q8:
-        ext = DecodeExtArgs(_ptr(kv_scale), int(window), int(sinks))
+        ext = DecodeExtArgs(_ptr(kv_scale), _c_int(window), _c_int(sinks))
     return PreparedDecode(a, ext, workspace, q_tilde.device)
 
 

@@ -20,3 +20,10 @@ def test_token_counts_beyond_int_are_refused(Q):  # noqa: F811
         assert lib.qkmla_decode_ext(ctypes.byref(a), ctypes.byref(x), None) == Q.ERR_INVALID
         a, x = args(Q, max_pages=pages, cache_dtype=Q.BF16)
         assert lib.qkmla_decode(ctypes.byref(a), None) == Q.ERR_INVALID
+
+
+def test_window_beyond_int_means_every_token(Q):  # noqa: F811
+    """ctypes cuts a Python int to 32 bits: 2^32 + 5 was a window of 5."""
+    for n, want in ((0, 0), (7, 7), (2 ** 31 - 1, 2 ** 31 - 1), (2 ** 32 + 5, 2 ** 31 - 1), (2 ** 63, 2 ** 31 - 1),
+                    (-1, -1), (-2 ** 32, -1)):
+        assert Q.DecodeExtArgs(None, Q._c_int(n), 0).window == want
