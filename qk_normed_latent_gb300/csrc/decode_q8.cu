@@ -50,12 +50,13 @@
 // the same on every call.  What N tokens are off by is then sqrt(N) steps of at most 2^-13,
 // not N of them.  (2) Long items raise their units, by one move, when some tiles have shown
 // what is large: more than 32 tiles after 4 of them, to 4 .. 8 for the largest contribution in
-// the first and the fifth tile (8 .. 16 in more than 128 tiles), more than 256 after 128
-// again, to 64 .. 128.  Few later ones exceed that.  A step is then at most 2^-14 (2^-15,
-// 2^-16, 2^-19) of the largest for 2^11 (2^13, 2^14, more) tokens: against 64 bits, one
-// token over a flat background with latents of 3 times its norm, at the worst ratio,
-// 4.9e-3 (4.4e-3, 3.1e-3, 3.6e-3) of the result's norm.  Both cost 0 .. 3 % (64 x 4096
-// tokens 89 -> 92 us, 4 x 262144 269 -> 276, windowed 99 -> 96, 512-token items nothing).
+// the first and the fifth tile (8 .. 16 in more than 128 tiles, and from 16 tiles on where lo has
+// its own accumulator), more than 256 after 128 again, to 64 .. 128.  Few later ones exceed that.
+// A step is then at most 2^-14 (2^-15, 2^-16, 2^-19) of the largest for 2^11 (2^13, 2^14, more)
+// tokens.  Against 64 bits, one token over a flat background of 2000 (8000, 16000, 262144), with
+// latents of up to 3 times its norm: 3.7e-3 (3.6e-3, 3.4e-3, 2.8e-3) of the result's norm at the
+// worst ratio.  Cost: 64 x 4096 tokens 89 -> 92 us, 4 x 262144 269 -> 276, windowed 99 -> 96,
+// few rows nothing.
 //
 // What bounds it (512 / 64, 64 rows): a tile takes 2340 cycles, of which the tensor core
 // needs 2076 (20 x 65 + 16 x 48) and shared memory at 128 bytes a cycle about 2200: the 36
@@ -95,8 +96,8 @@ constexpr float kTopP = 448.f;       // a P above this (e4m3's largest value) mo
 constexpr float kTopE = 1.09951163e12f;   // and so does 2^(x - m) above 2^40, fp32's margin for the row sums
 constexpr float kLoUnit = 16.f;      // of the remainder's column where it has an accumulator of its own
 constexpr int kSettle1 = 4, kSettle2 = 128;            // tiles after which items of more than
-constexpr int kSettleFrom1 = 32, kSettleFrom2 = 256;   // this many raise their units
-constexpr int kSettleMore = 128;                       // tiles from which the first time is one binade more
+constexpr int kSettleFrom1 = 32, kSettleFrom2 = 256;   // this many raise their units (two accumulators: 16, at no cost)
+constexpr int kSettleMore = 128;                       // tiles from which the first time is one binade more (always)
 
 template <int DC, int DR, int ROWS>
 struct Q8Layout {
@@ -593,7 +594,7 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
         // this group's rows in registers, two to a packed pair: -m, unit f, row sums
         constexpr int HP2 = kHpt / 2;
         uint64_t nm2[HP2], f2v[HP2], lsum2[HP2];
-        const int settle1 = n_t > kSettleFrom1 ? kSettle1 : INT32_MAX, settle2 = n_t > kSettleFrom2 ? kSettle2 : INT32_MAX;
+        const int settle1 = n_t > (LY::kStacked ? 16 : kSettleFrom1) ? kSettle1 : INT32_MAX, settle2 = n_t > kSettleFrom2 ? kSettle2 : INT32_MAX;
         auto reload = [&]() {
 #pragma unroll
             for (int u = 0; u < HP2; ++u) {
@@ -739,7 +740,7 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
                     const float m0 = m_s[r], v0 = v_s[r], f0 = f_s[r];
                     t_s[r] = vx = fmaxf(vx, t_s[r]);
                     // binades between the largest contribution and 16: the first tiles' will be exceeded
-                    const float room = j >= settle2 ? -3.f : j >= settle1 ? (n_t > kSettleMore ? 0.f : 1.f) : v0 == -INFINITY ? 2.f : 1.f;
+                    const float room = j >= settle2 ? -3.f : j >= settle1 ? (LY::kStacked || n_t > kSettleMore ? 0.f : 1.f) : v0 == -INFINITY ? 2.f : 1.f;
                     const float m1 = mx > m0 + 4.f ? ceilf(mx) : m0;
                     const float v1 = vx > v0 + fmaxf(2.f, 1.f - room) || (settle && vx > -INFINITY) ? ceilf(vx) + room : v0;
                     const float cm = m0 == -INFINITY ? 0.f : exp2f(m0 - m1);       // of the row sums
