@@ -58,15 +58,16 @@
 // worst ratio.  Cost: 64 x 4096 tokens 89 -> 92 us, 4 x 262144 269 -> 276, windowed 99 -> 96,
 // few rows nothing.
 //
-// What bounds it (512 / 64, 64 rows): a tile takes 2340 cycles, of which the tensor core
-// needs 2076 (20 x 65 + 16 x 48) and shared memory at 128 bytes a cycle about 2200: the 36
-// MMAs read 6 KB of operands each, 216 KB, the tile is 43 KB, P and the softmax's loads ~20 KB.
-// (With the query parts as the M = 128 operand an MMA takes 48 cycles and S fits twice, but it
-// reads the same 6 KB and the softmax, a thread to a row, loads twice as much: 2900 cycles.)
-// 64 sequences x 4096 tokens x 128 heads: 88 us (2.22 TB/s, 0.83 PFLOP/s counted once; the
-// two parts make it 1.6), of which ~13 us are the start and end of the items; 4 x 262144
-// tokens: 269 us (1.09 PFLOP/s).  The bf16 pair kernel takes 119 and 342 us.
-// With 16 rows (d_c = 256) the calls are latency-bound: 16 sequences of 1k-8k tokens 14 us.
+// What bounds it (512 / 64, 64 rows): a tile takes about 2380 cycles.  Its MMAs alone, one after
+// the other, would take 2076 (20 x 65 + 16 x 48; the pipe's own counter says 1880 busy) and shared
+// memory at 128 bytes a cycle about 2200: the 36 MMAs read 6 KB of operands each, 216 KB, the tile
+// is 43 KB, P and the softmax's loads ~20 KB.  (With the query parts as the M = 128 operand an MMA
+// takes 48 cycles and S fits twice, but it reads the same 6 KB and the softmax, a thread to a row,
+// loads twice as much: 2900 cycles.)  64 sequences x 4096 tokens x 128 heads: 92 us (2.13 TB/s,
+// 0.79 PFLOP/s counted once; the two parts make it 1.6) on 128 of the 152 SMs, of which ~13 us are
+// the start and end of the items; 4 x 262144 tokens: 279 us (1.05 PFLOP/s).  The bf16 pair kernel
+// takes 119 and 342 us.  With 16 rows (d_c = 256) the calls are latency-bound: 16 sequences of
+// 1k-8k tokens 14 us.
 //
 // Warps: 0 TMA producer (+ TMEM owner), 1 logit MMAs, 2 output MMAs (each issue loop in
 // one elected lane: a branch on the lane number costs ~88 cycles an MMA), then softmax and

@@ -17,7 +17,7 @@
 // chunks if below min_tokens); all chunks start first, then the remainders, longest
 // first.  Equal parts of about a share leave nothing short to fill up the second
 // wave: 32 sequences of 512-32k tokens, two query tokens, 8-bit cache, 208 us
-// against 172; windowed, bf16, 227 against 197.  (Chunks of 0.9-1.15 shares and the
+// against 172 (179 since small weights keep their sum); windowed, bf16, 227 against 199.  (Chunks of 0.9-1.15 shares and the
 // best of 8 lengths of equal parts are behind in a model of the plan.)  It costs
 // other calls up to 0.4 us.  Only qkmla_decode_ext's calls use it: the others keep
 // their results bit for bit.
