@@ -188,7 +188,10 @@ def _stream_object(stream):
     torch = _torch()
     if stream is None:
         return torch.cuda.current_stream()
-    return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream(stream))
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    handle = _stream(stream)             # 0: the default stream (as an external handle it would be a new stream)
+    return torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
 
 
 def _launching(stream):

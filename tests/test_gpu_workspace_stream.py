@@ -82,3 +82,24 @@ def test_workspace_made_behind_pending_work(Q):  # noqa: F811
         call(side)
         torch.cuda.synchronize()
         assert torch.equal(dev.o, want)
+
+
+@pytest.mark.parametrize("cache,window", CALLS)
+def test_decode_on_the_default_stream_by_handle(Q, cache, window):  # noqa: F811
+    """Handle 0 is the default stream, also where another one is current."""
+    c = R.Case([1500, 700], cache=cache, window=window)
+    dev = Device(Q, c, num_splits=3)
+    need = dev.call.workspace.numel()
+    dev.call()
+    torch.cuda.synchronize()
+    want = dev.o.clone()
+    dev.o.zero_()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(2000000)                                     # on the default stream
+    with torch.cuda.stream(torch.cuda.Stream()):
+        Q.decode(*arguments(dev, c), num_splits=3, kv_scale=dev.scale, window=window, stream=0)
+        own = [torch.full((need,), 7, dtype=torch.uint8, device="cuda") for _ in range(3)]
+    torch.cuda.synchronize()
+    assert all(bool((x == 7).all()) for x in own)
+    assert torch.equal(dev.o, want)
+    assert Q._stream_object(0) == torch.cuda.default_stream()
