@@ -590,7 +590,8 @@ decode_q8_kernel(const __grid_constant__ CUtensorMap tm_lat, const __grid_consta
         const int hshift = 31 - __clz(p.H / p.G);            // heads a group: 2, 4, 8 or 16 (H >= 16, G <= 8)
         const int h0 = (row0 + u0) % p.H;                    // its head: kHpt divides H, so the rows share a query token
         const int ak_at = tl * p.G + (h0 >> hshift);         // alpha^k of this token for the first of the rows
-        const int n_row = max(0, len - p.s_q + (row0 + u0) / p.H + 1);   // causal length of these rows
+        // causal length of these rows (those beyond the last query token, of no one, see what it sees)
+        const int n_row = max(0, min(len, len - p.s_q + (row0 + u0) / p.H + 1));
         const int w_row = p.window > 0 ? n_row - p.window : 0;
         // this group's rows in registers, two to a packed pair: -m, unit f, row sums
         constexpr int HP2 = kHpt / 2;
