@@ -46,7 +46,9 @@
  *    stream.  Reads of inputs no kernel of the library writes may start
  *    earlier: seq_lens in qkmla_decode and qkmla_decode_ext; W^K, the new tokens,
  *    their slots and positions in qkmla_append, qkmla_append_rope and
- *    qkmla_append_q8.  A previous kernel that
+ *    qkmla_append_q8; the positions in qkmla_rope; out_start, first and the page table
+ *    in qkmla_read_cache; seq_lens, chunk_start, the page table and the gains in
+ *    qkmla_prefill.  A previous kernel that
  *    itself signals early dependent launch must therefore not be writing
  *    those inputs (kernels that do not signal it, and copies, are waited for
  *    in full as usual).
@@ -408,6 +410,174 @@ int qkmla_decode_noalloc(const qkmla_decode_args* a, void* stream);
  */
 int qkmla_up_project(const void* o, int o_dtype, const void* w_v, int rows, int H, int G_v, int d_c,
                      int d_v, void* out, int out_dtype, void* stream);
+
+/* Layouts and frequencies of qkmla_rope. */
+enum { QKMLA_ROPE_INTERLEAVED = 0, QKMLA_ROPE_HALVES = 1 };
+enum { QKMLA_ROPE_PLAIN = 0, QKMLA_ROPE_LINEAR = 1, QKMLA_ROPE_YARN = 2, QKMLA_ROPE_GIVEN = 3 };
+
+/* Arguments of qkmla_rope. */
+typedef struct qkmla_rope_args {
+    const void* x;              /* element (r, h, j) at x + r x_row_stride + h x_head_stride + j, in dtype */
+    void* out;                  /* likewise; may be x with x's strides (in place), else no overlap with x */
+    const int32_t* positions;   /* [rows] int32 device: any value */
+    int64_t x_row_stride, x_head_stride, out_row_stride, out_head_stride;   /* in elements */
+    int rows, heads, d_r;       /* d_r even, at most 256: the elements of each head that are rotated */
+    int dtype;                  /* QKMLA_F32 or QKMLA_BF16, of x and out */
+    int layout;                 /* pairs (2i, 2i + 1), or with QKMLA_ROPE_HALVES (i, i + d_r / 2) */
+    int inverse;                /* not 0: turned back, by the opposite angles (also the backward pass) */
+    int scaling;                /* QKMLA_ROPE_*: how the pairs' frequencies are formed */
+    float theta;                /* frequency of pair i: theta^(-2i/d_r); > 1 (not read with GIVEN) */
+    float factor;               /* LINEAR, YARN: how many times the original context */
+    int original_context;       /* YARN: tokens of the original context */
+    float beta_fast, beta_slow; /* YARN: turns within it, usually 32 and 1 */
+    float attention_factor;     /* multiplies the result; 0 means 1 */
+    const double* frequencies;  /* GIVEN: HOST array [d_r / 2], radians a position; read during the call */
+} qkmla_rope_args;
+
+/*
+ * qkmla_rope -- rotary positions on RoPE blocks that lie on their own or inside a
+ * head: queries and keys whose positions are scaled for a long context or whose
+ * pairs are halves apart, which the rotations fused into qkmla_project_query and
+ * qkmla_append_rope (interleaved, unscaled) do not serve.
+ *
+ *   (a, b) -> attention_factor (a cos - b sin, a sin + b cos),  angle = positions[r] f_i
+ *
+ * f_i = theta^(-2i/d_r); LINEAR: divided by factor; YARN: with u_i the ramp from 0 at
+ * pair floor(c(beta_fast)) to 1 at pair ceil(c(beta_slow)), both within [0, d_r - 1],
+ * c(n) = d_r ln(original_context / (2 pi n)) / (2 ln theta): f_i (u_i / factor + 1 - u_i);
+ * GIVEN: frequencies[i].  Elements outside the rotated part are neither read nor
+ * written.  Computed in fp32 with angles exact to 2^-24 of a turn or better at every
+ * position, one rounding to bf16.  rows == 0 is a no-op.
+ * Errors: INVALID for null pointers, sizes, an odd d_r, unknown layout or scaling, theta <= 1,
+ * factor <= 0, bad betas, a frequency that is not finite, misaligned elements; UNSUPPORTED
+ * for another dtype, d_r > 256 or more heads than a launch takes.
+ */
+int qkmla_rope(const qkmla_rope_args* a, void* stream);
+
+/* Arguments of qkmla_read_cache. */
+typedef struct qkmla_read_cache_args {
+    const void* kv_cache;       /* [num_slots][d_c+d_r] cache_dtype; with QKMLA_E4M3 rows of d_c codes and d_r bf16 */
+    const float* kv_scale;      /* [num_slots] fp32, with QKMLA_E4M3 only (else NULL) */
+    const void* ak_cache;       /* [num_slots][G] fp32 (fp16 with QKMLA_FLAG_ALPHA_F16); NULL without ak */
+    const int32_t* out_start;   /* [B+1] int32 device, not decreasing: output rows of each sequence */
+    const int32_t* first;       /* [B] int32 device: a sequence's first token to be read, or NULL (0) */
+    const int32_t* page_table;  /* [B][max_pages] int32 device, or NULL (contiguous) */
+    int64_t num_slots;
+    int page_size, max_pages;
+    int B, rows, G, d_c, d_r;   /* rows: of the outputs; those outside [out_start[0], out_start[B]) stay as they are */
+    int cache_dtype;            /* QKMLA_F32, QKMLA_BF16 or QKMLA_E4M3 */
+    int out_dtype;              /* QKMLA_F32 or QKMLA_BF16, of c and r */
+    unsigned flags;             /* QKMLA_FLAG_ALPHA_F16 */
+    void* c;                    /* [rows][d_c] the stored latents */
+    void* r;                    /* [rows][d_r] the stored (normalised) RoPE keys */
+    float* ak;                  /* [rows][G] fp32, or NULL */
+} qkmla_read_cache_args;
+
+/*
+ * qkmla_read_cache -- the counterpart of qkmla_append and qkmla_append_q8: rows of
+ * the cache, wherever their pages lie, as contiguous arrays (to move a prefix to
+ * another cache, cache type or device, or to keep it).
+ *
+ * Row n, out_start[b] <= n < out_start[b+1], is token first[b] + n - out_start[b] of
+ * sequence b: c = cast(c^_t) with c^_t the stored latent (8-bit cache: code x scale),
+ * r = cast(k^rope_t), ak = alpha^k_t; casts to a narrower type round to nearest even.
+ * A token outside [0, max_pages * page_size) or a page id outside [0, num_slots /
+ * page_size) sets QKMLA_ERR_DEVICE_BOUNDS and leaves its row as it was.  rows == 0 is
+ * a no-op.  Errors: INVALID for null pointers, sizes, misaligned elements, kv_scale
+ * without QKMLA_E4M3 or the reverse, an odd d_c with QKMLA_E4M3; UNSUPPORTED for other
+ * dtypes.
+ */
+int qkmla_read_cache(const qkmla_read_cache_args* a, void* stream);
+
+/*
+ * qkmla_prefill_pack_weights -- the up-projections in the layout qkmla_prefill's
+ * tensor-core product reads: once for a layer's weights.
+ * w_k [G][d_c][d_h] fp32, w_v [G_v][d_c][d_v] bf16 (as in qkmla_append and
+ * qkmla_up_project); packed: qkmla_prefill_weights_size(...) bytes, 16-byte aligned.
+ * Each matrix is stored as fp16 times a power of two of its own (its largest value in
+ * [1, 2)): W^K is off by 2^-11 of itself, W^V exact, down to 2^-14 of the matrix's
+ * largest value.
+ * qkmla_prefill_weights_size: 0 for sizes qkmla_prefill does not serve.
+ * Errors: INVALID for null pointers, sizes or misaligned bases; UNSUPPORTED for sizes
+ * that qkmla_prefill does not serve.
+ */
+size_t qkmla_prefill_weights_size(int G, int G_v, int d_c, int d_h, int d_v);
+int qkmla_prefill_pack_weights(const float* w_k, const void* w_v, int G, int G_v, int d_c, int d_h, int d_v,
+                               void* packed, void* stream);
+
+/* Arguments of qkmla_prefill. */
+typedef struct qkmla_prefill_args {
+    const void* q;              /* (row, h, j) at q + row q_row_stride + h q_head_stride + j, in q_dtype: not normalised */
+    const void* q_rope;         /* likewise, post-RoPE, not normalised */
+    int64_t q_row_stride, q_head_stride, qr_row_stride, qr_head_stride;   /* in elements, multiples of 4 */
+    const float* gamma_q;       /* [d_h] */
+    const float* gamma_k;       /* [d_h] */
+    const float* gamma_rope_q;  /* [d_r] or NULL (ones) */
+    const void* weights;        /* from qkmla_prefill_pack_weights */
+    const void* kv_cache;       /* as in qkmla_decode_args: QKMLA_BF16, or QKMLA_E4M3 with kv_scale */
+    const float* kv_scale;      /* [num_slots] fp32 with QKMLA_E4M3, else NULL */
+    const void* ak_cache;       /* [num_slots][G] fp32 (fp16 with QKMLA_FLAG_ALPHA_F16) */
+    const int32_t* chunk_start; /* [B+1] int32 device, chunk_start[0] = 0, not decreasing, the last <= rows */
+    const int32_t* seq_lens;    /* [B] int32 device: tokens in the cache incl. the chunk's */
+    const int32_t* page_table;  /* [B][max_pages] int32 device, or NULL (contiguous) */
+    int64_t num_slots;
+    int64_t total_tokens;       /* at least the sum of seq_lens: sizes the workspace */
+    int page_size, max_pages;
+    int B, rows, H, G, G_v, d_c, d_h, d_r, d_v;
+    int cache_dtype, q_dtype, o_dtype;   /* q_dtype, o_dtype: QKMLA_F32 or QKMLA_BF16 */
+    float softmax_scale, eps;
+    int window, sinks;          /* as in qkmla_decode_ext_args */
+    unsigned flags;             /* QKMLA_FLAG_ALPHA_F16 */
+    void* workspace;            /* device scratch, >= qkmla_prefill_workspace_size(args) bytes, 256-byte aligned */
+    size_t workspace_bytes;
+    void* o;                    /* [rows][H][d_v] in o_dtype: per-head values */
+    float* lse;                 /* [rows][H] fp32, or NULL */
+} qkmla_prefill_args;
+
+/*
+ * qkmla_prefill -- attention of a chunk of new tokens over the paged latent cache,
+ * the chunk's own tokens (already appended) among it: a prompt's prefill whole or in
+ * chunks, several sequences a call, single decode tokens among them.
+ * Source: as qkmla_decode; Technical Summary, Problem Statement (keys and values are
+ * up-projections of the latent).  With many query rows a token it costs less to recover
+ * each cached token's key and value once, k_{t,g} = alpha^k_{t,g} c^_t W^K_g and
+ * v_t = c^_t W^V, than to attend in latent space: 2 (d_h + d_r + d_v) flops a pair and
+ * head instead of 2 (2 d_c + d_r).  The cache, its bytes and the result are the same.
+ *
+ * Row r of sequence b, chunk_start[b] <= r < chunk_start[b+1], is query i = r - chunk_start[b]
+ * of n_b: it attends to tokens t < n = seq_lens[b] - n_b + i + 1, with a window w and sinks f
+ * to those with t < f or t >= n - w;
+ *   l = softmax_scale ( q^ . k_{t,g(h)} + q^rope . k^rope_t ),  q^ = q gamma_q gamma_k / rms(q),
+ *   q^rope = q_rope gamma_rope_q / rms(q_rope),  rms(z) = sqrt(mean z^2 + eps)
+ *   o[r][h] = sum_t softmax_t(l) v_t,  lse = ln sum_t exp(l_t)
+ * = qkmla_absorb_query, qkmla_decode_ext and qkmla_up_project over the same cache.
+ * A query without a visible token gives o = 0, lse = -inf.  Rows from chunk_start[B] on
+ * stay as they are.  Stored values that no query of a row's step sees do not reach its
+ * result, NaN included; a NaN in what a query sees, or in its own row, is NaN in its o
+ * and lse.
+ *
+ * Accuracy: fp16 operands (11 significant bits) of tensor-core products, fp32 sums:
+ * recovered keys and values, normalised queries (scaled by a power of two a row) and
+ * softmax weights are each off by 2^-11 of themselves, values of less than 2^-13 of the largest
+ * among 128 neighbouring tokens by up to 2^-25 of that largest; where 128 neighbouring
+ * tokens' latents differ by more than 2^12, or leave 2^-40 .. 2^40, their values and
+ * weights are bf16 (2^-8).  A weight below 2^-22 of the row's largest loses bits, one below 2^-32 is 0.
+ * RoPE keys are taken as fp16: up to 65504.
+ *
+ * Sizes: d_h and d_v 64 or 128, d_r 32 or 64, d_c a multiple of 64 up to 512, H / max(G, G_v)
+ * 1, 2, 4, ... or 128, the larger of G and G_v a multiple of the other, B <= 4096, any page size; rows of 16-byte
+ * aligned bases.
+ * Device-side: a seq_len outside [0, max_pages * page_size], lengths that add up to more than
+ * total_tokens, chunk starts out of order or beyond rows, or a page id outside [0, num_slots /
+ * page_size) set QKMLA_ERR_DEVICE_BOUNDS; the affected rows are then undefined.
+ * rows == 0 is a no-op.  Errors: INVALID for null pointers, sizes, strides, alignment, window or
+ * sinks as in qkmla_decode_ext, kv_scale without QKMLA_E4M3 or the reverse; UNSUPPORTED for other
+ * sizes or dtypes, or with QKMLA_FLAG_PLAIN_MLA; WORKSPACE.
+ * qkmla_prefill_workspace_size: 0 for arguments that the call rejects; reads the sizes alone.  Depends
+ * on the current device.
+ */
+int qkmla_prefill(const qkmla_prefill_args* a, void* stream);
+size_t qkmla_prefill_workspace_size(const qkmla_prefill_args* a);
 
 /* Bytes of scratch qkmla_decode_noalloc can use (its fixed array). */
 size_t qkmla_decode_noalloc_max_workspace(void);

@@ -9,7 +9,10 @@ Calls: absorb_query, append (append_q8 for the 8-bit cache), decode -- over any
 of the caches, whole or through a window with sinks -- (or make_decode_args +
 decode_raw to keep one argument block); prepare_absorb_query / prepare_append /
 prepare_append_q8 / prepare_decode return a prepared call whose arguments are
-marshalled once, for loops over fixed buffers.
+marshalled once, for loops over fixed buffers.  Around them project_query and
+up_project; for prompts prefill (attention of chunks of new tokens, with weights
+from prefill_weights), rope (rotary positions in both layouts, scaled for long
+contexts) and read_cache (cache rows as contiguous arrays), each with its prepare_.
 """
 from __future__ import annotations
 
@@ -33,8 +36,12 @@ SYMBOLS = [
     "qkmla_get_device_status", "qkmla_status_string", "qkmla_version", "qkmla_decode_kernel_name",
     "qkmla_decode_launch_count", "qkmla_up_project", "qkmla_append_rope", "qkmla_project_query",
     "qkmla_append_q8", "qkmla_decode_ext", "qkmla_decode_ext_workspace_size", "qkmla_decode_ext_kernel_name",
-    "qkmla_decode_ext_launch_count",
+    "qkmla_decode_ext_launch_count", "qkmla_rope", "qkmla_read_cache", "qkmla_prefill_weights_size",
+    "qkmla_prefill_pack_weights", "qkmla_prefill", "qkmla_prefill_workspace_size",
 ]
+
+ROPE_INTERLEAVED, ROPE_HALVES = 0, 1
+ROPE_PLAIN, ROPE_LINEAR, ROPE_YARN, ROPE_GIVEN = 0, 1, 2, 3
 
 
 class QkmlaError(RuntimeError):
@@ -85,6 +92,106 @@ class DecodeExtArgs(ctypes.Structure):
     ]
 
 
+class RopeArgs(ctypes.Structure):
+    """Mirror of `qkmla_rope_args` in include/qkmla.h (same field order)."""
+    _fields_ = [
+        ("x", ctypes.c_void_p),
+        ("out", ctypes.c_void_p),
+        ("positions", ctypes.c_void_p),
+        ("x_row_stride", ctypes.c_int64),
+        ("x_head_stride", ctypes.c_int64),
+        ("out_row_stride", ctypes.c_int64),
+        ("out_head_stride", ctypes.c_int64),
+        ("rows", ctypes.c_int),
+        ("heads", ctypes.c_int),
+        ("d_r", ctypes.c_int),
+        ("dtype", ctypes.c_int),
+        ("layout", ctypes.c_int),
+        ("inverse", ctypes.c_int),
+        ("scaling", ctypes.c_int),
+        ("theta", ctypes.c_float),
+        ("factor", ctypes.c_float),
+        ("original_context", ctypes.c_int),
+        ("beta_fast", ctypes.c_float),
+        ("beta_slow", ctypes.c_float),
+        ("attention_factor", ctypes.c_float),
+        ("frequencies", ctypes.POINTER(ctypes.c_double)),
+    ]
+
+
+class ReadCacheArgs(ctypes.Structure):
+    """Mirror of `qkmla_read_cache_args` in include/qkmla.h (same field order)."""
+    _fields_ = [
+        ("kv_cache", ctypes.c_void_p),
+        ("kv_scale", ctypes.c_void_p),
+        ("ak_cache", ctypes.c_void_p),
+        ("out_start", ctypes.c_void_p),
+        ("first", ctypes.c_void_p),
+        ("page_table", ctypes.c_void_p),
+        ("num_slots", ctypes.c_int64),
+        ("page_size", ctypes.c_int),
+        ("max_pages", ctypes.c_int),
+        ("B", ctypes.c_int),
+        ("rows", ctypes.c_int),
+        ("G", ctypes.c_int),
+        ("d_c", ctypes.c_int),
+        ("d_r", ctypes.c_int),
+        ("cache_dtype", ctypes.c_int),
+        ("out_dtype", ctypes.c_int),
+        ("flags", ctypes.c_uint),
+        ("c", ctypes.c_void_p),
+        ("r", ctypes.c_void_p),
+        ("ak", ctypes.c_void_p),
+    ]
+
+
+class PrefillArgs(ctypes.Structure):
+    """Mirror of `qkmla_prefill_args` in include/qkmla.h (same field order)."""
+    _fields_ = [
+        ("q", ctypes.c_void_p),
+        ("q_rope", ctypes.c_void_p),
+        ("q_row_stride", ctypes.c_int64),
+        ("q_head_stride", ctypes.c_int64),
+        ("qr_row_stride", ctypes.c_int64),
+        ("qr_head_stride", ctypes.c_int64),
+        ("gamma_q", ctypes.c_void_p),
+        ("gamma_k", ctypes.c_void_p),
+        ("gamma_rope_q", ctypes.c_void_p),
+        ("weights", ctypes.c_void_p),
+        ("kv_cache", ctypes.c_void_p),
+        ("kv_scale", ctypes.c_void_p),
+        ("ak_cache", ctypes.c_void_p),
+        ("chunk_start", ctypes.c_void_p),
+        ("seq_lens", ctypes.c_void_p),
+        ("page_table", ctypes.c_void_p),
+        ("num_slots", ctypes.c_int64),
+        ("total_tokens", ctypes.c_int64),
+        ("page_size", ctypes.c_int),
+        ("max_pages", ctypes.c_int),
+        ("B", ctypes.c_int),
+        ("rows", ctypes.c_int),
+        ("H", ctypes.c_int),
+        ("G", ctypes.c_int),
+        ("G_v", ctypes.c_int),
+        ("d_c", ctypes.c_int),
+        ("d_h", ctypes.c_int),
+        ("d_r", ctypes.c_int),
+        ("d_v", ctypes.c_int),
+        ("cache_dtype", ctypes.c_int),
+        ("q_dtype", ctypes.c_int),
+        ("o_dtype", ctypes.c_int),
+        ("softmax_scale", ctypes.c_float),
+        ("eps", ctypes.c_float),
+        ("window", ctypes.c_int),
+        ("sinks", ctypes.c_int),
+        ("flags", ctypes.c_uint),
+        ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t),
+        ("o", ctypes.c_void_p),
+        ("lse", ctypes.c_void_p),
+    ]
+
+
 _lib: Optional[ctypes.CDLL] = None
 
 
@@ -131,6 +238,18 @@ def lib() -> ctypes.CDLL:
         L.qkmla_decode_ext_kernel_name.restype = ctypes.c_char_p
         L.qkmla_decode_ext_launch_count.argtypes = [pa, px]
         L.qkmla_decode_ext_launch_count.restype = i
+        L.qkmla_rope.argtypes = [ctypes.POINTER(RopeArgs), vp]
+        L.qkmla_rope.restype = i
+        L.qkmla_read_cache.argtypes = [ctypes.POINTER(ReadCacheArgs), vp]
+        L.qkmla_read_cache.restype = i
+        L.qkmla_prefill_weights_size.argtypes = [i, i, i, i, i]
+        L.qkmla_prefill_weights_size.restype = sz
+        L.qkmla_prefill_pack_weights.argtypes = [vp, vp, i, i, i, i, i, vp, vp]
+        L.qkmla_prefill_pack_weights.restype = i
+        L.qkmla_prefill.argtypes = [ctypes.POINTER(PrefillArgs), vp]
+        L.qkmla_prefill.restype = i
+        L.qkmla_prefill_workspace_size.argtypes = [ctypes.POINTER(PrefillArgs)]
+        L.qkmla_prefill_workspace_size.restype = sz
         if hasattr(L, "qkmla_decode_noalloc"):
             L.qkmla_decode_noalloc.argtypes = [ctypes.POINTER(DecodeArgs), vp]
             L.qkmla_decode_noalloc.restype = i
@@ -433,10 +552,13 @@ class PreparedDecode:
     every stream's calls are done."""
 
     def __init__(self, args: DecodeArgs, ext: Optional[DecodeExtArgs], workspace, device):
-        torch = _torch()
         self.args, self.ext = args, ext
         self.name = "qkmla_decode" if ext is None else "qkmla_decode_ext"
         self.refs = (ctypes.byref(args),) if ext is None else (ctypes.byref(args), ctypes.byref(ext))
+        self._allocate(args, workspace, device)
+
+    def _allocate(self, args, workspace, device) -> None:
+        torch = _torch()
         need = int(getattr(lib(), self.name + "_workspace_size")(*self.refs))
         if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
             workspace = torch.empty(need, dtype=torch.uint8, device=device)
@@ -525,3 +647,253 @@ def up_project(o, w_v, out, stream=None):
 
 def get_device_status(stream=None) -> int:
     return int(lib().qkmla_get_device_status(_stream(stream)))
+
+
+# ----------------------------------------------------------------------------
+# prompts: rotary positions, reading the cache back, prefill
+# ----------------------------------------------------------------------------
+class RopeScaling:
+    """How qkmla_rope forms its frequencies (see linear_scaling, yarn_scaling and given_frequencies)."""
+
+    def __init__(self, kind: int, **fields):
+        self.kind, self.fields = kind, fields
+
+
+def linear_scaling(factor: float) -> RopeScaling:
+    """Every frequency divided by `factor`."""
+    return RopeScaling(ROPE_LINEAR, factor=float(factor))
+
+
+def yarn_scaling(factor: float, original_context: int, beta_fast: float = 32.0, beta_slow: float = 1.0) -> RopeScaling:
+    """Pairs of more than beta_fast turns within the original context keep their frequency, of less than
+    beta_slow are divided by `factor`, a ramp between."""
+    return RopeScaling(ROPE_YARN, factor=float(factor), original_context=int(original_context),
+                       beta_fast=float(beta_fast), beta_slow=float(beta_slow))
+
+
+def given_frequencies(radians) -> RopeScaling:
+    """One frequency a pair, in radians a position (a sequence of d_r / 2 numbers)."""
+    radians = [float(f) for f in radians]
+    return RopeScaling(ROPE_GIVEN, frequencies=(ctypes.c_double * len(radians))(*radians))
+
+
+def _inner(name: str, t) -> int:
+    """Address of a tensor whose last dimension is contiguous (its others may have any stride)."""
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"qkmla: {name} must be contiguous in its last dimension")
+    if not t.is_cuda:
+        raise ValueError("qkmla: tensors must live on a CUDA device")
+    return t.data_ptr()
+
+
+class PreparedStruct:
+    """One call that takes an argument block, marshalled once; see Prepared."""
+
+    def __init__(self, name: str, args, keep=None):
+        self.name, self.args, self.keep = name, args, keep
+        self.fn = getattr(lib(), name)
+        self.ref = ctypes.byref(args)
+
+    def __call__(self, stream=None) -> None:
+        _check(self.name, self.fn(self.ref, _stream(stream)))
+
+
+def prepare_rope(x, positions, out, theta: float = 10000.0, layout: str = "interleaved",
+                 scaling: Optional[RopeScaling] = None, inverse: bool = False,
+                 attention_factor: float = 1.0) -> PreparedStruct:
+    """qkmla_rope for fixed tensors (see rope)."""
+    torch = _torch()
+    if x.dim() not in (2, 3) or out.shape != x.shape or out.dtype != x.dtype:
+        raise ValueError(f"qkmla: x and out are [rows, heads, d_r] or [rows, d_r] of one type, not {x.dtype} "
+                         f"{tuple(x.shape)} and {out.dtype} {tuple(out.shape)}")
+    if layout not in ("interleaved", "half"):
+        raise ValueError(f"qkmla: layout is interleaved or half, not {layout}")
+    rows, d_r = x.shape[0], x.shape[-1]
+    _expect("positions", positions, torch.int32, rows)
+    a = RopeArgs()
+    a.x, a.out, a.positions = _inner("x", x), _inner("out", out), _ptr(positions)
+    a.x_row_stride, a.out_row_stride = x.stride(0), out.stride(0)
+    a.heads = 1
+    if x.dim() == 3:
+        a.heads, a.x_head_stride, a.out_head_stride = x.shape[1], x.stride(1), out.stride(1)
+    a.rows, a.d_r, a.dtype = rows, d_r, _dtype_code(x.dtype)
+    a.layout = ROPE_HALVES if layout == "half" else ROPE_INTERLEAVED
+    a.inverse = 1 if inverse else 0
+    a.theta, a.attention_factor = float(theta), float(attention_factor)
+    if not a.attention_factor > 0:
+        raise ValueError("qkmla: attention_factor is positive")
+    if scaling is not None:
+        a.scaling = scaling.kind
+        for k, v in scaling.fields.items():
+            if k == "frequencies":
+                if len(v) != d_r // 2:
+                    raise ValueError(f"qkmla: {d_r // 2} frequencies for {d_r} elements, not {len(v)}")
+                v = ctypes.cast(v, ctypes.POINTER(ctypes.c_double))
+            setattr(a, k, v)
+    return PreparedStruct("qkmla_rope", a, scaling)
+
+
+def rope(x, positions, out=None, theta: float = 10000.0, layout: str = "interleaved",
+         scaling: Optional[RopeScaling] = None, inverse: bool = False, attention_factor: float = 1.0, stream=None):
+    """x [rows, heads, d_r] or [rows, d_r] (a view into heads of more elements will do) with every head's pairs
+    turned by positions [rows] (int32) times their frequencies, into out (None: in place).  layout
+    "interleaved": pairs (2i, 2i + 1); "half": (i, i + d_r / 2).  inverse: turned back."""
+    out = x if out is None else out
+    prepare_rope(x, positions, out, theta, layout, scaling, inverse, attention_factor)(stream)
+    return out
+
+
+def prepare_read_cache(kv_cache, ak_cache, out_start, page_table, page_size: int, max_pages: int, c, r, ak=None,
+                       kv_scale=None, first=None) -> PreparedStruct:
+    """qkmla_read_cache for fixed tensors (see read_cache)."""
+    torch = _torch()
+    f32 = torch.float32
+    rows, d_c = c.shape
+    d_r = r.shape[1] if r is not None else 0
+    q8 = kv_cache.dtype == torch.uint8
+    if q8:
+        _check_q8_cache(kv_cache, kv_scale, d_c, d_r)
+    else:
+        _expect("kv_cache", kv_cache, (f32, torch.bfloat16), kv_cache.shape[0], d_c + d_r)
+        if kv_scale is not None:
+            raise ValueError("qkmla: kv_scale belongs to the 8-bit cache")
+    _expect("c", c, (f32, torch.bfloat16), rows, d_c)
+    if r is not None:
+        _expect("r", r, c.dtype, rows, d_r)
+    B = out_start.numel() - 1
+    _expect("out_start", out_start, torch.int32, B + 1)
+    a = ReadCacheArgs()
+    if ak is not None:
+        G = ak.shape[1]
+        _expect("ak", ak, f32, rows, G)
+        _expect("ak_cache", ak_cache, (f32, torch.float16), kv_cache.shape[0], G)
+        a.ak_cache, a.ak, a.G, a.flags = _ptr(ak_cache), _ptr(ak), G, _alpha_flag(ak_cache)
+    if first is not None:
+        _expect("first", first, torch.int32, B)
+    if page_table is not None:
+        _expect("page_table", page_table, torch.int32, B, max_pages)
+    a.kv_cache, a.kv_scale, a.out_start, a.first = _ptr(kv_cache), _ptr(kv_scale), _ptr(out_start), _ptr(first)
+    a.page_table, a.num_slots = _ptr(page_table), kv_cache.shape[0]
+    a.page_size, a.max_pages, a.B, a.rows, a.d_c, a.d_r = int(page_size), int(max_pages), B, rows, d_c, d_r
+    a.cache_dtype = E4M3 if q8 else _dtype_code(kv_cache.dtype)
+    a.out_dtype = _dtype_code(c.dtype)
+    a.c, a.r = _ptr(c), _ptr(r)
+    return PreparedStruct("qkmla_read_cache", a)
+
+
+def read_cache(kv_cache, ak_cache, out_start, page_table, page_size: int, max_pages: int, c, r, ak=None,
+               kv_scale=None, first=None, stream=None):
+    """Rows of the cache (kv_scale: of the 8-bit one) as contiguous arrays c [rows, d_c], r [rows, d_r] (fp32 or
+    bf16) and, where given, ak [rows, G] fp32: row n of sequence b, out_start[b] <= n < out_start[b + 1] (int32
+    [B + 1]), is its token first[b] (0 without `first`) + n - out_start[b]."""
+    prepare_read_cache(kv_cache, ak_cache, out_start, page_table, page_size, max_pages, c, r, ak, kv_scale, first)(stream)
+    return c, r, ak
+
+
+class PrefillWeights:
+    """W^K and W^V in prefill's layout (see prefill_weights)."""
+
+    def __init__(self, packed, G: int, G_v: int, d_c: int, d_h: int, d_v: int):
+        self.packed, self.G, self.G_v, self.d_c, self.d_h, self.d_v = packed, G, G_v, d_c, d_h, d_v
+
+
+def prefill_weights(w_k, w_v, stream=None) -> PrefillWeights:
+    """w_k [G, d_c, d_h] fp32 and w_v [G_v, d_c, d_v] bf16 laid out for prefill, once for a layer's weights."""
+    torch = _torch()
+    G, d_c, d_h = w_k.shape
+    G_v, _, d_v = w_v.shape
+    _expect("w_k", w_k, torch.float32, G, d_c, d_h)
+    _expect("w_v", w_v, torch.bfloat16, G_v, d_c, d_v)
+    need = int(lib().qkmla_prefill_weights_size(G, G_v, d_c, d_h, d_v))
+    if need == 0:
+        raise QkmlaError("qkmla_prefill_weights_size", ERR_UNSUPPORTED)
+    with _launching(stream):
+        packed = torch.empty(need, dtype=torch.uint8, device=w_k.device)
+    _check("qkmla_prefill_pack_weights",
+           lib().qkmla_prefill_pack_weights(_ptr(w_k), _ptr(w_v), G, G_v, d_c, d_h, d_v, _ptr(packed), _stream(stream)))
+    return PrefillWeights(packed, G, G_v, d_c, d_h, d_v)
+
+
+class PreparedPrefill(PreparedDecode):
+    """One qkmla_prefill call with its arguments marshalled and its workspace allocated once; the workspace
+    as in PreparedDecode."""
+
+    def __init__(self, args: PrefillArgs, weights: PrefillWeights, workspace, device):
+        self.args, self.weights = args, weights
+        self.name = "qkmla_prefill"
+        self.refs = (ctypes.byref(args),)
+        self._allocate(args, workspace, device)
+
+    @property
+    def kernel_name(self) -> str:
+        return "tcgen05"
+
+    @property
+    def launch_count(self) -> int:
+        return 0 if self.args.rows == 0 else 4
+
+
+def prepare_prefill(q, q_rope, gamma_q, gamma_k, gamma_rope_q, weights: PrefillWeights, kv_cache, ak_cache, chunk_start,
+                    seq_lens, page_table, page_size: int, max_pages: int, total_tokens: int, softmax_scale: float,
+                    eps: float, o, lse=None, kv_scale=None, window: int = 0, sinks: int = 0,
+                    workspace=None) -> PreparedPrefill:
+    """prefill() for fixed tensors (see prefill)."""
+    torch = _torch()
+    f32, bf16 = torch.float32, torch.bfloat16
+    w = weights
+    rows, H, d_h = q.shape
+    d_r = q_rope.shape[-1]
+    B = seq_lens.numel()
+    _expect("q", q, (f32, bf16), rows, H, w.d_h)
+    _expect("q_rope", q_rope, q.dtype, rows, H, d_r)
+    _expect("gamma_q", gamma_q, f32, d_h)
+    _expect("gamma_k", gamma_k, f32, d_h)
+    if gamma_rope_q is not None:
+        _expect("gamma_rope_q", gamma_rope_q, f32, d_r)
+    if kv_cache.dtype == torch.uint8:
+        _check_q8_cache(kv_cache, kv_scale, w.d_c, d_r)
+    else:
+        _expect("kv_cache", kv_cache, bf16, kv_cache.shape[0], w.d_c + d_r)
+        if kv_scale is not None:
+            raise ValueError("qkmla: kv_scale belongs to the 8-bit cache")
+    _expect("ak_cache", ak_cache, (f32, torch.float16), kv_cache.shape[0], w.G)
+    _expect("chunk_start", chunk_start, torch.int32, B + 1)
+    _expect("seq_lens", seq_lens, torch.int32, B)
+    if page_table is not None:
+        _expect("page_table", page_table, torch.int32, B, max_pages)
+    _expect("o", o, (f32, bf16), rows, H, w.d_v)
+    if lse is not None:
+        _expect("lse", lse, f32, rows, H)
+    a = PrefillArgs()
+    a.q, a.q_rope = _inner("q", q), _inner("q_rope", q_rope)
+    a.q_row_stride, a.q_head_stride = q.stride(0), q.stride(1)
+    a.qr_row_stride, a.qr_head_stride = q_rope.stride(0), q_rope.stride(1)
+    a.gamma_q, a.gamma_k, a.gamma_rope_q = _ptr(gamma_q), _ptr(gamma_k), _ptr(gamma_rope_q)
+    a.weights = _ptr(w.packed)
+    a.kv_cache, a.kv_scale, a.ak_cache = _ptr(kv_cache), _ptr(kv_scale), _ptr(ak_cache)
+    a.chunk_start, a.seq_lens, a.page_table = _ptr(chunk_start), _ptr(seq_lens), _ptr(page_table)
+    a.num_slots, a.total_tokens = kv_cache.shape[0], int(total_tokens)
+    a.page_size, a.max_pages, a.B, a.rows, a.H = int(page_size), int(max_pages), B, rows, H
+    a.G, a.G_v, a.d_c, a.d_h, a.d_r, a.d_v = w.G, w.G_v, w.d_c, w.d_h, d_r, w.d_v
+    a.cache_dtype = E4M3 if kv_cache.dtype == torch.uint8 else BF16
+    a.q_dtype, a.o_dtype = _dtype_code(q.dtype), _dtype_code(o.dtype)
+    a.softmax_scale, a.eps = float(softmax_scale), float(eps)
+    a.window, a.sinks = _c_int(window), _c_int(sinks)
+    a.flags = _alpha_flag(ak_cache)
+    a.o, a.lse = _ptr(o), _ptr(lse)
+    return PreparedPrefill(a, w, workspace, kv_cache.device)
+
+
+def prefill(q, q_rope, gamma_q, gamma_k, gamma_rope_q, weights: PrefillWeights, kv_cache, ak_cache, chunk_start, seq_lens,
+            page_table, page_size: int, max_pages: int, total_tokens: int, softmax_scale: float, eps: float, o, lse=None,
+            kv_scale=None, window: int = 0, sinks: int = 0, workspace=None, stream=None):
+    """Attention of chunks of new tokens, already appended, over the paged latent cache: o [rows, H, d_v] (bf16 or
+    fp32), lse [rows, H].  q [rows, H, d_h], q_rope [rows, H, d_r] (fp32 or bf16; views into wider heads will do), the
+    rows of sequence b chunk_start[b] .. chunk_start[b + 1] - 1 (int32 [B + 1]).  total_tokens: at least the sum of
+    seq_lens, known on the host (it sizes the workspace).  kv_scale, window and sinks as in decode()."""
+    with _launching(stream):
+        call = prepare_prefill(q, q_rope, gamma_q, gamma_k, gamma_rope_q, weights, kv_cache, ak_cache, chunk_start, seq_lens,
+                               page_table, page_size, max_pages, total_tokens, softmax_scale, eps, o, lse, kv_scale, window,
+                               sinks, workspace)
+    call(stream)
+    return o, lse

@@ -1,0 +1,133 @@
+// What the kernels of qkmla_prefill share: sizes, the workspace and the plan of the attention's work.
+//
+// A call runs four kernels.  prefill_query_kernel normalises the queries into tiles (its first block makes
+// the plan), prefill_expand_kernel recovers keys and values of the cached tokens, prefill_attend_kernel
+// attends, prefill_join_kernel joins the rows whose tokens were cut between two CTAs.
+//
+// Everything a tensor-core product reads is written by the first two kernels in 16 KB blocks of 128 rows x
+// 64 fp16 values, as it lies in shared memory (rows of 128 bytes, 128-byte swizzle), so that one
+// contiguous bulk copy brings it in and no tensor map is made.
+#pragma once
+
+#include "common.cuh"
+#include "decode_common.cuh"
+#include "tc_ptx.cuh"
+
+namespace qkmla {
+namespace pf {
+
+constexpr int kTile = 128;                 // tokens of a tile
+constexpr int kRowsQ = 256;                // query rows (tokens x heads of a unit) of a tile: two halves of 128
+constexpr int kBlock = 16384;              // bytes of a block of 128 x 64 values
+constexpr int kMaxE = 40;                  // largest exponent of a tile's values
+constexpr int kCostStart = 2;              // cost of starting on a query tile, in tiles of tokens
+constexpr int kMinPiece = 2;               // no piece of a cut query tile has fewer tiles of tokens
+constexpr int kMinShare = 5;               // nor a CTA fewer units of cost
+
+struct Params {
+    // the caller's
+    const void *q, *q_rope;
+    int64_t q_row, q_head, qr_row, qr_head;
+    const float *gamma_q, *gamma_k, *gamma_rope;
+    const uint8_t* weights;
+    const uint8_t* kv;
+    const float* kv_scale;
+    const void* ak;
+    const int32_t *chunk_start, *seq_lens, *page_table;
+    int64_t num_pages;
+    int page_size, max_pages;
+    int B, rows, H, G, Gv, d_c, d_h, d_r, d_v;
+    float scale_log2, eps;
+    int window, sinks;
+    int ak_f16;
+    int64_t total_tokens;
+    void* o;
+    float* lse;
+    // derived
+    int units;                             // heads with a key and a value matrix in common: max(G, G_v) units
+    int hp;                                // heads of a unit
+    int tq;                                // query tokens of a tile: 256 / hp
+    int nq;                                // slots of query tiles: rows / tq + B
+    int max_tiles;                         // total_tokens / 128 + B
+    int ctas;                              // of the attention kernel
+    // the workspace
+    int4* seq;                             // [B]: length, first tile, first row, rows
+    int4* qinfo;                           // [nq][2]: {b, first query, tiles, head tiles}, {gap, length of the first query, queries, -}
+    int64_t* pre;                          // [nq + 1]: cost of the slots ahead
+    int* tinfo;                            // [max_tiles]: exponent + 64, | 256 where the values are bf16
+    uint8_t *krope, *kc, *v, *qt;          // blocks: [tile], [tile][G][d_h / 64], [tile][G_v][d_v / 64], [unit][slot][half][d_h / 64 + 1]
+    float* qc;                             // [unit][slot][256]: factor of a row's logits
+    float* part_o;                         // [2 ctas][256][d_v]
+    float2* part_ml;                       // [2 ctas][256]: reference and sum
+    int* status;
+};
+
+// The packed weights: fp16 blocks of 128 output columns x 64 latents [N-tile][d_c / 64], after a table of
+// the power of two of each matrix.
+__host__ __device__ inline int column_blocks(int G, int Gv, int d_h, int d_v) { return G * (d_h / 64) + Gv * (d_v / 64); }
+__host__ __device__ inline int n_tiles(int G, int Gv, int d_h, int d_v) { return (column_blocks(G, Gv, d_h, d_v) + 1) / 2; }
+constexpr size_t kWeightTable = 4096;      // int32 exponents of up to 1024 matrices
+
+// First slot of a sequence's query tiles: its rows start at chunk_start[b], and rounding up for each of the
+// b sequences ahead takes at most b slots, so ranges never meet and need no sum over the sequences.
+__device__ __forceinline__ int first_slot(int row, int b, int tq) { return row / tq + b; }
+
+// A place in the list of all work (unit-major, then slots): tile `t` of slot `j` of unit `u`.
+struct Place {
+    int u, j, t, nt;
+    __device__ __forceinline__ bool same(const Place& o) const { return u == o.u && j == o.j && t == o.t; }
+    __device__ __forceinline__ bool inside() const { return t > 0 && t < nt; }
+};
+
+// The place of cost x: whole warp.  A cut that would leave a piece of fewer than kMinPiece tiles moves to
+// the query tile's start or end.
+__device__ __forceinline__ Place place_of(const Params& p, int64_t x, int64_t one) {
+    Place r;
+    const int lane = threadIdx.x & 31;
+    r.u = (int)(x / one);
+    if (r.u >= p.units) { r.u = p.units; r.j = 0; r.t = 0; r.nt = 0; return r; }
+    const int64_t y = x - (int64_t)r.u * one;
+    int lo = 0, n = p.nq;                                  // the last j in [lo, lo + n) with pre[j] <= y
+    while (n > 1) {
+        const int step = (n + 31) / 32;
+        const int at = lo + lane * step;
+        const bool le = lane * step < n && p.pre[at] <= y;
+        const unsigned m = __ballot_sync(0xffffffffu, le);
+        const int k = 31 - __clz(m | 1u);
+        n = min(step, n - k * step);
+        lo += k * step;
+    }
+    r.j = lo;
+    const int64_t at = p.pre[lo];
+    r.nt = (int)(p.pre[lo + 1] - at) - kCostStart;
+    int t = (int)(y - at) - kCostStart;
+    if (t < kMinPiece) t = 0;
+    else if (r.nt - t < kMinPiece) t = r.nt;
+    r.t = t;
+    return r;
+}
+
+// CTAs that share the work: no more than leave each kMinShare.
+__device__ __forceinline__ int sharing(const Params& p, int64_t all) {
+    const int64_t n = all / kMinShare;
+    return n < 1 ? 1 : n < p.ctas ? (int)n : p.ctas;
+}
+__device__ __forceinline__ int64_t share_start(int64_t all, int n, int c) { return all / n * c + all % n * c / n; }
+
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+// 2^e as an exact float, e in [-126, 127]
+__device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
+
+int launch_query(const Params& p, bool q_bf16, cudaStream_t s);
+int launch_expand(const Params& p, bool q8, cudaStream_t s);
+int launch_attend(const Params& p, int o_dtype, cudaStream_t s);
+
+}  // namespace pf
+}  // namespace qkmla
