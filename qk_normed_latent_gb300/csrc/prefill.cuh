@@ -1,12 +1,12 @@
 // What the kernels of qkmla_prefill share: sizes, the workspace and the plan of the attention's work.
 //
-// A call runs four kernels.  prefill_query_kernel normalises the queries into tiles (its first block makes
-// the plan), prefill_expand_kernel recovers keys and values of the cached tokens, prefill_attend_kernel
-// attends, prefill_join_kernel joins the rows whose tokens were cut between two CTAs.
+// A call runs three kernels.  prefill_expand_kernel recovers keys and values of the cached tokens (its last block
+// makes the plan), prefill_attend_kernel normalises the queries and attends, prefill_join_kernel joins the rows
+// whose tokens were cut between two CTAs.
 //
-// Everything a tensor-core product reads is written by the first two kernels in 16 KB blocks of 128 rows x
-// 64 fp16 values, as it lies in shared memory (rows of 128 bytes, 128-byte swizzle), so that one
-// contiguous bulk copy brings it in and no tensor map is made.
+// Everything a tensor-core product reads is written in 16 KB blocks of 128 rows x 64 fp16 values, as it lies in
+// shared memory (rows of 128 bytes, 128-byte swizzle), so that one contiguous bulk copy brings it in and no tensor
+// map is made.
 #pragma once
 
 #include "common.cuh"
@@ -39,13 +39,13 @@ struct Params {
     int B, rows, H, G, Gv, d_c, d_h, d_r, d_v;
     float scale_log2, eps;
     int window, sinks;
-    int ak_f16;
+    int ak_f16, q_bf16, o_f32;
     int64_t total_tokens;
     void* o;
     float* lse;
     // derived
     int units;                             // heads with a key and a value matrix in common: max(G, G_v) units
-    int hp;                                // heads of a unit
+    int hp, hp_log;                        // heads of a unit, a power of two
     int tq;                                // query tokens of a tile: 256 / hp
     int nq;                                // slots of query tiles: rows / tq + B
     int max_tiles;                         // total_tokens / 128 + B
@@ -55,8 +55,9 @@ struct Params {
     int4* qinfo;                           // [nq][2]: {b, first query, tiles, head tiles}, {gap, length of the first query, queries, -}
     int64_t* pre;                          // [nq + 1]: cost of the slots ahead
     int* tinfo;                            // [max_tiles]: exponent + 64, | 256 where the values are bf16
-    uint8_t *krope, *kc, *v, *qt;          // blocks: [tile], [tile][G][d_h / 64], [tile][G_v][d_v / 64], [unit][slot][half][d_h / 64 + 1]
-    float* qc;                             // [unit][slot][256]: factor of a row's logits
+    uint8_t *krope, *kc, *v;               // blocks: [tile], [tile][G][d_h / 64], [tile][G_v][d_v / 64]
+    uint8_t* qs;                           // [cta][2][half][d_h / 64 + 1]: the normalised queries of a CTA's next two pieces
+    float* qcs;                            // [cta][2][256]: factor of a row's logits
     float* part_o;                         // [2 ctas][256][d_v]
     float2* part_ml;                       // [2 ctas][256]: reference and sum
     int* status;
@@ -125,9 +126,8 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 // 2^e as an exact float, e in [-126, 127]
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
 
-int launch_query(const Params& p, bool q_bf16, cudaStream_t s);
 int launch_expand(const Params& p, bool q8, cudaStream_t s);
-int launch_attend(const Params& p, int o_dtype, cudaStream_t s);
+int launch_attend(const Params& p, cudaStream_t s);
 
 }  // namespace pf
 }  // namespace qkmla

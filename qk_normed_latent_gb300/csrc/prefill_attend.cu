@@ -36,54 +36,69 @@ using namespace tc;
 
 constexpr int kThreadsA = 384;
 // Registers: 384 threads start with 168 each, the most that 65536 allow.  The softmax keeps a row of 128 logits,
-// so the warpgroup of the loads and products gives up 96 of its 168 and each half's takes 48 of them:
-// 2 x 216 + 72 = 3 x 168.
-constexpr int kRegsSoftmax = 216, kRegsOther = 72;
+// so the warpgroup of the other warps gives up 80 of its 168 and each half's takes 40 of them:
+// 2 x 208 + 88 = 3 x 168.
+constexpr int kRegsSoftmax = 208, kRegsOther = 88;
 static_assert(2 * kRegsSoftmax + kRegsOther <= 3 * 168, "register split");
 constexpr int kUnits = 8;                  // ring, in blocks
 constexpr int kGroups = 8;                 // barriers of groups (a token tile's key blocks, or its value blocks)
 
+// A piece of work: tiles [t0, t1) of a query tile.
+struct Piece {
+    int unit;                              // -1: the end
+    int t0, t1, nt;                        // nt: tiles of the whole query tile
+    int head, gap;                         // tile t is token tile t below head, t + gap from there
+    int tile0;                             // first token tile of the sequence in the workspace
+    int n_lo;                              // causal length of the first query
+    int queries;
+    int row0;                              // first row in q and o
+};
+
 struct __align__(8) Shared {
     uint64_t full[kGroups], empty[kGroups];
-    uint64_t q_full, q_empty;
-    uint64_t s_full[2], p_full[2], o_full[2];
+    uint64_t q_full[2], q_empty[2], q0_full[2];
+    uint64_t s_full[2], pa_full[2], pb_full[2], o_full[2];
+    uint64_t piece_full[2], piece_empty[2], conv_full[2];
     uint64_t done;
+    Piece piece[2];
     uint32_t tmem;
     int fail;
     int issued;                            // groups whose copies were issued
-    int q_issued;                          // query tiles whose copies were issued
+    int q_issued[2];                       // query halves whose copies were issued
 };
+static_assert(sizeof(Shared) <= 1024, "beside the blocks");
 
 template <int DH>
 constexpr int smem_bytes() { return (2 * (DH / 64 + 1) + kUnits) * kBlock + 1024 + 1024; }
 
-// One CTA's part of the list, walked alike by every warp.
+// One CTA's part of the list.
 struct Walk {
     Place at, end;
-    int64_t one;
     bool first;
 
-    // The next piece: tiles [t0, t1) of slot j of unit u, of nt; false at the end.
-    struct Piece {
-        int u, j, t0, t1, nt;
-        int4 a, b;                         // qinfo
-    };
+    // The next piece; false at the end.
     __device__ __forceinline__ bool next(const Params& p, Piece& s) {
         for (;;) {
             if (at.u > end.u || (at.u == end.u && at.j > end.j) || at.u >= p.units) return false;
             const bool last = at.u == end.u && at.j == end.j;
             if (last && end.t == 0) return false;
-            s.u = at.u;
-            s.j = at.j;
+            const int j = at.j;
+            s.unit = at.u;
             s.t0 = first ? at.t : 0;
             first = false;
             if (++at.j == p.nq) { at.j = 0; ++at.u; }
-            s.a = p.qinfo[2 * s.j];
-            if (s.a.x < 0) continue;                       // an unused slot
-            s.b = p.qinfo[2 * s.j + 1];
-            s.nt = s.a.z;
+            const int4 a = p.qinfo[2 * j], b = p.qinfo[2 * j + 1];
+            if (a.x < 0) continue;                         // an unused slot
+            s.nt = a.z;
             s.t1 = last ? end.t : s.nt;
             if (s.t0 == s.t1 && s.nt > 0) continue;
+            s.head = a.w;
+            s.gap = b.x;
+            s.n_lo = b.y;
+            s.queries = b.z;
+            const int4 seq = p.seq[a.x];
+            s.tile0 = seq.y;
+            s.row0 = seq.z + a.y;
             return true;
         }
     }
@@ -92,6 +107,11 @@ struct Walk {
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float y;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
     return y;
 }
 
@@ -112,7 +132,123 @@ __device__ __forceinline__ bool wait_or_fail(uint64_t* bar, uint32_t parity, Sha
     }
 }
 
-template <int DH, int DV, typename OT>
+// ---- queries ----
+// Four rows of a query tile, rt .. rt + 3, eight lanes a row: normalised, with the gains, times a power of two that
+// brings the row's largest value into [1, 2), as fp16 to row rt & 127 of the half at `dst` (blocks of 64 columns).
+// Returns the row's factor: softmax_scale, log2 e and that power.  A lane's values are 4 of every 32 neighbours.
+template <int N>
+struct QueryRow {
+    float v[N][4];
+    __device__ __forceinline__ void load(const void* x, int64_t at, bool bf16, int sub) {
+        if (!bf16) {
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const float4 f = *reinterpret_cast<const float4*>((const float*)x + at + (j * 8 + sub) * 4);
+                v[j][0] = f.x; v[j][1] = f.y; v[j][2] = f.z; v[j][3] = f.w;
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const uint2 u = *reinterpret_cast<const uint2*>((const uint16_t*)x + at + (j * 8 + sub) * 4);
+                v[j][0] = __uint_as_float(u.x << 16); v[j][1] = __uint_as_float(u.x & 0xffff0000u);
+                v[j][2] = __uint_as_float(u.y << 16); v[j][3] = __uint_as_float(u.y & 0xffff0000u);
+            }
+        }
+    }
+    __device__ __forceinline__ float squares() const {
+        float s = 0.f;
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s = fmaf(v[j][i], v[j][i], s);
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        return s;
+    }
+    __device__ __forceinline__ float scale(float a, const float* g1, const float* g2, int sub) {
+        float top = 0.f;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            float g[4] = {1.f, 1.f, 1.f, 1.f};
+            if (g1) {
+                const float4 f = __ldg(reinterpret_cast<const float4*>(g1) + j * 8 + sub);
+                g[0] = f.x; g[1] = f.y; g[2] = f.z; g[3] = f.w;
+            }
+            if (g2) {
+                const float4 f = __ldg(reinterpret_cast<const float4*>(g2) + j * 8 + sub);
+                g[0] *= f.x; g[1] *= f.y; g[2] *= f.z; g[3] *= f.w;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[j][i] *= a * g[i];
+                top = fmaxf(top, fabsf(v[j][i]));
+            }
+        }
+        return top;
+    }
+    __device__ __forceinline__ void store(uint8_t* dst, int row, float f, int sub) const {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const int col = (j * 8 + sub) * 4;
+            *reinterpret_cast<uint2*>(dst + (col >> 6) * kBlock + sw128_offset(row, col & 63)) =
+                make_uint2(pack_f16(v[j][0] * f, v[j][1] * f), pack_f16(v[j][2] * f, v[j][3] * f));
+        }
+    }
+};
+
+template <int DH, int DR>
+__device__ __forceinline__ float query_rows(const Params& p, const Piece& s, int rt, uint8_t* dst, int lane) {
+    const int sub = lane & 7;
+    rt += lane >> 3;
+    const int i = rt >> p.hp_log;
+    const bool there = i < s.queries;
+    const int64_t row = s.row0 + (there ? i : 0), head = (int64_t)s.unit * p.hp + (rt & (p.hp - 1));
+    QueryRow<DH / 32> x;
+    QueryRow<DR / 32> y;
+    x.load(p.q, row * p.q_row + head * p.q_head, p.q_bf16, sub);
+    y.load(p.q_rope, row * p.qr_row + head * p.qr_head, p.q_bf16, sub);
+    const float ax = rsqrtf(x.squares() / DH + p.eps), ay = rsqrtf(y.squares() / DR + p.eps);
+    float top = fmaxf(x.scale(ax, p.gamma_q, p.gamma_k, sub), y.scale(ay, p.gamma_rope, nullptr, sub));
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    // the exponent of a normal number; 0 for zero, infinity and NaN
+    const int bits = __float_as_int(top) >> 23;
+    const int e = bits > 0 && bits < 255 ? min(max(bits - 127, -100), 100) : 0;
+    const float f = pow2i(-e);
+    x.store(dst, rt & 127, f, sub);
+    y.store(dst + DH / 64 * kBlock, rt & 127, f, sub);
+    return p.scale_log2 * pow2i(e);
+}
+
+// ---- softmax of a tile's row: weights in place of logits ----
+// Two 64-token halves, each signalled as soon as it lies in TMEM.  Returns the sum of the unrounded weights.
+template <bool BF>
+__device__ __forceinline__ float weights_out(float (&x)[128], float c, float off, uint32_t t_s, uint64_t* first, uint64_t* second, int lane) {
+    const uint64_t c2 = dec::f2(c, c), off2 = dec::f2(off, off);
+    uint64_t sum[2] = {0, 0};
+#pragma unroll
+    for (int k = 0; k < 128; k += 32) {
+        uint32_t w[16];
+#pragma unroll
+        for (int q = 0; q < 16; ++q) {
+            const float2 a = dec::f2_unpack(dec::f2_fma(dec::f2(x[k + 2 * q], x[k + 2 * q + 1]), c2, off2));
+            const float u = ex2(a.x), v = ex2(a.y);
+            sum[q & 1] = dec::f2_add(sum[q & 1], dec::f2(u, v));
+            w[q] = BF ? pack_bf16(u, v) : pack_f16(u, v);
+        }
+        tmem_st16(t_s + k / 2, w);
+        if (k == 32 || k == 96) {
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(k == 32 ? first : second);
+        }
+    }
+    const float2 s = dec::f2_unpack(dec::f2_add(sum[0], sum[1]));
+    return s.x + s.y;
+}
+
+template <int DH, int DR, int DV>
 __global__ void __launch_bounds__(kThreadsA, 1) prefill_attend_kernel(const __grid_constant__ Params p) {
     constexpr int KU = DH / 64 + 1;                        // blocks of a key tile
     constexpr int VU = DV / 64;
@@ -123,16 +259,26 @@ __global__ void __launch_bounds__(kThreadsA, 1) prefill_attend_kernel(const __gr
     uint8_t* ring = sm + 2 * kHalf;
     Shared* sh = reinterpret_cast<Shared*>(ring + kUnits * kBlock);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int cta = blockIdx.x;
 
     if (tid == 0) {
         for (int i = 0; i < kGroups; ++i) { mbar_init(&sh->full[i], 1); mbar_init(&sh->empty[i], 1); }
-        mbar_init(&sh->q_full, 1);
-        mbar_init(&sh->q_empty, 1);
-        for (int i = 0; i < 2; ++i) { mbar_init(&sh->s_full[i], 1); mbar_init(&sh->p_full[i], 128); mbar_init(&sh->o_full[i], 1); }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh->q_full[i], 1);
+            mbar_init(&sh->q_empty[i], 1);
+            mbar_init(&sh->q0_full[i], 4);
+            mbar_init(&sh->s_full[i], 1);
+            mbar_init(&sh->pa_full[i], 4);
+            mbar_init(&sh->pb_full[i], 4);
+            mbar_init(&sh->o_full[i], 1);
+            mbar_init(&sh->piece_full[i], 1);
+            mbar_init(&sh->piece_empty[i], 10);            // loads, products, eight softmax warps
+            mbar_init(&sh->conv_full[i], 2);
+            sh->q_issued[i] = 0;
+        }
         mbar_init(&sh->done, 1);
         sh->fail = 0;
         sh->issued = 0;
-        sh->q_issued = 0;
         fence_barrier_init();
     }
     if (warp == 9) {
@@ -145,18 +291,9 @@ __global__ void __launch_bounds__(kThreadsA, 1) prefill_attend_kernel(const __gr
     const uint32_t tmem = sh->tmem;
     pdl_wait();
     pdl_trigger();
-
-    Walk walk;
-    walk.one = p.pre[p.nq];
-    const int64_t all = walk.one * p.units;
+    const int64_t one = p.pre[p.nq], all = one * p.units;
     const int n_cta = sharing(p, all);
-    const int cta = blockIdx.x;
     const bool busy = all > 0 && cta < n_cta;              // uniform
-    if (busy) {
-        walk.at = place_of(p, share_start(all, n_cta, cta), walk.one);
-        walk.end = place_of(p, share_start(all, n_cta, cta + 1), walk.one);
-        walk.first = true;
-    }
 
     if (!busy) {
     } else if (warp >= 8) {
@@ -166,7 +303,8 @@ __global__ void __launch_bounds__(kThreadsA, 1) prefill_attend_kernel(const __gr
         if (lane == 0) {
             int group = 0, unit = 0;                       // issued so far
             int freed = 0, freed_units = 0;
-            int tiles_q = 0;
+            uint32_t qe_phase[2] = {0, 0};
+            int last_halves = 0;                           // of the last piece with tiles
             bool ok = true;
             auto put = [&](const uint8_t* a, int na, const uint8_t* b2, int nb) {      // a group: na blocks at a, nb at b2
                 const int n = na + nb;
@@ -185,27 +323,38 @@ __global__ void __launch_bounds__(kThreadsA, 1) prefill_attend_kernel(const __gr
                 ++group;
                 *(volatile int*)&sh->issued = group;
             };
-            typename Walk::Piece s;
-            while (ok && walk.next(p, s)) {
-                if (s.t0 == s.t1) continue;
-                const int4 seq = p.seq[s.a.x];
-                const int g = (int)((int64_t)s.u * p.G / p.units), gv = (int)((int64_t)s.u * p.Gv / p.units);
-                const bool two = s.b.z * p.hp > 128;
-                for (int t = s.t0; t < s.t1 && ok; ++t) {
-                    const size_t tile = (size_t)seq.y + (t < s.a.w ? t : t + s.b.x);
+            for (int k = 0; ok; ++k) {
+                ok = wait_or_fail(&sh->piece_full[k & 1], (k >> 1) & 1, sh, p.status);
+                if (!ok) break;
+                const Piece s = sh->piece[k & 1];
+                if (s.unit < 0) break;
+                const int g = (int)((int64_t)s.unit * p.G / p.units), gv = (int)((int64_t)s.unit * p.Gv / p.units);
+                const int halves = s.queries * p.hp > 128 ? 2 : 1;
+                auto key = [&](int t) {
+                    const size_t tile = (size_t)s.tile0 + (t < s.head ? t : t + s.gap);
                     put(p.kc + (tile * p.G + g) * (size_t)((KU - 1) * kBlock), KU - 1, p.krope + tile * kBlock, 1);
-                    if (t == s.t0 && ok) {
-                        // the queries, once the last tile's are no longer read
-                        if (tiles_q > 0) ok = wait_or_fail(&sh->q_empty, (tiles_q - 1) & 1, sh, p.status);
-                        if (!ok) break;
-                        const int bytes = (two ? 2 : 1) * kHalf;
-                        mbar_arrive_expect_tx(&sh->q_full, bytes);
-                        const uint8_t* q = p.qt + ((size_t)s.u * p.nq + s.j) * (size_t)(2 * kHalf);
-                        for (int i = 0; i < (two ? 2 : 1); ++i) bulk_load(sm + i * kHalf, q + (size_t)i * kHalf, kHalf, &sh->q_full);
-                        ++tiles_q;
-                        *(volatile int*)&sh->q_issued = tiles_q;
+                };
+                if (s.t0 < s.t1) key(s.t0);
+                // a query half is read by the products until the last ones of the piece ahead have ended
+                for (int h = 0; h < 2 && ok; ++h) {
+                    if (h < last_halves) {
+                        ok = wait_or_fail(&sh->q_empty[h], qe_phase[h], sh, p.status);
+                        qe_phase[h] ^= 1;
                     }
+                    if (!ok || s.t0 == s.t1 || h >= halves || k == 0) continue;       // (the first piece's rows go to shared memory directly)
+                    if (h == 0) ok = wait_or_fail(&sh->conv_full[k & 1], ((k - 1) >> 1) & 1, sh, p.status);
+                    if (!ok) break;
+                    mbar_arrive_expect_tx(&sh->q_full[h], kHalf);
+                    bulk_load(sm + h * kHalf, p.qs + ((size_t)(2 * cta + (k & 1)) * 2 + h) * kHalf, kHalf, &sh->q_full[h]);
+                    *(volatile int*)&sh->q_issued[h] = *(volatile int*)&sh->q_issued[h] + 1;
+                }
+                if (k > 0) mbar_arrive(&sh->piece_empty[(k - 1) & 1]);                // the converted rows of piece k - 1 are no longer read
+                if (s.t0 < s.t1) last_halves = halves;
+                else if (last_halves) last_halves = 0;
+                for (int t = s.t0; t < s.t1 && ok; ++t) {
+                    const size_t tile = (size_t)s.tile0 + (t < s.head ? t : t + s.gap);
                     put(p.v + (tile * p.Gv + gv) * (size_t)(VU * kBlock), VU, nullptr, 0);
+                    if (t + 1 < s.t1) key(t + 1);
                 }
             }
         }
@@ -216,9 +365,8 @@ __global__ void __launch_bounds__(kThreadsA, 1) prefill_attend_kernel(const __gr
         const uint32_t id_s = idesc_bf16(128, 128, 0, 0) & ~bf;
         const uint32_t id_o = idesc_bf16(128, DV, 0, 1) & ~bf;
         const uint32_t id_o64 = idesc_bf16(128, 64, 0, 1) & ~bf;
-        const int rope_steps = p.d_r / 16;
-        int group = 0, unit = 0, tiles_q = 0;
-        uint32_t p_phase[2] = {0, 0};
+        int group = 0, unit = 0, k = 0;
+        uint32_t p_phase[2] = {0, 0}, q_phase[2] = {0, 0};
         bool ok = true;
         auto block_at = [&](int u) { return smem_u32(ring + (u % kUnits) * kBlock); };
         // S of half h from the key blocks at `u`
@@ -226,38 +374,37 @@ __global__ void __launch_bounds__(kThreadsA, 1) prefill_attend_kernel(const __gr
             const uint32_t q = smem_u32(sm + h * kHalf);
             if (elect_one()) {
 #pragma unroll
-                for (int blk = 0; blk < KU - 1; ++blk) {
-                    const uint32_t k = block_at(u + blk);
+                for (int blk = 0; blk < KU; ++blk) {
+                    const uint32_t kb = block_at(u + blk);
+                    const int steps = blk < KU - 1 ? 4 : DR / 16;
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
+                    for (int kk = 0; kk < steps; ++kk)
                         mma_bf16(tmem + kS + h * 128, smem_desc(q + blk * kBlock + kk * 32, 16, 1024, kSwizzle128B),
-                                 smem_desc(k + kk * 32, 16, 1024, kSwizzle128B), id_s, (blk > 0 || kk > 0) ? 1u : 0u);
+                                 smem_desc(kb + kk * 32, 16, 1024, kSwizzle128B), id_s, (blk > 0 || kk > 0) ? 1u : 0u);
                 }
-                const uint32_t k = block_at(u + KU - 1);
-                for (int kk = 0; kk < rope_steps; ++kk)
-                    mma_bf16(tmem + kS + h * 128, smem_desc(q + (KU - 1) * kBlock + kk * 32, 16, 1024, kSwizzle128B),
-                             smem_desc(k + kk * 32, 16, 1024, kSwizzle128B), id_s, 1u);
                 mma_commit(&sh->s_full[h]);
             }
             __syncwarp();
         };
-        auto pv = [&](int h, int u, bool as_bf, bool acc) {
+        // half (0 or 1) of the tokens of O += P V
+        auto pv = [&](int h, int u, bool as_bf, bool acc, int part) {
             const uint32_t v0 = block_at(u), v1 = block_at(u + VU - 1);
             const uint32_t fmt = as_bf ? bf : 0u;
+            const uint32_t o = tmem + kO + h * 128, a = tmem + kS + h * 128;
             if (elect_one()) {
                 if (VU == 1 || v1 > v0) {
 #pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
-                        mma_bf16_tmem_a(tmem + kO + h * 128, tmem + kS + h * 128 + kk * 8, smem_desc(v0 + kk * 2048, kBlock, 1024, kSwizzle128B),
-                                        id_o | fmt, (acc || kk > 0) ? 1u : 0u);
+                    for (int i = 0; i < 4; ++i) {
+                        const int kk = part * 4 + i;
+                        mma_bf16_tmem_a(o, a + kk * 8, smem_desc(v0 + kk * 2048, kBlock, 1024, kSwizzle128B), id_o | fmt, (acc || kk > 0) ? 1u : 0u);
+                    }
                 } else {
                     // the value blocks wrap around the ring's end: 64 columns at a time
 #pragma unroll
-                    for (int kk = 0; kk < 8; ++kk) {
-                        mma_bf16_tmem_a(tmem + kO + h * 128, tmem + kS + h * 128 + kk * 8, smem_desc(v0 + kk * 2048, kBlock, 1024, kSwizzle128B),
-                                        id_o64 | fmt, (acc || kk > 0) ? 1u : 0u);
-                        mma_bf16_tmem_a(tmem + kO + h * 128 + 64, tmem + kS + h * 128 + kk * 8, smem_desc(v1 + kk * 2048, kBlock, 1024, kSwizzle128B),
-                                        id_o64 | fmt, (acc || kk > 0) ? 1u : 0u);
+                    for (int i = 0; i < 4; ++i) {
+                        const int kk = part * 4 + i;
+                        mma_bf16_tmem_a(o, a + kk * 8, smem_desc(v0 + kk * 2048, kBlock, 1024, kSwizzle128B), id_o64 | fmt, (acc || kk > 0) ? 1u : 0u);
+                        mma_bf16_tmem_a(o + 64, a + kk * 8, smem_desc(v1 + kk * 2048, kBlock, 1024, kSwizzle128B), id_o64 | fmt, (acc || kk > 0) ? 1u : 0u);
                     }
                 }
             }
@@ -268,177 +415,250 @@ __global__ void __launch_bounds__(kThreadsA, 1) prefill_attend_kernel(const __gr
             if (elect_one()) mma_commit(bar);
             __syncwarp();
         };
-        typename Walk::Piece s;
-        while (ok && walk.next(p, s)) {
-            if (s.t0 == s.t1) continue;
-            const int4 seq = p.seq[s.a.x];
-            const int halves = s.b.z * p.hp > 128 ? 2 : 1;
-            const int n = s.t1 - s.t0;
-            auto tile_of = [&](int t) { return seq.y + (t < s.a.w ? t : t + s.b.x); };
-            int info = p.tinfo[tile_of(s.t0)];
-            if (!(ok = wait_group(group))) break;
-            if (!(ok = wait_or_fail(&sh->q_full, tiles_q & 1, sh, p.status))) break;
-            ++tiles_q;
-            tc_fence_after();
-            for (int h = 0; h < halves; ++h) qk(h, unit);
-            commit(&sh->empty[group % kGroups]);
-            if (n == 1) commit(&sh->q_empty);
+        // The next piece with tiles, from the queue; halves 0 at the end.
+        struct Next { int n, halves, k, tile0, t0, head, gap; };
+        auto fetch = [&]() {
+            Next x{};
+            for (;; ++k) {
+                if (!(ok = wait_or_fail(&sh->piece_full[k & 1], (k >> 1) & 1, sh, p.status))) return x;
+                const Piece s = sh->piece[k & 1];
+                __syncwarp();
+                if (s.unit < 0) return x;
+                if (lane == 0) mbar_arrive(&sh->piece_empty[k & 1]);
+                if (s.t0 == s.t1) continue;
+                x = Next{s.t1 - s.t0, s.queries * p.hp > 128 ? 2 : 1, k, s.tile0, s.t0, s.head, s.gap};
+                ++k;
+                return x;
+            }
+        };
+        auto wait_query = [&](const Next& x, int h) {
+            if (x.k == 0) return wait_or_fail(&sh->q0_full[h], 0, sh, p.status);
+            const bool r = wait_or_fail(&sh->q_full[h], q_phase[h], sh, p.status);
+            q_phase[h] ^= 1;
+            return r;
+        };
+        Next cur = fetch(), nxt{};
+        // the first tile's logits
+        if (ok && cur.halves) {
+            ok = wait_group(group);
+            for (int h = 0; h < cur.halves && ok; ++h) {
+                if (!(ok = wait_query(cur, h))) break;
+                tc_fence_after();
+                qk(h, unit);
+                if (cur.n == 1) commit(&sh->q_empty[h]);
+            }
+            if (ok) commit(&sh->empty[group % kGroups]);
             ++group;
             unit += KU;
-            for (int j = 0; j < n && ok; ++j) {
+        }
+        while (ok && cur.halves) {
+            int info = p.tinfo[cur.tile0 + (cur.t0 < cur.head ? cur.t0 : cur.t0 + cur.gap)];
+            for (int j = 0; j < cur.n && ok; ++j) {
                 const int vu = unit, ku = unit + VU, gv = group, gk = group + 1;
-                const bool as_bf = (info & 256) != 0, more = j + 1 < n;
-                if (more) info = p.tinfo[tile_of(s.t0 + j + 1)];
-                for (int h = 0; h < halves; ++h) {
-                    ok = wait_or_fail(&sh->p_full[h], p_phase[h], sh, p.status);
-                    if (!ok) break;
-                    p_phase[h] ^= 1;
+                const bool as_bf = (info & 256) != 0, more = j + 1 < cur.n;
+                if (more) {
+                    const int t = cur.t0 + j + 1;
+                    info = p.tinfo[cur.tile0 + (t < cur.head ? t : t + cur.gap)];
+                }
+                int follow = cur.halves;                   // halves that have a product S to come
+                for (int h = 0; h < cur.halves; ++h) {
+                    if (!(ok = wait_or_fail(&sh->pa_full[h], p_phase[h], sh, p.status))) break;
                     if (h == 0 && !(ok = wait_group(gv))) break;
                     tc_fence_after();
-                    pv(h, vu, as_bf, j > 0);
-                    if (h == halves - 1) commit(&sh->empty[gv % kGroups]);
+                    pv(h, vu, as_bf, j > 0, 0);
+                    if (!(ok = wait_or_fail(&sh->pb_full[h], p_phase[h], sh, p.status))) break;
+                    p_phase[h] ^= 1;
+                    tc_fence_after();
+                    pv(h, vu, as_bf, true, 1);
+                    if (h == cur.halves - 1) commit(&sh->empty[gv % kGroups]);
                     if (!more) {
                         commit(&sh->o_full[h]);
-                    } else {
-                        if (h == 0 && !(ok = wait_group(gk))) break;
-                        tc_fence_after();
-                        qk(h, ku);
-                        if (h == halves - 1) commit(&sh->empty[gk % kGroups]);
+                        if (h == 0) {
+                            nxt = fetch();
+                            if (!ok) break;
+                            follow = nxt.halves;
+                        }
                     }
+                    // the next tile's logits: this piece's, or the next piece's first
+                    const int upto = !more && h == cur.halves - 1 ? follow : min(h + 1, follow);
+                    for (int g = h; g < upto && ok; ++g) {
+                        if (g == 0 && !(ok = wait_group(gk))) break;
+                        if (!more && !(ok = wait_query(nxt, g))) break;
+                        tc_fence_after();
+                        qk(g, ku);
+                        if (more ? j + 2 == cur.n : nxt.n == 1) commit(&sh->q_empty[g]);
+                        if (g == follow - 1) commit(&sh->empty[gk % kGroups]);
+                    }
+                    if (!ok) break;
                 }
-                if (more && j + 2 == n && ok) commit(&sh->q_empty);
-                group += more ? 2 : 1;
-                unit += VU + (more ? KU : 0);
+                const bool went = more || nxt.halves > 0;
+                group += went ? 2 : 1;
+                unit += VU + (went ? KU : 0);
             }
+            cur = nxt;
+            nxt = Next{};
         }
         commit(&sh->done);
+      } else {
+        // ---- the list, and the queries of every piece but the first ----
+        Walk walk;
+        walk.at = place_of(p, share_start(all, n_cta, cta), one);
+        walk.end = place_of(p, share_start(all, n_cta, cta + 1), one);
+        walk.first = true;
+        bool ok = true;
+        for (int k = 0;; ++k) {
+            Piece s;
+            if (!walk.next(p, s)) s.unit = -1;
+            if (k >= 2) ok = wait_or_fail(&sh->piece_empty[k & 1], ((k >> 1) - 1) & 1, sh, p.status);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            if (warp == 10 && lane == 0) {
+                sh->piece[k & 1] = s;
+                mbar_arrive(&sh->piece_full[k & 1]);
+            }
+            if (s.unit < 0) break;
+            if (k == 0) continue;
+            if (s.t0 < s.t1) {
+                const int rows = min(s.queries * p.hp, kRowsQ);
+                const size_t buf = 2 * cta + (k & 1);
+                uint8_t* dst = p.qs + buf * (2 * kHalf);
+                for (int rt = (warp - 10) * 4; rt < rows; rt += 8) {
+                    const float c = query_rows<DH, DR>(p, s, rt, dst + (rt >> 7) * kHalf, lane);
+                    if ((lane & 7) == 0) p.qcs[buf * kRowsQ + rt + (lane >> 3)] = c;
+                }
+                asm volatile("fence.proxy.async.global;" ::: "memory");
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh->conv_full[k & 1]);
+        }
       }
     } else {
         // ---- softmax: thread = row ----
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-        const int h = warp >> 2, row = tid & 127;
+        const int h = warp >> 2, row = tid & 127, rt = tid;
         const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t t_s = tmem + lane_base + kS + h * 128, t_o = tmem + lane_base + kO + h * 128;
         const int* we = reinterpret_cast<const int*>(p.weights);
         uint32_t s_phase = 0, o_phase = 0;
         bool ok = true;
-        typename Walk::Piece s;
-        while (walk.next(p, s)) {
-            if (h == 1 && s.b.z * p.hp <= 128) continue;
-            const int4 seq = p.seq[s.a.x];
-            const int rt = h * 128 + row, i = rt / p.hp;               // the row's query within the tile
-            const bool there = i < s.b.z;
-            const int n_row = there ? s.b.y + i : 0;                    // causal length
-            const int n_hi = s.b.y + s.b.z - 1;
-            const float c = p.qc[((size_t)s.u * p.nq + s.j) * kRowsQ + rt];
+        (void)row;
+        for (int k = 0;; ++k) {
+            ok = wait_or_fail(&sh->piece_full[k & 1], (k >> 1) & 1, sh, p.status);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            const Piece s = sh->piece[k & 1];
+            if (s.unit < 0) break;
+            const bool mine = h == 0 || s.queries * p.hp > 128;         // uniform in a warp
+            float c = 0.f;
+            if (mine && k == 0 && s.t0 < s.t1) {
+                // the first piece's queries, straight to shared memory: a warp its own 32 rows
+#pragma unroll 2
+                for (int q = 0; q < 32; q += 4) {
+                    const float f = query_rows<DH, DR>(p, s, warp * 32 + q, sm + h * kHalf, lane);
+                    const float g = __shfl_sync(0xffffffffu, f, (lane & 3) * 8);
+                    if ((lane >> 2) == (q >> 2)) c = g;
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh->q0_full[h]);
+            }
+            const int i = rt >> p.hp_log;                               // the row's query within the tile
+            const bool there = i < s.queries;
+            const int n_row = there ? s.n_lo + i : 0;                   // causal length
             float m = -INFINITY, sum = 0.f;
-            auto tile_at = [&](int t) { return t < s.a.w ? t : t + s.b.x; };
-            int info = s.t0 < s.t1 ? p.tinfo[seq.y + tile_at(s.t0)] : 0;
-            for (int t = s.t0; t < s.t1 && ok; ++t) {
+            auto tile_at = [&](int t) { return t < s.head ? t : t + s.gap; };
+            int info = mine && s.t0 < s.t1 ? p.tinfo[s.tile0 + tile_at(s.t0)] : 0;
+            for (int t = s.t0; t < s.t1 && mine; ++t) {
                 const int first = tile_at(t) * kTile;
                 const int e = (info & 255) - 64;
                 const bool as_bf = (info & 256) != 0;
-                if (t + 1 < s.t1) info = p.tinfo[seq.y + tile_at(t + 1)];
+                if (t + 1 < s.t1) info = p.tinfo[s.tile0 + tile_at(t + 1)];
                 ok = wait_or_fail(&sh->s_full[h], s_phase, sh, p.status);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 s_phase ^= 1;
                 tc_fence_after();
+                if (t == s.t0 && k > 0) c = *(volatile const float*)&p.qcs[(size_t)(2 * cta + (k & 1)) * kRowsQ + rt];
                 float x[128];
                 tmem_ld64(t_s, *reinterpret_cast<uint32_t(*)[64]>(x));
                 tmem_ld64(t_s + 64, *reinterpret_cast<uint32_t(*)[64]>(x + 64));
                 tmem_wait_ld();
                 // tiles that some row does not see whole (uniform over the tile's rows)
-                const bool edge = first + kTile > s.b.y || (p.window > 0 && first < n_hi - p.window && first + kTile > p.sinks);
+                const bool edge = first + kTile > s.n_lo || (p.window > 0 && first < s.n_lo + s.queries - 1 - p.window && first + kTile > p.sinks);
                 if (edge) {
                     const int end = n_row - first;
                     const int from = p.window > 0 ? n_row - p.window - first : -1, sink = p.window > 0 ? p.sinks - first : -1;
 #pragma unroll
-                    for (int k = 0; k < 128; ++k)
-                        if (k >= end || (k < from && k >= sink)) x[k] = -INFINITY;
+                    for (int q = 0; q < 128; ++q)
+                        if (q >= end || (q < from && q >= sink)) x[q] = -INFINITY;
                 }
-                float top[2] = {fmaxf(x[0], x[2]), fmaxf(x[1], x[3])};
+                float top[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-                for (int k = 4; k < 128; k += 4) {
-                    top[0] = fmaxf(top[0], fmaxf(x[k], x[k + 2]));
-                    top[1] = fmaxf(top[1], fmaxf(x[k + 1], x[k + 3]));
+                for (int q = 4; q < 124; q += 8) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) top[r] = max3(top[r], x[q + r], x[q + 4 + r]);
                 }
-                const float cand = fmaf(fmaxf(top[0], top[1]), c, (float)e);
+                const float cand = fmaf(fmaxf(max3(top[0], top[1], x[124]), max3(fmaxf(top[2], top[3]), fmaxf(x[125], x[126]), x[127])), c, (float)e);
                 const bool move = cand > m + 8.f;
                 if (__any_sync(0xffffffffu, move)) {
                     const float m2 = move ? cand : m;
                     const float a = move ? ex2(m - m2) : 1.f;           // 0 while nothing was seen
                     sum *= a;
                     if (t > s.t0) {
-#pragma unroll
-                        for (int k = 0; k < DV; k += 16) {
+#pragma unroll 1
+                        for (int q = 0; q < DV; q += 16) {
                             uint32_t o[16];
-                            tmem_ld16(t_o + k, o);
+                            tmem_ld16(t_o + q, o);
                             tmem_wait_ld();
 #pragma unroll
-                            for (int q = 0; q < 16; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * a);
-                            tmem_st16(t_o + k, o);
+                            for (int r = 0; r < 16; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * a);
+                            tmem_st16(t_o + q, o);
                         }
                     }
                     m = m2;
                 }
                 const float off = (float)(e + 7) - (m == -INFINITY ? 0.f : m);
-                float part[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int k = 0; k < 128; k += 32) {
-                    uint32_t w[16];
-#pragma unroll
-                    for (int q = 0; q < 32; ++q) {
-                        x[k + q] = ex2(fmaf(x[k + q], c, off));
-                        part[q & 3] += x[k + q];
-                    }
-                    if (as_bf) {
-#pragma unroll
-                        for (int q = 0; q < 16; ++q) w[q] = pack_bf16(x[k + 2 * q], x[k + 2 * q + 1]);
-                    } else {
-#pragma unroll
-                        for (int q = 0; q < 16; ++q) w[q] = pack_f16(x[k + 2 * q], x[k + 2 * q + 1]);
-                    }
-                    tmem_st16(t_s + k / 2, w);
-                }
-                tmem_wait_st();
-                tc_fence_before();
-                mbar_arrive(&sh->p_full[h]);
-                sum = fmaf((part[0] + part[1]) + (part[2] + part[3]), pow2i(-e), sum);
+                const float part = as_bf ? weights_out<true>(x, c, off, t_s, &sh->pa_full[h], &sh->pb_full[h], lane)
+                                         : weights_out<false>(x, c, off, t_s, &sh->pa_full[h], &sh->pb_full[h], lane);
+                sum = fmaf(part, pow2i(-e), sum);
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh->piece_empty[k & 1]);        // (s and c are in registers)
+            if (!mine) continue;
             if (s.t0 < s.t1 && ok) ok = wait_or_fail(&sh->o_full[h], o_phase, sh, p.status);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
-            const bool whole = s.t0 == 0 && s.t1 == s.nt;
             if (s.t0 < s.t1) {
                 o_phase ^= 1;
                 tc_fence_after();
             }
-            const int gv = (int)((int64_t)s.u * p.Gv / p.units);
-            if (whole) {
+            if (s.t0 == 0 && s.t1 == s.nt) {
+                const int gv = (int)((int64_t)s.unit * p.Gv / p.units);
                 const float inv = sum == 0.f ? 0.f : ldexpf(1.f / sum, we[p.G + gv]);
-                const int head = s.u * p.hp + rt % p.hp;
-                const int64_t r = seq.z + s.a.y + i;
-                OT* dst = reinterpret_cast<OT*>(p.o) + (r * p.H + head) * DV;
+                const int head = s.unit * p.hp + (rt & (p.hp - 1));
+                const int64_t r = (int64_t)s.row0 + i;
+                const int64_t to = (r * p.H + head) * DV;
 #pragma unroll 1
-                for (int k = 0; k < DV; k += 32) {
+                for (int q = 0; q < DV; q += 32) {
                     float o[32];
                     if (s.t0 < s.t1) {
-                        tmem_ld16(t_o + k, *reinterpret_cast<uint32_t(*)[16]>(o));
-                        tmem_ld16(t_o + k + 16, *reinterpret_cast<uint32_t(*)[16]>(o + 16));
+                        tmem_ld16(t_o + q, *reinterpret_cast<uint32_t(*)[16]>(o));
+                        tmem_ld16(t_o + q + 16, *reinterpret_cast<uint32_t(*)[16]>(o + 16));
                         tmem_wait_ld();
                     }
 #pragma unroll
-                    for (int q = 0; q < 32; ++q) o[q] = sum == 0.f ? 0.f : o[q] * inv;
+                    for (int w = 0; w < 32; ++w) o[w] = sum == 0.f ? 0.f : o[w] * inv;
                     if (there) {
-                        if constexpr (sizeof(OT) == 4) {
+                        if (p.o_f32) {
+                            float4* dst = reinterpret_cast<float4*>((float*)p.o + to + q);
 #pragma unroll
-                            for (int q = 0; q < 8; ++q) reinterpret_cast<float4*>(dst + k)[q] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+                            for (int w = 0; w < 8; ++w) dst[w] = make_float4(o[4 * w], o[4 * w + 1], o[4 * w + 2], o[4 * w + 3]);
                         } else {
+                            uint4* dst = reinterpret_cast<uint4*>((uint16_t*)p.o + to + q);
 #pragma unroll
-                            for (int q = 0; q < 4; ++q)
-                                reinterpret_cast<uint4*>(dst + k)[q] = make_uint4(pack_bf16(o[8 * q], o[8 * q + 1]), pack_bf16(o[8 * q + 2], o[8 * q + 3]),
-                                                                                  pack_bf16(o[8 * q + 4], o[8 * q + 5]), pack_bf16(o[8 * q + 6], o[8 * q + 7]));
+                            for (int w = 0; w < 4; ++w)
+                                dst[w] = make_uint4(pack_bf16(o[8 * w], o[8 * w + 1]), pack_bf16(o[8 * w + 2], o[8 * w + 3]),
+                                                                                  pack_bf16(o[8 * w + 4], o[8 * w + 5]), pack_bf16(o[8 * w + 6], o[8 * w + 7]));
                         }
                     }
                 }
@@ -447,14 +667,14 @@ __global__ void __launch_bounds__(kThreadsA, 1) prefill_attend_kernel(const __gr
                 const size_t part = (size_t)(2 * cta + (s.t0 > 0 ? 0 : 1)) * kRowsQ + rt;
                 float* dst = p.part_o + part * DV;
 #pragma unroll 1
-                for (int k = 0; k < DV; k += 32) {
+                for (int q = 0; q < DV; q += 32) {
                     float o[32];
-                    tmem_ld16(t_o + k, *reinterpret_cast<uint32_t(*)[16]>(o));
-                    tmem_ld16(t_o + k + 16, *reinterpret_cast<uint32_t(*)[16]>(o + 16));
+                    tmem_ld16(t_o + q, *reinterpret_cast<uint32_t(*)[16]>(o));
+                    tmem_ld16(t_o + q + 16, *reinterpret_cast<uint32_t(*)[16]>(o + 16));
                     tmem_wait_ld();
                     if (there) {
 #pragma unroll
-                        for (int q = 0; q < 8; ++q) reinterpret_cast<float4*>(dst + k)[q] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+                        for (int w = 0; w < 8; ++w) reinterpret_cast<float4*>(dst + q)[w] = make_float4(o[4 * w], o[4 * w + 1], o[4 * w + 2], o[4 * w + 3]);
                     }
                 }
                 if (there) p.part_ml[part] = make_float2(m, sum);
@@ -468,9 +688,12 @@ __global__ void __launch_bounds__(kThreadsA, 1) prefill_attend_kernel(const __gr
         wait_or_fail(&sh->done, 0, sh, p.status);
         if (*(volatile int*)&sh->fail && tid == 0) {
             dec::wait_bounded(&sh->done, 0, p.status);
-            const int n = *(volatile int*)&sh->issued, q = *(volatile int*)&sh->q_issued;
+            const int n = *(volatile int*)&sh->issued;
             for (int g = max(0, n - kGroups); g < n; ++g) dec::wait_bounded(&sh->full[g % kGroups], (g / kGroups) & 1, p.status);
-            if (q > 0) dec::wait_bounded(&sh->q_full, (q - 1) & 1, p.status);
+            for (int h = 0; h < 2; ++h) {
+                const int q = *(volatile int*)&sh->q_issued[h];
+                if (q > 0) dec::wait_bounded(&sh->q_full[h], (q - 1) & 1, p.status);
+            }
         }
     }
     tc_fence_before();
@@ -489,7 +712,7 @@ __global__ void __launch_bounds__(kThreadsA, 1) prefill_attend_kernel(const __gr
 constexpr int kThreadsJ = 128;
 constexpr int kRowsJ = 16;
 
-template <int DV, typename OT>
+template <int DV>
 __global__ void __launch_bounds__(kThreadsJ) prefill_join_kernel(const __grid_constant__ Params p) {
     pdl_wait();
     pdl_trigger();
@@ -553,33 +776,31 @@ __global__ void __launch_bounds__(kThreadsJ) prefill_join_kernel(const __grid_co
         const float inv = sum == 0.f ? 0.f : ldexpf(1.f / sum, e);
 #pragma unroll
         for (int c = 0; c < 4; ++c) o[c] = sum == 0.f ? 0.f : o[c] * inv;
-        OT* dst = reinterpret_cast<OT*>(p.o) + (r * p.H + head) * DV + col;
-        if constexpr (sizeof(OT) == 4) *reinterpret_cast<float4*>(dst) = make_float4(o[0], o[1], o[2], o[3]);
-        else *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]));
+        const int64_t to = (r * p.H + head) * DV + col;
+        if (p.o_f32) *reinterpret_cast<float4*>((float*)p.o + to) = make_float4(o[0], o[1], o[2], o[3]);
+        else *reinterpret_cast<uint2*>((uint16_t*)p.o + to) = make_uint2(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]));
         if (col == 0 && p.lse) p.lse[r * p.H + head] = sum == 0.f ? -INFINITY : (top - 7.f) * kLn2 + logf(sum);
     }
 }
 
-template <int DH, int DV, typename OT>
+template <int DH, int DR, int DV>
 int launch(const Params& p, cudaStream_t s) {
-    auto k = prefill_attend_kernel<DH, DV, OT>;
+    auto k = prefill_attend_kernel<DH, DR, DV>;
     if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<DH>()) != cudaSuccess) return QKMLA_ERR_CUDA;
     if (launch_pdl(k, dim3(p.ctas), dim3(kThreadsA), smem_bytes<DH>(), s, p) != cudaSuccess) return QKMLA_ERR_CUDA;
     if (p.ctas < 2) return QKMLA_OK;
-    return launch_pdl(prefill_join_kernel<DV, OT>, dim3(p.ctas - 1, kRowsQ / kRowsJ), dim3(kThreadsJ), 0, s, p) == cudaSuccess ? QKMLA_OK
-                                                                                                                             : QKMLA_ERR_CUDA;
+    return launch_pdl(prefill_join_kernel<DV>, dim3(p.ctas - 1, kRowsQ / kRowsJ), dim3(kThreadsJ), 0, s, p) == cudaSuccess ? QKMLA_OK
+                                                                                                                         : QKMLA_ERR_CUDA;
 }
 
-template <typename OT>
-int launch_dims(const Params& p, cudaStream_t s) {
-    if (p.d_h == 128) return p.d_v == 128 ? launch<128, 128, OT>(p, s) : launch<128, 64, OT>(p, s);
-    return p.d_v == 128 ? launch<64, 128, OT>(p, s) : launch<64, 64, OT>(p, s);
-}
+template <int DH, int DR>
+int launch_dv(const Params& p, cudaStream_t s) { return p.d_v == 128 ? launch<DH, DR, 128>(p, s) : launch<DH, DR, 64>(p, s); }
 
 }  // namespace
 
-int launch_attend(const Params& p, int o_dtype, cudaStream_t s) {
-    return o_dtype == QKMLA_F32 ? launch_dims<float>(p, s) : launch_dims<__nv_bfloat16>(p, s);
+int launch_attend(const Params& p, cudaStream_t s) {
+    if (p.d_h == 128) return p.d_r == 64 ? launch_dv<128, 64>(p, s) : launch_dv<128, 32>(p, s);
+    return p.d_r == 64 ? launch_dv<64, 64>(p, s) : launch_dv<64, 32>(p, s);
 }
 
 }  // namespace pf
@@ -627,10 +848,13 @@ int make_params(const qkmla_prefill_args* a, bool sizes_only, pf::Params* p, siz
     const int64_t longest = (int64_t)a->max_pages * a->page_size;
     p->window = (int)(a->window < longest ? a->window : a->window ? longest : 0);
     p->sinks = (int)(a->sinks < longest ? a->sinks : longest);
+    p->q_bf16 = a->q_dtype == QKMLA_BF16;
+    p->o_f32 = a->o_dtype == QKMLA_F32;
     p->ak_f16 = (a->flags & QKMLA_FLAG_ALPHA_F16) ? 1 : 0;
     p->total_tokens = a->total_tokens;
     p->units = units;
     p->hp = hp;
+    while ((1 << p->hp_log) < hp) ++p->hp_log;
     p->tq = pf::kRowsQ / hp;
     p->nq = a->rows / p->tq + a->B;
     p->max_tiles = (int)(a->total_tokens / pf::kTile) + a->B;
@@ -649,12 +873,12 @@ int make_params(const qkmla_prefill_args* a, bool sizes_only, pf::Params* p, siz
     p->pre = (int64_t*)take(8 * (nq + 1));
     p->tinfo = (int*)take(4 * tiles);
     p->part_ml = (float2*)take(sizeof(float2) * 2 * p->ctas * pf::kRowsQ);
-    p->qc = (float*)take(4 * (size_t)units * nq * pf::kRowsQ);
+    p->qcs = (float*)take(4 * (size_t)2 * p->ctas * pf::kRowsQ);
     p->part_o = (float*)take(4 * (size_t)2 * p->ctas * pf::kRowsQ * a->d_v);
     p->krope = (uint8_t*)take(tiles * pf::kBlock);
     p->kc = (uint8_t*)take(tiles * a->G * (a->d_h / 64) * pf::kBlock);
     p->v = (uint8_t*)take(tiles * a->G_v * (a->d_v / 64) * pf::kBlock);
-    p->qt = (uint8_t*)take((size_t)units * nq * 2 * (a->d_h / 64 + 1) * pf::kBlock);
+    p->qs = (uint8_t*)take((size_t)p->ctas * 4 * (a->d_h / 64 + 1) * pf::kBlock);
     *bytes = at - (uintptr_t)a->workspace;
     if (sizes_only) return QKMLA_OK;
     if (q8 != (a->kv_scale != nullptr)) return QKMLA_ERR_INVALID;
@@ -708,7 +932,6 @@ extern "C" int qkmla_prefill(const qkmla_prefill_args* a, void* stream) {
     int rc = make_params(a, false, &p, &bytes);
     if (rc != QKMLA_OK || a->rows == 0) return rc;
     cudaStream_t s = (cudaStream_t)stream;
-    if ((rc = pf::launch_query(p, a->q_dtype == QKMLA_BF16, s)) != QKMLA_OK) return rc;
     if ((rc = pf::launch_expand(p, a->cache_dtype == QKMLA_E4M3, s)) != QKMLA_OK) return rc;
-    return pf::launch_attend(p, a->o_dtype, s);
+    return pf::launch_attend(p, s);
 }

@@ -3,12 +3,8 @@
 // prefill_pack_kernel   W^K (fp32) and W^V (bf16) as fp16 K-major blocks, each matrix times a power of two
 //                       that brings its largest value into [1, 2): fp16's 11 bits hold W^V's 8 exactly and
 //                       W^K to 2^-11, whatever the weights' scale.
-// prefill_query_kernel  q^ = q gamma_q gamma_k / rms(q) and the RoPE part likewise, one row (query token,
-//                       head) a warp, times a power of two a row that brings its largest value into
-//                       [1, 2), rounded to fp16; softmax_scale, log2 e and that power are the row's factor
-//                       in the attention kernel, where it costs nothing.  HBM-bound: 768 bytes read and 384
-//                       written a row.  Block 0 makes the plan instead.
-// prefill_expand_kernel keys and values of 128 cached tokens, on the tensor cores.
+// prefill_expand_kernel keys and values of the cached tokens, 128 a tile, on the tensor cores; its last block makes
+//                       the plan of the attention's work.
 #include "prefill.cuh"
 
 namespace qkmla {
@@ -58,10 +54,9 @@ __global__ void __launch_bounds__(256) prefill_pack_kernel(const float* __restri
 }
 
 // ---------------------------------------------------------------------------
-// queries and the plan
+// the plan
 // ---------------------------------------------------------------------------
-constexpr int kThreadsQ = 256;
-constexpr int kRowsWarp = 4;               // rows a warp has in flight
+constexpr int kThreadsE = 320;
 
 // Sum of the block's values ahead of this thread's; the whole sum in *all.
 __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* warps, int64_t* all) {
@@ -77,7 +72,7 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* warps, int64_t
     __syncthreads();
     int64_t ahead = 0, sum = 0;
 #pragma unroll
-    for (int i = 0; i < kThreadsQ / 32; ++i) {
+    for (int i = 0; i < kThreadsE / 32; ++i) {
         if (i < warp) ahead += warps[i];
         sum += warps[i];
     }
@@ -85,12 +80,12 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* warps, int64_t
     return ahead + s - v;
 }
 
-__device__ void make_plan(const Params& p) {
-    __shared__ int64_t warps[kThreadsQ / 32];
+// `warps`: shared memory for a number a warp.
+__device__ void make_plan(const Params& p, int64_t* warps) {
     const int tid = threadIdx.x;
     // sequences: lengths, first tiles, rows
     int64_t tiles = 0, tokens = 0, all;
-    const int per = (p.B + kThreadsQ - 1) / kThreadsQ;
+    const int per = (p.B + kThreadsE - 1) / kThreadsE;
     for (int k = 0; k < per; ++k) {
         const int b = tid * per + k;
         if (b >= p.B) break;
@@ -116,10 +111,10 @@ __device__ void make_plan(const Params& p) {
         p.seq[b] = make_int4(ok && fits ? len : 0, (int)min(at, (int64_t)p.max_tiles), rows_ok ? r0 : 0, rows_ok ? r1 - r0 : 0);
         at += n;
     }
-    for (int j = tid; j < p.nq; j += kThreadsQ) p.qinfo[2 * j] = make_int4(-1, 0, 0, 0);
+    for (int j = tid; j < p.nq; j += kThreadsE) p.qinfo[2 * j] = make_int4(-1, 0, 0, 0);
     __syncthreads();
     // query tiles: the tiles of tokens that any of their queries sees
-    for (int b = tid >> 5; b < p.B; b += kThreadsQ / 32) {
+    for (int b = tid >> 5; b < p.B; b += kThreadsE / 32) {
         const int4 s = p.seq[b];
         const int n = s.w, j0 = first_slot(s.z, b, p.tq);
         for (int k = tid & 31; k * (int64_t)p.tq < n; k += 32) {
@@ -137,7 +132,7 @@ __device__ void make_plan(const Params& p) {
         }
     }
     __syncthreads();
-    const int pq = (p.nq + kThreadsQ - 1) / kThreadsQ;
+    const int pq = (p.nq + kThreadsE - 1) / kThreadsE;
     int64_t mine = 0;
     for (int k = 0; k < pq; ++k) {
         const int j = tid * pq + k;
@@ -156,445 +151,359 @@ __device__ void make_plan(const Params& p) {
     if (tid == 0) p.pre[p.nq] = all;
 }
 
-template <typename T, int N>
-__device__ __forceinline__ void load_n(const T* p, float (&v)[N]) {
-    if constexpr (sizeof(T) == 4) {
-        if constexpr (N == 4) { const float4 f = *reinterpret_cast<const float4*>(p); v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w; }
-        else if constexpr (N == 2) { const float2 f = *reinterpret_cast<const float2*>(p); v[0] = f.x; v[1] = f.y; }
-        else v[0] = *p;
-    } else {
-        uint32_t w[(N + 1) / 2];
-        if constexpr (N == 4) { const uint2 u = *reinterpret_cast<const uint2*>(p); w[0] = u.x; w[1] = u.y; }
-        else if constexpr (N == 2) w[0] = *reinterpret_cast<const uint32_t*>(p);
-        else w[0] = *reinterpret_cast<const uint16_t*>(p);
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
-    }
-}
-template <int N>
-__device__ __forceinline__ void store_n(uint8_t* p, const float (&v)[N]) {
-    if constexpr (N == 4) *reinterpret_cast<uint2*>(p) = make_uint2(pack_f16(v[0], v[1]), pack_f16(v[2], v[3]));
-    else if constexpr (N == 2) *reinterpret_cast<uint32_t*>(p) = pack_f16(v[0], v[1]);
-    else *reinterpret_cast<__half*>(p) = __float2half_rn(v[0]);
-}
-
-// DH values of content and DR of RoPE a row; a lane holds DH / 32 and DR / 32 neighbours.
-template <typename T, int DH, int DR>
-__global__ void __launch_bounds__(kThreadsQ) prefill_query_kernel(const Params p) {
-    constexpr int NH = DH / 32, NR = DR / 32, KU = DH / 64 + 1;
-    pdl_wait();                                            // the workspace may still be in use
-    pdl_trigger();
-    if (blockIdx.x == 0) {
-        make_plan(p);
-        return;
-    }
-    const int lane = threadIdx.x & 31;
-    float gam[NH], gr[NR];
-#pragma unroll
-    for (int i = 0; i < NH; ++i) gam[i] = p.gamma_q[lane * NH + i] * p.gamma_k[lane * NH + i];
-#pragma unroll
-    for (int i = 0; i < NR; ++i) gr[i] = p.gamma_rope ? p.gamma_rope[lane * NR + i] : 1.f;
-    const int64_t item0 = ((int64_t)(blockIdx.x - 1) * (kThreadsQ / 32) + (threadIdx.x >> 5)) * kRowsWarp;
-    const int64_t items = (int64_t)p.rows * p.H;
-    // lane j < kRowsWarp finds the place of row item0 + j: its sequence by bisection
-    int64_t dst = -1, tile = 0;
-    int row = 0, r = 0, h = 0;
-    if (lane < kRowsWarp && item0 + lane < items) {
-        r = (int)((item0 + lane) / p.H);
-        h = (int)((item0 + lane) % p.H);
-        if (r >= p.chunk_start[0] && r < p.chunk_start[p.B]) {
-            int lo = 0, hi = p.B - 1;                      // the last b with chunk_start[b] <= r
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                if (p.chunk_start[mid] <= r) lo = mid;
-                else hi = mid - 1;
-            }
-            const int cs = p.chunk_start[lo], i = r - cs;
-            const int j = first_slot(cs, lo, p.tq) + i / p.tq;
-            if (cs >= 0 && j < p.nq) {
-                tile = (int64_t)(h / p.hp) * p.nq + j;
-                row = (i % p.tq) * p.hp + h % p.hp;
-                dst = (tile * 2 + (row >> 7)) * (KU * (int64_t)kBlock);
-            }
-        }
-    }
-    int64_t to[kRowsWarp];
-    float x[kRowsWarp][NH], y[kRowsWarp][NR];
-#pragma unroll
-    for (int j = 0; j < kRowsWarp; ++j) {
-        to[j] = __shfl_sync(0xffffffffu, dst, j);
-        const int rr = __shfl_sync(0xffffffffu, r, j), hh = __shfl_sync(0xffffffffu, h, j);
-        if (to[j] < 0) continue;
-        load_n<T, NH>((const T*)p.q + rr * p.q_row + hh * p.q_head + lane * NH, x[j]);
-        load_n<T, NR>((const T*)p.q_rope + rr * p.qr_row + hh * p.qr_head + lane * NR, y[j]);
-    }
-#pragma unroll
-    for (int j = 0; j < kRowsWarp; ++j) {
-        if (to[j] < 0) continue;
-        float sx = 0.f, sy = 0.f;
-#pragma unroll
-        for (int i = 0; i < NH; ++i) sx = fmaf(x[j][i], x[j][i], sx);
-#pragma unroll
-        for (int i = 0; i < NR; ++i) sy = fmaf(y[j][i], y[j][i], sy);
-        sx = warp_sum(sx);
-        sy = warp_sum(sy);
-        const float ax = 1.f / sqrtf(sx / DH + p.eps), ay = 1.f / sqrtf(sy / DR + p.eps);
-        float top = 0.f;
-#pragma unroll
-        for (int i = 0; i < NH; ++i) top = fmaxf(top, fabsf(x[j][i] = x[j][i] * ax * gam[i]));
-#pragma unroll
-        for (int i = 0; i < NR; ++i) top = fmaxf(top, fabsf(y[j][i] = y[j][i] * ay * gr[i]));
-        top = warp_max(top);
-        const int e = top > 0.f && isfinite(top) ? min(max(ilogbf(top), -100), 100) : 0;
-        const float f = pow2i(-e);
-#pragma unroll
-        for (int i = 0; i < NH; ++i) x[j][i] *= f;
-#pragma unroll
-        for (int i = 0; i < NR; ++i) y[j][i] *= f;
-        const int rw = __shfl_sync(0xffffffffu, row, j), r7 = rw & 127;
-        const int64_t tl = __shfl_sync(0xffffffffu, tile, j);
-        uint8_t* q = p.qt + to[j];
-        const int col = lane * NH;
-        store_n<NH>(q + (col >> 6) * kBlock + sw128_offset(r7, col & 63), x[j]);
-        store_n<NR>(q + (KU - 1) * kBlock + sw128_offset(r7, lane * NR), y[j]);
-        if (lane == 0) p.qc[tl * kRowsQ + rw] = p.scale_log2 * pow2i(e);
-    }
-}
-
 // ---------------------------------------------------------------------------
 // keys and values
 // ---------------------------------------------------------------------------
 // C [128 tokens, d_c] x [W^K_0 .. W^K_{G-1} | W^V_0 ..] in N-tiles of 128 columns.  The latents lie in shared
-// memory for the whole CTA (d_c / 64 blocks), each token times a power of two of its own that brings its
+// memory while their tile is worked on (d_c / 64 blocks), each token times a power of two of its own that brings its
 // largest value into [1, 2): exact as fp16 for a bf16 or an 8-bit latent, but for what lies 2^-14 below that
 // value.  Warps 0-7 gather and convert them, then take the results out of TMEM: a key row is scaled by the
-// stored alpha^k, a value row by its share of the tile's common exponent.  Warp 8 streams the packed
-// weights through a ring of blocks, warp 9 issues the products (M = N = 128, K = 64 a block), the
-// accumulator double-buffered.  Blocks of results are staged in shared memory and leave as bulk copies.
+// stored alpha^k, a value row by its share of the tile's common exponent.  A thread holds 64 columns of a token,
+// one 128-byte line of a block, and stores it 32 bytes at a time.  Warp 8 streams the packed weights through a
+// ring of blocks, warp 9 issues the products (M = N = 128, K = 64 a block), the accumulator double-buffered.
 //
-// Bound: the tensor core for many tokens (2 d_c flops a value), next to it the weights, which every CTA
-// streams through L2 (128 bytes a 256 flops: 63 bytes a cycle and SM at full rate).
-constexpr int kThreadsE = 320;
-constexpr int kRing = 4;                   // weight blocks in flight
+// Bound: the tensor core for many tokens (2 d_c flops a value); next to it the weights, which every tile
+// streams through L2 (16 KB a block of 260 cycles: 63 bytes a cycle and SM at full rate), so the ring takes all the
+// shared memory that the latents leave (six blocks at d_c = 512).  Few tiles: their columns are cut over several CTAs.
+constexpr int kRingMax = 6;
+constexpr int kNone = -1000, kBad = 1000;      // exponents of an all-zero and of a not finite token
 
-struct ExpandLayout {
-    int a, ring, stage, misc, bytes;
-    __host__ __device__ explicit ExpandLayout(int d_c) {
-        a = 0;
-        ring = d_c / 64 * kBlock;
-        stage = ring + kRing * kBlock;
-        misc = stage + 2 * kBlock;
-        bytes = misc + 2048 + 1024;
-    }
+__host__ __device__ inline int expand_ring(int d_c) { return d_c <= 256 ? 2 : kRingMax; }
+__host__ __device__ inline int expand_bytes(int d_c) { return (d_c / 64 + expand_ring(d_c)) * kBlock + 1024 + 2048; }
+
+struct __align__(16) ExpandShared {
+    uint64_t full[kRingMax], empty[kRingMax];
+    uint64_t acc_full[2], acc_empty[2], a_full, done;
+    int exps[2][kTile];
+    int hi[2][8], lo[2][8];
+    uint32_t tmem;
+    int fail, issued;
 };
+static_assert(sizeof(ExpandShared) <= 2048, "beside the blocks");
 
-template <bool Q8>
-__global__ void __launch_bounds__(kThreadsE, 1) prefill_expand_kernel(const Params p, int splits) {
+struct TileOf { int b, t0, len; bool wanted; };
+// The sequence and the first token of a tile of the workspace, by the lengths ahead of it: whole warp.
+__device__ __forceinline__ TileOf locate(const Params& p, int tile) {
+    const int lane = threadIdx.x & 31;
+    int ahead = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+        const int b = b0 + lane;
+        int len = b < p.B ? p.seq_lens[b] : 0;
+        if (len < 0 || len > (int64_t)p.max_pages * p.page_size) len = 0;
+        int n = (len + kTile - 1) / kTile, s = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) s += u;
+        }
+        const int all = __shfl_sync(0xffffffffu, s, 31);
+        if (ahead + all > tile) {
+            const unsigned m = __ballot_sync(0xffffffffu, ahead + s > tile);
+            const int l = __ffs(m) - 1;
+            TileOf r;
+            r.b = b0 + l;
+            r.len = __shfl_sync(0xffffffffu, len, l);
+            r.t0 = (tile - ahead - __shfl_sync(0xffffffffu, s - n, l)) * kTile;
+            const int rows = p.chunk_start[r.b + 1] - p.chunk_start[r.b];
+            r.wanted = rows > 0;
+            // tiles that no query of the step sees are left out
+            if (p.window > 0) r.wanted = r.wanted && (r.t0 < p.sinks || r.t0 + kTile > (int64_t)r.len - rows + 1 - p.window);
+            return r;
+        }
+        ahead += all;
+    }
+    return TileOf{0, 0, 0, false};
+}
+
+__device__ __forceinline__ void st_global_v8(void* p, const uint32_t (&a)[4], const uint32_t (&b)[4]) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]),
+                 "r"(b[1]), "r"(b[2]), "r"(b[3])
+                 : "memory");
+}
+
+// NV: vectors of 8 latents a lane, d_c up to 256 NV; at 1 two CTAs fit on an SM, one gathering while the other multiplies.
+template <bool Q8, int NV>
+__global__ void __launch_bounds__(kThreadsE, NV == 1 ? 2 : 1) prefill_expand_kernel(const __grid_constant__ Params p, int splits) {
     extern __shared__ __align__(1024) uint8_t smraw[];
     uint8_t* sm = smraw + ((1024u - (smem_u32(smraw) & 1023u)) & 1023u);
-    const ExpandLayout L(p.d_c);
-    uint64_t* full = reinterpret_cast<uint64_t*>(sm + L.misc);          // [kRing]
-    uint64_t* empty = full + kRing;                                     // [kRing]
-    uint64_t* acc_full = empty + kRing;                                 // [2]
-    uint64_t* acc_empty = acc_full + 2;                                 // [2]
-    uint64_t* done = acc_empty + 2;
-    int64_t* slots = reinterpret_cast<int64_t*>(done + 1);              // [128] slot of a token, -1 for none
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(slots + kTile);
-    int* fail = reinterpret_cast<int*>(tmem_slot + 1);
-    int* issued_s = fail + 1;
-    int* warp_hi = issued_s + 1;                                        // [8]
-    int* warp_lo = warp_hi + 8;                                         // [8]
-    int* exps = warp_lo + 8;                                            // [128] exponent, or kNone / kBad
-    constexpr int kNone = -1000, kBad = 1000;
+    constexpr int kRing = NV == 1 ? 2 : kRingMax;
+    const int kb = p.d_c / 64;
+    uint8_t* ring = sm + kb * kBlock;
+    ExpandShared* sh = reinterpret_cast<ExpandShared*>(ring + kRing * kBlock);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int tile = blockIdx.x / splits, part = blockIdx.x % splits;
-    const int nkb = p.d_h / 64, nvb = p.d_v / 64, kb = p.d_c / 64;
+    const int nkb = p.d_h / 64, nvb = p.d_v / 64;
     const int blocks = column_blocks(p.G, p.Gv, p.d_h, p.d_v), nt = (blocks + 1) / 2;
-    const int n0 = nt * part / splits, n1 = nt * (part + 1) / splits;
+    const int items = p.max_tiles * splits, ctas = gridDim.x - 1;
 
+    if (blockIdx.x == ctas) {
+        pdl_wait();                                        // the workspace may still be in use
+        pdl_trigger();
+        make_plan(p, reinterpret_cast<int64_t*>(sm));
+        return;
+    }
     if (tid == 0) {
-        for (int i = 0; i < kRing; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
-        for (int i = 0; i < 2; ++i) { mbar_init(&acc_full[i], 1); mbar_init(&acc_empty[i], 256); }
-        mbar_init(done, 1);
-        *fail = 0;
-        *issued_s = 0;
+        for (int i = 0; i < kRing; ++i) { mbar_init(&sh->full[i], 1); mbar_init(&sh->empty[i], 1); }
+        for (int i = 0; i < 2; ++i) { mbar_init(&sh->acc_full[i], 1); mbar_init(&sh->acc_empty[i], 8); }
+        mbar_init(&sh->a_full, 8);
+        mbar_init(&sh->done, 1);
+        sh->fail = 0;
+        sh->issued = 0;
         fence_barrier_init();
     }
     if (warp == 9) {
-        tmem_alloc(tmem_slot, 256);
+        tmem_alloc(&sh->tmem, 256);
         tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = sh->tmem;
+    auto gave_up = [&]() { return *(volatile int*)&sh->fail != 0; };
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (gave_up()) return false;
+        if (dec::wait_bounded(bar, parity, p.status)) return true;
+        *(volatile int*)&sh->fail = 1;
+        return false;
+    };
     pdl_wait();
     pdl_trigger();
 
-    // the tile's sequence: the last one that starts at or before it and has tiles (uniform)
-    int b = 0;
-    {
-        int lo = 0, hi = p.B - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (p.seq[mid].y <= tile) lo = mid;
-            else hi = mid - 1;
-        }
-        b = lo;
-    }
-    const int4 seq = p.seq[b];
-    const int t0 = (tile - seq.y) * kTile;
-    const int tokens = min(kTile, seq.x - t0);
-    // tiles that no query of the step sees are left out
-    bool wanted = tile >= seq.y && tokens > 0 && seq.w > 0;
-    if (wanted && p.window > 0) {
-        const int lo = seq.x - seq.w + 1 - p.window;                    // the first query's window starts here
-        wanted = t0 < p.sinks || t0 + kTile > lo;
-    }
-    if (!wanted) {                                                      // uniform
-        __syncthreads();
-        if (warp == 9) tmem_dealloc(tmem, 256);
-        return;
-    }
-
-    if (warp < 8) {
-        // ---- gather: a warp's 16 tokens, their slots by its first 16 lanes ----
-        int64_t slot = -1;
-        const int tok = t0 + warp * 16 + lane;
-        if (lane < 16 && tok < seq.x) slot = slot_of(p.page_table, b, tok, p.page_size, p.max_pages, p.num_pages, p.status);
-        if (lane < 16) slots[warp * 16 + lane] = slot;
-        const int row_bytes = Q8 ? p.d_c + 2 * p.d_r : 2 * (p.d_c + p.d_r);
-        int hi = kNone, lo = kBad;                                      // largest and least exponent of the warp's tokens
-        constexpr int kAhead = 4;                                       // tokens in flight
-        const int per = p.d_c / 8;                                      // vectors of 8 latents a token
-#pragma unroll 1
-        for (int k0 = 0; k0 < 16; k0 += kAhead) {
-            uint4 raw[kAhead][2];
-            int64_t sl[kAhead];
-#pragma unroll
-            for (int k = 0; k < kAhead; ++k) {
-                sl[k] = __shfl_sync(0xffffffffu, slot, k0 + k);
-                const uint8_t* src = p.kv + (sl[k] < 0 ? 0 : sl[k]) * (int64_t)row_bytes;
-#pragma unroll
-                for (int v = 0; v < 2; ++v) {
-                    raw[k][v] = make_uint4(0, 0, 0, 0);
-                    const int c = lane + 32 * v;
-                    if (sl[k] >= 0 && c < per) {
-                        if constexpr (Q8) {
-                            const uint2 u = *reinterpret_cast<const uint2*>(src + c * 8);
-                            raw[k][v].x = u.x;
-                            raw[k][v].y = u.y;
-                        } else {
-                            raw[k][v] = *reinterpret_cast<const uint4*>(src + c * 16);
-                        }
-                    }
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < kAhead; ++k) {
-                float x[2][8];
-                float top = 0.f;
-                bool bad = false;
-#pragma unroll
-                for (int v = 0; v < 2; ++v) {
-                    const uint32_t w[4] = {raw[k][v].x, raw[k][v].y, raw[k][v].z, raw[k][v].w};
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        if constexpr (Q8) x[v][i] = e4m3_to_float((uint8_t)(w[i >> 2] >> (8 * (i & 3))));
-                        else x[v][i] = __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
-                        top = fmaxf(top, fabsf(x[v][i]));
-                        bad |= !isfinite(x[v][i]);
-                    }
-                }
-                top = warp_max(top);
-                bad = __any_sync(0xffffffffu, bad);
-                int e = top > 0.f ? ilogbf(top) : kNone;                // of the latent, or of its codes
-                int se = 0;
-                if (Q8 && sl[k] >= 0) {
-                    const float s = p.kv_scale[sl[k]];
-                    bad |= !isfinite(s);
-                    if (s == 0.f) e = kNone;
-                    else se = ilogbf(s);
-                    // a scale that is no power of two (none that this library writes): its mantissa goes into the codes
-                    const float m = s == 0.f ? 0.f : ldexpf(s, -se);
-                    if (m != 1.f) {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) x[i >> 3][i & 7] *= m;
-                        if (e != kNone) e = ilogbf(top * fabsf(m));
-                    }
-                }
-                const bool zero = bad || e == kNone;
-                const int row = warp * 16 + k0 + k;
-                const float f1 = zero ? 0.f : pow2i(-(e / 2)), f2 = zero ? 0.f : pow2i(-(e - e / 2));
-#pragma unroll
-                for (int v = 0; v < 2; ++v) {
-                    const int c = lane + 32 * v;
-                    if (c < per) {
-                        uint32_t h[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            h[i] = zero ? 0u : pack_f16(x[v][2 * i] * f1 * f2, x[v][2 * i + 1] * f1 * f2);
-                        *reinterpret_cast<uint4*>(sm + L.a + (c >> 3) * kBlock + sw128_offset(row, (c & 7) * 8)) = make_uint4(h[0], h[1], h[2], h[3]);
-                    }
-                }
-                const int et = bad ? kBad : e == kNone ? kNone : e + se;
-                if (lane == 0) exps[row] = et;
-                if (et != kBad && et != kNone) { hi = max(hi, et); lo = min(lo, et); }
-            }
-        }
-        if (lane == 0) { warp_hi[warp] = hi; warp_lo[warp] = lo; }
-        fence_proxy_async_smem();
-    }
-    __syncthreads();
-    int e_hi = kNone, e_lo = kBad;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) { e_hi = max(e_hi, warp_hi[i]); e_lo = min(e_lo, warp_lo[i]); }
-    // one exponent for the tile's values; bf16 where fp16 would not hold them beside one another
-    const bool bf = e_hi != kNone && (e_hi - e_lo > 12 || e_hi > kMaxE || e_hi < -kMaxE);
-    const int e_tile = e_hi == kNone ? 0 : min(max(e_hi, -kMaxE), kMaxE);
-    if (part == 0 && tid == 0) p.tinfo[tile] = (e_tile + 64) | (bf ? 256 : 0);
-
     if (warp == 8) {
         // ---- weights ----
-        const uint8_t* w = p.weights + kWeightTable + (size_t)n0 * kb * kBlock;
-        const int all = (n1 - n0) * kb;
         int i = 0;
-        for (; i < all; ++i) {
-            const int s = i % kRing;
-            if (i >= kRing && !dec::wait_bounded(&empty[s], ((i / kRing) - 1) & 1, p.status)) break;
-            if (*(volatile int*)fail) break;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(&full[s], kBlock);
-                bulk_load(sm + L.ring + s * kBlock, w + (size_t)i * kBlock, kBlock, &full[s]);
-            }
-            __syncwarp();
-        }
-        if (lane == 0) {
-            *(volatile int*)issued_s = i;
-            if (i < all) *(volatile int*)fail = 1;
-        }
-    } else if (warp == 9) {
-        // ---- products ----
-        const uint32_t idesc = idesc_bf16(128, 128, 0, 0) & ~((1u << 7) | (1u << 10));      // fp16 operands
-        int i = 0, n = n0;
         bool ok = true;
-        for (; n < n1 && ok; ++n) {
-            const int a = (n - n0) & 1;
-            if (n - n0 >= 2) ok = dec::wait_bounded(&acc_empty[a], (((n - n0) >> 1) - 1) & 1, p.status);
-            if (!ok) break;
-            tc_fence_after();
-            for (int k = 0; k < kb; ++k, ++i) {
+        for (int item = blockIdx.x; item < items && ok; item += ctas) {
+            if (!locate(p, item / splits).wanted) continue;
+            const int part = item % splits, n0 = nt * part / splits, n1 = nt * (part + 1) / splits;
+            const uint8_t* w = p.weights + kWeightTable + (size_t)n0 * kb * kBlock;
+            for (int q = 0; q < (n1 - n0) * kb; ++q, ++i) {
                 const int s = i % kRing;
-                if (!dec::wait_bounded(&full[s], (i / kRing) & 1, p.status)) { ok = false; break; }
-                tc_fence_after();
-                if (elect_one()) {
-                    const uint32_t A = smem_u32(sm + L.a + k * kBlock), Bw = smem_u32(sm + L.ring + s * kBlock);
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        mma_bf16(tmem + a * 128, smem_desc(A + kk * 32, 16, 1024, kSwizzle128B),
-                                 smem_desc(Bw + kk * 32, 16, 1024, kSwizzle128B), idesc, (k > 0 || kk > 0) ? 1u : 0u);
-                    mma_commit(&empty[s]);
-                    if (k == kb - 1) mma_commit(&acc_full[a]);
+                if (i >= kRing && !(ok = wait(&sh->empty[s], ((i / kRing) - 1) & 1))) break;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&sh->full[s], kBlock);
+                    bulk_load(ring + s * kBlock, w + (size_t)q * kBlock, kBlock, &sh->full[s]);
                 }
                 __syncwarp();
             }
         }
-        if (!ok && lane == 0) *(volatile int*)fail = 1;
-        if (elect_one()) mma_commit(done);
-        __syncwarp();
-    } else {
-        // ---- results: thread = token, its warp's half of the 128 columns (one 64-column block) ----
-        const int half = warp >> 2, row = 32 * (warp & 3) + lane;
-        const int et = exps[row];
-        const int64_t slot = slots[row];
-        const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
-        const int* we = reinterpret_cast<const int*>(p.weights);
-        uint8_t* stage = sm + L.stage + half * kBlock;
-        if (part == 0 && half == 0) {
-            // RoPE keys: 16-byte pieces of 8 values, a 128-byte row by 8 (or 4) lanes
-            const int row_bytes = Q8 ? p.d_c + 2 * p.d_r : 2 * (p.d_c + p.d_r);
-            const int pieces = p.d_r / 8;
-            for (int i = tid; i < kTile * pieces; i += 128) {
-                const int r = i / pieces, c = i % pieces;
-                const int64_t sl = slots[r];
-                uint32_t h[4] = {0, 0, 0, 0};
-                if (sl >= 0) {
-                    const uint4 u = *reinterpret_cast<const uint4*>(p.kv + sl * (int64_t)row_bytes + (Q8 ? p.d_c : 2 * p.d_c) + c * 16);
-                    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        if (lane == 0) *(volatile int*)&sh->issued = i;
+    } else if (warp == 9) {
+        // ---- products ----
+        const uint32_t idesc = idesc_bf16(128, 128, 0, 0) & ~((1u << 7) | (1u << 10));      // fp16 operands
+        int i = 0, n = 0, it = 0;                          // blocks, N-tiles and tiles so far
+        bool ok = true;
+        for (int item = blockIdx.x; item < items && ok; item += ctas) {
+            if (!locate(p, item / splits).wanted) continue;
+            const int part = item % splits, n0 = nt * part / splits, n1 = nt * (part + 1) / splits;
+            if (!(ok = wait(&sh->a_full, it & 1))) break;
+            ++it;
+            for (int q = n0; q < n1 && ok; ++q, ++n) {
+                const int a = n & 1;
+                if (n >= 2 && !(ok = wait(&sh->acc_empty[a], ((n >> 1) - 1) & 1))) break;
+                for (int k = 0; k < kb; ++k, ++i) {
+                    const int s = i % kRing;
+                    if (!(ok = wait(&sh->full[s], (i / kRing) & 1))) break;
+                    tc_fence_after();
+                    if (elect_one()) {
+                        const uint32_t A = smem_u32(sm + k * kBlock), Bw = smem_u32(ring + s * kBlock);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) h[k] = pack_f16(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u));
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_bf16(tmem + a * 128, smem_desc(A + kk * 32, 16, 1024, kSwizzle128B),
+                                     smem_desc(Bw + kk * 32, 16, 1024, kSwizzle128B), idesc, (k > 0 || kk > 0) ? 1u : 0u);
+                        mma_commit(&sh->empty[s]);
+                        if (k == kb - 1) mma_commit(&sh->acc_full[a]);
+                    }
+                    __syncwarp();
                 }
-                *reinterpret_cast<uint4*>(p.krope + (size_t)tile * kBlock + sw128_offset(r, c * 8)) = make_uint4(h[0], h[1], h[2], h[3]);
             }
         }
-        bool ok = true;                                                 // a thread that gave up still meets the barriers
-        for (int n = n0; n < n1; ++n) {
-            const int a = (n - n0) & 1;
-            if (ok && (*(volatile int*)fail || !dec::wait_bounded(&acc_full[a], ((n - n0) >> 1) & 1, p.status))) {
-                *(volatile int*)fail = 1;
-                ok = false;
-            }
-            ok = __all_sync(0xffffffffu, ok);                           // (the TMEM load is the warp's)
-            if (!ok) {
-                if (2 * n + half < blocks) {
-                    asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");
-                    asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");
+        if (elect_one()) mma_commit(&sh->done);
+        __syncwarp();
+    } else {
+        const int row_bytes = Q8 ? p.d_c + 2 * p.d_r : 2 * (p.d_c + p.d_r);
+        const int per = p.d_c / 8;                          // vectors of 8 latents a token
+        const int* we = reinterpret_cast<const int*>(p.weights);
+        int n = 0, it = 0;
+        bool ok = true;
+        for (int item = blockIdx.x; item < items && ok; item += ctas) {
+            const int tile = item / splits, part = item % splits;
+            const TileOf at = locate(p, tile);
+            if (!at.wanted) continue;
+            const int n0 = nt * part / splits, n1 = nt * (part + 1) / splits, buf = it & 1;
+            // ---- gather: a warp's 16 tokens, their slots by its first 16 lanes ----
+            auto slot_at = [&](int t) {
+                return t < at.len ? slot_of(p.page_table, at.b, t, p.page_size, p.max_pages, p.num_pages, p.status) : (int64_t)-1;
+            };
+            const int64_t slot = lane < 16 ? slot_at(at.t0 + warp * 16 + lane) : -1;
+            const int row = 32 * (warp & 3) + lane;          // this thread's token in the results
+            const int64_t row_slot = slot_at(at.t0 + row);
+            int hi = kNone, lo = kBad;                       // largest and least exponent of the warp's tokens
+            constexpr int kAhead = 8;                        // tokens in flight
+#pragma unroll 1
+            for (int k0 = 0; k0 < 16; k0 += kAhead) {
+                uint4 raw[kAhead][NV];
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) {
+                    const int64_t sl = __shfl_sync(0xffffffffu, slot, k0 + k);
+                    const uint8_t* src = p.kv + (sl < 0 ? 0 : sl) * (int64_t)row_bytes;
+#pragma unroll
+                    for (int v = 0; v < NV; ++v) {
+                        raw[k][v] = make_uint4(0, 0, 0, 0);
+                        const int c = lane + 32 * v;
+                        if (sl >= 0 && c < per) {
+                            if constexpr (Q8) {
+                                const uint2 u = *reinterpret_cast<const uint2*>(src + c * 8);
+                                raw[k][v].x = u.x;
+                                raw[k][v].y = u.y;
+                            } else {
+                                raw[k][v] = *reinterpret_cast<const uint4*>(src + c * 16);
+                            }
+                        }
+                    }
                 }
-                continue;
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) {
+                    const int64_t sl = __shfl_sync(0xffffffffu, slot, k0 + k);
+                    float x[NV][8];
+                    float top = 0.f;
+                    bool bad = false;
+#pragma unroll
+                    for (int v = 0; v < NV; ++v) {
+                        const uint32_t w[4] = {raw[k][v].x, raw[k][v].y, raw[k][v].z, raw[k][v].w};
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            if constexpr (Q8) x[v][i] = e4m3_to_float((uint8_t)(w[i >> 2] >> (8 * (i & 3))));
+                            else x[v][i] = __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
+                            top = fmaxf(top, fabsf(x[v][i]));
+                            bad |= !(fabsf(x[v][i]) <= 3.402823466e38f);
+                        }
+                    }
+                    top = warp_max(top);
+                    bad = __any_sync(0xffffffffu, bad);
+                    int e = top > 0.f ? ilogbf(top) : kNone;  // of the latent, or of its codes
+                    int se = 0;
+                    if (Q8 && sl >= 0) {
+                        const float s = p.kv_scale[sl];
+                        bad |= !isfinite(s);
+                        if (s == 0.f) e = kNone;
+                        else se = ilogbf(s);
+                        // a scale that is no power of two (none that this library writes): its mantissa goes into the codes
+                        const float m = s == 0.f ? 0.f : ldexpf(s, -se);
+                        if (m != 1.f) {
+#pragma unroll
+                            for (int i = 0; i < 8 * NV; ++i) x[i >> 3][i & 7] *= m;
+                            if (e != kNone) e = ilogbf(top * fabsf(m));
+                        }
+                    }
+                    const bool zero = bad || e == kNone;
+                    const int r = warp * 16 + k0 + k;
+                    const float f1 = zero ? 0.f : pow2i(-(e / 2)), f2 = zero ? 0.f : pow2i(-(e - e / 2));
+#pragma unroll
+                    for (int v = 0; v < NV; ++v) {
+                        const int c = lane + 32 * v;
+                        if (c < per) {
+                            uint32_t h[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) h[i] = zero ? 0u : pack_f16(x[v][2 * i] * f1 * f2, x[v][2 * i + 1] * f1 * f2);
+                            *reinterpret_cast<uint4*>(sm + (c >> 3) * kBlock + sw128_offset(r, (c & 7) * 8)) = make_uint4(h[0], h[1], h[2], h[3]);
+                        }
+                    }
+                    const int et = bad ? kBad : e == kNone ? kNone : e + se;
+                    if (lane == 0) sh->exps[buf][r] = et;
+                    if (et != kBad && et != kNone) { hi = max(hi, et); lo = min(lo, et); }
+                }
             }
-            tc_fence_after();
-            uint32_t v[64];
-            tmem_ld64(tmem + lane_base + a * 128 + half * 64, v);
-            tmem_wait_ld();
-            tc_fence_before();
-            mbar_arrive(&acc_empty[a]);
-            const int cb = 2 * n + half;
-            if (cb < blocks) {
+            if (part == 0) {
+                // RoPE keys of the warp's tokens: 16-byte pieces of 8 values, a row by 8 (or 4) lanes
+                const int pieces = p.d_r / 8;
+                for (int i = lane; i < 16 * pieces; i += 32) {
+                    const int k = i / pieces, c = i % pieces;
+                    const int64_t sl = __shfl_sync(0xffffffffu, slot, k);
+                    uint32_t h[4] = {0, 0, 0, 0};
+                    if (sl >= 0) {
+                        const uint4 u = *reinterpret_cast<const uint4*>(p.kv + sl * (int64_t)row_bytes + (Q8 ? p.d_c : 2 * p.d_c) + c * 16);
+                        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) h[q] = pack_f16(__uint_as_float(w[q] << 16), __uint_as_float(w[q] & 0xffff0000u));
+                    }
+                    *reinterpret_cast<uint4*>(p.krope + (size_t)tile * kBlock + sw128_offset(warp * 16 + k, c * 8)) = make_uint4(h[0], h[1], h[2], h[3]);
+                }
+            }
+            if (lane == 0) { sh->hi[buf][warp] = hi; sh->lo[buf][warp] = lo; }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh->a_full);
+            const int half = warp >> 2;
+            auto alpha_of = [&](int cb) {                    // of the key block's group
+                if (cb >= p.G * nkb || row_slot < 0) return 0.f;
+                const int64_t i = row_slot * p.G + cb / nkb;
+                return p.ak_f16 ? load_alpha<true>(p.ak, i) : load_alpha<false>(p.ak, i);
+            };
+            float al = alpha_of(2 * n0 + half);
+            ok = wait(&sh->a_full, it & 1);
+            ++it;
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            int e_hi = kNone, e_lo = kBad;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) { e_hi = max(e_hi, sh->hi[buf][i]); e_lo = min(e_lo, sh->lo[buf][i]); }
+            // one exponent for the tile's values; bf16 where fp16 would not hold them beside one another
+            const bool bf = e_hi != kNone && (e_hi - e_lo > 12 || e_hi > kMaxE || e_hi < -kMaxE);
+            const int e_tile = e_hi == kNone ? 0 : min(max(e_hi, -kMaxE), kMaxE);
+            if (part == 0 && tid == 0) p.tinfo[tile] = (e_tile + 64) | (bf ? 256 : 0);
+            // ---- results: thread = token, its warp's half of the 128 columns (one 64-column block) ----
+            const int et = sh->exps[buf][row];
+            const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
+            for (int q = n0; q < n1; ++q, ++n) {
+                const int a = n & 1, cb = 2 * q + half;
+                const float al_now = al;
+                if (q + 1 < n1) al = alpha_of(cb + 2);
+                ok = wait(&sh->acc_full[a], (n >> 1) & 1);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc_fence_after();
+                uint32_t v[64];
+                tmem_ld64(tmem + lane_base + a * 128 + half * 64, v);
+                tmem_wait_ld();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh->acc_empty[a]);
+                if (cb >= blocks) continue;
                 const bool key = cb < p.G * nkb;
                 float f;
                 uint8_t* dst;
-                bool as_bf = false;
                 if (key) {
-                    const int g = cb / nkb;
-                    float al = 0.f;
-                    if (slot >= 0) al = p.ak_f16 ? load_alpha<true>(p.ak, slot * p.G + g) : load_alpha<false>(p.ak, slot * p.G + g);
                     // NaN where the latent is not finite: rows that see the token become NaN, others do not
-                    f = et == kBad ? __int_as_float(0x7fc00000) : et == kNone ? 0.f : ldexpf(al, et + we[g]);
+                    f = et == kBad ? __int_as_float(0x7fc00000) : et == kNone ? 0.f : ldexpf(al_now, et + we[cb / nkb]);
                     dst = p.kc + ((size_t)tile * p.G * nkb + cb) * kBlock;
                 } else {
                     f = et == kBad || et == kNone ? 0.f : ldexpf(1.f, et - e_tile);
-                    as_bf = bf;
                     dst = p.v + ((size_t)tile * p.Gv * nvb + (cb - p.G * nkb)) * kBlock;
                 }
-                // the staging block is free once the last copy out of it has been read
-                if ((warp & 3) == 0 && lane == 0) dec::bulk_wait_read_all();
-                asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");
+                const bool as_bf = bf && !key;
+                dst += row * 128;
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    uint32_t h[4];
+                for (int c = 0; c < 4; ++c) {                // two neighbouring 16-byte pieces, in swizzled order
+                    uint32_t h[2][4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float x = __uint_as_float(v[8 * c + 2 * i]) * f, y = __uint_as_float(v[8 * c + 2 * i + 1]) * f;
-                        h[i] = as_bf ? pack_bf16(x, y) : pack_f16(x, y);
+                    for (int i = 0; i < 8; ++i) {
+                        const float x = __uint_as_float(v[16 * c + 2 * i]) * f, y = __uint_as_float(v[16 * c + 2 * i + 1]) * f;
+                        h[i >> 2][i & 3] = as_bf ? pack_bf16(x, y) : pack_f16(x, y);
                     }
-                    *reinterpret_cast<uint4*>(stage + sw128_offset(row, c * 8)) = make_uint4(h[0], h[1], h[2], h[3]);
-                }
-                fence_proxy_async_smem();
-                asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");
-                if ((warp & 3) == 0 && lane == 0) {
-                    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(reinterpret_cast<uint64_t>(dst)),
-                                 "r"(smem_u32(stage)), "r"(kBlock) : "memory");
-                    dec::bulk_commit_group();
+                    uint8_t* to = dst + ((c ^ ((row >> 1) & 3)) << 5);
+                    uint32_t u[4], w[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) { u[i] = row & 1 ? h[1][i] : h[0][i]; w[i] = row & 1 ? h[0][i] : h[1][i]; }
+                    st_global_v8(to, u, w);
                 }
             }
         }
-        if ((warp & 3) == 0 && lane == 0) dec::bulk_wait_all();
     }
     __syncthreads();
-    dec::wait_bounded(done, 0, p.status);
-    if (*(volatile int*)fail && tid == 0) {
-        const int issued = *(volatile int*)issued_s;
-        for (int j = max(0, issued - kRing); j < issued; ++j) dec::wait_bounded(&full[j % kRing], (j / kRing) & 1, p.status);
+    dec::wait_bounded(&sh->done, 0, p.status);
+    if (gave_up() && tid == 0) {
+        const int issued = *(volatile int*)&sh->issued;
+        for (int j = max(0, issued - kRing); j < issued; ++j) dec::wait_bounded(&sh->full[j % kRing], (j / kRing) & 1, p.status);
     }
     tc_fence_before();
     __syncthreads();
@@ -604,34 +513,24 @@ __global__ void __launch_bounds__(kThreadsE, 1) prefill_expand_kernel(const Para
     }
 }
 
-template <typename T>
-int launch_query_type(const Params& p, cudaStream_t s) {
-    const int64_t items = (int64_t)p.rows * p.H, per = kThreadsQ / 32 * kRowsWarp;
-    const dim3 grid((unsigned)((items + per - 1) / per + 1)), block(kThreadsQ);
-    cudaError_t e;
-    if (p.d_h == 128) e = p.d_r == 64 ? launch_pdl(prefill_query_kernel<T, 128, 64>, grid, block, 0, s, p)
-                                      : launch_pdl(prefill_query_kernel<T, 128, 32>, grid, block, 0, s, p);
-    else e = p.d_r == 64 ? launch_pdl(prefill_query_kernel<T, 64, 64>, grid, block, 0, s, p)
-                         : launch_pdl(prefill_query_kernel<T, 64, 32>, grid, block, 0, s, p);
-    return e == cudaSuccess ? QKMLA_OK : QKMLA_ERR_CUDA;
+template <bool Q8, int NV>
+int launch_expand_as(const Params& p, cudaStream_t s) {
+    auto k = prefill_expand_kernel<Q8, NV>;
+    const int bytes = expand_bytes(p.d_c), sms = device_sm_count() * (NV == 1 ? 2 : 1);
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return QKMLA_ERR_CUDA;
+    // few tiles: their columns are cut over several CTAs
+    const int nt = n_tiles(p.G, p.Gv, p.d_h, p.d_v);
+    const int splits = max(1, min(nt, sms / p.max_tiles));
+    if ((int64_t)p.max_tiles * splits > INT32_MAX) return QKMLA_ERR_UNSUPPORTED;
+    const int ctas = min(p.max_tiles * splits, sms);
+    return launch_pdl(k, dim3((unsigned)(ctas + 1)), dim3(kThreadsE), bytes, s, p, splits) == cudaSuccess ? QKMLA_OK : QKMLA_ERR_CUDA;
 }
 
 }  // namespace
 
-int launch_query(const Params& p, bool q_bf16, cudaStream_t s) {
-    return q_bf16 ? launch_query_type<__nv_bfloat16>(p, s) : launch_query_type<float>(p, s);
-}
-
 int launch_expand(const Params& p, bool q8, cudaStream_t s) {
-    const ExpandLayout L(p.d_c);
-    auto k = q8 ? prefill_expand_kernel<true> : prefill_expand_kernel<false>;
-    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, L.bytes) != cudaSuccess) return QKMLA_ERR_CUDA;
-    // few tiles: their columns are cut over several CTAs
-    const int nt = n_tiles(p.G, p.Gv, p.d_h, p.d_v);
-    const int splits = max(1, min(nt, device_sm_count() / max(1, p.max_tiles)));
-    if ((int64_t)p.max_tiles * splits > INT32_MAX) return QKMLA_ERR_UNSUPPORTED;
-    return launch_pdl(k, dim3((unsigned)(p.max_tiles * splits)), dim3(kThreadsE), L.bytes, s, p, splits) == cudaSuccess ? QKMLA_OK
-                                                                                                                      : QKMLA_ERR_CUDA;
+    if (p.d_c <= 256) return q8 ? launch_expand_as<true, 1>(p, s) : launch_expand_as<false, 1>(p, s);
+    return q8 ? launch_expand_as<true, 2>(p, s) : launch_expand_as<false, 2>(p, s);
 }
 
 }  // namespace pf
