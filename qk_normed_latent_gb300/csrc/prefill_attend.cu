@@ -54,22 +54,24 @@ struct Piece {
     int row0;                              // first row in q and o
 };
 
-struct __align__(8) Shared {
+struct __align__(16) Shared {
     uint64_t full[kGroups], empty[kGroups];
     uint64_t q_full[2], q_empty[2], q0_full[2];
     uint64_t s_full[2], pa_full[2], pb_full[2], o_full[2];
     uint64_t piece_full[2], piece_empty[2], conv_full[2];
     uint64_t done;
     Piece piece[2];
+    int info[4];                           // tinfo of the last token tiles whose keys were issued
     uint32_t tmem;
     int fail;
     int issued;                            // groups whose copies were issued
     int q_issued[2];                       // query halves whose copies were issued
+    alignas(16) float gain[192];           // gamma_q gamma_k, then gamma_rope_q
 };
-static_assert(sizeof(Shared) <= 1024, "beside the blocks");
+static_assert(sizeof(Shared) <= 2048, "beside the blocks");
 
 template <int DH>
-constexpr int smem_bytes() { return (2 * (DH / 64 + 1) + kUnits) * kBlock + 1024 + 1024; }
+constexpr int smem_bytes() { return (2 * (DH / 64 + 1) + kUnits) * kBlock + 1024 + 2048; }
 
 // One CTA's part of the list.
 struct Walk {
@@ -115,15 +117,17 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return y;
 }
 
-// Named barriers cannot be used where a thread may have given up; every wait below ends by itself.
+// Every wait ends by itself: in success, because another warp gave up, or after kWaitNs.  (Named barriers cannot be
+// used where a thread may have given up.)
 __device__ __forceinline__ bool wait_or_fail(uint64_t* bar, uint32_t parity, Shared* sh, int* status) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = dec::globaltimer();
+    uint64_t t0 = 0;
     for (uint32_t i = 1;; ++i) {
         if (mbar_try_wait(bar, parity)) return true;
         if ((i & 63u) == 0) {
             if (*(volatile int*)&sh->fail) return false;
-            if (dec::globaltimer() - t0 > dec::kWaitNs) {
+            const uint64_t t = dec::globaltimer();
+            if (t0 == 0) t0 = t;
+            if (t - t0 > dec::kWaitNs) {
                 report(status, QKMLA_ERR_TIMEOUT);
                 *(volatile int*)&sh->fail = 1;
                 return false;
@@ -131,7 +135,6 @@ __device__ __forceinline__ bool wait_or_fail(uint64_t* bar, uint32_t parity, Sha
         }
     }
 }
-
 // ---- queries ----
 // Four rows of a query tile, rt .. rt + 3, eight lanes a row: normalised, with the gains, times a power of two that
 // brings the row's largest value into [1, 2), as fp16 to row rt & 127 of the half at `dst` (blocks of 64 columns).
@@ -165,24 +168,13 @@ struct QueryRow {
         for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
         return s;
     }
-    __device__ __forceinline__ float scale(float a, const float* g1, const float* g2, int sub) {
+    __device__ __forceinline__ float scale(float a, const float* gain, int sub) {
         float top = 0.f;
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-            float g[4] = {1.f, 1.f, 1.f, 1.f};
-            if (g1) {
-                const float4 f = __ldg(reinterpret_cast<const float4*>(g1) + j * 8 + sub);
-                g[0] = f.x; g[1] = f.y; g[2] = f.z; g[3] = f.w;
-            }
-            if (g2) {
-                const float4 f = __ldg(reinterpret_cast<const float4*>(g2) + j * 8 + sub);
-                g[0] *= f.x; g[1] *= f.y; g[2] *= f.z; g[3] *= f.w;
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                v[j][i] *= a * g[i];
-                top = fmaxf(top, fabsf(v[j][i]));
-            }
+            const float4 g = *reinterpret_cast<const float4*>(gain + (j * 8 + sub) * 4);
+            v[j][0] *= a * g.x; v[j][1] *= a * g.y; v[j][2] *= a * g.z; v[j][3] *= a * g.w;
+            top = max3(max3(top, fabsf(v[j][0]), fabsf(v[j][1])), fabsf(v[j][2]), fabsf(v[j][3]));
         }
         return top;
     }
@@ -197,28 +189,32 @@ struct QueryRow {
 };
 
 template <int DH, int DR>
-__device__ __forceinline__ float query_rows(const Params& p, const Piece& s, int rt, uint8_t* dst, int lane) {
-    const int sub = lane & 7;
-    rt += lane >> 3;
-    const int i = rt >> p.hp_log;
-    const bool there = i < s.queries;
-    const int64_t row = s.row0 + (there ? i : 0), head = (int64_t)s.unit * p.hp + (rt & (p.hp - 1));
+struct QueryRows {
     QueryRow<DH / 32> x;
     QueryRow<DR / 32> y;
-    x.load(p.q, row * p.q_row + head * p.q_head, p.q_bf16, sub);
-    y.load(p.q_rope, row * p.qr_row + head * p.qr_head, p.q_bf16, sub);
-    const float ax = rsqrtf(x.squares() / DH + p.eps), ay = rsqrtf(y.squares() / DR + p.eps);
-    float top = fmaxf(x.scale(ax, p.gamma_q, p.gamma_k, sub), y.scale(ay, p.gamma_rope, nullptr, sub));
+    __device__ __forceinline__ void load(const Params& p, const Piece& s, int rt, int lane) {
+        rt += lane >> 3;
+        const int i = rt >> p.hp_log;
+        const int64_t row = s.row0 + (i < s.queries ? i : 0), head = (int64_t)s.unit * p.hp + (rt & (p.hp - 1));
+        x.load(p.q, row * p.q_row + head * p.q_head, p.q_bf16, lane & 7);
+        y.load(p.q_rope, row * p.qr_row + head * p.qr_head, p.q_bf16, lane & 7);
+    }
+    __device__ __forceinline__ float finish(const Params& p, const float* gain, int rt, uint8_t* dst, int lane) {
+        const int sub = lane & 7;
+        rt += lane >> 3;
+        const float ax = rsqrtf(x.squares() / DH + p.eps), ay = rsqrtf(y.squares() / DR + p.eps);
+        float top = fmaxf(x.scale(ax, gain, sub), y.scale(ay, gain + DH, sub));
 #pragma unroll
-    for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    // the exponent of a normal number; 0 for zero, infinity and NaN
-    const int bits = __float_as_int(top) >> 23;
-    const int e = bits > 0 && bits < 255 ? min(max(bits - 127, -100), 100) : 0;
-    const float f = pow2i(-e);
-    x.store(dst, rt & 127, f, sub);
-    y.store(dst + DH / 64 * kBlock, rt & 127, f, sub);
-    return p.scale_log2 * pow2i(e);
-}
+        for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        // the exponent of a normal number; 0 for zero, infinity and NaN
+        const int bits = __float_as_int(top) >> 23;
+        const int e = bits > 0 && bits < 255 ? min(max(bits - 127, -100), 100) : 0;
+        const float f = pow2i(-e);
+        x.store(dst, rt & 127, f, sub);
+        y.store(dst + DH / 64 * kBlock, rt & 127, f, sub);
+        return p.scale_log2 * pow2i(e);
+    }
+};
 
 // ---- softmax of a tile's row: weights in place of logits ----
 // Two 64-token halves, each signalled as soon as it lies in TMEM.  Returns the sum of the unrounded weights.
@@ -285,6 +281,8 @@ __global__ void __launch_bounds__(kThreadsA, 1) prefill_attend_kernel(const __gr
         tmem_alloc(&sh->tmem, 512);
         tmem_relinquish();
     }
+    for (int i = tid; i < DH + DR; i += kThreadsA)
+        sh->gain[i] = i < DH ? p.gamma_q[i] * p.gamma_k[i] : p.gamma_rope ? p.gamma_rope[i - DH] : 1.f;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -303,7 +301,7 @@ __global__ void __launch_bounds__(kThreadsA, 1) prefill_attend_kernel(const __gr
         if (lane == 0) {
             int group = 0, unit = 0;                       // issued so far
             int freed = 0, freed_units = 0;
-            uint32_t qe_phase[2] = {0, 0};
+            uint32_t qe_phase = 0;                         // bit h
             int last_halves = 0;                           // of the last piece with tiles
             bool ok = true;
             auto put = [&](const uint8_t* a, int na, const uint8_t* b2, int nb) {      // a group: na blocks at a, nb at b2
@@ -330,16 +328,21 @@ __global__ void __launch_bounds__(kThreadsA, 1) prefill_attend_kernel(const __gr
                 if (s.unit < 0) break;
                 const int g = (int)((int64_t)s.unit * p.G / p.units), gv = (int)((int64_t)s.unit * p.Gv / p.units);
                 const int halves = s.queries * p.hp > 128 ? 2 : 1;
+                auto tile_at = [&](int t) { return (size_t)s.tile0 + (t < s.head ? t : t + s.gap); };
+                int info = s.t0 < s.t1 ? p.tinfo[tile_at(s.t0)] : 0;
+                // (through shared memory: a load from L2 in the loop of the products or of the softmax would be waited for there)
                 auto key = [&](int t) {
-                    const size_t tile = (size_t)s.tile0 + (t < s.head ? t : t + s.gap);
+                    const size_t tile = tile_at(t);
+                    sh->info[(group >> 1) & 3] = info;
+                    if (t + 1 < s.t1) info = p.tinfo[tile_at(t + 1)];
                     put(p.kc + (tile * p.G + g) * (size_t)((KU - 1) * kBlock), KU - 1, p.krope + tile * kBlock, 1);
                 };
                 if (s.t0 < s.t1) key(s.t0);
                 // a query half is read by the products until the last ones of the piece ahead have ended
                 for (int h = 0; h < 2 && ok; ++h) {
                     if (h < last_halves) {
-                        ok = wait_or_fail(&sh->q_empty[h], qe_phase[h], sh, p.status);
-                        qe_phase[h] ^= 1;
+                        ok = wait_or_fail(&sh->q_empty[h], (qe_phase >> h) & 1, sh, p.status);
+                        qe_phase ^= 1u << h;
                     }
                     if (!ok || s.t0 == s.t1 || h >= halves || k == 0) continue;       // (the first piece's rows go to shared memory directly)
                     if (h == 0) ok = wait_or_fail(&sh->conv_full[k & 1], ((k - 1) >> 1) & 1, sh, p.status);
@@ -352,7 +355,7 @@ __global__ void __launch_bounds__(kThreadsA, 1) prefill_attend_kernel(const __gr
                 if (s.t0 < s.t1) last_halves = halves;
                 else if (last_halves) last_halves = 0;
                 for (int t = s.t0; t < s.t1 && ok; ++t) {
-                    const size_t tile = (size_t)s.tile0 + (t < s.head ? t : t + s.gap);
+                    const size_t tile = tile_at(t);
                     put(p.v + (tile * p.Gv + gv) * (size_t)(VU * kBlock), VU, nullptr, 0);
                     if (t + 1 < s.t1) key(t + 1);
                 }
@@ -361,144 +364,157 @@ __global__ void __launch_bounds__(kThreadsA, 1) prefill_attend_kernel(const __gr
         __syncwarp();
       } else if (warp == 9) {
         // ---- products ----
+        if (elect_one()) {
         constexpr uint32_t bf = (1u << 7) | (1u << 10);
-        const uint32_t id_s = idesc_bf16(128, 128, 0, 0) & ~bf;
-        const uint32_t id_o = idesc_bf16(128, DV, 0, 1) & ~bf;
-        const uint32_t id_o64 = idesc_bf16(128, 64, 0, 1) & ~bf;
-        int group = 0, unit = 0, k = 0;
-        uint32_t p_phase[2] = {0, 0}, q_phase[2] = {0, 0};
-        bool ok = true;
-        auto block_at = [&](int u) { return smem_u32(ring + (u % kUnits) * kBlock); };
-        // S of half h from the key blocks at `u`
-        auto qk = [&](int h, int u) {
-            const uint32_t q = smem_u32(sm + h * kHalf);
-            if (elect_one()) {
-#pragma unroll
-                for (int blk = 0; blk < KU; ++blk) {
-                    const uint32_t kb = block_at(u + blk);
-                    const int steps = blk < KU - 1 ? 4 : DR / 16;
-#pragma unroll
-                    for (int kk = 0; kk < steps; ++kk)
-                        mma_bf16(tmem + kS + h * 128, smem_desc(q + blk * kBlock + kk * 32, 16, 1024, kSwizzle128B),
-                                 smem_desc(kb + kk * 32, 16, 1024, kSwizzle128B), id_s, (blk > 0 || kk > 0) ? 1u : 0u);
-                }
-                mma_commit(&sh->s_full[h]);
-            }
-            __syncwarp();
-        };
-        // half (0 or 1) of the tokens of O += P V
-        auto pv = [&](int h, int u, bool as_bf, bool acc, int part) {
-            const uint32_t v0 = block_at(u), v1 = block_at(u + VU - 1);
-            const uint32_t fmt = as_bf ? bf : 0u;
-            const uint32_t o = tmem + kO + h * 128, a = tmem + kS + h * 128;
-            if (elect_one()) {
-                if (VU == 1 || v1 > v0) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int kk = part * 4 + i;
-                        mma_bf16_tmem_a(o, a + kk * 8, smem_desc(v0 + kk * 2048, kBlock, 1024, kSwizzle128B), id_o | fmt, (acc || kk > 0) ? 1u : 0u);
-                    }
-                } else {
-                    // the value blocks wrap around the ring's end: 64 columns at a time
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int kk = part * 4 + i;
-                        mma_bf16_tmem_a(o, a + kk * 8, smem_desc(v0 + kk * 2048, kBlock, 1024, kSwizzle128B), id_o64 | fmt, (acc || kk > 0) ? 1u : 0u);
-                        mma_bf16_tmem_a(o + 64, a + kk * 8, smem_desc(v1 + kk * 2048, kBlock, 1024, kSwizzle128B), id_o64 | fmt, (acc || kk > 0) ? 1u : 0u);
-                    }
-                }
-            }
-            __syncwarp();
-        };
-        auto wait_group = [&](int g) { return wait_or_fail(&sh->full[g % kGroups], (g / kGroups) & 1, sh, p.status); };
-        auto commit = [&](uint64_t* bar) {
-            if (elect_one()) mma_commit(bar);
-            __syncwarp();
-        };
-        // The next piece with tiles, from the queue; halves 0 at the end.
-        struct Next { int n, halves, k, tile0, t0, head, gap; };
-        auto fetch = [&]() {
-            Next x{};
-            for (;; ++k) {
-                if (!(ok = wait_or_fail(&sh->piece_full[k & 1], (k >> 1) & 1, sh, p.status))) return x;
-                const Piece s = sh->piece[k & 1];
-                __syncwarp();
-                if (s.unit < 0) return x;
-                if (lane == 0) mbar_arrive(&sh->piece_empty[k & 1]);
-                if (s.t0 == s.t1) continue;
-                x = Next{s.t1 - s.t0, s.queries * p.hp > 128 ? 2 : 1, k, s.tile0, s.t0, s.head, s.gap};
+        constexpr uint32_t id_s = idesc_bf16(128, 128, 0, 0) & ~bf;
+        constexpr uint32_t id_o = idesc_bf16(128, DV, 0, 1) & ~bf;
+        // descriptors are formed once and moved by offsets: the issue has to keep up with 65 cycles a product
+        constexpr uint32_t kStep = kBlock >> 4;
+        const uint64_t q_desc = smem_desc(smem_u32(sm), 16, 1024, kSwizzle128B);
+        const uint64_t k_desc = smem_desc(smem_u32(ring), 16, 1024, kSwizzle128B);
+        const uint64_t v_desc = smem_desc(smem_u32(ring), kBlock / 2, 1024, kSwizzle128B);   // 64 tokens, 64-column boxes 8 KB apart
+        int group = 0, unit = 0, k = 0;                    // groups and blocks consumed, pieces fetched
+        uint32_t p_phase = 0, q_phase = 0;                 // bit h (arrays would lie in local memory)
+        int halves = 0, left = 0, q_at = 0;                // of the piece whose logits come next: tiles left, its place in the queue
+        int cur = 0;                                       // halves whose weights are awaited
+        bool cur_first = false, cur_last = false;
+        bool seen_a = false, seen_v = false, seen_1 = false;   // barriers of the next round found complete ahead of it
+        // A round: for each half, O += P V of the tile whose weights are awaited, then S of the next tile (of the
+        // same piece or of the next one).
+        for (;;) {
+            bool first = false;
+            // the next piece (halves -1: there is none); with weights awaited no more than one, which may have no tiles:
+            // the one behind it is not listed before they have been used
+            while (left == 0 && halves >= 0) {
+                if (!wait_or_fail(&sh->piece_full[k & 1], (k >> 1) & 1, sh, p.status)) goto give_up;
+                const Piece& s = sh->piece[k & 1];
+                if (s.unit < 0) { halves = -1; break; }
+                left = s.t1 - s.t0;
+                halves = s.queries * p.hp > 128 ? 2 : 1;
+                first = true;
+                q_at = k;
+                mbar_arrive(&sh->piece_empty[k & 1]);
                 ++k;
-                return x;
+                if (cur > 0) break;
             }
-        };
-        auto wait_query = [&](const Next& x, int h) {
-            if (x.k == 0) return wait_or_fail(&sh->q0_full[h], 0, sh, p.status);
-            const bool r = wait_or_fail(&sh->q_full[h], q_phase[h], sh, p.status);
-            q_phase[h] ^= 1;
-            return r;
-        };
-        Next cur = fetch(), nxt{};
-        // the first tile's logits
-        if (ok && cur.halves) {
-            ok = wait_group(group);
-            for (int h = 0; h < cur.halves && ok; ++h) {
-                if (!(ok = wait_query(cur, h))) break;
-                tc_fence_after();
-                qk(h, unit);
-                if (cur.n == 1) commit(&sh->q_empty[h]);
-            }
-            if (ok) commit(&sh->empty[group % kGroups]);
-            ++group;
-            unit += KU;
-        }
-        while (ok && cur.halves) {
-            int info = p.tinfo[cur.tile0 + (cur.t0 < cur.head ? cur.t0 : cur.t0 + cur.gap)];
-            for (int j = 0; j < cur.n && ok; ++j) {
-                const int vu = unit, ku = unit + VU, gv = group, gk = group + 1;
-                const bool as_bf = (info & 256) != 0, more = j + 1 < cur.n;
-                if (more) {
-                    const int t = cur.t0 + j + 1;
-                    info = p.tinfo[cur.tile0 + (t < cur.head ? t : t + cur.gap)];
+            const int nxt = left > 0 ? halves : 0;
+            if (cur == 0 && nxt == 0) break;
+            const int gv = group, gk = group + (cur > 0 ? 1 : 0);
+            const bool as_bf = (sh->info[(gv >> 1) & 3] & 256) != 0;
+            const uint32_t fmt = as_bf ? bf : 0u;
+            if (cur == 2 && nxt == 2 && !first) {
+                // The same round in a straight line, each barrier looked at while the products ahead of its use are still
+                // being taken (the unit takes six or so ahead; a wait that succeeds at once would cost as much as two).
+                const uint64_t v0 = v_desc + (uint64_t)((unit % kUnits) * kStep), v1 = VU == 2 ? v_desc + (uint64_t)(((unit + 1) % kUnits) * kStep) : v0 + kStep / 2;
+                uint64_t kd[KU];
+#pragma unroll
+                for (int blk = 0; blk < KU; ++blk) kd[blk] = k_desc + (uint64_t)(((unit + VU + blk) % kUnits) * kStep);
+                const uint32_t acc = cur_first ? 0u : 1u;
+                const int next_gv = gk + 1;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t ph = (p_phase >> h) & 1;
+                    const uint32_t o = tmem + kO + h * 128, a = tmem + kS + h * 128;
+                    if (!(h == 0 ? seen_a : seen_1) && !wait_or_fail(&sh->pa_full[h], ph, sh, p.status)) goto give_up;
+                    if (h == 0 && !seen_v && !wait_or_fail(&sh->full[gv % kGroups], (gv / kGroups) & 1, sh, p.status)) goto give_up;
+                    tc_fence_after();
+                    mma_bf16_tmem_a(o, a, v0, id_o | fmt, acc);
+                    mma_bf16_tmem_a(o, a + 8, v0 + 128, id_o | fmt, 1u);
+                    const bool seen_b = mbar_test_wait(&sh->pb_full[h], ph);
+                    mma_bf16_tmem_a(o, a + 16, v0 + 256, id_o | fmt, 1u);
+                    mma_bf16_tmem_a(o, a + 24, v0 + 384, id_o | fmt, 1u);
+                    if (!seen_b && !wait_or_fail(&sh->pb_full[h], ph, sh, p.status)) goto give_up;
+                    tc_fence_after();
+                    mma_bf16_tmem_a(o, a + 32, v1, id_o | fmt, 1u);
+                    mma_bf16_tmem_a(o, a + 40, v1 + 128, id_o | fmt, 1u);
+                    bool seen_k = true;
+                    if (h == 0) seen_k = mbar_test_wait(&sh->full[gk % kGroups], (gk / kGroups) & 1);
+                    mma_bf16_tmem_a(o, a + 48, v1 + 256, id_o | fmt, 1u);
+                    mma_bf16_tmem_a(o, a + 56, v1 + 384, id_o | fmt, 1u);
+                    if (h == 1) mma_commit(&sh->empty[gv % kGroups]);
+                    if (!seen_k && !wait_or_fail(&sh->full[gk % kGroups], (gk / kGroups) & 1, sh, p.status)) goto give_up;
+                    const uint32_t d = tmem + kS + h * 128;
+#pragma unroll
+                    for (int blk = 0; blk < KU; ++blk) {
+                        if (blk == KU - 1) {                // one more block of products to come
+                            if (h == 0) {
+                                seen_1 = mbar_test_wait(&sh->pa_full[1], (p_phase >> 1) & 1);
+                            } else {
+                                seen_a = mbar_test_wait(&sh->pa_full[0], (p_phase ^ 1) & 1);
+                                seen_v = mbar_test_wait(&sh->full[next_gv % kGroups], (next_gv / kGroups) & 1);
+                            }
+                        }
+#pragma unroll
+                        for (int kk = 0; kk < (blk < KU - 1 ? 4 : DR / 16); ++kk)
+                            mma_bf16(d, q_desc + (uint64_t)((h * KU + blk) * kStep + kk * 2), kd[blk] + (uint64_t)(kk * 2), id_s, (blk > 0 || kk > 0) ? 1u : 0u);
+                    }
+                    mma_commit(&sh->s_full[h]);
+                    if (left == 1) mma_commit(&sh->q_empty[h]);
                 }
-                int follow = cur.halves;                   // halves that have a product S to come
-                for (int h = 0; h < cur.halves; ++h) {
-                    if (!(ok = wait_or_fail(&sh->pa_full[h], p_phase[h], sh, p.status))) break;
-                    if (h == 0 && !(ok = wait_group(gv))) break;
-                    tc_fence_after();
-                    pv(h, vu, as_bf, j > 0, 0);
-                    if (!(ok = wait_or_fail(&sh->pb_full[h], p_phase[h], sh, p.status))) break;
-                    p_phase[h] ^= 1;
-                    tc_fence_after();
-                    pv(h, vu, as_bf, true, 1);
-                    if (h == cur.halves - 1) commit(&sh->empty[gv % kGroups]);
-                    if (!more) {
-                        commit(&sh->o_full[h]);
-                        if (h == 0) {
-                            nxt = fetch();
-                            if (!ok) break;
-                            follow = nxt.halves;
+                mma_commit(&sh->empty[gk % kGroups]);
+                p_phase ^= 3;
+                group = next_gv;
+                unit += VU + KU;
+                cur_first = false;
+                cur_last = left == 1;
+                --left;
+                continue;
+            }
+            seen_a = seen_v = false;
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {
+                if (h < cur) {
+                    const uint32_t o = tmem + kO + h * 128, a = tmem + kS + h * 128;
+#pragma unroll 1
+                    for (int part = 0; part < 2; ++part) { // 64 tokens each
+                        if (!wait_or_fail(part ? &sh->pb_full[h] : &sh->pa_full[h], (p_phase >> h) & 1, sh, p.status)) goto give_up;
+                        if (h + part == 0 && !wait_or_fail(&sh->full[gv % kGroups], (gv / kGroups) & 1, sh, p.status)) goto give_up;
+                        tc_fence_after();
+                        const uint64_t v = v_desc + (uint64_t)(VU == 2 ? ((unit + part) % kUnits) * kStep : (unit % kUnits) * kStep + part * (kStep / 2));
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            mma_bf16_tmem_a(o, a + part * 32 + i * 8, v + (uint64_t)(i * 128), id_o | fmt, (!cur_first || part > 0 || i > 0) ? 1u : 0u);
+                    }
+                    p_phase ^= 1u << h;
+                    if (h == cur - 1) mma_commit(&sh->empty[gv % kGroups]);
+                    if (cur_last) mma_commit(&sh->o_full[h]);
+                }
+                if (h < nxt) {
+                    if (h == 0 && !wait_or_fail(&sh->full[gk % kGroups], (gk / kGroups) & 1, sh, p.status)) goto give_up;
+                    if (first) {
+                        if (q_at == 0) {
+                            if (!wait_or_fail(&sh->q0_full[h], 0, sh, p.status)) goto give_up;
+                        } else {
+                            if (!wait_or_fail(&sh->q_full[h], (q_phase >> h) & 1, sh, p.status)) goto give_up;
+                            q_phase ^= 1u << h;
                         }
                     }
-                    // the next tile's logits: this piece's, or the next piece's first
-                    const int upto = !more && h == cur.halves - 1 ? follow : min(h + 1, follow);
-                    for (int g = h; g < upto && ok; ++g) {
-                        if (g == 0 && !(ok = wait_group(gk))) break;
-                        if (!more && !(ok = wait_query(nxt, g))) break;
-                        tc_fence_after();
-                        qk(g, ku);
-                        if (more ? j + 2 == cur.n : nxt.n == 1) commit(&sh->q_empty[g]);
-                        if (g == follow - 1) commit(&sh->empty[gk % kGroups]);
+                    tc_fence_after();
+                    const int u = unit + (cur > 0 ? VU : 0);
+                    const uint32_t d = tmem + kS + h * 128;
+#pragma unroll
+                    for (int blk = 0; blk < KU; ++blk) {
+                        const uint64_t kd = k_desc + (uint64_t)(((u + blk) % kUnits) * kStep), qd = q_desc + (uint64_t)((h * KU + blk) * kStep);
+#pragma unroll
+                        for (int kk = 0; kk < (blk < KU - 1 ? 4 : DR / 16); ++kk)
+                            mma_bf16(d, qd + (uint64_t)(kk * 2), kd + (uint64_t)(kk * 2), id_s, (blk > 0 || kk > 0) ? 1u : 0u);
                     }
-                    if (!ok) break;
+                    mma_commit(&sh->s_full[h]);
+                    if (left == 1) mma_commit(&sh->q_empty[h]);
+                    if (h == nxt - 1) mma_commit(&sh->empty[gk % kGroups]);
                 }
-                const bool went = more || nxt.halves > 0;
-                group += went ? 2 : 1;
-                unit += VU + (went ? KU : 0);
             }
+            group = gk + (nxt > 0 ? 1 : 0);
+            unit += (cur > 0 ? VU : 0) + (nxt > 0 ? KU : 0);
             cur = nxt;
-            nxt = Next{};
+            cur_first = first;
+            cur_last = left == 1;
+            left -= nxt > 0 ? 1 : 0;
         }
-        commit(&sh->done);
+give_up:
+        mma_commit(&sh->done);
+        }
+        __syncwarp();
       } else {
         // ---- the list, and the queries of every piece but the first ----
         Walk walk;
@@ -509,6 +525,17 @@ __global__ void __launch_bounds__(kThreadsA, 1) prefill_attend_kernel(const __gr
         for (int k = 0;; ++k) {
             Piece s;
             if (!walk.next(p, s)) s.unit = -1;
+            if (k > 0 && s.unit >= 0 && s.t0 < s.t1) {
+                // the raw rows into L2: reading them then takes its latency
+                const int row_bytes = p.q_bf16 ? 2 * DH : 4 * DH, rope_bytes = p.q_bf16 ? 2 * DR : 4 * DR, esz = p.q_bf16 ? 2 : 4;
+                for (int rt = (warp - 10) * 32 + lane; rt < min(s.queries * p.hp, kRowsQ); rt += 64) {
+                    const int64_t row = s.row0 + (rt >> p.hp_log), head = (int64_t)s.unit * p.hp + (rt & (p.hp - 1));
+                    const char* x = (const char*)p.q + (row * p.q_row + head * p.q_head) * esz;
+                    const char* y = (const char*)p.q_rope + (row * p.qr_row + head * p.qr_head) * esz;
+                    for (int i = 0; i < row_bytes; i += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(x + i));
+                    for (int i = 0; i < rope_bytes; i += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(y + i));
+                }
+            }
             if (k >= 2) ok = wait_or_fail(&sh->piece_empty[k & 1], ((k >> 1) - 1) & 1, sh, p.status);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
@@ -522,9 +549,15 @@ __global__ void __launch_bounds__(kThreadsA, 1) prefill_attend_kernel(const __gr
                 const int rows = min(s.queries * p.hp, kRowsQ);
                 const size_t buf = 2 * cta + (k & 1);
                 uint8_t* dst = p.qs + buf * (2 * kHalf);
-                for (int rt = (warp - 10) * 4; rt < rows; rt += 8) {
-                    const float c = query_rows<DH, DR>(p, s, rt, dst + (rt >> 7) * kHalf, lane);
+                QueryRows<DH, DR> now, next;               // the next rows are loaded while these are worked on
+                int rt = (warp - 10) * 4;
+                now.load(p, s, rt, lane);
+#pragma unroll 1
+                for (; rt < rows; rt += 8) {
+                    next.load(p, s, min(rt + 8, rows - 1), lane);
+                    const float c = now.finish(p, sh->gain, rt, dst + (rt >> 7) * kHalf, lane);
                     if ((lane & 7) == 0) p.qcs[buf * kRowsQ + rt + (lane >> 3)] = c;
+                    now = next;
                 }
                 asm volatile("fence.proxy.async.global;" ::: "memory");
             }
@@ -535,13 +568,13 @@ __global__ void __launch_bounds__(kThreadsA, 1) prefill_attend_kernel(const __gr
     } else {
         // ---- softmax: thread = row ----
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-        const int h = warp >> 2, row = tid & 127, rt = tid;
+        const int h = warp >> 2, rt = tid;
         const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t t_s = tmem + lane_base + kS + h * 128, t_o = tmem + lane_base + kO + h * 128;
         const int* we = reinterpret_cast<const int*>(p.weights);
         uint32_t s_phase = 0, o_phase = 0;
+        int tiles = 0;                                                  // token tiles of the CTA so far
         bool ok = true;
-        (void)row;
         for (int k = 0;; ++k) {
             ok = wait_or_fail(&sh->piece_full[k & 1], (k >> 1) & 1, sh, p.status);
             ok = __all_sync(0xffffffffu, ok);
@@ -552,9 +585,11 @@ __global__ void __launch_bounds__(kThreadsA, 1) prefill_attend_kernel(const __gr
             float c = 0.f;
             if (mine && k == 0 && s.t0 < s.t1) {
                 // the first piece's queries, straight to shared memory: a warp its own 32 rows
-#pragma unroll 2
+#pragma unroll 1
                 for (int q = 0; q < 32; q += 4) {
-                    const float f = query_rows<DH, DR>(p, s, warp * 32 + q, sm + h * kHalf, lane);
+                    QueryRows<DH, DR> rows;
+                    rows.load(p, s, warp * 32 + q, lane);
+                    const float f = rows.finish(p, sh->gain, warp * 32 + q, sm + h * kHalf, lane);
                     const float g = __shfl_sync(0xffffffffu, f, (lane & 3) * 8);
                     if ((lane >> 2) == (q >> 2)) c = g;
                 }
@@ -567,17 +602,16 @@ __global__ void __launch_bounds__(kThreadsA, 1) prefill_attend_kernel(const __gr
             const int n_row = there ? s.n_lo + i : 0;                   // causal length
             float m = -INFINITY, sum = 0.f;
             auto tile_at = [&](int t) { return t < s.head ? t : t + s.gap; };
-            int info = mine && s.t0 < s.t1 ? p.tinfo[s.tile0 + tile_at(s.t0)] : 0;
-            for (int t = s.t0; t < s.t1 && mine; ++t) {
+            if (!mine) tiles += s.t1 - s.t0;
+            for (int t = s.t0; t < s.t1 && mine; ++t, ++tiles) {
                 const int first = tile_at(t) * kTile;
-                const int e = (info & 255) - 64;
-                const bool as_bf = (info & 256) != 0;
-                if (t + 1 < s.t1) info = p.tinfo[s.tile0 + tile_at(t + 1)];
                 ok = wait_or_fail(&sh->s_full[h], s_phase, sh, p.status);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 s_phase ^= 1;
                 tc_fence_after();
+                const int info = sh->info[tiles & 3], e = (info & 255) - 64;
+                const bool as_bf = (info & 256) != 0;
                 if (t == s.t0 && k > 0) c = *(volatile const float*)&p.qcs[(size_t)(2 * cta + (k & 1)) * kRowsQ + rt];
                 float x[128];
                 tmem_ld64(t_s, *reinterpret_cast<uint32_t(*)[64]>(x));

@@ -475,13 +475,14 @@ __global__ void __launch_bounds__(kThreadsE, NV == 1 ? 2 : 1) prefill_expand_ker
                 if (key) {
                     // NaN where the latent is not finite: rows that see the token become NaN, others do not
                     f = et == kBad ? __int_as_float(0x7fc00000) : et == kNone ? 0.f : ldexpf(al_now, et + we[cb / nkb]);
-                    dst = p.kc + ((size_t)tile * p.G * nkb + cb) * kBlock;
+                    dst = p.kc + ((size_t)tile * p.G * nkb + cb) * kBlock + row * 128;
                 } else {
                     f = et == kBad || et == kNone ? 0.f : ldexpf(1.f, et - e_tile);
-                    dst = p.v + ((size_t)tile * p.Gv * nvb + (cb - p.G * nkb)) * kBlock;
+                    // a matrix's values by 64 tokens, then by 64 columns
+                    const int m = (cb - p.G * nkb) / nvb, c = (cb - p.G * nkb) % nvb;
+                    dst = p.v + (((size_t)tile * p.Gv + m) * nvb * 2 + (row >> 6) * nvb + c) * (kBlock / 2) + (row & 63) * 128;
                 }
                 const bool as_bf = bf && !key;
-                dst += row * 128;
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {                // two neighbouring 16-byte pieces, in swizzled order
                     uint32_t h[2][4];
