@@ -9,7 +9,7 @@
 //   O += P V             M = 128, N = d_v, K = 128 tokens, A = P out of TMEM, O in TMEM (128 columns a half)
 //
 // Warps 0-3 and 4-7 are the two halves' softmax, warp 8 loads (bulk copies of prepared blocks into a ring),
-// warp 9 issues (10 and 11 make the warpgroup whole).  The halves alternate: while one half's S is worked on, the other's PV and the next QK run:
+// warp 9 issues, warps 10-15 list the CTA's pieces of work and normalise the next piece's queries.  The halves alternate: while one half's S is worked on, the other's PV and the next QK run:
 // PV0(j) QK0(j+1) PV1(j) QK1(j+1).  The products of one thread run in order, so QK may write S over the P
 // that the PV ahead of it reads, and a half whose S(j) is complete knows that its PV(j-1) is.
 //
@@ -34,12 +34,8 @@ namespace {
 
 using namespace tc;
 
-constexpr int kThreadsA = 384;
-// Registers: 384 threads start with 168 each, the most that 65536 allow.  The softmax keeps a row of 128 logits,
-// so the warpgroup of the other warps gives up 80 of its 168 and each half's takes 40 of them:
-// 2 x 208 + 88 = 3 x 168.
-constexpr int kRegsSoftmax = 208, kRegsOther = 88;
-static_assert(2 * kRegsSoftmax + kRegsOther <= 3 * 168, "register split");
+constexpr int kConverters = 6;             // warps that list the work and normalise queries
+constexpr int kThreadsA = (10 + kConverters) * 32;
 constexpr int kUnits = 8;                  // ring, in blocks
 constexpr int kGroups = 8;                 // barriers of groups (a token tile's key blocks, or its value blocks)
 
@@ -217,31 +213,39 @@ struct QueryRows {
 };
 
 // ---- softmax of a tile's row: weights in place of logits ----
-// Two 64-token halves, each signalled as soon as it lies in TMEM.  Returns the sum of the unrounded weights.
-template <bool BF>
-__device__ __forceinline__ float weights_out(float (&x)[128], float c, float off, uint32_t t_s, uint64_t* first, uint64_t* second, int lane) {
-    const uint64_t c2 = dec::f2(c, c), off2 = dec::f2(off, off);
-    uint64_t sum[2] = {0, 0};
+// 32 columns of the row; and 64 columns together with their maximum (a reduction in the load, on sm_103a).
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&x)[32]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7]), "=f"(x[8]), "=f"(x[9]), 
+          "=f"(x[10]), "=f"(x[11]), "=f"(x[12]), "=f"(x[13]), "=f"(x[14]), "=f"(x[15]), "=f"(x[16]), "=f"(x[17]), "=f"(x[18]), "=f"(x[19]), 
+          "=f"(x[20]), "=f"(x[21]), "=f"(x[22]), "=f"(x[23]), "=f"(x[24]), "=f"(x[25]), "=f"(x[26]), "=f"(x[27]), "=f"(x[28]), "=f"(x[29]), 
+          "=f"(x[30]), "=f"(x[31])
+        : "r"(taddr));
+}
+__device__ __forceinline__ float tmem_max64(uint32_t taddr) {
+    [[maybe_unused]] float x[64];
+    float top;
+    asm volatile("tcgen05.ld.red.sync.aligned.32x32b.x64.max.f32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, %64, [%65];"
+        : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7]), "=f"(x[8]), "=f"(x[9]), 
+          "=f"(x[10]), "=f"(x[11]), "=f"(x[12]), "=f"(x[13]), "=f"(x[14]), "=f"(x[15]), "=f"(x[16]), "=f"(x[17]), "=f"(x[18]), "=f"(x[19]), 
+          "=f"(x[20]), "=f"(x[21]), "=f"(x[22]), "=f"(x[23]), "=f"(x[24]), "=f"(x[25]), "=f"(x[26]), "=f"(x[27]), "=f"(x[28]), "=f"(x[29]), 
+          "=f"(x[30]), "=f"(x[31]), "=f"(x[32]), "=f"(x[33]), "=f"(x[34]), "=f"(x[35]), "=f"(x[36]), "=f"(x[37]), "=f"(x[38]), "=f"(x[39]), 
+          "=f"(x[40]), "=f"(x[41]), "=f"(x[42]), "=f"(x[43]), "=f"(x[44]), "=f"(x[45]), "=f"(x[46]), "=f"(x[47]), "=f"(x[48]), "=f"(x[49]), 
+          "=f"(x[50]), "=f"(x[51]), "=f"(x[52]), "=f"(x[53]), "=f"(x[54]), "=f"(x[55]), "=f"(x[56]), "=f"(x[57]), "=f"(x[58]), "=f"(x[59]), 
+          "=f"(x[60]), "=f"(x[61]), "=f"(x[62]), "=f"(x[63]),
+          "=f"(top)
+        : "r"(taddr));
+    return top;
+}
+// Bit k: whether the row sees column c0 + k.  It sees columns below `end`, with a window those from `from` on or below
+// `sink`.
+__device__ __forceinline__ uint32_t below(int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; }
+__device__ __forceinline__ uint32_t seen32(int c0, int end, int from, int sink) {
+    return below(end - c0) & (~below(from - c0) | below(sink - c0));
+}
+__device__ __forceinline__ void hide(float (&x)[32], uint32_t seen) {
 #pragma unroll
-    for (int k = 0; k < 128; k += 32) {
-        uint32_t w[16];
-#pragma unroll
-        for (int q = 0; q < 16; ++q) {
-            const float2 a = dec::f2_unpack(dec::f2_fma(dec::f2(x[k + 2 * q], x[k + 2 * q + 1]), c2, off2));
-            const float u = ex2(a.x), v = ex2(a.y);
-            sum[q & 1] = dec::f2_add(sum[q & 1], dec::f2(u, v));
-            w[q] = BF ? pack_bf16(u, v) : pack_f16(u, v);
-        }
-        tmem_st16(t_s + k / 2, w);
-        if (k == 32 || k == 96) {
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(k == 32 ? first : second);
-        }
-    }
-    const float2 s = dec::f2_unpack(dec::f2_add(sum[0], sum[1]));
-    return s.x + s.y;
+    for (int k = 0; k < 32; ++k) x[k] = seen >> k & 1 ? x[k] : -INFINITY;
 }
 
 template <int DH, int DR, int DV>
@@ -269,7 +273,7 @@ __global__ void __launch_bounds__(kThreadsA, 1) prefill_attend_kernel(const __gr
             mbar_init(&sh->o_full[i], 1);
             mbar_init(&sh->piece_full[i], 1);
             mbar_init(&sh->piece_empty[i], 10);            // loads, products, eight softmax warps
-            mbar_init(&sh->conv_full[i], 2);
+            mbar_init(&sh->conv_full[i], kConverters);
             sh->q_issued[i] = 0;
         }
         mbar_init(&sh->done, 1);
@@ -295,7 +299,6 @@ __global__ void __launch_bounds__(kThreadsA, 1) prefill_attend_kernel(const __gr
 
     if (!busy) {
     } else if (warp >= 8) {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
       if (warp == 8) {
         // ---- loads ----
         if (lane == 0) {
@@ -528,7 +531,7 @@ give_up:
             if (k > 0 && s.unit >= 0 && s.t0 < s.t1) {
                 // the raw rows into L2: reading them then takes its latency
                 const int row_bytes = p.q_bf16 ? 2 * DH : 4 * DH, rope_bytes = p.q_bf16 ? 2 * DR : 4 * DR, esz = p.q_bf16 ? 2 : 4;
-                for (int rt = (warp - 10) * 32 + lane; rt < min(s.queries * p.hp, kRowsQ); rt += 64) {
+                for (int rt = (warp - 10) * 32 + lane; rt < min(s.queries * p.hp, kRowsQ); rt += kConverters * 32) {
                     const int64_t row = s.row0 + (rt >> p.hp_log), head = (int64_t)s.unit * p.hp + (rt & (p.hp - 1));
                     const char* x = (const char*)p.q + (row * p.q_row + head * p.q_head) * esz;
                     const char* y = (const char*)p.q_rope + (row * p.qr_row + head * p.qr_head) * esz;
@@ -551,10 +554,10 @@ give_up:
                 uint8_t* dst = p.qs + buf * (2 * kHalf);
                 QueryRows<DH, DR> now, next;               // the next rows are loaded while these are worked on
                 int rt = (warp - 10) * 4;
-                now.load(p, s, rt, lane);
+                now.load(p, s, min(rt, rows - 1), lane);
 #pragma unroll 1
-                for (; rt < rows; rt += 8) {
-                    next.load(p, s, min(rt + 8, rows - 1), lane);
+                for (; rt < rows; rt += kConverters * 4) {
+                    next.load(p, s, min(rt + kConverters * 4, rows - 1), lane);
                     const float c = now.finish(p, sh->gain, rt, dst + (rt >> 7) * kHalf, lane);
                     if ((lane & 7) == 0) p.qcs[buf * kRowsQ + rt + (lane >> 3)] = c;
                     now = next;
@@ -567,7 +570,6 @@ give_up:
       }
     } else {
         // ---- softmax: thread = row ----
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
         const int h = warp >> 2, rt = tid;
         const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t t_s = tmem + lane_base + kS + h * 128, t_o = tmem + lane_base + kO + h * 128;
@@ -579,7 +581,7 @@ give_up:
             ok = wait_or_fail(&sh->piece_full[k & 1], (k >> 1) & 1, sh, p.status);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
-            const Piece s = sh->piece[k & 1];
+            const Piece& s = sh->piece[k & 1];                          // (read where it is needed: registers are few)
             if (s.unit < 0) break;
             const bool mine = h == 0 || s.queries * p.hp > 128;         // uniform in a warp
             float c = 0.f;
@@ -613,26 +615,31 @@ give_up:
                 const int info = sh->info[tiles & 3], e = (info & 255) - 64;
                 const bool as_bf = (info & 256) != 0;
                 if (t == s.t0 && k > 0) c = *(volatile const float*)&p.qcs[(size_t)(2 * cta + (k & 1)) * kRowsQ + rt];
-                float x[128];
-                tmem_ld64(t_s, *reinterpret_cast<uint32_t(*)[64]>(x));
-                tmem_ld64(t_s + 64, *reinterpret_cast<uint32_t(*)[64]>(x + 64));
-                tmem_wait_ld();
                 // tiles that some row does not see whole (uniform over the tile's rows)
                 const bool edge = first + kTile > s.n_lo || (p.window > 0 && first < s.n_lo + s.queries - 1 - p.window && first + kTile > p.sinks);
-                if (edge) {
-                    const int end = n_row - first;
-                    const int from = p.window > 0 ? n_row - p.window - first : -1, sink = p.window > 0 ? p.sinks - first : -1;
+                const int end = n_row - first, from = p.window > 0 ? end - p.window : 0, sink = p.window > 0 ? p.sinks - first : 0;
+                float x[32], top;
+                if (!edge) {
+                    top = -INFINITY;
+#pragma unroll 1
+                    for (int q = 0; q < 128; q += 64) {                 // (both at once would take 128 registers)
+                        const float other = tmem_max64(t_s + q);
+                        tmem_wait_ld();
+                        top = fmaxf(top, other);
+                    }
+                } else {
+                    top = -INFINITY;
+#pragma unroll 1
+                    for (int q = 0; q < 128; q += 32) {
+                        tmem_ld32(t_s + q, x);
+                        tmem_wait_ld();
+                        hide(x, seen32(q, end, from, sink));
 #pragma unroll
-                    for (int q = 0; q < 128; ++q)
-                        if (q >= end || (q < from && q >= sink)) x[q] = -INFINITY;
+                        for (int r = 0; r < 32; r += 2) top = max3(top, x[r], x[r + 1]);
+                    }
                 }
-                float top[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-                for (int q = 4; q < 124; q += 8) {
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) top[r] = max3(top[r], x[q + r], x[q + 4 + r]);
-                }
-                const float cand = fmaf(fmaxf(max3(top[0], top[1], x[124]), max3(fmaxf(top[2], top[3]), fmaxf(x[125], x[126]), x[127])), c, (float)e);
+                tmem_ld32(t_s, x);
+                const float cand = fmaf(top, c, (float)e);
                 const bool move = cand > m + 8.f;
                 if (__any_sync(0xffffffffu, move)) {
                     const float m2 = move ? cand : m;
@@ -652,13 +659,47 @@ give_up:
                     m = m2;
                 }
                 const float off = (float)(e + 7) - (m == -INFINITY ? 0.f : m);
-                const float part = as_bf ? weights_out<true>(x, c, off, t_s, &sh->pa_full[h], &sh->pb_full[h], lane)
-                                         : weights_out<false>(x, c, off, t_s, &sh->pa_full[h], &sh->pb_full[h], lane);
-                sum = fmaf(part, pow2i(-e), sum);
+                const uint64_t c2 = dec::f2(c, c), off2 = dec::f2(off, off);
+                uint64_t part[2] = {0, 0};
+                // a rolled loop of 32 tokens a step: its code stays in the instruction cache beside the other warps'
+#pragma unroll 1
+                for (int q = 0; q < 128; q += 32) {
+                    tmem_wait_ld();
+                    if (edge) hide(x, seen32(q, end, from, sink));
+                    uint64_t y[16];
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) y[r] = dec::f2_fma(dec::f2(x[2 * r], x[2 * r + 1]), c2, off2);
+                    if (q < 96) tmem_ld32(t_s + q + 32, x);
+                    uint32_t w[16];
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) {
+                        const float2 a = dec::f2_unpack(y[r]);
+                        y[r] = dec::f2(ex2(a.x), ex2(a.y));
+                        part[r & 1] = dec::f2_add(part[r & 1], y[r]);
+                    }
+                    if (!as_bf) {
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) { const float2 a = dec::f2_unpack(y[r]); w[r] = pack_f16(a.x, a.y); }
+                    } else {
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) { const float2 a = dec::f2_unpack(y[r]); w[r] = pack_bf16(a.x, a.y); }
+                    }
+                    tmem_st16(t_s + q / 2, w);
+                    if (q & 32) {                                       // 64 tokens' weights lie in TMEM
+                        tmem_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(q == 32 ? &sh->pa_full[h] : &sh->pb_full[h]);
+                    }
+                }
+                const float2 both = dec::f2_unpack(dec::f2_add(part[0], part[1]));
+                sum = fmaf(both.x + both.y, pow2i(-e), sum);
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh->piece_empty[k & 1]);        // (s and c are in registers)
-            if (!mine) continue;
+            if (!mine) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh->piece_empty[k & 1]);
+                continue;
+            }
             if (s.t0 < s.t1 && ok) ok = wait_or_fail(&sh->o_full[h], o_phase, sh, p.status);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
@@ -714,6 +755,8 @@ give_up:
                 if (there) p.part_ml[part] = make_float2(m, sum);
             }
             tc_fence_before();                                          // the next tile's PV writes O after this half's P
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh->piece_empty[k & 1]);
         }
     }
     __syncthreads();
