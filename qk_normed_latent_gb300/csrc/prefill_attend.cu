@@ -36,6 +36,10 @@ using namespace tc;
 
 constexpr int kConverters = 6;             // warps that list the work and normalise queries
 constexpr int kThreadsA = (10 + kConverters) * 32;
+// Registers: 512 threads start with 128 each, the whole register file.  The softmax keeps a row of 128 logits, so the
+// two warpgroups of the other warps give up 64 of theirs and each half's takes as many.
+constexpr int kRegsSoftmax = 192, kRegsOther = 64;
+static_assert(2 * kRegsSoftmax + 2 * kRegsOther <= 4 * 128, "register split");
 constexpr int kUnits = 8;                  // ring, in blocks
 constexpr int kGroups = 8;                 // barriers of groups (a token tile's key blocks, or its value blocks)
 
@@ -213,29 +217,18 @@ struct QueryRows {
 };
 
 // ---- softmax of a tile's row: weights in place of logits ----
-// 32 columns of the row; and 64 columns together with their maximum (a reduction in the load, on sm_103a).
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&x)[32]) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7]), "=f"(x[8]), "=f"(x[9]), 
-          "=f"(x[10]), "=f"(x[11]), "=f"(x[12]), "=f"(x[13]), "=f"(x[14]), "=f"(x[15]), "=f"(x[16]), "=f"(x[17]), "=f"(x[18]), "=f"(x[19]), 
-          "=f"(x[20]), "=f"(x[21]), "=f"(x[22]), "=f"(x[23]), "=f"(x[24]), "=f"(x[25]), "=f"(x[26]), "=f"(x[27]), "=f"(x[28]), "=f"(x[29]), 
-          "=f"(x[30]), "=f"(x[31])
-        : "r"(taddr));
-}
-__device__ __forceinline__ float tmem_max64(uint32_t taddr) {
-    [[maybe_unused]] float x[64];
-    float top;
+// 64 columns of the row together with their maximum (a reduction in the load, on sm_103a).
+__device__ __forceinline__ void tmem_ld64_max(uint32_t taddr, float* x, float& top) {
     asm volatile("tcgen05.ld.red.sync.aligned.32x32b.x64.max.f32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, %64, [%65];"
-        : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7]), "=f"(x[8]), "=f"(x[9]), 
-          "=f"(x[10]), "=f"(x[11]), "=f"(x[12]), "=f"(x[13]), "=f"(x[14]), "=f"(x[15]), "=f"(x[16]), "=f"(x[17]), "=f"(x[18]), "=f"(x[19]), 
-          "=f"(x[20]), "=f"(x[21]), "=f"(x[22]), "=f"(x[23]), "=f"(x[24]), "=f"(x[25]), "=f"(x[26]), "=f"(x[27]), "=f"(x[28]), "=f"(x[29]), 
-          "=f"(x[30]), "=f"(x[31]), "=f"(x[32]), "=f"(x[33]), "=f"(x[34]), "=f"(x[35]), "=f"(x[36]), "=f"(x[37]), "=f"(x[38]), "=f"(x[39]), 
-          "=f"(x[40]), "=f"(x[41]), "=f"(x[42]), "=f"(x[43]), "=f"(x[44]), "=f"(x[45]), "=f"(x[46]), "=f"(x[47]), "=f"(x[48]), "=f"(x[49]), 
-          "=f"(x[50]), "=f"(x[51]), "=f"(x[52]), "=f"(x[53]), "=f"(x[54]), "=f"(x[55]), "=f"(x[56]), "=f"(x[57]), "=f"(x[58]), "=f"(x[59]), 
-          "=f"(x[60]), "=f"(x[61]), "=f"(x[62]), "=f"(x[63]),
+        : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7]), "=f"(x[8]), "=f"(x[9]),
+          "=f"(x[10]), "=f"(x[11]), "=f"(x[12]), "=f"(x[13]), "=f"(x[14]), "=f"(x[15]), "=f"(x[16]), "=f"(x[17]), "=f"(x[18]),
+          "=f"(x[19]), "=f"(x[20]), "=f"(x[21]), "=f"(x[22]), "=f"(x[23]), "=f"(x[24]), "=f"(x[25]), "=f"(x[26]), "=f"(x[27]),
+          "=f"(x[28]), "=f"(x[29]), "=f"(x[30]), "=f"(x[31]), "=f"(x[32]), "=f"(x[33]), "=f"(x[34]), "=f"(x[35]), "=f"(x[36]),
+          "=f"(x[37]), "=f"(x[38]), "=f"(x[39]), "=f"(x[40]), "=f"(x[41]), "=f"(x[42]), "=f"(x[43]), "=f"(x[44]), "=f"(x[45]),
+          "=f"(x[46]), "=f"(x[47]), "=f"(x[48]), "=f"(x[49]), "=f"(x[50]), "=f"(x[51]), "=f"(x[52]), "=f"(x[53]), "=f"(x[54]),
+          "=f"(x[55]), "=f"(x[56]), "=f"(x[57]), "=f"(x[58]), "=f"(x[59]), "=f"(x[60]), "=f"(x[61]), "=f"(x[62]), "=f"(x[63]),
           "=f"(top)
         : "r"(taddr));
-    return top;
 }
 // Bit k: whether the row sees column c0 + k.  It sees columns below `end`, with a window those from `from` on or below
 // `sink`.
@@ -243,9 +236,33 @@ __device__ __forceinline__ uint32_t below(int n) { return n >= 32 ? 0xffffffffu 
 __device__ __forceinline__ uint32_t seen32(int c0, int end, int from, int sink) {
     return below(end - c0) & (~below(from - c0) | below(sink - c0));
 }
-__device__ __forceinline__ void hide(float (&x)[32], uint32_t seen) {
+
+// Weights of the row's 128 tokens to TMEM in two halves, each signalled as soon as it lies there.  Returns the sum of the
+// unrounded weights.
+template <bool BF>
+__device__ __forceinline__ float weights_out(float (&x)[128], float c, float off, uint32_t t_s, uint64_t* first, uint64_t* second, int lane) {
+    const uint64_t c2 = dec::f2(c, c), off2 = dec::f2(off, off);
+    uint64_t sum[2] = {0, 0};
 #pragma unroll
-    for (int k = 0; k < 32; ++k) x[k] = seen >> k & 1 ? x[k] : -INFINITY;
+    for (int k = 0; k < 128; k += 32) {
+        uint32_t w[16];
+#pragma unroll
+        for (int q = 0; q < 16; ++q) {
+            const float2 a = dec::f2_unpack(dec::f2_fma(dec::f2(x[k + 2 * q], x[k + 2 * q + 1]), c2, off2));
+            const float u = ex2(a.x), v = ex2(a.y);
+            sum[q & 1] = dec::f2_add(sum[q & 1], dec::f2(u, v));
+            w[q] = BF ? pack_bf16(u, v) : pack_f16(u, v);
+        }
+        tmem_st16(t_s + k / 2, w);
+        if (k == 32 || k == 96) {
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(k == 32 ? first : second);
+        }
+    }
+    const float2 s = dec::f2_unpack(dec::f2_add(sum[0], sum[1]));
+    return s.x + s.y;
 }
 
 template <int DH, int DR, int DV>
@@ -299,6 +316,7 @@ __global__ void __launch_bounds__(kThreadsA, 1) prefill_attend_kernel(const __gr
 
     if (!busy) {
     } else if (warp >= 8) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
       if (warp == 8) {
         // ---- loads ----
         if (lane == 0) {
@@ -381,7 +399,6 @@ __global__ void __launch_bounds__(kThreadsA, 1) prefill_attend_kernel(const __gr
         int halves = 0, left = 0, q_at = 0;                // of the piece whose logits come next: tiles left, its place in the queue
         int cur = 0;                                       // halves whose weights are awaited
         bool cur_first = false, cur_last = false;
-        bool seen_a = false, seen_v = false, seen_1 = false;   // barriers of the next round found complete ahead of it
         // A round: for each half, O += P V of the tile whose weights are awaited, then S of the next tile (of the
         // same piece or of the next one).
         for (;;) {
@@ -406,64 +423,93 @@ __global__ void __launch_bounds__(kThreadsA, 1) prefill_attend_kernel(const __gr
             const bool as_bf = (sh->info[(gv >> 1) & 3] & 256) != 0;
             const uint32_t fmt = as_bf ? bf : 0u;
             if (cur == 2 && nxt == 2 && !first) {
-                // The same round in a straight line, each barrier looked at while the products ahead of its use are still
-                // being taken (the unit takes six or so ahead; a wait that succeeds at once would cost as much as two).
-                const uint64_t v0 = v_desc + (uint64_t)((unit % kUnits) * kStep), v1 = VU == 2 ? v_desc + (uint64_t)(((unit + 1) % kUnits) * kStep) : v0 + kStep / 2;
-                uint64_t kd[KU];
+                // The same rounds in a straight line, to the piece's end.  The unit takes six or so products ahead; each
+                // barrier is looked at, and the next round's operands are formed, while products are still being taken (a
+                // wait that succeeds at once costs as much as two of them).
+                auto value = [&](int u) { return v_desc + (uint64_t)((u % kUnits) * kStep); };
+                uint64_t v0 = value(unit), v1 = VU == 2 ? value(unit + 1) : v0 + kStep / 2, kd[KU];
 #pragma unroll
                 for (int blk = 0; blk < KU; ++blk) kd[blk] = k_desc + (uint64_t)(((unit + VU + blk) % kUnits) * kStep);
-                const uint32_t acc = cur_first ? 0u : 1u;
-                const int next_gv = gk + 1;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint32_t ph = (p_phase >> h) & 1;
-                    const uint32_t o = tmem + kO + h * 128, a = tmem + kS + h * 128;
-                    if (!(h == 0 ? seen_a : seen_1) && !wait_or_fail(&sh->pa_full[h], ph, sh, p.status)) goto give_up;
-                    if (h == 0 && !seen_v && !wait_or_fail(&sh->full[gv % kGroups], (gv / kGroups) & 1, sh, p.status)) goto give_up;
-                    tc_fence_after();
-                    mma_bf16_tmem_a(o, a, v0, id_o | fmt, acc);
-                    mma_bf16_tmem_a(o, a + 8, v0 + 128, id_o | fmt, 1u);
-                    const bool seen_b = mbar_test_wait(&sh->pb_full[h], ph);
-                    mma_bf16_tmem_a(o, a + 16, v0 + 256, id_o | fmt, 1u);
-                    mma_bf16_tmem_a(o, a + 24, v0 + 384, id_o | fmt, 1u);
-                    if (!seen_b && !wait_or_fail(&sh->pb_full[h], ph, sh, p.status)) goto give_up;
-                    tc_fence_after();
-                    mma_bf16_tmem_a(o, a + 32, v1, id_o | fmt, 1u);
-                    mma_bf16_tmem_a(o, a + 40, v1 + 128, id_o | fmt, 1u);
-                    bool seen_k = true;
-                    if (h == 0) seen_k = mbar_test_wait(&sh->full[gk % kGroups], (gk / kGroups) & 1);
-                    mma_bf16_tmem_a(o, a + 48, v1 + 256, id_o | fmt, 1u);
-                    mma_bf16_tmem_a(o, a + 56, v1 + 384, id_o | fmt, 1u);
-                    if (h == 1) mma_commit(&sh->empty[gv % kGroups]);
-                    if (!seen_k && !wait_or_fail(&sh->full[gk % kGroups], (gk / kGroups) & 1, sh, p.status)) goto give_up;
-                    const uint32_t d = tmem + kS + h * 128;
-#pragma unroll
-                    for (int blk = 0; blk < KU; ++blk) {
-                        if (blk == KU - 1) {                // one more block of products to come
-                            if (h == 0) {
-                                seen_1 = mbar_test_wait(&sh->pa_full[1], (p_phase >> 1) & 1);
-                            } else {
-                                seen_a = mbar_test_wait(&sh->pa_full[0], (p_phase ^ 1) & 1);
-                                seen_v = mbar_test_wait(&sh->full[next_gv % kGroups], (next_gv / kGroups) & 1);
-                            }
-                        }
-#pragma unroll
-                        for (int kk = 0; kk < (blk < KU - 1 ? 4 : DR / 16); ++kk)
-                            mma_bf16(d, q_desc + (uint64_t)((h * KU + blk) * kStep + kk * 2), kd[blk] + (uint64_t)(kk * 2), id_s, (blk > 0 || kk > 0) ? 1u : 0u);
-                    }
-                    mma_commit(&sh->s_full[h]);
-                    if (left == 1) mma_commit(&sh->q_empty[h]);
-                }
-                mma_commit(&sh->empty[gk % kGroups]);
-                p_phase ^= 3;
-                group = next_gv;
+                uint32_t acc = cur_first ? 0u : 1u, id = id_o | fmt;
+                uint64_t *b_v = &sh->full[gv % kGroups], *b_k = &sh->full[gk % kGroups], *f_v = &sh->empty[gv % kGroups], *f_k = &sh->empty[gk % kGroups];
+                uint32_t ph_v = (gv / kGroups) & 1, ph_k = (gk / kGroups) & 1, ph = p_phase & 1;       // (both halves' phases are alike in a piece of two)
+                uint32_t ph1 = (p_phase >> 1) & 1;
+                group = gk + 1;
                 unit += VU + KU;
+                bool seen_a = false, seen_v = false, seen_1 = false;
+                for (;;) {
+                    uint64_t v0n, v1n, kn[KU], *b_vn, *b_kn, *f_vn, *f_kn;
+                    uint32_t ph_vn, ph_kn, idn;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t o = tmem + kO + h * 128, a = tmem + kS + h * 128, d = a;
+                        const uint32_t php = h ? ph1 : ph;
+                        if (!(h == 0 ? seen_a : seen_1) && !wait_or_fail(&sh->pa_full[h], php, sh, p.status)) goto give_up;
+                        if (h == 0 && !seen_v && !wait_or_fail(b_v, ph_v, sh, p.status)) goto give_up;
+                        tc_fence_after();
+                        mma_bf16_tmem_a(o, a, v0, id, acc);
+                        mma_bf16_tmem_a(o, a + 8, v0 + 128, id, 1u);
+                        const bool seen_b = mbar_test_wait(&sh->pb_full[h], php);
+                        mma_bf16_tmem_a(o, a + 16, v0 + 256, id, 1u);
+                        mma_bf16_tmem_a(o, a + 24, v0 + 384, id, 1u);
+                        if (!seen_b && !wait_or_fail(&sh->pb_full[h], php, sh, p.status)) goto give_up;
+                        tc_fence_after();
+                        mma_bf16_tmem_a(o, a + 32, v1, id, 1u);
+                        mma_bf16_tmem_a(o, a + 40, v1 + 128, id, 1u);
+                        bool seen_k = true;
+                        if (h == 0) seen_k = mbar_test_wait(b_k, ph_k);
+                        mma_bf16_tmem_a(o, a + 48, v1 + 256, id, 1u);
+                        mma_bf16_tmem_a(o, a + 56, v1 + 384, id, 1u);
+                        if (h == 1) mma_commit(f_v);
+                        if (!seen_k && !wait_or_fail(b_k, ph_k, sh, p.status)) goto give_up;
+#pragma unroll
+                        for (int blk = 0; blk < KU; ++blk) {
+                            if (blk == KU - 1) {            // one more block of products to come
+                                if (h == 0) {
+                                    seen_1 = mbar_test_wait(&sh->pa_full[1], ph1);
+                                } else {
+                                    const int gn = group, kg = group + 1;
+                                    v0n = value(unit);
+                                    v1n = VU == 2 ? value(unit + 1) : v0n + kStep / 2;
+#pragma unroll
+                                    for (int q = 0; q < KU; ++q) kn[q] = k_desc + (uint64_t)(((unit + VU + q) % kUnits) * kStep);
+                                    b_vn = &sh->full[gn % kGroups];
+                                    b_kn = &sh->full[kg % kGroups];
+                                    f_vn = &sh->empty[gn % kGroups];
+                                    f_kn = &sh->empty[kg % kGroups];
+                                    ph_vn = (gn / kGroups) & 1;
+                                    ph_kn = (kg / kGroups) & 1;
+                                    idn = id_o | ((sh->info[(gn >> 1) & 3] & 256) ? bf : 0u);
+                                    seen_a = mbar_test_wait(&sh->pa_full[0], ph ^ 1);
+                                    seen_v = mbar_test_wait(b_vn, ph_vn);
+                                }
+                            }
+#pragma unroll
+                            for (int kk = 0; kk < (blk < KU - 1 ? 4 : DR / 16); ++kk)
+                                mma_bf16(d, q_desc + (uint64_t)((h * KU + blk) * kStep + kk * 2), kd[blk] + (uint64_t)(kk * 2), id_s, (blk > 0 || kk > 0) ? 1u : 0u);
+                        }
+                        mma_commit(&sh->s_full[h]);
+                        if (left == 1) mma_commit(&sh->q_empty[h]);
+                    }
+                    mma_commit(f_k);
+                    ph ^= 1;
+                    ph1 ^= 1;
+                    acc = 1u;
+                    if (--left == 0) break;
+                    v0 = v0n;
+                    v1 = v1n;
+#pragma unroll
+                    for (int q = 0; q < KU; ++q) kd[q] = kn[q];
+                    b_v = b_vn; b_k = b_kn; f_v = f_vn; f_k = f_kn;
+                    ph_v = ph_vn; ph_k = ph_kn; id = idn;
+                    group += 2;
+                    unit += VU + KU;
+                }
+                p_phase = ph | ph1 << 1;
                 cur_first = false;
-                cur_last = left == 1;
-                --left;
+                cur_last = true;
                 continue;
             }
-            seen_a = seen_v = false;
 #pragma unroll 1
             for (int h = 0; h < 2; ++h) {
                 if (h < cur) {
@@ -552,15 +598,12 @@ give_up:
                 const int rows = min(s.queries * p.hp, kRowsQ);
                 const size_t buf = 2 * cta + (k & 1);
                 uint8_t* dst = p.qs + buf * (2 * kHalf);
-                QueryRows<DH, DR> now, next;               // the next rows are loaded while these are worked on
-                int rt = (warp - 10) * 4;
-                now.load(p, s, min(rt, rows - 1), lane);
 #pragma unroll 1
-                for (; rt < rows; rt += kConverters * 4) {
-                    next.load(p, s, min(rt + kConverters * 4, rows - 1), lane);
-                    const float c = now.finish(p, sh->gain, rt, dst + (rt >> 7) * kHalf, lane);
+                for (int rt = (warp - 10) * 4; rt < rows; rt += kConverters * 4) {
+                    QueryRows<DH, DR> four;
+                    four.load(p, s, rt, lane);
+                    const float c = four.finish(p, sh->gain, rt, dst + (rt >> 7) * kHalf, lane);
                     if ((lane & 7) == 0) p.qcs[buf * kRowsQ + rt + (lane >> 3)] = c;
-                    now = next;
                 }
                 asm volatile("fence.proxy.async.global;" ::: "memory");
             }
@@ -570,6 +613,7 @@ give_up:
       }
     } else {
         // ---- softmax: thread = row ----
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
         const int h = warp >> 2, rt = tid;
         const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t t_s = tmem + lane_base + kS + h * 128, t_o = tmem + lane_base + kO + h * 128;
@@ -618,27 +662,24 @@ give_up:
                 // tiles that some row does not see whole (uniform over the tile's rows)
                 const bool edge = first + kTile > s.n_lo || (p.window > 0 && first < s.n_lo + s.queries - 1 - p.window && first + kTile > p.sinks);
                 const int end = n_row - first, from = p.window > 0 ? end - p.window : 0, sink = p.window > 0 ? p.sinks - first : 0;
-                float x[32], top;
-                if (!edge) {
+                float x[128], top, top2;
+                tmem_ld64_max(t_s, x, top);
+                tmem_ld64_max(t_s + 64, x + 64, top2);
+                tmem_wait_ld();
+                top = fmaxf(top, top2);
+                if (edge) {
                     top = -INFINITY;
-#pragma unroll 1
-                    for (int q = 0; q < 128; q += 64) {                 // (both at once would take 128 registers)
-                        const float other = tmem_max64(t_s + q);
-                        tmem_wait_ld();
-                        top = fmaxf(top, other);
-                    }
-                } else {
-                    top = -INFINITY;
-#pragma unroll 1
-                    for (int q = 0; q < 128; q += 32) {
-                        tmem_ld32(t_s + q, x);
-                        tmem_wait_ld();
-                        hide(x, seen32(q, end, from, sink));
 #pragma unroll
-                        for (int r = 0; r < 32; r += 2) top = max3(top, x[r], x[r + 1]);
+                    for (int q = 0; q < 128; q += 32) {
+                        const uint32_t seen = seen32(q, end, from, sink);
+#pragma unroll
+                        for (int r = 0; r < 32; r += 2) {
+                            x[q + r] = seen >> r & 1 ? x[q + r] : -INFINITY;
+                            x[q + r + 1] = seen >> (r + 1) & 1 ? x[q + r + 1] : -INFINITY;
+                            top = max3(top, x[q + r], x[q + r + 1]);
+                        }
                     }
                 }
-                tmem_ld32(t_s, x);
                 const float cand = fmaf(top, c, (float)e);
                 const bool move = cand > m + 8.f;
                 if (__any_sync(0xffffffffu, move)) {
@@ -659,41 +700,9 @@ give_up:
                     m = m2;
                 }
                 const float off = (float)(e + 7) - (m == -INFINITY ? 0.f : m);
-                const uint64_t c2 = dec::f2(c, c), off2 = dec::f2(off, off);
-                uint64_t part[2] = {0, 0};
-                // a rolled loop of 32 tokens a step: its code stays in the instruction cache beside the other warps'
-#pragma unroll 1
-                for (int q = 0; q < 128; q += 32) {
-                    tmem_wait_ld();
-                    if (edge) hide(x, seen32(q, end, from, sink));
-                    uint64_t y[16];
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) y[r] = dec::f2_fma(dec::f2(x[2 * r], x[2 * r + 1]), c2, off2);
-                    if (q < 96) tmem_ld32(t_s + q + 32, x);
-                    uint32_t w[16];
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) {
-                        const float2 a = dec::f2_unpack(y[r]);
-                        y[r] = dec::f2(ex2(a.x), ex2(a.y));
-                        part[r & 1] = dec::f2_add(part[r & 1], y[r]);
-                    }
-                    if (!as_bf) {
-#pragma unroll
-                        for (int r = 0; r < 16; ++r) { const float2 a = dec::f2_unpack(y[r]); w[r] = pack_f16(a.x, a.y); }
-                    } else {
-#pragma unroll
-                        for (int r = 0; r < 16; ++r) { const float2 a = dec::f2_unpack(y[r]); w[r] = pack_bf16(a.x, a.y); }
-                    }
-                    tmem_st16(t_s + q / 2, w);
-                    if (q & 32) {                                       // 64 tokens' weights lie in TMEM
-                        tmem_wait_st();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(q == 32 ? &sh->pa_full[h] : &sh->pb_full[h]);
-                    }
-                }
-                const float2 both = dec::f2_unpack(dec::f2_add(part[0], part[1]));
-                sum = fmaf(both.x + both.y, pow2i(-e), sum);
+                const float part = as_bf ? weights_out<true>(x, c, off, t_s, &sh->pa_full[h], &sh->pb_full[h], lane)
+                                         : weights_out<false>(x, c, off, t_s, &sh->pa_full[h], &sh->pb_full[h], lane);
+                sum = fmaf(part, pow2i(-e), sum);
             }
             if (!mine) {
                 __syncwarp();
