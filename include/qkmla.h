@@ -565,8 +565,8 @@ typedef struct qkmla_prefill_args {
  * RoPE keys are taken as fp16: up to 65504.
  *
  * Sizes: d_h and d_v 64 or 128, d_r 32 or 64, d_c a multiple of 64 up to 512, H / max(G, G_v)
- * 1, 2, 4, ... or 128, the larger of G and G_v a multiple of the other, B <= 4096, any page size; rows of 16-byte
- * aligned bases.
+ * 1, 2, 4, ... or 128, the larger of G and G_v a multiple of the other, B <= 4096, any page size; 16-byte
+ * aligned bases (o: 32-byte).
  * Device-side: a seq_len outside [0, max_pages * page_size], lengths that add up to more than
  * total_tokens, chunk starts out of order or beyond rows, or a page id outside [0, num_slots /
  * page_size) set QKMLA_ERR_DEVICE_BOUNDS; the affected rows are then undefined.

@@ -22,6 +22,7 @@ constexpr int kBlock = 16384;              // bytes of a block of 128 x 64 value
 constexpr int kMaxE = 40;                  // largest exponent of a tile's values
 constexpr int kCostStart = 2;              // cost of starting on a query tile, in tiles of tokens
 constexpr int kMinPiece = 2;               // no piece of a cut query tile has fewer tiles of tokens
+constexpr int kMaxCtas = 256;
 constexpr int kMinShare = 5;               // nor a CTA fewer units of cost
 
 struct Params {
@@ -57,7 +58,6 @@ struct Params {
     int* tinfo;                            // [max_tiles]: exponent + 64, | 256 where the values are bf16
     uint8_t *krope, *kc, *v;               // blocks: [tile], [tile][G][d_h / 64], [tile][G_v][d_v / 64]
     uint8_t* qs;                           // [cta][2][half][d_h / 64 + 1]: the normalised queries of a CTA's next two pieces
-    float* qcs;                            // [cta][2][256]: factor of a row's logits
     float* part_o;                         // [2 ctas][256][d_v]
     float2* part_ml;                       // [2 ctas][256]: reference and sum
     int* status;
@@ -108,6 +108,26 @@ __device__ __forceinline__ Place place_of(const Params& p, int64_t x, int64_t on
     return r;
 }
 
+// The same by one thread.
+__device__ __forceinline__ Place place_of_one(const Params& p, int64_t x, int64_t one) {
+    Place r;
+    r.u = (int)(x / one);
+    if (r.u >= p.units) { r.u = p.units; r.j = 0; r.t = 0; r.nt = 0; return r; }
+    const int64_t y = x - (int64_t)r.u * one;
+    int lo = 0, hi = p.nq - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (p.pre[mid] <= y) lo = mid;
+        else hi = mid - 1;
+    }
+    r.j = lo;
+    const int64_t at = p.pre[lo];
+    r.nt = (int)(p.pre[lo + 1] - at) - kCostStart;
+    const int t = (int)(y - at) - kCostStart;
+    r.t = t < kMinPiece ? 0 : r.nt - t < kMinPiece ? r.nt : t;
+    return r;
+}
+
 // CTAs that share the work: no more than leave each kMinShare.
 __device__ __forceinline__ int sharing(const Params& p, int64_t all) {
     const int64_t n = all / kMinShare;
@@ -125,6 +145,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 }
 // 2^e as an exact float, e in [-126, 127]
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
+
+__device__ __forceinline__ void st_global_v8(void* p, const uint32_t (&a)[4], const uint32_t (&b)[4]) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]),
+                 "r"(b[1]), "r"(b[2]), "r"(b[3])
+                 : "memory");
+}
 
 int launch_expand(const Params& p, bool q8, cudaStream_t s);
 int launch_attend(const Params& p, cudaStream_t s);

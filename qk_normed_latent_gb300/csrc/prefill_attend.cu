@@ -66,7 +66,8 @@ struct __align__(16) Shared {
     int fail;
     int issued;                            // groups whose copies were issued
     int q_issued[2];                       // query halves whose copies were issued
-    alignas(16) float gain[192];           // gamma_q gamma_k, then gamma_rope_q
+    alignas(16) float gain[192];           // gamma_q gamma_k, then gamma_rope_q, times a power of two
+    float factor;                          // of the logits: softmax_scale, log2 e and that power
 };
 static_assert(sizeof(Shared) <= 2048, "beside the blocks");
 
@@ -136,85 +137,68 @@ __device__ __forceinline__ bool wait_or_fail(uint64_t* bar, uint32_t parity, Sha
     }
 }
 // ---- queries ----
-// Four rows of a query tile, rt .. rt + 3, eight lanes a row: normalised, with the gains, times a power of two that
-// brings the row's largest value into [1, 2), as fp16 to row rt & 127 of the half at `dst` (blocks of 64 columns).
-// Returns the row's factor: softmax_scale, log2 e and that power.  A lane's values are 4 of every 32 neighbours.
+// Four rows of a query tile, rt .. rt + 3, eight lanes a row: normalised and times the gains as fp16 to row rt & 127 of
+// the half at `dst` (blocks of 64 columns).  Normalised values are at most sqrt d; the gains come with a power of two that
+// brings the largest into [1, 2), so that no scale overflows, and what fp16 loses below 2^-14 is 2^-25 of a logit's range.
+// A lane's values are 4 of every 32 neighbours.
 template <int N>
 struct QueryRow {
-    float v[N][4];
+    uint64_t v[N][2];                      // packed pairs
     __device__ __forceinline__ void load(const void* x, int64_t at, bool bf16, int sub) {
         if (!bf16) {
 #pragma unroll
             for (int j = 0; j < N; ++j) {
                 const float4 f = *reinterpret_cast<const float4*>((const float*)x + at + (j * 8 + sub) * 4);
-                v[j][0] = f.x; v[j][1] = f.y; v[j][2] = f.z; v[j][3] = f.w;
+                v[j][0] = dec::f2(f.x, f.y);
+                v[j][1] = dec::f2(f.z, f.w);
             }
         } else {
 #pragma unroll
             for (int j = 0; j < N; ++j) {
                 const uint2 u = *reinterpret_cast<const uint2*>((const uint16_t*)x + at + (j * 8 + sub) * 4);
-                v[j][0] = __uint_as_float(u.x << 16); v[j][1] = __uint_as_float(u.x & 0xffff0000u);
-                v[j][2] = __uint_as_float(u.y << 16); v[j][3] = __uint_as_float(u.y & 0xffff0000u);
+                v[j][0] = dec::f2(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u));
+                v[j][1] = dec::f2(__uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
             }
         }
     }
     __device__ __forceinline__ float squares() const {
-        float s = 0.f;
+        uint64_t a = dec::f2_mul(v[0][0], v[0][0]), b = dec::f2_mul(v[0][1], v[0][1]);
 #pragma unroll
-        for (int j = 0; j < N; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s = fmaf(v[j][i], v[j][i], s);
+        for (int j = 1; j < N; ++j) {
+            a = dec::f2_fma(v[j][0], v[j][0], a);
+            b = dec::f2_fma(v[j][1], v[j][1], b);
+        }
+        const float2 t = dec::f2_unpack(dec::f2_add(a, b));
+        float s = t.x + t.y;
 #pragma unroll
         for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
         return s;
     }
-    __device__ __forceinline__ float scale(float a, const float* gain, int sub) {
-        float top = 0.f;
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-            const float4 g = *reinterpret_cast<const float4*>(gain + (j * 8 + sub) * 4);
-            v[j][0] *= a * g.x; v[j][1] *= a * g.y; v[j][2] *= a * g.z; v[j][3] *= a * g.w;
-            top = max3(max3(top, fabsf(v[j][0]), fabsf(v[j][1])), fabsf(v[j][2]), fabsf(v[j][3]));
-        }
-        return top;
-    }
-    __device__ __forceinline__ void store(uint8_t* dst, int row, float f, int sub) const {
+    __device__ __forceinline__ void store(float a, const float* gain, uint8_t* dst, int row, int sub) const {
+        const uint64_t a2 = dec::f2(a, a);
 #pragma unroll
         for (int j = 0; j < N; ++j) {
             const int col = (j * 8 + sub) * 4;
-            *reinterpret_cast<uint2*>(dst + (col >> 6) * kBlock + sw128_offset(row, col & 63)) =
-                make_uint2(pack_f16(v[j][0] * f, v[j][1] * f), pack_f16(v[j][2] * f, v[j][3] * f));
+            const ulonglong2 g = *reinterpret_cast<const ulonglong2*>(gain + col);
+            const float2 lo = dec::f2_unpack(dec::f2_mul(dec::f2_mul(v[j][0], a2), g.x)), hi = dec::f2_unpack(dec::f2_mul(dec::f2_mul(v[j][1], a2), g.y));
+            *reinterpret_cast<uint2*>(dst + (col >> 6) * kBlock + sw128_offset(row, col & 63)) = make_uint2(pack_f16(lo.x, lo.y), pack_f16(hi.x, hi.y));
         }
     }
 };
 
 template <int DH, int DR>
-struct QueryRows {
+__device__ __forceinline__ void query_rows(const Params& p, const Piece& s, const float* gain, int rt, uint8_t* dst, int lane) {
+    const int sub = lane & 7;
+    rt += lane >> 3;
+    const int i = rt >> p.hp_log;
+    const int64_t row = s.row0 + (i < s.queries ? i : 0), head = (int64_t)s.unit * p.hp + (rt & (p.hp - 1));
     QueryRow<DH / 32> x;
     QueryRow<DR / 32> y;
-    __device__ __forceinline__ void load(const Params& p, const Piece& s, int rt, int lane) {
-        rt += lane >> 3;
-        const int i = rt >> p.hp_log;
-        const int64_t row = s.row0 + (i < s.queries ? i : 0), head = (int64_t)s.unit * p.hp + (rt & (p.hp - 1));
-        x.load(p.q, row * p.q_row + head * p.q_head, p.q_bf16, lane & 7);
-        y.load(p.q_rope, row * p.qr_row + head * p.qr_head, p.q_bf16, lane & 7);
-    }
-    __device__ __forceinline__ float finish(const Params& p, const float* gain, int rt, uint8_t* dst, int lane) {
-        const int sub = lane & 7;
-        rt += lane >> 3;
-        const float ax = rsqrtf(x.squares() / DH + p.eps), ay = rsqrtf(y.squares() / DR + p.eps);
-        float top = fmaxf(x.scale(ax, gain, sub), y.scale(ay, gain + DH, sub));
-#pragma unroll
-        for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        // the exponent of a normal number; 0 for zero, infinity and NaN
-        const int bits = __float_as_int(top) >> 23;
-        const int e = bits > 0 && bits < 255 ? min(max(bits - 127, -100), 100) : 0;
-        const float f = pow2i(-e);
-        x.store(dst, rt & 127, f, sub);
-        y.store(dst + DH / 64 * kBlock, rt & 127, f, sub);
-        return p.scale_log2 * pow2i(e);
-    }
-};
+    x.load(p.q, row * p.q_row + head * p.q_head, p.q_bf16, sub);
+    y.load(p.q_rope, row * p.qr_row + head * p.qr_head, p.q_bf16, sub);
+    x.store(rsqrtf(x.squares() / DH + p.eps), gain, dst, rt & 127, sub);
+    y.store(rsqrtf(y.squares() / DR + p.eps), gain + DH, dst + DH / 64 * kBlock, rt & 127, sub);
+}
 
 // ---- softmax of a tile's row: weights in place of logits ----
 // 64 columns of the row together with their maximum (a reduction in the load, on sm_103a).
@@ -302,8 +286,20 @@ __global__ void __launch_bounds__(kThreadsA, 1) prefill_attend_kernel(const __gr
         tmem_alloc(&sh->tmem, 512);
         tmem_relinquish();
     }
-    for (int i = tid; i < DH + DR; i += kThreadsA)
-        sh->gain[i] = i < DH ? p.gamma_q[i] * p.gamma_k[i] : p.gamma_rope ? p.gamma_rope[i - DH] : 1.f;
+    if (warp == 10) {
+        float g[(DH + DR) / 32], top = 0.f;
+#pragma unroll
+        for (int i = 0; i < (DH + DR) / 32; ++i) {
+            const int j = i * 32 + lane;
+            g[i] = j < DH ? p.gamma_q[j] * p.gamma_k[j] : p.gamma_rope ? p.gamma_rope[j - DH] : 1.f;
+            if (isfinite(g[i])) top = fmaxf(top, fabsf(g[i]));
+        }
+        top = warp_max(top);
+        const int e = top > 0.f ? min(max(ilogbf(top), -100), 100) : 0;
+#pragma unroll
+        for (int i = 0; i < (DH + DR) / 32; ++i) sh->gain[i * 32 + lane] = g[i] * pow2i(-e);
+        if (lane == 0) sh->factor = p.scale_log2 * pow2i(e);
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -596,15 +592,9 @@ give_up:
             if (k == 0) continue;
             if (s.t0 < s.t1) {
                 const int rows = min(s.queries * p.hp, kRowsQ);
-                const size_t buf = 2 * cta + (k & 1);
-                uint8_t* dst = p.qs + buf * (2 * kHalf);
+                uint8_t* dst = p.qs + (size_t)(2 * cta + (k & 1)) * (2 * kHalf);
 #pragma unroll 1
-                for (int rt = (warp - 10) * 4; rt < rows; rt += kConverters * 4) {
-                    QueryRows<DH, DR> four;
-                    four.load(p, s, rt, lane);
-                    const float c = four.finish(p, sh->gain, rt, dst + (rt >> 7) * kHalf, lane);
-                    if ((lane & 7) == 0) p.qcs[buf * kRowsQ + rt + (lane >> 3)] = c;
-                }
+                for (int rt = (warp - 10) * 4; rt < rows; rt += kConverters * 4) query_rows<DH, DR>(p, s, sh->gain, rt, dst + (rt >> 7) * kHalf, lane);
                 asm volatile("fence.proxy.async.global;" ::: "memory");
             }
             __syncwarp();
@@ -620,6 +610,7 @@ give_up:
         const int* we = reinterpret_cast<const int*>(p.weights);
         uint32_t s_phase = 0, o_phase = 0;
         int tiles = 0;                                                  // token tiles of the CTA so far
+        const float c = sh->factor;
         bool ok = true;
         for (int k = 0;; ++k) {
             ok = wait_or_fail(&sh->piece_full[k & 1], (k >> 1) & 1, sh, p.status);
@@ -628,17 +619,10 @@ give_up:
             const Piece& s = sh->piece[k & 1];                          // (read where it is needed: registers are few)
             if (s.unit < 0) break;
             const bool mine = h == 0 || s.queries * p.hp > 128;         // uniform in a warp
-            float c = 0.f;
             if (mine && k == 0 && s.t0 < s.t1) {
                 // the first piece's queries, straight to shared memory: a warp its own 32 rows
 #pragma unroll 1
-                for (int q = 0; q < 32; q += 4) {
-                    QueryRows<DH, DR> rows;
-                    rows.load(p, s, warp * 32 + q, lane);
-                    const float f = rows.finish(p, sh->gain, warp * 32 + q, sm + h * kHalf, lane);
-                    const float g = __shfl_sync(0xffffffffu, f, (lane & 3) * 8);
-                    if ((lane >> 2) == (q >> 2)) c = g;
-                }
+                for (int q = 0; q < 32; q += 4) query_rows<DH, DR>(p, s, sh->gain, warp * 32 + q, sm + h * kHalf, lane);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh->q0_full[h]);
@@ -651,6 +635,8 @@ give_up:
             if (!mine) tiles += s.t1 - s.t0;
             for (int t = s.t0; t < s.t1 && mine; ++t, ++tiles) {
                 const int first = tile_at(t) * kTile;
+                // tiles that some row does not see whole (uniform over the tile's rows)
+                const bool edge = first + kTile > s.n_lo || (p.window > 0 && first < s.n_lo + s.queries - 1 - p.window && first + kTile > p.sinks);
                 ok = wait_or_fail(&sh->s_full[h], s_phase, sh, p.status);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
@@ -658,16 +644,13 @@ give_up:
                 tc_fence_after();
                 const int info = sh->info[tiles & 3], e = (info & 255) - 64;
                 const bool as_bf = (info & 256) != 0;
-                if (t == s.t0 && k > 0) c = *(volatile const float*)&p.qcs[(size_t)(2 * cta + (k & 1)) * kRowsQ + rt];
-                // tiles that some row does not see whole (uniform over the tile's rows)
-                const bool edge = first + kTile > s.n_lo || (p.window > 0 && first < s.n_lo + s.queries - 1 - p.window && first + kTile > p.sinks);
-                const int end = n_row - first, from = p.window > 0 ? end - p.window : 0, sink = p.window > 0 ? p.sinks - first : 0;
                 float x[128], top, top2;
                 tmem_ld64_max(t_s, x, top);
                 tmem_ld64_max(t_s + 64, x + 64, top2);
                 tmem_wait_ld();
                 top = fmaxf(top, top2);
                 if (edge) {
+                    const int end = n_row - first, from = p.window > 0 ? end - p.window : 0, sink = p.window > 0 ? p.sinks - first : 0;
                     top = -INFINITY;
 #pragma unroll
                     for (int q = 0; q < 128; q += 32) {
@@ -738,11 +721,12 @@ give_up:
 #pragma unroll
                             for (int w = 0; w < 8; ++w) dst[w] = make_float4(o[4 * w], o[4 * w + 1], o[4 * w + 2], o[4 * w + 3]);
                         } else {
-                            uint4* dst = reinterpret_cast<uint4*>((uint16_t*)p.o + to + q);
+                            uint16_t* dst = (uint16_t*)p.o + to + q;
+                            uint32_t w[16];
 #pragma unroll
-                            for (int w = 0; w < 4; ++w)
-                                dst[w] = make_uint4(pack_bf16(o[8 * w], o[8 * w + 1]), pack_bf16(o[8 * w + 2], o[8 * w + 3]),
-                                                                                  pack_bf16(o[8 * w + 4], o[8 * w + 5]), pack_bf16(o[8 * w + 6], o[8 * w + 7]));
+                            for (int r2 = 0; r2 < 16; ++r2) w[r2] = pack_bf16(o[2 * r2], o[2 * r2 + 1]);
+                            st_global_v8(dst, *reinterpret_cast<const uint32_t(*)[4]>(w), *reinterpret_cast<const uint32_t(*)[4]>(w + 4));
+                            st_global_v8(dst + 16, *reinterpret_cast<const uint32_t(*)[4]>(w + 8), *reinterpret_cast<const uint32_t(*)[4]>(w + 12));
                         }
                     }
                 }
@@ -806,31 +790,29 @@ __global__ void __launch_bounds__(kThreadsJ) prefill_join_kernel(const __grid_co
     const int n_cta = sharing(p, all);
     const int k = blockIdx.x + 1;
     if (all == 0 || k >= n_cta) return;
-    const Place at = place_of(p, share_start(all, n_cta, k), one);
+    // the boundaries from k - 1 on, a thread each
+    __shared__ Place places[kMaxCtas + 1];
+    __shared__ int parts[kMaxCtas];
+    __shared__ int count;
+    for (int q = k - 1 + threadIdx.x; q <= n_cta; q += kThreadsJ) places[q] = place_of_one(p, share_start(all, n_cta, q), one);
+    __syncthreads();
+    const Place at = places[k];
     if (!at.inside()) return;
     if (k > 1) {
-        const Place prev = place_of(p, share_start(all, n_cta, k - 1), one);
+        const Place prev = places[k - 1];
         if (prev.inside() && prev.u == at.u && prev.j == at.j) return;
     }
     // parts: CTA k - 1's last piece, then the first pieces of CTAs k .. last - 1 (one that got no tile has none)
-    __shared__ int parts[160];
-    __shared__ int count;
-    if (threadIdx.x < 32) {
-        int n = 0;
-        if (threadIdx.x == 0) parts[0] = 2 * (k - 1) + 1;
-        n = 1;
-        Place from = at;
+    if (threadIdx.x == 0) {
+        parts[0] = 2 * (k - 1) + 1;
+        int n = 1;
         for (int q = k; q < n_cta; ++q) {
-            const Place to = place_of(p, share_start(all, n_cta, q + 1), one);
+            const Place to = places[q + 1];
             const bool same = to.u == at.u && to.j == at.j && to.t < at.nt;
-            if (!(same && to.t == from.t)) {
-                if (threadIdx.x == 0) parts[n] = 2 * q;
-                ++n;
-            }
+            if (!(same && to.t == places[q].t)) parts[n++] = 2 * q;
             if (!same) break;
-            from = to;
         }
-        if (threadIdx.x == 0) count = n;
+        count = n;
     }
     __syncthreads();
     const int n = count;
@@ -946,7 +928,7 @@ int make_params(const qkmla_prefill_args* a, bool sizes_only, pf::Params* p, siz
     p->max_tiles = (int)(a->total_tokens / pf::kTile) + a->B;
     p->ctas = device_sm_count();
     if (p->ctas <= 0) return QKMLA_ERR_CUDA;
-    if (p->ctas > 158) p->ctas = 158;                      // the join's list of parts
+    if (p->ctas > pf::kMaxCtas) p->ctas = pf::kMaxCtas;
     uintptr_t at = (uintptr_t)a->workspace;
     auto take = [&](size_t n) {
         const uintptr_t r = at;
@@ -959,7 +941,6 @@ int make_params(const qkmla_prefill_args* a, bool sizes_only, pf::Params* p, siz
     p->pre = (int64_t*)take(8 * (nq + 1));
     p->tinfo = (int*)take(4 * tiles);
     p->part_ml = (float2*)take(sizeof(float2) * 2 * p->ctas * pf::kRowsQ);
-    p->qcs = (float*)take(4 * (size_t)2 * p->ctas * pf::kRowsQ);
     p->part_o = (float*)take(4 * (size_t)2 * p->ctas * pf::kRowsQ * a->d_v);
     p->krope = (uint8_t*)take(tiles * pf::kBlock);
     p->kc = (uint8_t*)take(tiles * a->G * (a->d_h / 64) * pf::kBlock);
@@ -974,7 +955,8 @@ int make_params(const qkmla_prefill_args* a, bool sizes_only, pf::Params* p, siz
     if (!a->q || !a->q_rope || !a->gamma_q || !a->gamma_k || !a->weights || !a->kv_cache || !a->ak_cache || !a->chunk_start ||
         !a->seq_lens || !a->o)
         return QKMLA_ERR_INVALID;
-    for (const void* ptr : {a->q, a->q_rope, a->weights, a->kv_cache, (const void*)a->o})
+    if ((uintptr_t)a->o % 32) return QKMLA_ERR_INVALID;
+    for (const void* ptr : {a->q, a->q_rope, a->weights, a->kv_cache})
         if ((uintptr_t)ptr % 16) return QKMLA_ERR_INVALID;
     for (const void* ptr : {(const void*)a->gamma_q, (const void*)a->gamma_k, (const void*)a->gamma_rope_q, (const void*)a->kv_scale,
                             (const void*)a->chunk_start, (const void*)a->seq_lens, (const void*)a->page_table, (const void*)a->lse})

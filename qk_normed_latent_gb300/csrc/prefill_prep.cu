@@ -215,12 +215,6 @@ __device__ __forceinline__ TileOf locate(const Params& p, int tile) {
     return TileOf{0, 0, 0, false};
 }
 
-__device__ __forceinline__ void st_global_v8(void* p, const uint32_t (&a)[4], const uint32_t (&b)[4]) {
-    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]),
-                 "r"(b[1]), "r"(b[2]), "r"(b[3])
-                 : "memory");
-}
-
 // NV: vectors of 8 latents a lane, d_c up to 256 NV; at 1 two CTAs fit on an SM, one gathering while the other multiplies.
 template <bool Q8, int NV>
 __global__ void __launch_bounds__(kThreadsE, NV == 1 ? 2 : 1) prefill_expand_kernel(const __grid_constant__ Params p, int splits) {
