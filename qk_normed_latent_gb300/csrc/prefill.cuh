@@ -89,6 +89,7 @@ __device__ __forceinline__ Place place_of(const Params& p, int64_t x, int64_t on
     if (r.u >= p.units) { r.u = p.units; r.j = 0; r.t = 0; r.nt = 0; return r; }
     const int64_t y = x - (int64_t)r.u * one;
     int lo = 0, n = p.nq;                                  // the last j in [lo, lo + n) with pre[j] <= y
+#pragma unroll 1
     while (n > 1) {
         const int step = (n + 31) / 32;
         const int at = lo + lane * step;
@@ -115,6 +116,7 @@ __device__ __forceinline__ Place place_of_one(const Params& p, int64_t x, int64_
     if (r.u >= p.units) { r.u = p.units; r.j = 0; r.t = 0; r.nt = 0; return r; }
     const int64_t y = x - (int64_t)r.u * one;
     int lo = 0, hi = p.nq - 1;
+#pragma unroll 1
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (p.pre[mid] <= y) lo = mid;

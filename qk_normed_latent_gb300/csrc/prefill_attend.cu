@@ -76,11 +76,12 @@ constexpr int smem_bytes() { return (2 * (DH / 64 + 1) + kUnits) * kBlock + 1024
 
 // One CTA's part of the list.
 struct Walk {
-    Place at, end;
+    Place at, end = {};
     bool first;
 
     // The next piece; false at the end.
     __device__ __forceinline__ bool next(const Params& p, Piece& s) {
+#pragma unroll 1
         for (;;) {
             if (at.u > end.u || (at.u == end.u && at.j > end.j) || at.u >= p.units) return false;
             const bool last = at.u == end.u && at.j == end.j;
@@ -118,24 +119,45 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return y;
 }
 
-// Every wait ends by itself: in success, because another warp gave up, or after kWaitNs.  (Named barriers cannot be
-// used where a thread may have given up.)
-__device__ __forceinline__ bool wait_or_fail(uint64_t* bar, uint32_t parity, Shared* sh, int* status) {
-    uint64_t t0 = 0;
-    for (uint32_t i = 1;; ++i) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if ((i & 63u) == 0) {
-            if (*(volatile int*)&sh->fail) return false;
-            const uint64_t t = dec::globaltimer();
-            if (t0 == 0) t0 = t;
-            if (t - t0 > dec::kWaitNs) {
-                report(status, QKMLA_ERR_TIMEOUT);
-                *(volatile int*)&sh->fail = 1;
-                return false;
-            }
+// Every wait ends by itself, after kSpins tries (each of 50 ns or more); a warp that gives up says so and leaves, and the
+// others' waits end likewise.  (Named barriers cannot be used where a thread may have given up.)  Small on purpose: beyond
+// some 64 KB of code the instruction cache misses and every warp slows down to 5 cycles an instruction and more.
+constexpr uint32_t kSpins = 1u << 22;
+__device__ __forceinline__ bool wait_or_fail(uint64_t* bar, uint32_t parity, Shared* sh) {
+    uint32_t i = 0;
+#pragma unroll 1
+    while (!mbar_try_wait(bar, parity))
+        if (++i == kSpins) {
+            *(volatile int*)&sh->fail = 1;
+            return false;
         }
-    }
+    return true;
 }
+
+// ---- products ----
+// Descriptors as their low word (address and leading offset) and a high word common to all (rows of 128 bytes, 8-row
+// groups 1024 apart): the products then take 8 machine instructions each where 64-bit descriptors took 16, and the issue's
+// code half the room.
+constexpr uint32_t kDescHigh = (1024u >> 4) | 1u << 14 | kSwizzle128B << 29;
+__device__ __forceinline__ uint32_t desc_low(const void* at, uint32_t lbo) { return (smem_u32(at) >> 4) | lbo >> 4 << 16; }
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tmov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}"
+        ::"r"(d), "r"(a), "r"(b), "r"(kDescHigh), "r"(idesc), "r"(acc)
+        : "memory");
+}
+// A out of TMEM.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tmov.b64 b, {%2, %3};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}"
+        ::"r"(d), "r"(a), "r"(b), "r"(kDescHigh), "r"(idesc), "r"(acc)
+        : "memory");
+}
+
 // ---- queries ----
 // Four rows of a query tile, rt .. rt + 3, eight lanes a row: normalised and times the gains as fp16 to row rt & 127 of
 // the half at `dst` (blocks of 64 columns).  Normalised values are at most sqrt d; the gains come with a power of two that
@@ -259,7 +281,8 @@ __global__ void __launch_bounds__(kThreadsA, 1) prefill_attend_kernel(const __gr
     uint8_t* sm = smraw + ((1024u - (smem_u32(smraw) & 1023u)) & 1023u);
     uint8_t* ring = sm + 2 * kHalf;
     Shared* sh = reinterpret_cast<Shared*>(ring + kUnits * kBlock);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // (the warp's number by a shuffle: the compiler then knows that a role's branches and addresses are the warp's)
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int cta = blockIdx.x;
 
     if (tid == 0) {
@@ -323,14 +346,16 @@ __global__ void __launch_bounds__(kThreadsA, 1) prefill_attend_kernel(const __gr
             bool ok = true;
             auto put = [&](const uint8_t* a, int na, const uint8_t* b2, int nb) {      // a group: na blocks at a, nb at b2
                 const int n = na + nb;
+#pragma unroll 1
                 while (ok && unit + n - kUnits > freed_units) {
-                    ok = wait_or_fail(&sh->empty[freed % kGroups], (freed / kGroups) & 1, sh, p.status);
+                    ok = wait_or_fail(&sh->empty[freed % kGroups], (freed / kGroups) & 1, sh);
                     freed_units += (freed & 1) ? VU : KU;
                     ++freed;
                 }
                 if (!ok) return;
                 uint64_t* bar = &sh->full[group % kGroups];
                 mbar_arrive_expect_tx(bar, n * kBlock);
+#pragma unroll 1
                 for (int i = 0; i < n; ++i) {
                     bulk_load(ring + (unit % kUnits) * kBlock, i < na ? a + (size_t)i * kBlock : b2 + (size_t)(i - na) * kBlock, kBlock, bar);
                     ++unit;
@@ -338,8 +363,9 @@ __global__ void __launch_bounds__(kThreadsA, 1) prefill_attend_kernel(const __gr
                 ++group;
                 *(volatile int*)&sh->issued = group;
             };
+#pragma unroll 1
             for (int k = 0; ok; ++k) {
-                ok = wait_or_fail(&sh->piece_full[k & 1], (k >> 1) & 1, sh, p.status);
+                ok = wait_or_fail(&sh->piece_full[k & 1], (k >> 1) & 1, sh);
                 if (!ok) break;
                 const Piece s = sh->piece[k & 1];
                 if (s.unit < 0) break;
@@ -356,13 +382,14 @@ __global__ void __launch_bounds__(kThreadsA, 1) prefill_attend_kernel(const __gr
                 };
                 if (s.t0 < s.t1) key(s.t0);
                 // a query half is read by the products until the last ones of the piece ahead have ended
+#pragma unroll 1
                 for (int h = 0; h < 2 && ok; ++h) {
                     if (h < last_halves) {
-                        ok = wait_or_fail(&sh->q_empty[h], (qe_phase >> h) & 1, sh, p.status);
+                        ok = wait_or_fail(&sh->q_empty[h], (qe_phase >> h) & 1, sh);
                         qe_phase ^= 1u << h;
                     }
                     if (!ok || s.t0 == s.t1 || h >= halves || k == 0) continue;       // (the first piece's rows go to shared memory directly)
-                    if (h == 0) ok = wait_or_fail(&sh->conv_full[k & 1], ((k - 1) >> 1) & 1, sh, p.status);
+                    if (h == 0) ok = wait_or_fail(&sh->conv_full[k & 1], ((k - 1) >> 1) & 1, sh);
                     if (!ok) break;
                     mbar_arrive_expect_tx(&sh->q_full[h], kHalf);
                     bulk_load(sm + h * kHalf, p.qs + ((size_t)(2 * cta + (k & 1)) * 2 + h) * kHalf, kHalf, &sh->q_full[h]);
@@ -371,6 +398,7 @@ __global__ void __launch_bounds__(kThreadsA, 1) prefill_attend_kernel(const __gr
                 if (k > 0) mbar_arrive(&sh->piece_empty[(k - 1) & 1]);                // the converted rows of piece k - 1 are no longer read
                 if (s.t0 < s.t1) last_halves = halves;
                 else if (last_halves) last_halves = 0;
+#pragma unroll 1
                 for (int t = s.t0; t < s.t1 && ok; ++t) {
                     const size_t tile = tile_at(t);
                     put(p.v + (tile * p.Gv + gv) * (size_t)(VU * kBlock), VU, nullptr, 0);
@@ -387,9 +415,9 @@ __global__ void __launch_bounds__(kThreadsA, 1) prefill_attend_kernel(const __gr
         constexpr uint32_t id_o = idesc_bf16(128, DV, 0, 1) & ~bf;
         // descriptors are formed once and moved by offsets: the issue has to keep up with 65 cycles a product
         constexpr uint32_t kStep = kBlock >> 4;
-        const uint64_t q_desc = smem_desc(smem_u32(sm), 16, 1024, kSwizzle128B);
-        const uint64_t k_desc = smem_desc(smem_u32(ring), 16, 1024, kSwizzle128B);
-        const uint64_t v_desc = smem_desc(smem_u32(ring), kBlock / 2, 1024, kSwizzle128B);   // 64 tokens, 64-column boxes 8 KB apart
+        const uint32_t q_desc = desc_low(sm, 16);
+        const uint32_t k_desc = desc_low(ring, 16);
+        const uint32_t v_desc = desc_low(ring, kBlock / 2);   // 64 tokens, 64-column boxes 8 KB apart
         int group = 0, unit = 0, k = 0;                    // groups and blocks consumed, pieces fetched
         uint32_t p_phase = 0, q_phase = 0;                 // bit h (arrays would lie in local memory)
         int halves = 0, left = 0, q_at = 0;                // of the piece whose logits come next: tiles left, its place in the queue
@@ -402,7 +430,7 @@ __global__ void __launch_bounds__(kThreadsA, 1) prefill_attend_kernel(const __gr
             // the next piece (halves -1: there is none); with weights awaited no more than one, which may have no tiles:
             // the one behind it is not listed before they have been used
             while (left == 0 && halves >= 0) {
-                if (!wait_or_fail(&sh->piece_full[k & 1], (k >> 1) & 1, sh, p.status)) goto give_up;
+                if (!wait_or_fail(&sh->piece_full[k & 1], (k >> 1) & 1, sh)) goto give_up;
                 const Piece& s = sh->piece[k & 1];
                 if (s.unit < 0) { halves = -1; break; }
                 left = s.t1 - s.t0;
@@ -422,10 +450,10 @@ __global__ void __launch_bounds__(kThreadsA, 1) prefill_attend_kernel(const __gr
                 // The same rounds in a straight line, to the piece's end.  The unit takes six or so products ahead; each
                 // barrier is looked at, and the next round's operands are formed, while products are still being taken (a
                 // wait that succeeds at once costs as much as two of them).
-                auto value = [&](int u) { return v_desc + (uint64_t)((u % kUnits) * kStep); };
-                uint64_t v0 = value(unit), v1 = VU == 2 ? value(unit + 1) : v0 + kStep / 2, kd[KU];
+                auto value = [&](int u) { return v_desc + (uint32_t)((u % kUnits) * kStep); };
+                uint32_t v0 = value(unit), v1 = VU == 2 ? value(unit + 1) : v0 + kStep / 2, kd[KU];
 #pragma unroll
-                for (int blk = 0; blk < KU; ++blk) kd[blk] = k_desc + (uint64_t)(((unit + VU + blk) % kUnits) * kStep);
+                for (int blk = 0; blk < KU; ++blk) kd[blk] = k_desc + (uint32_t)(((unit + VU + blk) % kUnits) * kStep);
                 uint32_t acc = cur_first ? 0u : 1u, id = id_o | fmt;
                 uint64_t *b_v = &sh->full[gv % kGroups], *b_k = &sh->full[gk % kGroups], *f_v = &sh->empty[gv % kGroups], *f_k = &sh->empty[gk % kGroups];
                 uint32_t ph_v = (gv / kGroups) & 1, ph_k = (gk / kGroups) & 1, ph = p_phase & 1;       // (both halves' phases are alike in a piece of two)
@@ -434,30 +462,31 @@ __global__ void __launch_bounds__(kThreadsA, 1) prefill_attend_kernel(const __gr
                 unit += VU + KU;
                 bool seen_a = false, seen_v = false, seen_1 = false;
                 for (;;) {
-                    uint64_t v0n, v1n, kn[KU], *b_vn, *b_kn, *f_vn, *f_kn;
+                    uint32_t v0n, v1n, kn[KU];
+                    uint64_t *b_vn, *b_kn, *f_vn, *f_kn;
                     uint32_t ph_vn, ph_kn, idn;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const uint32_t o = tmem + kO + h * 128, a = tmem + kS + h * 128, d = a;
                         const uint32_t php = h ? ph1 : ph;
-                        if (!(h == 0 ? seen_a : seen_1) && !wait_or_fail(&sh->pa_full[h], php, sh, p.status)) goto give_up;
-                        if (h == 0 && !seen_v && !wait_or_fail(b_v, ph_v, sh, p.status)) goto give_up;
+                        if (!(h == 0 ? seen_a : seen_1) && !wait_or_fail(&sh->pa_full[h], php, sh)) goto give_up;
+                        if (h == 0 && !seen_v && !wait_or_fail(b_v, ph_v, sh)) goto give_up;
                         tc_fence_after();
-                        mma_bf16_tmem_a(o, a, v0, id, acc);
-                        mma_bf16_tmem_a(o, a + 8, v0 + 128, id, 1u);
+                        mma_ts(o, a, v0, id, acc);
+                        mma_ts(o, a + 8, v0 + 128, id, 1u);
                         const bool seen_b = mbar_test_wait(&sh->pb_full[h], php);
-                        mma_bf16_tmem_a(o, a + 16, v0 + 256, id, 1u);
-                        mma_bf16_tmem_a(o, a + 24, v0 + 384, id, 1u);
-                        if (!seen_b && !wait_or_fail(&sh->pb_full[h], php, sh, p.status)) goto give_up;
+                        mma_ts(o, a + 16, v0 + 256, id, 1u);
+                        mma_ts(o, a + 24, v0 + 384, id, 1u);
+                        if (!seen_b && !wait_or_fail(&sh->pb_full[h], php, sh)) goto give_up;
                         tc_fence_after();
-                        mma_bf16_tmem_a(o, a + 32, v1, id, 1u);
-                        mma_bf16_tmem_a(o, a + 40, v1 + 128, id, 1u);
+                        mma_ts(o, a + 32, v1, id, 1u);
+                        mma_ts(o, a + 40, v1 + 128, id, 1u);
                         bool seen_k = true;
                         if (h == 0) seen_k = mbar_test_wait(b_k, ph_k);
-                        mma_bf16_tmem_a(o, a + 48, v1 + 256, id, 1u);
-                        mma_bf16_tmem_a(o, a + 56, v1 + 384, id, 1u);
+                        mma_ts(o, a + 48, v1 + 256, id, 1u);
+                        mma_ts(o, a + 56, v1 + 384, id, 1u);
                         if (h == 1) mma_commit(f_v);
-                        if (!seen_k && !wait_or_fail(b_k, ph_k, sh, p.status)) goto give_up;
+                        if (!seen_k && !wait_or_fail(b_k, ph_k, sh)) goto give_up;
 #pragma unroll
                         for (int blk = 0; blk < KU; ++blk) {
                             if (blk == KU - 1) {            // one more block of products to come
@@ -468,7 +497,7 @@ __global__ void __launch_bounds__(kThreadsA, 1) prefill_attend_kernel(const __gr
                                     v0n = value(unit);
                                     v1n = VU == 2 ? value(unit + 1) : v0n + kStep / 2;
 #pragma unroll
-                                    for (int q = 0; q < KU; ++q) kn[q] = k_desc + (uint64_t)(((unit + VU + q) % kUnits) * kStep);
+                                    for (int q = 0; q < KU; ++q) kn[q] = k_desc + (uint32_t)(((unit + VU + q) % kUnits) * kStep);
                                     b_vn = &sh->full[gn % kGroups];
                                     b_kn = &sh->full[kg % kGroups];
                                     f_vn = &sh->empty[gn % kGroups];
@@ -482,7 +511,7 @@ __global__ void __launch_bounds__(kThreadsA, 1) prefill_attend_kernel(const __gr
                             }
 #pragma unroll
                             for (int kk = 0; kk < (blk < KU - 1 ? 4 : DR / 16); ++kk)
-                                mma_bf16(d, q_desc + (uint64_t)((h * KU + blk) * kStep + kk * 2), kd[blk] + (uint64_t)(kk * 2), id_s, (blk > 0 || kk > 0) ? 1u : 0u);
+                                mma_ss(d, q_desc + (uint32_t)((h * KU + blk) * kStep + kk * 2), kd[blk] + (uint32_t)(kk * 2), id_s, (blk > 0 || kk > 0) ? 1u : 0u);
                         }
                         mma_commit(&sh->s_full[h]);
                         if (left == 1) mma_commit(&sh->q_empty[h]);
@@ -512,25 +541,25 @@ __global__ void __launch_bounds__(kThreadsA, 1) prefill_attend_kernel(const __gr
                     const uint32_t o = tmem + kO + h * 128, a = tmem + kS + h * 128;
 #pragma unroll 1
                     for (int part = 0; part < 2; ++part) { // 64 tokens each
-                        if (!wait_or_fail(part ? &sh->pb_full[h] : &sh->pa_full[h], (p_phase >> h) & 1, sh, p.status)) goto give_up;
-                        if (h + part == 0 && !wait_or_fail(&sh->full[gv % kGroups], (gv / kGroups) & 1, sh, p.status)) goto give_up;
+                        if (!wait_or_fail(part ? &sh->pb_full[h] : &sh->pa_full[h], (p_phase >> h) & 1, sh)) goto give_up;
+                        if (h + part == 0 && !wait_or_fail(&sh->full[gv % kGroups], (gv / kGroups) & 1, sh)) goto give_up;
                         tc_fence_after();
-                        const uint64_t v = v_desc + (uint64_t)(VU == 2 ? ((unit + part) % kUnits) * kStep : (unit % kUnits) * kStep + part * (kStep / 2));
+                        const uint32_t v = v_desc + (uint32_t)(VU == 2 ? ((unit + part) % kUnits) * kStep : (unit % kUnits) * kStep + part * (kStep / 2));
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            mma_bf16_tmem_a(o, a + part * 32 + i * 8, v + (uint64_t)(i * 128), id_o | fmt, (!cur_first || part > 0 || i > 0) ? 1u : 0u);
+                            mma_ts(o, a + part * 32 + i * 8, v + (uint32_t)(i * 128), id_o | fmt, (!cur_first || part > 0 || i > 0) ? 1u : 0u);
                     }
                     p_phase ^= 1u << h;
                     if (h == cur - 1) mma_commit(&sh->empty[gv % kGroups]);
                     if (cur_last) mma_commit(&sh->o_full[h]);
                 }
                 if (h < nxt) {
-                    if (h == 0 && !wait_or_fail(&sh->full[gk % kGroups], (gk / kGroups) & 1, sh, p.status)) goto give_up;
+                    if (h == 0 && !wait_or_fail(&sh->full[gk % kGroups], (gk / kGroups) & 1, sh)) goto give_up;
                     if (first) {
                         if (q_at == 0) {
-                            if (!wait_or_fail(&sh->q0_full[h], 0, sh, p.status)) goto give_up;
+                            if (!wait_or_fail(&sh->q0_full[h], 0, sh)) goto give_up;
                         } else {
-                            if (!wait_or_fail(&sh->q_full[h], (q_phase >> h) & 1, sh, p.status)) goto give_up;
+                            if (!wait_or_fail(&sh->q_full[h], (q_phase >> h) & 1, sh)) goto give_up;
                             q_phase ^= 1u << h;
                         }
                     }
@@ -539,10 +568,10 @@ __global__ void __launch_bounds__(kThreadsA, 1) prefill_attend_kernel(const __gr
                     const uint32_t d = tmem + kS + h * 128;
 #pragma unroll
                     for (int blk = 0; blk < KU; ++blk) {
-                        const uint64_t kd = k_desc + (uint64_t)(((u + blk) % kUnits) * kStep), qd = q_desc + (uint64_t)((h * KU + blk) * kStep);
+                        const uint32_t kd = k_desc + (uint32_t)(((u + blk) % kUnits) * kStep), qd = q_desc + (uint32_t)((h * KU + blk) * kStep);
 #pragma unroll
                         for (int kk = 0; kk < (blk < KU - 1 ? 4 : DR / 16); ++kk)
-                            mma_bf16(d, qd + (uint64_t)(kk * 2), kd + (uint64_t)(kk * 2), id_s, (blk > 0 || kk > 0) ? 1u : 0u);
+                            mma_ss(d, qd + (uint32_t)(kk * 2), kd + (uint32_t)(kk * 2), id_s, (blk > 0 || kk > 0) ? 1u : 0u);
                     }
                     mma_commit(&sh->s_full[h]);
                     if (left == 1) mma_commit(&sh->q_empty[h]);
@@ -563,25 +592,32 @@ give_up:
       } else {
         // ---- the list, and the queries of every piece but the first ----
         Walk walk;
-        walk.at = place_of(p, share_start(all, n_cta, cta), one);
-        walk.end = place_of(p, share_start(all, n_cta, cta + 1), one);
+#pragma unroll 1
+        for (int i = 0; i < 2; ++i) {
+            walk.at = walk.end;
+            walk.end = place_of(p, share_start(all, n_cta, cta + i), one);
+        }
         walk.first = true;
         bool ok = true;
+#pragma unroll 1
         for (int k = 0;; ++k) {
             Piece s;
             if (!walk.next(p, s)) s.unit = -1;
             if (k > 0 && s.unit >= 0 && s.t0 < s.t1) {
                 // the raw rows into L2: reading them then takes its latency
                 const int row_bytes = p.q_bf16 ? 2 * DH : 4 * DH, rope_bytes = p.q_bf16 ? 2 * DR : 4 * DR, esz = p.q_bf16 ? 2 : 4;
+#pragma unroll 1
                 for (int rt = (warp - 10) * 32 + lane; rt < min(s.queries * p.hp, kRowsQ); rt += kConverters * 32) {
                     const int64_t row = s.row0 + (rt >> p.hp_log), head = (int64_t)s.unit * p.hp + (rt & (p.hp - 1));
                     const char* x = (const char*)p.q + (row * p.q_row + head * p.q_head) * esz;
                     const char* y = (const char*)p.q_rope + (row * p.qr_row + head * p.qr_head) * esz;
+#pragma unroll 1
                     for (int i = 0; i < row_bytes; i += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(x + i));
+#pragma unroll 1
                     for (int i = 0; i < rope_bytes; i += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(y + i));
                 }
             }
-            if (k >= 2) ok = wait_or_fail(&sh->piece_empty[k & 1], ((k >> 1) - 1) & 1, sh, p.status);
+            if (k >= 2) ok = wait_or_fail(&sh->piece_empty[k & 1], ((k >> 1) - 1) & 1, sh);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             if (warp == 10 && lane == 0) {
@@ -612,8 +648,9 @@ give_up:
         int tiles = 0;                                                  // token tiles of the CTA so far
         const float c = sh->factor;
         bool ok = true;
+#pragma unroll 1
         for (int k = 0;; ++k) {
-            ok = wait_or_fail(&sh->piece_full[k & 1], (k >> 1) & 1, sh, p.status);
+            ok = wait_or_fail(&sh->piece_full[k & 1], (k >> 1) & 1, sh);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             const Piece& s = sh->piece[k & 1];                          // (read where it is needed: registers are few)
@@ -633,11 +670,12 @@ give_up:
             float m = -INFINITY, sum = 0.f;
             auto tile_at = [&](int t) { return t < s.head ? t : t + s.gap; };
             if (!mine) tiles += s.t1 - s.t0;
+#pragma unroll 1
             for (int t = s.t0; t < s.t1 && mine; ++t, ++tiles) {
                 const int first = tile_at(t) * kTile;
                 // tiles that some row does not see whole (uniform over the tile's rows)
                 const bool edge = first + kTile > s.n_lo || (p.window > 0 && first < s.n_lo + s.queries - 1 - p.window && first + kTile > p.sinks);
-                ok = wait_or_fail(&sh->s_full[h], s_phase, sh, p.status);
+                ok = wait_or_fail(&sh->s_full[h], s_phase, sh);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 s_phase ^= 1;
@@ -692,7 +730,7 @@ give_up:
                 if (lane == 0) mbar_arrive(&sh->piece_empty[k & 1]);
                 continue;
             }
-            if (s.t0 < s.t1 && ok) ok = wait_or_fail(&sh->o_full[h], o_phase, sh, p.status);
+            if (s.t0 < s.t1 && ok) ok = wait_or_fail(&sh->o_full[h], o_phase, sh);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             if (s.t0 < s.t1) {
@@ -755,9 +793,9 @@ give_up:
     __syncthreads();
     if (busy) {
         // a CTA that gave up waits for its copies in flight, and always for its products
-        wait_or_fail(&sh->done, 0, sh, p.status);
+        wait_or_fail(&sh->done, 0, sh);
         if (*(volatile int*)&sh->fail && tid == 0) {
-            dec::wait_bounded(&sh->done, 0, p.status);
+            report(p.status, QKMLA_ERR_TIMEOUT);
             const int n = *(volatile int*)&sh->issued;
             for (int g = max(0, n - kGroups); g < n; ++g) dec::wait_bounded(&sh->full[g % kGroups], (g / kGroups) & 1, p.status);
             for (int h = 0; h < 2; ++h) {
