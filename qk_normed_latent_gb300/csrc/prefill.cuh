@@ -148,6 +148,44 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 // 2^e as an exact float, e in [-126, 127]
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
 
+// Every wait ends by itself, after kSpins tries (each of 50 ns or more); a warp that gives up says so and leaves, and the
+// others' waits end likewise.  (Named barriers cannot be used where a thread may have given up.)  Small on purpose: beyond
+// some 64 KB of code the instruction cache misses and every warp slows down to 5 cycles an instruction and more.
+constexpr uint32_t kSpins = 1u << 22;
+__device__ __forceinline__ bool wait_or_fail(uint64_t* bar, uint32_t parity, int* fail) {
+    uint32_t i = 0;
+#pragma unroll 1
+    while (!tc::mbar_try_wait(bar, parity))
+        if (++i == kSpins) {
+            *(volatile int*)fail = 1;
+            return false;
+        }
+    return true;
+}
+
+// Descriptors as their low word (address and leading offset) and a high word common to all (rows of 128 bytes, 8-row
+// groups 1024 apart): the products then take 8 machine instructions each where 64-bit descriptors took 16, and the issue's
+// code half the room.
+constexpr uint32_t kDescHigh = (1024u >> 4) | 1u << 14 | tc::kSwizzle128B << 29;
+__device__ __forceinline__ uint32_t desc_low(const void* at, uint32_t lbo) { return (tc::smem_u32(at) >> 4) | lbo >> 4 << 16; }
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tmov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}"
+        ::"r"(d), "r"(a), "r"(b), "r"(kDescHigh), "r"(idesc), "r"(acc)
+        : "memory");
+}
+// A out of TMEM.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tmov.b64 b, {%2, %3};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}"
+        ::"r"(d), "r"(a), "r"(b), "r"(kDescHigh), "r"(idesc), "r"(acc)
+        : "memory");
+}
+
 __device__ __forceinline__ void st_global_v8(void* p, const uint32_t (&a)[4], const uint32_t (&b)[4]) {
     asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]),
                  "r"(b[1]), "r"(b[2]), "r"(b[3])

@@ -119,45 +119,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return y;
 }
 
-// Every wait ends by itself, after kSpins tries (each of 50 ns or more); a warp that gives up says so and leaves, and the
-// others' waits end likewise.  (Named barriers cannot be used where a thread may have given up.)  Small on purpose: beyond
-// some 64 KB of code the instruction cache misses and every warp slows down to 5 cycles an instruction and more.
-constexpr uint32_t kSpins = 1u << 22;
-__device__ __forceinline__ bool wait_or_fail(uint64_t* bar, uint32_t parity, Shared* sh) {
-    uint32_t i = 0;
-#pragma unroll 1
-    while (!mbar_try_wait(bar, parity))
-        if (++i == kSpins) {
-            *(volatile int*)&sh->fail = 1;
-            return false;
-        }
-    return true;
-}
-
-// ---- products ----
-// Descriptors as their low word (address and leading offset) and a high word common to all (rows of 128 bytes, 8-row
-// groups 1024 apart): the products then take 8 machine instructions each where 64-bit descriptors took 16, and the issue's
-// code half the room.
-constexpr uint32_t kDescHigh = (1024u >> 4) | 1u << 14 | kSwizzle128B << 29;
-__device__ __forceinline__ uint32_t desc_low(const void* at, uint32_t lbo) { return (smem_u32(at) >> 4) | lbo >> 4 << 16; }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tmov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
-        "setp.ne.b32 p, %5, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}"
-        ::"r"(d), "r"(a), "r"(b), "r"(kDescHigh), "r"(idesc), "r"(acc)
-        : "memory");
-}
-// A out of TMEM.
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tmov.b64 b, {%2, %3};\n\t"
-        "setp.ne.b32 p, %5, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}"
-        ::"r"(d), "r"(a), "r"(b), "r"(kDescHigh), "r"(idesc), "r"(acc)
-        : "memory");
-}
-
 // ---- queries ----
 // Four rows of a query tile, rt .. rt + 3, eight lanes a row: normalised and times the gains as fp16 to row rt & 127 of
 // the half at `dst` (blocks of 64 columns).  Normalised values are at most sqrt d; the gains come with a power of two that
@@ -348,7 +309,7 @@ __global__ void __launch_bounds__(kThreadsA, 1) prefill_attend_kernel(const __gr
                 const int n = na + nb;
 #pragma unroll 1
                 while (ok && unit + n - kUnits > freed_units) {
-                    ok = wait_or_fail(&sh->empty[freed % kGroups], (freed / kGroups) & 1, sh);
+                    ok = wait_or_fail(&sh->empty[freed % kGroups], (freed / kGroups) & 1, &sh->fail);
                     freed_units += (freed & 1) ? VU : KU;
                     ++freed;
                 }
@@ -365,7 +326,7 @@ __global__ void __launch_bounds__(kThreadsA, 1) prefill_attend_kernel(const __gr
             };
 #pragma unroll 1
             for (int k = 0; ok; ++k) {
-                ok = wait_or_fail(&sh->piece_full[k & 1], (k >> 1) & 1, sh);
+                ok = wait_or_fail(&sh->piece_full[k & 1], (k >> 1) & 1, &sh->fail);
                 if (!ok) break;
                 const Piece s = sh->piece[k & 1];
                 if (s.unit < 0) break;
@@ -385,11 +346,11 @@ __global__ void __launch_bounds__(kThreadsA, 1) prefill_attend_kernel(const __gr
 #pragma unroll 1
                 for (int h = 0; h < 2 && ok; ++h) {
                     if (h < last_halves) {
-                        ok = wait_or_fail(&sh->q_empty[h], (qe_phase >> h) & 1, sh);
+                        ok = wait_or_fail(&sh->q_empty[h], (qe_phase >> h) & 1, &sh->fail);
                         qe_phase ^= 1u << h;
                     }
                     if (!ok || s.t0 == s.t1 || h >= halves || k == 0) continue;       // (the first piece's rows go to shared memory directly)
-                    if (h == 0) ok = wait_or_fail(&sh->conv_full[k & 1], ((k - 1) >> 1) & 1, sh);
+                    if (h == 0) ok = wait_or_fail(&sh->conv_full[k & 1], ((k - 1) >> 1) & 1, &sh->fail);
                     if (!ok) break;
                     mbar_arrive_expect_tx(&sh->q_full[h], kHalf);
                     bulk_load(sm + h * kHalf, p.qs + ((size_t)(2 * cta + (k & 1)) * 2 + h) * kHalf, kHalf, &sh->q_full[h]);
@@ -430,7 +391,7 @@ __global__ void __launch_bounds__(kThreadsA, 1) prefill_attend_kernel(const __gr
             // the next piece (halves -1: there is none); with weights awaited no more than one, which may have no tiles:
             // the one behind it is not listed before they have been used
             while (left == 0 && halves >= 0) {
-                if (!wait_or_fail(&sh->piece_full[k & 1], (k >> 1) & 1, sh)) goto give_up;
+                if (!wait_or_fail(&sh->piece_full[k & 1], (k >> 1) & 1, &sh->fail)) goto give_up;
                 const Piece& s = sh->piece[k & 1];
                 if (s.unit < 0) { halves = -1; break; }
                 left = s.t1 - s.t0;
@@ -469,15 +430,15 @@ __global__ void __launch_bounds__(kThreadsA, 1) prefill_attend_kernel(const __gr
                     for (int h = 0; h < 2; ++h) {
                         const uint32_t o = tmem + kO + h * 128, a = tmem + kS + h * 128, d = a;
                         const uint32_t php = h ? ph1 : ph;
-                        if (!(h == 0 ? seen_a : seen_1) && !wait_or_fail(&sh->pa_full[h], php, sh)) goto give_up;
-                        if (h == 0 && !seen_v && !wait_or_fail(b_v, ph_v, sh)) goto give_up;
+                        if (!(h == 0 ? seen_a : seen_1) && !wait_or_fail(&sh->pa_full[h], php, &sh->fail)) goto give_up;
+                        if (h == 0 && !seen_v && !wait_or_fail(b_v, ph_v, &sh->fail)) goto give_up;
                         tc_fence_after();
                         mma_ts(o, a, v0, id, acc);
                         mma_ts(o, a + 8, v0 + 128, id, 1u);
                         const bool seen_b = mbar_test_wait(&sh->pb_full[h], php);
                         mma_ts(o, a + 16, v0 + 256, id, 1u);
                         mma_ts(o, a + 24, v0 + 384, id, 1u);
-                        if (!seen_b && !wait_or_fail(&sh->pb_full[h], php, sh)) goto give_up;
+                        if (!seen_b && !wait_or_fail(&sh->pb_full[h], php, &sh->fail)) goto give_up;
                         tc_fence_after();
                         mma_ts(o, a + 32, v1, id, 1u);
                         mma_ts(o, a + 40, v1 + 128, id, 1u);
@@ -486,7 +447,7 @@ __global__ void __launch_bounds__(kThreadsA, 1) prefill_attend_kernel(const __gr
                         mma_ts(o, a + 48, v1 + 256, id, 1u);
                         mma_ts(o, a + 56, v1 + 384, id, 1u);
                         if (h == 1) mma_commit(f_v);
-                        if (!seen_k && !wait_or_fail(b_k, ph_k, sh)) goto give_up;
+                        if (!seen_k && !wait_or_fail(b_k, ph_k, &sh->fail)) goto give_up;
 #pragma unroll
                         for (int blk = 0; blk < KU; ++blk) {
                             if (blk == KU - 1) {            // one more block of products to come
@@ -541,8 +502,8 @@ __global__ void __launch_bounds__(kThreadsA, 1) prefill_attend_kernel(const __gr
                     const uint32_t o = tmem + kO + h * 128, a = tmem + kS + h * 128;
 #pragma unroll 1
                     for (int part = 0; part < 2; ++part) { // 64 tokens each
-                        if (!wait_or_fail(part ? &sh->pb_full[h] : &sh->pa_full[h], (p_phase >> h) & 1, sh)) goto give_up;
-                        if (h + part == 0 && !wait_or_fail(&sh->full[gv % kGroups], (gv / kGroups) & 1, sh)) goto give_up;
+                        if (!wait_or_fail(part ? &sh->pb_full[h] : &sh->pa_full[h], (p_phase >> h) & 1, &sh->fail)) goto give_up;
+                        if (h + part == 0 && !wait_or_fail(&sh->full[gv % kGroups], (gv / kGroups) & 1, &sh->fail)) goto give_up;
                         tc_fence_after();
                         const uint32_t v = v_desc + (uint32_t)(VU == 2 ? ((unit + part) % kUnits) * kStep : (unit % kUnits) * kStep + part * (kStep / 2));
 #pragma unroll
@@ -554,12 +515,12 @@ __global__ void __launch_bounds__(kThreadsA, 1) prefill_attend_kernel(const __gr
                     if (cur_last) mma_commit(&sh->o_full[h]);
                 }
                 if (h < nxt) {
-                    if (h == 0 && !wait_or_fail(&sh->full[gk % kGroups], (gk / kGroups) & 1, sh)) goto give_up;
+                    if (h == 0 && !wait_or_fail(&sh->full[gk % kGroups], (gk / kGroups) & 1, &sh->fail)) goto give_up;
                     if (first) {
                         if (q_at == 0) {
-                            if (!wait_or_fail(&sh->q0_full[h], 0, sh)) goto give_up;
+                            if (!wait_or_fail(&sh->q0_full[h], 0, &sh->fail)) goto give_up;
                         } else {
-                            if (!wait_or_fail(&sh->q_full[h], (q_phase >> h) & 1, sh)) goto give_up;
+                            if (!wait_or_fail(&sh->q_full[h], (q_phase >> h) & 1, &sh->fail)) goto give_up;
                             q_phase ^= 1u << h;
                         }
                     }
@@ -617,7 +578,7 @@ give_up:
                     for (int i = 0; i < rope_bytes; i += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(y + i));
                 }
             }
-            if (k >= 2) ok = wait_or_fail(&sh->piece_empty[k & 1], ((k >> 1) - 1) & 1, sh);
+            if (k >= 2) ok = wait_or_fail(&sh->piece_empty[k & 1], ((k >> 1) - 1) & 1, &sh->fail);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             if (warp == 10 && lane == 0) {
@@ -650,7 +611,7 @@ give_up:
         bool ok = true;
 #pragma unroll 1
         for (int k = 0;; ++k) {
-            ok = wait_or_fail(&sh->piece_full[k & 1], (k >> 1) & 1, sh);
+            ok = wait_or_fail(&sh->piece_full[k & 1], (k >> 1) & 1, &sh->fail);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             const Piece& s = sh->piece[k & 1];                          // (read where it is needed: registers are few)
@@ -675,7 +636,7 @@ give_up:
                 const int first = tile_at(t) * kTile;
                 // tiles that some row does not see whole (uniform over the tile's rows)
                 const bool edge = first + kTile > s.n_lo || (p.window > 0 && first < s.n_lo + s.queries - 1 - p.window && first + kTile > p.sinks);
-                ok = wait_or_fail(&sh->s_full[h], s_phase, sh);
+                ok = wait_or_fail(&sh->s_full[h], s_phase, &sh->fail);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 s_phase ^= 1;
@@ -730,7 +691,7 @@ give_up:
                 if (lane == 0) mbar_arrive(&sh->piece_empty[k & 1]);
                 continue;
             }
-            if (s.t0 < s.t1 && ok) ok = wait_or_fail(&sh->o_full[h], o_phase, sh);
+            if (s.t0 < s.t1 && ok) ok = wait_or_fail(&sh->o_full[h], o_phase, &sh->fail);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             if (s.t0 < s.t1) {
@@ -793,7 +754,7 @@ give_up:
     __syncthreads();
     if (busy) {
         // a CTA that gave up waits for its copies in flight, and always for its products
-        wait_or_fail(&sh->done, 0, sh);
+        wait_or_fail(&sh->done, 0, &sh->fail);
         if (*(volatile int*)&sh->fail && tid == 0) {
             report(p.status, QKMLA_ERR_TIMEOUT);
             const int n = *(volatile int*)&sh->issued;

@@ -181,38 +181,139 @@ struct __align__(16) ExpandShared {
 };
 static_assert(sizeof(ExpandShared) <= 2048, "beside the blocks");
 
-struct TileOf { int b, t0, len; bool wanted; };
-// The sequence and the first token of a tile of the workspace, by the lengths ahead of it: whole warp.
-__device__ __forceinline__ TileOf locate(const Params& p, int tile) {
-    const int lane = threadIdx.x & 31;
-    int ahead = 0;
-    for (int b0 = 0; b0 < p.B; b0 += 32) {
-        const int b = b0 + lane;
-        int len = b < p.B ? p.seq_lens[b] : 0;
-        if (len < 0 || len > (int64_t)p.max_pages * p.page_size) len = 0;
-        int n = (len + kTile - 1) / kTile, s = n;
+// The sequence of a tile of the workspace, by the lengths ahead of it; tiles are asked for in rising order, so the next
+// tile's is mostly the same one.  Whole warp.
+struct Sequence {
+    int b = 0, first = 0, last = 0, len = 0, rows = 0;     // its tiles: [first, last)
+    int b0 = 0, ahead = 0;                                 // where the next search starts: sequences, and tiles ahead of them
+    __device__ __forceinline__ bool find(const Params& p, int tile) {
+        if (tile < last) return wanted(p, tile);
+        const int lane = threadIdx.x & 31;
+#pragma unroll 1
+        for (; b0 < p.B; b0 += 32) {
+            const int at = b0 + lane;
+            int n = at < p.B ? p.seq_lens[at] : 0;
+            if (n < 0 || n > (int64_t)p.max_pages * p.page_size) n = 0;
+            const int t = (n + kTile - 1) / kTile;
+            int s = t;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int u = __shfl_up_sync(0xffffffffu, s, o);
-            if (lane >= o) s += u;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int u = __shfl_up_sync(0xffffffffu, s, o);
+                if (lane >= o) s += u;
+            }
+            const int all = __shfl_sync(0xffffffffu, s, 31);
+            if (ahead + all > tile) {
+                const int l = __ffs(__ballot_sync(0xffffffffu, ahead + s > tile)) - 1;
+                b = b0 + l;
+                len = __shfl_sync(0xffffffffu, n, l);
+                last = ahead + __shfl_sync(0xffffffffu, s, l);
+                first = last - __shfl_sync(0xffffffffu, t, l);
+                rows = p.chunk_start[b + 1] - p.chunk_start[b];
+                return wanted(p, tile);
+            }
+            ahead += all;
         }
-        const int all = __shfl_sync(0xffffffffu, s, 31);
-        if (ahead + all > tile) {
-            const unsigned m = __ballot_sync(0xffffffffu, ahead + s > tile);
-            const int l = __ffs(m) - 1;
-            TileOf r;
-            r.b = b0 + l;
-            r.len = __shfl_sync(0xffffffffu, len, l);
-            r.t0 = (tile - ahead - __shfl_sync(0xffffffffu, s - n, l)) * kTile;
-            const int rows = p.chunk_start[r.b + 1] - p.chunk_start[r.b];
-            r.wanted = rows > 0;
-            // tiles that no query of the step sees are left out
-            if (p.window > 0) r.wanted = r.wanted && (r.t0 < p.sinks || r.t0 + kTile > (int64_t)r.len - rows + 1 - p.window);
-            return r;
-        }
-        ahead += all;
+        last = first = 1 << 30;                            // behind the last sequence
+        rows = 0;
+        return false;
     }
-    return TileOf{0, 0, 0, false};
+    __device__ __forceinline__ int token(int tile) const { return (tile - first) * kTile; }
+    // Tiles that no query of the step sees are left out.
+    __device__ __forceinline__ bool wanted(const Params& p, int tile) const {
+        if (rows <= 0 || tile < first) return false;
+        const int t0 = token(tile);
+        return p.window == 0 || t0 < p.sinks || t0 + kTile > (int64_t)len - rows + 1 - p.window;
+    }
+};
+
+// A token's latents, NV vectors of 8 a lane, to row r of the tile's blocks as fp16 times 2^-e, e the exponent of its largest
+// value.  Returns the token's exponent (with its scale's), kNone for zeros, kBad (and zeros) where one is not finite.
+template <bool Q8, int NV>
+__device__ __forceinline__ int convert_token(const uint4 (&raw)[NV], float scale, int per, uint8_t* blocks, int r, int lane) {
+    uint32_t h[NV][4];
+    int e;
+    bool bad;
+    if constexpr (Q8) {
+        // codes are fp16 values: two at a time throughout
+        __half2 x[NV][4], top = __float2half2_rn(0.f);
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const uint32_t w[2] = {raw[v].x, raw[v].y};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const __half2_raw q = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[i >> 1] >> (16 * (i & 1))), __NV_E4M3);
+                x[v][i] = __half2(q);
+                top = __hmax2_nan(top, __habs2(x[v][i]));
+            }
+        }
+        const __half m = __hmax_nan(__low2half(top), __high2half(top));
+        // NaN is above every number as a pattern
+        const uint32_t most = __reduce_max_sync(0xffffffffu, (uint32_t)__half_as_ushort(m) & 0x7fffu);
+        bad = most > 0x7c00u || !(fabsf(scale) <= 3.402823466e38f);
+        const float t = __half2float(__ushort_as_half((unsigned short)most));
+        e = most == 0 ? kNone : ilogbf(t);
+        int se = 0;
+        float f = 1.f;
+        if (scale == 0.f) {
+            e = kNone;
+        } else if (!bad && e != kNone) {
+            // (a scale that is no power of two -- none that this library writes -- leaves its mantissa in the codes)
+            se = ilogbf(scale);
+            f = ldexpf(scale, -se);
+            e = ilogbf(t * fabsf(f));
+            f *= pow2i(-e);
+            const bool exact = (__float_as_int(f) & 0x7fffff) == 0;
+            if (exact) {
+                const __half2 f2 = __float2half2_rn(f);
+#pragma unroll
+                for (int v = 0; v < NV; ++v)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[v][i] = __hmul2(x[v][i], f2);
+            } else {
+#pragma unroll
+                for (int v = 0; v < NV; ++v)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[v][i] = __floats2half2_rn(__low2float(x[v][i]) * f, __high2float(x[v][i]) * f);
+            }
+        }
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) h[v][i] = *reinterpret_cast<const uint32_t*>(&x[v][i]);
+        if (e != kNone) e += se;
+    } else {
+        // the largest magnitude by the bf16 patterns, two at a time
+        uint32_t top = 0;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const uint32_t w[4] = {raw[v].x, raw[v].y, raw[v].z, raw[v].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) top = __vmaxu2(top, w[i] & 0x7fff7fffu);
+        }
+        const uint32_t most = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
+        bad = most >= 0x7f80u;
+        e = most == 0 ? kNone : min(max((int)(most >> 7) - 127, -126), 126);
+        const float f = e == kNone || bad ? 0.f : pow2i(-e);
+        const uint64_t f2 = dec::f2(f, f);
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const uint32_t w[4] = {raw[v].x, raw[v].y, raw[v].z, raw[v].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 y = dec::f2_unpack(dec::f2_mul(dec::f2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u)), f2));
+                h[v][i] = pack_f16(y.x, y.y);
+            }
+        }
+    }
+    const bool zero = bad || e == kNone;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        const int c = lane + 32 * v;
+        if (c < per)
+            *reinterpret_cast<uint4*>(blocks + (c >> 3) * kBlock + sw128_offset(r, (c & 7) * 8)) =
+                zero ? make_uint4(0, 0, 0, 0) : make_uint4(h[v][0], h[v][1], h[v][2], h[v][3]);
+    }
+    return bad ? kBad : e;
 }
 
 // NV: vectors of 8 latents a lane, d_c up to 256 NV; at 1 two CTAs fit on an SM, one gathering while the other multiplies.
@@ -252,64 +353,75 @@ __global__ void __launch_bounds__(kThreadsE, NV == 1 ? 2 : 1) prefill_expand_ker
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sh->tmem;
-    auto gave_up = [&]() { return *(volatile int*)&sh->fail != 0; };
-    auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (gave_up()) return false;
-        if (dec::wait_bounded(bar, parity, p.status)) return true;
-        *(volatile int*)&sh->fail = 1;
-        return false;
-    };
+    int* fail = &sh->fail;
     pdl_wait();
     pdl_trigger();
 
     if (warp == 8) {
         // ---- weights ----
+        Sequence seq;
         int i = 0;
         bool ok = true;
+#pragma unroll 1
         for (int item = blockIdx.x; item < items && ok; item += ctas) {
-            if (!locate(p, item / splits).wanted) continue;
+            if (!seq.find(p, item / splits)) continue;
             const int part = item % splits, n0 = nt * part / splits, n1 = nt * (part + 1) / splits;
             const uint8_t* w = p.weights + kWeightTable + (size_t)n0 * kb * kBlock;
-            for (int q = 0; q < (n1 - n0) * kb; ++q, ++i) {
-                const int s = i % kRing;
-                if (i >= kRing && !(ok = wait(&sh->empty[s], ((i / kRing) - 1) & 1))) break;
-                if (lane == 0) {
+            if (lane == 0) {
+#pragma unroll 1
+                for (int q = 0; q < (n1 - n0) * kb; ++q, ++i) {
+                    const int s = i % kRing;
+                    if (i >= kRing && !(ok = wait_or_fail(&sh->empty[s], ((i / kRing) - 1) & 1, fail))) break;
                     mbar_arrive_expect_tx(&sh->full[s], kBlock);
                     bulk_load(ring + s * kBlock, w + (size_t)q * kBlock, kBlock, &sh->full[s]);
                 }
-                __syncwarp();
             }
+            ok = __shfl_sync(0xffffffffu, ok, 0);
         }
         if (lane == 0) *(volatile int*)&sh->issued = i;
     } else if (warp == 9) {
-        // ---- products ----
-        const uint32_t idesc = idesc_bf16(128, 128, 0, 0) & ~((1u << 7) | (1u << 10));      // fp16 operands
+        // ---- products: each barrier is looked at while the ones ahead of its use are being taken ----
+        constexpr uint32_t idesc = idesc_bf16(128, 128, 0, 0) & ~((1u << 7) | (1u << 10));      // fp16 operands
+        const uint32_t a_desc = desc_low(sm, 16), w_desc = desc_low(ring, 16);
+        Sequence seq;
         int i = 0, n = 0, it = 0;                          // blocks, N-tiles and tiles so far
         bool ok = true;
+#pragma unroll 1
         for (int item = blockIdx.x; item < items && ok; item += ctas) {
-            if (!locate(p, item / splits).wanted) continue;
+            if (!seq.find(p, item / splits)) continue;
             const int part = item % splits, n0 = nt * part / splits, n1 = nt * (part + 1) / splits;
-            if (!(ok = wait(&sh->a_full, it & 1))) break;
-            ++it;
-            for (int q = n0; q < n1 && ok; ++q, ++n) {
-                const int a = n & 1;
-                if (n >= 2 && !(ok = wait(&sh->acc_empty[a], ((n >> 1) - 1) & 1))) break;
-                for (int k = 0; k < kb; ++k, ++i) {
-                    const int s = i % kRing;
-                    if (!(ok = wait(&sh->full[s], (i / kRing) & 1))) break;
-                    tc_fence_after();
-                    if (elect_one()) {
-                        const uint32_t A = smem_u32(sm + k * kBlock), Bw = smem_u32(ring + s * kBlock);
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            mma_bf16(tmem + a * 128, smem_desc(A + kk * 32, 16, 1024, kSwizzle128B),
-                                     smem_desc(Bw + kk * 32, 16, 1024, kSwizzle128B), idesc, (k > 0 || kk > 0) ? 1u : 0u);
-                        mma_commit(&sh->empty[s]);
-                        if (k == kb - 1) mma_commit(&sh->acc_full[a]);
+            if (elect_one()) {
+                ok = wait_or_fail(&sh->a_full, it & 1, fail);
+                bool seen = false;
+                const int blocks_all = (n1 - n0) * kb;
+                int k = 0;
+#pragma unroll 1
+                for (int q = 0; q < blocks_all && ok; ++q, ++i) {
+                    const int s = i % kRing, a = n & 1;
+                    if (k == 0 && n >= 2 && !(ok = wait_or_fail(&sh->acc_empty[a], ((n >> 1) - 1) & 1, fail))) break;
+                    if (!seen && !(ok = wait_or_fail(&sh->full[s], (i / kRing) & 1, fail))) break;
+                    if (k == 0) tc_fence_after();
+                    const uint32_t A = a_desc + k * (kBlock >> 4), W = w_desc + s * (kBlock >> 4), d = tmem + a * 128;
+                    mma_ss(d, A, W, idesc, k > 0 ? 1u : 0u);
+                    mma_ss(d, A + 2, W + 2, idesc, 1u);
+                    const int s2 = (i + 1) % kRing;
+                    seen = mbar_test_wait(&sh->full[s2], ((i + 1) / kRing) & 1);
+                    mma_ss(d, A + 4, W + 4, idesc, 1u);
+                    mma_ss(d, A + 6, W + 6, idesc, 1u);
+                    mma_commit(&sh->empty[s]);
+                    if (++k == kb) {
+                        mma_commit(&sh->acc_full[a]);
+                        k = 0;
+                        ++n;
                     }
-                    __syncwarp();
                 }
             }
+            __syncwarp();
+            // (the counts are the elected lane's; the others' follow from the item's size)
+            ok = __all_sync(0xffffffffu, ok);
+            ++it;
+            i = __reduce_max_sync(0xffffffffu, i);
+            n = __reduce_max_sync(0xffffffffu, n);
         }
         if (elect_one()) mma_commit(&sh->done);
         __syncwarp();
@@ -317,22 +429,26 @@ __global__ void __launch_bounds__(kThreadsE, NV == 1 ? 2 : 1) prefill_expand_ker
         const int row_bytes = Q8 ? p.d_c + 2 * p.d_r : 2 * (p.d_c + p.d_r);
         const int per = p.d_c / 8;                          // vectors of 8 latents a token
         const int* we = reinterpret_cast<const int*>(p.weights);
+        Sequence seq;
         int n = 0, it = 0;
         bool ok = true;
+#pragma unroll 1
         for (int item = blockIdx.x; item < items && ok; item += ctas) {
             const int tile = item / splits, part = item % splits;
-            const TileOf at = locate(p, tile);
-            if (!at.wanted) continue;
-            const int n0 = nt * part / splits, n1 = nt * (part + 1) / splits, buf = it & 1;
+            if (!seq.find(p, tile)) continue;
+            const int t0 = seq.token(tile), len = seq.len, n0 = nt * part / splits, n1 = nt * (part + 1) / splits, buf = it & 1;
             // ---- gather: a warp's 16 tokens, their slots by its first 16 lanes ----
-            auto slot_at = [&](int t) {
-                return t < at.len ? slot_of(p.page_table, at.b, t, p.page_size, p.max_pages, p.num_pages, p.status) : (int64_t)-1;
-            };
-            const int64_t slot = lane < 16 ? slot_at(at.t0 + warp * 16 + lane) : -1;
             const int row = 32 * (warp & 3) + lane;          // this thread's token in the results
-            const int64_t row_slot = slot_at(at.t0 + row);
+            const int mine = t0 + (lane < 16 ? warp * 16 + lane : row);
+            auto slot_at = [&](int t) {
+                return t < len ? slot_of(p.page_table, seq.b, t, p.page_size, p.max_pages, p.num_pages, p.status) : (int64_t)-1;
+            };
+            const int64_t slot = slot_at(mine);              // (of lanes from 16 on it is not used)
+            const int64_t row_slot = slot_at(t0 + row);
+            float scale = 0.f;                               // of lane's token, 8-bit cache
+            if (Q8 && lane < 16 && slot >= 0) scale = p.kv_scale[slot];
             int hi = kNone, lo = kBad;                       // largest and least exponent of the warp's tokens
-            constexpr int kAhead = 8;                        // tokens in flight
+            constexpr int kAhead = 8 / NV;                   // tokens in flight
 #pragma unroll 1
             for (int k0 = 0; k0 < 16; k0 += kAhead) {
                 uint4 raw[kAhead][NV];
@@ -357,69 +473,32 @@ __global__ void __launch_bounds__(kThreadsE, NV == 1 ? 2 : 1) prefill_expand_ker
                 }
 #pragma unroll
                 for (int k = 0; k < kAhead; ++k) {
-                    const int64_t sl = __shfl_sync(0xffffffffu, slot, k0 + k);
-                    float x[NV][8];
-                    float top = 0.f;
-                    bool bad = false;
-#pragma unroll
-                    for (int v = 0; v < NV; ++v) {
-                        const uint32_t w[4] = {raw[k][v].x, raw[k][v].y, raw[k][v].z, raw[k][v].w};
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            if constexpr (Q8) x[v][i] = e4m3_to_float((uint8_t)(w[i >> 2] >> (8 * (i & 3))));
-                            else x[v][i] = __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
-                            top = fmaxf(top, fabsf(x[v][i]));
-                            bad |= !(fabsf(x[v][i]) <= 3.402823466e38f);
-                        }
-                    }
-                    top = warp_max(top);
-                    bad = __any_sync(0xffffffffu, bad);
-                    int e = top > 0.f ? ilogbf(top) : kNone;  // of the latent, or of its codes
-                    int se = 0;
-                    if (Q8 && sl >= 0) {
-                        const float s = p.kv_scale[sl];
-                        bad |= !isfinite(s);
-                        if (s == 0.f) e = kNone;
-                        else se = ilogbf(s);
-                        // a scale that is no power of two (none that this library writes): its mantissa goes into the codes
-                        const float m = s == 0.f ? 0.f : ldexpf(s, -se);
-                        if (m != 1.f) {
-#pragma unroll
-                            for (int i = 0; i < 8 * NV; ++i) x[i >> 3][i & 7] *= m;
-                            if (e != kNone) e = ilogbf(top * fabsf(m));
-                        }
-                    }
-                    const bool zero = bad || e == kNone;
                     const int r = warp * 16 + k0 + k;
-                    const float f1 = zero ? 0.f : pow2i(-(e / 2)), f2 = zero ? 0.f : pow2i(-(e - e / 2));
-#pragma unroll
-                    for (int v = 0; v < NV; ++v) {
-                        const int c = lane + 32 * v;
-                        if (c < per) {
-                            uint32_t h[4];
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) h[i] = zero ? 0u : pack_f16(x[v][2 * i] * f1 * f2, x[v][2 * i + 1] * f1 * f2);
-                            *reinterpret_cast<uint4*>(sm + (c >> 3) * kBlock + sw128_offset(r, (c & 7) * 8)) = make_uint4(h[0], h[1], h[2], h[3]);
-                        }
-                    }
-                    const int et = bad ? kBad : e == kNone ? kNone : e + se;
-                    if (lane == 0) sh->exps[buf][r] = et;
-                    if (et != kBad && et != kNone) { hi = max(hi, et); lo = min(lo, et); }
+                    const float s = __shfl_sync(0xffffffffu, scale, k0 + k);
+                    const int e = convert_token<Q8, NV>(raw[k], s, per, sm, r, lane);
+                    if (lane == 0) sh->exps[buf][r] = e;
+                    if (e != kBad && e != kNone) { hi = max(hi, e); lo = min(lo, e); }
                 }
             }
             if (part == 0) {
-                // RoPE keys of the warp's tokens: 16-byte pieces of 8 values, a row by 8 (or 4) lanes
+                // RoPE keys of the warp's tokens: 16-byte pieces of 8 values, a row by 8 (or 4) lanes, all in flight at once
                 const int pieces = p.d_r / 8;
-                for (int i = lane; i < 16 * pieces; i += 32) {
-                    const int k = i / pieces, c = i % pieces;
-                    const int64_t sl = __shfl_sync(0xffffffffu, slot, k);
-                    uint32_t h[4] = {0, 0, 0, 0};
-                    if (sl >= 0) {
-                        const uint4 u = *reinterpret_cast<const uint4*>(p.kv + sl * (int64_t)row_bytes + (Q8 ? p.d_c : 2 * p.d_c) + c * 16);
-                        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+                uint4 u[4];
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) h[q] = pack_f16(__uint_as_float(w[q] << 16), __uint_as_float(w[q] & 0xffff0000u));
-                    }
+                for (int q = 0; q < 4; ++q) {
+                    const int i = lane + 32 * q, k = i / pieces, c = i - k * pieces;
+                    const int64_t sl = __shfl_sync(0xffffffffu, slot, k & 15);
+                    u[q] = make_uint4(0, 0, 0, 0);
+                    if (k < 16 && sl >= 0) u[q] = *reinterpret_cast<const uint4*>(p.kv + sl * (int64_t)row_bytes + (Q8 ? p.d_c : 2 * p.d_c) + c * 16);
+                }
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int i = lane + 32 * q, k = i / pieces, c = i - k * pieces;
+                    if (k >= 16) continue;
+                    const uint32_t w[4] = {u[q].x, u[q].y, u[q].z, u[q].w};
+                    uint32_t h[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) h[j] = pack_f16(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xffff0000u));
                     *reinterpret_cast<uint4*>(p.krope + (size_t)tile * kBlock + sw128_offset(warp * 16 + k, c * 8)) = make_uint4(h[0], h[1], h[2], h[3]);
                 }
             }
@@ -434,7 +513,7 @@ __global__ void __launch_bounds__(kThreadsE, NV == 1 ? 2 : 1) prefill_expand_ker
                 return p.ak_f16 ? load_alpha<true>(p.ak, i) : load_alpha<false>(p.ak, i);
             };
             float al = alpha_of(2 * n0 + half);
-            ok = wait(&sh->a_full, it & 1);
+            ok = wait_or_fail(&sh->a_full, it & 1, fail);
             ++it;
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
@@ -448,11 +527,12 @@ __global__ void __launch_bounds__(kThreadsE, NV == 1 ? 2 : 1) prefill_expand_ker
             // ---- results: thread = token, its warp's half of the 128 columns (one 64-column block) ----
             const int et = sh->exps[buf][row];
             const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
+#pragma unroll 1
             for (int q = n0; q < n1; ++q, ++n) {
                 const int a = n & 1, cb = 2 * q + half;
                 const float al_now = al;
                 if (q + 1 < n1) al = alpha_of(cb + 2);
-                ok = wait(&sh->acc_full[a], (n >> 1) & 1);
+                ok = wait_or_fail(&sh->acc_full[a], (n >> 1) & 1, fail);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
@@ -477,13 +557,14 @@ __global__ void __launch_bounds__(kThreadsE, NV == 1 ? 2 : 1) prefill_expand_ker
                     dst = p.v + (((size_t)tile * p.Gv + m) * nvb * 2 + (row >> 6) * nvb + c) * (kBlock / 2) + (row & 63) * 128;
                 }
                 const bool as_bf = bf && !key;
+                const uint64_t f2 = dec::f2(f, f);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {                // two neighbouring 16-byte pieces, in swizzled order
                     uint32_t h[2][4];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const float x = __uint_as_float(v[16 * c + 2 * i]) * f, y = __uint_as_float(v[16 * c + 2 * i + 1]) * f;
-                        h[i >> 2][i & 3] = as_bf ? pack_bf16(x, y) : pack_f16(x, y);
+                        const float2 x = dec::f2_unpack(dec::f2_mul(dec::f2(__uint_as_float(v[16 * c + 2 * i]), __uint_as_float(v[16 * c + 2 * i + 1])), f2));
+                        h[i >> 2][i & 3] = as_bf ? pack_bf16(x.x, x.y) : pack_f16(x.x, x.y);
                     }
                     uint8_t* to = dst + ((c ^ ((row >> 1) & 3)) << 5);
                     uint32_t u[4], w[4];
@@ -495,8 +576,9 @@ __global__ void __launch_bounds__(kThreadsE, NV == 1 ? 2 : 1) prefill_expand_ker
         }
     }
     __syncthreads();
-    dec::wait_bounded(&sh->done, 0, p.status);
-    if (gave_up() && tid == 0) {
+    wait_or_fail(&sh->done, 0, fail);
+    if (*(volatile int*)fail && tid == 0) {
+        report(p.status, QKMLA_ERR_TIMEOUT);
         const int issued = *(volatile int*)&sh->issued;
         for (int j = max(0, issued - kRing); j < issued; ++j) dec::wait_bounded(&sh->full[j % kRing], (j / kRing) & 1, p.status);
     }
