@@ -63,10 +63,13 @@ struct Params {
     int* status;
 };
 
-// The packed weights: fp16 blocks of 128 output columns x 64 latents [N-tile][d_c / 64], after a table of
-// the power of two of each matrix.
+// The packed weights: fp16 blocks of 64 output columns x 64 latents, [N-tile][d_c / 64][2 or 4 blocks of columns], after a
+// table of the power of two of each matrix.
 __host__ __device__ inline int column_blocks(int G, int Gv, int d_h, int d_v) { return G * (d_h / 64) + Gv * (d_v / 64); }
-__host__ __device__ inline int n_tiles(int G, int Gv, int d_h, int d_v) { return (column_blocks(G, Gv, d_h, d_v) + 1) / 2; }
+__host__ __device__ inline int blocks_per_tile(int d_c) { return d_c > 256 ? 4 : 2; }    // column blocks of an N-tile
+__host__ __device__ inline int n_tiles(int G, int Gv, int d_h, int d_v, int d_c) {
+    return (column_blocks(G, Gv, d_h, d_v) + blocks_per_tile(d_c) - 1) / blocks_per_tile(d_c);
+}
 constexpr size_t kWeightTable = 4096;      // int32 exponents of up to 1024 matrices
 
 // First slot of a sequence's query tiles: its rows start at chunk_start[b], and rounding up for each of the

@@ -48,8 +48,9 @@ __global__ void __launch_bounds__(256) prefill_pack_kernel(const float* __restri
         const size_t at = (size_t)(c0 + c) * d + j;
         const float w = ldexpf(key ? k[at] : __bfloat162float(v[at]), -e);
         const int cb = first + j / 64;                     // 64-column block
-        uint8_t* blk = blocks + ((size_t)(cb / 2) * (d_c / 64) + blockIdx.y) * kBlock;
-        *reinterpret_cast<__half*>(blk + sw128_offset((cb & 1) * 64 + j % 64, c)) = __float2half_rn(w);
+        const int nb = blocks_per_tile(d_c);
+        uint8_t* blk = blocks + ((size_t)(cb / nb) * (d_c / 64) + blockIdx.y) * (nb * (kBlock / 2));
+        *reinterpret_cast<__half*>(blk + sw128_offset(cb % nb * 64 + j % 64, c)) = __float2half_rn(w);
     }
 }
 
@@ -154,22 +155,23 @@ __device__ void make_plan(const Params& p, int64_t* warps) {
 // ---------------------------------------------------------------------------
 // keys and values
 // ---------------------------------------------------------------------------
-// C [128 tokens, d_c] x [W^K_0 .. W^K_{G-1} | W^V_0 ..] in N-tiles of 128 columns.  The latents lie in shared
+// C [128 tokens, d_c] x [W^K_0 .. W^K_{G-1} | W^V_0 ..] in N-tiles of 256 columns (128 up
+// to d_c = 256, where two CTAs share an SM and its TMEM).  The latents lie in shared
 // memory while their tile is worked on (d_c / 64 blocks), each token times a power of two of its own that brings its
 // largest value into [1, 2): exact as fp16 for a bf16 or an 8-bit latent, but for what lies 2^-14 below that
 // value.  Warps 0-7 gather and convert them, then take the results out of TMEM: a key row is scaled by the
 // stored alpha^k, a value row by its share of the tile's common exponent.  A thread holds 64 columns of a token,
 // one 128-byte line of a block, and stores it 32 bytes at a time.  Warp 8 streams the packed weights through a
-// ring of blocks, warp 9 issues the products (M = N = 128, K = 64 a block), the accumulator double-buffered.
+// ring, warp 9 issues the products (M = 128, N = 128 or 256, K = 64 a stage), the accumulator double-buffered.
 //
 // Bound: the tensor core for many tokens (2 d_c flops a value); next to it the weights, which every tile
-// streams through L2 (16 KB a block of 260 cycles: 63 bytes a cycle and SM at full rate), so the ring takes all the
-// shared memory that the latents leave (six blocks at d_c = 512).  Few tiles: their columns are cut over several CTAs.
-constexpr int kRingMax = 6;
+// streams through L2 (32 KB a stage of 512 cycles: 64 bytes a cycle and SM at full rate), so the ring takes all the
+// shared memory that the latents leave (three stages at d_c = 512).  Few tiles: their columns are cut over several CTAs.
+constexpr int kRingMax = 3;
 constexpr int kNone = -1000, kBad = 1000;      // exponents of an all-zero and of a not finite token
 
-__host__ __device__ inline int expand_ring(int d_c) { return d_c <= 256 ? 2 : kRingMax; }
-__host__ __device__ inline int expand_bytes(int d_c) { return (d_c / 64 + expand_ring(d_c)) * kBlock + 1024 + 2048; }
+// blocks of the latents, a ring of three stages of 32 KB or two of 16 KB
+__host__ __device__ inline int expand_bytes(int d_c) { return (d_c / 64 + (d_c <= 256 ? 2 : 2 * kRingMax)) * kBlock + 1024 + 2048; }
 
 struct __align__(16) ExpandShared {
     uint64_t full[kRingMax], empty[kRingMax];
@@ -322,12 +324,15 @@ __global__ void __launch_bounds__(kThreadsE, NV == 1 ? 2 : 1) prefill_expand_ker
     extern __shared__ __align__(1024) uint8_t smraw[];
     uint8_t* sm = smraw + ((1024u - (smem_u32(smraw) & 1023u)) & 1023u);
     constexpr int kRing = NV == 1 ? 2 : kRingMax;
+    constexpr int NB = NV == 1 ? 2 : 4;                     // column blocks of an N-tile
+    constexpr int kStage = NB * (kBlock / 2);
+    constexpr uint32_t kCols = NB * 64;
     const int kb = p.d_c / 64;
     uint8_t* ring = sm + kb * kBlock;
-    ExpandShared* sh = reinterpret_cast<ExpandShared*>(ring + kRing * kBlock);
+    ExpandShared* sh = reinterpret_cast<ExpandShared*>(ring + kRing * kStage);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int nkb = p.d_h / 64, nvb = p.d_v / 64;
-    const int blocks = column_blocks(p.G, p.Gv, p.d_h, p.d_v), nt = (blocks + 1) / 2;
+    const int blocks = column_blocks(p.G, p.Gv, p.d_h, p.d_v), nt = (blocks + NB - 1) / NB;
     const int items = p.max_tiles * splits, ctas = gridDim.x - 1;
 
     if (blockIdx.x == ctas) {
@@ -346,7 +351,7 @@ __global__ void __launch_bounds__(kThreadsE, NV == 1 ? 2 : 1) prefill_expand_ker
         fence_barrier_init();
     }
     if (warp == 9) {
-        tmem_alloc(&sh->tmem, 256);
+        tmem_alloc(&sh->tmem, 2 * kCols);
         tmem_relinquish();
     }
     tc_fence_before();
@@ -366,14 +371,14 @@ __global__ void __launch_bounds__(kThreadsE, NV == 1 ? 2 : 1) prefill_expand_ker
         for (int item = blockIdx.x; item < items && ok; item += ctas) {
             if (!seq.find(p, item / splits)) continue;
             const int part = item % splits, n0 = nt * part / splits, n1 = nt * (part + 1) / splits;
-            const uint8_t* w = p.weights + kWeightTable + (size_t)n0 * kb * kBlock;
+            const uint8_t* w = p.weights + kWeightTable + (size_t)n0 * kb * kStage;
             if (lane == 0) {
 #pragma unroll 1
                 for (int q = 0; q < (n1 - n0) * kb; ++q, ++i) {
                     const int s = i % kRing;
                     if (i >= kRing && !(ok = wait_or_fail(&sh->empty[s], ((i / kRing) - 1) & 1, fail))) break;
-                    mbar_arrive_expect_tx(&sh->full[s], kBlock);
-                    bulk_load(ring + s * kBlock, w + (size_t)q * kBlock, kBlock, &sh->full[s]);
+                    mbar_arrive_expect_tx(&sh->full[s], kStage);
+                    bulk_load(ring + s * kStage, w + (size_t)q * kStage, kStage, &sh->full[s]);
                 }
             }
             ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -381,7 +386,7 @@ __global__ void __launch_bounds__(kThreadsE, NV == 1 ? 2 : 1) prefill_expand_ker
         if (lane == 0) *(volatile int*)&sh->issued = i;
     } else if (warp == 9) {
         // ---- products: each barrier is looked at while the ones ahead of its use are being taken ----
-        constexpr uint32_t idesc = idesc_bf16(128, 128, 0, 0) & ~((1u << 7) | (1u << 10));      // fp16 operands
+        constexpr uint32_t idesc = idesc_bf16(128, kCols, 0, 0) & ~((1u << 7) | (1u << 10));      // fp16 operands
         const uint32_t a_desc = desc_low(sm, 16), w_desc = desc_low(ring, 16);
         Sequence seq;
         int i = 0, n = 0, it = 0;                          // blocks, N-tiles and tiles so far
@@ -401,7 +406,7 @@ __global__ void __launch_bounds__(kThreadsE, NV == 1 ? 2 : 1) prefill_expand_ker
                     if (k == 0 && n >= 2 && !(ok = wait_or_fail(&sh->acc_empty[a], ((n >> 1) - 1) & 1, fail))) break;
                     if (!seen && !(ok = wait_or_fail(&sh->full[s], (i / kRing) & 1, fail))) break;
                     if (k == 0) tc_fence_after();
-                    const uint32_t A = a_desc + k * (kBlock >> 4), W = w_desc + s * (kBlock >> 4), d = tmem + a * 128;
+                    const uint32_t A = a_desc + k * (kBlock >> 4), W = w_desc + s * (kStage >> 4), d = tmem + a * kCols;
                     mma_ss(d, A, W, idesc, k > 0 ? 1u : 0u);
                     mma_ss(d, A + 2, W + 2, idesc, 1u);
                     const int s2 = (i + 1) % kRing;
@@ -506,13 +511,19 @@ __global__ void __launch_bounds__(kThreadsE, NV == 1 ? 2 : 1) prefill_expand_ker
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh->a_full);
+            // the next tile's rows into L2, where it is of the same sequence
+            if (const int next = (item + ctas) / splits; next > tile && next < seq.last && lane < 16) {
+                const int64_t sl = slot_at(seq.token(next) + warp * 16 + lane);
+                if (sl >= 0)
+                    for (int i = 0; i < row_bytes; i += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(p.kv + sl * (int64_t)row_bytes + i));
+            }
             const int half = warp >> 2;
             auto alpha_of = [&](int cb) {                    // of the key block's group
                 if (cb >= p.G * nkb || row_slot < 0) return 0.f;
                 const int64_t i = row_slot * p.G + cb / nkb;
                 return p.ak_f16 ? load_alpha<true>(p.ak, i) : load_alpha<false>(p.ak, i);
             };
-            float al = alpha_of(2 * n0 + half);
+            float al = alpha_of(NB * n0 + half * (NB / 2));
             ok = wait_or_fail(&sh->a_full, it & 1, fail);
             ++it;
             ok = __all_sync(0xffffffffu, ok);
@@ -529,19 +540,24 @@ __global__ void __launch_bounds__(kThreadsE, NV == 1 ? 2 : 1) prefill_expand_ker
             const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
 #pragma unroll 1
             for (int q = n0; q < n1; ++q, ++n) {
-                const int a = n & 1, cb = 2 * q + half;
-                const float al_now = al;
-                if (q + 1 < n1) al = alpha_of(cb + 2);
+                const int a = n & 1;
                 ok = wait_or_fail(&sh->acc_full[a], (n >> 1) & 1, fail);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
+#pragma unroll 1
+                for (int sub = 0; sub < NB / 2; ++sub) {
+                const int cb = NB * q + half * (NB / 2) + sub;
+                const float al_now = al;
+                al = alpha_of(sub + 1 < NB / 2 ? cb + 1 : cb + 1 + NB / 2);
                 uint32_t v[64];
-                tmem_ld64(tmem + lane_base + a * 128 + half * 64, v);
+                tmem_ld64(tmem + lane_base + a * kCols + (half * (NB / 2) + sub) * 64, v);
                 tmem_wait_ld();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh->acc_empty[a]);
+                if (sub == NB / 2 - 1) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh->acc_empty[a]);
+                }
                 if (cb >= blocks) continue;
                 const bool key = cb < p.G * nkb;
                 float f;
@@ -572,6 +588,7 @@ __global__ void __launch_bounds__(kThreadsE, NV == 1 ? 2 : 1) prefill_expand_ker
                     for (int i = 0; i < 4; ++i) { u[i] = row & 1 ? h[1][i] : h[0][i]; w[i] = row & 1 ? h[0][i] : h[1][i]; }
                     st_global_v8(to, u, w);
                 }
+                }
             }
         }
     }
@@ -586,7 +603,7 @@ __global__ void __launch_bounds__(kThreadsE, NV == 1 ? 2 : 1) prefill_expand_ker
     __syncthreads();
     if (warp == 9) {
         tc_fence_after();
-        tmem_dealloc(tmem, 256);
+        tmem_dealloc(tmem, 2 * kCols);
     }
 }
 
@@ -596,7 +613,7 @@ int launch_expand_as(const Params& p, cudaStream_t s) {
     const int bytes = expand_bytes(p.d_c), sms = device_sm_count() * (NV == 1 ? 2 : 1);
     if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return QKMLA_ERR_CUDA;
     // few tiles: their columns are cut over several CTAs
-    const int nt = n_tiles(p.G, p.Gv, p.d_h, p.d_v);
+    const int nt = n_tiles(p.G, p.Gv, p.d_h, p.d_v, p.d_c);
     const int splits = max(1, min(nt, sms / p.max_tiles));
     if ((int64_t)p.max_tiles * splits > INT32_MAX) return QKMLA_ERR_UNSUPPORTED;
     const int ctas = min(p.max_tiles * splits, sms);
@@ -621,7 +638,7 @@ static bool weights_served(int G, int Gv, int d_c, int d_h, int d_v) {
 
 extern "C" size_t qkmla_prefill_weights_size(int G, int G_v, int d_c, int d_h, int d_v) {
     if (G < 1 || G_v < 1 || d_c < 1 || d_h < 1 || d_v < 1 || !weights_served(G, G_v, d_c, d_h, d_v)) return 0;
-    return pf::kWeightTable + (size_t)pf::n_tiles(G, G_v, d_h, d_v) * (d_c / 64) * pf::kBlock;
+    return pf::kWeightTable + (size_t)pf::n_tiles(G, G_v, d_h, d_v, d_c) * (d_c / 64) * pf::blocks_per_tile(d_c) * (pf::kBlock / 2);
 }
 
 extern "C" int qkmla_prefill_pack_weights(const float* w_k, const void* w_v, int G, int G_v, int d_c, int d_h, int d_v,
