@@ -195,6 +195,26 @@ __device__ __forceinline__ void st_global_v8(void* p, const uint32_t (&a)[4], co
                  : "memory");
 }
 
+// Four rows a quad of lanes, four pieces of 32 bytes a row: from piece k of the lane's own row in h[k] to piece lane % 4 of
+// row k of the quad.  A store of a row a lane touches 32 lines an instruction, and each costs a cycle of the data path that
+// the tensor core's operands come through; a quad's four lanes then write one whole line.
+__device__ __forceinline__ void quad_transpose(uint32_t (&h)[4][8], int lane) {
+#pragma unroll
+    for (int bit = 1; bit <= 2; bit <<= 1) {
+        const bool up = lane & bit;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (k & bit) continue;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t r = __shfl_xor_sync(0xffffffffu, up ? h[k][i] : h[k | bit][i], bit);
+                if (up) h[k][i] = r;
+                else h[k | bit][i] = r;
+            }
+        }
+    }
+}
+
 int launch_expand(const Params& p, bool q8, cudaStream_t s);
 int launch_attend(const Params& p, cudaStream_t s);
 

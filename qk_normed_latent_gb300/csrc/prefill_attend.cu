@@ -698,53 +698,50 @@ give_up:
                 o_phase ^= 1;
                 tc_fence_after();
             }
-            if (s.t0 == 0 && s.t1 == s.nt) {
-                const int gv = (int)((int64_t)s.unit * p.Gv / p.units);
-                const float inv = sum == 0.f ? 0.f : ldexpf(1.f / sum, we[p.G + gv]);
-                const int head = s.unit * p.hp + (rt & (p.hp - 1));
-                const int64_t r = (int64_t)s.row0 + i;
-                const int64_t to = (r * p.H + head) * DV;
+            // the row's output, or its part's fp32 sums and, for the join, reference and sum
+            const bool whole = s.t0 == 0 && s.t1 == s.nt;
+            const int gv = (int)((int64_t)s.unit * p.Gv / p.units);
+            const float inv = !whole ? 1.f : sum == 0.f ? 0.f : ldexpf(1.f / sum, we[p.G + gv]);
+            const size_t part = (size_t)(2 * cta + (s.t0 > 0 ? 0 : 1)) * kRowsQ;
+            // (row r of the tile: query r / hp, head r % hp of the unit)
+            auto out = [&](int r) { return ((int64_t)s.row0 + (r >> p.hp_log)) * p.H + s.unit * p.hp + (r & (p.hp - 1)); };
+            const bool narrow = whole && !p.o_f32;
+            const int r0 = rt & ~3;
 #pragma unroll 1
-                for (int q = 0; q < DV; q += 32) {
-                    float o[32];
+            for (int q = 0; q < DV; q += narrow ? 64 : 32) {
+                uint32_t h[4][8];
+                // 16 columns a piece as bf16, 8 as fp32; columns from q on
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t o[16];
                     if (s.t0 < s.t1) {
-                        tmem_ld16(t_o + q, *reinterpret_cast<uint32_t(*)[16]>(o));
-                        tmem_ld16(t_o + q + 16, *reinterpret_cast<uint32_t(*)[16]>(o + 16));
+                        if (narrow) tmem_ld16(t_o + q + c * 16, o);
+                        else if (c < 2) tmem_ld16(t_o + q + c * 16, o);
                         tmem_wait_ld();
                     }
+                    if (narrow) {
 #pragma unroll
-                    for (int w = 0; w < 32; ++w) o[w] = sum == 0.f ? 0.f : o[w] * inv;
-                    if (there) {
-                        if (p.o_f32) {
-                            float4* dst = reinterpret_cast<float4*>((float*)p.o + to + q);
+                        for (int i = 0; i < 8; ++i)
+                            h[c][i] = inv == 0.f ? 0u : pack_bf16(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
+                    } else if (c < 2) {
 #pragma unroll
-                            for (int w = 0; w < 8; ++w) dst[w] = make_float4(o[4 * w], o[4 * w + 1], o[4 * w + 2], o[4 * w + 3]);
-                        } else {
-                            uint16_t* dst = (uint16_t*)p.o + to + q;
-                            uint32_t w[16];
-#pragma unroll
-                            for (int r2 = 0; r2 < 16; ++r2) w[r2] = pack_bf16(o[2 * r2], o[2 * r2 + 1]);
-                            st_global_v8(dst, *reinterpret_cast<const uint32_t(*)[4]>(w), *reinterpret_cast<const uint32_t(*)[4]>(w + 4));
-                            st_global_v8(dst + 16, *reinterpret_cast<const uint32_t(*)[4]>(w + 8), *reinterpret_cast<const uint32_t(*)[4]>(w + 12));
-                        }
+                        for (int i = 0; i < 16; ++i) h[2 * c + (i >> 3)][i & 7] = inv == 0.f ? 0u : __float_as_uint(__uint_as_float(o[i]) * inv);
                     }
                 }
-                if (there && p.lse) p.lse[r * p.H + head] = sum == 0.f ? -INFINITY : (m - 7.f) * kLn2 + logf(sum);
-            } else {
-                const size_t part = (size_t)(2 * cta + (s.t0 > 0 ? 0 : 1)) * kRowsQ + rt;
-                float* dst = p.part_o + part * DV;
-#pragma unroll 1
-                for (int q = 0; q < DV; q += 32) {
-                    float o[32];
-                    tmem_ld16(t_o + q, *reinterpret_cast<uint32_t(*)[16]>(o));
-                    tmem_ld16(t_o + q + 16, *reinterpret_cast<uint32_t(*)[16]>(o + 16));
-                    tmem_wait_ld();
-                    if (there) {
+                quad_transpose(h, lane);
 #pragma unroll
-                        for (int w = 0; w < 8; ++w) reinterpret_cast<float4*>(dst + q)[w] = make_float4(o[4 * w], o[4 * w + 1], o[4 * w + 2], o[4 * w + 3]);
-                    }
+                for (int k = 0; k < 4; ++k) {
+                    const int r = r0 + k;
+                    if ((r >> p.hp_log) >= s.queries) continue;
+                    uint8_t* dst = narrow ? (uint8_t*)((uint16_t*)p.o + out(r) * DV + q) : whole ? (uint8_t*)((float*)p.o + out(r) * DV + q)
+                                                                                                : (uint8_t*)(p.part_o + (part + r) * DV + q);
+                    const uint32_t (&one)[8] = h[k];
+                    st_global_v8(dst + (lane & 3) * 32, {one[0], one[1], one[2], one[3]}, {one[4], one[5], one[6], one[7]});
                 }
-                if (there) p.part_ml[part] = make_float2(m, sum);
+            }
+            if (there) {
+                if (!whole) p.part_ml[part + rt] = make_float2(m, sum);
+                else if (p.lse) p.lse[out(rt)] = sum == 0.f ? -INFINITY : (m - 7.f) * kLn2 + logf(sum);
             }
             tc_fence_before();                                          // the next tile's PV writes O after this half's P
             __syncwarp();

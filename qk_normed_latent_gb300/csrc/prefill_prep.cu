@@ -161,7 +161,7 @@ __device__ void make_plan(const Params& p, int64_t* warps) {
 // largest value into [1, 2): exact as fp16 for a bf16 or an 8-bit latent, but for what lies 2^-14 below that
 // value.  Warps 0-7 gather and convert them, then take the results out of TMEM: a key row is scaled by the
 // stored alpha^k, a value row by its share of the tile's common exponent.  A thread holds 64 columns of a token,
-// one 128-byte line of a block, and stores it 32 bytes at a time.  Warp 8 streams the packed weights through a
+// one 128-byte line of a block; quads of lanes exchange pieces so that each store writes whole lines.  Warp 8 streams the packed weights through a
 // ring, warp 9 issues the products (M = 128, N = 128 or 256, K = 64 a stage), the accumulator double-buffered.
 //
 // Bound: the tensor core for many tokens (2 d_c flops a value); next to it the weights, which every tile
@@ -561,32 +561,38 @@ __global__ void __launch_bounds__(kThreadsE, NV == 1 ? 2 : 1) prefill_expand_ker
                 if (cb >= blocks) continue;
                 const bool key = cb < p.G * nkb;
                 float f;
-                uint8_t* dst;
+                uint8_t* dst;                                // of the block
+                int split = 0;                               // what rows from 64 on add (a matrix's values lie by 64 tokens, then by 64 columns)
                 if (key) {
                     // NaN where the latent is not finite: rows that see the token become NaN, others do not
                     f = et == kBad ? __int_as_float(0x7fc00000) : et == kNone ? 0.f : ldexpf(al_now, et + we[cb / nkb]);
-                    dst = p.kc + ((size_t)tile * p.G * nkb + cb) * kBlock + row * 128;
+                    dst = p.kc + ((size_t)tile * p.G * nkb + cb) * kBlock;
                 } else {
                     f = et == kBad || et == kNone ? 0.f : ldexpf(1.f, et - e_tile);
-                    // a matrix's values by 64 tokens, then by 64 columns
                     const int m = (cb - p.G * nkb) / nvb, c = (cb - p.G * nkb) % nvb;
-                    dst = p.v + (((size_t)tile * p.Gv + m) * nvb * 2 + (row >> 6) * nvb + c) * (kBlock / 2) + (row & 63) * 128;
+                    dst = p.v + ((size_t)tile * p.Gv + m) * nvb * kBlock + c * (kBlock / 2);
+                    split = (nvb - 1) * (kBlock / 2);
                 }
                 const bool as_bf = bf && !key;
                 const uint64_t f2 = dec::f2(f, f);
+                uint32_t h[4][8];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {                // two neighbouring 16-byte pieces, in swizzled order
-                    uint32_t h[2][4];
+                for (int c = 0; c < 4; ++c)
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const float2 x = dec::f2_unpack(dec::f2_mul(dec::f2(__uint_as_float(v[16 * c + 2 * i]), __uint_as_float(v[16 * c + 2 * i + 1])), f2));
-                        h[i >> 2][i & 3] = as_bf ? pack_bf16(x.x, x.y) : pack_f16(x.x, x.y);
+                        h[c][i] = as_bf ? pack_bf16(x.x, x.y) : pack_f16(x.x, x.y);
                     }
-                    uint8_t* to = dst + ((c ^ ((row >> 1) & 3)) << 5);
-                    uint32_t u[4], w[4];
+                quad_transpose(h, lane);
+                const int r0 = row & ~3;
+                dst += r0 * 128 + (r0 >= 64 ? split : 0);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) { u[i] = row & 1 ? h[1][i] : h[0][i]; w[i] = row & 1 ? h[0][i] : h[1][i]; }
-                    st_global_v8(to, u, w);
+                for (int k = 0; k < 4; ++k) {                // row r0 + k: two neighbouring 16-byte pieces, in swizzled order
+                    const int r = r0 + k;
+                    uint8_t* to = dst + k * 128 + (((lane & 3) ^ ((r >> 1) & 3)) << 5);
+                    const uint32_t (&one)[8] = h[k];
+                    if (k & 1) st_global_v8(to, {one[4], one[5], one[6], one[7]}, {one[0], one[1], one[2], one[3]});
+                    else st_global_v8(to, {one[0], one[1], one[2], one[3]}, {one[4], one[5], one[6], one[7]});
                 }
                 }
             }
