@@ -7,8 +7,9 @@
 //
 // Bound: HBM, a row read and written once.  What costs time beyond that is the chain row -> sequence ->
 // page -> slot in front of the row's own load, so a warp takes four neighbouring rows, its lanes follow the
-// four chains at once, and the four rows' loads are all in flight together.  16-byte accesses (8 bytes of
-// codes) where d_c, d_r and the bases allow, else element by element.
+// four chains at once, and all that the four rows need -- latents, RoPE keys, scales, alpha^k -- is on its way before
+// the first value is used.  16-byte accesses (8 bytes of codes) where d_c, d_r and the bases allow, else element by
+// element.
 #include "common.cuh"
 
 namespace qkmla {
@@ -31,27 +32,30 @@ struct ReadParams {
     int* status;
 };
 
-// 8 elements of a row as fp32.
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&v)[8]) {
-    if constexpr (sizeof(T) == 4) {
-        const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-    } else if constexpr (sizeof(T) == 2) {
-        const uint4 u = *reinterpret_cast<const uint4*>(p);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+// 8 elements of a row as they are stored, and as fp32.
+template <typename T> struct Eight {
+    uint32_t w[2 * sizeof(T)];
+    __device__ __forceinline__ void load(const T* p) {
+        if constexpr (sizeof(T) == 1) {
+            const uint2 u = *reinterpret_cast<const uint2*>(p);
+            w[0] = u.x; w[1] = u.y;
+        } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[2 * i] = __uint_as_float(w[i] << 16);
-            v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+                const uint4 u = reinterpret_cast<const uint4*>(p)[i];
+                w[4 * i] = u.x; w[4 * i + 1] = u.y; w[4 * i + 2] = u.z; w[4 * i + 3] = u.w;
+            }
         }
-    } else {
-        const uint2 u = *reinterpret_cast<const uint2*>(p);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = e4m3_to_float((uint8_t)((i < 4 ? u.x : u.y) >> (8 * (i & 3))));
     }
-}
+    __device__ __forceinline__ void get(float (&v)[8], float scale) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if constexpr (sizeof(T) == 4) v[i] = __uint_as_float(w[i]);
+            else if constexpr (sizeof(T) == 2) v[i] = __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
+            else v[i] = e4m3_to_float((uint8_t)(w[i >> 2] >> (8 * (i & 3)))) * scale;
+        }
+    }
+};
 __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
     reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
     reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
@@ -68,37 +72,6 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
 __device__ __forceinline__ float one(const float* p) { return *p; }
 __device__ __forceinline__ float one(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 __device__ __forceinline__ float one(const uint8_t* p) { return e4m3_to_float(*p); }
-
-// The n elements at src[j] (times scale[j]) to dst + j * n, for the rows j whose bit is set.
-template <typename T, typename OT, bool VEC>
-__device__ __forceinline__ void copy_rows(const T* const (&src)[kRowsW], OT* dst, int n, const float (&scale)[kRowsW],
-                                          unsigned rows, int lane) {
-    if constexpr (VEC) {
-        for (int e = lane * 8; e < n; e += 256) {
-            float v[kRowsW][8];
-#pragma unroll
-            for (int j = 0; j < kRowsW; ++j)
-                if (rows >> j & 1) load8(src[j] + e, v[j]);
-#pragma unroll
-            for (int j = 0; j < kRowsW; ++j)
-                if (rows >> j & 1) {
-                    if constexpr (sizeof(T) == 1) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) v[j][i] *= scale[j];
-                    }
-                    store8(dst + (int64_t)j * n + e, v[j]);
-                }
-        }
-    } else {
-        for (int j = 0; j < kRowsW; ++j)
-            if (rows >> j & 1)
-                for (int e = lane; e < n; e += 32) {
-                    float v = one(src[j] + e);
-                    if constexpr (sizeof(T) == 1) v *= scale[j];
-                    Elem<OT>::store(dst + (int64_t)j * n + e, v);
-                }
-    }
-}
 
 // CT: the latent's stored type (uint8_t: e4m3 codes), RT: the RoPE key's.
 template <typename CT, typename RT, typename OT, bool VEC>
@@ -130,30 +103,85 @@ __global__ void __launch_bounds__(kThreadsC) read_cache_kernel(const ReadParams 
     const unsigned rows = __ballot_sync(0xffffffffu, slot >= 0);
     if (!rows) return;
     const int64_t row_bytes = (int64_t)p.d_c * sizeof(CT) + (int64_t)p.d_r * sizeof(RT);
-    const CT* c[kRowsW];
-    const RT* r[kRowsW];
-    float scale[kRowsW];
-    int64_t sl[kRowsW];
+    float my_scale = 1.f;
+    if (sizeof(CT) == 1 && slot >= 0) my_scale = p.kv_scale[slot];       // lane j's row
+    OT *out_c = reinterpret_cast<OT*>(p.c) + row0 * p.d_c, *out_r = reinterpret_cast<OT*>(p.r) + row0 * p.d_r;
+    auto row_of = [&](int j) { return p.kv + max((int64_t)0, __shfl_sync(0xffffffffu, slot, j)) * row_bytes; };
+    // the first 32 of the four rows' alpha^k
+    float al = 0.f;
+    const int aj = p.G > 0 ? lane / p.G : 4, ag = lane - aj * p.G;
+    const int64_t a_slot = __shfl_sync(0xffffffffu, slot, aj & 3);
+    const bool a_there = p.ak_out && aj < kRowsW && (rows >> (aj & 3) & 1);
+    if (a_there) al = p.ak_f16 ? load_alpha<true>(p.ak, a_slot * p.G + ag) : load_alpha<false>(p.ak, a_slot * p.G + ag);
+    if constexpr (VEC) {
+        // RoPE keys: a vector a lane, first all rows' that 32 lanes hold
+        const int rv = p.d_r / 8, rj = rv > 0 ? lane / rv : 4, re = (lane - rj * rv) * 8;
+        const uint8_t* r_row = row_of(rj & 3);
+        const bool r_there = rv > 0 && rj < kRowsW && (rows >> (rj & 3) & 1);
+        Eight<RT> rope;
+        if (r_there) rope.load(reinterpret_cast<const RT*>(r_row + (int64_t)p.d_c * sizeof(CT)) + re);
+        constexpr int kStep = sizeof(CT) == 4 ? 256 : 512;   // latents of a row in flight
+        for (int e0 = 0; e0 < p.d_c; e0 += kStep) {
+            Eight<CT> x[kRowsW][kStep / 256];
 #pragma unroll
-    for (int j = 0; j < kRowsW; ++j) {
-        sl[j] = __shfl_sync(0xffffffffu, slot, j);
-        if (sl[j] < 0) sl[j] = 0;
-        const uint8_t* base = p.kv + sl[j] * row_bytes;
-        c[j] = reinterpret_cast<const CT*>(base);
-        r[j] = reinterpret_cast<const RT*>(base + (int64_t)p.d_c * sizeof(CT));
-        scale[j] = sizeof(CT) == 1 ? p.kv_scale[sl[j]] : 1.f;
-    }
-    if (p.ak_out)
-        for (int e = lane; e < kRowsW * p.G; e += 32) {
-            const int j = e / p.G, g = e - j * p.G;
-            int64_t s = sl[0];
+            for (int j = 0; j < kRowsW; ++j) {
+                const CT* c = reinterpret_cast<const CT*>(row_of(j));
 #pragma unroll
-            for (int q = 1; q < kRowsW; ++q) s = j == q ? sl[q] : s;
-            if (rows >> j & 1)
-                p.ak_out[(row0 + j) * p.G + g] = p.ak_f16 ? load_alpha<true>(p.ak, s * p.G + g) : load_alpha<false>(p.ak, s * p.G + g);
+                for (int q = 0; q < kStep / 256; ++q)
+                    if ((rows >> j & 1) && e0 + q * 256 + lane * 8 < p.d_c) x[j][q].load(c + e0 + q * 256 + lane * 8);
+            }
+#pragma unroll
+            for (int j = 0; j < kRowsW; ++j) {
+                const float scale = __shfl_sync(0xffffffffu, my_scale, j);
+#pragma unroll
+                for (int q = 0; q < kStep / 256; ++q) {
+                    const int e = e0 + q * 256 + lane * 8;
+                    if ((rows >> j & 1) && e < p.d_c) {
+                        float v[8];
+                        x[j][q].get(v, scale);
+                        store8(out_c + (int64_t)j * p.d_c + e, v);
+                    }
+                }
+            }
         }
-    copy_rows<CT, OT, VEC>(c, reinterpret_cast<OT*>(p.c) + row0 * p.d_c, p.d_c, scale, rows, lane);
-    if (p.d_r > 0) copy_rows<RT, OT, VEC>(r, reinterpret_cast<OT*>(p.r) + row0 * p.d_r, p.d_r, scale, rows, lane);
+        if (r_there) {
+            float v[8];
+            rope.get(v, 1.f);
+            store8(out_r + (int64_t)rj * p.d_r + re, v);
+        }
+        if (rv > 8)                                          // more than 32 vectors
+            for (int j = 0; j < kRowsW; ++j) {
+                const uint8_t* row = row_of(j);
+                if (rows >> j & 1)
+                    for (int e = lane * 8; e < p.d_r; e += 256) {
+                        rope.load(reinterpret_cast<const RT*>(row + (int64_t)p.d_c * sizeof(CT)) + e);
+                        float v[8];
+                        rope.get(v, 1.f);
+                        store8(out_r + (int64_t)j * p.d_r + e, v);
+                    }
+            }
+    } else {
+        for (int j = 0; j < kRowsW; ++j) {
+            const uint8_t* row = row_of(j);
+            const float scale = __shfl_sync(0xffffffffu, my_scale, j);
+            if (!(rows >> j & 1)) continue;
+            for (int e = lane; e < p.d_c; e += 32) {
+                float v = one(reinterpret_cast<const CT*>(row) + e);
+                if constexpr (sizeof(CT) == 1) v *= scale;
+                Elem<OT>::store(out_c + (int64_t)j * p.d_c + e, v);
+            }
+            for (int e = lane; e < p.d_r; e += 32)
+                Elem<OT>::store(out_r + (int64_t)j * p.d_r + e, one(reinterpret_cast<const RT*>(row + (int64_t)p.d_c * sizeof(CT)) + e));
+        }
+    }
+    if (a_there) p.ak_out[(row0 + aj) * p.G + ag] = al;
+    if (p.ak_out && p.G > 8)                                 // more than 32 of them
+        for (int j = 0; j < kRowsW; ++j) {
+            const int64_t sl = __shfl_sync(0xffffffffu, slot, j);
+            if (rows >> j & 1)
+                for (int g = lane; g < p.G; g += 32)
+                    p.ak_out[(row0 + j) * p.G + g] = p.ak_f16 ? load_alpha<true>(p.ak, sl * p.G + g) : load_alpha<false>(p.ak, sl * p.G + g);
+        }
 }
 
 template <typename CT, typename RT, typename OT>

@@ -12,8 +12,8 @@
 // small angle keeps its relative precision; sincospif takes it from there.
 //
 // Bound: HBM, each element read and written once (3 flops an element).  A block of 256 threads takes whole
-// rows: it forms the row's cosines and sines once in shared memory, ahead of the wait for the previous
-// kernel, and every head uses them.  16-byte accesses where strides, bases and d_r allow them, else one
+// rows, up to four vectors (or pairs of them) a thread: their loads go out first, and while they are on their way the
+// block forms the rows' cosines and sines once in shared memory, for every head.  16-byte accesses where strides, bases and d_r allow them, else one
 // pair at a time.
 #include <cmath>
 
@@ -80,45 +80,45 @@ __global__ void __launch_bounds__(kThreadsR) rope_kernel(const __grid_constant__
     const int nr = min(p.rows_per_block, p.rows - r0);
     const int h0 = blockIdx.y * p.heads_per_block;
     const int nh = min(p.heads_per_block, p.heads - h0);
+    const int units = p.pairs / kPairs;                 // a head's
+    const int n = nr * nh * units;                      // at most kThreadsR * kItems
+    pdl_wait();
+    pdl_trigger();
+    float a[kItems][V], b[kItems][HALF ? V : 1];
+    int at[kItems];
+    int64_t to[kItems];
+#pragma unroll
+    for (int j = 0; j < kItems; ++j) {
+        const int k = threadIdx.x + j * kThreadsR;
+        at[j] = -1;
+        if (k >= n) continue;
+        const int u = k % units, rh = k / units;
+        const int r = rh / nh, h = rh - r * nh;
+        const T* x = (const T*)p.x + (int64_t)(r0 + r) * p.xr + (int64_t)(h0 + h) * p.xh + u * V;
+        at[j] = r * p.pairs + u * kPairs;
+        to[j] = (int64_t)(r0 + r) * p.yr + (int64_t)(h0 + h) * p.yh + u * V;
+        if constexpr (V == Vec<T>::kFull) {
+            Vec<T>::load(x, a[j]);
+            if constexpr (HALF) Vec<T>::load(x + p.pairs, b[j]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                a[j][e] = Elem<T>::load(x + e);
+                if constexpr (HALF) b[j][e] = Elem<T>::load(x + p.pairs + e);
+            }
+        }
+    }
     for (int k = threadIdx.x; k < nr * p.pairs; k += kThreadsR) {
         const int r = k / p.pairs, i = k - r * p.pairs;
-        const int64_t a = (int64_t)((uint64_t)(int64_t)p.positions[r0 + r] * p.turn[i]);
+        const int64_t turn = (int64_t)((uint64_t)(int64_t)p.positions[r0 + r] * p.turn[i]);
         float s, c;
-        sincospif((float)a * 1.0842021724855044e-19f, &s, &c);      // 2^-63: sin and cos of pi x take half turns
+        sincospif((float)turn * 1.0842021724855044e-19f, &s, &c);   // 2^-63: sin and cos of pi x take half turns
         cs[k] = c * p.gain;
         sn[k] = s * p.gain * p.sign;
     }
-    pdl_wait();
-    pdl_trigger();
     __syncthreads();
-    const int units = p.pairs / kPairs;                 // a head's
-    const int n = nr * nh * units;
-    for (int k0 = threadIdx.x; k0 < n; k0 += kThreadsR * kItems) {
-        float a[kItems][V], b[kItems][HALF ? V : 1];
-        int at[kItems];
-        int64_t to[kItems];
 #pragma unroll
-        for (int j = 0; j < kItems; ++j) {
-            const int k = k0 + j * kThreadsR;
-            if (k >= n) { at[j] = -1; continue; }
-            const int u = k % units, rh = k / units;
-            const int r = rh / nh, h = rh - r * nh;
-            const T* x = (const T*)p.x + (int64_t)(r0 + r) * p.xr + (int64_t)(h0 + h) * p.xh + u * V;
-            at[j] = r * p.pairs + u * kPairs;
-            to[j] = (int64_t)(r0 + r) * p.yr + (int64_t)(h0 + h) * p.yh + u * V;
-            if constexpr (V == Vec<T>::kFull) {
-                Vec<T>::load(x, a[j]);
-                if constexpr (HALF) Vec<T>::load(x + p.pairs, b[j]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    a[j][e] = Elem<T>::load(x + e);
-                    if constexpr (HALF) b[j][e] = Elem<T>::load(x + p.pairs + e);
-                }
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < kItems; ++j) {
+    for (int j = 0; j < kItems; ++j) {
             if (at[j] < 0) continue;
 #pragma unroll
             for (int i = 0; i < kPairs; ++i) {
@@ -141,7 +141,6 @@ __global__ void __launch_bounds__(kThreadsR) rope_kernel(const __grid_constant__
                     if constexpr (HALF) Elem<T>::store(y + p.pairs + e, b[j][e]);
                 }
             }
-        }
     }
 }
 
