@@ -37,36 +37,21 @@ struct RopeParams {
     float gain, sign;
 };
 
-template <typename T> struct Vec;          // V elements as they are loaded
-template <> struct Vec<float> {
-    static constexpr int kFull = 4;
-    static __device__ __forceinline__ void load(const float* p, float (&v)[4]) {
-        const float4 f = *reinterpret_cast<const float4*>(p);
-        v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
-    }
-    static __device__ __forceinline__ void store(float* p, const float (&v)[4]) {
-        *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-    }
-};
-template <> struct Vec<__nv_bfloat16> {
-    static constexpr int kFull = 8;
-    static __device__ __forceinline__ void load(const __nv_bfloat16* p, float (&v)[8]) {
-        const uint4 u = *reinterpret_cast<const uint4*>(p);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+// V elements as they lie in memory: 16 bytes, or V of them one by one.
+template <typename T> constexpr int kFull = 16 / (int)sizeof(T);
+template <typename T, int V> struct Held {
+    alignas(V == kFull<T> ? 16 : alignof(T)) T e[V];
+    __device__ __forceinline__ void load(const T* p) {
+        if constexpr (V == kFull<T>) *reinterpret_cast<uint4*>(e) = *reinterpret_cast<const uint4*>(p);
+        else
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[2 * i] = __uint_as_float(w[i] << 16);
-            v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        }
+            for (int i = 0; i < V; ++i) e[i] = p[i];
     }
-    static __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&v)[8]) {
-        uint32_t w[4];
+    __device__ __forceinline__ void store(T* p) const {
+        if constexpr (V == kFull<T>) *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(e);
+        else
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-            w[i] = *reinterpret_cast<const uint32_t*>(&b);
-        }
-        *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int i = 0; i < V; ++i) p[i] = e[i];
     }
 };
 
@@ -84,7 +69,7 @@ __global__ void __launch_bounds__(kThreadsR) rope_kernel(const __grid_constant__
     const int n = nr * nh * units;                      // at most kThreadsR * kItems
     pdl_wait();
     pdl_trigger();
-    float a[kItems][V], b[kItems][HALF ? V : 1];
+    Held<T, V> a[kItems], b[HALF ? kItems : 1];
     int at[kItems];
     int64_t to[kItems];
 #pragma unroll
@@ -97,16 +82,8 @@ __global__ void __launch_bounds__(kThreadsR) rope_kernel(const __grid_constant__
         const T* x = (const T*)p.x + (int64_t)(r0 + r) * p.xr + (int64_t)(h0 + h) * p.xh + u * V;
         at[j] = r * p.pairs + u * kPairs;
         to[j] = (int64_t)(r0 + r) * p.yr + (int64_t)(h0 + h) * p.yh + u * V;
-        if constexpr (V == Vec<T>::kFull) {
-            Vec<T>::load(x, a[j]);
-            if constexpr (HALF) Vec<T>::load(x + p.pairs, b[j]);
-        } else {
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                a[j][e] = Elem<T>::load(x + e);
-                if constexpr (HALF) b[j][e] = Elem<T>::load(x + p.pairs + e);
-            }
-        }
+        a[j].load(x);
+        if constexpr (HALF) b[j].load(x + p.pairs);
     }
     for (int k = threadIdx.x; k < nr * p.pairs; k += kThreadsR) {
         const int r = k / p.pairs, i = k - r * p.pairs;
@@ -119,28 +96,20 @@ __global__ void __launch_bounds__(kThreadsR) rope_kernel(const __grid_constant__
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < kItems; ++j) {
-            if (at[j] < 0) continue;
+        if (at[j] < 0) continue;
 #pragma unroll
-            for (int i = 0; i < kPairs; ++i) {
-                const float c = cs[at[j] + i], s = sn[at[j] + i];
-                float *u, *v;
-                if constexpr (HALF) { u = &a[j][i]; v = &b[j][i]; }
-                else { u = &a[j][2 * i]; v = &a[j][2 * i + 1]; }
-                const float u2 = fmaf(-*v, s, *u * c), v2 = fmaf(*u, s, *v * c);
-                *u = u2;
-                *v = v2;
-            }
-            T* y = (T*)p.out + to[j];
-            if constexpr (V == Vec<T>::kFull) {
-                Vec<T>::store(y, a[j]);
-                if constexpr (HALF) Vec<T>::store(y + p.pairs, b[j]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    Elem<T>::store(y + e, a[j][e]);
-                    if constexpr (HALF) Elem<T>::store(y + p.pairs + e, b[j][e]);
-                }
-            }
+        for (int i = 0; i < kPairs; ++i) {
+            const float c = cs[at[j] + i], s = sn[at[j] + i];
+            T *u, *v;
+            if constexpr (HALF) { u = &a[j].e[i]; v = &b[j].e[i]; }
+            else { u = &a[j].e[2 * i]; v = &a[j].e[2 * i + 1]; }
+            const float x = Elem<T>::load(u), y = Elem<T>::load(v);
+            Elem<T>::store(u, fmaf(-y, s, x * c));
+            Elem<T>::store(v, fmaf(x, s, y * c));
+        }
+        T* y = (T*)p.out + to[j];
+        a[j].store(y);
+        if constexpr (HALF) b[j].store(y + p.pairs);
     }
 }
 
@@ -195,7 +164,7 @@ int launch_rope(RopeParams& p, cudaStream_t s) {
 
 template <typename T>
 int launch_rope_type(RopeParams& p, bool half, bool vec, cudaStream_t s) {
-    constexpr int F = Vec<T>::kFull;
+    constexpr int F = kFull<T>;
     if (half) return vec ? launch_rope<T, true, F>(p, s) : launch_rope<T, true, 1>(p, s);
     return vec ? launch_rope<T, false, F>(p, s) : launch_rope<T, false, 2>(p, s);
 }
