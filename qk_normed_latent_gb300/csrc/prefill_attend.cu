@@ -303,67 +303,65 @@ __global__ void __launch_bounds__(kThreadsA, 1) prefill_attend_kernel(const __gr
             int group = 0, unit = 0;                       // issued so far
             int freed = 0, freed_units = 0;
             uint32_t qe_phase = 0;                         // bit h
-            int last_halves = 0;                           // of the last piece with tiles
+            int last_halves = 0;                           // of the piece ahead, 0 if it has no tiles
             bool ok = true;
-            auto put = [&](const uint8_t* a, int na, const uint8_t* b2, int nb) {      // a group: na blocks at a, nb at b2
-                const int n = na + nb;
-#pragma unroll 1
-                while (ok && unit + n - kUnits > freed_units) {
-                    ok = wait_or_fail(&sh->empty[freed % kGroups], (freed / kGroups) & 1, &sh->fail);
-                    freed_units += (freed & 1) ? VU : KU;
-                    ++freed;
-                }
-                if (!ok) return;
-                uint64_t* bar = &sh->full[group % kGroups];
-                mbar_arrive_expect_tx(bar, n * kBlock);
-#pragma unroll 1
-                for (int i = 0; i < n; ++i) {
-                    bulk_load(ring + (unit % kUnits) * kBlock, i < na ? a + (size_t)i * kBlock : b2 + (size_t)(i - na) * kBlock, kBlock, bar);
-                    ++unit;
-                }
-                ++group;
-                *(volatile int*)&sh->issued = group;
-            };
 #pragma unroll 1
             for (int k = 0; ok; ++k) {
-                ok = wait_or_fail(&sh->piece_full[k & 1], (k >> 1) & 1, &sh->fail);
-                if (!ok) break;
+                if (!(ok = wait_or_fail(&sh->piece_full[k & 1], (k >> 1) & 1, &sh->fail))) break;
                 const Piece s = sh->piece[k & 1];
                 if (s.unit < 0) break;
-                const int g = (int)((int64_t)s.unit * p.G / p.units), gv = (int)((int64_t)s.unit * p.Gv / p.units);
-                const int halves = s.queries * p.hp > 128 ? 2 : 1;
-                auto tile_at = [&](int t) { return (size_t)s.tile0 + (t < s.head ? t : t + s.gap); };
-                int info = s.t0 < s.t1 ? p.tinfo[tile_at(s.t0)] : 0;
-                // (through shared memory: a load from L2 in the loop of the products or of the softmax would be waited for there)
-                auto key = [&](int t) {
-                    const size_t tile = tile_at(t);
-                    sh->info[(group >> 1) & 3] = info;
-                    if (t + 1 < s.t1) info = p.tinfo[tile_at(t + 1)];
-                    put(p.kc + (tile * p.G + g) * (size_t)((KU - 1) * kBlock), KU - 1, p.krope + tile * kBlock, 1);
-                };
-                if (s.t0 < s.t1) key(s.t0);
-                // a query half is read by the products until the last ones of the piece ahead have ended
+                const int n = s.t1 - s.t0, halves = n == 0 ? 0 : s.queries * p.hp > 128 ? 2 : 1;
+                const size_t g = (size_t)((int64_t)s.unit * p.G / p.units), gv = (size_t)((int64_t)s.unit * p.Gv / p.units);
+                size_t tile = 0;
+                int info_next = n > 0 ? p.tinfo[s.tile0 + (s.t0 < s.head ? s.t0 : s.t0 + s.gap)] : 0;
+                // keys and values of a tile in turn, the piece's queries behind the first keys
 #pragma unroll 1
-                for (int h = 0; h < 2 && ok; ++h) {
-                    if (h < last_halves) {
-                        ok = wait_or_fail(&sh->q_empty[h], (qe_phase >> h) & 1, &sh->fail);
-                        qe_phase ^= 1u << h;
+                for (int q = 0; q < max(2 * n, 1) && ok; ++q) {
+                    const bool value = q & 1;
+                    if (n > 0) {
+                        const int blocks = value ? VU : KU;
+                        if (!value) {
+                            const int t = s.t0 + (q >> 1);
+                            tile = (size_t)s.tile0 + (t < s.head ? t : t + s.gap);
+                            // (through shared memory: a load from L2 in the other warps' loops would be waited for there)
+                            sh->info[(group >> 1) & 3] = info_next;
+                            if (t + 1 < s.t1) info_next = p.tinfo[s.tile0 + (t + 1 < s.head ? t + 1 : t + 1 + s.gap)];
+                        }
+                        const uint8_t* src = value ? p.v + (tile * p.Gv + gv) * (size_t)(VU * kBlock) : p.kc + (tile * p.G + g) * (size_t)((KU - 1) * kBlock);
+#pragma unroll 1
+                        while (ok && unit + blocks - kUnits > freed_units) {
+                            ok = wait_or_fail(&sh->empty[freed % kGroups], (freed / kGroups) & 1, &sh->fail);
+                            freed_units += (freed & 1) ? VU : KU;
+                            ++freed;
+                        }
+                        if (!ok) break;
+                        uint64_t* bar = &sh->full[group % kGroups];
+                        mbar_arrive_expect_tx(bar, blocks * kBlock);
+#pragma unroll 1
+                        for (int i = 0; i < blocks; ++i, ++unit)
+                            bulk_load(ring + (unit % kUnits) * kBlock, !value && i == KU - 1 ? p.krope + tile * kBlock : src + (size_t)i * kBlock, kBlock, bar);
+                        ++group;
+                        *(volatile int*)&sh->issued = group;
                     }
-                    if (!ok || s.t0 == s.t1 || h >= halves || k == 0) continue;       // (the first piece's rows go to shared memory directly)
-                    if (h == 0) ok = wait_or_fail(&sh->conv_full[k & 1], ((k - 1) >> 1) & 1, &sh->fail);
-                    if (!ok) break;
-                    mbar_arrive_expect_tx(&sh->q_full[h], kHalf);
-                    bulk_load(sm + h * kHalf, p.qs + ((size_t)(2 * cta + (k & 1)) * 2 + h) * kHalf, kHalf, &sh->q_full[h]);
-                    *(volatile int*)&sh->q_issued[h] = *(volatile int*)&sh->q_issued[h] + 1;
-                }
-                if (k > 0) mbar_arrive(&sh->piece_empty[(k - 1) & 1]);                // the converted rows of piece k - 1 are no longer read
-                if (s.t0 < s.t1) last_halves = halves;
-                else if (last_halves) last_halves = 0;
+                    if (q > 0) continue;
+                    // a query half is read by the products until the last ones of the piece ahead have ended
+                    bool converted = false;
 #pragma unroll 1
-                for (int t = s.t0; t < s.t1 && ok; ++t) {
-                    const size_t tile = tile_at(t);
-                    put(p.v + (tile * p.Gv + gv) * (size_t)(VU * kBlock), VU, nullptr, 0);
-                    if (t + 1 < s.t1) key(t + 1);
+                    for (int h = 0; h < 2 && ok; ++h) {
+                        if (h < last_halves) {
+                            ok = wait_or_fail(&sh->q_empty[h], (qe_phase >> h) & 1, &sh->fail);
+                            qe_phase ^= 1u << h;
+                        }
+                        if (!ok || h >= halves || k == 0) continue;            // (the first piece's rows go to shared memory directly)
+                        if (!converted) ok = wait_or_fail(&sh->conv_full[k & 1], ((k - 1) >> 1) & 1, &sh->fail);
+                        converted = true;
+                        if (!ok) break;
+                        mbar_arrive_expect_tx(&sh->q_full[h], kHalf);
+                        bulk_load(sm + h * kHalf, p.qs + ((size_t)(2 * cta + (k & 1)) * 2 + h) * kHalf, kHalf, &sh->q_full[h]);
+                        *(volatile int*)&sh->q_issued[h] = *(volatile int*)&sh->q_issued[h] + 1;
+                    }
+                    if (k > 0) mbar_arrive(&sh->piece_empty[(k - 1) & 1]);     // the converted rows of piece k - 1 are no longer read
+                    last_halves = halves;
                 }
             }
         }
@@ -506,7 +504,7 @@ __global__ void __launch_bounds__(kThreadsA, 1) prefill_attend_kernel(const __gr
                         if (h + part == 0 && !wait_or_fail(&sh->full[gv % kGroups], (gv / kGroups) & 1, &sh->fail)) goto give_up;
                         tc_fence_after();
                         const uint32_t v = v_desc + (uint32_t)(VU == 2 ? ((unit + part) % kUnits) * kStep : (unit % kUnits) * kStep + part * (kStep / 2));
-#pragma unroll
+#pragma unroll 1
                         for (int i = 0; i < 4; ++i)
                             mma_ts(o, a + part * 32 + i * 8, v + (uint32_t)(i * 128), id_o | fmt, (!cur_first || part > 0 || i > 0) ? 1u : 0u);
                     }
@@ -527,10 +525,10 @@ __global__ void __launch_bounds__(kThreadsA, 1) prefill_attend_kernel(const __gr
                     tc_fence_after();
                     const int u = unit + (cur > 0 ? VU : 0);
                     const uint32_t d = tmem + kS + h * 128;
-#pragma unroll
+#pragma unroll 1
                     for (int blk = 0; blk < KU; ++blk) {
                         const uint32_t kd = k_desc + (uint32_t)(((u + blk) % kUnits) * kStep), qd = q_desc + (uint32_t)((h * KU + blk) * kStep);
-#pragma unroll
+#pragma unroll 1
                         for (int kk = 0; kk < (blk < KU - 1 ? 4 : DR / 16); ++kk)
                             mma_ss(d, qd + (uint32_t)(kk * 2), kd + (uint32_t)(kk * 2), id_s, (blk > 0 || kk > 0) ? 1u : 0u);
                     }
@@ -643,25 +641,30 @@ give_up:
                 tc_fence_after();
                 const int info = sh->info[tiles & 3], e = (info & 255) - 64;
                 const bool as_bf = (info & 256) != 0;
+                if (edge) {
+                    // hidden logits to -inf, in place: a rolled loop of 16 columns
+                    const int end = n_row - first, from = p.window > 0 ? end - p.window : 0, sink = p.window > 0 ? p.sinks - first : 0;
+#pragma unroll 1
+                    for (int q = 0; q < 128; q += 32) {
+                        uint32_t seen = seen32(q, end, from, sink);
+#pragma unroll 1
+                        for (int r = 0; r < 32; r += 16, seen >>= 16) {
+                            if (__all_sync(0xffffffffu, (seen & 0xffffu) == 0xffffu)) continue;
+                            uint32_t v[16];
+                            tmem_ld16(t_s + q + r, v);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int i2 = 0; i2 < 16; ++i2) v[i2] = seen >> i2 & 1 ? v[i2] : 0xff800000u;
+                            tmem_st16(t_s + q + r, v);
+                        }
+                    }
+                    tmem_wait_st();
+                }
                 float x[128], top, top2;
                 tmem_ld64_max(t_s, x, top);
                 tmem_ld64_max(t_s + 64, x + 64, top2);
                 tmem_wait_ld();
                 top = fmaxf(top, top2);
-                if (edge) {
-                    const int end = n_row - first, from = p.window > 0 ? end - p.window : 0, sink = p.window > 0 ? p.sinks - first : 0;
-                    top = -INFINITY;
-#pragma unroll
-                    for (int q = 0; q < 128; q += 32) {
-                        const uint32_t seen = seen32(q, end, from, sink);
-#pragma unroll
-                        for (int r = 0; r < 32; r += 2) {
-                            x[q + r] = seen >> r & 1 ? x[q + r] : -INFINITY;
-                            x[q + r + 1] = seen >> (r + 1) & 1 ? x[q + r + 1] : -INFINITY;
-                            top = max3(top, x[q + r], x[q + r + 1]);
-                        }
-                    }
-                }
                 const float cand = fmaf(top, c, (float)e);
                 const bool move = cand > m + 8.f;
                 if (__any_sync(0xffffffffu, move)) {
