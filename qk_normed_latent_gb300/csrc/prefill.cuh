@@ -51,10 +51,11 @@ struct Params {
     int nq;                                // slots of query tiles: rows / tq + B
     int max_tiles;                         // total_tokens / 128 + B
     int ctas;                              // of the attention kernel
+    int deep;                              // places a CTA: units nq / ctas, rounded up
     // the workspace
     int4* seq;                             // [B]: length, first tile, first row, rows
     int4* qinfo;                           // [nq][2]: {b, first query, tiles, head tiles}, {gap, length of the first query, queries, -}
-    int64_t* pre;                          // [nq + 1]: cost of the slots ahead
+    int64_t* pre;                          // [ctas deep + 1]: cost of the places ahead
     int* tinfo;                            // [max_tiles]: exponent + 64, | 256 where the values are bf16
     uint8_t *krope, *kc, *v;               // blocks: [tile], [tile][G][d_h / 64], [tile][G_v][d_v / 64]
     uint8_t* qs;                           // [cta][2][half][d_h / 64 + 1]: the normalised queries of a CTA's next two pieces
@@ -76,60 +77,67 @@ constexpr size_t kWeightTable = 4096;      // int32 exponents of up to 1024 matr
 // b sequences ahead takes at most b slots, so ranges never meet and need no sum over the sequences.
 __device__ __forceinline__ int first_slot(int row, int b, int tq) { return row / tq + b; }
 
-// A place in the list of all work (unit-major, then slots): tile `t` of slot `j` of unit `u`.
+// The list of all work.  Query tiles in their own order -- by unit, sequence and row -- are dealt out to the CTAs in turn,
+// and the list is one CTA's hand after the other's: place m = c deep + i holds the tile i ctas + c.  An even share of the
+// list is then about a hand, and at any time the CTAs work on neighbouring tiles, whose keys and values the L2 holds (a
+// CTA on neighbouring tiles of its own has all units' going at once: 2.6 times the traffic to memory on whole prompts).
+__device__ __forceinline__ bool tile_of_place(const Params& p, int m, int& u, int& j) {
+    const int c = m / p.deep, n = (m - c * p.deep) * p.ctas + c;
+    u = n / p.nq;
+    j = n - u * p.nq;
+    return u < p.units;
+}
+
+// A place, and a tile `t` of tokens of it out of nt.
 struct Place {
-    int u, j, t, nt;
-    __device__ __forceinline__ bool same(const Place& o) const { return u == o.u && j == o.j && t == o.t; }
+    int m, t, nt;
+    __device__ __forceinline__ bool same(const Place& o) const { return m == o.m && t == o.t; }
     __device__ __forceinline__ bool inside() const { return t > 0 && t < nt; }
 };
-
-// The place of cost x: whole warp.  A cut that would leave a piece of fewer than kMinPiece tiles moves to
-// the query tile's start or end.
-__device__ __forceinline__ Place place_of(const Params& p, int64_t x, int64_t one) {
+// A cut that would leave a piece of fewer than kMinPiece tiles moves to the query tile's start or end.
+__device__ __forceinline__ Place place_at(const Params& p, int m, int64_t x) {
     Place r;
+    r.m = m;
+    const int64_t at = p.pre[m];
+    r.nt = (int)(p.pre[m + 1] - at) - kCostStart;
+    const int t = (int)(x - at) - kCostStart;
+    r.t = t < kMinPiece ? 0 : r.nt - t < kMinPiece ? r.nt : t;
+    return r;
+}
+
+// The place of cost x, 0 <= x <= all, all > 0 (for x = all the end of the last query tile): whole warp.
+__device__ __forceinline__ Place place_of(const Params& p, int64_t x, int64_t all) {
+    const bool end = x == all;
+    if (end) --x;
     const int lane = threadIdx.x & 31;
-    r.u = (int)(x / one);
-    if (r.u >= p.units) { r.u = p.units; r.j = 0; r.t = 0; r.nt = 0; return r; }
-    const int64_t y = x - (int64_t)r.u * one;
-    int lo = 0, n = p.nq;                                  // the last j in [lo, lo + n) with pre[j] <= y
+    int lo = 0, n = p.ctas * p.deep;                       // the last m in [lo, lo + n) with pre[m] <= x
 #pragma unroll 1
     while (n > 1) {
         const int step = (n + 31) / 32;
-        const int at = lo + lane * step;
-        const bool le = lane * step < n && p.pre[at] <= y;
+        const bool le = lane * step < n && p.pre[lo + lane * step] <= x;
         const unsigned m = __ballot_sync(0xffffffffu, le);
         const int k = 31 - __clz(m | 1u);
         n = min(step, n - k * step);
         lo += k * step;
     }
-    r.j = lo;
-    const int64_t at = p.pre[lo];
-    r.nt = (int)(p.pre[lo + 1] - at) - kCostStart;
-    int t = (int)(y - at) - kCostStart;
-    if (t < kMinPiece) t = 0;
-    else if (r.nt - t < kMinPiece) t = r.nt;
-    r.t = t;
+    Place r = place_at(p, lo, x);
+    if (end) r.t = r.nt;
     return r;
 }
 
 // The same by one thread.
-__device__ __forceinline__ Place place_of_one(const Params& p, int64_t x, int64_t one) {
-    Place r;
-    r.u = (int)(x / one);
-    if (r.u >= p.units) { r.u = p.units; r.j = 0; r.t = 0; r.nt = 0; return r; }
-    const int64_t y = x - (int64_t)r.u * one;
-    int lo = 0, hi = p.nq - 1;
+__device__ __forceinline__ Place place_of_one(const Params& p, int64_t x, int64_t all) {
+    const bool end = x == all;
+    if (end) --x;
+    int lo = 0, hi = p.ctas * p.deep - 1;
 #pragma unroll 1
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (p.pre[mid] <= y) lo = mid;
+        if (p.pre[mid] <= x) lo = mid;
         else hi = mid - 1;
     }
-    r.j = lo;
-    const int64_t at = p.pre[lo];
-    r.nt = (int)(p.pre[lo + 1] - at) - kCostStart;
-    const int t = (int)(y - at) - kCostStart;
-    r.t = t < kMinPiece ? 0 : r.nt - t < kMinPiece ? r.nt : t;
+    Place r = place_at(p, lo, x);
+    if (end) r.t = r.nt;
     return r;
 }
 

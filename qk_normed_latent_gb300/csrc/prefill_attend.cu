@@ -83,14 +83,13 @@ struct Walk {
     __device__ __forceinline__ bool next(const Params& p, Piece& s) {
 #pragma unroll 1
         for (;;) {
-            if (at.u > end.u || (at.u == end.u && at.j > end.j) || at.u >= p.units) return false;
-            const bool last = at.u == end.u && at.j == end.j;
-            if (last && end.t == 0) return false;
-            const int j = at.j;
-            s.unit = at.u;
+            if (at.m > end.m || at.m >= p.ctas * p.deep) return false;
+            const bool last = at.m == end.m;
+            if (last && end.t == 0 && end.nt > 0) return false;
             s.t0 = first ? at.t : 0;
             first = false;
-            if (++at.j == p.nq) { at.j = 0; ++at.u; }
+            int j;
+            if (!tile_of_place(p, at.m++, s.unit, j)) continue;
             const int4 a = p.qinfo[2 * j], b = p.qinfo[2 * j + 1];
             if (a.x < 0) continue;                         // an unused slot
             s.nt = a.z;
@@ -113,12 +112,6 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-__device__ __forceinline__ float max3(float a, float b, float c) {
-    float y;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
-    return y;
-}
-
 // ---- queries ----
 // Four rows of a query tile, rt .. rt + 3, eight lanes a row: normalised and times the gains as fp16 to row rt & 127 of
 // the half at `dst` (blocks of 64 columns).  Normalised values are at most sqrt d; the gains come with a power of two that
@@ -290,7 +283,7 @@ __global__ void __launch_bounds__(kThreadsA, 1) prefill_attend_kernel(const __gr
     const uint32_t tmem = sh->tmem;
     pdl_wait();
     pdl_trigger();
-    const int64_t one = p.pre[p.nq], all = one * p.units;
+    const int64_t all = p.pre[p.ctas * p.deep];
     const int n_cta = sharing(p, all);
     const bool busy = all > 0 && cta < n_cta;              // uniform
 
@@ -554,7 +547,7 @@ give_up:
 #pragma unroll 1
         for (int i = 0; i < 2; ++i) {
             walk.at = walk.end;
-            walk.end = place_of(p, share_start(all, n_cta, cta + i), one);
+            walk.end = place_of(p, share_start(all, n_cta, cta + i), all);
         }
         walk.first = true;
         bool ok = true;
@@ -785,7 +778,7 @@ template <int DV>
 __global__ void __launch_bounds__(kThreadsJ) prefill_join_kernel(const __grid_constant__ Params p) {
     pdl_wait();
     pdl_trigger();
-    const int64_t one = p.pre[p.nq], all = one * p.units;
+    const int64_t all = p.pre[p.ctas * p.deep];
     const int n_cta = sharing(p, all);
     const int k = blockIdx.x + 1;
     if (all == 0 || k >= n_cta) return;
@@ -793,13 +786,13 @@ __global__ void __launch_bounds__(kThreadsJ) prefill_join_kernel(const __grid_co
     __shared__ Place places[kMaxCtas + 1];
     __shared__ int parts[kMaxCtas];
     __shared__ int count;
-    for (int q = k - 1 + threadIdx.x; q <= n_cta; q += kThreadsJ) places[q] = place_of_one(p, share_start(all, n_cta, q), one);
+    for (int q = k - 1 + threadIdx.x; q <= n_cta; q += kThreadsJ) places[q] = place_of_one(p, share_start(all, n_cta, q), all);
     __syncthreads();
     const Place at = places[k];
     if (!at.inside()) return;
     if (k > 1) {
         const Place prev = places[k - 1];
-        if (prev.inside() && prev.u == at.u && prev.j == at.j) return;
+        if (prev.inside() && prev.m == at.m) return;
     }
     // parts: CTA k - 1's last piece, then the first pieces of CTAs k .. last - 1 (one that got no tile has none)
     if (threadIdx.x == 0) {
@@ -807,7 +800,7 @@ __global__ void __launch_bounds__(kThreadsJ) prefill_join_kernel(const __grid_co
         int n = 1;
         for (int q = k; q < n_cta; ++q) {
             const Place to = places[q + 1];
-            const bool same = to.u == at.u && to.j == at.j && to.t < at.nt;
+            const bool same = to.m == at.m && to.t < at.nt;
             if (!(same && to.t == places[q].t)) parts[n++] = 2 * q;
             if (!same) break;
         }
@@ -815,9 +808,11 @@ __global__ void __launch_bounds__(kThreadsJ) prefill_join_kernel(const __grid_co
     }
     __syncthreads();
     const int n = count;
-    const int4 a = p.qinfo[2 * at.j], b = p.qinfo[2 * at.j + 1];
+    int unit, j;
+    tile_of_place(p, at.m, unit, j);
+    const int4 a = p.qinfo[2 * j], b = p.qinfo[2 * j + 1];
     const int4 seq = p.seq[a.x];
-    const int gv = (int)((int64_t)at.u * p.Gv / p.units);
+    const int gv = (int)((int64_t)unit * p.Gv / p.units);
     const int e = reinterpret_cast<const int*>(p.weights)[p.G + gv];
     constexpr int kLanes = DV / 4;                          // lanes a row, 4 values each
     constexpr int kPerPass = kThreadsJ / kLanes;
@@ -838,7 +833,7 @@ __global__ void __launch_bounds__(kThreadsJ) prefill_join_kernel(const __grid_co
             sum = fmaf(w, ml.y, sum);
             o[0] = fmaf(w, v.x, o[0]); o[1] = fmaf(w, v.y, o[1]); o[2] = fmaf(w, v.z, o[2]); o[3] = fmaf(w, v.w, o[3]);
         }
-        const int head = at.u * p.hp + rt % p.hp;
+        const int head = unit * p.hp + rt % p.hp;
         const int64_t r = seq.z + a.y + i;
         const float inv = sum == 0.f ? 0.f : ldexpf(1.f / sum, e);
 #pragma unroll
@@ -928,6 +923,7 @@ int make_params(const qkmla_prefill_args* a, bool sizes_only, pf::Params* p, siz
     p->ctas = device_sm_count();
     if (p->ctas <= 0) return QKMLA_ERR_CUDA;
     if (p->ctas > pf::kMaxCtas) p->ctas = pf::kMaxCtas;
+    p->deep = (int)(((int64_t)units * p->nq + p->ctas - 1) / p->ctas);
     uintptr_t at = (uintptr_t)a->workspace;
     auto take = [&](size_t n) {
         const uintptr_t r = at;
@@ -937,7 +933,7 @@ int make_params(const qkmla_prefill_args* a, bool sizes_only, pf::Params* p, siz
     const size_t tiles = p->max_tiles, nq = p->nq;
     p->seq = (int4*)take(sizeof(int4) * a->B);
     p->qinfo = (int4*)take(sizeof(int4) * 2 * nq);
-    p->pre = (int64_t*)take(8 * (nq + 1));
+    p->pre = (int64_t*)take(8 * ((size_t)p->ctas * p->deep + 1));
     p->tinfo = (int*)take(4 * tiles);
     p->part_ml = (float2*)take(sizeof(float2) * 2 * p->ctas * pf::kRowsQ);
     p->part_o = (float*)take(4 * (size_t)2 * p->ctas * pf::kRowsQ * a->d_v);

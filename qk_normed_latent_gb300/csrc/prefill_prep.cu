@@ -133,23 +133,28 @@ __device__ void make_plan(const Params& p, int64_t* warps) {
         }
     }
     __syncthreads();
-    const int pq = (p.nq + kThreadsE - 1) / kThreadsE;
-    int64_t mine = 0;
-    for (int k = 0; k < pq; ++k) {
-        const int j = tid * pq + k;
-        if (j >= p.nq) break;
+    // the costs ahead of each place of the list
+    const int places = p.ctas * p.deep, pq = (places + kThreadsE - 1) / kThreadsE;
+    auto cost = [&](int m) {
+        int u, j;
+        if (!tile_of_place(p, m, u, j)) return 0;
         const int4 q = p.qinfo[2 * j];
-        if (q.x >= 0) mine += q.z + kCostStart;
-    }
-    int64_t ahead = block_scan(mine, warps, &all);
+        return q.x >= 0 ? q.z + kCostStart : 0;
+    };
+    int64_t mine_sum = 0;
     for (int k = 0; k < pq; ++k) {
-        const int j = tid * pq + k;
-        if (j >= p.nq) break;
-        p.pre[j] = ahead;
-        const int4 q = p.qinfo[2 * j];
-        if (q.x >= 0) ahead += q.z + kCostStart;
+        const int m = tid * pq + k;
+        if (m >= places) break;
+        mine_sum += cost(m);
     }
-    if (tid == 0) p.pre[p.nq] = all;
+    int64_t ahead = block_scan(mine_sum, warps, &all);
+    for (int k = 0; k < pq; ++k) {
+        const int m = tid * pq + k;
+        if (m >= places) break;
+        p.pre[m] = ahead;
+        ahead += cost(m);
+    }
+    if (tid == 0) p.pre[places] = all;
 }
 
 // ---------------------------------------------------------------------------
