@@ -56,6 +56,7 @@ struct Params {
     int4* seq;                             // [B]: length, first tile, first row, rows
     int4* qinfo;                           // [nq][2]: {b, first query, tiles, head tiles}, {gap, length of the first query, queries, -}
     int64_t* pre;                          // [ctas deep + 1]: cost of the places ahead
+    int4* cuts;                            // [ctas + 1]: where each CTA's share starts
     int* tinfo;                            // [max_tiles]: exponent + 64, | 256 where the values are bf16
     uint8_t *krope, *kc, *v;               // blocks: [tile], [tile][G][d_h / 64], [tile][G_v][d_v / 64]
     uint8_t* qs;                           // [cta][2][half][d_h / 64 + 1]: the normalised queries of a CTA's next two pieces
@@ -119,22 +120,6 @@ __device__ __forceinline__ Place place_of(const Params& p, int64_t x, int64_t al
         const int k = 31 - __clz(m | 1u);
         n = min(step, n - k * step);
         lo += k * step;
-    }
-    Place r = place_at(p, lo, x);
-    if (end) r.t = r.nt;
-    return r;
-}
-
-// The same by one thread.
-__device__ __forceinline__ Place place_of_one(const Params& p, int64_t x, int64_t all) {
-    const bool end = x == all;
-    if (end) --x;
-    int lo = 0, hi = p.ctas * p.deep - 1;
-#pragma unroll 1
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (p.pre[mid] <= x) lo = mid;
-        else hi = mid - 1;
     }
     Place r = place_at(p, lo, x);
     if (end) r.t = r.nt;

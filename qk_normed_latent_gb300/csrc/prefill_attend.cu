@@ -550,6 +550,10 @@ give_up:
             walk.end = place_of(p, share_start(all, n_cta, cta + i), all);
         }
         walk.first = true;
+        if (warp == 10 && lane == 0) {                     // for the join
+            p.cuts[cta] = make_int4(walk.at.m, walk.at.t, walk.at.nt, 0);
+            if (cta == n_cta - 1) p.cuts[n_cta] = make_int4(walk.end.m, walk.end.t, walk.end.nt, 0);
+        }
         bool ok = true;
 #pragma unroll 1
         for (int k = 0;; ++k) {
@@ -782,11 +786,13 @@ __global__ void __launch_bounds__(kThreadsJ) prefill_join_kernel(const __grid_co
     const int n_cta = sharing(p, all);
     const int k = blockIdx.x + 1;
     if (all == 0 || k >= n_cta) return;
-    // the boundaries from k - 1 on, a thread each
     __shared__ Place places[kMaxCtas + 1];
     __shared__ int parts[kMaxCtas];
     __shared__ int count;
-    for (int q = k - 1 + threadIdx.x; q <= n_cta; q += kThreadsJ) places[q] = place_of_one(p, share_start(all, n_cta, q), all);
+    for (int q = k - 1 + threadIdx.x; q <= n_cta; q += kThreadsJ) {
+        const int4 c = p.cuts[q];
+        places[q] = Place{c.x, c.y, c.z};
+    }
     __syncthreads();
     const Place at = places[k];
     if (!at.inside()) return;
@@ -816,19 +822,21 @@ __global__ void __launch_bounds__(kThreadsJ) prefill_join_kernel(const __grid_co
     const int e = reinterpret_cast<const int*>(p.weights)[p.G + gv];
     constexpr int kLanes = DV / 4;                          // lanes a row, 4 values each
     constexpr int kPerPass = kThreadsJ / kLanes;
+#pragma unroll 1
     for (int q = threadIdx.x / kLanes; q < kRowsJ; q += kPerPass) {
         const int rt = blockIdx.y * kRowsJ + q, i = rt / p.hp;
         if (i >= b.z) continue;
         float top = -INFINITY;
+#pragma unroll 4
         for (int s = 0; s < n; ++s) top = fmaxf(top, p.part_ml[(size_t)parts[s] * kRowsQ + rt].x);
         float sum = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
         const int col = threadIdx.x % kLanes * 4;
+#pragma unroll 4
         for (int s = 0; s < n; ++s) {
             const size_t row = (size_t)parts[s] * kRowsQ + rt;
             const float2 ml = p.part_ml[row];
             // a part that saw nothing has m = -inf and weight 0, unless its sum is NaN (a key that is not finite)
             const float w = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : exp2f(ml.x - top);
-            if (w == 0.f && ml.y == ml.y) continue;
             const float4 v = *reinterpret_cast<const float4*>(p.part_o + row * DV + col);
             sum = fmaf(w, ml.y, sum);
             o[0] = fmaf(w, v.x, o[0]); o[1] = fmaf(w, v.y, o[1]); o[2] = fmaf(w, v.z, o[2]); o[3] = fmaf(w, v.w, o[3]);
@@ -934,6 +942,7 @@ int make_params(const qkmla_prefill_args* a, bool sizes_only, pf::Params* p, siz
     p->seq = (int4*)take(sizeof(int4) * a->B);
     p->qinfo = (int4*)take(sizeof(int4) * 2 * nq);
     p->pre = (int64_t*)take(8 * ((size_t)p->ctas * p->deep + 1));
+    p->cuts = (int4*)take(sizeof(int4) * (p->ctas + 1));
     p->tinfo = (int*)take(4 * tiles);
     p->part_ml = (float2*)take(sizeof(float2) * 2 * p->ctas * pf::kRowsQ);
     p->part_o = (float*)take(4 * (size_t)2 * p->ctas * pf::kRowsQ * a->d_v);
