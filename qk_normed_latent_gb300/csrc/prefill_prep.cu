@@ -241,53 +241,45 @@ __device__ __forceinline__ int convert_token(const uint4 (&raw)[NV], float scale
     int e;
     bool bad;
     if constexpr (Q8) {
-        // codes are fp16 values: two at a time throughout
-        __half2 x[NV][4], top = __float2half2_rn(0.f);
+        // codes are fp16 values: two at a time throughout, the largest magnitude by their patterns (NaN above all numbers)
+        __half2 x[NV][4];
+        uint32_t top = 0;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             const uint32_t w[2] = {raw[v].x, raw[v].y};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const __half2_raw q = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[i >> 1] >> (16 * (i & 1))), __NV_E4M3);
-                x[v][i] = __half2(q);
-                top = __hmax2_nan(top, __habs2(x[v][i]));
+                x[v][i] = __half2(__half2_raw(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[i >> 1] >> (16 * (i & 1))), __NV_E4M3)));
+                top = __vmaxu2(top, *reinterpret_cast<const uint32_t*>(&x[v][i]) & 0x7fff7fffu);
             }
         }
-        const __half m = __hmax_nan(__low2half(top), __high2half(top));
-        // NaN is above every number as a pattern
-        const uint32_t most = __reduce_max_sync(0xffffffffu, (uint32_t)__half_as_ushort(m) & 0x7fffu);
-        bad = most > 0x7c00u || !(fabsf(scale) <= 3.402823466e38f);
-        const float t = __half2float(__ushort_as_half((unsigned short)most));
-        e = most == 0 ? kNone : ilogbf(t);
-        int se = 0;
-        float f = 1.f;
-        if (scale == 0.f) {
-            e = kNone;
-        } else if (!bad && e != kNone) {
-            // (a scale that is no power of two -- none that this library writes -- leaves its mantissa in the codes)
-            se = ilogbf(scale);
-            f = ldexpf(scale, -se);
-            e = ilogbf(t * fabsf(f));
-            f *= pow2i(-e);
-            const bool exact = (__float_as_int(f) & 0x7fffff) == 0;
-            if (exact) {
-                const __half2 f2 = __float2half2_rn(f);
+        const uint32_t most = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
+        const uint32_t sb = __float_as_uint(scale);
+        bad = most > 0x7c00u || (sb & 0x7f800000u) == 0x7f800000u;
+        e = most == 0 || scale == 0.f ? kNone : (int)(most >> 10) - 15;      // (the least code, 2^-9, is a normal fp16 number)
+        __half f = __ushort_as_half((unsigned short)((15 - (e == kNone ? 0 : e)) << 10));
+        if ((sb & 0x807fffffu) == 0 || bad || e == kNone) {                  // a power of two, as this library writes them
+            e = e == kNone ? kNone : e + (int)(sb >> 23) - 127;
+            const __half2 f2 = __half2half2(f);
 #pragma unroll
-                for (int v = 0; v < NV; ++v)
+            for (int v = 0; v < NV; ++v)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) x[v][i] = __hmul2(x[v][i], f2);
-            } else {
+                for (int i = 0; i < 4; ++i) x[v][i] = __hmul2(x[v][i], f2);
+        } else {                                                             // any other scale leaves its mantissa in the codes
+            const int se = ilogbf(scale);
+            const float m = ldexpf(scale, -se), t = __half2float(__ushort_as_half((unsigned short)most)) * fabsf(m);
+            e = ilogbf(t);
+            const float g = m * pow2i(-e);
+            e += se;
 #pragma unroll
-                for (int v = 0; v < NV; ++v)
+            for (int v = 0; v < NV; ++v)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) x[v][i] = __floats2half2_rn(__low2float(x[v][i]) * f, __high2float(x[v][i]) * f);
-            }
+                for (int i = 0; i < 4; ++i) x[v][i] = __floats2half2_rn(__low2float(x[v][i]) * g, __high2float(x[v][i]) * g);
         }
 #pragma unroll
         for (int v = 0; v < NV; ++v)
 #pragma unroll
             for (int i = 0; i < 4; ++i) h[v][i] = *reinterpret_cast<const uint32_t*>(&x[v][i]);
-        if (e != kNone) e += se;
     } else {
         // the largest magnitude by the bf16 patterns, two at a time
         uint32_t top = 0;
@@ -458,7 +450,7 @@ __global__ void __launch_bounds__(kThreadsE, NV == 1 ? 2 : 1) prefill_expand_ker
             float scale = 0.f;                               // of lane's token, 8-bit cache
             if (Q8 && lane < 16 && slot >= 0) scale = p.kv_scale[slot];
             int hi = kNone, lo = kBad;                       // largest and least exponent of the warp's tokens
-            constexpr int kAhead = 8 / NV;                   // tokens in flight
+            constexpr int kAhead = 8;                        // tokens in flight
 #pragma unroll 1
             for (int k0 = 0; k0 < 16; k0 += kAhead) {
                 uint4 raw[kAhead][NV];
