@@ -20,10 +20,10 @@ constexpr int kTile = 128;                 // tokens of a tile
 constexpr int kRowsQ = 256;                // query rows (tokens x heads of a unit) of a tile: two halves of 128
 constexpr int kBlock = 16384;              // bytes of a block of 128 x 64 values
 constexpr int kMaxE = 40;                  // largest exponent of a tile's values
-constexpr int kCostStart = 2;              // cost of starting on a query tile, in tiles of tokens
+constexpr int kCostStart = 4;              // cost of starting on a query tile, in tiles of tokens
 constexpr int kMinPiece = 2;               // no piece of a cut query tile has fewer tiles of tokens
 constexpr int kMaxCtas = 256;
-constexpr int kMinShare = 5;               // nor a CTA fewer units of cost
+constexpr int kMinShare = 6;               // nor a CTA fewer units of cost
 
 struct Params {
     // the caller's
@@ -53,7 +53,7 @@ struct Params {
     int ctas;                              // of the attention kernel
     int deep;                              // places a CTA: units nq / ctas, rounded up
     // the workspace
-    int4* seq;                             // [B]: length, first tile, first row, rows
+    int4* seq;                             // [B][2]: {length, first tile, first row, rows}, {tiles left out behind its head, -}
     int4* qinfo;                           // [nq][2]: {b, first query, tiles, head tiles}, {gap, length of the first query, queries, -}
     int64_t* pre;                          // [ctas deep + 1]: cost of the places ahead
     int4* cuts;                            // [ctas + 1]: where each CTA's share starts
@@ -73,6 +73,21 @@ __host__ __device__ inline int n_tiles(int G, int Gv, int d_h, int d_v, int d_c)
     return (column_blocks(G, Gv, d_h, d_v) + blocks_per_tile(d_c) - 1) / blocks_per_tile(d_c);
 }
 constexpr size_t kWeightTable = 4096;      // int32 exponents of up to 1024 matrices
+
+// Token tiles of a sequence that its rows see: those below `head` and those from head + gap on (all of them without a
+// window, none for a sequence without rows or with a bad length).  The workspace holds these alone, one sequence's
+// behind the other's.
+struct Needed { int tiles, head, gap; };
+__device__ __forceinline__ Needed needed(const Params& p, int len, int rows) {
+    if (len < 0 || len > (int64_t)p.max_pages * p.page_size || rows <= 0) return Needed{0, 0, 0};
+    const int total = (len + kTile - 1) / kTile;
+    const int lo = len - rows + 1 - p.window;              // the first row's window starts here
+    if (p.window > 0 && lo > 0) {
+        const int from = lo / kTile, head = (min(p.sinks, lo) + kTile - 1) / kTile;
+        if (from > head) return Needed{total - (from - head), head, from - head};
+    }
+    return Needed{total, total, 0};
+}
 
 // First slot of a sequence's query tiles: its rows start at chunk_start[b], and rounding up for each of the
 // b sequences ahead takes at most b slots, so ranges never meet and need no sum over the sequences.

@@ -48,7 +48,7 @@ struct Piece {
     int unit;                              // -1: the end
     int t0, t1, nt;                        // nt: tiles of the whole query tile
     int head, gap;                         // tile t is token tile t below head, t + gap from there
-    int tile0;                             // first token tile of the sequence in the workspace
+    int tile0, skip;                       // and tile0 + t of the workspace, tile0 + t + skip from there
     int n_lo;                              // causal length of the first query
     int queries;
     int row0;                              // first row in q and o
@@ -99,7 +99,8 @@ struct Walk {
             s.gap = b.x;
             s.n_lo = b.y;
             s.queries = b.z;
-            const int4 seq = p.seq[a.x];
+            const int4 seq = p.seq[2 * a.x];
+            s.skip = s.gap - p.seq[2 * a.x + 1].x;
             s.tile0 = seq.y;
             s.row0 = seq.z + a.y;
             return true;
@@ -306,7 +307,7 @@ __global__ void __launch_bounds__(kThreadsA, 1) prefill_attend_kernel(const __gr
                 const int n = s.t1 - s.t0, halves = n == 0 ? 0 : s.queries * p.hp > 128 ? 2 : 1;
                 const size_t g = (size_t)((int64_t)s.unit * p.G / p.units), gv = (size_t)((int64_t)s.unit * p.Gv / p.units);
                 size_t tile = 0;
-                int info_next = n > 0 ? p.tinfo[s.tile0 + (s.t0 < s.head ? s.t0 : s.t0 + s.gap)] : 0;
+                int info_next = n > 0 ? p.tinfo[s.tile0 + (s.t0 < s.head ? s.t0 : s.t0 + s.skip)] : 0;
                 // keys and values of a tile in turn, the piece's queries behind the first keys
 #pragma unroll 1
                 for (int q = 0; q < max(2 * n, 1) && ok; ++q) {
@@ -315,10 +316,10 @@ __global__ void __launch_bounds__(kThreadsA, 1) prefill_attend_kernel(const __gr
                         const int blocks = value ? VU : KU;
                         if (!value) {
                             const int t = s.t0 + (q >> 1);
-                            tile = (size_t)s.tile0 + (t < s.head ? t : t + s.gap);
+                            tile = (size_t)s.tile0 + (t < s.head ? t : t + s.skip);
                             // (through shared memory: a load from L2 in the other warps' loops would be waited for there)
                             sh->info[(group >> 1) & 3] = info_next;
-                            if (t + 1 < s.t1) info_next = p.tinfo[s.tile0 + (t + 1 < s.head ? t + 1 : t + 1 + s.gap)];
+                            if (t + 1 < s.t1) info_next = p.tinfo[s.tile0 + (t + 1 < s.head ? t + 1 : t + 1 + s.skip)];
                         }
                         const uint8_t* src = value ? p.v + (tile * p.Gv + gv) * (size_t)(VU * kBlock) : p.kc + (tile * p.G + g) * (size_t)((KU - 1) * kBlock);
 #pragma unroll 1
@@ -817,7 +818,7 @@ __global__ void __launch_bounds__(kThreadsJ) prefill_join_kernel(const __grid_co
     int unit, j;
     tile_of_place(p, at.m, unit, j);
     const int4 a = p.qinfo[2 * j], b = p.qinfo[2 * j + 1];
-    const int4 seq = p.seq[a.x];
+    const int4 seq = p.seq[2 * a.x];
     const int gv = (int)((int64_t)unit * p.Gv / p.units);
     const int e = reinterpret_cast<const int*>(p.weights)[p.G + gv];
     constexpr int kLanes = DV / 4;                          // lanes a row, 4 values each
@@ -939,7 +940,7 @@ int make_params(const qkmla_prefill_args* a, bool sizes_only, pf::Params* p, siz
         return r;
     };
     const size_t tiles = p->max_tiles, nq = p->nq;
-    p->seq = (int4*)take(sizeof(int4) * a->B);
+    p->seq = (int4*)take(sizeof(int4) * 2 * a->B);
     p->qinfo = (int4*)take(sizeof(int4) * 2 * nq);
     p->pre = (int64_t*)take(8 * ((size_t)p->ctas * p->deep + 1));
     p->cuts = (int4*)take(sizeof(int4) * (p->ctas + 1));

@@ -91,9 +91,8 @@ __device__ void make_plan(const Params& p, int64_t* warps) {
         const int b = tid * per + k;
         if (b >= p.B) break;
         const int len = p.seq_lens[b];
-        if (len < 0 || len > (int64_t)p.max_pages * p.page_size) continue;
-        tiles += (len + kTile - 1) / kTile;
-        tokens += len;
+        tiles += needed(p, len, p.chunk_start[b + 1] - p.chunk_start[b]).tiles;
+        tokens += max(len, 0);
     }
     int64_t at = block_scan(tiles, warps, &all);
     int64_t sum;
@@ -104,19 +103,20 @@ __device__ void make_plan(const Params& p, int64_t* warps) {
         if (b >= p.B) break;
         int len = p.seq_lens[b];
         const int r0 = p.chunk_start[b], r1 = p.chunk_start[b + 1];
-        bool ok = len >= 0 && len <= (int64_t)p.max_pages * p.page_size;
-        const int64_t n = ok ? (len + kTile - 1) / kTile : 0;
-        bool rows_ok = r0 >= 0 && r0 <= r1 && r1 <= p.rows && (b > 0 || r0 == 0);
+        const bool ok = len >= 0 && len <= (int64_t)p.max_pages * p.page_size;
+        const Needed n = needed(p, len, r1 - r0);
+        const bool rows_ok = r0 >= 0 && r0 <= r1 && r1 <= p.rows && (b > 0 || r0 == 0);
         if (!ok || !rows_ok) report(p.status, QKMLA_ERR_DEVICE_BOUNDS);
-        const bool fits = at + n <= p.max_tiles;           // no tile is written beyond the workspace
-        p.seq[b] = make_int4(ok && fits ? len : 0, (int)min(at, (int64_t)p.max_tiles), rows_ok ? r0 : 0, rows_ok ? r1 - r0 : 0);
-        at += n;
+        const bool fits = at + n.tiles <= p.max_tiles;     // no tile is read or written beyond the workspace
+        p.seq[2 * b] = make_int4(ok && fits ? len : 0, (int)min(at, (int64_t)p.max_tiles), rows_ok ? r0 : 0, rows_ok ? r1 - r0 : 0);
+        p.seq[2 * b + 1] = make_int4(n.gap, 0, 0, 0);
+        at += n.tiles;
     }
     for (int j = tid; j < p.nq; j += kThreadsE) p.qinfo[2 * j] = make_int4(-1, 0, 0, 0);
     __syncthreads();
     // query tiles: the tiles of tokens that any of their queries sees
     for (int b = tid >> 5; b < p.B; b += kThreadsE / 32) {
-        const int4 s = p.seq[b];
+        const int4 s = p.seq[2 * b];
         const int n = s.w, j0 = first_slot(s.z, b, p.tq);
         for (int k = tid & 31; k * (int64_t)p.tq < n; k += 32) {
             const int i0 = k * p.tq, i1 = min(n, i0 + p.tq);
@@ -188,21 +188,20 @@ struct __align__(16) ExpandShared {
 };
 static_assert(sizeof(ExpandShared) <= 2048, "beside the blocks");
 
-// The sequence of a tile of the workspace, by the lengths ahead of it; tiles are asked for in rising order, so the next
-// tile's is mostly the same one.  Whole warp.
+// The sequence of a tile of the workspace, by the tiles of those ahead of it; tiles are asked for in rising order, so the
+// next tile's is mostly the same one.  Whole warp.
 struct Sequence {
-    int b = 0, first = 0, last = 0, len = 0, rows = 0;     // its tiles: [first, last)
+    int b = 0, first = 0, last = 0, len = 0, head = 0, gap = 0;         // its tiles: [first, last)
     int b0 = 0, ahead = 0;                                 // where the next search starts: sequences, and tiles ahead of them
     __device__ __forceinline__ bool find(const Params& p, int tile) {
-        if (tile < last) return wanted(p, tile);
+        if (tile < last) return tile >= first;
         const int lane = threadIdx.x & 31;
 #pragma unroll 1
         for (; b0 < p.B; b0 += 32) {
             const int at = b0 + lane;
-            int n = at < p.B ? p.seq_lens[at] : 0;
-            if (n < 0 || n > (int64_t)p.max_pages * p.page_size) n = 0;
-            const int t = (n + kTile - 1) / kTile;
-            int s = t;
+            const int n = at < p.B ? p.seq_lens[at] : 0;
+            const Needed d = at < p.B ? needed(p, n, p.chunk_start[at + 1] - p.chunk_start[at]) : Needed{0, 0, 0};
+            int s = d.tiles;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int u = __shfl_up_sync(0xffffffffu, s, o);
@@ -213,23 +212,54 @@ struct Sequence {
                 const int l = __ffs(__ballot_sync(0xffffffffu, ahead + s > tile)) - 1;
                 b = b0 + l;
                 len = __shfl_sync(0xffffffffu, n, l);
+                head = __shfl_sync(0xffffffffu, d.head, l);
+                gap = __shfl_sync(0xffffffffu, d.gap, l);
                 last = ahead + __shfl_sync(0xffffffffu, s, l);
-                first = last - __shfl_sync(0xffffffffu, t, l);
-                rows = p.chunk_start[b + 1] - p.chunk_start[b];
-                return wanted(p, tile);
+                first = last - __shfl_sync(0xffffffffu, d.tiles, l);
+                return true;
             }
             ahead += all;
         }
         last = first = 1 << 30;                            // behind the last sequence
-        rows = 0;
         return false;
     }
-    __device__ __forceinline__ int token(int tile) const { return (tile - first) * kTile; }
-    // Tiles that no query of the step sees are left out.
-    __device__ __forceinline__ bool wanted(const Params& p, int tile) const {
-        if (rows <= 0 || tile < first) return false;
-        const int t0 = token(tile);
-        return p.window == 0 || t0 < p.sinks || t0 + kTile > (int64_t)len - rows + 1 - p.window;
+    // The first token of a tile.
+    __device__ __forceinline__ int token(int tile) const { return (tile - first < head ? tile - first : tile - first + gap) * kTile; }
+};
+
+// A CTA's share of the work, in N-tiles of all tiles: where the tiles are fewer than CTAs, each CTA a part of one tile;
+// else equal shares, whose ends may cut a tile (its latents are then gathered twice).  Whole warp.
+struct Share {
+    int64_t at, end;
+    __device__ __forceinline__ Share(const Params& p, int nt, int cta, int ctas) {
+        const int lane = threadIdx.x & 31;
+        int64_t tiles = 0;
+        for (int b = lane; b < p.B; b += 32) tiles += needed(p, p.seq_lens[b], p.chunk_start[b + 1] - p.chunk_start[b]).tiles;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
+        tiles = min(tiles, (int64_t)p.max_tiles);
+        at = end = 0;
+        if (tiles == 0) return;
+        if (tiles <= ctas) {
+            const int parts = min(nt, (int)(ctas / tiles)), tile = cta / parts, part = cta - tile * parts;
+            if (tile >= tiles) return;
+            at = (int64_t)tile * nt + nt * part / parts;
+            end = (int64_t)tile * nt + nt * (part + 1) / parts;
+        } else {
+            // (with few N-tiles a tile is cheaper done whole than gathered twice: 36 against 44 us for 480 tiles of four)
+            const int cut = nt >= 8 ? 1 : nt;
+            at = tiles * nt / cut * cta / ctas * cut;
+            end = tiles * nt / cut * (cta + 1) / ctas * cut;
+        }
+    }
+    // The next tile and its N-tiles [n0, n1).
+    __device__ __forceinline__ bool next(int nt, int& tile, int& n0, int& n1) {
+        if (at >= end) return false;
+        tile = (int)(at / nt);
+        n0 = (int)(at - (int64_t)tile * nt);
+        n1 = (int)min((int64_t)nt, n0 + (end - at));
+        at += n1 - n0;
+        return true;
     }
 };
 
@@ -317,7 +347,7 @@ __device__ __forceinline__ int convert_token(const uint4 (&raw)[NV], float scale
 
 // NV: vectors of 8 latents a lane, d_c up to 256 NV; at 1 two CTAs fit on an SM, one gathering while the other multiplies.
 template <bool Q8, int NV>
-__global__ void __launch_bounds__(kThreadsE, NV == 1 ? 2 : 1) prefill_expand_kernel(const __grid_constant__ Params p, int splits) {
+__global__ void __launch_bounds__(kThreadsE, NV == 1 ? 2 : 1) prefill_expand_kernel(const __grid_constant__ Params p) {
     extern __shared__ __align__(1024) uint8_t smraw[];
     uint8_t* sm = smraw + ((1024u - (smem_u32(smraw) & 1023u)) & 1023u);
     constexpr int kRing = NV == 1 ? 2 : kRingMax;
@@ -330,7 +360,7 @@ __global__ void __launch_bounds__(kThreadsE, NV == 1 ? 2 : 1) prefill_expand_ker
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int nkb = p.d_h / 64, nvb = p.d_v / 64;
     const int blocks = column_blocks(p.G, p.Gv, p.d_h, p.d_v), nt = (blocks + NB - 1) / NB;
-    const int items = p.max_tiles * splits, ctas = gridDim.x - 1;
+    const int ctas = gridDim.x - 1;
 
     if (blockIdx.x == ctas) {
         pdl_wait();                                        // the workspace may still be in use
@@ -361,13 +391,11 @@ __global__ void __launch_bounds__(kThreadsE, NV == 1 ? 2 : 1) prefill_expand_ker
 
     if (warp == 8) {
         // ---- weights ----
-        Sequence seq;
-        int i = 0;
+        Share share(p, nt, blockIdx.x, ctas);
+        int i = 0, tile, n0, n1;
         bool ok = true;
 #pragma unroll 1
-        for (int item = blockIdx.x; item < items && ok; item += ctas) {
-            if (!seq.find(p, item / splits)) continue;
-            const int part = item % splits, n0 = nt * part / splits, n1 = nt * (part + 1) / splits;
+        while (ok && share.next(nt, tile, n0, n1)) {
             const uint8_t* w = p.weights + kWeightTable + (size_t)n0 * kb * kStage;
             if (lane == 0) {
 #pragma unroll 1
@@ -385,13 +413,11 @@ __global__ void __launch_bounds__(kThreadsE, NV == 1 ? 2 : 1) prefill_expand_ker
         // ---- products: each barrier is looked at while the ones ahead of its use are being taken ----
         constexpr uint32_t idesc = idesc_bf16(128, kCols, 0, 0) & ~((1u << 7) | (1u << 10));      // fp16 operands
         const uint32_t a_desc = desc_low(sm, 16), w_desc = desc_low(ring, 16);
-        Sequence seq;
-        int i = 0, n = 0, it = 0;                          // blocks, N-tiles and tiles so far
+        Share share(p, nt, blockIdx.x, ctas);
+        int i = 0, n = 0, it = 0, tile, n0, n1;            // blocks, N-tiles and tiles so far
         bool ok = true;
 #pragma unroll 1
-        for (int item = blockIdx.x; item < items && ok; item += ctas) {
-            if (!seq.find(p, item / splits)) continue;
-            const int part = item % splits, n0 = nt * part / splits, n1 = nt * (part + 1) / splits;
+        while (ok && share.next(nt, tile, n0, n1)) {
             if (elect_one()) {
                 ok = wait_or_fail(&sh->a_full, it & 1, fail);
                 bool seen = false;
@@ -431,14 +457,14 @@ __global__ void __launch_bounds__(kThreadsE, NV == 1 ? 2 : 1) prefill_expand_ker
         const int row_bytes = Q8 ? p.d_c + 2 * p.d_r : 2 * (p.d_c + p.d_r);
         const int per = p.d_c / 8;                          // vectors of 8 latents a token
         const int* we = reinterpret_cast<const int*>(p.weights);
+        Share share(p, nt, blockIdx.x, ctas);
         Sequence seq;
-        int n = 0, it = 0;
+        int n = 0, it = 0, tile, n0, n1;
         bool ok = true;
 #pragma unroll 1
-        for (int item = blockIdx.x; item < items && ok; item += ctas) {
-            const int tile = item / splits, part = item % splits;
-            if (!seq.find(p, tile)) continue;
-            const int t0 = seq.token(tile), len = seq.len, n0 = nt * part / splits, n1 = nt * (part + 1) / splits, buf = it & 1;
+        while (ok && share.next(nt, tile, n0, n1)) {
+            seq.find(p, tile);
+            const int t0 = seq.token(tile), len = seq.len, buf = it & 1;
             // ---- gather: a warp's 16 tokens, their slots by its first 16 lanes ----
             const int row = 32 * (warp & 3) + lane;          // this thread's token in the results
             const int mine = t0 + (lane < 16 ? warp * 16 + lane : row);
@@ -482,7 +508,7 @@ __global__ void __launch_bounds__(kThreadsE, NV == 1 ? 2 : 1) prefill_expand_ker
                     if (e != kBad && e != kNone) { hi = max(hi, e); lo = min(lo, e); }
                 }
             }
-            if (part == 0) {
+            if (n0 == 0) {
                 // RoPE keys of the warp's tokens: 16-byte pieces of 8 values, a row by 8 (or 4) lanes, all in flight at once
                 const int pieces = p.d_r / 8;
                 uint4 u[4];
@@ -509,8 +535,8 @@ __global__ void __launch_bounds__(kThreadsE, NV == 1 ? 2 : 1) prefill_expand_ker
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh->a_full);
             // the next tile's rows into L2, where it is of the same sequence
-            if (const int next = (item + ctas) / splits; next > tile && next < seq.last && lane < 16) {
-                const int64_t sl = slot_at(seq.token(next) + warp * 16 + lane);
+            if (share.at < share.end && tile + 1 < seq.last && lane < 16) {
+                const int64_t sl = slot_at(seq.token(tile + 1) + warp * 16 + lane);
                 if (sl >= 0)
                     for (int i = 0; i < row_bytes; i += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(p.kv + sl * (int64_t)row_bytes + i));
             }
@@ -531,7 +557,7 @@ __global__ void __launch_bounds__(kThreadsE, NV == 1 ? 2 : 1) prefill_expand_ker
             // one exponent for the tile's values; bf16 where fp16 would not hold them beside one another
             const bool bf = e_hi != kNone && (e_hi - e_lo > 12 || e_hi > kMaxE || e_hi < -kMaxE);
             const int e_tile = e_hi == kNone ? 0 : min(max(e_hi, -kMaxE), kMaxE);
-            if (part == 0 && tid == 0) p.tinfo[tile] = (e_tile + 64) | (bf ? 256 : 0);
+            if (n0 == 0 && tid == 0) p.tinfo[tile] = (e_tile + 64) | (bf ? 256 : 0);
             // ---- results: thread = token, its warp's half of the 128 columns (one 64-column block) ----
             const int et = sh->exps[buf][row];
             const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
@@ -615,12 +641,9 @@ int launch_expand_as(const Params& p, cudaStream_t s) {
     auto k = prefill_expand_kernel<Q8, NV>;
     const int bytes = expand_bytes(p.d_c), sms = device_sm_count() * (NV == 1 ? 2 : 1);
     if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return QKMLA_ERR_CUDA;
-    // few tiles: their columns are cut over several CTAs
-    const int nt = n_tiles(p.G, p.Gv, p.d_h, p.d_v, p.d_c);
-    const int splits = max(1, min(nt, sms / p.max_tiles));
-    if ((int64_t)p.max_tiles * splits > INT32_MAX) return QKMLA_ERR_UNSUPPORTED;
-    const int ctas = min(p.max_tiles * splits, sms);
-    return launch_pdl(k, dim3((unsigned)(ctas + 1)), dim3(kThreadsE), bytes, s, p, splits) == cudaSuccess ? QKMLA_OK : QKMLA_ERR_CUDA;
+    const int64_t most = (int64_t)p.max_tiles * n_tiles(p.G, p.Gv, p.d_h, p.d_v, p.d_c);
+    const int ctas = (int)min((int64_t)sms, most);
+    return launch_pdl(k, dim3((unsigned)(ctas + 1)), dim3(kThreadsE), bytes, s, p) == cudaSuccess ? QKMLA_OK : QKMLA_ERR_CUDA;
 }
 
 }  // namespace
