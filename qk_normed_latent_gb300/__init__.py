@@ -710,6 +710,10 @@ def prepare_rope(x, positions, out, theta: float = 10000.0, layout: str = "inter
         raise ValueError(f"qkmla: layout is interleaved or half, not {layout}")
     rows, d_r = x.shape[0], x.shape[-1]
     _expect("positions", positions, torch.int32, rows)
+    if not float(attention_factor) > 0:
+        raise ValueError("qkmla: attention_factor is positive")
+    if scaling is not None and "frequencies" in scaling.fields and len(scaling.fields["frequencies"]) != d_r // 2:
+        raise ValueError(f"qkmla: {d_r // 2} frequencies for {d_r} elements, not {len(scaling.fields['frequencies'])}")
     a = RopeArgs()
     a.x, a.out, a.positions = _inner("x", x), _inner("out", out), _ptr(positions)
     a.x_row_stride, a.out_row_stride = x.stride(0), out.stride(0)
@@ -720,14 +724,10 @@ def prepare_rope(x, positions, out, theta: float = 10000.0, layout: str = "inter
     a.layout = ROPE_HALVES if layout == "half" else ROPE_INTERLEAVED
     a.inverse = 1 if inverse else 0
     a.theta, a.attention_factor = float(theta), float(attention_factor)
-    if not a.attention_factor > 0:
-        raise ValueError("qkmla: attention_factor is positive")
     if scaling is not None:
         a.scaling = scaling.kind
         for k, v in scaling.fields.items():
             if k == "frequencies":
-                if len(v) != d_r // 2:
-                    raise ValueError(f"qkmla: {d_r // 2} frequencies for {d_r} elements, not {len(v)}")
                 v = ctypes.cast(v, ctypes.POINTER(ctypes.c_double))
             setattr(a, k, v)
     return PreparedStruct("qkmla_rope", a, scaling)
@@ -762,16 +762,17 @@ def prepare_read_cache(kv_cache, ak_cache, out_start, page_table, page_size: int
         _expect("r", r, c.dtype, rows, d_r)
     B = out_start.numel() - 1
     _expect("out_start", out_start, torch.int32, B + 1)
-    a = ReadCacheArgs()
     if ak is not None:
         G = ak.shape[1]
         _expect("ak", ak, f32, rows, G)
         _expect("ak_cache", ak_cache, (f32, torch.float16), kv_cache.shape[0], G)
-        a.ak_cache, a.ak, a.G, a.flags = _ptr(ak_cache), _ptr(ak), G, _alpha_flag(ak_cache)
     if first is not None:
         _expect("first", first, torch.int32, B)
     if page_table is not None:
         _expect("page_table", page_table, torch.int32, B, max_pages)
+    a = ReadCacheArgs()
+    if ak is not None:
+        a.ak_cache, a.ak, a.G, a.flags = _ptr(ak_cache), _ptr(ak), G, _alpha_flag(ak_cache)
     a.kv_cache, a.kv_scale, a.out_start, a.first = _ptr(kv_cache), _ptr(kv_scale), _ptr(out_start), _ptr(first)
     a.page_table, a.num_slots = _ptr(page_table), kv_cache.shape[0]
     a.page_size, a.max_pages, a.B, a.rows, a.d_c, a.d_r = int(page_size), int(max_pages), B, rows, d_c, d_r
@@ -830,7 +831,7 @@ class PreparedPrefill(PreparedDecode):
 
     @property
     def launch_count(self) -> int:
-        return 0 if self.args.rows == 0 else 4
+        return 0 if self.args.rows == 0 else 3
 
 
 def prepare_prefill(q, q_rope, gamma_q, gamma_k, gamma_rope_q, weights: PrefillWeights, kv_cache, ak_cache, chunk_start,

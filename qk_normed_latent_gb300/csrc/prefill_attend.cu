@@ -881,8 +881,7 @@ using namespace qkmla;
 
 namespace {
 
-// Argument checks and everything that follows from the sizes; pointers into the workspace at `base`.
-int make_params(const qkmla_prefill_args* a, bool sizes_only, pf::Params* p, size_t* bytes) {
+int check_sizes(const qkmla_prefill_args* a) {
     if (!a) return QKMLA_ERR_INVALID;
     if (a->B < 1 || a->rows < 0 || a->H < 1 || a->G < 1 || a->G_v < 1 || a->d_c < 1 || a->d_h < 1 || a->d_r < 1 || a->d_v < 1)
         return QKMLA_ERR_INVALID;
@@ -901,6 +900,32 @@ int make_params(const qkmla_prefill_args* a, bool sizes_only, pf::Params* p, siz
     if ((a->d_h != 64 && a->d_h != 128) || (a->d_v != 64 && a->d_v != 128) || (a->d_r != 32 && a->d_r != 64)) return QKMLA_ERR_UNSUPPORTED;
     if (a->d_c % 64 || a->d_c > 512 || a->B > 4096 || units > 512) return QKMLA_ERR_UNSUPPORTED;
     if ((int64_t)a->rows * a->H > INT32_MAX || a->total_tokens / pf::kTile + a->B > (1 << 24)) return QKMLA_ERR_UNSUPPORTED;
+    return QKMLA_OK;
+}
+
+int check_pointers(const qkmla_prefill_args* a) {
+    const bool q8 = a->cache_dtype == QKMLA_E4M3;
+    if (q8 != (a->kv_scale != nullptr)) return QKMLA_ERR_INVALID;
+    for (int64_t st : {a->q_row_stride, a->q_head_stride, a->qr_row_stride, a->qr_head_stride})
+        if (st % 4) return QKMLA_ERR_INVALID;
+    if (!a->q || !a->q_rope || !a->gamma_q || !a->gamma_k || !a->weights || !a->kv_cache || !a->ak_cache || !a->chunk_start ||
+        !a->seq_lens || !a->o)
+        return QKMLA_ERR_INVALID;
+    if ((uintptr_t)a->o % 32) return QKMLA_ERR_INVALID;
+    for (const void* ptr : {a->q, a->q_rope, a->weights, a->kv_cache})
+        if ((uintptr_t)ptr % 16) return QKMLA_ERR_INVALID;
+    for (const void* ptr : {(const void*)a->gamma_q, (const void*)a->gamma_k, (const void*)a->gamma_rope_q, (const void*)a->kv_scale,
+                            (const void*)a->chunk_start, (const void*)a->seq_lens, (const void*)a->page_table, (const void*)a->lse})
+        if ((uintptr_t)ptr % 4) return QKMLA_ERR_INVALID;
+    if ((uintptr_t)a->ak_cache % ((a->flags & QKMLA_FLAG_ALPHA_F16) ? 2 : 4)) return QKMLA_ERR_INVALID;
+    if (!a->workspace) return QKMLA_ERR_WORKSPACE;
+    if ((uintptr_t)a->workspace % 256) return QKMLA_ERR_INVALID;
+    return QKMLA_OK;
+}
+
+// Everything that follows from the (checked) arguments; the workspace's parts from a->workspace on.
+int make_params(const qkmla_prefill_args* a, pf::Params* p, size_t* bytes) {
+    const int units = a->G > a->G_v ? a->G : a->G_v, hp = a->H / units;
     *p = pf::Params{};
     p->page_size = a->page_size;
     p->max_pages = a->max_pages;
@@ -952,23 +977,6 @@ int make_params(const qkmla_prefill_args* a, bool sizes_only, pf::Params* p, siz
     p->v = (uint8_t*)take(tiles * a->G_v * (a->d_v / 64) * pf::kBlock);
     p->qs = (uint8_t*)take((size_t)p->ctas * 4 * (a->d_h / 64 + 1) * pf::kBlock);
     *bytes = at - (uintptr_t)a->workspace;
-    if (sizes_only) return QKMLA_OK;
-    if (q8 != (a->kv_scale != nullptr)) return QKMLA_ERR_INVALID;
-    for (int64_t st : {a->q_row_stride, a->q_head_stride, a->qr_row_stride, a->qr_head_stride})
-        if (st % 4) return QKMLA_ERR_INVALID;
-    if (a->rows == 0) return QKMLA_OK;
-    if (!a->q || !a->q_rope || !a->gamma_q || !a->gamma_k || !a->weights || !a->kv_cache || !a->ak_cache || !a->chunk_start ||
-        !a->seq_lens || !a->o)
-        return QKMLA_ERR_INVALID;
-    if ((uintptr_t)a->o % 32) return QKMLA_ERR_INVALID;
-    for (const void* ptr : {a->q, a->q_rope, a->weights, a->kv_cache})
-        if ((uintptr_t)ptr % 16) return QKMLA_ERR_INVALID;
-    for (const void* ptr : {(const void*)a->gamma_q, (const void*)a->gamma_k, (const void*)a->gamma_rope_q, (const void*)a->kv_scale,
-                            (const void*)a->chunk_start, (const void*)a->seq_lens, (const void*)a->page_table, (const void*)a->lse})
-        if ((uintptr_t)ptr % 4) return QKMLA_ERR_INVALID;
-    if ((uintptr_t)a->ak_cache % (p->ak_f16 ? 2 : 4)) return QKMLA_ERR_INVALID;
-    if (!a->workspace || a->workspace_bytes < *bytes) return QKMLA_ERR_WORKSPACE;
-    if ((uintptr_t)a->workspace % 256) return QKMLA_ERR_INVALID;
     p->q = a->q;
     p->q_rope = a->q_rope;
     p->q_row = a->q_row_stride;
@@ -987,7 +995,6 @@ int make_params(const qkmla_prefill_args* a, bool sizes_only, pf::Params* p, siz
     p->page_table = a->page_table;
     p->o = a->o;
     p->lse = a->lse;
-    p->status = device_status_ptr();
     return QKMLA_OK;
 }
 
@@ -996,14 +1003,18 @@ int make_params(const qkmla_prefill_args* a, bool sizes_only, pf::Params* p, siz
 extern "C" size_t qkmla_prefill_workspace_size(const qkmla_prefill_args* a) {
     pf::Params p;
     size_t bytes = 0;
-    return make_params(a, true, &p, &bytes) == QKMLA_OK ? bytes : 0;
+    return check_sizes(a) == QKMLA_OK && make_params(a, &p, &bytes) == QKMLA_OK ? bytes : 0;
 }
 
 extern "C" int qkmla_prefill(const qkmla_prefill_args* a, void* stream) {
+    int rc = check_sizes(a);
+    if (rc != QKMLA_OK || a->rows == 0) return rc;
+    if ((rc = check_pointers(a)) != QKMLA_OK) return rc;
     pf::Params p;
     size_t bytes = 0;
-    int rc = make_params(a, false, &p, &bytes);
-    if (rc != QKMLA_OK || a->rows == 0) return rc;
+    if ((rc = make_params(a, &p, &bytes)) != QKMLA_OK) return rc;
+    if (a->workspace_bytes < bytes) return QKMLA_ERR_WORKSPACE;
+    p.status = device_status_ptr();
     cudaStream_t s = (cudaStream_t)stream;
     if ((rc = pf::launch_expand(p, a->cache_dtype == QKMLA_E4M3, s)) != QKMLA_OK) return rc;
     return pf::launch_attend(p, s);

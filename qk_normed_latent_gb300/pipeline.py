@@ -1,4 +1,5 @@
-"""Run the decode path (absorb -> append -> decode) on a synthetic workload.
+"""Run the decode path (absorb -> append -> decode) on a synthetic workload, or its step's queries as a
+chunk of a prompt (append -> prefill).
 
 Device-side driver used by the tests, the benchmark and the smoke check.  It
 only moves the seeded inputs of `workloads` to the GPU and calls the library;
@@ -12,7 +13,7 @@ import torch
 import workloads as W
 
 from . import (F32, BF16, append, append_q8, decode_workspace_size, decode_raw, make_decode_args,
-               prepare_absorb_query, prepare_append, prepare_append_q8, prepare_decode)
+               prefill_weights, prepare_absorb_query, prepare_append, prepare_append_q8, prepare_decode, prepare_prefill)
 
 # element types; "e4m3" is the 8-bit latent cache (bytes: codes and the bf16 RoPE key, scales beside them)
 _TORCH_DT = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16, "e4m3": torch.uint8}
@@ -142,6 +143,7 @@ class DeviceState:
         self.args = None
         self._absorb = self._append = None
         self._decode = {}
+        self._prefill = {}
 
     # -- the three calls -------------------------------------------------------
     def absorb(self, stream=None):
@@ -204,3 +206,20 @@ class DeviceState:
         if self.args is None or num_splits != self.args.num_splits:
             self.args = self.decode_args(num_splits, force_simt)
         decode_raw(self.args, stream)
+
+    def prefill(self, w_v, o_dtype=torch.bfloat16, stream=None):
+        """The step's queries as chunks of s_q tokens: per-head values [rows, H, d_v] with W^V [G_v, d_c, d_v] (bf16),
+        as decode and up_project give them.  Append the step's tokens first."""
+        w = self.w
+        key = (w_v.data_ptr(), o_dtype)
+        if self._prefill.get(key) is None:
+            weights = prefill_weights(self.wk, w_v)
+            start = torch.arange(0, w.rows + 1, w.s_q, dtype=torch.int32, device=self.dev)
+            o = torch.empty((w.rows, w.H, weights.d_v), dtype=o_dtype, device=self.dev)
+            self._prefill[key] = (prepare_prefill(
+                self.q, self.q_rope.reshape(w.rows, w.H, w.d_r), self.gq, self.gk, self.grq, weights, self.kv, self.ak, start,
+                self.seq_lens, self.page_table, self.page_size, self.max_pages, int(self.lens.sum()), w.scale, w.eps, o,
+                kv_scale=self.kv_scale, window=self.window, sinks=self.sinks), o, w_v)
+        call, o, _ = self._prefill[key]
+        call(stream)
+        return o
