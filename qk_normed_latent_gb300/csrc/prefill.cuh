@@ -81,9 +81,9 @@ struct Needed { int tiles, head, gap; };
 __device__ __forceinline__ Needed needed(const Params& p, int len, int rows) {
     if (len < 0 || len > (int64_t)p.max_pages * p.page_size || rows <= 0) return Needed{0, 0, 0};
     const int total = (len + kTile - 1) / kTile;
-    const int lo = len - rows + 1 - p.window;              // the first row's window starts here
+    const int64_t lo = (int64_t)len - rows + 1 - p.window;              // the first row's window starts here
     if (p.window > 0 && lo > 0) {
-        const int from = lo / kTile, head = (min(p.sinks, lo) + kTile - 1) / kTile;
+        const int from = (int)(lo / kTile), head = (int)((min((int64_t)p.sinks, lo) + kTile - 1) / kTile);
         if (from > head) return Needed{total - (from - head), head, from - head};
     }
     return Needed{total, total, 0};
@@ -168,6 +168,18 @@ __device__ __forceinline__ bool wait_or_fail(uint64_t* bar, uint32_t parity, int
 #pragma unroll 1
     while (!tc::mbar_try_wait(bar, parity))
         if (++i == kSpins) {
+            *(volatile int*)fail = 1;
+            return false;
+        }
+    return true;
+}
+
+// The same for a wait that may last as long as a whole query tile's work: it ends when another warp gives up, too.
+__device__ __forceinline__ bool wait_long(uint64_t* bar, uint32_t parity, int* fail) {
+    uint32_t i = 0;
+#pragma unroll 1
+    while (!tc::mbar_try_wait(bar, parity))
+        if (++i == 1u << 28 || *(volatile int*)fail) {
             *(volatile int*)fail = 1;
             return false;
         }

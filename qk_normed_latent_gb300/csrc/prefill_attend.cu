@@ -574,7 +574,7 @@ give_up:
                     for (int i = 0; i < rope_bytes; i += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(y + i));
                 }
             }
-            if (k >= 2) ok = wait_or_fail(&sh->piece_empty[k & 1], ((k >> 1) - 1) & 1, &sh->fail);
+            if (k >= 2) ok = wait_long(&sh->piece_empty[k & 1], ((k >> 1) - 1) & 1, &sh->fail);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             if (warp == 10 && lane == 0) {

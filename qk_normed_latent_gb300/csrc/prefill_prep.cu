@@ -94,6 +94,14 @@ __device__ void make_plan(const Params& p, int64_t* warps) {
         tiles += needed(p, len, p.chunk_start[b + 1] - p.chunk_start[b]).tiles;
         tokens += max(len, 0);
     }
+    // chunk starts out of order: nothing is done, since ranges of query tiles could meet
+    bool bad = false;
+    for (int b = tid; b < p.B; b += kThreadsE) {
+        const int r0 = p.chunk_start[b], r1 = p.chunk_start[b + 1];
+        bad |= r0 < 0 || r0 > r1 || r1 > p.rows || (b == 0 && r0 != 0);
+    }
+    const bool ordered = !__syncthreads_or(bad);
+    if (tid == 0 && !ordered) report(p.status, QKMLA_ERR_DEVICE_BOUNDS);
     int64_t at = block_scan(tiles, warps, &all);
     int64_t sum;
     block_scan(tokens, warps, &sum);
@@ -105,10 +113,9 @@ __device__ void make_plan(const Params& p, int64_t* warps) {
         const int r0 = p.chunk_start[b], r1 = p.chunk_start[b + 1];
         const bool ok = len >= 0 && len <= (int64_t)p.max_pages * p.page_size;
         const Needed n = needed(p, len, r1 - r0);
-        const bool rows_ok = r0 >= 0 && r0 <= r1 && r1 <= p.rows && (b > 0 || r0 == 0);
-        if (!ok || !rows_ok) report(p.status, QKMLA_ERR_DEVICE_BOUNDS);
+        if (!ok) report(p.status, QKMLA_ERR_DEVICE_BOUNDS);
         const bool fits = at + n.tiles <= p.max_tiles;     // no tile is read or written beyond the workspace
-        p.seq[2 * b] = make_int4(ok && fits ? len : 0, (int)min(at, (int64_t)p.max_tiles), rows_ok ? r0 : 0, rows_ok ? r1 - r0 : 0);
+        p.seq[2 * b] = make_int4(ok && fits ? len : 0, (int)min(at, (int64_t)p.max_tiles), ordered ? r0 : 0, ordered ? r1 - r0 : 0);
         p.seq[2 * b + 1] = make_int4(n.gap, 0, 0, 0);
         at += n.tiles;
     }
@@ -123,9 +130,9 @@ __device__ void make_plan(const Params& p, int64_t* warps) {
             const int lo = s.x - n + i0 + 1, hi = s.x - n + i1;        // causal lengths of the first and the last query
             const int total = hi > 0 ? (hi + kTile - 1) / kTile : 0;
             int head = total, gap = 0;
-            if (p.window > 0 && lo - p.window > 0) {
-                const int from = min((lo - p.window) / kTile, total);
-                const int h = (min(p.sinks, lo - p.window) + kTile - 1) / kTile;
+            if (const int64_t start = (int64_t)lo - p.window; p.window > 0 && start > 0) {
+                const int from = (int)min(start / kTile, (int64_t)total);
+                const int h = (int)((min((int64_t)p.sinks, start) + kTile - 1) / kTile);
                 if (from > h) { head = h; gap = from - h; }
             }
             p.qinfo[2 * (j0 + k)] = make_int4(b, i0, total - gap, head);

@@ -283,3 +283,88 @@ def test_same_as_the_decode_path(Q):
     a, b = o, out.double().cpu().numpy()
     assert np.linalg.norm(a - b) <= (2.7e-3 + 5e-3) * np.linalg.norm(b)         # plus the bf16 query's rule
     assert np.abs(lse - lse2.view(8, -1).double().cpu().numpy()).max() <= 2e-2 + 7e-3
+
+
+def test_many_sequences(Q):
+    """More sequences than a warp looks at at once, among them idle slots (no rows, no tokens)."""
+    lens = [(37 * i) % 211 for i in range(150)]
+    new = [min(n, (13 * i) % 7) for i, n in enumerate(lens)]
+    check(Q, lens=lens, new=new, H=4, G=2, d_c=64, page=16)
+
+
+@pytest.mark.parametrize("window", [0, 100])
+def test_more_tiles_than_ctas(Q, window):
+    """Shares of the expansion that cut a tile, and long query lists."""
+    check(Q, lens=[30000, 9000], new=[70, 5], H=4, G=4, d_c=512, d_h=128, d_r=64, d_v=128, window=window, sinks=5 if window else 0)
+
+
+def test_no_rows_at_all(Q):
+    """A padded step none of whose slots has a chunk: nothing is written."""
+    c = R.Case(lens=[40, 0, 9], new=[0, 0, 0], spare_rows=6)
+    dev = Device(Q, c)
+    dev.o.fill_(3)
+    dev.lse.fill_(3)
+    o, lse = dev.run(Q)
+    assert (o == 3).all() and (lse == 3).all()
+
+
+def bounds(Q, change, keep=None):
+    """The call reports what is out of range; a sequence of the step that it does not touch is right."""
+    c = R.Case(lens=[200, 150, 90], new=[20, 30, 9])
+    dev = Device(Q, c)
+    change(dev)
+    dev.call()
+    assert Q.get_device_status() == Q.ERR_DEVICE_BOUNDS
+    if keep is not None:
+        rows = slice(int(c.start[keep]), int(c.start[keep + 1]))
+        a, b = dev.o[rows].double().cpu().numpy(), c.o[rows]
+        assert np.linalg.norm(a - b) <= 2.7e-3 * np.linalg.norm(b)
+    # and the device is as before
+    compare(c, *Device(Q, c).run(Q))
+
+
+@pytest.mark.parametrize("page", [-1, 10 ** 6])
+def test_bad_page(Q, page):
+    bounds(Q, lambda d: d.table[1].__setitem__(2, page), keep=0)
+
+
+@pytest.mark.parametrize("length", [-1, 2 ** 31 - 1, 209])
+def test_bad_length(Q, length):
+    bounds(Q, lambda d: d.lens.__setitem__(1, length), keep=0)
+
+
+def test_total_tokens_too_small(Q):
+    c = R.Case(lens=[2000, 150], new=[20, 30])
+    dev = Device(Q, c, total=300)
+    dev.call()
+    assert Q.get_device_status() == Q.ERR_DEVICE_BOUNDS
+
+
+@pytest.mark.parametrize("start", [[0, 30, 20, 59], [0, 20, 50, 60], [3, 20, 50, 59], [0, -5, 50, 59]])
+def test_chunk_starts_out_of_order(Q, start):
+    bounds(Q, lambda d: d.start.copy_(torch.tensor(start, dtype=torch.int32)))
+
+
+def test_workspace(Q):
+    """A caller's workspace is used if it is large enough; too small a one is replaced, and refused by the C call."""
+    import ctypes
+    c = R.Case(lens=[100], new=[10])
+    dev = Device(Q, c)
+    need = Q.lib().qkmla_prefill_workspace_size(ctypes.byref(dev.call.args))
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    call = Q.prepare_prefill(*dev.args, **dev.kw, workspace=ws)
+    assert call.workspace is ws
+    call()
+    assert Q.get_device_status() == 0
+    compare(c, dev.o.double().cpu().numpy(), dev.lse.double().cpu().numpy())
+    call.args.workspace_bytes = need - 1
+    assert Q.lib().qkmla_prefill(ctypes.byref(call.args), None) == Q.ERR_WORKSPACE
+
+
+def test_results_do_not_depend_on_what_the_workspace_held(Q):
+    c = R.Case(lens=[700, 40], new=[60, 3], window=200, sinks=3)
+    dev = Device(Q, c)
+    first = dev.run(Q)[0]
+    dev.call.workspace.fill_(0xFF)
+    again = dev.run(Q)[0]
+    assert (first == again).all()
