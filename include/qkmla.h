@@ -47,11 +47,10 @@
  *    earlier: seq_lens in qkmla_decode and qkmla_decode_ext; W^K, the new tokens,
  *    their slots and positions in qkmla_append, qkmla_append_rope and
  *    qkmla_append_q8; the positions in qkmla_rope; out_start, first and the page table
- *    in qkmla_read_cache; seq_lens, chunk_start, the page table and the gains in
- *    qkmla_prefill.  A previous kernel that
- *    itself signals early dependent launch must therefore not be writing
- *    those inputs (kernels that do not signal it, and copies, are waited for
- *    in full as usual).
+ *    in qkmla_read_cache; W^K and W^V in qkmla_prefill_pack_weights.  A previous
+ *    kernel that itself signals early dependent launch must therefore not be
+ *    writing those inputs (kernels that do not signal it, and copies, are waited
+ *    for in full as usual).
  */
 #ifndef QKMLA_H
 #define QKMLA_H
@@ -557,7 +556,7 @@ typedef struct qkmla_prefill_args {
  * and lse.
  *
  * Accuracy: fp16 operands (11 significant bits) of tensor-core products, fp32 sums:
- * recovered keys and values, normalised queries (scaled by a power of two a row) and
+ * recovered keys and values, normalised queries (the gains times one power of two a call) and
  * softmax weights are each off by 2^-11 of themselves, values of less than 2^-13 of the largest
  * among 128 neighbouring tokens by up to 2^-25 of that largest; where 128 neighbouring
  * tokens' latents differ by more than 2^12, or leave 2^-40 .. 2^40, their values and
@@ -569,7 +568,8 @@ typedef struct qkmla_prefill_args {
  * aligned bases (o: 32-byte).
  * Device-side: a seq_len outside [0, max_pages * page_size], lengths that add up to more than
  * total_tokens, chunk starts out of order or beyond rows, or a page id outside [0, num_slots /
- * page_size) set QKMLA_ERR_DEVICE_BOUNDS; the affected rows are then undefined.
+ * page_size) set QKMLA_ERR_DEVICE_BOUNDS; the affected sequences' rows are then undefined (with
+ * chunk starts out of order, every row).
  * rows == 0 is a no-op.  Errors: INVALID for null pointers, sizes, strides, alignment, window or
  * sinks as in qkmla_decode_ext, kv_scale without QKMLA_E4M3 or the reverse; UNSUPPORTED for other
  * sizes or dtypes, or with QKMLA_FLAG_PLAIN_MLA; WORKSPACE.

@@ -5,15 +5,17 @@
 // once for 16 query tokens, and a causal edge is at most one tile wide.
 //
 //   S = Q K^T            M = 128 rows, N = 128 tokens, K = d_h + d_r, into TMEM (a half's 128 columns)
-//   softmax              thread = row: reads S, moves its running maximum, writes P (fp16) over S
+//   softmax              thread = row: holds S in registers (its maximum comes with the TMEM load), moves its
+//                        running maximum, writes P over S; the product waits for 64 tokens at a time
 //   O += P V             M = 128, N = d_v, K = 128 tokens, A = P out of TMEM, O in TMEM (128 columns a half)
 //
 // Warps 0-3 and 4-7 are the two halves' softmax, warp 8 loads (bulk copies of prepared blocks into a ring),
-// warp 9 issues, warps 10-15 list the CTA's pieces of work and normalise the next piece's queries.  The halves alternate: while one half's S is worked on, the other's PV and the next QK run:
-// PV0(j) QK0(j+1) PV1(j) QK1(j+1).  The products of one thread run in order, so QK may write S over the P
-// that the PV ahead of it reads, and a half whose S(j) is complete knows that its PV(j-1) is.
+// warp 9 issues, warps 10-15 list the CTA's pieces of work and normalise the next piece's queries.  The halves
+// alternate: while one half's S is worked on, the other's PV and the next QK run: PV0(j) QK0(j+1) PV1(j)
+// QK1(j+1).  The products of one thread run in order, so QK may write S over the P that the PV ahead of it
+// reads, and a half whose S(j) is complete knows that its PV(j-1) is.
 //
-// Numbers.  S is in units of the row's factor c (softmax_scale, log2 e and the query's power of two).  The
+// Numbers.  S is in units of one factor c (softmax_scale, log2 e and the gains' power of two).  The
 // tile's values are 2^-E of themselves, so a row's weights are P_t = 2^(c S_t + E + 7 - m) with m a running
 // maximum of c S_t + E, moved only when it is exceeded by 2^8: P <= 2^15 fits fp16, whose normal range then
 // reaches 2^-21 below the largest weight.  The sum of the softmax is kept in fp32 from the unrounded
@@ -22,10 +24,15 @@
 // same rate.  A tile whose latents differ too much holds its values as bf16, and its P is bf16 too.
 //
 // Work.  A CTA an SM takes an even share of the list of (unit, query tile, token tile); a query tile that is
-// cut leaves its parts in the workspace and prefill_join_kernel adds them, by weights 2^(m_s - max m).
+// cut leaves its parts in the workspace and prefill_join_kernel adds them, by weights 2^(m_s - max m).  Query
+// tiles go to the CTAs in turn, so that neighbours work on one unit and share its keys and values in L2: four
+// prompts of 4096 tokens took 2468 us with contiguous shares and 2180 so.
 //
-// Bound: the tensor core (20 products of 128 x 128 x 16 a half and token tile for d_h + d_r + d_v = 320,
-// 1300 cycles), next to it shared-memory bandwidth (each product reads 4 KB of B and, for QK, 4 KB of A).
+// Bound: the tensor core.  A token tile takes 24 + 16 products of 128 x 128 x 16 (d_h + d_r = 192, d_v = 128), 64 cycles
+// each: 2560; PV's are slower, B in rows of tokens, for 2688.  The steady state takes 3790: shared memory carries each
+// product's 4 KB of B, QK's 4 KB of A and the ring's copies, and the softmax chain (load, maximum, exponentials,
+// store) of a half has to end within the other half's products.  128 heads, 1024 queries over 16000 tokens: 750 us
+// for this kernel, 1.74 PFLOP/s of 1.96 measured for a bf16 library product; 75 % of tensor cycles active.
 #include "prefill.cuh"
 
 namespace qkmla {
@@ -36,8 +43,9 @@ using namespace tc;
 
 constexpr int kConverters = 6;             // warps that list the work and normalise queries
 constexpr int kThreadsA = (10 + kConverters) * 32;
-// Registers: 512 threads start with 128 each, the whole register file.  The softmax keeps a row of 128 logits, so the
-// two warpgroups of the other warps give up 64 of theirs and each half's takes as many.
+// Registers: 512 threads start with 128 each, the whole register file.  The softmax keeps a row of 128 logits (a loop over
+// parts of the row, read twice, took 1029 us where this takes 909, on 1024 queries over 16000 tokens), so each of the
+// other warps' two warpgroups gives up 64 a thread and each half's takes as many.
 constexpr int kRegsSoftmax = 192, kRegsOther = 64;
 static_assert(2 * kRegsSoftmax + 2 * kRegsOther <= 4 * 128, "register split");
 constexpr int kUnits = 8;                  // ring, in blocks
@@ -776,6 +784,8 @@ give_up:
 // ---------------------------------------------------------------------------
 // Block (k, y): rows 16 y .. 16 y + 15 of the query tile that the boundary between CTA k and k + 1 cuts, if no
 // earlier boundary cuts it.  Half a warp a row of 64, a warp a row of 128 values.
+// Bound: latency (each row's parts and their references are found, then read): 151 cut tiles of 256 x 128 values, 49 MB,
+// take 24 us with a cold L2 and less behind the attention, which leaves the parts there.
 constexpr int kThreadsJ = 128;
 constexpr int kRowsJ = 16;
 

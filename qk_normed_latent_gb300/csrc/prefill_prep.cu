@@ -5,6 +5,18 @@
 //                       W^K to 2^-11, whatever the weights' scale.
 // prefill_expand_kernel keys and values of the cached tokens, 128 a tile, on the tensor cores; its last block makes
 //                       the plan of the attention's work.
+//
+// Expansion.  A tile's latents are gathered once, as fp16 times 2^-e of each token, and stay in shared memory as A
+// (M = 128 tokens, K = d_c) for all columns of W^K and W^V; weights stream through a ring, in N-tiles of 256 columns
+// (128 up to d_c 256, where two CTAs fit on an SM).  The epilogue multiplies a token's key by alpha^k and its power of
+// two, a value by the latter over the tile's largest.  Tiles that no row sees behind a window are left out (585 -> 555
+// us of a windowed call), and a CTA takes an equal number of N-tiles, cutting a token tile where it must (223 -> 197
+// us on a mixed batch).
+//
+// Bound: for large d_c the products (2 d_c (G d_h + G_v d_v) flops a token: 33.6 GFLOP, 17 us, for 16000 tokens at
+// d_c 512 and 8 groups of 128 + 128) and, per tile, the gather's latency and conversions in front of them (9 us a
+// tile, of which the next tile's loads are prefetched) and the weights' stream out of L2.  Those 16000 tokens take
+// 45-48 us, 29 % of tensor cycles; 131072 of the 8-bit cache 296 us.
 #include "prefill.cuh"
 
 namespace qkmla {

@@ -12,9 +12,11 @@
 // small angle keeps its relative precision; sincospif takes it from there.
 //
 // Bound: HBM, each element read and written once (3 flops an element).  A block of 256 threads takes whole
-// rows, up to four vectors (or pairs of them) a thread: their loads go out first, and while they are on their way the
-// block forms the rows' cosines and sines once in shared memory, for every head.  16-byte accesses where strides, bases and d_r allow them, else one
-// pair at a time.
+// rows, up to four vectors (or pairs of them) a thread: their loads go out first, and while they are on their way
+// the block forms the rows' cosines and sines once in shared memory, for every head.  Vectors stay as they lie in
+// memory until they are turned: as fp32 from the start they took twice the registers, and 4096 x 128 RoPE blocks of
+// 64 bf16 values 38.4 us where this takes 23.4 (134 MB: 5.7 TB/s).  16 x 16 blocks of 32 take 3 us, a launch and one
+// chain of loads.  16-byte accesses where strides, bases and d_r allow them, else one pair at a time.
 #include <cmath>
 
 #include "common.cuh"
