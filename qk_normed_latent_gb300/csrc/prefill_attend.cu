@@ -66,9 +66,9 @@ struct __align__(16) Shared {
     uint64_t full[kGroups], empty[kGroups];
     uint64_t q_full[2], q_empty[2], q0_full[2];
     uint64_t s_full[2], pa_full[2], pb_full[2], o_full[2];
-    uint64_t piece_full[2], piece_empty[2], conv_full[2];
+    uint64_t piece_full[kAhead], piece_empty[kAhead], conv_full[kAhead];
     uint64_t done;
-    Piece piece[2];
+    Piece piece[kAhead];
     int info[4];                           // tinfo of the last token tiles whose keys were issued
     uint32_t tmem;
     int fail;
@@ -250,6 +250,11 @@ __global__ void __launch_bounds__(kThreadsA, 1) prefill_attend_kernel(const __gr
 
     if (tid == 0) {
         for (int i = 0; i < kGroups; ++i) { mbar_init(&sh->full[i], 1); mbar_init(&sh->empty[i], 1); }
+        for (int i = 0; i < kAhead; ++i) {
+            mbar_init(&sh->piece_full[i], 1);
+            mbar_init(&sh->piece_empty[i], 10);            // loads, products, eight softmax warps
+            mbar_init(&sh->conv_full[i], kConverters);
+        }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh->q_full[i], 1);
             mbar_init(&sh->q_empty[i], 1);
@@ -258,9 +263,6 @@ __global__ void __launch_bounds__(kThreadsA, 1) prefill_attend_kernel(const __gr
             mbar_init(&sh->pa_full[i], 4);
             mbar_init(&sh->pb_full[i], 4);
             mbar_init(&sh->o_full[i], 1);
-            mbar_init(&sh->piece_full[i], 1);
-            mbar_init(&sh->piece_empty[i], 10);            // loads, products, eight softmax warps
-            mbar_init(&sh->conv_full[i], kConverters);
             sh->q_issued[i] = 0;
         }
         mbar_init(&sh->done, 1);
@@ -309,8 +311,8 @@ __global__ void __launch_bounds__(kThreadsA, 1) prefill_attend_kernel(const __gr
             bool ok = true;
 #pragma unroll 1
             for (int k = 0; ok; ++k) {
-                if (!(ok = wait_or_fail(&sh->piece_full[k & 1], (k >> 1) & 1, &sh->fail))) break;
-                const Piece s = sh->piece[k & 1];
+                if (!(ok = wait_or_fail(&sh->piece_full[k % kAhead], (k / kAhead) & 1, &sh->fail))) break;
+                const Piece s = sh->piece[k % kAhead];
                 if (s.unit < 0) break;
                 const int n = s.t1 - s.t0, halves = n == 0 ? 0 : s.queries * p.hp > 128 ? 2 : 1;
                 const size_t g = (size_t)((int64_t)s.unit * p.G / p.units), gv = (size_t)((int64_t)s.unit * p.Gv / p.units);
@@ -355,14 +357,14 @@ __global__ void __launch_bounds__(kThreadsA, 1) prefill_attend_kernel(const __gr
                             qe_phase ^= 1u << h;
                         }
                         if (!ok || h >= halves || k == 0) continue;            // (the first piece's rows go to shared memory directly)
-                        if (!converted) ok = wait_or_fail(&sh->conv_full[k & 1], ((k - 1) >> 1) & 1, &sh->fail);
+                        if (!converted) ok = wait_or_fail(&sh->conv_full[k % kAhead], ((k - 1) / kAhead) & 1, &sh->fail);
                         converted = true;
                         if (!ok) break;
                         mbar_arrive_expect_tx(&sh->q_full[h], kHalf);
-                        bulk_load(sm + h * kHalf, p.qs + ((size_t)(2 * cta + (k & 1)) * 2 + h) * kHalf, kHalf, &sh->q_full[h]);
+                        bulk_load(sm + h * kHalf, p.qs + ((size_t)(kAhead * cta + k % kAhead) * 2 + h) * kHalf, kHalf, &sh->q_full[h]);
                         *(volatile int*)&sh->q_issued[h] = *(volatile int*)&sh->q_issued[h] + 1;
                     }
-                    if (k > 0) mbar_arrive(&sh->piece_empty[(k - 1) & 1]);     // the converted rows of piece k - 1 are no longer read
+                    if (k > 0) mbar_arrive(&sh->piece_empty[(k - 1) % kAhead]);     // the converted rows of piece k - 1 are no longer read
                     last_halves = halves;
                 }
             }
@@ -391,14 +393,14 @@ __global__ void __launch_bounds__(kThreadsA, 1) prefill_attend_kernel(const __gr
             // the next piece (halves -1: there is none); with weights awaited no more than one, which may have no tiles:
             // the one behind it is not listed before they have been used
             while (left == 0 && halves >= 0) {
-                if (!wait_or_fail(&sh->piece_full[k & 1], (k >> 1) & 1, &sh->fail)) goto give_up;
-                const Piece& s = sh->piece[k & 1];
+                if (!wait_or_fail(&sh->piece_full[k % kAhead], (k / kAhead) & 1, &sh->fail)) goto give_up;
+                const Piece& s = sh->piece[k % kAhead];
                 if (s.unit < 0) { halves = -1; break; }
                 left = s.t1 - s.t0;
                 halves = s.queries * p.hp > 128 ? 2 : 1;
                 first = true;
                 q_at = k;
-                mbar_arrive(&sh->piece_empty[k & 1]);
+                mbar_arrive(&sh->piece_empty[k % kAhead]);
                 ++k;
                 if (cur > 0) break;
             }
@@ -582,24 +584,24 @@ give_up:
                     for (int i = 0; i < rope_bytes; i += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(y + i));
                 }
             }
-            if (k >= 2) ok = wait_long(&sh->piece_empty[k & 1], ((k >> 1) - 1) & 1, &sh->fail);
+            if (k >= kAhead) ok = wait_long(&sh->piece_empty[k % kAhead], (k / kAhead - 1) & 1, &sh->fail);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             if (warp == 10 && lane == 0) {
-                sh->piece[k & 1] = s;
-                mbar_arrive(&sh->piece_full[k & 1]);
+                sh->piece[k % kAhead] = s;
+                mbar_arrive(&sh->piece_full[k % kAhead]);
             }
             if (s.unit < 0) break;
             if (k == 0) continue;
             if (s.t0 < s.t1) {
                 const int rows = min(s.queries * p.hp, kRowsQ);
-                uint8_t* dst = p.qs + (size_t)(2 * cta + (k & 1)) * (2 * kHalf);
+                uint8_t* dst = p.qs + (size_t)(kAhead * cta + k % kAhead) * (2 * kHalf);
 #pragma unroll 1
                 for (int rt = (warp - 10) * 4; rt < rows; rt += kConverters * 4) query_rows<DH, DR>(p, s, sh->gain, rt, dst + (rt >> 7) * kHalf, lane);
                 asm volatile("fence.proxy.async.global;" ::: "memory");
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sh->conv_full[k & 1]);
+            if (lane == 0) mbar_arrive(&sh->conv_full[k % kAhead]);
         }
       }
     } else {
@@ -615,10 +617,10 @@ give_up:
         bool ok = true;
 #pragma unroll 1
         for (int k = 0;; ++k) {
-            ok = wait_or_fail(&sh->piece_full[k & 1], (k >> 1) & 1, &sh->fail);
+            ok = wait_or_fail(&sh->piece_full[k % kAhead], (k / kAhead) & 1, &sh->fail);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
-            const Piece& s = sh->piece[k & 1];                          // (read where it is needed: registers are few)
+            const Piece& s = sh->piece[k % kAhead];                          // (read where it is needed: registers are few)
             if (s.unit < 0) break;
             const bool mine = h == 0 || s.queries * p.hp > 128;         // uniform in a warp
             if (mine && k == 0 && s.t0 < s.t1) {
@@ -697,7 +699,7 @@ give_up:
             }
             if (!mine) {
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sh->piece_empty[k & 1]);
+                if (lane == 0) mbar_arrive(&sh->piece_empty[k % kAhead]);
                 continue;
             }
             if (s.t0 < s.t1 && ok) ok = wait_or_fail(&sh->o_full[h], o_phase, &sh->fail);
@@ -754,7 +756,7 @@ give_up:
             }
             tc_fence_before();                                          // the next tile's PV writes O after this half's P
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sh->piece_empty[k & 1]);
+            if (lane == 0) mbar_arrive(&sh->piece_empty[k % kAhead]);
         }
     }
     __syncthreads();
@@ -985,7 +987,7 @@ int make_params(const qkmla_prefill_args* a, pf::Params* p, size_t* bytes) {
     p->krope = (uint8_t*)take(tiles * pf::kBlock);
     p->kc = (uint8_t*)take(tiles * a->G * (a->d_h / 64) * pf::kBlock);
     p->v = (uint8_t*)take(tiles * a->G_v * (a->d_v / 64) * pf::kBlock);
-    p->qs = (uint8_t*)take((size_t)p->ctas * 4 * (a->d_h / 64 + 1) * pf::kBlock);
+    p->qs = (uint8_t*)take((size_t)p->ctas * 2 * pf::kAhead * (a->d_h / 64 + 1) * pf::kBlock);
     *bytes = at - (uintptr_t)a->workspace;
     p->q = a->q;
     p->q_rope = a->q_rope;
