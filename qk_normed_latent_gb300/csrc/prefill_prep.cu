@@ -14,8 +14,8 @@
 // us on a mixed batch).
 //
 // Bound: for large d_c the products (2 d_c (G d_h + G_v d_v) flops a token: 33.6 GFLOP, 17 us, for 16000 tokens at
-// d_c 512 and 8 groups of 128 + 128) and, per tile, the gather's latency and conversions in front of them (9 us a
-// tile, of which the next tile's loads are prefetched) and the weights' stream out of L2.  Those 16000 tokens take
+// d_c 512 and 8 groups of 128 + 128), five fourths of that by shared memory's rate, and, per tile, the gather's latency and
+// conversions in front of them (9 us a tile, of which the next tile's loads are prefetched).  Those 16000 tokens take
 // 45-48 us, 29 % of tensor cycles; 131072 of the 8-bit cache 296 us.
 #include "prefill.cuh"
 
@@ -188,9 +188,10 @@ __device__ void make_plan(const Params& p, int64_t* warps) {
 // one 128-byte line of a block; quads of lanes exchange pieces so that each store writes whole lines.  Warp 8 streams the packed weights through a
 // ring, warp 9 issues the products (M = 128, N = 128 or 256, K = 64 a stage), the accumulator double-buffered.
 //
-// Bound: the tensor core for many tokens (2 d_c flops a value); next to it the weights, which every tile
-// streams through L2 (32 KB a stage of 512 cycles: 64 bytes a cycle and SM at full rate), so the ring takes all the
-// shared memory that the latents leave (three stages at d_c = 512).  Few tiles: their columns are cut over several CTAs.
+// Bound: shared memory.  A stage's four products take 512 cycles of the tensor core, but read 4 x (4 KB of latents + 8 KB of
+// weights) while 32 KB of the next weights are written: 80 KB, 640 cycles at 128 bytes, and 640 a stage is what it takes.
+// (Two CTAs that bring half of each stage for both were no faster: L2 does not hold it back.)  The ring takes all the shared
+// memory that the latents leave (three stages at d_c = 512).  Few tiles: their columns are cut over several CTAs.
 constexpr int kRingMax = 3;
 constexpr int kNone = -1000, kBad = 1000;      // exponents of an all-zero and of a not finite token
 

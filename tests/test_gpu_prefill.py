@@ -368,3 +368,83 @@ def test_results_do_not_depend_on_what_the_workspace_held(Q):
     dev.call.workspace.fill_(0xFF)
     again = dev.run(Q)[0]
     assert (first == again).all()
+
+
+@pytest.mark.parametrize("cache", ["bf16", "q8"])
+def test_pages_beyond_4_gb(Q, cache):
+    """A cache of more than 2^32 bytes whose pages in use lie at its end."""
+    c = R.Case(lens=[300, 40], new=[20, 3], H=8, G=2, d_c=512, d_h=128, d_r=64, d_v=128, page=16, cache=cache)
+    dev = Device(Q, c)
+    slots, width = dev.kv.shape
+    far = (2 ** 32 // (width * dev.kv.element_size()) + slots) // 16 * 16 + 16
+    grown = []
+    for t in (dev.kv, dev.ak, dev.kv_scale):
+        if t is not None:
+            g = torch.empty((far, *t.shape[1:]), dtype=t.dtype, device="cuda")
+            g[far - slots:] = t
+            t = g
+        grown.append(t)
+    table = torch.where(dev.table >= 0, dev.table + (far - slots) // 16, dev.table)
+    args = list(dev.args)
+    args[6], args[7], args[10] = grown[0], grown[1], table
+    Q.prefill(*args, **{**dev.kw, "kv_scale": grown[2]})
+    assert Q.get_device_status() == 0
+    compare(c, dev.o.double().cpu().numpy(), dev.lse.double().cpu().numpy())
+    rows = torch.tensor([0, 300, 340], dtype=torch.int32, device="cuda")
+    outs = []
+    for kv, ak, scale, t in ((dev.kv, dev.ak, dev.kv_scale, dev.table), (*grown, table)):
+        x = [torch.zeros((340, n), device="cuda") for n in (512, 64, 2)]
+        Q.read_cache(kv, ak, rows, t, 16, c.max_pages, *x, scale)
+        outs.append(x)
+    assert Q.get_device_status() == 0
+    assert all(torch.equal(a, b) for a, b in zip(*outs))
+
+
+def test_a_page_in_two_places_and_two_sequences(Q):
+    """A prefix shared by two sequences, and a page that lies twice in one of them."""
+    c = R.Case(lens=[64, 64], new=[1, 1], page=16, rope_gain=False)
+    dev = Device(Q, c)
+    dev.table[1, :2] = dev.table[0, :2]                     # the same first 32 tokens
+    dev.table[1, 2] = dev.table[0, 0]                       # and the first 16 once more
+    dev.run(Q)
+    a, lse = dev.o[1].clone(), dev.lse[1].clone()
+    # the same sequence with copies of those pages
+    copy = Device(Q, c)
+    at = lambda t, j: slice(int(t[j]) * 16, int(t[j]) * 16 + 16)  # noqa: E731
+    spare = torch.cat([copy.kv, copy.kv.new_zeros(48, copy.kv.shape[1])]), torch.cat([copy.ak, copy.ak.new_zeros(48, copy.ak.shape[1])])
+    first = copy.kv.shape[0] // 16
+    for k, j in enumerate((0, 1, 0)):
+        for t in spare:
+            t[(first + k) * 16:(first + k + 1) * 16] = t[at(copy.table[0], j)]
+        copy.table[1, k] = first + k
+    args = list(copy.args)
+    args[6], args[7] = spare
+    Q.prefill(*args, **copy.kw)
+    assert Q.get_device_status() == 0
+    assert torch.equal(a, copy.o[1]) and torch.equal(lse, copy.lse[1])
+
+
+def test_two_calls_at_once(Q):
+    """Two prepared calls, each with its workspace, on two streams: as each alone, many times."""
+    cs = [R.Case(lens=[900], new=[130], seed=1), R.Case(lens=[400, 700], new=[60, 9], seed=2)]
+    devs = [Device(Q, c) for c in cs]
+    alone = [d.run(Q)[0] for d in devs]
+    streams = [torch.cuda.Stream() for _ in devs]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for d, s in zip(devs, streams):
+            d.call(s)
+    torch.cuda.synchronize()
+    assert Q.get_device_status() == 0
+    assert all((d.o.double().cpu().numpy() == a).all() for d, a in zip(devs, alone))
+
+
+@pytest.mark.parametrize("H,G,G_v", [(512, 512, 512), (4, 1, 4), (128, 2, 1)])
+def test_head_extremes(Q, H, G, G_v):
+    check(Q, lens=[150], new=[5], H=H, G=G, G_v=G_v, d_c=64)
+
+
+def test_many_empty_chunks_and_one_row(Q):
+    """4096 sequences, most of them idle."""
+    lens = [3 if i % 500 == 7 else 0 for i in range(4096)]
+    check(Q, lens=lens, new=[1 if n else 0 for n in lens], d_c=64)
