@@ -448,3 +448,28 @@ def test_many_empty_chunks_and_one_row(Q):
     """4096 sequences, most of them idle."""
     lens = [3 if i % 500 == 7 else 0 for i in range(4096)]
     check(Q, lens=lens, new=[1 if n else 0 for n in lens], d_c=64)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "q8"])
+def test_contiguous_cache(Q, cache):
+    check(Q, lens=[130, 1, 77], new=[40, 1, 20], contiguous=True, cache=cache)
+
+
+def test_graph_replayed_over_another_step(Q):
+    """A captured call takes lengths, chunks, pages and inputs as they are when it is replayed."""
+    a, b = R.Case(lens=[100, 60], new=[10, 20]), R.Case(lens=[60, 100], new=[25, 5], window=0, seed=5)
+    dev, other = Device(Q, a), Device(Q, b)
+    dev.run(Q)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        dev.call()
+    for name in ("q", "qr", "kv", "ak", "start", "lens", "table"):
+        getattr(dev, name).copy_(getattr(other, name))
+    for x, y in zip(dev.gains, other.gains):
+        x.copy_(y)
+    dev.weights.packed.copy_(other.weights.packed)
+    dev.o.fill_(float("nan"))
+    g.replay()
+    torch.cuda.synchronize()
+    assert Q.get_device_status() == 0
+    compare(b, dev.o.double().cpu().numpy(), dev.lse.double().cpu().numpy())
