@@ -9,8 +9,8 @@
 // page -> slot in front of the row's own load, so a warp takes four neighbouring rows, its lanes follow the
 // four chains at once, and all that the four rows need -- latents, RoPE keys, scales, alpha^k -- is on its way
 // before the first value is used.  32768 rows of an 8-bit cache (512 + 64) to bf16: 26.4 us with the rows one after
-// the other, 11.7 so (61 MB: 5.2 TB/s); 38200 bf16 rows (256 + 32) of 16 sequences to fp32: 17.7 and 14.3 us (67 MB:
-// 4.7 TB/s).  16-byte accesses (8 bytes of codes) where d_c, d_r and the bases allow, else element by element.
+// the other, 11.7 so (61 MB: 5.2 TB/s); 38200 bf16 rows (256 + 32) of 16 sequences to fp32: 17.7 and 14.4, with
+// whole sectors a store 13.4 us (67 MB: 5.0 TB/s).  16-byte accesses (8 bytes of codes) where d_c, d_r and the bases allow, else element by element.
 #include "common.cuh"
 
 namespace qkmla {
@@ -58,6 +58,12 @@ template <typename T> struct Eight {
     }
 };
 __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
+    if ((uintptr_t)p % 32 == 0) {                          // whole sectors at once (all of a row's pieces, or none)
+        asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]),
+                     "f"(v[5]), "f"(v[6]), "f"(v[7])
+                     : "memory");
+        return;
+    }
     reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
     reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
 }

@@ -124,3 +124,21 @@ def test_moved_to_another_cache(Q):
     assert Q.get_device_status() == 0
     s = torch.from_numpy(case.slot[0]).cuda()
     assert (ak2[:60] - ak[s]).abs().max() <= 1e-5 * ak[s].abs().max()
+
+
+@pytest.mark.parametrize("off", [1, 2, 4, 8])
+def test_alignment_of_the_outputs(Q, off):
+    """Outputs `off` elements into their buffers: bases of every alignment that the call takes."""
+    case = R.Case(lens=[70], new=[0])
+    kv, _, ak = cache(case)
+    start = torch.tensor([0, 70], dtype=torch.int32, device="cuda")
+    table = torch.from_numpy(case.table).cuda()
+    for out in (torch.float32, torch.bfloat16):
+        got = []
+        for o in (0, off):
+            c, r = (torch.full((70 * d + 16,), 5.0, dtype=out, device="cuda") for d in (case.d_c, case.d_r))
+            Q.read_cache(kv, ak, start, table, case.page, case.max_pages, c[o:o + 70 * case.d_c].view(70, -1), r[o:o + 70 * case.d_r].view(70, -1))
+            assert (c[:o] == 5).all() and (c[o + 70 * case.d_c:] == 5).all() and (r[:o] == 5).all() and (r[o + 70 * case.d_r:] == 5).all()
+            got.append((c[o:o + 70 * case.d_c], r[o:o + 70 * case.d_r]))
+        assert Q.get_device_status() == 0
+        assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
