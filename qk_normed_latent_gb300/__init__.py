@@ -843,7 +843,11 @@ def prepare_prefill(q, q_rope, gamma_q, gamma_k, gamma_rope_q, weights: PrefillW
     torch = _torch()
     f32, bf16 = torch.float32, torch.bfloat16
     w = weights
+    if q.dim() != 3:                     # both are read by their strides: no other form will do
+        raise ValueError(f"qkmla: q is [rows, H, d_h], not {tuple(q.shape)}")
     rows, H, d_h = q.shape
+    if q_rope.dim() != 3 or q_rope.shape[:2] != q.shape[:2]:
+        raise ValueError(f"qkmla: q_rope is [rows, H, d_r] with q's rows and heads, not {tuple(q_rope.shape)}")
     d_r = q_rope.shape[-1]
     B = seq_lens.numel()
     _expect("q", q, (f32, bf16), rows, H, w.d_h)
