@@ -348,18 +348,18 @@ __global__ void __launch_bounds__(kThreadsA, 1) prefill_attend_kernel(const __gr
                         *(volatile int*)&sh->issued = group;
                     }
                     if (q > 0) continue;
+                    // Every piece's conversion is waited for, of one without tiles too: piece_empty then says that all converting
+                    // warps have been through the piece, so that none falls a phase of either barrier behind.  (The first
+                    // piece's rows go to shared memory directly.)
+                    if (k > 0) ok = wait_or_fail(&sh->conv_full[k % kAhead], ((k - 1) / kAhead) & 1, &sh->fail);
                     // a query half is read by the products until the last ones of the piece ahead have ended
-                    bool converted = false;
 #pragma unroll 1
                     for (int h = 0; h < 2 && ok; ++h) {
                         if (h < last_halves) {
                             ok = wait_or_fail(&sh->q_empty[h], (qe_phase >> h) & 1, &sh->fail);
                             qe_phase ^= 1u << h;
                         }
-                        if (!ok || h >= halves || k == 0) continue;            // (the first piece's rows go to shared memory directly)
-                        if (!converted) ok = wait_or_fail(&sh->conv_full[k % kAhead], ((k - 1) / kAhead) & 1, &sh->fail);
-                        converted = true;
-                        if (!ok) break;
+                        if (!ok || h >= halves || k == 0) continue;
                         mbar_arrive_expect_tx(&sh->q_full[h], kHalf);
                         bulk_load(sm + h * kHalf, p.qs + ((size_t)(kAhead * cta + k % kAhead) * 2 + h) * kHalf, kHalf, &sh->q_full[h]);
                         *(volatile int*)&sh->q_issued[h] = *(volatile int*)&sh->q_issued[h] + 1;
