@@ -20,6 +20,7 @@ constexpr int kTile = 128;                 // tokens of a tile
 constexpr int kRowsQ = 256;                // query rows (tokens x heads of a unit) of a tile: two halves of 128
 constexpr int kBlock = 16384;              // bytes of a block of 128 x 64 values
 constexpr int kMaxE = 40;                  // largest exponent of a tile's values
+constexpr int kNone = -1000, kBad = 1000;  // exponents of an all-zero and of a not finite token
 constexpr int kCostStart = 4;              // cost of starting on a query tile, in tiles of tokens
 constexpr int kMinPiece = 2;               // no piece of a cut query tile has fewer tiles of tokens
 // Pieces of work listed, and their queries normalised, ahead: with 2 a short piece ends before the next one's queries are
@@ -60,7 +61,7 @@ struct Params {
     int4* qinfo;                           // [nq][2]: {b, first query, tiles, head tiles}, {gap, length of the first query, queries, -}
     int64_t* pre;                          // [ctas deep + 1]: cost of the places ahead
     int4* cuts;                            // [ctas + 1]: where each CTA's share starts
-    int* tinfo;                            // [max_tiles]: exponent + 64, | 256 where the values are bf16
+    int* tinfo;                            // [max_tiles]: TileScale::packed()
     uint8_t *krope, *kc, *v;               // blocks: [tile], [tile][G][d_h / 64], [tile][G_v][d_v / 64]
     uint8_t* qs;                           // [cta][kAhead][half][d_h / 64 + 1]: the normalised queries of a CTA's next pieces
     float* part_o;                         // [2 ctas][256][d_v]
@@ -161,6 +162,27 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 }
 // 2^e as an exact float, e in [-126, 127]
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
+
+// How a tile's values are held, from the largest and the least exponent of its tokens' latents (zeros left out): as 2^-e of
+// themselves, in fp16 or, where that would not hold them beside one another, bf16.  A row's softmax reference follows the
+// tile that moves it, of weight 2^e there; a row may not see the tile's largest token, or give it no weight, and a reference
+// too high takes bits from the weights of all other tiles.  So the reference is set `drop` lower, e - drop the least
+// exponent: bf16 has the range to take that one as e; fp16's values grow by up to 2^4 (2^11, the sum of 512 products of
+// numbers below 2, becomes 2^15), and its weights give up to 2^8 of their own room above 2^7.
+struct TileScale {
+    int e, drop;
+    bool bf;
+    __device__ __forceinline__ TileScale(int hi, int lo) {
+        const int spread = hi - lo;
+        bf = hi != kNone && (spread > 12 || hi > kMaxE || hi < -kMaxE);
+        if (hi == kNone) e = 0;
+        else if (bf) e = min(max(lo, max(hi - 80, -kMaxE)), kMaxE);      // (values then stay below 2^91, or as large as they are)
+        else e = hi - min(spread, 4);
+        drop = bf || hi == kNone ? 0 : spread - min(spread, 4);
+    }
+    // [e + 64 | bf << 8 | drop << 9]
+    __device__ __forceinline__ int packed() const { return (e + 64) | (bf ? 256 : 0) | drop << 9; }
+};
 
 // Every wait ends by itself, after kSpins tries (each of 50 ns or more); a warp that gives up says so and leaves, and the
 // others' waits end likewise.  (Named barriers cannot be used where a thread may have given up.)  Small on purpose: beyond

@@ -17,11 +17,12 @@
 //
 // Numbers.  S is in units of one factor c (softmax_scale, log2 e and the gains' power of two).  The
 // tile's values are 2^-E of themselves, so a row's weights are P_t = 2^(c S_t + E + 7 - m) with m a running
-// maximum of c S_t + E, moved only when it is exceeded by 2^8: P <= 2^15 fits fp16, whose normal range then
-// reaches 2^-21 below the largest weight.  The sum of the softmax is kept in fp32 from the unrounded
-// weights, 2^-E of each tile's; O, in TMEM, is in fp32.  fp16 instead of bf16 because keys and queries are
-// normalised (bounded) and a tile's values have an exponent of their own: 8 times smaller roundings at the
-// same rate.  A tile whose latents differ too much holds its values as bf16, and its P is bf16 too.
+// reference: moved only when the maximum of c S_t + E exceeds it by 2^8, to that maximum less the tile's spread of
+// sizes (TileScale: so that a large token that the row does not see, or gives no weight, takes no bits from the
+// others).  P <= 2^15 fits fp16, whose normal range then reaches 2^-21 below the largest weight.  The sum of the softmax
+// is kept in fp32 from the unrounded weights, 2^-E of each tile's; O, in TMEM, is in fp32.  fp16 instead of bf16 because
+// keys and queries are normalised (bounded) and a tile's values have an exponent of their own: 8 times smaller roundings
+// at the same rate.  A tile whose latents differ too much holds its values as bf16, and its P is bf16 too.
 //
 // Work.  A CTA an SM takes an even share of the list of (unit, query tile, token tile); a query tile that is
 // cut leaves its parts in the workspace and prefill_join_kernel adds them, by weights 2^(m_s - max m).  Query
@@ -676,7 +677,7 @@ give_up:
                 const float cand = fmaf(top, c, (float)e);
                 const bool move = cand > m + 8.f;
                 if (__any_sync(0xffffffffu, move)) {
-                    const float m2 = move ? cand : m;
+                    const float m2 = move ? cand - (float)(info >> 9) : m;
                     const float a = move ? ex2(m - m2) : 1.f;           // 0 while nothing was seen
                     sum *= a;
                     if (t > s.t0) {

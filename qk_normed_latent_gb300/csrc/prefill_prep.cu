@@ -193,7 +193,6 @@ __device__ void make_plan(const Params& p, int64_t* warps) {
 // (Two CTAs that bring half of each stage for both were no faster: L2 does not hold it back.)  The ring takes all the shared
 // memory that the latents leave (three stages at d_c = 512).  Few tiles: their columns are cut over several CTAs.
 constexpr int kRingMax = 3;
-constexpr int kNone = -1000, kBad = 1000;      // exponents of an all-zero and of a not finite token
 
 // blocks of the latents, a ring of three stages of 32 KB or two of 16 KB
 __host__ __device__ inline int expand_bytes(int d_c) { return (d_c / 64 + (d_c <= 256 ? 2 : 2 * kRingMax)) * kBlock + 1024 + 2048; }
@@ -574,10 +573,10 @@ __global__ void __launch_bounds__(kThreadsE, NV == 1 ? 2 : 1) prefill_expand_ker
             int e_hi = kNone, e_lo = kBad;
 #pragma unroll
             for (int i = 0; i < 8; ++i) { e_hi = max(e_hi, sh->hi[buf][i]); e_lo = min(e_lo, sh->lo[buf][i]); }
-            // one exponent for the tile's values; bf16 where fp16 would not hold them beside one another
-            const bool bf = e_hi != kNone && (e_hi - e_lo > 12 || e_hi > kMaxE || e_hi < -kMaxE);
-            const int e_tile = e_hi == kNone ? 0 : min(max(e_hi, -kMaxE), kMaxE);
-            if (n0 == 0 && tid == 0) p.tinfo[tile] = (e_tile + 64) | (bf ? 256 : 0);
+            const TileScale ts(e_hi, e_lo);
+            const bool bf = ts.bf;
+            const int e_tile = ts.e;
+            if (n0 == 0 && tid == 0) p.tinfo[tile] = ts.packed();
             // ---- results: thread = token, its warp's half of the 128 columns (one 64-column block) ----
             const int et = sh->exps[buf][row];
             const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
