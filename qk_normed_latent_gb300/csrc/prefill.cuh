@@ -175,7 +175,7 @@ struct TileScale {
     __device__ __forceinline__ TileScale(int hi, int lo) {
         const int spread = hi - lo;
         bf = hi != kNone && (spread > 12 || hi > kMaxE || hi < -kMaxE);
-        if (hi == kNone) e = 0;
+        if (hi == kNone) e = -kMaxE;                       // zeros are of no size that others are measured by
         else if (bf) e = min(max(lo, max(hi - 80, -kMaxE)), kMaxE);      // (values then stay below 2^91, or as large as they are)
         else e = hi - min(spread, 4);
         drop = bf || hi == kNone ? 0 : spread - min(spread, 4);

@@ -77,3 +77,15 @@ def test_sizes_that_grow_and_fall(Q, new):  # noqa: F811
         case.c *= (2.0 ** np.repeat(g.integers(-12, 13, -(-n // 128)), 128)[:n] * 2.0 ** g.integers(0, 15, n))[:, None].astype(np.float32)
     c = R.Case(lens=[4000], new=[new], outliers=0, change=change)
     compare(c, *Device(Q, c).run(Q), wide=True)
+
+
+@pytest.mark.parametrize("by", [2.0 ** -20, 2.0 ** -30, 2.0 ** -38])
+@pytest.mark.parametrize("zeros", [slice(0, 128), slice(256, 384), slice(130, 200)])
+def test_zero_latents_beside_small_ones(Q, zeros, by):  # noqa: F811
+    """A tile of zeros has no size that the others could be measured by."""
+    def change(case):
+        case.c *= np.float32(by)
+        case.c[zeros] = 0
+    c = R.Case(lens=[600], new=[50], outliers=0, change=change)
+    o, lse = Device(Q, c).run(Q)
+    close(c, o, lse, slice(0, 50), NARROW)
