@@ -211,6 +211,7 @@ static_assert(sizeof(ExpandShared) <= 2048, "beside the blocks");
 // next tile's is mostly the same one.  Whole warp.
 struct Sequence {
     int b = 0, first = 0, last = 0, len = 0, head = 0, gap = 0;         // its tiles: [first, last)
+    int from = 0;                                          // where its first row's window starts
     int b0 = 0, ahead = 0;                                 // where the next search starts: sequences, and tiles ahead of them
     __device__ __forceinline__ bool find(const Params& p, int tile) {
         if (tile < last) return tile >= first;
@@ -219,7 +220,8 @@ struct Sequence {
         for (; b0 < p.B; b0 += 32) {
             const int at = b0 + lane;
             const int n = at < p.B ? p.seq_lens[at] : 0;
-            const Needed d = at < p.B ? needed(p, n, p.chunk_start[at + 1] - p.chunk_start[at]) : Needed{0, 0, 0};
+            const int rows = at < p.B ? p.chunk_start[at + 1] - p.chunk_start[at] : 0;
+            const Needed d = needed(p, n, rows);
             int s = d.tiles;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -233,6 +235,7 @@ struct Sequence {
                 len = __shfl_sync(0xffffffffu, n, l);
                 head = __shfl_sync(0xffffffffu, d.head, l);
                 gap = __shfl_sync(0xffffffffu, d.gap, l);
+                from = p.window > 0 ? (int)max((int64_t)len - __shfl_sync(0xffffffffu, rows, l) + 1 - p.window, (int64_t)0) : 0;
                 last = ahead + __shfl_sync(0xffffffffu, s, l);
                 first = last - __shfl_sync(0xffffffffu, d.tiles, l);
                 return true;
@@ -242,6 +245,9 @@ struct Sequence {
         last = first = 1 << 30;                            // behind the last sequence
         return false;
     }
+    // Whether some row sees token t.  What none sees is taken as zeros, here and in all that is formed from a tile's tokens
+    // together, and its page is not looked up.
+    __device__ __forceinline__ bool sees(const Params& p, int t) const { return t < len && (t >= from || t < p.sinks); }
     // The first token of a tile.
     __device__ __forceinline__ int token(int tile) const { return (tile - first < head ? tile - first : tile - first + gap) * kTile; }
 };
@@ -483,12 +489,12 @@ __global__ void __launch_bounds__(kThreadsE, NV == 1 ? 2 : 1) prefill_expand_ker
 #pragma unroll 1
         while (ok && share.next(nt, tile, n0, n1)) {
             seq.find(p, tile);
-            const int t0 = seq.token(tile), len = seq.len, buf = it & 1;
+            const int t0 = seq.token(tile), buf = it & 1;
             // ---- gather: a warp's 16 tokens, their slots by its first 16 lanes ----
             const int row = 32 * (warp & 3) + lane;          // this thread's token in the results
             const int mine = t0 + (lane < 16 ? warp * 16 + lane : row);
             auto slot_at = [&](int t) {
-                return t < len ? slot_of(p.page_table, seq.b, t, p.page_size, p.max_pages, p.num_pages, p.status) : (int64_t)-1;
+                return seq.sees(p, t) ? slot_of(p.page_table, seq.b, t, p.page_size, p.max_pages, p.num_pages, p.status) : (int64_t)-1;
             };
             const int64_t slot = slot_at(mine);              // (of lanes from 16 on it is not used)
             const int64_t row_slot = slot_at(t0 + row);

@@ -89,3 +89,30 @@ def test_zero_latents_beside_small_ones(Q, zeros, by):  # noqa: F811
     c = R.Case(lens=[600], new=[50], outliers=0, change=change)
     o, lse = Device(Q, c).run(Q)
     close(c, o, lse, slice(0, 50), NARROW)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "q8"])
+@pytest.mark.parametrize("value", [2.0 ** 30, 2.0 ** 100, float("nan")])
+@pytest.mark.parametrize("sinks", [0, 2])
+def test_token_that_no_row_sees_changes_nothing(Q, sinks, value, cache):  # noqa: F811
+    """Not a bit of any row, where a tile holds visible tokens beside it."""
+    def run(change):
+        c = R.Case(lens=[1024, 300], new=[20, 7], window=1000, sinks=sinks, cache=cache, change=change)
+        return c, Device(Q, c).run(Q)
+
+    def change(case):
+        case.c[3:5] *= np.float32(value)                       # the first row sees tokens from 5 on, and the sinks
+    c, (o, lse) = run(None)
+    compare(c, o, lse)
+    _, (o2, lse2) = run(change)
+    assert (o == o2).all() and (lse == lse2).all()
+
+
+def test_page_that_no_row_sees(Q):  # noqa: F811
+    """Pages in front of the windows may be given back: their entries are not looked up."""
+    c = R.Case(lens=[1024], new=[20], window=950, page=16)                    # the first row sees tokens from 55 on
+    dev = Device(Q, c)
+    want = dev.run(Q)
+    dev.table[0, :3] = torch.tensor([-1, 2 ** 31 - 1, -7], dtype=torch.int32)
+    got = dev.run(Q)
+    assert all((a == b).all() for a, b in zip(got, want))
