@@ -12,8 +12,9 @@ import torch
 
 import workloads as W
 
-from . import (F32, BF16, append, append_q8, decode_workspace_size, decode_raw, make_decode_args,
-               prefill_weights, prepare_absorb_query, prepare_append, prepare_append_q8, prepare_decode, prepare_prefill)
+from . import (F32, BF16, PrefillWeights, _launching, append, append_q8, decode_workspace_size,
+               decode_raw, make_decode_args, prefill, prefill_weights, prepare_absorb_query, prepare_append, prepare_append_q8,
+               prepare_decode)
 
 # element types; "e4m3" is the 8-bit latent cache (bytes: codes and the bf16 RoPE key, scales beside them)
 _TORCH_DT = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16, "e4m3": torch.uint8}
@@ -143,7 +144,6 @@ class DeviceState:
         self.args = None
         self._absorb = self._append = None
         self._decode = {}
-        self._prefill = {}
 
     # -- the three calls -------------------------------------------------------
     def absorb(self, stream=None):
@@ -208,18 +208,15 @@ class DeviceState:
         decode_raw(self.args, stream)
 
     def prefill(self, w_v, o_dtype=torch.bfloat16, stream=None):
-        """The step's queries as chunks of s_q tokens: per-head values [rows, H, d_v] with W^V [G_v, d_c, d_v] (bf16),
-        as decode and up_project give them.  Append the step's tokens first."""
+        """The step's queries as chunks of s_q tokens: per-head values [rows, H, d_v], the caller's own, with W^V [G_v, d_c, d_v]
+        (bf16, laid out in every call) or what prefill_weights(self.wk, W^V) gave, as decode and up_project give them.  Append
+        the step's tokens first."""
         w = self.w
-        key = (w_v.data_ptr(), o_dtype)
-        if self._prefill.get(key) is None:
-            weights = prefill_weights(self.wk, w_v)
+        weights = w_v if isinstance(w_v, PrefillWeights) else prefill_weights(self.wk, w_v, stream)
+        with _launching(stream):
             start = torch.arange(0, w.rows + 1, w.s_q, dtype=torch.int32, device=self.dev)
             o = torch.empty((w.rows, w.H, weights.d_v), dtype=o_dtype, device=self.dev)
-            self._prefill[key] = (prepare_prefill(
-                self.q, self.q_rope.reshape(w.rows, w.H, w.d_r), self.gq, self.gk, self.grq, weights, self.kv, self.ak, start,
+        prefill(self.q, self.q_rope.reshape(w.rows, w.H, w.d_r), self.gq, self.gk, self.grq, weights, self.kv, self.ak, start,
                 self.seq_lens, self.page_table, self.page_size, self.max_pages, int(self.lens.sum()), w.scale, w.eps, o,
-                kv_scale=self.kv_scale, window=self.window, sinks=self.sinks), o, w_v)
-        call, o, _ = self._prefill[key]
-        call(stream)
+                kv_scale=self.kv_scale, window=self.window, sinks=self.sinks, stream=stream)
         return o
