@@ -12,7 +12,7 @@ import torch
 
 import workloads as W
 
-from . import (F32, BF16, PrefillWeights, _launching, append, append_q8, decode_workspace_size,
+from . import (ERR_UNSUPPORTED, F32, BF16, PrefillWeights, QkmlaError, _launching, append, append_q8, decode_workspace_size,
                decode_raw, make_decode_args, prefill, prefill_weights, prepare_absorb_query, prepare_append, prepare_append_q8,
                prepare_decode)
 
@@ -212,6 +212,8 @@ class DeviceState:
         (bf16, laid out in every call) or what prefill_weights(self.wk, W^V) gave, as decode and up_project give them.  Append
         the step's tokens first."""
         w = self.w
+        if self.plain:
+            raise QkmlaError("qkmla_prefill", ERR_UNSUPPORTED)
         weights = w_v if isinstance(w_v, PrefillWeights) else prefill_weights(self.wk, w_v, stream)
         with _launching(stream):
             start = torch.arange(0, w.rows + 1, w.s_q, dtype=torch.int32, device=self.dev)

@@ -1,4 +1,4 @@
-"""DeviceState.prefill: weights as they are at each call, and outputs of its own."""
+"""DeviceState.prefill: weights as they are at each call, outputs of its own, and what it refuses."""
 import pytest
 import torch
 
@@ -70,3 +70,11 @@ def test_on_a_stream(Q):  # noqa: F811
     s.synchronize()
     for o in outs:
         expect(Q, st, o, w_v)
+
+
+def test_plain_attention_is_refused(Q):  # noqa: F811
+    """Prefill normalises; a state without the normalisation gave that other attention."""
+    st = state(plain=True)
+    with pytest.raises(Q.QkmlaError) as e:
+        st.prefill(values(st.w, st.w.G, 128, 7))
+    assert e.value.code == Q.ERR_UNSUPPORTED
