@@ -447,9 +447,9 @@ typedef struct qkmla_rope_args {
  * GIVEN: frequencies[i].  Elements outside the rotated part are neither read nor
  * written.  Computed in fp32 with angles exact to 2^-24 of a turn or better at every
  * position, one rounding to bf16.  rows == 0 is a no-op.
- * Errors: INVALID for null pointers, sizes, an odd d_r, unknown layout or scaling, theta <= 1,
- * factor <= 0, bad betas, a frequency that is not finite, misaligned elements; UNSUPPORTED
- * for another dtype, d_r > 256 or more heads than a launch takes.
+ * Errors: INVALID for null pointers, sizes, an odd d_r, outputs that share elements (a stride
+ * below d_r), unknown layout or scaling, theta <= 1, factor <= 0, bad betas, a frequency that is
+ * not finite, misaligned elements; UNSUPPORTED for another dtype, d_r > 256 or more heads than a launch takes.
  */
 int qkmla_rope(const qkmla_rope_args* a, void* stream);
 

@@ -737,7 +737,7 @@ def prepare_rope(x, positions, out, theta: float = 10000.0, layout: str = "inter
 def rope(x, positions, out=None, theta: float = 10000.0, layout: str = "interleaved",
          scaling: Optional[RopeScaling] = None, inverse: bool = False, attention_factor: float = 1.0, stream=None):
     """x [rows, heads, d_r] or [rows, d_r] (a view into heads of more elements will do) with every head's pairs
-    turned by positions [rows] (int32) times their frequencies, into out (None: in place).  layout
+    turned by positions [rows] (int32) times their frequencies, into out (None: in place; x may be broadcast, out not).  layout
     "interleaved": pairs (2i, 2i + 1); "half": (i, i + d_r / 2).  inverse: turned back."""
     out = x if out is None else out
     prepare_rope(x, positions, out, theta, layout, scaling, inverse, attention_factor)(stream)

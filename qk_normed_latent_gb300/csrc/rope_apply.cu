@@ -18,6 +18,7 @@
 // 64 bf16 values 38.4 us where this takes 23.4 (134 MB: 5.7 TB/s).  16 x 16 blocks of 32 take 3 us, a launch and one
 // chain of loads, 16001 fp32 keys of 64 4.2.  16-byte accesses where strides, bases and d_r allow them, else one pair at a time.
 #include <cmath>
+#include <cstdlib>
 
 #include "common.cuh"
 
@@ -203,6 +204,9 @@ extern "C" int qkmla_rope(const qkmla_rope_args* a, void* stream) {
     if (a->dtype != QKMLA_F32 && a->dtype != QKMLA_BF16) return QKMLA_ERR_UNSUPPORTED;
     if (a->d_r > 2 * kMaxPairs) return QKMLA_ERR_UNSUPPORTED;
     if (a->rows == 0) return QKMLA_OK;
+    // rows or heads that share elements of the output would be written (in place: read and written) by several threads
+    if ((a->rows > 1 && std::llabs(a->out_row_stride) < a->d_r) || (a->heads > 1 && std::llabs(a->out_head_stride) < a->d_r))
+        return QKMLA_ERR_INVALID;
     if (!a->x || !a->out || !a->positions) return QKMLA_ERR_INVALID;
     const int esz = a->dtype == QKMLA_F32 ? 4 : 2;
     if ((uintptr_t)a->x % esz || (uintptr_t)a->out % esz || (uintptr_t)a->positions % 4) return QKMLA_ERR_INVALID;
