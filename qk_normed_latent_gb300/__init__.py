@@ -299,7 +299,8 @@ def _stream(stream) -> Optional[int]:
     if stream is None:                   # (the handle alone: a Stream object costs 2.8 us, half of a small call)
         torch = _torch()
         device = torch.cuda.current_device()
-        return torch._C._cuda_getCurrentRawStream(device)
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)       # private: a torch without it has the public form
+        return raw(device) if raw is not None else torch.cuda.current_stream(device).cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
