@@ -46,9 +46,9 @@
  *    stream.  Reads of inputs no kernel of the library writes may start
  *    earlier: seq_lens in qkmla_decode and qkmla_decode_ext; W^K, the new tokens,
  *    their slots and positions in qkmla_append, qkmla_append_rope and
- *    qkmla_append_q8; the positions in qkmla_rope; out_start, first and the page table
- *    in qkmla_read_cache; W^K and W^V in qkmla_prefill_pack_weights.  A previous
- *    kernel that itself signals early dependent launch must therefore not be
+ *    qkmla_append_q8; out_start, first and the page table in qkmla_read_cache; W^K
+ *    and W^V in qkmla_prefill_pack_weights.  A previous kernel that itself signals
+ *    early dependent launch must therefore not be
  *    writing those inputs (kernels that do not signal it, and copies, are waited
  *    for in full as usual).
  */
@@ -445,8 +445,11 @@ typedef struct qkmla_rope_args {
  * pair floor(c(beta_fast)) to 1 at pair ceil(c(beta_slow)), both within [0, d_r - 1],
  * c(n) = d_r ln(original_context / (2 pi n)) / (2 ln theta): f_i (u_i / factor + 1 - u_i);
  * GIVEN: frequencies[i].  Elements outside the rotated part are neither read nor
- * written.  Computed in fp32 with angles exact to 2^-24 of a turn or better at every
- * position, one rounding to bf16.  rows == 0 is a no-op.
+ * written.  Computed in fp32, one rounding to bf16.  A frequency is a 64-bit number, to 2^-48 of
+ * itself (2^-46 on YARN's ramp; theta up to 10^8): an angle of N turns, N = |positions[r] f_i| /
+ * (2 pi), is off by at most N times that and 2^-26 of a turn, 2^-25 for positions below 2^24 and
+ * f_i <= 1 off the ramp.
+ * rows == 0 is a no-op.
  * Errors: INVALID for null pointers, sizes, an odd d_r, outputs that share elements (a stride
  * below d_r), unknown layout or scaling, theta <= 1, factor <= 0, bad betas, a frequency that is
  * not finite, misaligned elements; UNSUPPORTED for another dtype, d_r > 256 or more heads than a launch takes.

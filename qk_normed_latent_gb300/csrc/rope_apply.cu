@@ -6,8 +6,8 @@
 // (YaRN: pairs of more than beta_fast turns within the original context keep their frequency, of less
 // than beta_slow are divided, a ramp between) -- or given.
 //
-// Angles.  The host forms each frequency in turns a position, in 64 bits, and hands the kernel its
-// fraction as a 64-bit integer F (unit 2^-64 turns): p F modulo 2^64 is the angle modulo one turn, by one
+// Angles.  The host forms each frequency in turns a position, in 64 bits (to 2^-48 of itself: neighbours by products, up to seven
+// behind a power), and hands the kernel its fraction as a 64-bit integer F (unit 2^-64 turns): p F modulo 2^64 is the angle modulo one turn, by one
 // integer product, for every int32 position.  Read as a signed number it is the turn nearest 0, so that a
 // small angle keeps its relative precision; sincospif takes it from there.
 //
@@ -215,9 +215,10 @@ extern "C" int qkmla_rope(const qkmla_rope_args* a, void* stream) {
     if (!frequencies(a, f)) return QKMLA_ERR_INVALID;
     p.pairs = a->d_r / 2;
     for (int i = 0; i < p.pairs; ++i) {
-        double turn = f[i] * 0.15915494309189533576888376337251;       // 1 / (2 pi)
-        turn -= std::floor(turn);                                      // in [0, 1]
-        p.turn[i] = turn >= 1.0 ? 0 : (uint64_t)(turn * 18446744073709551616.0);
+        double turn = std::fabs(f[i]) * 0.15915494309189533576888376337251;       // 1 / (2 pi)
+        turn -= std::floor(turn);                                      // exact, in [0, 1)
+        const uint64_t n = (uint64_t)(turn * 18446744073709551616.0);
+        p.turn[i] = f[i] < 0.0 ? 0 - n : n;                            // (1 - turn would drop bits of a small one)
     }
     p.x = a->x;
     p.out = a->out;
