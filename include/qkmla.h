@@ -40,17 +40,18 @@
  *  - The library is stateless apart from the status word and a small per-
  *    device table of launch limits; it is thread-safe.
  *  - Every kernel is launched with programmatic stream serialization and lets
- *    the next kernel of the stream launch early.  Its writes, and its reads of
- *    anything a kernel of this library produces (q~, alpha^q, the cache, q and
- *    q_rope of qkmla_project_query, o), wait for the previous kernel of the
- *    stream.  Reads of inputs no kernel of the library writes may start
+ *    the next kernel of the stream launch early, but for those of qkmla_rope and
+ *    qkmla_read_cache, which are waited for in full: what they write may be an
+ *    append's new tokens.  A kernel's writes, and its reads of anything another
+ *    kernel of this library produces (q~, alpha^q, the cache, q and q_rope of
+ *    qkmla_project_query, o), wait for the previous kernel of the stream.  Reads
+ *    of inputs no kernel of the library writes, or only those two, may start
  *    earlier: seq_lens in qkmla_decode and qkmla_decode_ext; W^K, the new tokens,
  *    their slots and positions in qkmla_append, qkmla_append_rope and
  *    qkmla_append_q8; out_start, first and the page table in qkmla_read_cache; W^K
  *    and W^V in qkmla_prefill_pack_weights.  A previous kernel that itself signals
- *    early dependent launch must therefore not be
- *    writing those inputs (kernels that do not signal it, and copies, are waited
- *    for in full as usual).
+ *    early dependent launch must therefore not be writing those inputs (kernels
+ *    that do not signal it, and copies, are waited for in full as usual).
  */
 #ifndef QKMLA_H
 #define QKMLA_H

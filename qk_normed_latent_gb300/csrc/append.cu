@@ -132,9 +132,10 @@ append_split_kernel(const float* __restrict__ c_new, const float* __restrict__ r
     if (positions && tid < d_r / 2) freq[tid] = rope_freq(theta, tid, d_r);
     __syncthreads();
     pdl_trigger();
-    // Every input (the weights, the new tokens, their slots and positions) is one no
-    // kernel of this library writes, so the loads and the partial keys run before the
-    // dependency wait, overlapping the previous kernel; only the cache writes wait.
+    // Every input (the weights, the new tokens, their slots and positions) is one that no
+    // kernel of this library writes, or only one that is waited for in full (qkmla_rope,
+    // qkmla_read_cache), so the loads and the partial keys run before the dependency wait,
+    // overlapping the previous kernel; only the cache writes wait.
     if (tid == 0) {
         mbar_arrive_expect_tx(bar, (uint32_t)((nvalid * kKS + kKS * kDh) * 4));
         bulk_load(Ws, wk + ((int64_t)g * kDc + k0) * kDh, (uint32_t)(kKS * kDh * 4), bar);

@@ -22,7 +22,8 @@ __device__ __forceinline__ void report(int* st, int code) {
 // the stream is still running, so it first does only work that touches no
 // global memory, then waits (pdl_wait) until the previous grid has completed and
 // its writes are visible, and then lets the next kernel start its own launch
-// (pdl_trigger).  Launched without the attribute, both are no-ops.
+// (pdl_trigger; a kernel that never does is waited for in full, as by a launch without
+// the attribute).  Launched without the attribute, both are no-ops.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

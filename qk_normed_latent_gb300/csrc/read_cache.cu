@@ -105,8 +105,7 @@ __global__ void __launch_bounds__(kThreadsC) read_cache_kernel(const ReadParams 
         }
     }
     if (t >= 0) slot = slot_of(p.page_table, b, (int)t, p.page_size, p.max_pages, p.num_pages, p.status);
-    pdl_wait();
-    pdl_trigger();
+    pdl_wait();                                          // (no early launch of the next kernel: append reads new tokens ahead of its wait)
     const unsigned rows = __ballot_sync(0xffffffffu, slot >= 0);
     if (!rows) return;
     const int64_t row_bytes = (int64_t)p.d_c * sizeof(CT) + (int64_t)p.d_r * sizeof(RT);

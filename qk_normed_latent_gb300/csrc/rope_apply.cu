@@ -79,8 +79,7 @@ __global__ void __launch_bounds__(kThreadsR) rope_kernel(const __grid_constant__
         for (int i = threadIdx.x; i < p.pairs; i += kThreadsR) freq[i] = p.turn[i];
         __syncthreads();
     }
-    pdl_wait();
-    pdl_trigger();
+    pdl_wait();                                         // (no early launch of the next kernel: append reads new tokens ahead of its wait)
     Held<T, V> a[kItems], b[HALF ? kItems : 1];
     int at[kItems];
     int64_t to[kItems];
