@@ -556,16 +556,21 @@ typedef struct qkmla_prefill_args {
  * = qkmla_absorb_query, qkmla_decode_ext and qkmla_up_project over the same cache.
  * A query without a visible token gives o = 0, lse = -inf.  Rows from chunk_start[B] on
  * stay as they are.  Stored values that no query of a row's step sees do not reach its
- * result, NaN included; a NaN in what a query sees, or in its own row, is NaN in its o
- * and lse.
+ * result, NaN included, and pages of such tokens alone are not looked up; a NaN in what a
+ * query sees, or in its own row, is NaN in its o and lse.
+ *
+ * For few rows a sequence decode costs less (absorb + decode + up-projection against this call,
+ * 16 sequences of 4096 tokens: 128 heads, d_c 512, one row 96 against 237 us, equal between 8 and
+ * 12 rows; 16 heads, d_c 256, one row 26 against 80, equal at about 32).
  *
  * Accuracy: fp16 operands (11 significant bits) of tensor-core products, fp32 sums:
  * recovered keys and values, normalised queries (the gains times one power of two a call) and
  * softmax weights are each off by 2^-11 of themselves, values of less than 2^-13 of the largest
  * among 128 neighbouring tokens by up to 2^-25 of that largest; where 128 neighbouring
- * tokens' latents differ by more than 2^12, or leave 2^-40 .. 2^40, their values and
- * weights are bf16 (2^-8).  A weight below 2^-22 of the row's largest loses bits, one below 2^-32 is 0.
- * RoPE keys are taken as fp16: up to 65504.
+ * tokens' latents (of those that some row of the step sees, zeros left out) differ by more
+ * than 2^12, or leave 2^-40 .. 2^40, their values and weights are bf16 (2^-8).  With l the
+ * smallest of those 128 latents' sizes, a weight p loses bits where p l is below 2^-21 of the row's
+ * largest p l, and may be 0 below 2^-32 of it.  RoPE keys are taken as fp16: up to 65504.
  *
  * Sizes: d_h and d_v 64 or 128, d_r 32 or 64, d_c a multiple of 64 up to 512, H / max(G, G_v)
  * 1, 2, 4, ... or 128, the larger of G and G_v a multiple of the other, B <= 4096, any page size; 16-byte
@@ -578,7 +583,8 @@ typedef struct qkmla_prefill_args {
  * sinks as in qkmla_decode_ext, kv_scale without QKMLA_E4M3 or the reverse; UNSUPPORTED for other
  * sizes or dtypes, or with QKMLA_FLAG_PLAIN_MLA; WORKSPACE.
  * qkmla_prefill_workspace_size: 0 for arguments that the call rejects; reads the sizes alone.  Depends
- * on the current device.
+ * on the current device.  Keys and values of all tokens lie there at once: 2 (G d_h + G_v d_v + 64)
+ * bytes a token of total_tokens, rounded up to 128 tokens a sequence (8 groups of 128 + 128: 4.2 KB).
  */
 int qkmla_prefill(const qkmla_prefill_args* a, void* stream);
 size_t qkmla_prefill_workspace_size(const qkmla_prefill_args* a);

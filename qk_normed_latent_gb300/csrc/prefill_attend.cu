@@ -32,8 +32,8 @@
 // Bound: the tensor core.  A token tile takes 24 + 16 products of 128 x 128 x 16 (d_h + d_r = 192, d_v = 128), 64 cycles
 // each: 2560; PV's are slower, B in rows of tokens, for 2688.  The steady state takes 3790: shared memory carries each
 // product's 4 KB of B, QK's 4 KB of A and the ring's copies, and the softmax chain (load, maximum, exponentials,
-// store) of a half has to end within the other half's products.  128 heads, 1024 queries over 16000 tokens: 743 us
-// for this kernel, 1.75 PFLOP/s of 1.96 measured for a bf16 library product; 76 % of tensor cycles active.
+// store) of a half has to end within the other half's products.  128 heads, 1024 queries over 16000 tokens: 731 us
+// for this kernel, 1.78 PFLOP/s of 1.96 measured for a bf16 library product; 76 % of tensor cycles active.
 #include "prefill.cuh"
 
 namespace qkmla {

@@ -10,7 +10,8 @@
 // four chains at once, and all that the four rows need -- latents, RoPE keys, scales, alpha^k -- is on its way
 // before the first value is used.  32768 rows of an 8-bit cache (512 + 64) to bf16: 26.4 us with the rows one after
 // the other, 11.7 so (61 MB: 5.2 TB/s); 38200 bf16 rows (256 + 32) of 16 sequences to fp32: 17.7 and 14.4, with
-// whole sectors a store 13.4 us (67 MB: 5.0 TB/s).  16-byte accesses (8 bytes of codes) where d_c, d_r and the bases allow, else element by element.
+// whole sectors a store 13.4 us (67 MB: 5.0 TB/s).  Those are calls in a row that overlapped; since the next launch waits for the
+// last store they are 12.6 and 14.7 apart.  16-byte accesses (8 bytes of codes) where d_c, d_r and the bases allow, else element by element.
 #include "common.cuh"
 
 namespace qkmla {

@@ -16,7 +16,7 @@
 // the block forms the rows' cosines and sines once in shared memory, for every head.  Vectors stay as they lie in
 // memory until they are turned: as fp32 from the start they took twice the registers, and 4096 x 128 RoPE blocks of
 // 64 bf16 values 38.4 us where this takes 23.4 (134 MB: 5.7 TB/s).  16 x 16 blocks of 32 take 3 us, a launch and one
-// chain of loads, 16001 fp32 keys of 64 4.2.  16-byte accesses where strides, bases and d_r allow them, else one pair at a time.
+// chain of loads, 16001 fp32 keys of 64 4.6 (4.3 while the next launch could start early).  16-byte accesses where strides, bases and d_r allow them, else one pair at a time.
 #include <cmath>
 #include <cstdlib>
 
@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(kThreadsR) rope_kernel(const __grid_constant__
     const int units = p.pairs / kPairs;                 // a head's
     const int n = nr * nh * units;                      // at most kThreadsR * kItems
     // A warp's 32 frequencies are 32 addresses in constant memory, which serves one at a time.  Where a thread has more
-    // than one angle they are copied out of it once (16001 keys of 64: 7.0 us without, 4.2 with; 4096 x 128 blocks, two rows
+    // than one angle they are copied out of it once (16001 keys of 64, calls in a row that overlapped: 7.0 us without, 4.2 with; 4096 x 128 blocks, two rows
     // a block: 23.35 and 23.6).
     const bool many = nr * p.pairs > kThreadsR;
     if (many) {
