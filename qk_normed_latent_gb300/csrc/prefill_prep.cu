@@ -4,7 +4,8 @@
 //                       that brings its largest value into [1, 2): fp16's 11 bits hold W^V's 8 exactly and
 //                       W^K to 2^-11, whatever the weights' scale.
 // prefill_expand_kernel keys and values of the cached tokens, 128 a tile, on the tensor cores; its last block makes
-//                       the plan of the attention's work.
+//                       the plan of the attention's work (where the others fill every SM, as the first of them ends;
+//                       given an SM of its own the calls took as long).
 //
 // Expansion.  A tile's latents are gathered once, as fp16 times 2^-e of each token, and stay in shared memory as A
 // (M = 128 tokens, K = d_c) for all columns of W^K and W^V; weights stream through a ring, in N-tiles of 256 columns
