@@ -681,7 +681,7 @@ def given_frequencies(radians) -> RopeScaling:
 
 def _inner(name: str, t) -> int:
     """Address of a tensor whose last dimension is contiguous (its others may have any stride)."""
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    if t.shape[-1] > 1 and t.stride(-1) != 1 and t.numel() > 0:
         raise ValueError(f"qkmla: {name} must be contiguous in its last dimension")
     if not t.is_cuda:
         raise ValueError("qkmla: tensors must live on a CUDA device")

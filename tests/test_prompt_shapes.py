@@ -28,3 +28,10 @@ def test_rope_queries_have_the_queries_form(shape):
 def test_queries_have_three_dimensions(shape):
     with pytest.raises(ValueError, match="q is"):
         call(zeros(*shape), zeros(8, 16, 32))
+
+
+def test_no_rows_have_no_strides():
+    """A tensor without elements may carry any strides (numpy's do): a step without rows is no error."""
+    for empty in (torch.empty_strided((0, 16, 64), (0, 0, 0)), torch.empty_strided((0, 16, 64), (1024, 2, 2))):
+        with pytest.raises(ValueError, match="CUDA device"):               # what any tensor of the CPU meets
+            Q._inner("q", empty)
