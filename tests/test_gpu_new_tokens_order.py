@@ -93,3 +93,42 @@ def test_two_appends_behind_two_ropes(Q):  # noqa: F811
     calls = [Q.prepare_rope(x, pos, x) for x in xs] + [append(Q, False, c, x[-16:], wk, slots, *o) for x, o in zip(xs, outs)]
     replay(calls, lambda: [x.copy_(t) for x, t in zip(xs, raw)], [o[k] for o in outs for k in (0, 2)])
     assert Q.get_device_status() == 0
+
+
+@pytest.mark.parametrize("q8", [False, True])
+def test_layers_in_a_row(Q, q8):  # noqa: F811
+    """rope, append, prefill and read_cache of three layers, nothing waiting on the host between them."""
+    H, D_V, B, N, PAGE = 16, 64, 3, 130, 16
+    g = torch.Generator(device="cuda").manual_seed(9)
+    pages = 40
+    table = torch.randperm(B * pages, generator=g, device="cuda").to(torch.int32).view(B, pages)
+    lens = torch.tensor([600, 131, 333], dtype=torch.int32, device="cuda")
+    start = torch.arange(0, B * N + 1, N, dtype=torch.int32, device="cuda")
+    t = torch.cat([torch.arange(int(n) - N, int(n), device="cuda") for n in lens])
+    b = torch.arange(B, device="cuda").repeat_interleave(N)
+    slots = table.long()[b, t // PAGE] * PAGE + t % PAGE
+    pos = t.to(torch.int32)
+    ones_h, ones_r = torch.ones(D_H, device="cuda"), torch.ones(D_R, device="cuda")
+    calls, outputs, raws, kept = [], [], [], []               # (prepared calls hold addresses alone: what they name is kept)
+    for _ in range(3):
+        wk, wv = rand(g, G, D_C, D_H) / 16, (rand(g, G, D_C, D_V) / 16).bfloat16()
+        kv, scale, ak = caches(q8, B * pages * PAGE)
+        old = torch.arange(B * pages * PAGE, device="cuda")
+        past = rand(g, len(old), D_C), rand(g, len(old), D_R)
+        append(Q, q8, *past, wk, old, kv, scale, ak)()
+        torch.cuda.synchronize()
+        raw_k, raw_q = rand(g, B * N, D_R), rand(g, B * N, H, D_R)
+        k, qr, new, q = raw_k.clone(), raw_q.clone(), rand(g, B * N, D_C), rand(g, B * N, H, D_H)
+        raws += [(k, raw_k), (qr, raw_q)]
+        weights, first = Q.prefill_weights(wk, wv), lens - N
+        o = torch.empty((B * N, H, D_V), device="cuda")
+        c, r, a = (torch.empty((B * N, n), device="cuda") for n in (D_C, D_R, G))
+        calls += [Q.prepare_rope(k, pos, k), Q.prepare_rope(qr, pos, qr, layout="half"),
+                  append(Q, q8, new, k, wk, slots, kv, scale, ak),
+                  Q.prepare_prefill(q, qr, ones_h, ones_h, ones_r, weights, kv, ak, start, lens, table, PAGE, pages, int(lens.sum()), 0.1, EPS,
+                                    o, kv_scale=scale),
+                  Q.prepare_read_cache(kv, ak, start, table, PAGE, pages, c, r, a, kv_scale=scale, first=first)]
+        outputs += [o, c, r, a]
+        kept.append((wk, wv, kv, scale, ak, new, q, weights, first))
+    replay(calls, lambda: [x.copy_(y) for x, y in raws], outputs)
+    assert Q.get_device_status() == 0
